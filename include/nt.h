@@ -607,6 +607,190 @@ nt_status nt_varlen_attn_bwd(nt_dtype dtype, const void* q, const void* k, const
                              float scale, int32_t causal, void* dq, void* dk, void* dv,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rotary frequency scaling of nt_rope_turns. */
+typedef enum {
+  NT_ROPE_NONE = 0,    /* f_j = base^(-2 j / rot_dim) */
+  NT_ROPE_LINEAR = 1,  /* f_j / factor: positions interpolated */
+  NT_ROPE_NTK = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  NT_ROPE_BANDS = 3    /* by the pair's turns r = original_len f_j / 2 pi within the original length:
+                          interpolated (f_j / factor) for r <= low, kept for r >= high, between them
+                          f_j ((1 - g) / factor + g) with g = (r - low) / (high - low) */
+} nt_rope_scaling;
+
+/*
+ * nt_rope_turns -- the frequency table of nt_qk_norm_rope, formed on the host
+ * in fp64: turns[j] = f_j / (2 pi) modulo 1 as a 64-bit binary fraction, j in
+ * [0, rot_dim / 2), so that position p turns pair j by p * turns[j] modulo
+ * 2^64, exactly, however far the position.  The caller copies the table to
+ * the device once and keeps it (any other frequencies may be given in the
+ * same form).
+ *   rot_dim       even, in [2, 65536].   base > 0, finite.
+ *   factor        > 0, finite (ignored for NT_ROPE_NONE).
+ *   original_len, low, high   NT_ROPE_BANDS only: original_len > 0, low < high.
+ *   turns         [rot_dim / 2] HOST memory, written.
+ * No CUDA call is made.
+ */
+nt_status nt_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor, double original_len,
+                        double low, double high, uint64_t* turns);
+
+/*
+ * nt_qk_norm_rope -- RMS norm of every query and key head and rotary
+ * positions, in one pass over packed tokens (what feeds nt_varlen_attn in
+ * training and prefill, and nt_paged_write / nt_paged_attn in decoding):
+ *     y = x gamma / sqrt(mean_c x_c^2 + eps)   (gamma NULL: y = x)
+ *     out_a = rot_scale (y_a cos t - y_b sin t),
+ *     out_b = rot_scale (y_a sin t + y_b cos t),   t = 2 pi position turns[j]
+ * over the pairs j of the first rot_dim columns; later columns keep y.
+ *   q, k          [T, H_q, d], [T, H_k, d] tokens q_stride / k_stride elements
+ *                 apart (>= H * d, multiples of 8 bf16 / 4 fp32 elements; a
+ *                 slice of a fused projection is read in place).  H_k = 0
+ *                 with k, k_out NULL: queries only; H_q = 0 likewise.
+ *   d             a multiple of 16 in [16, 256].
+ *   q_gamma, k_gamma  [d] fp32, each NULL for no norm of that side.
+ *   eps           >= 0, finite.
+ *   positions: either d_positions [T] int32 (any values), with d_cu_seqlens
+ *                 and d_pos0 NULL; or d_cu_seqlens [B+1] int32 as in
+ *                 nt_varlen_attn, token t of segment b at position
+ *                 t - cu[b] + d_pos0[b] (d_pos0 [B] int32 or NULL for 0: for
+ *                 decoding, the tokens already in the cache).  A token that
+ *                 the offsets place in no segment is flagged
+ *                 (NT_ERR_DEVICE_CHECK) and not written.
+ *   d_turns       [rot_dim / 2] device, from nt_rope_turns.
+ *   rot_dim       a multiple of 16, in [0, d]; 0 rotates nothing (norm only;
+ *                 d_turns and the positions are not read and may be NULL).
+ *   interleaved   0: pairs (j, j + rot_dim / 2); 1: pairs (2 j, 2 j + 1).
+ *   rot_scale     finite; multiplies the rotated columns (1 normally).
+ *   q_out, k_out  [T, H, d], tokens q_out_stride / k_out_stride elements
+ *                 apart; may equal q / k with the same stride (in place),
+ *                 otherwise must not overlap any input.
+ * fp32 arithmetic, one rounding to the I/O dtype at the end.  Asynchronous.
+ */
+nt_status nt_qk_norm_rope(nt_dtype dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          int64_t T, int32_t H_q, int32_t H_k, int32_t d, const float* q_gamma,
+                          const float* k_gamma, float eps, const int32_t* d_cu_seqlens, int32_t B,
+                          const int32_t* d_pos0, const int32_t* d_positions, const uint64_t* d_turns,
+                          int32_t rot_dim, int32_t interleaved, float rot_scale, void* q_out,
+                          int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* Bytes of device workspace nt_qk_norm_rope_bwd needs when a gamma is given
+ * (the partial sums of the gammas' gradients); 0 for a bad d. */
+size_t nt_qk_norm_rope_bwd_workspace_bytes(int32_t d);
+
+/*
+ * nt_qk_norm_rope_bwd -- gradients of nt_qk_norm_rope: with g the upstream
+ * gradient rotated back (and times rot_scale), r = 1 / sqrt(mean x^2 + eps),
+ *     dgamma = sum over tokens and heads of g x r,
+ *     dx = r (h - x r mean_c(h x r)),  h = g gamma      (no norm: dx = g)
+ *   dq_out, dk_out   the upstream gradients, in the I/O dtype.
+ *   q, k             the forward's inputs; read only for a side with a gamma
+ *                    (NULL allowed otherwise).
+ *   dq, dk           the inputs' gradients, out; may equal dq_out / dk_out
+ *                    with the same stride.
+ *   dq_gamma, dk_gamma  [d] fp32 out, required where the gamma is given (and
+ *                    NULL where it is not); overwritten.
+ *   workspace        >= nt_qk_norm_rope_bwd_workspace_bytes(d) bytes, 16-byte
+ *                    aligned, when a gamma is given.
+ * The sums run in fp32 in a fixed order on one device (bit-reproducible).
+ * Other arguments, refusals and device checks as in nt_qk_norm_rope.
+ */
+nt_status nt_qk_norm_rope_bwd(nt_dtype dtype, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                              int64_t dk_out_stride, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, int64_t T, int32_t H_q, int32_t H_k, int32_t d,
+                              const float* q_gamma, const float* k_gamma, float eps, const int32_t* d_cu_seqlens,
+                              int32_t B, const int32_t* d_pos0, const int32_t* d_positions, const uint64_t* d_turns,
+                              int32_t rot_dim, int32_t interleaved, float rot_scale, void* dq, int64_t dq_stride,
+                              void* dk, int64_t dk_stride, float* dq_gamma, float* dk_gamma, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a key/value cache (a host struct naming device buffers the
+ * caller owns).  Page p holds page_size consecutive positions of one
+ * sequence: k and v are [n_pages, H_kv, page_size, d].  Which pages are whose
+ * is in the callers' block tables, [B, max_pages] int32 on the device:
+ * position x of sequence b is row x % page_size of page
+ * d_block_table[b * max_pages + x / page_size].  Sequences may share pages.
+ * Entries behind a sequence's last position are never read.
+ *   n_pages >= 0, page_size in [1, 65536], H_kv >= 1, d * element size a
+ *   multiple of 16; k, v 16-byte aligned (NULL if n_pages = 0).
+ */
+typedef struct nt_kv_pages {
+  void* k;
+  void* v;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t H_kv;
+  int32_t d;
+  nt_dtype dtype;
+} nt_kv_pages;
+
+/*
+ * nt_paged_write -- the keys and values of T packed tokens into the pages of
+ * their sequences: token t of segment b goes to position
+ * d_pos0[b] + t - cu[b].  A prefill passes d_pos0 NULL (0), a decoding step
+ * cu = 0, 1, ..., B and the lengths before the step.
+ *   k, v          [T, H_kv, d] in the pages' dtype, tokens k_stride /
+ *                 v_stride elements apart (>= H_kv * d, multiples of 8 bf16 /
+ *                 4 fp32 elements).
+ *   d_cu_seqlens  [B+1] int32, as in nt_varlen_attn.   d_pos0 [B] or NULL.
+ *   d_block_table [B, max_pages] int32.
+ * Two tokens of one call may not share a position of a page (a page that
+ * several sequences share must be copied before one of them writes to it).
+ * A token outside every segment, a negative position, one beyond max_pages,
+ * or a page that is not in [0, n_pages) is flagged (NT_ERR_DEVICE_CHECK) and
+ * not written.  Asynchronous.
+ */
+nt_status nt_paged_write(const nt_kv_pages* pages, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         int64_t T, const int32_t* d_cu_seqlens, int32_t B, const int32_t* d_pos0,
+                         const int32_t* d_block_table, int32_t max_pages, void* stream);
+
+/*
+ * nt_paged_copy -- page src[i] copied over page dst[i], keys and values, for
+ * i < n: what forking a sequence's last page, or moving pages together,
+ * needs.
+ *   src, dst      [n] int32 HOST arrays, read before the call returns (they
+ *                 travel in the launches' arguments, so a captured graph
+ *                 keeps its list).  Every entry in [0, n_pages); no page
+ *                 twice in dst, and none both in src and in dst: the copies
+ *                 run in no particular order (NT_ERR_INVALID otherwise).
+ * Asynchronous.
+ */
+nt_status nt_paged_copy(const nt_kv_pages* pages, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* Bytes of device workspace nt_paged_attn needs for H query heads on H_kv key
+ * heads of width d: the partial results of sequences split over CTAs, for up
+ * to 16 of a key head's query heads (at most 8.5 MB; it does not grow with
+ * the batch or the lengths).  0 for sizes the call refuses.  Calls that may
+ * overlap on the GPU need workspaces of their own; nothing needs clearing. */
+size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
+
+/*
+ * nt_paged_attn -- attention of one new token per sequence over its paged
+ * cache:
+ *     o[b, h, :] = sum_{x < len_b} softmax_x(scale q[b, h] . K[x, h / G]) V[x, h / G]
+ * with G = H / H_kv query heads per key head.  The new token's own key and
+ * value are in the cache already (nt_paged_write comes first).
+ *   q             [B, H, d] in the pages' dtype, sequences q_stride elements
+ *                 apart (>= H * d, a multiple of 8 bf16 / 4 fp32 elements).
+ *   H             a multiple of H_kv.   d in {32, 64, 128}.
+ *   d_block_table [B, max_pages] int32.
+ *   d_lengths     [B] int32, the positions of each sequence that are attended
+ *                 to; 0 gives o = 0 and lse = -inf.  Lengths are read on the
+ *                 device only: a captured call follows them.  A negative
+ *                 length, one beyond max_pages * page_size (read as that),
+ *                 and a page outside [0, n_pages) (read as zeros) are flagged
+ *                 (NT_ERR_DEVICE_CHECK).
+ *   scale         finite and > 0.
+ *   o             [B, H, d] contiguous, out.   lse [H, B] fp32 natural-log
+ *                 log-sum-exp of the scaled scores, or NULL.
+ *   workspace     >= nt_paged_attn_workspace_bytes(H, H_kv, d) bytes, 16-byte aligned.
+ * The softmax statistics and sums are fp32; bf16 probabilities are rounded to
+ * bf16 before they multiply the values where tensor cores form the product.
+ * Results do not depend on scheduling.  Asynchronous.
+ */
+nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,
+                        const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device status word set by
  * device-side checks (bounded waits that ran out: NT_ERR_TIMEOUT; failed data
  * checks: NT_ERR_DEVICE_CHECK).  NT_OK if nothing was flagged. */

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -157,6 +158,73 @@ nt_status pair_transition(const nt_partition* part, nt_dtype dtype, const void* 
   if (st != NT_OK) return st;
   return transition_cells(part->P, dtype, z_in, z_out, C_z, H_t, ln_gamma, ln_beta, ln_eps, W1, b1, W3, b3, W2,
                           b2, stream);
+}
+
+// Sizes, strides, positions and pointers that nt_qk_norm_rope and its
+// backward share.
+nt_status check_rope(nt_dtype dtype, int64_t T, int32_t H_q, int32_t H_k, int32_t d, float eps,
+                     const int32_t* cu, int32_t B, const int32_t* pos0, const int32_t* positions,
+                     const uint64_t* turns, int32_t rot_dim, int32_t interleaved, float rot_scale) {
+  if (!dtype_ok(dtype)) return fail(NT_ERR_INVALID, "bad dtype %d", (int)dtype);
+  if (T < 0 || H_q < 0 || H_k < 0 || d <= 0 || B < 0 || rot_dim < 0)
+    return fail(NT_ERR_INVALID, "bad sizes T=%lld H_q=%d H_k=%d d=%d B=%d rot_dim=%d", (long long)T, H_q, H_k, d, B,
+                rot_dim);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (H_q > 65536 || H_k > 65536) return fail(NT_ERR_UNSUPPORTED, "H_q=%d, H_k=%d: at most 65536 heads", H_q, H_k);
+  if (d % 16 || d > 256) return fail(NT_ERR_UNSUPPORTED, "head width d=%d must be a multiple of 16 up to 256", d);
+  if (rot_dim > d) return fail(NT_ERR_INVALID, "rot_dim=%d > d=%d", rot_dim, d);
+  if (rot_dim % 16) return fail(NT_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16", rot_dim);
+  if (interleaved != 0 && interleaved != 1) return fail(NT_ERR_INVALID, "interleaved must be 0 or 1");
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(NT_ERR_INVALID, "eps must be finite and >= 0");
+  if (!std::isfinite(rot_scale)) return fail(NT_ERR_INVALID, "rot_scale must be finite");
+  if (positions && (cu || pos0)) return fail(NT_ERR_INVALID, "positions are given twice (d_positions and d_cu_seqlens)");
+  if (T > 0 && rot_dim > 0) {
+    if (!turns) return fail(NT_ERR_INVALID, "d_turns is NULL");
+    if (!positions && (!cu || B == 0)) return fail(NT_ERR_INVALID, "no positions (d_positions or d_cu_seqlens)");
+  }
+  if (T > 0 && cu && B == 0) return fail(NT_ERR_INVALID, "T > 0 with no segments");
+  if ((reinterpret_cast<uintptr_t>(turns) & 7u) || (reinterpret_cast<uintptr_t>(cu) & 3u) ||
+      (reinterpret_cast<uintptr_t>(pos0) & 3u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(NT_ERR_INVALID, "d_turns, d_cu_seqlens, d_pos0 or d_positions misaligned");
+  return NT_OK;
+}
+
+// One token-strided tensor [T, H, d].
+nt_status check_tokens(nt_dtype dtype, const char* name, const void* p, int64_t stride, int64_t T, int32_t H,
+                       int32_t d) {
+  if (T == 0 || H == 0) return NT_OK;
+  if (!p) return fail(NT_ERR_INVALID, "%s is NULL", name);
+  if (!aligned16(p)) return fail(NT_ERR_INVALID, "%s must be 16-byte aligned", name);
+  if (stride < (int64_t)H * d || stride % (dtype == NT_BF16 ? 8 : 4) || stride > (1LL << 40))
+    return fail(NT_ERR_INVALID, "%s: token stride %lld must be >= H * d = %lld and a multiple of %d", name,
+                (long long)stride, (long long)H * d, dtype == NT_BF16 ? 8 : 4);
+  return NT_OK;
+}
+
+nt_status check_pages(const nt_kv_pages* p) {
+  if (!p) return fail(NT_ERR_INVALID, "pages is NULL");
+  if (!dtype_ok(p->dtype)) return fail(NT_ERR_INVALID, "bad dtype %d", (int)p->dtype);
+  if (p->n_pages < 0 || p->page_size < 1 || p->page_size > 65536 || p->H_kv < 1 || p->H_kv > 65536 || p->d < 1)
+    return fail(NT_ERR_INVALID, "bad pages n_pages=%d page_size=%d H_kv=%d d=%d", p->n_pages, p->page_size, p->H_kv,
+                p->d);
+  if (!width_ok(p->dtype, p->d) || p->d > 65536)
+    return fail(NT_ERR_UNSUPPORTED, "head width d=%d must be a multiple of %d", p->d, p->dtype == NT_BF16 ? 8 : 4);
+  if (p->n_pages > 0 && (!p->k || !p->v)) return fail(NT_ERR_INVALID, "NULL page pointer");
+  if (!aligned16(p->k) || !aligned16(p->v)) return fail(NT_ERR_INVALID, "pages must be 16-byte aligned");
+  if ((int64_t)p->n_pages * p->H_kv > 0x7fffffffLL)
+    return fail(NT_ERR_OVERFLOW, "n_pages * H_kv = %lld must fit int32", (long long)p->n_pages * p->H_kv);
+  return NT_OK;
+}
+
+PagedPool pool_of(const nt_kv_pages* p) {
+  return {p->k, p->v, p->n_pages, p->page_size, p->H_kv, (int)(p->d * esize(p->dtype))};
+}
+
+nt_status check_table(const int32_t* table, int32_t max_pages, int32_t B) {
+  if (max_pages < 0) return fail(NT_ERR_INVALID, "max_pages=%d < 0", max_pages);
+  if (B > 0 && max_pages > 0 && !table) return fail(NT_ERR_INVALID, "d_block_table is NULL");
+  if (reinterpret_cast<uintptr_t>(table) & 3u) return fail(NT_ERR_INVALID, "d_block_table misaligned");
+  return NT_OK;
 }
 
 // u = s_left W_a^T (T rows), v = s_right W_b^T (T_cols rows), fp32.
@@ -847,6 +915,237 @@ nt_status nt_pair_block_loss_backward(const nt_partition* part, nt_dtype dtype, 
   return block_backward_run(part, dtype, s, C_s, W_a, W_b, C_z, H_t, ln_gamma, ln_beta, ln_eps, W1, b1, W2, W_g, m,
                             dx, tc ? nullptr : dz, tc ? z_tilde : nullptr, ds, dW_a, dW_b, dgamma, dbeta, dW1, db1,
                             dW2, db2, dW_g, db_g, w + L.bwd, st_);
+}
+
+nt_status nt_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor, double original_len,
+                        double low, double high, uint64_t* turns) {
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > 65536)
+    return fail(NT_ERR_INVALID, "rot_dim=%d must be even, in [2, 65536]", rot_dim);
+  if (!turns) return fail(NT_ERR_INVALID, "turns is NULL");
+  if (!(base > 0) || std::isinf(base)) return fail(NT_ERR_INVALID, "base must be finite and > 0");
+  if (scaling < NT_ROPE_NONE || scaling > NT_ROPE_BANDS) return fail(NT_ERR_INVALID, "bad scaling %d", scaling);
+  if (scaling != NT_ROPE_NONE && (!(factor > 0) || std::isinf(factor)))
+    return fail(NT_ERR_INVALID, "factor must be finite and > 0");
+  if (scaling == NT_ROPE_BANDS && (!(original_len > 0) || std::isinf(original_len) || !(low < high) ||
+                                   std::isinf(low) || std::isinf(high)))
+    return fail(NT_ERR_INVALID, "bands need original_len > 0 and low < high");
+  const double two_pi = 6.283185307179586476925;
+  if (scaling == NT_ROPE_NTK && rot_dim > 2) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = std::pow(base, -2.0 * j / rot_dim);
+    if (scaling == NT_ROPE_LINEAR) f /= factor;
+    if (scaling == NT_ROPE_BANDS) {
+      double g = (original_len * f / two_pi - low) / (high - low);
+      g = g < 0 ? 0 : g > 1 ? 1 : g;
+      f *= (1 - g) / factor + g;
+    }
+    const double t = f / two_pi;
+    if (!std::isfinite(t)) return fail(NT_ERR_INVALID, "frequency %d is not finite", j);
+    turns[j] = (uint64_t)std::ldexp(t - std::floor(t), 64);     // the fraction is below 1 - 2^-53
+  }
+  return NT_OK;
+}
+
+nt_status nt_qk_norm_rope(nt_dtype dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          int64_t T, int32_t H_q, int32_t H_k, int32_t d, const float* q_gamma,
+                          const float* k_gamma, float eps, const int32_t* d_cu_seqlens, int32_t B,
+                          const int32_t* d_pos0, const int32_t* d_positions, const uint64_t* d_turns,
+                          int32_t rot_dim, int32_t interleaved, float rot_scale, void* q_out,
+                          int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  nt_status st = check_rope(dtype, T, H_q, H_k, d, eps, d_cu_seqlens, B, d_pos0, d_positions, d_turns, rot_dim,
+                            interleaved, rot_scale);
+  if (st == NT_OK) st = check_tokens(dtype, "q", q, q_stride, T, H_q, d);
+  if (st == NT_OK) st = check_tokens(dtype, "k", k, k_stride, T, H_k, d);
+  if (st == NT_OK) st = check_tokens(dtype, "q_out", q_out, q_out_stride, T, H_q, d);
+  if (st == NT_OK) st = check_tokens(dtype, "k_out", k_out, k_out_stride, T, H_k, d);
+  if (st != NT_OK) return st;
+  if (!aligned16(q_gamma) || !aligned16(k_gamma)) return fail(NT_ERR_INVALID, "gammas must be 16-byte aligned");
+  if (T > 0 && ((H_q > 0 && q_out == q && q_out_stride != q_stride) ||
+                (H_k > 0 && k_out == k && k_out_stride != k_stride)))
+    return fail(NT_ERR_INVALID, "in place needs equal strides");
+  if (T == 0 || (H_q == 0 && H_k == 0)) return NT_OK;
+  RopeProblem p = {};
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.T = T;
+  p.H_q = H_q;
+  p.H_k = H_k;
+  p.d = d;
+  p.q_gamma = q_gamma;
+  p.k_gamma = k_gamma;
+  p.eps = eps;
+  p.cu = d_cu_seqlens;
+  p.B = B;
+  p.pos0 = d_pos0;
+  p.positions = d_positions;
+  p.turns = d_turns;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved;
+  p.rot_scale = rot_scale;
+  const cudaError_t e = launch_qk_rope(dtype, p, false, nullptr, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk norm and rope launch");
+  return NT_OK;
+}
+
+size_t nt_qk_norm_rope_bwd_workspace_bytes(int32_t d) {
+  if (d <= 0 || d > 256) return 0;
+  return qk_rope_bwd_workspace_bytes(d);
+}
+
+nt_status nt_qk_norm_rope_bwd(nt_dtype dtype, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                              int64_t dk_out_stride, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, int64_t T, int32_t H_q, int32_t H_k, int32_t d,
+                              const float* q_gamma, const float* k_gamma, float eps, const int32_t* d_cu_seqlens,
+                              int32_t B, const int32_t* d_pos0, const int32_t* d_positions, const uint64_t* d_turns,
+                              int32_t rot_dim, int32_t interleaved, float rot_scale, void* dq, int64_t dq_stride,
+                              void* dk, int64_t dk_stride, float* dq_gamma, float* dk_gamma, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  nt_status st = check_rope(dtype, T, H_q, H_k, d, eps, d_cu_seqlens, B, d_pos0, d_positions, d_turns, rot_dim,
+                            interleaved, rot_scale);
+  if (st == NT_OK) st = check_tokens(dtype, "dq_out", dq_out, dq_out_stride, T, H_q, d);
+  if (st == NT_OK) st = check_tokens(dtype, "dk_out", dk_out, dk_out_stride, T, H_k, d);
+  if (st == NT_OK && q_gamma) st = check_tokens(dtype, "q", q, q_stride, T, H_q, d);
+  if (st == NT_OK && k_gamma) st = check_tokens(dtype, "k", k, k_stride, T, H_k, d);
+  if (st == NT_OK) st = check_tokens(dtype, "dq", dq, dq_stride, T, H_q, d);
+  if (st == NT_OK) st = check_tokens(dtype, "dk", dk, dk_stride, T, H_k, d);
+  if (st != NT_OK) return st;
+  if (!aligned16(q_gamma) || !aligned16(k_gamma) || !aligned16(dq_gamma) || !aligned16(dk_gamma) ||
+      !aligned16(workspace))
+    return fail(NT_ERR_INVALID, "gammas, their gradients and the workspace must be 16-byte aligned");
+  if ((q_gamma != nullptr) != (dq_gamma != nullptr) || (k_gamma != nullptr) != (dk_gamma != nullptr))
+    return fail(NT_ERR_INVALID, "a gamma and its gradient go together");
+  if (T > 0 && ((H_q > 0 && dq == dq_out && dq_stride != dq_out_stride) ||
+                (H_k > 0 && dk == dk_out && dk_stride != dk_out_stride)))
+    return fail(NT_ERR_INVALID, "in place needs equal strides");
+  if ((q_gamma || k_gamma) && (!workspace || workspace_bytes < qk_rope_bwd_workspace_bytes(d)))
+    return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace ? workspace_bytes : (size_t)0,
+                qk_rope_bwd_workspace_bytes(d));
+  RopeProblem p = {};
+  p.q = q;
+  p.k = k;
+  p.dq_out = dq_out;
+  p.dk_out = dk_out;
+  p.q_out = dq;
+  p.k_out = dk;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.dq_out_stride = dq_out_stride;
+  p.dk_out_stride = dk_out_stride;
+  p.q_out_stride = dq_stride;
+  p.k_out_stride = dk_stride;
+  p.T = H_q == 0 && H_k == 0 ? 0 : T;
+  p.H_q = H_q;
+  p.H_k = H_k;
+  p.d = d;
+  p.q_gamma = q_gamma;
+  p.k_gamma = k_gamma;
+  p.eps = eps;
+  p.cu = d_cu_seqlens;
+  p.B = B;
+  p.pos0 = d_pos0;
+  p.positions = d_positions;
+  p.turns = d_turns;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved;
+  p.rot_scale = rot_scale;
+  p.dq_gamma = dq_gamma;
+  p.dk_gamma = dk_gamma;
+  const cudaError_t e = launch_qk_rope(dtype, p, true, static_cast<float*>(workspace), status_word(),
+                                       static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk norm and rope backward launch");
+  return NT_OK;
+}
+
+nt_status nt_paged_write(const nt_kv_pages* pages, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         int64_t T, const int32_t* d_cu_seqlens, int32_t B, const int32_t* d_pos0,
+                         const int32_t* d_block_table, int32_t max_pages, void* stream) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (T < 0 || B < 0) return fail(NT_ERR_INVALID, "bad sizes T=%lld B=%d", (long long)T, B);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  st = check_table(d_block_table, max_pages, B);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "k", k, k_stride, T, pages->H_kv, pages->d);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "v", v, v_stride, T, pages->H_kv, pages->d);
+  if (st != NT_OK) return st;
+  if (T > 0 && (B == 0 || !d_cu_seqlens)) return fail(NT_ERR_INVALID, "T > 0 with no segments");
+  if ((reinterpret_cast<uintptr_t>(d_cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(d_pos0) & 3u))
+    return fail(NT_ERR_INVALID, "d_cu_seqlens or d_pos0 misaligned");
+  if (T == 0) return NT_OK;
+  const int64_t es = (int64_t)esize(pages->dtype);
+  const cudaError_t e = launch_paged_write(pool_of(pages), k, k_stride * es, v, v_stride * es, T, d_cu_seqlens, B,
+                                           d_pos0, d_block_table, max_pages, status_word(),
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged write launch");
+  return NT_OK;
+}
+
+nt_status nt_paged_copy(const nt_kv_pages* pages, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (n < 0) return fail(NT_ERR_INVALID, "n=%lld < 0", (long long)n);
+  if (n == 0) return NT_OK;
+  if (!src || !dst) return fail(NT_ERR_INVALID, "NULL page list");
+  if (n > pages->n_pages) return fail(NT_ERR_INVALID, "%lld copies among %d pages", (long long)n, pages->n_pages);
+  // which pages are destinations: one bit per page
+  const size_t words = ((size_t)pages->n_pages + 63) / 64;
+  uint64_t* is_dst = static_cast<uint64_t*>(std::calloc(words, sizeof(uint64_t)));
+  if (!is_dst) return fail(NT_ERR_INVALID, "no host memory for %zu bytes", words * sizeof(uint64_t));
+  for (int64_t i = 0; i < n && st == NT_OK; ++i) {
+    const int32_t p = dst[i];
+    if (p < 0 || p >= pages->n_pages || src[i] < 0 || src[i] >= pages->n_pages)
+      st = fail(NT_ERR_INVALID, "copy %lld: pages %d -> %d of %d", (long long)i, src[i], p, pages->n_pages);
+    else if (is_dst[p >> 6] >> (p & 63) & 1)
+      st = fail(NT_ERR_INVALID, "copy %lld: page %d is written twice", (long long)i, p);
+    else
+      is_dst[p >> 6] |= 1ull << (p & 63);
+  }
+  for (int64_t i = 0; i < n && st == NT_OK; ++i)
+    if (is_dst[src[i] >> 6] >> (src[i] & 63) & 1)
+      st = fail(NT_ERR_INVALID, "copy %lld: page %d is read and written", (long long)i, src[i]);
+  std::free(is_dst);
+  if (st != NT_OK) return st;
+  const cudaError_t e = launch_paged_copy(pool_of(pages), src, dst, n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+  return NT_OK;
+}
+
+size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d) {
+  if (H <= 0 || H_kv <= 0 || H % H_kv || (d != 32 && d != 64 && d != 128)) return 0;
+  return paged_attn_workspace_bytes(H / H_kv, d);
+}
+
+nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,
+                        const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (B < 0 || H <= 0) return fail(NT_ERR_INVALID, "bad sizes B=%d H=%d", B, H);
+  if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
+  if (pages->d != 32 && pages->d != 64 && pages->d != 128)
+    return fail(NT_ERR_UNSUPPORTED, "head width d=%d (32, 64 or 128)", pages->d);
+  if (!(scale > 0.f) || std::isinf(scale)) return fail(NT_ERR_INVALID, "scale must be finite and > 0");
+  st = check_table(d_block_table, max_pages, B);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "q", q, q_stride, B, H, pages->d);
+  if (st != NT_OK) return st;
+  if (B > 0 && (!d_lengths || !o || !workspace)) return fail(NT_ERR_INVALID, "NULL pointer");
+  if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(d_lengths) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(NT_ERR_INVALID, "d_lengths or lse misaligned");
+  const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
+  if (B > 0 && workspace_bytes < need)
+    return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  if (B == 0) return NT_OK;
+  const PagedAttnProblem p = {pool_of(pages), q, q_stride, B, H, pages->d, d_block_table, max_pages, d_lengths,
+                              scale, o, lse, workspace};
+  const cudaError_t e = launch_paged_attn(pages->dtype, p, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return NT_OK;
 }
 
 nt_status nt_selftest_bounded_wait(int32_t mode, uint64_t delay_ns, uint64_t limit_ns, int64_t* d_result,

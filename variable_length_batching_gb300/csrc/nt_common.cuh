@@ -318,6 +318,67 @@ size_t wgrad_tc_workspace_bytes(int64_t P, int M, int N);
 cudaError_t launch_wgrad_tc(const void* A, int lda, const void* B, int ldb, int64_t P, int M, int N, float* G,
                             float* colsum, void* workspace, unsigned int* status, cudaStream_t s);
 
+// Per-head RMS norm and rotary positions of packed q and k (bwd: their
+// gradients; then q_out / k_out are the input gradients and dq_out / dk_out
+// the upstream ones).  Strides are in elements between tokens.
+struct RopeProblem {
+  const void* q;
+  const void* k;
+  const void* dq_out;
+  const void* dk_out;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, dq_out_stride, dk_out_stride, q_out_stride, k_out_stride;
+  int64_t T;
+  int H_q, H_k, d;
+  const float* q_gamma;
+  const float* k_gamma;
+  float eps;
+  const int32_t* cu;
+  int B;
+  const int32_t* pos0;
+  const int32_t* positions;
+  const uint64_t* turns;
+  int rot_dim, interleaved;
+  float rot_scale;
+  float* dq_gamma;
+  float* dk_gamma;
+};
+constexpr int kRopeMaxParts = 1024;     // CTAs of the backward, at most
+size_t qk_rope_bwd_workspace_bytes(int d);
+cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* workspace, unsigned int* status,
+                           cudaStream_t s);
+
+// The pages of a key/value cache: k and v [n_pages][H][page_size][d].
+struct PagedPool {
+  void* k;
+  void* v;
+  int n_pages, page_size, H, row_bytes;   // row_bytes = d * element size
+};
+cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stride_bytes, const void* v,
+                               int64_t v_stride_bytes, int64_t T, const int32_t* cu, int B, const int32_t* pos0,
+                               const int32_t* table, int max_pages, unsigned int* status, cudaStream_t s);
+cudaError_t launch_paged_copy(const PagedPool& p, const int32_t* src, const int32_t* dst, int64_t n, cudaStream_t s);
+
+// One query token per sequence over a paged cache.
+struct PagedAttnProblem {
+  PagedPool pool;
+  const void* q;          // [B] tokens of [H, d], q_stride elements apart
+  int64_t q_stride;
+  int B, H, d;
+  const int32_t* table;   // [B, max_pages]
+  int max_pages;
+  const int32_t* lengths;
+  float scale;
+  void* o;                // [B, H, d]
+  float* lse;             // [H, B] or NULL
+  void* workspace;
+};
+constexpr int kPagedMaxCtas = 512;      // CTAs of the split, at most (two partial results each)
+constexpr int kPagedMaxHeads = 16;      // query heads of one item, at most
+size_t paged_attn_workspace_bytes(int G, int d);
+cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
+
 bool attn_simt_supported(int d);
 cudaError_t launch_attn_simt(nt_dtype dt, const AttnProblem& p, unsigned int* status, cudaStream_t s);
 bool attn_tc_supported(nt_dtype dt, int d);

@@ -37,10 +37,17 @@ class nt_partition(ctypes.Structure):
                 ("T_cols", ctypes.c_int64), ("max_col_len", ctypes.c_int32)]
 
 
+class nt_kv_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 _lib = None
 
 _P, _I32, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _PP = ctypes.POINTER(nt_partition)
+_PG, _D = ctypes.POINTER(nt_kv_pages), ctypes.c_double
 SIGNATURES = {
     "nt_partition_build": (_I32, [_P, _I32, _P, _P, _P, _PP, _P]),
     "nt_partition_build_rect": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _PP, _P]),
@@ -77,6 +84,16 @@ SIGNATURES = {
     "nt_varlen_attn_bwd_workspace_bytes": (_SZ, [_I64, _I32]),
     "nt_varlen_attn_bwd": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _I32, _I32, _I32, _I32,
                                   _F, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "nt_rope_turns": (_I32, [_I32, _D, _I32, _D, _D, _D, _D, _P]),
+    "nt_qk_norm_rope": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _F, _P, _I32, _P, _P, _P,
+                               _I32, _I32, _F, _P, _I64, _P, _I64, _P]),
+    "nt_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I32]),
+    "nt_qk_norm_rope_bwd": (_I32, [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _F,
+                                   _P, _I32, _P, _P, _P, _I32, _I32, _F, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "nt_paged_write": (_I32, [_PG, _P, _I64, _P, _I64, _I64, _P, _I32, _P, _P, _I32, _P]),
+    "nt_paged_copy": (_I32, [_PG, _P, _P, _I64, _P]),
+    "nt_paged_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "nt_paged_attn": (_I32, [_PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_device_status": (_I32, [_P]),
     "nt_selftest_bounded_wait": (_I32, [_I32, ctypes.c_uint64, ctypes.c_uint64, _P, _P]),
     "nt_status_str": (ctypes.c_char_p, [_I32]),
@@ -582,6 +599,281 @@ def nt_varlen_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: tor
                                   ws.numel(), _stream(stream))
     _check(st, "nt_varlen_attn_bwd")
     return dq, dk, dv
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
+
+
+def nt_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_len: float = 0.0, low: float = 1.0, high: float = 32.0, device=None) -> torch.Tensor:
+    """The rotary frequency table (rot_dim / 2 fractions of a turn per
+    position, 64-bit, held as int64), formed on the host and placed on
+    ``device``: made once and kept.  ``scaling``: "none", "linear" (positions
+    interpolated by ``factor``), "ntk" (the base stretched) or "bands" (pairs
+    that turn at most ``low`` times in ``original_len`` positions interpolated,
+    those that turn ``high`` times or more kept, a ramp between)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"unknown scaling {scaling!r}: one of {', '.join(ROPE_SCALING)}")
+    t = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.int64)
+    _check(lib().nt_rope_turns(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor), float(original_len),
+                               float(low), float(high), t.data_ptr()), "nt_rope_turns")
+    return t if device is None else t.to(device)
+
+
+def _on(t: Optional[torch.Tensor], dev, dtype=None, name: str = "tensor"):
+    """Address of a contiguous tensor that must live on ``dev`` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _tokens(t: Optional[torch.Tensor], dev, dtype, name: str):
+    """(address, token stride) of packed tokens (T, H, d) whose heads are
+    contiguous within a token; tokens may be any stride apart."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, d)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    T, H, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * d
+
+
+class _launch:
+    """The device and stream of one call: makes ``dev`` current while the
+    call runs if it is not, and gives the stream's handle."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.prev = None
+        self.dev = dev
+        self.stream = stream
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if self.dev.index != cur:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+        s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma):
+    """Shapes, device and position arguments of the rope calls."""
+    t = q if q is not None else k
+    if t is None:
+        raise ValueError("q or k is needed")
+    if t.dim() != 3:
+        raise ValueError("q and k must be (tokens, heads, d)")
+    T, d, dev = t.shape[0], t.shape[2], t.device
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != d):
+        raise ValueError("q and k must share their tokens and head width")
+    if positions is not None and (cu_seqlens is not None or pos0 is not None):
+        raise ValueError("give positions or cu_seqlens (with pos0), not both")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("one position per token")
+    if pos0 is not None and (cu_seqlens is None or pos0.numel() != cu_seqlens.numel() - 1):
+        raise ValueError("pos0 is one start per cu_seqlens segment")
+    for g in (q_gamma, k_gamma):
+        if g is not None and g.numel() != d:
+            raise ValueError("gammas must have d entries")
+    i32 = torch.int32
+    B = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens has B + 1 entries")
+    tail = (_on(cu_seqlens, dev, i32, "cu_seqlens"), B, _on(pos0, dev, i32, "pos0"),
+            _on(positions, dev, i32, "positions"), _on(turns, dev, torch.int64, "turns"),
+            0 if turns is None else 2 * turns.numel())
+    return T, d, dev, t.dtype, tail
+
+
+def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns: Optional[torch.Tensor],
+                    cu_seqlens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    pos0: Optional[torch.Tensor] = None, q_gamma: Optional[torch.Tensor] = None,
+                    k_gamma: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                    rot_scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                    k_out: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of every head (where a gamma is given) and rotary positions
+    of packed q (T, H_q, d) and k (T, H_k, d), in one pass: returns (q_out,
+    k_out).  Positions run from 0 (or ``pos0``) within each ``cu_seqlens``
+    segment, or are given as ``positions``.  ``turns`` from nt_rope_turns
+    sets the rotated columns (None: norm only).  q and k may be slices of a
+    fused projection; ``q_out=q, k_out=k`` works in place."""
+    T, d, dev, dt, tail = _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+    for x, y in ((q, q_out), (k, k_out)):
+        if (x is None) != (y is None) or (x is not None and x.shape != y.shape):
+            raise ValueError("outputs must have their inputs' shapes")
+    qp, qs = _tokens(q, dev, dt, "q")
+    kp, ks = _tokens(k, dev, dt, "k")
+    qo, qos = _tokens(q_out, dev, dt, "q_out")
+    ko, kos = _tokens(k_out, dev, dt, "k_out")
+    f32 = torch.float32
+    with _launch(dev, stream) as s:
+        st = lib().nt_qk_norm_rope(_dtype(q if q is not None else k), qp, qs, kp, ks, T,
+                                   0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d,
+                                   _on(q_gamma, dev, f32, "q_gamma"), _on(k_gamma, dev, f32, "k_gamma"), float(eps),
+                                   *tail, int(bool(interleaved)), float(rot_scale), qo, qos, ko, kos, s)
+        _check(st, "nt_qk_norm_rope")
+    return q_out, k_out
+
+
+def nt_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    return int(lib().nt_qk_norm_rope_bwd_workspace_bytes(int(d)))
+
+
+def nt_qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor],
+                        turns: Optional[torch.Tensor], q: Optional[torch.Tensor] = None,
+                        k: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                        positions: Optional[torch.Tensor] = None, pos0: Optional[torch.Tensor] = None,
+                        q_gamma: Optional[torch.Tensor] = None, k_gamma: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of nt_qk_norm_rope for the upstream gradients of its outputs:
+    (dq, dk, dq_gamma, dk_gamma), the gammas' in fp32, None where there is no
+    input.  ``q`` and ``k`` are the forward's inputs, needed for the sides
+    that have a gamma."""
+    T, d, dev, dt, tail = _rope_args(dq_out, dk_out, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
+    f32 = torch.float32
+    for x, u, g, name in ((q, dq_out, q_gamma, "q"), (k, dk_out, k_gamma, "k")):
+        if g is not None and (x is None or u is None or x.shape != u.shape):
+            raise ValueError(f"{name}'s norm needs {name} and its upstream gradient, of one shape")
+    dq = None if dq_out is None else torch.empty(dq_out.shape, dtype=dt, device=dev)
+    dk = None if dk_out is None else torch.empty(dk_out.shape, dtype=dt, device=dev)
+    dqg = None if q_gamma is None else torch.empty(d, dtype=f32, device=dev)
+    dkg = None if k_gamma is None else torch.empty(d, dtype=f32, device=dev)
+    if workspace is None and (q_gamma is not None or k_gamma is not None):
+        workspace = torch.empty(nt_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
+    uq, uqs = _tokens(dq_out, dev, dt, "dq_out")
+    uk, uks = _tokens(dk_out, dev, dt, "dk_out")
+    qp, qs = _tokens(q if q_gamma is not None else None, dev, dt, "q")
+    kp, ks = _tokens(k if k_gamma is not None else None, dev, dt, "k")
+    H_q = 0 if dq_out is None else dq_out.shape[1]
+    H_k = 0 if dk_out is None else dk_out.shape[1]
+    with _launch(dev, stream) as s:
+        st = lib().nt_qk_norm_rope_bwd(
+            _dtype(dq_out if dq_out is not None else dk_out), uq, uqs, uk, uks, qp, qs, kp, ks, T, H_q, H_k, d,
+            _on(q_gamma, dev, f32, "q_gamma"), _on(k_gamma, dev, f32, "k_gamma"), float(eps), *tail,
+            int(bool(interleaved)), float(rot_scale), _on(dq, dev), H_q * d, _on(dk, dev), H_k * d, _on(dqg, dev),
+            _on(dkg, dev), _on(workspace, dev, None, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), s)
+        _check(st, "nt_qk_norm_rope_bwd")
+    return dq, dk, dqg, dkg
+
+
+class KVPages:
+    """The pages of a key/value cache: ``k`` and ``v`` (n_pages, H_kv,
+    page_size, d), contiguous device tensors the caller owns."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must share the shape (n_pages, H_kv, page_size, d), dtype and device")
+        self.k, self.v = k, v
+        self.device, self.dtype = k.device, k.dtype
+        self.n_pages, self.H_kv, self.page_size, self.d = k.shape
+        if self.device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.c = nt_kv_pages(_on(k, self.device) or None, _on(v, self.device) or None, self.n_pages, self.page_size,
+                             self.H_kv, self.d, _dtype(k))
+        self.ref = ctypes.byref(self.c)
+
+
+def _table(block_table: torch.Tensor, B: int, dev):
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be (B = {B}, max_pages)")
+    return _on(block_table, dev, torch.int32, "block_table"), block_table.shape[1]
+
+
+def nt_paged_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                   block_table: torch.Tensor, pos0: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keys and values of packed tokens (T, H_kv, d) into their sequences'
+    pages: token t of ``cu_seqlens`` segment b goes to position
+    pos0[b] + t - cu[b] (``pos0`` None: 0) of row b of ``block_table``."""
+    dev = pages.device
+    if k.shape != v.shape or k.dim() != 3 or tuple(k.shape[1:]) != (pages.H_kv, pages.d):
+        raise ValueError("k and v must be (T, H_kv, d) of the pages")
+    B = cu_seqlens.numel() - 1
+    if pos0 is not None and pos0.numel() != B:
+        raise ValueError("pos0 is one start per cu_seqlens segment")
+    kp, ks = _tokens(k, dev, pages.dtype, "k")
+    vp, vs = _tokens(v, dev, pages.dtype, "v")
+    tab, max_pages = _table(block_table, B, dev)
+    i32 = torch.int32
+    with _launch(dev, stream) as s:
+        st = lib().nt_paged_write(pages.ref, kp, ks, vp, vs, k.shape[0], _on(cu_seqlens, dev, i32, "cu_seqlens"), B,
+                                  _on(pos0, dev, i32, "pos0"), tab, max_pages, s)
+        _check(st, "nt_paged_write")
+
+
+def nt_paged_copy(pages: KVPages, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Page src[i] copied over page dst[i] (int32 HOST tensors): no page
+    twice in dst, none in both."""
+    if src.device.type != "cpu" or dst.device.type != "cpu":
+        raise ValueError("src and dst are host tensors")
+    if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be int32, one entry per copy")
+    if not (src.is_contiguous() and dst.is_contiguous()):
+        raise ValueError("src and dst must be contiguous")
+    with _launch(pages.device, stream) as s:
+        _check(lib().nt_paged_copy(pages.ref, src.data_ptr(), dst.data_ptr(), src.numel(), s), "nt_paged_copy")
+
+
+def nt_paged_attn_workspace_bytes(H: int, H_kv: int, d: int) -> int:
+    return int(lib().nt_paged_attn_workspace_bytes(int(H), int(H_kv), int(d)))
+
+
+def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one new token per sequence, q (B, H, d), over the first
+    lengths[b] positions of its paged cache; H a multiple of H_kv.  Returns
+    (o, lse [H, B] or None).  ``workspace``: nt_paged_attn_workspace_bytes()
+    bytes (None allocates them per call)."""
+    dev, d = pages.device, pages.d
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be (B, H, d) with the pages' d")
+    B, H, _ = q.shape
+    if lengths.numel() != B:
+        raise ValueError("one length per sequence")
+    qp, qs = _tokens(q, dev, pages.dtype, "q")
+    tab, max_pages = _table(block_table, B, dev)
+    if out is None:
+        out = torch.empty(B, H, d, dtype=pages.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if want_lse and lse is None:
+        lse = torch.empty(H, B, dtype=torch.float32, device=dev)
+    if lse is not None and tuple(lse.shape) != (H, B):
+        raise ValueError("lse must be (H, B)")
+    if workspace is None:
+        workspace = torch.empty(nt_paged_attn_workspace_bytes(H, pages.H_kv, d), dtype=torch.uint8, device=dev)
+    with _launch(dev, stream) as s:
+        st = lib().nt_paged_attn(pages.ref, qp, qs, B, H, tab, max_pages, _on(lengths, dev, torch.int32, "lengths"),
+                                 d ** -0.5 if scale is None else float(scale), _on(out, dev, pages.dtype, "out"),
+                                 _on(lse, dev, torch.float32, "lse"), _on(workspace, dev, None, "workspace"),
+                                 workspace.numel() * workspace.element_size(), s)
+        _check(st, "nt_paged_attn")
+    return out, lse
 
 
 def nt_device_status(stream=None) -> int:
