@@ -771,7 +771,8 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  * value are in the cache already (nt_paged_write comes first).
  *   q             [B, H, d] in the pages' dtype, sequences q_stride elements
  *                 apart (>= H * d, a multiple of 8 bf16 / 4 fp32 elements).
- *   H             a multiple of H_kv.   d in {32, 64, 128}.
+ *   H             a multiple of H_kv.   d in {32, 64, 128}.  B * max_pages *
+ *                 page_size * H at most 1e15 (NT_ERR_OVERFLOW).
  *   d_block_table [B, max_pages] int32.
  *   d_lengths     [B] int32, the positions of each sequence that are attended
  *                 to; 0 gives o = 0 and lse = -inf.  Lengths are read on the

@@ -310,6 +310,40 @@ def test_attn_two_streams(nt):
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+@pytest.mark.parametrize("d,page,H", [(128, 64, 8), (128, 16, 24), (64, 64, 8), (64, 8, 32)])
+def test_attn_long_contexts_many_times(nt, d, page, H):
+    """Contexts of tens of thousands of keys, bf16, repeated back to back on
+    one workspace: every repeat gives the first one's bits, and those are
+    right (fp64 on the device)."""
+    lens, Hk = [70001, 40000, 3, 65536], 2
+    need = [-(-n // page) for n in lens]
+    ids = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    table = torch.zeros(4, max(need), dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    kp = torch.randn(at, Hk, page, d, generator=gen, device=DEV, dtype=BF)
+    vp = torch.randn(at, Hk, page, d, generator=gen, device=DEV, dtype=BF)
+    q = 2 * torch.randn(4, H, d, generator=gen, device=DEV, dtype=BF)
+    pages, tab, ln = nt.KVPages(kp, vp), table.to(DEV), _i32(lens)
+    ws = torch.empty(nt.nt_paged_attn_workspace_bytes(H, Hk, d), dtype=torch.uint8, device=DEV)
+    outs = [nt.nt_paged_attn(pages, q, tab, ln, workspace=ws)[0] for _ in range(60)]
+    nt.nt_device_status()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    for b, n in enumerate(lens):
+        rows = tab[b, :need[b]].long()
+        k = kp[rows].transpose(0, 1).reshape(Hk, -1, d)[:, :n].double()
+        v = vp[rows].transpose(0, 1).reshape(Hk, -1, d)[:, :n].double()
+        qb = q[b].double().reshape(Hk, -1, d)
+        p = torch.softmax(qb @ k.transpose(1, 2) * d ** -0.5, -1)
+        ro, mag = (p @ v).reshape(H, d).cpu(), (p @ v.abs()).reshape(H, d).cpu()
+        cond = ((qb.abs() @ k.abs().transpose(1, 2)).amax(-1) * d ** -0.5).reshape(H, 1).cpu()
+        err = (outs[0][b].double().cpu() - ro).abs()
+        assert bool((err <= attn_bound(ro, mag, cond, n, BF)).all())
+
+
 def test_attn_far_page_offsets(nt):
     """Pages behind 2^31 elements of the pool are addressed in full."""
     page, Hk, d = 256, 64, 128

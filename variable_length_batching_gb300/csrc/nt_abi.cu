@@ -1137,6 +1137,9 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(d_lengths) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(NT_ERR_INVALID, "d_lengths or lse misaligned");
+  if ((double)B * max_pages * pages->page_size * H > 1e15)
+    return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e15",
+                (double)B * max_pages * pages->page_size * H);
   const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
   if (B > 0 && workspace_bytes < need)
     return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);

@@ -79,6 +79,33 @@ __device__ __forceinline__ void flag_device(unsigned int* status, unsigned int b
   if (status) atomicOr(status, bits);
 }
 
+// Segment of packed token t: the last b in [0, B) with cu[b] <= t (0 if there
+// is none; the caller checks that the segment holds t).  One thread's search,
+// and one by a whole warp for one token, 32 probes a step, every lane with
+// the result.
+__device__ __forceinline__ int segment_of_thread(const int32_t* cu, int B, int64_t t) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
+    if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int segment_of_warp(const int32_t* cu, int B, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;                       // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int64_t at = (int64_t)lane * step;
+    const bool below = at < n && cu[lo + at] <= t;
+    const int c = max(1, __popc(__ballot_sync(0xffffffffu, below)));
+    const int skip = (c - 1) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
 // Programmatic dependent launch.  A kernel started by launch_pdl may begin
 // while the kernel before it in the stream is still running: every thread
 // calls pdl_wait() before it reads or writes global memory that kernel
@@ -378,6 +405,9 @@ constexpr int kPagedMaxCtas = 512;      // CTAs of the split, at most (two parti
 constexpr int kPagedMaxHeads = 16;      // query heads of one item, at most
 size_t paged_attn_workspace_bytes(int G, int d);
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
+// The tensor-core kernel: bf16, d = 64 or 128, pages of a multiple of 8.
+bool paged_attn_tc_supported(nt_dtype dt, const PagedAttnProblem& p);
+cudaError_t launch_paged_attn_tc(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 
 bool attn_simt_supported(int d);
 cudaError_t launch_attn_simt(nt_dtype dt, const AttnProblem& p, unsigned int* status, cudaStream_t s);

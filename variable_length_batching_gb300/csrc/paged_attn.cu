@@ -23,6 +23,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 64;           // keys per unit of the split
 constexpr int kHeads = 8;           // query heads of one item, at most
+constexpr int kExtra = 2;           // an item's cost beside its tiles, in tiles
 
 template <int N>
 __device__ __forceinline__ void load_row(const float* p, float* x) {
@@ -69,7 +70,8 @@ __device__ __forceinline__ float butterfly(float (&v)[32]) {
 
 template <typename T, int D, int GP>
 __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnProblem p, int items, int hgroups,
-                                                              int G, float scale_log2, unsigned int* status) {
+                                                              int G, bool whole_items, float scale_log2,
+                                                              unsigned int* status) {
   constexpr int N = D / 32;          // elements of a row per lane
   constexpr int KB = 32 / GP;        // keys of a batch
   __shared__ PagedPlanShared plan;
@@ -79,8 +81,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
   const int64_t cap = min64((int64_t)p.max_pages * p.pool.page_size, 0x7fffffff);
   const int heads = min(kHeads, G);
   const PagedPartials part = paged_partials(p.workspace, gridDim.x, heads);
-  paged_plan(p.lengths, p.B, cap, items, kTile, blockIdx.x, gridDim.x, &plan, status, kThreads);
-  if (threadIdx.x < 2) part.id[2 * blockIdx.x + threadIdx.x] = -1;
+  pdl_wait();
+  pdl_trigger();
+  paged_plan(p.lengths, p.B, cap, items, kTile, kExtra, blockIdx.x, gridDim.x, &plan, status, kThreads);
   // sequences with no key: zeros
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (paged_length(p.lengths, b, cap, nullptr) != 0) continue;
@@ -90,10 +93,11 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
       for (int h = threadIdx.x; h < p.H; h += kThreads) p.lse[(int64_t)h * p.B + b] = -INFINITY;
   }
   PagedWalk w;
-  w.init(&plan, p.lengths, cap, kTile);
+  w.init(&plan, p.lengths, cap, kTile, kExtra, whole_items);
   const int ps = p.pool.page_size;
-  const int my_head = lane % GP, my_key = lane / GP;
-  while (w.next(p.lengths, p.B, cap, items, kTile)) {
+  const int my_key = lane / GP;
+  int64_t open_id = -1, open_parts = 0;      // the item left unfinished
+  while (w.next(p.lengths, p.B, cap, items, kTile, kExtra)) {
     const int kvh = w.seg_item / hgroups, h0 = (w.seg_item % hgroups) * kHeads;
     const int nh = min(kHeads, G - h0);                      // query heads of the item
     const int64_t qh = (int64_t)kvh * G + h0;                // the first of them
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
 #pragma unroll
         for (int c = 0; c < N; ++c) q[g][c] = 0.f;
     float o[GP][N] = {};
-    float m = -INFINITY, l = 0.f;            // of head my_head, over this lane's keys' batch mates
+    float m = -INFINITY, l = 0.f;            // of head lane % GP
     const int k_end = (int)min64((int64_t)w.seg_len, w.t1 * kTile);
     const int32_t* table = p.table + (int64_t)w.seg_b * p.max_pages;
     for (int64_t kb = w.t0 * kTile + warp * KB; kb < k_end; kb += kWarps * KB) {
@@ -203,51 +207,95 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
         }
       }
     }
-    if (!whole && threadIdx.x == 0) part.id[slot] = (int64_t)w.seg_b * items + w.seg_item;
+    if (w.begins && !w.ends) {
+      open_id = (int64_t)w.seg_b * items + w.seg_item;
+      open_parts = w.parts(&plan, kExtra, blockIdx.x, gridDim.x);
+    }
     __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    part.id[2 * blockIdx.x] = open_id;
+    part.id[2 * blockIdx.x + 1] = open_parts;
   }
 }
 
-// One CTA per (CTA of the split, head of an item): if that CTA began an item
-// it did not finish, the following CTAs' slots 0 with the same item are the
-// rest of it.  Partials are added in CTA order within each thread row, and
-// the rows in order, so the result does not depend on scheduling.
-template <typename T>
+// One CTA per (CTA of the split, head of an item): joins the item that CTA
+// began and left unfinished, whose rest is the slots 0 of the CTAs after it.
+// Four columns per thread; a row of threads takes every rows-th partial with
+// a running maximum, then the rows are joined in order, so the result does
+// not depend on scheduling.
+template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnProblem p, int ctas, int items, int heads,
                                                          int hgroups, int G) {
-  __shared__ float red[256];
-  __shared__ int count;
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+  __shared__ float4 red[kRows][kLanes];
+  __shared__ float red_m[kRows], red_l[kRows];
+  pdl_wait();
   const int stride = min(heads, G);
   const PagedPartials part = paged_partials(p.workspace, ctas, stride);
-  const int c0 = blockIdx.x, g = blockIdx.y, D = p.d;
-  const int64_t id = part.id[2 * c0 + 1];
+  const int c0 = blockIdx.x, g = blockIdx.y;
+  const longlong2 open = *reinterpret_cast<const longlong2*>(part.id + 2 * c0);
+  const int64_t id = open.x;
   if (id < 0) return;
+  const int n = (int)open.y;                       // partial i: slot 1 of c0, then slot 0 of c0 + i
   const int b = (int)(id / items), item = (int)(id % items);
-  const int kvh = item / hgroups, h0 = (item % hgroups) * heads;
+  const int h0 = (item % hgroups) * heads;
   if (h0 + g >= G) return;
-  const int64_t h = (int64_t)kvh * G + h0 + g;
-  if (threadIdx.x == 0) count = 0;
+  const int64_t h = (int64_t)(item / hgroups) * G + h0 + g;
+  const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = row; i < n; i += kRows) {
+    const int64_t s = (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * stride + g;
+    const float2 ml = *reinterpret_cast<const float2*>(part.ml + s * 2);
+    const float4 v = *reinterpret_cast<const float4*>(part.o + s * D + 4 * lane);
+    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - base), fi = exp2f(ml.x - base);
+    m = mn;
+    l = l * f + ml.y * fi;
+    o.x = o.x * f + v.x * fi;
+    o.y = o.y * f + v.y * fi;
+    o.z = o.z * f + v.z * fi;
+    o.w = o.w * f + v.w * fi;
+  }
+  red[row][lane] = o;
+  if (lane == 0) {
+    red_m[row] = m;
+    red_l[row] = l;
+  }
   __syncthreads();
-  int mine = 0;
-  for (int c = c0 + 1 + threadIdx.x; c < ctas; c += 256) mine += part.id[2 * c] == id;
-  if (mine) atomicAdd(&count, mine);
-  __syncthreads();
-  const int n = count + 1;                         // partial i: slot 1 of c0, then slot 0 of c0 + i
-  auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * stride + g; };
-  float mm = -INFINITY;
-  for (int i = 0; i < n; ++i) mm = fmaxf(mm, part.ml[slot(i) * 2]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-  for (int i = 0; i < n; ++i) ll += exp2f(part.ml[slot(i) * 2] - base) * part.ml[slot(i) * 2 + 1];
-  const int c = threadIdx.x % D, row = threadIdx.x / D, rows = 256 / D;
-  float oo = 0.f;
-  for (int i = row; i < n; i += rows) oo += exp2f(part.ml[slot(i) * 2] - base) * part.o[slot(i) * D + c];
-  red[threadIdx.x] = oo;
-  __syncthreads();
-  if (row == 0) {
-    for (int r = 1; r < rows; ++r) oo += red[r * D + c];
-    static_cast<T*>(p.o)[((int64_t)b * p.H + h) * D + c] = from_f32<T>(oo / ll);
-    if (p.lse && c == 0) p.lse[h * p.B + b] = (mm + log2f(ll)) * 0.6931471805599453f;
+  if (row != 0) return;
+  const int rows = min(n, kRows);
+  for (int r = 1; r < rows; ++r) m = fmaxf(m, red_m[r]);
+  const float base = m == -INFINITY ? 0.f : m;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r = 0; r < rows; ++r) {
+    const float f = exp2f(red_m[r] - base);
+    const float4 v = red[r][lane];
+    l += red_l[r] * f;
+    o.x += v.x * f;
+    o.y += v.y * f;
+    o.z += v.z * f;
+    o.w += v.w * f;
+  }
+  T* out = static_cast<T*>(p.o) + ((int64_t)b * p.H + h) * D + 4 * lane;
+  out[0] = from_f32<T>(o.x / l);
+  out[1] = from_f32<T>(o.y / l);
+  out[2] = from_f32<T>(o.z / l);
+  out[3] = from_f32<T>(o.w / l);
+  if (p.lse && lane == 0) p.lse[h * p.B + b] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <typename T>
+cudaError_t join(const PagedAttnProblem& p, int ctas, int items, int heads, cudaStream_t s) {
+  const int G = p.H / p.pool.H, hgroups = items / p.pool.H;
+  const dim3 grid(ctas, min(heads, G)), block(256);
+  switch (p.d) {
+    case 32: return launch_pdl(paged_join_kernel<T, 32>, grid, block, 0, s, p, ctas, items, heads, hgroups, G);
+    case 64: return launch_pdl(paged_join_kernel<T, 64>, grid, block, 0, s, p, ctas, items, heads, hgroups, G);
+    default: return launch_pdl(paged_join_kernel<T, 128>, grid, block, 0, s, p, ctas, items, heads, hgroups, G);
   }
 }
 
@@ -255,9 +303,10 @@ template <typename T, int D, int GP>
 cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
   const int G = p.H / p.pool.H, hgroups = (G + kHeads - 1) / kHeads, items = p.pool.H * hgroups;
   const int ctas = min(2 * sm_count(), kPagedMaxCtas);
-  paged_attn_kernel<T, D, GP><<<ctas, kThreads, 0, s>>>(p, items, hgroups, G, p.scale * 1.4426950408889634f, status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const bool whole = paged_whole_items(p, sizeof(T));
+  cudaError_t e = launch_pdl(paged_attn_kernel<T, D, GP>, dim3(ctas), dim3(kThreads), 0, s, p, items, hgroups, G,
+                             whole, p.scale * 1.4426950408889634f, status);
+  if (e != cudaSuccess || whole) return e;
   return launch_paged_join(sizeof(T) == 2 ? NT_BF16 : NT_F32, p, ctas, items, kHeads, s);
 }
 
@@ -290,15 +339,12 @@ size_t paged_attn_workspace_bytes(int G, int d) {
 
 cudaError_t launch_paged_join(nt_dtype dt, const PagedAttnProblem& p, int ctas, int items, int heads,
                               cudaStream_t s) {
-  const int G = p.H / p.pool.H, hgroups = items / p.pool.H;
-  const dim3 grid(ctas, min(heads, G));
-  if (dt == NT_BF16) paged_join_kernel<bf16><<<grid, 256, 0, s>>>(p, ctas, items, heads, hgroups, G);
-  else paged_join_kernel<float><<<grid, 256, 0, s>>>(p, ctas, items, heads, hgroups, G);
-  return cudaGetLastError();
+  return dt == NT_BF16 ? join<bf16>(p, ctas, items, heads, s) : join<float>(p, ctas, items, heads, s);
 }
 
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
+  if (paged_attn_tc_supported(dt, p)) return launch_paged_attn_tc(p, status, s);
   return dt == NT_BF16 ? run_d<bf16>(p, status, s) : run_d<float>(p, status, s);
 }
 

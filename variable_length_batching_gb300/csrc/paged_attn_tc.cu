@@ -1,0 +1,506 @@
+// Attention of one new token per sequence over a paged key/value cache, bf16,
+// head width 64 or 128, pages of a multiple of 8 positions.
+//
+// The floor is the cache's bytes: 2 len H_kv d elements read once, for G
+// multiply-adds per element (G query heads to a key head), so the kernel is
+// a stream of TMA loads and everything else has to hide behind it.  One CTA
+// per SM holds 128 to 192 KB of key/value tiles in flight (what a latency of
+// about 1 us at the SM's share of the bandwidth needs, three times over).
+//
+// Two producer warps walk the CTA's share of the batch (paged_plan.cuh), 64
+// keys at a time, tiles alternating: one box of R = gcd(page_size, 64) keys
+// per lane, its page looked up a tile ahead, into a ring of stages in the
+// 128-byte swizzle.  (One warp takes about 1,100 cycles for a tile and 85
+// more for each box after the fourth: more than HBM takes for 64 keys of
+// d = 64.)  A third warp copies the items' query rows.  Eight
+// consumer warps take 16 keys each, four to a stage, stages alternating
+// between the two fours, every warp with its own running maximum, sum and
+// output.  A warp's part is
+//   S = Q K^T      (heads x 16 keys; rows beyond the item's heads are zero)
+//   P = exp2(S - max), rounded to bf16 for the product (the sum keeps fp32)
+//   O^T += V^T P^T (d x heads): S's accumulator layout is the B operand's, so
+//                  P goes from registers to the product, and V^T comes from
+//                  the tile by transposed matrix loads.
+// These are mma.sync products of 16 rows: a decode item has at most 16 query
+// rows where a tcgen05 tile has 64 at least, and its accumulators' round trip
+// through TMEM would be longer than the whole product.  The products and
+// matrix loads of a 32 KB stage take about a tenth of the time HBM takes to
+// deliver it.
+//
+// At the end of a segment the eight warps merge through shared memory, and
+// either write the output or leave a partial result for the join.
+#include "paged_plan.cuh"
+#include "tc_ptx.cuh"
+
+namespace nt {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 64;                   // keys per stage, and per unit of the split
+constexpr int kConsumers = 8;               // warps
+constexpr int kProducers = 2;               // warps, tiles alternating
+constexpr int kQSlots = 4;                  // items whose query rows are in flight or in use
+constexpr int kThreads = (kConsumers + kProducers + 1) * 32;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kHeads = 8 * NT;                       // query heads of an item, at most
+  static constexpr uint32_t kSide = kTile * 2 * D;            // K or V of a stage
+  static constexpr uint32_t kStage = 2 * kSide;
+  static constexpr int kRedStride = D + 4;                    // floats: keeps the merge's writes conflict-free
+  static constexpr uint32_t kRed = kConsumers * kHeads * kRedStride * 4;
+  static constexpr uint32_t kQBytes = kHeads * D * 2;
+  static constexpr int kExtra = D == 64 ? 3 : 2;               // an item's cost beside its tiles, in tiles
+  static constexpr uint32_t kFixed = kRed + kQSlots * kQBytes + 2048 /* statistics, barriers, plan */;
+  // An even number: a stage is then always the same four warps' and they see
+  // every phase of its barriers.  (With an odd number a warp would wait on a
+  // phase whose predecessor it never waited for, which parity cannot tell
+  // apart from the phase before that.)
+  static constexpr int kStages = (int)((226 * 1024 - 1024 - kFixed) / kStage) & ~1;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kFixed;
+  static_assert(kStages >= 4 && kStages % 2 == 0 && kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Ctl {
+  uint64_t full[16], empty[16], q_full[kQSlots], q_empty[kQSlots];
+  float m[kConsumers][16], l[kConsumers][16];
+  PagedPlanShared plan;
+  int abort;
+};
+static_assert(sizeof(Ctl) <= 2048, "control block");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct TcArgs {
+  const bf16* q;
+  int64_t q_stride;
+  const int32_t* table;
+  const int32_t* lengths;
+  bf16* o;
+  float* lse;
+  void* workspace;
+  int B, H, G, Hkv, max_pages, page_size, n_pages;
+  int items, hgroups, heads;      // head items per sequence; item slots of the partials
+  bool whole;                     // items are not split
+  int box;                        // keys per box: gcd(page_size, 64)
+  float scale_log2;
+  unsigned int* status;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const TcArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int kHeads = C::kHeads, S = C::kStages;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* stages = smem;
+  float* red = reinterpret_cast<float*>(smem + S * C::kStage);
+  uint8_t* qbuf = reinterpret_cast<uint8_t*>(red) + C::kRed;
+  Ctl* ctl = reinterpret_cast<Ctl*>(qbuf + kQSlots * C::kQBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t cap = min64((int64_t)a.max_pages * a.page_size, 0x7fffffff);
+  const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 4);
+    }
+    for (int i = 0; i < kQSlots; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], kConsumers);
+    }
+    ctl->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  pdl_wait();
+  pdl_trigger();
+  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status,
+             kThreads);
+  __syncthreads();
+
+  PagedWalk w;
+  w.init(&ctl->plan, a.lengths, cap, kTile, C::kExtra, a.whole);
+
+  if (warp >= kConsumers + kProducers) {
+    // ---- query rows, item by item ------------------------------------------
+    uint32_t segs = 0;
+    while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      const int slot = segs % kQSlots;
+      if (!mbar_wait_warp(&ctl->q_empty[slot], ((segs / kQSlots) & 1) ^ 1, &ctl->abort, a.status)) break;
+      const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
+      const uint32_t bytes = min(kHeads, a.G - h0) * D * 2;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl->q_full[slot], bytes);
+        bulk_load(qbuf + slot * C::kQBytes, a.q + w.seg_b * a.q_stride + (int64_t)(kvh * a.G + h0) * D, bytes,
+                  &ctl->q_full[slot]);
+      }
+      ++segs;
+    }
+    if (ctl->abort && lane == 0)                      // given up: the copies in flight land first
+      for (uint32_t i = segs > kQSlots ? segs - kQSlots : 0; i < segs; ++i)
+        mbar_wait(&ctl->q_full[i % kQSlots], (i / kQSlots) & 1, nullptr, a.status);
+    return;
+  }
+  if (warp >= kConsumers) {
+    // ---- producers: tiles warp - kConsumers, + kProducers, ... ----------------
+    const uint32_t me = warp - kConsumers;
+    const uint32_t rows = kTile / a.box;              // boxes down a tile
+    const uint32_t rb = lane % rows, side = lane / rows;
+    const bool has_box = side < 2;
+    const CUtensorMap* map = side ? &vmap : &kmap;
+    const uint32_t dst = side * C::kSide + rb * a.box * (2 * D);
+    const uint32_t ps = a.page_size, step_pg = kProducers * kTile / ps, step_row = kProducers * kTile % ps;
+    // The walk runs one of the warp's tiles ahead of the copies, so that the
+    // page lookup's latency passes behind a tile's wait.
+    uint32_t seg_it = 0;                              // the segment's first tile in the CTA's order
+    int64_t t = 0;
+    uint32_t pg = 0, row = 0;                         // of this lane's box of tile t
+    const int32_t* trow = nullptr;
+    bool more = true;
+    auto advance = [&](bool start) {
+      bool jump = start;
+      if (!start) {
+        t += kProducers;
+        pg += step_pg;
+        row += step_row;
+        if (row >= ps) {
+          row -= ps;
+          ++pg;
+        }
+        jump = t >= w.t1;
+      }
+      while (jump) {
+        if (!start) seg_it += (uint32_t)(w.t1 - w.t0);
+        start = false;
+        if (!w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+          more = false;
+          return;
+        }
+        t = w.t0 + ((me - seg_it) & (kProducers - 1));
+        jump = t >= w.t1;
+        if (!jump) {
+          const uint32_t key = (uint32_t)t * kTile + rb * a.box;
+          pg = key / ps;
+          row = key - pg * ps;
+          trow = a.table + (int64_t)w.seg_b * a.max_pages;
+        }
+      }
+    };
+    auto page_of = [&]() -> int {                     // this lane's page of tile t, -1 if it loads nothing
+      if (!more || !has_box || t * kTile + rb * a.box >= w.seg_len) return -1;
+      return trow[pg];
+    };
+    auto loads = [&]() { return more && has_box && t * kTile + rb * a.box < w.seg_len; };
+    advance(true);
+    bool mine = loads();
+    int id = page_of();
+    uint32_t last = 0;
+    bool ok = true;
+    while (more) {
+      const uint32_t it = seg_it + (uint32_t)(t - w.t0);
+      const int y = (int)row, kvh = w.seg_item / a.hgroups;
+      const bool now = mine;
+      const int page = id;
+      advance(false);
+      mine = loads();
+      id = page_of();
+      int z = page * a.Hkv + kvh;
+      if (now && (uint32_t)page >= (uint32_t)a.n_pages) {
+        flag_device(a.status, kDevCheck);
+        z = a.n_pages * a.Hkv;                        // outside the map: reads as zeros
+      }
+      const int st = it % S;
+      ok = mbar_wait_warp(&ctl->empty[st], ((it / S) & 1) ^ 1, &ctl->abort, a.status);
+      if (!ok) break;
+      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, now));
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * a.box * (2 * D));
+      __syncwarp();
+      if (now) tma_load_4d(stages + st * C::kStage + dst, map, &ctl->full[st], 0, y, 0, z);
+      last = it + 1;
+    }
+    if (!ok && lane == 0)                             // given up: the copies in flight land first
+      for (uint32_t i = 0; i < (uint32_t)S && i < last; ++i)
+        if (((last - 1 - i) & (kProducers - 1)) == me)
+          mbar_wait(&ctl->full[(last - 1 - i) % S], ((last - 1 - i) / S) & 1, nullptr, a.status);
+    return;
+  }
+
+  // ---- consumers -------------------------------------------------------------
+  // sequences with no key: zeros
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (paged_length(a.lengths, b, cap, nullptr) != 0) continue;
+    for (int e = threadIdx.x; e < a.H * D / 2; e += kConsumers * 32)
+      reinterpret_cast<uint32_t*>(a.o + (int64_t)b * a.H * D)[e] = 0;
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.H; h += kConsumers * 32) a.lse[(int64_t)h * a.B + b] = -INFINITY;
+  }
+  const int grp = warp >> 2, slice = warp & 3;
+  const int g = lane >> 2, tq = lane & 3;              // accumulator row (head) and column pair
+  // this lane's row of a 16-key slice in the matrix loads, and its 16-byte chunk's swizzle
+  const int mrow = slice * 16 + ((lane >> 4) << 3) + (lane & 7);
+  const uint32_t hs = a.box * 128;                     // a box's 64 columns; its next 64 follow
+  auto row_at = [&](int r) -> uint32_t { return (uint32_t)(r / a.box) * a.box * (2 * D) + r % a.box * 128; };
+  const uint32_t row_off = row_at(mrow);
+  const uint32_t xr = ((((uint32_t)lane >> 3) & 1) ^ (mrow & 7)) << 4;
+  uint32_t it = 0, segs = 0;
+  int64_t open_id = -1, open_parts = 0;      // the item left unfinished
+  bool ok = true;                // a warp that gave up still meets the others at the merges
+  while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+    const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
+    const int nh = min(kHeads, a.G - h0);
+    const int slot = segs % kQSlots;
+    if (ok) ok = mbar_wait_warp(&ctl->q_full[slot], (segs / kQSlots) & 1, &ctl->abort, a.status);
+    uint32_t qa[D / 16][4];
+    {
+      const uint32_t* qrow = reinterpret_cast<const uint32_t*>(qbuf + slot * C::kQBytes);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qa[ks][0] = g < nh ? qrow[(g * D + ks * 16) / 2 + tq] : 0u;
+        qa[ks][2] = g < nh ? qrow[(g * D + ks * 16 + 8) / 2 + tq] : 0u;
+        qa[ks][1] = NT == 2 && g + 8 < nh ? qrow[((g + 8) * D + ks * 16) / 2 + tq] : 0u;
+        qa[ks][3] = NT == 2 && g + 8 < nh ? qrow[((g + 8) * D + ks * 16 + 8) / 2 + tq] : 0u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+    }
+    ++segs;
+    float m[NT], l[NT], o[NT][D / 16][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+    }
+    bool active = false;
+    for (int64_t t = w.t0; t < w.t1; ++t, ++it) {
+      if ((it & 1) != (uint32_t)grp) continue;
+      const int st = it % S;
+      if (ok) ok = mbar_wait_warp(&ctl->full[st], (it / S) & 1, &ctl->abort, a.status);
+      const int left = (int)min64(w.seg_len - t * kTile - slice * 16, 16);     // keys of this slice
+      if (ok && left > 0) {
+        active = true;
+        const uint32_t kbase = smem_u32(stages + st * C::kStage), vbase = kbase + C::kSide;
+        if (left < 16) {
+          // rows behind the last key may hold anything: zeros instead, so that a probability of 0 adds 0
+          for (int e = lane; e < (16 - left) * (D / 8); e += 32) {
+            const int row = slice * 16 + left + e / (D / 8), ch = e % (D / 8);
+            *reinterpret_cast<uint4*>(stages + st * C::kStage + C::kSide + row_at(row) + (ch >> 3) * hs +
+                                      (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+        float s[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kb[4];
+          ldsm4(kbase + (ks >> 2) * hs + row_off + ((((uint32_t)ks & 3) << 5) ^ xr), kb);
+          mma16816(s[0], qa[ks], kb[0], kb[1]);
+          mma16816(s[1], qa[ks], kb[2], kb[3]);
+        }
+        uint32_t pb[NT][2];
+        float corr[NT];
+        bool moved = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float v[4] = {s[0][2 * n] * a.scale_log2, s[0][2 * n + 1] * a.scale_log2, s[1][2 * n] * a.scale_log2,
+                        s[1][2 * n + 1] * a.scale_log2};
+          if (left < 16) {
+            if (2 * tq >= left) v[0] = -INFINITY;
+            if (2 * tq + 1 >= left) v[1] = -INFINITY;
+            if (8 + 2 * tq >= left) v[2] = -INFINITY;
+            if (9 + 2 * tq >= left) v[3] = -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[n], mx);
+          const float base = mn == -INFINITY ? 0.f : mn;
+          moved |= mn > m[n];
+          corr[n] = ex2_approx(m[n] - base);
+          m[n] = mn;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = ex2_approx(v[c] - base);
+          l[n] = l[n] * corr[n] + (v[0] + v[1]) + (v[2] + v[3]);
+          pb[n][0] = pack_bf16x2(v[0], v[1]);
+          pb[n][1] = pack_bf16x2(v[2], v[3]);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          // the output's columns are heads 2 tq and 2 tq + 1: their factors sit in those rows' lanes
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float c0 = __shfl_sync(0xffffffffu, corr[n], 8 * tq);
+            const float c1 = __shfl_sync(0xffffffffu, corr[n], 8 * tq + 4);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[n][i][0] *= c0;
+              o[n][i][1] *= c1;
+              o[n][i][2] *= c0;
+              o[n][i][3] *= c1;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t va[4];
+          ldsm4_t(vbase + (i >> 2) * hs + row_off + ((((uint32_t)i & 3) << 5) ^ xr), va);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[n][i], va, pb[n][0], pb[n][1]);
+        }
+        if (left < 16) fence_async_shared();       // the zeros, before the next copy into this stage
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->empty[st]);
+    }
+    // ---- merge the warps -------------------------------------------------------
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+      if (tq == 0) {
+        ctl->m[warp][n * 8 + g] = m[n];
+        ctl->l[warp][n * 8 + g] = active ? l[n] : -1.f;      // -1: no keys, nothing to add
+      }
+    }
+    if (active) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int h = n * 8 + 2 * tq + c;
+          if (h >= nh) continue;
+          float* r = red + (warp * kHeads + h) * C::kRedStride + g;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            r[i * 16] = o[n][i][c];
+            r[i * 16 + 8] = o[n][i][c + 2];
+          }
+        }
+    }
+    named_bar_sync(1, kConsumers * 32);
+    const bool whole = w.begins && w.ends;
+    const int64_t pslot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
+    const int64_t hq = (int64_t)kvh * a.G + h0;
+    for (int e = threadIdx.x; e < nh * (D / 4); e += kConsumers * 32) {
+      const int h = e / (D / 4), c = e % (D / 4) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kConsumers; ++x) mm = fmaxf(mm, ctl->m[x][h]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kConsumers; ++x) {
+        const float lx = ctl->l[x][h];
+        if (lx == -1.f) continue;
+        const float f = ex2_approx(ctl->m[x][h] - base);
+        const float4 v = *reinterpret_cast<const float4*>(red + (x * kHeads + h) * C::kRedStride + c);
+        ll += f * lx;
+        oo.x += f * v.x;
+        oo.y += f * v.y;
+        oo.z += f * v.z;
+        oo.w += f * v.w;
+      }
+      if (whole) {
+        const float inv = 1.f / ll;
+        uint2 out = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
+        *reinterpret_cast<uint2*>(a.o + ((int64_t)w.seg_b * a.H + hq + h) * D + c) = out;
+        if (a.lse && c == 0) a.lse[(hq + h) * a.B + w.seg_b] = (mm + log2f(ll)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(part.o + (pslot * a.heads + h) * D + c) = oo;
+        if (c == 0) {
+          part.ml[(pslot * a.heads + h) * 2] = mm;
+          part.ml[(pslot * a.heads + h) * 2 + 1] = ll;
+        }
+      }
+    }
+    if (w.begins && !w.ends) {
+      open_id = (int64_t)w.seg_b * a.items + w.seg_item;
+      open_parts = w.parts(&ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
+    }
+    named_bar_sync(1, kConsumers * 32);
+  }
+  if (threadIdx.x == 0) {
+    part.id[2 * blockIdx.x] = open_id;
+    part.id[2 * blockIdx.x + 1] = open_parts;
+  }
+}
+
+template <int D, int NT>
+cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  TcArgs a;
+  a.q = static_cast<const bf16*>(p.q);
+  a.q_stride = p.q_stride;
+  a.table = p.table;
+  a.lengths = p.lengths;
+  a.o = static_cast<bf16*>(p.o);
+  a.lse = p.lse;
+  a.workspace = p.workspace;
+  a.B = p.B;
+  a.H = p.H;
+  a.G = p.H / p.pool.H;
+  a.Hkv = p.pool.H;
+  a.max_pages = p.max_pages;
+  a.page_size = p.pool.page_size;
+  a.n_pages = p.pool.n_pages;
+  a.hgroups = (a.G + C::kHeads - 1) / C::kHeads;
+  a.items = a.Hkv * a.hgroups;
+  a.heads = min(C::kHeads, a.G);
+  a.whole = paged_whole_items(p, 2);
+  a.box = 64;
+  while (a.page_size % a.box) a.box >>= 1;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.status = status;
+  CUtensorMap maps[2];
+  // a page's rows as 64-column halves: one box holds both
+  const uint64_t rows = (uint64_t)a.page_size, row = (uint64_t)D * 2;
+  const uint64_t dims[4] = {64, rows, D / 64, (uint64_t)a.n_pages * a.Hkv};
+  const uint64_t strides[3] = {row, 128, row * rows};
+  const uint32_t box[4] = {64, (uint32_t)a.box, D / 64, 1};
+  if (!make_tmap_bf16(&maps[0], p.pool.k, 4, dims, strides, box) ||
+      !make_tmap_bf16(&maps[1], p.pool.v, 4, dims, strides, box))
+    return cudaErrorInvalidValue;
+  const int ctas = min(sm_count(), kPagedMaxCtas);
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_tc_kernel<D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[0], maps[1], a);
+  if (e != cudaSuccess || a.whole) return e;
+  return launch_paged_join(NT_BF16, p, ctas, a.items, C::kHeads, s);
+}
+
+}  // namespace
+
+bool paged_attn_tc_supported(nt_dtype dt, const PagedAttnProblem& p) {
+  return dt == NT_BF16 && (p.d == 64 || p.d == 128) && p.pool.page_size % 8 == 0 && p.pool.n_pages > 0;
+}
+
+cudaError_t launch_paged_attn_tc(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
+  const int G = p.H / p.pool.H;
+  if (p.d == 64) return G <= 8 ? run<64, 1>(p, status, s) : run<64, 2>(p, status, s);
+  return G <= 8 ? run<128, 1>(p, status, s) : run<128, 2>(p, status, s);
+}
+
+}  // namespace nt

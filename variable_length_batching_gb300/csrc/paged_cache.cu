@@ -11,7 +11,7 @@ namespace nt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteTokens = 8;       // tokens a CTA of the write takes
+constexpr int kWriteTokens = 32;      // tokens a CTA of the write takes, at most
 
 struct WriteArgs {
   const uint8_t* src[2];              // k, v
@@ -19,49 +19,72 @@ struct WriteArgs {
   int64_t stride[2];                  // bytes between tokens
   int64_t T;
   int n_pages, page_size, H, row_bytes, B, max_pages;
+  int tokens;                         // tokens a CTA takes
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* table;
   unsigned int* status;
 };
 
+// Byte offset in the pool of token t's row of head 0, or -1 (flagged).
+__device__ __forceinline__ int64_t write_offset(const WriteArgs& a, int64_t t, int b) {
+  const int start = a.cu[b];
+  int64_t off = -1;
+  if (start >= 0 && start <= t && a.cu[b + 1] > t) {
+    const int64_t pos = t - start + (a.pos0 ? a.pos0[b] : 0);
+    if (pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
+      const int pg = (int)(pos / a.page_size);
+      const int id = a.table[(int64_t)b * a.max_pages + pg];
+      if (id >= 0 && id < a.n_pages)
+        off = ((int64_t)id * a.H * a.page_size + (pos - (int64_t)pg * a.page_size)) * a.row_bytes;
+    }
+  }
+  if (off < 0) flag_device(a.status, kDevCheck);
+  return off;
+}
+
+// A warp copies a token's keys, then its values: 16 bytes a lane, kUnroll
+// loads in flight.  The rows of a token are contiguous at the source; each
+// head's row goes to its own place in the page.
 __global__ void __launch_bounds__(kThreads) paged_write_kernel(const WriteArgs a) {
-  __shared__ int64_t dst[kWriteTokens];        // byte offset of the token's row of head 0, or -1
-  const int64_t t0 = (int64_t)blockIdx.x * kWriteTokens;
-  const int n = (int)min64(kWriteTokens, a.T - t0);
-  if (threadIdx.x < n) {
-    const int64_t t = t0 + threadIdx.x;
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+  constexpr int kUnroll = 4;
+  __shared__ int64_t dst[kWriteTokens];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int n = (int)min64(a.tokens, a.T - t0);
+  pdl_wait();
+  if (n <= kThreads / 32) {
+    if (warp < n) {
+      const int b = segment_of_warp(a.cu, a.B, t0 + warp);
+      if (lane == 0) dst[warp] = write_offset(a, t0 + warp, b);
     }
-    const int start = a.cu[lo];
-    int64_t off = -1;
-    if (start >= 0 && start <= t && a.cu[lo + 1] > t) {
-      const int64_t pos = t - start + (a.pos0 ? a.pos0[lo] : 0);
-      const int64_t pg = pos / a.page_size;
-      if (pos >= 0 && pg < a.max_pages) {
-        const int id = a.table[(int64_t)lo * a.max_pages + pg];
-        if (id >= 0 && id < a.n_pages)
-          off = ((int64_t)id * a.H * a.page_size + (pos - pg * a.page_size)) * a.row_bytes;
-      }
-    }
-    if (off < 0) flag_device(a.status, kDevCheck);
-    dst[threadIdx.x] = off;
+  } else {
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      dst[i] = write_offset(a, t0 + i, segment_of_thread(a.cu, a.B, t0 + i));
   }
   __syncthreads();
-  const int row_words = a.row_bytes / 16, side_words = a.H * row_words, tok_words = 2 * side_words;
+  const int row_words = a.row_bytes / 16, words = a.H * row_words;
   const int64_t head_bytes = (int64_t)a.page_size * a.row_bytes;
-  for (int e = threadIdx.x; e < n * tok_words; e += kThreads) {
-    const int tok = e / tok_words;
-    int w = e - tok * tok_words;
-    const int sd = w >= side_words;
-    w -= sd * side_words;
-    const int h = w / row_words, c = w - h * row_words;
-    if (dst[tok] < 0) continue;
-    const uint4 x = *reinterpret_cast<const uint4*>(a.src[sd] + (t0 + tok) * a.stride[sd] + (int64_t)w * 16);
-    *reinterpret_cast<uint4*>(a.pool[sd] + dst[tok] + h * head_bytes + c * 16) = x;
+  // units of kUnroll x 32 words of one side of one token, over the warps
+  const int per = (words + 32 * kUnroll - 1) / (32 * kUnroll), units = n * 2 * per;
+  for (int u = warp; u < units; u += kThreads / 32) {
+    const int tok = u / (2 * per), rest = u - tok * 2 * per;
+    const int sd = rest >= per, w0 = (rest - sd * per) * 32 * kUnroll + lane;
+    const int64_t off = dst[tok];
+    if (off < 0) continue;
+    const uint8_t* src = a.src[sd] + (t0 + tok) * a.stride[sd];
+    uint8_t* out = a.pool[sd] + off;
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (w0 + 32 * k < words) x[k] = *reinterpret_cast<const uint4*>(src + (int64_t)(w0 + 32 * k) * 16);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int w = w0 + 32 * k;
+      if (w >= words) continue;
+      const int h = w / row_words, c = w - h * row_words;
+      *reinterpret_cast<uint4*>(out + h * head_bytes + c * 16) = x[k];
+    }
   }
 }
 
@@ -128,8 +151,10 @@ cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stri
   a.pos0 = pos0;
   a.table = table;
   a.status = status;
-  paged_write_kernel<<<(unsigned)((T + kWriteTokens - 1) / kWriteTokens), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // one token per CTA until that fills the SMs four times
+  a.tokens = 1;
+  while (a.tokens < kWriteTokens && T >= (int64_t)sm_count() * 4 * a.tokens * 2) a.tokens <<= 1;
+  return launch_pdl(paged_write_kernel, dim3((unsigned)((T + a.tokens - 1) / a.tokens)), dim3(kThreads), 0, s, a);
 }
 
 cudaError_t launch_paged_copy(const PagedPool& p, const int32_t* src, const int32_t* dst, int64_t n, cudaStream_t s) {

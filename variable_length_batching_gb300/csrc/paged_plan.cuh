@@ -17,10 +17,13 @@
 
 namespace nt {
 
+// An item costs more than its tiles (query rows, merge, output): it counts as
+// `extra` tiles more, in front of its first.  A CTA whose share ends among
+// those takes nothing of the item.
 struct PagedPlanShared {
   int64_t warp_sum[32];
-  int64_t total, lo, hi;   // tiles of the call, this CTA's range
-  int64_t start;           // first tile of sequence b0
+  int64_t total, lo, hi;   // units of the call, this CTA's range
+  int64_t start;           // first unit of sequence b0
   int b0;
 };
 
@@ -34,17 +37,26 @@ __device__ __forceinline__ int paged_length(const int32_t* lengths, int b, int64
 }
 __device__ __forceinline__ int64_t paged_tiles(int len, int tile) { return (len + tile - 1) / tile; }
 
+// Units of a sequence's items.
+__device__ __forceinline__ int64_t paged_units(int len, int tile, int items, int extra) {
+  return len > 0 ? (paged_tiles(len, tile) + extra) * items : 0;
+}
+// CTAs that share the units, and the first unit of CTA c of them.
+__device__ __forceinline__ int64_t paged_ctas(int64_t total, int ctas) { return max64(1, min64(ctas, total)); }
+__device__ __forceinline__ int64_t paged_first(int64_t total, int64_t n, int64_t c) {
+  return total / n * c + total % n * c / n;
+}
+
 // Every thread of the CTA calls this (nthreads a multiple of 32, at most
 // 1024): each sums a strip of the sequences, the strips are scanned, and the
-// thread whose strip holds the CTA's first tile walks to its sequence.
-__device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, int items, int tile, int cta, int ctas,
-                                  PagedPlanShared* s, unsigned int* status, int nthreads) {
+// thread whose strip holds the CTA's first unit walks to its sequence.
+__device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, int items, int tile, int extra, int cta,
+                                  int ctas, PagedPlanShared* s, unsigned int* status, int nthreads) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = nthreads >> 5;
   const int strip = (B + nthreads - 1) / nthreads;
   const int b_lo = min(B, tid * strip), b_hi = min(B, b_lo + strip);
   int64_t sum = 0;
-  for (int b = b_lo; b < b_hi; ++b) sum += paged_tiles(paged_length(lengths, b, cap, status), tile);
-  sum *= items;
+  for (int b = b_lo; b < b_hi; ++b) sum += paged_units(paged_length(lengths, b, cap, status), tile, items, extra);
   int64_t inc = sum;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -58,16 +70,15 @@ __device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, in
     if (w < warp) before += s->warp_sum[w];
     total += s->warp_sum[w];
   }
-  // with fewer tiles than CTAs the last CTAs get none, so that no CTA without
+  // with fewer units than CTAs the last CTAs get none, so that no CTA without
   // work lies between two that share an item
-  const int64_t n = max64(1, min64(ctas, total)), c = min64(cta, n), c1 = min64(cta + 1, n);
-  const int64_t lo = total / n * c + total % n * c / n;
-  const int64_t hi = total / n * c1 + total % n * c1 / n;
+  const int64_t n = paged_ctas(total, ctas), c = min64(cta, n), c1 = min64(cta + 1, n);
+  const int64_t lo = paged_first(total, n, c), hi = paged_first(total, n, c1);
   int64_t at = before + inc - sum;
   if (lo >= at && lo < at + sum) {
     int b = b_lo;
     for (; b < b_hi; ++b) {
-      const int64_t w = paged_tiles(paged_length(lengths, b, cap, nullptr), tile) * items;
+      const int64_t w = paged_units(paged_length(lengths, b, cap, nullptr), tile, items, extra);
       if (lo < at + w) break;
       at += w;
     }
@@ -82,61 +93,91 @@ __device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, in
   __syncthreads();
 }
 
-// Walks a CTA's range segment by segment.
+// Walks a CTA's range segment by segment.  With `whole`, items are not split:
+// the CTA takes those that start in its range, to their end.
 struct PagedWalk {
-  int64_t left;           // tiles of the range not yet handed out
+  bool whole;
+  int64_t left;           // units of the range not yet handed out
   int b, item, len;
-  int64_t tiles, tile;    // tiles of sequence b; first tile of the next segment
-  // the current segment
+  int64_t units;          // of an item of sequence b
+  int64_t unit;           // of the item, where the next segment starts
+  // the current segment: tiles [t0, t1) of item seg_item of sequence seg_b
   int seg_b, seg_item, seg_len;
   int64_t t0, t1;
   bool begins, ends;
 
-  __device__ __forceinline__ void init(const PagedPlanShared* s, const int32_t* lengths, int64_t cap, int tile_keys) {
+  __device__ __forceinline__ void init(const PagedPlanShared* s, const int32_t* lengths, int64_t cap, int tile_keys,
+                                       int extra, bool whole_items) {
+    whole = whole_items;
     left = s->hi - s->lo;
     if (left <= 0) return;
     b = s->b0;
     len = paged_length(lengths, b, cap, nullptr);
-    tiles = paged_tiles(len, tile_keys);
+    units = paged_tiles(len, tile_keys) + extra;
     const int64_t off = s->lo - s->start;
-    item = (int)(off / tiles);
-    tile = off % tiles;
-  }
-  __device__ __forceinline__ bool next(const int32_t* lengths, int B, int64_t cap, int items, int tile_keys) {
-    if (left <= 0) return false;
-    if (item == items) {
-      item = 0;
-      do {                              // the range holds a further tile, so a longer sequence follows
-        if (++b >= B) return false;
-        len = paged_length(lengths, b, cap, nullptr);
-      } while (len == 0);
-      tiles = paged_tiles(len, tile_keys);
+    item = (int)(off / units);
+    unit = off - item * units;
+    if (whole && unit > 0) {
+      left -= units - unit;
+      unit = 0;
+      ++item;
     }
-    seg_b = b;
-    seg_item = item;
-    seg_len = len;
-    t0 = tile;
-    t1 = min64(tiles, tile + left);
-    begins = t0 == 0;
-    ends = t1 == tiles;
-    left -= t1 - t0;
-    tile = 0;
-    ++item;
+  }
+  __device__ __forceinline__ bool next(const int32_t* lengths, int B, int64_t cap, int items, int tile_keys,
+                                       int extra) {
+    do {
+      if (left <= 0) return false;
+      if (item == items) {
+        item = 0;
+        do {                              // the range holds a further unit, so a longer sequence follows
+          if (++b >= B) return false;
+          len = paged_length(lengths, b, cap, nullptr);
+        } while (len == 0);
+        units = paged_tiles(len, tile_keys) + extra;
+      }
+      const int64_t end = whole ? units : min64(units, unit + left);
+      seg_b = b;
+      seg_item = item;
+      seg_len = len;
+      t0 = max64(0, unit - extra);
+      t1 = end - extra;
+      begins = t0 == 0;
+      ends = end == units;
+      left -= end - unit;
+      unit = 0;
+      ++item;
+    } while (t1 <= t0);                   // nothing but the item's extra units
     return true;
+  }
+  // CTAs that take tiles of the current segment's item, for a segment that
+  // begins its item and does not end it (so the range ends inside it): the
+  // item ends at unit e of the call, and CTA c starts in front of e when
+  // floor(total c / n) < e.
+  __device__ __forceinline__ int parts(const PagedPlanShared* s, int extra, int cta, int ctas) const {
+    const int64_t n = paged_ctas(s->total, ctas), e = s->hi + units - (t1 + extra);
+    return (int)((e * n + s->total - 1) / s->total) - cta;
   }
 };
 
-// The partials in the workspace: per slot (two per CTA) the item it belongs
-// to (b * items + item, -1 none), then a (max, sum) pair per query head of an
-// item (the max in base-2 logarithms), then the heads' d unnormalised fp32
-// outputs.
+// Whether a call keeps its items whole: when the longest the tables allow is
+// so short that one CTA reads it in about the time the join's launch costs.
+constexpr int64_t kPagedWholeBytes = 256 * 1024;
+inline bool paged_whole_items(const PagedAttnProblem& p, int elem) {
+  return (int64_t)p.max_pages * p.pool.page_size * p.d * 2 * elem <= kPagedWholeBytes;
+}
+
+// The partials in the workspace: per CTA the item that it begins and leaves
+// unfinished (b * items + item, -1 none) and how many CTAs share that item;
+// then per slot a (max, sum) pair for each query head of an item, the max in
+// base-2 logarithms, and the heads' d unnormalised fp32 outputs.  Slot 2 c of
+// CTA c holds an item begun by an earlier CTA, slot 2 c + 1 one begun there.
 struct PagedPartials {
   int64_t* id;
   float* ml;
   float* o;
 };
 __host__ __device__ __forceinline__ PagedPartials paged_partials(void* ws, int ctas, int heads) {
-  PagedPartials p;
+  PagedPartials p;                    // each part a multiple of 16 bytes
   p.id = static_cast<int64_t*>(ws);
   p.ml = reinterpret_cast<float*>(p.id + 2 * (int64_t)ctas);
   p.o = p.ml + 2 * (int64_t)ctas * heads * 2;

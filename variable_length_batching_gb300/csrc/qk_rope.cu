@@ -13,11 +13,15 @@
 // and backward, with g the upstream gradient rotated back,
 //   dgamma = sum g x r,  h = g gamma,  dx = r (h - x r mean(h x r)).
 //
-// A CTA takes TB tokens: it forms their cosines and sines once in shared
-// memory for all heads of q and k, then groups of LP lanes (two 8-element
-// chunks each, so that a lane holds both halves of its pairs in either
-// layout) take one (token, head) row at a time.  Everything between the load
-// and the one rounding of the store is fp32.
+// Both directions are bound by HBM (about ten operations an element), so the
+// layout is about keeping loads in flight.  A CTA serves q or k, for tb
+// tokens.  Groups of LP lanes take one (token, head) row at a time, a lane
+// two 8-element chunks: both halves of its eight pairs in either layout.  A
+// group stays with one token and walks its heads, so the token's cosines and
+// sines (formed once per CTA in shared memory), multiplied by gamma in the
+// forward, stay in registers, and the rows of kBatch heads are requested
+// before the first is used, in the forward before the table is even formed.
+// Everything between the load and the one rounding of the store is fp32.
 #include "nt_common.cuh"
 
 namespace nt {
@@ -34,42 +38,36 @@ struct Side {
   int64_t xs, us, os;   // token strides in elements
   const float* gamma;   // [d] or NULL (no norm)
   int H;
+  int hg_log2;          // groups that share a token: 1 << hg_log2
+  int ctas;             // CTAs that serve the side (the first side's come first)
 };
 
 struct Args {
   Side side[2];
   int64_t T;
-  int d, rot, interleaved, B, tb;
-  float eps, scale;
+  int d, rot, B;
+  float inv_d, eps, scale;
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* positions;
   const uint64_t* turns;
-  float* partial;       // backward: [grid][2][d] sums for dgamma
+  float* partial;       // backward: [CTAs][d] sums for dgamma
   unsigned int* status;
 };
 
-// Position of token t; false (flagged) if the offsets do not place it.
-__device__ bool token_position(const Args& a, int64_t t, int64_t& pos) {
-  if (a.positions) {
-    pos = a.positions[t];
-    return true;
-  }
-  int lo = 0, hi = a.B - 1;          // last segment that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  const int start = a.cu[lo];
-  if (start > t || a.cu[lo + 1] <= t || start < 0) {
+// Position of a token of segment b; false (flagged) if the offsets do not
+// place the token there.
+__device__ __forceinline__ bool position_in(const Args& a, int64_t t, int b, int64_t& pos) {
+  const int start = a.cu[b];
+  if (start > t || a.cu[b + 1] <= t || start < 0) {
     flag_device(a.status, kDevCheck);
     return false;
   }
-  pos = t - start + (a.pos0 ? a.pos0[lo] : 0);
+  pos = t - start + (a.pos0 ? a.pos0[b] : 0);
   return true;
 }
 
-// Shared: ok[tb] (int), pos[tb] (int64), then the tile's table: pairs of
+// Shared: pos[tb] (int64), ok[tb] (int), then the tile's table: pairs of
 // (cos, sin) as float4 {c0, s0, c1, s1}, the four of a lane's eight pairs
 // rot/16 apart, so that the lanes of a group read consecutive words.
 struct Tile {
@@ -77,20 +75,40 @@ struct Tile {
   int* ok;
   float4* cs;
 };
-__device__ __forceinline__ Tile tile_of(unsigned char* smem, const Args& a) {
+__host__ __device__ __forceinline__ int table_offset(int tb) { return (tb * 12 + 15) & ~15; }
+__device__ __forceinline__ Tile tile_of(unsigned char* smem, int tb) {
   Tile s;
   s.pos = reinterpret_cast<int64_t*>(smem);
-  s.ok = reinterpret_cast<int*>(smem + a.tb * 8);
-  s.cs = reinterpret_cast<float4*>(smem + ((a.tb * 12 + 15) & ~15));
+  s.ok = reinterpret_cast<int*>(smem + tb * 8);
+  s.cs = reinterpret_cast<float4*>(smem + table_offset(tb));
   return s;
 }
 
 // With nothing to rotate the positions are not read (and may be NULL).
 __device__ void fill_tile(const Args& a, const Tile& s, int64_t t0, int n) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    int64_t p = 0;
-    s.ok[i] = a.rot == 0 || token_position(a, t0 + i, p);
-    s.pos[i] = p;
+  if (a.rot == 0 || a.positions) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      s.ok[i] = 1;
+      s.pos[i] = a.rot == 0 ? 0 : a.positions[t0 + i];
+    }
+  } else if (n <= kWarps) {
+    // few tokens: one per warp, 32 probes a step (the latency of a search is
+    // what a decoding step waits for: 2 steps instead of 8 for 256 segments)
+    const int i = threadIdx.x >> 5;
+    if (i < n) {
+      const int b = segment_of_warp(a.cu, a.B, t0 + i);
+      if ((threadIdx.x & 31) == 0) {
+        int64_t p = 0;
+        s.ok[i] = position_in(a, t0 + i, b, p);
+        s.pos[i] = p;
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      int64_t p = 0;
+      s.ok[i] = position_in(a, t0 + i, segment_of_thread(a.cu, a.B, t0 + i), p);
+      s.pos[i] = p;
+    }
   }
   __syncthreads();
   const int quarter = a.rot >> 2;               // float4 words of one token
@@ -113,29 +131,43 @@ __device__ void fill_tile(const Args& a, const Tile& s, int64_t t0, int n) {
   __syncthreads();
 }
 
-// Rotate a lane's two chunks (dir = 1 forward, -1 transposed).
-__device__ __forceinline__ void rotate(float* xa, float* xb, const float4* cs, int lanes, int i, bool interleaved,
-                                       float dir) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float4 w = cs[q * lanes + i];
-    const float c0 = w.x, s0 = w.y * dir, c1 = w.z, s1 = w.w * dir;
-    if (interleaved) {     // pairs 2q and 2q + 1 of the lane: chunk a holds the first four, chunk b the rest
-      float* x = (q < 2 ? xa : xb) + (q & 1) * 4;
-      const float a0 = x[0], b0 = x[1], a1 = x[2], b1 = x[3];
-      x[0] = a0 * c0 - b0 * s0;
-      x[1] = a0 * s0 + b0 * c0;
-      x[2] = a1 * c1 - b1 * s1;
-      x[3] = a1 * s1 + b1 * c1;
+// A lane's place: its group's token within the tile and first head, and the
+// columns of its two chunks.
+template <int LP, bool kInter>
+struct Lane {
+  int i, tok, h0, hg, ca, cb;
+  bool on, rotated;
+  __device__ __forceinline__ Lane(const Args& a, const Side& p) {
+    i = threadIdx.x % LP;
+    const int g = threadIdx.x / LP;
+    hg = 1 << p.hg_log2;
+    tok = g >> p.hg_log2;
+    h0 = g & (hg - 1);
+    on = 16 * i < a.d;
+    rotated = 16 * i < a.rot;
+    if (!kInter && rotated) {
+      ca = 8 * i;
+      cb = (a.rot >> 1) + 8 * i;
     } else {
-      const float a0 = xa[2 * q], b0 = xb[2 * q], a1 = xa[2 * q + 1], b1 = xb[2 * q + 1];
-      xa[2 * q] = a0 * c0 - b0 * s0;
-      xb[2 * q] = a0 * s0 + b0 * c0;
-      xa[2 * q + 1] = a1 * c1 - b1 * s1;
-      xb[2 * q + 1] = a1 * s1 + b1 * c1;
+      ca = 16 * i;
+      cb = 16 * i + 8;
     }
   }
-}
+  // cosines and sines of the lane's eight pairs (1 and 0 where nothing turns)
+  __device__ __forceinline__ void angles(const Args& a, const Tile& s, float (&c)[8], float (&sn)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 w = rotated ? s.cs[tok * (a.rot >> 2) + q * (a.rot >> 4) + i] : make_float4(1.f, 0.f, 1.f, 0.f);
+      c[2 * q] = w.x;
+      sn[2 * q] = w.y;
+      c[2 * q + 1] = w.z;
+      sn[2 * q + 1] = w.w;
+    }
+  }
+};
+// Element indices (0..15: chunk a, then chunk b) of pair e's two parts.
+template <bool kInter> __device__ constexpr int part_a(int e) { return kInter ? 2 * e : e; }
+template <bool kInter> __device__ constexpr int part_b(int e) { return kInter ? 2 * e + 1 : e + 8; }
 
 template <int LP>
 __device__ __forceinline__ float group_sum(float v) {
@@ -144,138 +176,220 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Columns of lane i's two chunks.
-__device__ __forceinline__ void lane_columns(const Args& a, int i, int& ca, int& cb) {
-  if (!a.interleaved && 16 * i < a.rot) {
-    ca = 8 * i;
-    cb = (a.rot >> 1) + 8 * i;
-  } else {
-    ca = 16 * i;
-    cb = 16 * i + 8;
+// One row's two chunks as loaded, and as fp32.
+template <typename T> struct Raw;
+template <> struct Raw<bf16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const bf16* x, int ca, int cb) {
+    a = *reinterpret_cast<const uint4*>(x + ca);
+    b = *reinterpret_cast<const uint4*>(x + cb);
   }
-}
-
-template <typename T, int LP>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const Args a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const Tile s = tile_of(smem, a);
-  const int64_t t0 = (int64_t)blockIdx.x * a.tb;
-  const int n = (int)min64(a.tb, a.T - t0);
-  fill_tile(a, s, t0, n);
-  const int i = threadIdx.x % LP, g = threadIdx.x / LP;
-  const bool lane_on = 16 * i < a.d, rotated = 16 * i < a.rot;
-  const int lanes = a.rot >> 4;
-  int ca, cb;
-  lane_columns(a, i, ca, cb);
-#pragma unroll 1
-  for (int sd = 0; sd < 2; ++sd) {
-    const Side& p = a.side[sd];
-    if (p.H == 0) continue;
-    float ga[8], gb[8];
-    const bool norm = p.gamma != nullptr;
-    if (norm && lane_on) {
-      load8(p.gamma + ca, ga);
-      load8(p.gamma + cb, gb);
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
-    const int items = n * p.H;
-    // whole warps stay in the loop together (the group sums are shuffles)
-    for (int it0 = 0; it0 < items; it0 += kThreads / LP) {
-      const int it = it0 + g;
-      const int tok = it / p.H, h = it - tok * p.H;
-      const bool on = it < items && lane_on && s.ok[tok];
-      float xa[8] = {}, xb[8] = {};
-      const T* x = static_cast<const T*>(p.x) + (t0 + tok) * p.xs + (int64_t)h * a.d;
-      if (on) {
-        load8(x + ca, xa);
-        load8(x + cb, xb);
-      }
+  }
+};
+template <> struct Raw<float> {
+  float4 a[4];
+  __device__ __forceinline__ void load(const float* x, int ca, int cb) {
+    a[0] = *reinterpret_cast<const float4*>(x + ca);
+    a[1] = *reinterpret_cast<const float4*>(x + ca + 4);
+    a[2] = *reinterpret_cast<const float4*>(x + cb);
+    a[3] = *reinterpret_cast<const float4*>(x + cb + 4);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[4 * e] = a[e].x;
+      v[4 * e + 1] = a[e].y;
+      v[4 * e + 2] = a[e].z;
+      v[4 * e + 3] = a[e].w;
+    }
+  }
+};
+
+template <typename T, int LP, bool kInter>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const Args a) {
+  constexpr int kBatch = sizeof(T) == 2 ? 3 : 2;        // rows in flight per group
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int sd = blockIdx.x >= a.side[0].ctas;
+  const Side& p = a.side[sd];
+  const Lane<LP, kInter> me(a, p);
+  const int tb = kThreads / LP >> p.hg_log2;
+  const int64_t t0 = (int64_t)(blockIdx.x - (sd ? a.side[0].ctas : 0)) * tb;
+  const int n = (int)min64(tb, a.T - t0);
+  const Tile s = tile_of(smem, tb);
+  const bool here = me.on && me.tok < n;
+  const T* x = static_cast<const T*>(p.x) + (t0 + me.tok) * p.xs;
+  Raw<T> raw[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      raw[k].zero();
+      if (here && h + k * me.hg < p.H) raw[k].load(x + (int64_t)(h + k * me.hg) * a.d, me.ca, me.cb);
+    }
+  };
+  pdl_wait();
+  load(me.h0);
+  fill_tile(a, s, t0, n);
+  // pair e: out_a = r (x_a m[0] - x_b m[1]), out_b = r (x_a m[2] + x_b m[3])
+  float m[8][4];
+  const bool norm = p.gamma != nullptr;
+  {
+    float c[8], sn[8], gm[16];
+    if (here) {
+      me.angles(a, s, c, sn);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = sn[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) gm[e] = 1.f;
+    if (norm && me.on) {
+      Raw<float> g;
+      g.load(p.gamma, me.ca, me.cb);
+      g.get(gm);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float ga = gm[part_a<kInter>(e)], gb = gm[part_b<kInter>(e)];
+      m[e][0] = ga * c[e];
+      m[e][1] = gb * sn[e];
+      m[e][2] = ga * sn[e];
+      m[e][3] = gb * c[e];
+    }
+  }
+  const bool write = here && s.ok[me.tok];
+  T* o = static_cast<T*>(p.out) + (t0 + me.tok) * p.os;
+  // the loop's bounds are the warp's: its groups may hold different first heads
+  for (int hb = 0; hb < p.H; hb += kBatch * me.hg) {
+    const int h = hb + me.h0;
+    if (hb) load(h);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      float v[16];
+      raw[k].get(v);
+      float r = 1.f;
       if (norm) {
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += xa[e] * xa[e] + xb[e] * xb[e];
-        const float r = rsqrtf(group_sum<LP>(ss) / (float)a.d + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xa[e] *= r * ga[e];
-          xb[e] *= r * gb[e];
-        }
+        for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
+        r = rsqrtf(group_sum<LP>(ss) * a.inv_d + a.eps);
       }
-      if (on) {
-        if (rotated) rotate(xa, xb, s.cs + tok * (a.rot >> 2), lanes, i, a.interleaved, 1.f);
-        T* o = static_cast<T*>(p.out) + (t0 + tok) * p.os + (int64_t)h * a.d;
-        store8(o + ca, xa);
-        store8(o + cb, xb);
+      float w[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int ia = part_a<kInter>(e), ib = part_b<kInter>(e);
+        w[ia] = r * (v[ia] * m[e][0] - v[ib] * m[e][1]);
+        w[ib] = r * (v[ia] * m[e][2] + v[ib] * m[e][3]);
+      }
+      if (write && h + k * me.hg < p.H) {
+        T* y = o + (int64_t)(h + k * me.hg) * a.d;
+        store8(y + me.ca, w);
+        store8(y + me.cb, w + 8);
       }
     }
   }
 }
 
-template <typename T, int LP>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const Args a) {
+template <typename T, int LP, bool kInter>
+__global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
+  constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
   extern __shared__ __align__(16) unsigned char smem[];
-  const Tile s = tile_of(smem, a);
-  const int i = threadIdx.x % LP, g = threadIdx.x / LP;
-  const bool lane_on = 16 * i < a.d, rotated = 16 * i < a.rot;
-  const int lanes = a.rot >> 4;
-  int ca, cb;
-  lane_columns(a, i, ca, cb);
-  float acc[2][16] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.T; t0 += (int64_t)gridDim.x * a.tb) {
-    const int n = (int)min64(a.tb, a.T - t0);
+  const int sd = blockIdx.x >= a.side[0].ctas;
+  const Side& p = a.side[sd];
+  const Lane<LP, kInter> me(a, p);
+  const int tb = kThreads / LP >> p.hg_log2;
+  const Tile s = tile_of(smem, tb);
+  const bool norm = p.gamma != nullptr;
+  float gm[16], acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    gm[e] = 1.f;
+    acc[e] = 0.f;
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (norm && me.on) {
+    Raw<float> g;
+    g.load(p.gamma, me.ca, me.cb);
+    g.get(gm);
+  }
+  for (int64_t t0 = (int64_t)(blockIdx.x - (sd ? a.side[0].ctas : 0)) * tb; t0 < a.T; t0 += (int64_t)p.ctas * tb) {
+    const int n = (int)min64(tb, a.T - t0);
+    const bool here = me.on && me.tok < n;
+    const T* u = static_cast<const T*>(p.up) + (t0 + me.tok) * p.us;
+    const T* x = static_cast<const T*>(p.x) + (t0 + me.tok) * p.xs;
+    Raw<T> ru[kBatch], rx[kBatch];
+    auto load = [&](int h) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        ru[k].zero();
+        rx[k].zero();
+        if (here && h + k * me.hg < p.H) {
+          const int64_t at = (int64_t)(h + k * me.hg) * a.d;
+          ru[k].load(u + at, me.ca, me.cb);
+          if (norm) rx[k].load(x + at, me.ca, me.cb);
+        }
+      }
+    };
+    load(me.h0);
     __syncthreads();                         // the tile of the step before is read out
     fill_tile(a, s, t0, n);
+    float c[8], sn[8];
+    if (here) {
+      me.angles(a, s, c, sn);
+    } else {
 #pragma unroll
-    for (int sd = 0; sd < 2; ++sd) {
-      const Side& p = a.side[sd];
-      if (p.H == 0) continue;
-      const bool norm = p.gamma != nullptr;
-      const int items = n * p.H;
-      for (int it0 = 0; it0 < items; it0 += kThreads / LP) {
-        const int it = it0 + g;
-        const int tok = it / p.H, h = it - tok * p.H;
-        const bool on = it < items && lane_on && s.ok[tok];
-        float ga[8] = {}, gb[8] = {};        // upstream, then rotated back
-        if (on) {
-          const T* u = static_cast<const T*>(p.up) + (t0 + tok) * p.us + (int64_t)h * a.d;
-          load8(u + ca, ga);
-          load8(u + cb, gb);
-          if (rotated) rotate(ga, gb, s.cs + tok * (a.rot >> 2), lanes, i, a.interleaved, -1.f);
+      for (int e = 0; e < 8; ++e) c[e] = sn[e] = 0.f;
+    }
+    const bool write = here && s.ok[me.tok];
+    T* o = static_cast<T*>(p.out) + (t0 + me.tok) * p.os;
+    for (int hb = 0; hb < p.H; hb += kBatch * me.hg) {
+      const int h = hb + me.h0;
+      if (hb) load(h);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        float v[16], g[16];
+        ru[k].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int ia = part_a<kInter>(e), ib = part_b<kInter>(e);
+          g[ia] = v[ia] * c[e] + v[ib] * sn[e];
+          g[ib] = v[ib] * c[e] - v[ia] * sn[e];
         }
         if (norm) {
-          float xa[8] = {}, xb[8] = {};
-          if (on) {
-            const T* x = static_cast<const T*>(p.x) + (t0 + tok) * p.xs + (int64_t)h * a.d;
-            load8(x + ca, xa);
-            load8(x + cb, xb);
-          }
+          rx[k].get(v);
           float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss += xa[e] * xa[e] + xb[e] * xb[e];
-          const float r = rsqrtf(group_sum<LP>(ss) / (float)a.d + a.eps);
+          for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
+          const float r = rsqrtf(group_sum<LP>(ss) * a.inv_d + a.eps);
           float hx = 0.f;
-          if (on) {
+          const float keep = write ? r : 0.f;        // a token in no segment adds nothing
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              xa[e] *= r;
-              xb[e] *= r;
-              acc[sd][e] += ga[e] * xa[e];
-              acc[sd][8 + e] += gb[e] * xb[e];
-              ga[e] *= p.gamma[ca + e];
-              gb[e] *= p.gamma[cb + e];
-              hx += ga[e] * xa[e] + gb[e] * xb[e];
-            }
+          for (int e = 0; e < 16; ++e) {
+            v[e] *= keep;
+            acc[e] = fmaf(g[e], v[e], acc[e]);
+            g[e] *= gm[e];
+            hx = fmaf(g[e], v[e], hx);
           }
-          const float m = group_sum<LP>(hx) / (float)a.d;
+          const float mean = group_sum<LP>(hx) * a.inv_d;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ga[e] = r * (ga[e] - xa[e] * m);
-            gb[e] = r * (gb[e] - xb[e] * m);
-          }
+          for (int e = 0; e < 16; ++e) g[e] = r * (g[e] - v[e] * mean);
         }
-        if (on) {
-          T* o = static_cast<T*>(p.out) + (t0 + tok) * p.os + (int64_t)h * a.d;
-          store8(o + ca, ga);
-          store8(o + cb, gb);
+        if (write && h + k * me.hg < p.H) {
+          T* y = o + (int64_t)(h + k * me.hg) * a.d;
+          store8(y + me.ca, g);
+          store8(y + me.cb, g + 8);
         }
       }
     }
@@ -283,45 +397,46 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const Args a) {
   if (!a.partial) return;
   // dgamma: the groups of a warp by shuffle, the warps through shared memory
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);          // [kWarps][d], one side at a time
+  float* red = reinterpret_cast<float*>(smem);          // [kWarps][d]
   const int warp = threadIdx.x / 32;
 #pragma unroll
-  for (int sd = 0; sd < 2; ++sd) {
+  for (int e = 0; e < 16; ++e) {
+    float v = acc[e];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float v = acc[sd][e];
+    for (int m = 16; m >= LP; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if ((threadIdx.x & 31) < LP && me.on) red[warp * a.d + (e < 8 ? me.ca + e : me.cb + e - 8)] = v;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    float v = 0.f;
 #pragma unroll
-      for (int m = 16; m >= LP; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-      if ((threadIdx.x & 31) < LP && lane_on) red[warp * a.d + (e < 8 ? ca + e : cb + e - 8)] = v;
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w * a.d + c];
-      a.partial[((int64_t)blockIdx.x * 2 + sd) * a.d + c] = v;
-    }
-    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) v += red[w * a.d + c];
+    a.partial[(int64_t)blockIdx.x * a.d + c] = v;
   }
 }
 
-// dgamma[side][c] = the sum of the CTAs' partials, in CTA order within each
-// of eight strides, then across the strides.
-__global__ void __launch_bounds__(256) rope_dgamma_kernel(const float* partial, int parts, int d, float* dq_gamma,
-                                                          float* dk_gamma) {
-  __shared__ float red[8][32];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32, sd = blockIdx.y;
+// dgamma of side blockIdx.y: the sum of its CTAs' partials, in CTA order
+// within each of 32 strides, then across the strides.
+__global__ void __launch_bounds__(1024) rope_dgamma_kernel(const float* partial, int parts_q, int parts_k, int d,
+                                                           float* dq_gamma, float* dk_gamma) {
+  __shared__ float red[32][33];
+  const int col = threadIdx.x % 32, c = blockIdx.x * 32 + col, w = threadIdx.x / 32, sd = blockIdx.y;
   float* out = sd ? dk_gamma : dq_gamma;
+  pdl_wait();
   if (!out) return;
+  const int first = sd ? parts_q : 0, end = first + (sd ? parts_k : parts_q);
   float v = 0.f;
-  if (c < d)
-    for (int p = w; p < parts; p += 8) v += partial[((int64_t)p * 2 + sd) * d + c];
-  red[w][threadIdx.x % 32] = v;
-  __syncthreads();
-  if (w == 0 && c < d) {
-    for (int k = 1; k < 8; ++k) v += red[k][threadIdx.x];
-    out[c] = v;
+  if (c < d) {
+#pragma unroll 4
+    for (int p = first + w; p < end; p += 32) v += partial[(int64_t)p * d + c];
   }
+  red[w][col] = v;
+  __syncthreads();
+  // warp w sums column w of the strides
+  v = red[col][w];
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  if (col == 0 && blockIdx.x * 32 + w < d) out[blockIdx.x * 32 + w] = v;
 }
 
 int group_lanes(int d) {
@@ -330,38 +445,36 @@ int group_lanes(int d) {
   return lp;
 }
 
-template <typename T, int LP>
+template <typename T, int LP, bool kInter>
 cudaError_t run(const Args& a, bool bwd, int grid, size_t smem, cudaStream_t s) {
-  if (bwd) rope_bwd_kernel<T, LP><<<grid, kThreads, smem, s>>>(a);
-  else rope_fwd_kernel<T, LP><<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(bwd ? rope_bwd_kernel<T, LP, kInter> : rope_fwd_kernel<T, LP, kInter>, dim3(grid), dim3(kThreads),
+                    smem, s, a);
 }
 
-template <typename T>
+template <typename T, bool kInter>
 cudaError_t run_lp(const Args& a, bool bwd, int grid, size_t smem, cudaStream_t s) {
   switch (group_lanes(a.d)) {
-    case 1: return run<T, 1>(a, bwd, grid, smem, s);
-    case 2: return run<T, 2>(a, bwd, grid, smem, s);
-    case 4: return run<T, 4>(a, bwd, grid, smem, s);
-    case 8: return run<T, 8>(a, bwd, grid, smem, s);
-    default: return run<T, 16>(a, bwd, grid, smem, s);
+    case 1: return run<T, 1, kInter>(a, bwd, grid, smem, s);
+    case 2: return run<T, 2, kInter>(a, bwd, grid, smem, s);
+    case 4: return run<T, 4, kInter>(a, bwd, grid, smem, s);
+    case 8: return run<T, 8, kInter>(a, bwd, grid, smem, s);
+    default: return run<T, 16, kInter>(a, bwd, grid, smem, s);
   }
 }
 
 }  // namespace
 
-size_t qk_rope_bwd_workspace_bytes(int d) { return (size_t)kRopeMaxParts * 2 * (size_t)d * sizeof(float); }
+size_t qk_rope_bwd_workspace_bytes(int d) { return (size_t)kRopeMaxParts * (size_t)d * sizeof(float); }
 
 cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* workspace, unsigned int* status,
                            cudaStream_t s) {
-  const int LP = group_lanes(p.d);
   Args a = {};
-  a.side[0] = {p.q, p.dq_out, p.q_out, p.q_stride, p.dq_out_stride, p.q_out_stride, p.q_gamma, p.H_q};
-  a.side[1] = {p.k, p.dk_out, p.k_out, p.k_stride, p.dk_out_stride, p.k_out_stride, p.k_gamma, p.H_k};
+  a.side[0] = {p.q, p.dq_out, p.q_out, p.q_stride, p.dq_out_stride, p.q_out_stride, p.q_gamma, p.H_q, 0, 0};
+  a.side[1] = {p.k, p.dk_out, p.k_out, p.k_stride, p.dk_out_stride, p.k_out_stride, p.k_gamma, p.H_k, 0, 0};
   a.T = p.T;
   a.d = p.d;
   a.rot = p.rot_dim;
-  a.interleaved = p.interleaved;
+  a.inv_d = 1.f / p.d;
   a.B = p.B;
   a.eps = p.eps;
   a.scale = p.rot_scale;
@@ -372,27 +485,35 @@ cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* w
   a.status = status;
   const bool norm = p.q_gamma || p.k_gamma;
   a.partial = bwd && norm ? workspace : nullptr;
-  // tokens per CTA: one while the tokens do not fill the SMs, at most 16
-  const int sms = sm_count();
-  int tb = 1;
-  while (tb < 16 && p.T >= (int64_t)sms * 8 * tb * 2) tb <<= 1;
-  a.tb = tb;
-  const int64_t tiles = (p.T + tb - 1) / tb;
-  size_t smem = (size_t)((tb * 12 + 15) & ~15) + (size_t)tb * (p.rot_dim / 4) * 16;
-  int64_t grid = tiles;
-  if (bwd) {
-    grid = min64(tiles, min64(kRopeMaxParts, (int64_t)sms * 4));
-    const size_t red = (size_t)kWarps * p.d * sizeof(float);
-    if (smem < red) smem = red;
+  const int groups = kThreads / group_lanes(p.d), sms = sm_count();
+  size_t smem = bwd ? (size_t)kWarps * p.d * sizeof(float) : 0;
+  for (Side& sd : a.side) {
+    if (sd.H == 0 || p.T == 0) continue;
+    // Groups per token: few, so that a group walks three heads or more with
+    // one token's angles, unless the CTAs would then not fill the SMs twice.
+    int lg = 0;
+    while ((2 << lg) <= groups && (2 << lg) * 3 <= sd.H) ++lg;
+    while ((2 << lg) <= groups && (1 << lg) < sd.H && p.T < (int64_t)2 * sms * (groups >> lg)) ++lg;
+    const int tb = groups >> lg;
+    const int64_t tiles = (p.T + tb - 1) / tb;
+    sd.hg_log2 = lg;
+    // The backward's CTAs stay (their sums of dgamma are what is added up at
+    // the end): four per SM between the sides, by their heads.
+    sd.ctas = (int)(bwd ? max64(1, min64(tiles, (int64_t)sms * 4 * sd.H / (p.H_q + p.H_k))) : tiles);
+    const size_t need = (size_t)table_offset(tb) + (size_t)tb * (p.rot_dim / 4) * 16;
+    if (smem < need) smem = need;
   }
-  (void)LP;
+  const int grid = a.side[0].ctas + a.side[1].ctas;
   cudaError_t e = cudaSuccess;
-  if (p.T > 0)
-    e = dt == NT_BF16 ? run_lp<bf16>(a, bwd, (int)grid, smem, s) : run_lp<float>(a, bwd, (int)grid, smem, s);
+  if (grid > 0) {
+    if (dt == NT_BF16)
+      e = p.interleaved ? run_lp<bf16, true>(a, bwd, grid, smem, s) : run_lp<bf16, false>(a, bwd, grid, smem, s);
+    else
+      e = p.interleaved ? run_lp<float, true>(a, bwd, grid, smem, s) : run_lp<float, false>(a, bwd, grid, smem, s);
+  }
   if (e != cudaSuccess || !bwd || !norm) return e;
-  rope_dgamma_kernel<<<dim3((p.d + 31) / 32, 2), 256, 0, s>>>(workspace, p.T > 0 ? (int)grid : 0, p.d, p.dq_gamma,
-                                                            p.dk_gamma);
-  return cudaGetLastError();
+  return launch_pdl(rope_dgamma_kernel, dim3((p.d + 31) / 32, 2), dim3(1024), 0, s, (const float*)workspace,
+                    a.side[0].ctas, a.side[1].ctas, p.d, p.dq_gamma, p.dk_gamma);
 }
 
 }  // namespace nt

@@ -620,58 +620,58 @@ def nt_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", fa
     return t if device is None else t.to(device)
 
 
-def _on(t: Optional[torch.Tensor], dev, dtype=None, name: str = "tensor"):
-    """Address of a contiguous tensor that must live on ``dev`` (None -> NULL)."""
-    if t is None:
-        return None
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _refuse(t, index: int, dtype, name: str):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _on(t: Optional[torch.Tensor], index: int, dtype, name: str):
+    """Address of a contiguous tensor that must live on CUDA device ``index``
+    (None -> NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
+        _refuse(t, index, dtype, name)
     return t.data_ptr()
 
 
-def _tokens(t: Optional[torch.Tensor], dev, dtype, name: str):
+def _tokens(t: Optional[torch.Tensor], index: int, dtype, name: str):
     """(address, token stride) of packed tokens (T, H, d) whose heads are
     contiguous within a token; tokens may be any stride apart."""
     if t is None:
         return None, 0
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be (tokens, heads, d)")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    if t.get_device() != index or t.dtype is not dtype:
+        _refuse(t, index, dtype, name)
     T, H, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
+    stride, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if T > 1 else H * d
+    return t.data_ptr(), stride if T > 1 else H * d
 
 
-class _launch:
-    """The device and stream of one call: makes ``dev`` current while the
-    call runs if it is not, and gives the stream's handle."""
+def _cuda_index(t: torch.Tensor) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("expected CUDA tensors")
+    return i
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        self.prev = None
-        self.dev = dev
-        self.stream = stream
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.dev.index != cur:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-        s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _run(name: str, index: int, stream, *args):
+    """One call of the library on CUDA device ``index``, which is made current
+    while it runs, on its current stream (or ``stream``)."""
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        st = getattr(_lib or lib(), name)(*args, s)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(_lib or lib(), name)(*args, s)
+    if st != 0:
+        _check(st, name)
 
 
 def _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma):
@@ -681,26 +681,33 @@ def _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma):
         raise ValueError("q or k is needed")
     if t.dim() != 3:
         raise ValueError("q and k must be (tokens, heads, d)")
-    T, d, dev = t.shape[0], t.shape[2], t.device
-    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != d):
-        raise ValueError("q and k must share their tokens and head width")
-    if positions is not None and (cu_seqlens is not None or pos0 is not None):
-        raise ValueError("give positions or cu_seqlens (with pos0), not both")
-    if positions is not None and positions.numel() != T:
-        raise ValueError("one position per token")
-    if pos0 is not None and (cu_seqlens is None or pos0.numel() != cu_seqlens.numel() - 1):
+    T, _, d = t.shape
+    H_q = 0 if q is None else q.shape[1]
+    H_k = 0
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("q and k must share their tokens and head width")
+        H_k = k.shape[1]
+    B = 0
+    if positions is not None:
+        if cu_seqlens is not None or pos0 is not None:
+            raise ValueError("give positions or cu_seqlens (with pos0), not both")
+        if positions.numel() != T:
+            raise ValueError("one position per token")
+    elif cu_seqlens is not None:
+        B = cu_seqlens.numel() - 1
+        if B < 0:
+            raise ValueError("cu_seqlens has B + 1 entries")
+    if pos0 is not None and (cu_seqlens is None or pos0.numel() != B):
         raise ValueError("pos0 is one start per cu_seqlens segment")
-    for g in (q_gamma, k_gamma):
-        if g is not None and g.numel() != d:
-            raise ValueError("gammas must have d entries")
+    if (q_gamma is not None and q_gamma.numel() != d) or (k_gamma is not None and k_gamma.numel() != d):
+        raise ValueError("gammas must have d entries")
+    index = _cuda_index(t)
     i32 = torch.int32
-    B = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    if B < 0:
-        raise ValueError("cu_seqlens has B + 1 entries")
-    tail = (_on(cu_seqlens, dev, i32, "cu_seqlens"), B, _on(pos0, dev, i32, "pos0"),
-            _on(positions, dev, i32, "positions"), _on(turns, dev, torch.int64, "turns"),
+    tail = (_on(cu_seqlens, index, i32, "cu_seqlens"), B, _on(pos0, index, i32, "pos0"),
+            _on(positions, index, i32, "positions"), _on(turns, index, torch.int64, "turns"),
             0 if turns is None else 2 * turns.numel())
-    return T, d, dev, t.dtype, tail
+    return T, H_q, H_k, d, index, t.dtype, tail
 
 
 def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns: Optional[torch.Tensor],
@@ -715,25 +722,27 @@ def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns:
     segment, or are given as ``positions``.  ``turns`` from nt_rope_turns
     sets the rotated columns (None: norm only).  q and k may be slices of a
     fused projection; ``q_out=q, k_out=k`` works in place."""
-    T, d, dev, dt, tail = _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    for x, y in ((q, q_out), (k, k_out)):
-        if (x is None) != (y is None) or (x is not None and x.shape != y.shape):
-            raise ValueError("outputs must have their inputs' shapes")
-    qp, qs = _tokens(q, dev, dt, "q")
-    kp, ks = _tokens(k, dev, dt, "k")
-    qo, qos = _tokens(q_out, dev, dt, "q_out")
-    ko, kos = _tokens(k_out, dev, dt, "k_out")
+    T, H_q, H_k, d, index, dt, tail = _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
+    qp, qs = _tokens(q, index, dt, "q")
+    kp, ks = _tokens(k, index, dt, "k")
+    if q_out is None and q is not None:
+        q_out = torch.empty((T, H_q, d), dtype=dt, device=q.device)
+        qo, qos = q_out.data_ptr(), H_q * d
+    else:
+        if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
+            raise ValueError("q_out must have q's shape")
+        qo, qos = _tokens(q_out, index, dt, "q_out")
+    if k_out is None and k is not None:
+        k_out = torch.empty((T, H_k, d), dtype=dt, device=k.device)
+        ko, kos = k_out.data_ptr(), H_k * d
+    else:
+        if (k is None) != (k_out is None) or (k is not None and k.shape != k_out.shape):
+            raise ValueError("k_out must have k's shape")
+        ko, kos = _tokens(k_out, index, dt, "k_out")
     f32 = torch.float32
-    with _launch(dev, stream) as s:
-        st = lib().nt_qk_norm_rope(_dtype(q if q is not None else k), qp, qs, kp, ks, T,
-                                   0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d,
-                                   _on(q_gamma, dev, f32, "q_gamma"), _on(k_gamma, dev, f32, "k_gamma"), float(eps),
-                                   *tail, int(bool(interleaved)), float(rot_scale), qo, qos, ko, kos, s)
-        _check(st, "nt_qk_norm_rope")
+    _run("nt_qk_norm_rope", index, stream, _dtype(q if q is not None else k), qp, qs, kp, ks, T, H_q, H_k, d,
+         _on(q_gamma, index, f32, "q_gamma"), _on(k_gamma, index, f32, "k_gamma"), eps, *tail,
+         1 if interleaved else 0, rot_scale, qo, qos, ko, kos)
     return q_out, k_out
 
 
@@ -752,31 +761,40 @@ def nt_qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.T
     (dq, dk, dq_gamma, dk_gamma), the gammas' in fp32, None where there is no
     input.  ``q`` and ``k`` are the forward's inputs, needed for the sides
     that have a gamma."""
-    T, d, dev, dt, tail = _rope_args(dq_out, dk_out, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
+    T, H_q, H_k, d, index, dt, tail = _rope_args(dq_out, dk_out, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
     f32 = torch.float32
-    for x, u, g, name in ((q, dq_out, q_gamma, "q"), (k, dk_out, k_gamma, "k")):
-        if g is not None and (x is None or u is None or x.shape != u.shape):
-            raise ValueError(f"{name}'s norm needs {name} and its upstream gradient, of one shape")
-    dq = None if dq_out is None else torch.empty(dq_out.shape, dtype=dt, device=dev)
-    dk = None if dk_out is None else torch.empty(dk_out.shape, dtype=dt, device=dev)
-    dqg = None if q_gamma is None else torch.empty(d, dtype=f32, device=dev)
-    dkg = None if k_gamma is None else torch.empty(d, dtype=f32, device=dev)
-    if workspace is None and (q_gamma is not None or k_gamma is not None):
+    dev = (dq_out if dq_out is not None else dk_out).device
+    dq = dk = dqg = dkg = None
+    qp = kp = dqp = dkp = dqgp = dkgp = wsp = None
+    qs = ks = ws_bytes = 0
+    if q_gamma is not None:
+        if q is None or dq_out is None or q.shape != dq_out.shape:
+            raise ValueError("q's norm needs q and its upstream gradient, of one shape")
+        qp, qs = _tokens(q, index, dt, "q")
+        dqg = torch.empty(d, dtype=f32, device=dev)
+        dqgp = dqg.data_ptr()
+    if k_gamma is not None:
+        if k is None or dk_out is None or k.shape != dk_out.shape:
+            raise ValueError("k's norm needs k and its upstream gradient, of one shape")
+        kp, ks = _tokens(k, index, dt, "k")
+        dkg = torch.empty(d, dtype=f32, device=dev)
+        dkgp = dkg.data_ptr()
+    uq, uqs = _tokens(dq_out, index, dt, "dq_out")
+    uk, uks = _tokens(dk_out, index, dt, "dk_out")
+    if dq_out is not None:
+        dq = torch.empty((T, H_q, d), dtype=dt, device=dev)
+        dqp = dq.data_ptr()
+    if dk_out is not None:
+        dk = torch.empty((T, H_k, d), dtype=dt, device=dev)
+        dkp = dk.data_ptr()
+    if workspace is not None:
+        wsp, ws_bytes = _on(workspace, index, None, "workspace"), workspace.numel() * workspace.element_size()
+    elif dqg is not None or dkg is not None:
         workspace = torch.empty(nt_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
-    uq, uqs = _tokens(dq_out, dev, dt, "dq_out")
-    uk, uks = _tokens(dk_out, dev, dt, "dk_out")
-    qp, qs = _tokens(q if q_gamma is not None else None, dev, dt, "q")
-    kp, ks = _tokens(k if k_gamma is not None else None, dev, dt, "k")
-    H_q = 0 if dq_out is None else dq_out.shape[1]
-    H_k = 0 if dk_out is None else dk_out.shape[1]
-    with _launch(dev, stream) as s:
-        st = lib().nt_qk_norm_rope_bwd(
-            _dtype(dq_out if dq_out is not None else dk_out), uq, uqs, uk, uks, qp, qs, kp, ks, T, H_q, H_k, d,
-            _on(q_gamma, dev, f32, "q_gamma"), _on(k_gamma, dev, f32, "k_gamma"), float(eps), *tail,
-            int(bool(interleaved)), float(rot_scale), _on(dq, dev), H_q * d, _on(dk, dev), H_k * d, _on(dqg, dev),
-            _on(dkg, dev), _on(workspace, dev, None, "workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), s)
-        _check(st, "nt_qk_norm_rope_bwd")
+        wsp, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _run("nt_qk_norm_rope_bwd", index, stream, _dtype(dq_out if dq_out is not None else dk_out), uq, uqs, uk, uks,
+         qp, qs, kp, ks, T, H_q, H_k, d, _on(q_gamma, index, f32, "q_gamma"), _on(k_gamma, index, f32, "k_gamma"),
+         eps, *tail, 1 if interleaved else 0, rot_scale, dqp, H_q * d, dkp, H_k * d, dqgp, dkgp, wsp, ws_bytes)
     return dq, dk, dqg, dkg
 
 
@@ -788,19 +806,17 @@ class KVPages:
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must share the shape (n_pages, H_kv, page_size, d), dtype and device")
         self.k, self.v = k, v
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self.index = k.device, k.dtype, _cuda_index(k)
         self.n_pages, self.H_kv, self.page_size, self.d = k.shape
-        if self.device.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        self.c = nt_kv_pages(_on(k, self.device) or None, _on(v, self.device) or None, self.n_pages, self.page_size,
-                             self.H_kv, self.d, _dtype(k))
+        self.c = nt_kv_pages(_on(k, self.index, k.dtype, "k") or None, _on(v, self.index, k.dtype, "v") or None,
+                             self.n_pages, self.page_size, self.H_kv, self.d, _dtype(k))
         self.ref = ctypes.byref(self.c)
 
 
-def _table(block_table: torch.Tensor, B: int, dev):
+def _table(block_table: torch.Tensor, B: int, index: int):
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be (B = {B}, max_pages)")
-    return _on(block_table, dev, torch.int32, "block_table"), block_table.shape[1]
+    return _on(block_table, index, torch.int32, "block_table"), block_table.shape[1]
 
 
 def nt_paged_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -808,33 +824,30 @@ def nt_paged_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     """Keys and values of packed tokens (T, H_kv, d) into their sequences'
     pages: token t of ``cu_seqlens`` segment b goes to position
     pos0[b] + t - cu[b] (``pos0`` None: 0) of row b of ``block_table``."""
-    dev = pages.device
-    if k.shape != v.shape or k.dim() != 3 or tuple(k.shape[1:]) != (pages.H_kv, pages.d):
+    index, dt = pages.index, pages.dtype
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != pages.H_kv or k.shape[2] != pages.d:
         raise ValueError("k and v must be (T, H_kv, d) of the pages")
     B = cu_seqlens.numel() - 1
     if pos0 is not None and pos0.numel() != B:
         raise ValueError("pos0 is one start per cu_seqlens segment")
-    kp, ks = _tokens(k, dev, pages.dtype, "k")
-    vp, vs = _tokens(v, dev, pages.dtype, "v")
-    tab, max_pages = _table(block_table, B, dev)
+    kp, ks = _tokens(k, index, dt, "k")
+    vp, vs = _tokens(v, index, dt, "v")
+    tab, max_pages = _table(block_table, B, index)
     i32 = torch.int32
-    with _launch(dev, stream) as s:
-        st = lib().nt_paged_write(pages.ref, kp, ks, vp, vs, k.shape[0], _on(cu_seqlens, dev, i32, "cu_seqlens"), B,
-                                  _on(pos0, dev, i32, "pos0"), tab, max_pages, s)
-        _check(st, "nt_paged_write")
+    _run("nt_paged_write", index, stream, pages.ref, kp, ks, vp, vs, k.shape[0],
+         _on(cu_seqlens, index, i32, "cu_seqlens"), B, _on(pos0, index, i32, "pos0"), tab, max_pages)
 
 
 def nt_paged_copy(pages: KVPages, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Page src[i] copied over page dst[i] (int32 HOST tensors): no page
     twice in dst, none in both."""
-    if src.device.type != "cpu" or dst.device.type != "cpu":
+    if src.is_cuda or dst.is_cuda:
         raise ValueError("src and dst are host tensors")
-    if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.dim() != 1 or src.shape != dst.shape:
+    if src.dtype is not torch.int32 or dst.dtype is not torch.int32 or src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be int32, one entry per copy")
     if not (src.is_contiguous() and dst.is_contiguous()):
         raise ValueError("src and dst must be contiguous")
-    with _launch(pages.device, stream) as s:
-        _check(lib().nt_paged_copy(pages.ref, src.data_ptr(), dst.data_ptr(), src.numel(), s), "nt_paged_copy")
+    _run("nt_paged_copy", pages.index, stream, pages.ref, src.data_ptr(), dst.data_ptr(), src.numel())
 
 
 def nt_paged_attn_workspace_bytes(H: int, H_kv: int, d: int) -> int:
@@ -849,30 +862,29 @@ def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, le
     lengths[b] positions of its paged cache; H a multiple of H_kv.  Returns
     (o, lse [H, B] or None).  ``workspace``: nt_paged_attn_workspace_bytes()
     bytes (None allocates them per call)."""
-    dev, d = pages.device, pages.d
+    index, dt, d = pages.index, pages.dtype, pages.d
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError("q must be (B, H, d) with the pages' d")
     B, H, _ = q.shape
     if lengths.numel() != B:
         raise ValueError("one length per sequence")
-    qp, qs = _tokens(q, dev, pages.dtype, "q")
-    tab, max_pages = _table(block_table, B, dev)
+    qp, qs = _tokens(q, index, dt, "q")
+    tab, max_pages = _table(block_table, B, index)
     if out is None:
-        out = torch.empty(B, H, d, dtype=pages.dtype, device=dev)
+        out = torch.empty((B, H, d), dtype=dt, device=pages.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if want_lse and lse is None:
-        lse = torch.empty(H, B, dtype=torch.float32, device=dev)
-    if lse is not None and tuple(lse.shape) != (H, B):
+        lse = torch.empty((H, B), dtype=torch.float32, device=pages.device)
+    if lse is not None and (lse.dim() != 2 or lse.shape[0] != H or lse.shape[1] != B):
         raise ValueError("lse must be (H, B)")
     if workspace is None:
-        workspace = torch.empty(nt_paged_attn_workspace_bytes(H, pages.H_kv, d), dtype=torch.uint8, device=dev)
-    with _launch(dev, stream) as s:
-        st = lib().nt_paged_attn(pages.ref, qp, qs, B, H, tab, max_pages, _on(lengths, dev, torch.int32, "lengths"),
-                                 d ** -0.5 if scale is None else float(scale), _on(out, dev, pages.dtype, "out"),
-                                 _on(lse, dev, torch.float32, "lse"), _on(workspace, dev, None, "workspace"),
-                                 workspace.numel() * workspace.element_size(), s)
-        _check(st, "nt_paged_attn")
+        workspace = torch.empty(nt_paged_attn_workspace_bytes(H, pages.H_kv, d), dtype=torch.uint8,
+                                device=pages.device)
+    _run("nt_paged_attn", index, stream, pages.ref, qp, qs, B, H, tab, max_pages,
+         _on(lengths, index, torch.int32, "lengths"), d ** -0.5 if scale is None else scale,
+         _on(out, index, dt, "out"), _on(lse, index, torch.float32, "lse"), _on(workspace, index, None, "workspace"),
+         workspace.numel() * workspace.element_size())
     return out, lse
 
 
