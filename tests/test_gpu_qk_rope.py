@@ -59,6 +59,8 @@ CASES = [
     ([77, 3], None, 7, 0, 32, 32, False, True, False, {}, 1.0),       # queries only
     ([77, 3], None, 0, 5, 32, 16, True, False, True, {}, 1.0),        # keys only
     ([3000, 1, 2048], None, 5, 1, 64, 64, False, True, True, {}, 1.0),
+    ([1] + [0] * 70 + [2, 0, 1, 3] + [0] * 33 + [1] * 90 + [0] * 1200 + [5], None, 2, 1, 32, 32, False, True, True, {}, 1.0),
+    ([1] * 1500, list(range(1500)), 1, 1, 16, 16, True, False, True, {}, 1.0),   # 32 tokens, 32 segments a warp
 ]
 
 
@@ -158,6 +160,26 @@ def test_nan_rows_stay_in_their_row(nt):
                                 q_gamma=torch.ones(64, device=DEV))
     bad = torch.isnan(out.cpu()).any(-1)
     assert bad[4, 1] and bad[7, 0] and int(bad.sum()) == 2
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinities_stay_in_their_pair(nt, interleaved):
+    """Without a norm a column mixes with its pair's other column only, and
+    one behind the rotated part with none, in both directions."""
+    q = _rand(1, 5, 1, 64)
+    q[0, 0, 40] = math.inf
+    q[1, 0, 50] = -math.inf
+    q[2, 0, 3] = math.nan
+    a, b = columns(32, interleaved)
+    pair = {int(x): int(y) for x, y in zip(a, b)} | {int(y): int(x) for x, y in zip(a, b)}
+    turns = nt.nt_rope_turns(32, device=DEV)
+    pos = torch.arange(1, 6, dtype=torch.int32, device=DEV)
+    fwd = nt.nt_qk_norm_rope(q.to(DEV), None, turns, positions=pos, interleaved=interleaved)[0].cpu()
+    bwd = nt.nt_qk_norm_rope_bwd(q.to(DEV), None, turns, positions=pos, interleaved=interleaved)[0].cpu()
+    for out in (fwd, bwd):
+        assert out[0, 0, 40] == math.inf and out[1, 0, 50] == -math.inf
+        bad = ~torch.isfinite(out)
+        assert bad[2].nonzero()[:, 1].tolist() == sorted((3, pair[3])) and int(bad.sum()) == 4
 
 
 # Backward: g is off by 8 steps of its pair's |.| + |.| (as above without the

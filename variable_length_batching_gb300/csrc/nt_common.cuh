@@ -371,7 +371,7 @@ struct RopeProblem {
   float* dq_gamma;
   float* dk_gamma;
 };
-constexpr int kRopeMaxParts = 1024;     // CTAs of the backward, at most
+constexpr int kRopeMaxCtas = 512;
 size_t qk_rope_bwd_workspace_bytes(int d);
 cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* workspace, unsigned int* status,
                            cudaStream_t s);

@@ -13,19 +13,26 @@
 // and backward, with g the upstream gradient rotated back,
 //   dgamma = sum g x r,  h = g gamma,  dx = r (h - x r mean(h x r)).
 //
-// Both directions are bound by HBM (about ten operations an element), so the
-// layout is about keeping loads in flight.  A CTA serves q or k, for tb
-// tokens.  Groups of LP lanes take one (token, head) row at a time, a lane
-// two 8-element chunks: both halves of its eight pairs in either layout.  A
-// group stays with one token and walks its heads, so the token's cosines and
-// sines (formed once per CTA in shared memory), multiplied by gamma in the
-// forward, stay in registers, and the rows of kBatch heads are requested
-// before the first is used, in the forward before the table is even formed.
-// Everything between the load and the one rounding of the store is fp32.
-#include "nt_common.cuh"
+// Both directions are bound by HBM, and at about ten operations an element
+// not by much, so the layout keeps loads in flight without holding registers
+// or waiting at barriers.  A row (one head of one token) is a group of LP
+// lanes, a lane two 8-element chunks: both halves of its eight pairs in
+// either layout.  A warp takes 32 / LP tokens at a time and walks their
+// heads, one row per group and step; the steps of the whole call are one line
+// that the warps share out evenly.  Each thread copies its own chunks of the
+// rows kSlots steps ahead into its own words of shared memory (cp.async), so
+// nothing but its own copies is ever waited for, and 128 KB per SM are in
+// flight.  A warp forms its tokens' cosines and sines itself when it comes to
+// new tokens (a tenth of the work of their heads), and keeps them, in the
+// forward multiplied by gamma, in registers.  Everything between the load and
+// the one rounding of the store is fp32, in packed pairs.
+#include "tc_ptx.cuh"
 
 namespace nt {
 namespace {
+
+using tc::ffma2;
+using tc::fmul2;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -38,111 +45,69 @@ struct Side {
   int64_t xs, us, os;   // token strides in elements
   const float* gamma;   // [d] or NULL (no norm)
   int H;
-  int hg_log2;          // groups that share a token: 1 << hg_log2
-  int ctas;             // CTAs that serve the side (the first side's come first)
 };
 
 struct Args {
   Side side[2];
   int64_t T;
+  int64_t per_warp, extra;   // steps of a warp, and how many warps take one more
+  int64_t side_steps;        // backward: steps of the first side
   int d, rot, B;
   float inv_d, eps, scale;
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* positions;
   const uint64_t* turns;
-  float* partial;       // backward: [CTAs][d] sums for dgamma
+  float* partial;            // backward: [CTAs][2][d] sums for dgamma
   unsigned int* status;
 };
 
-// Position of a token of segment b; false (flagged) if the offsets do not
-// place the token there.
-__device__ __forceinline__ bool position_in(const Args& a, int64_t t, int b, int64_t& pos) {
-  const int start = a.cu[b];
-  if (start > t || a.cu[b + 1] <= t || start < 0) {
+// Position of this lane's token t; the warp's tokens are t_first, ...,
+// t_last (consecutive, clipped to T).  False (flagged) if the offsets place
+// it in no segment.  The warp searches its first token's segment together, 32
+// probes a step (two dependent loads for up to 1,024 segments), and finds the
+// others among the 32 boundaries that follow; a token behind those (tokens
+// separated by many empty segments) is searched by itself.
+__device__ __forceinline__ bool lane_position(const Args& a, int64_t t, int64_t t_first, int n_tok, int64_t& pos) {
+  const int lane = threadIdx.x & 31;
+  pos = 0;
+  if (a.rot == 0) return true;
+  if (a.positions) {
+    pos = a.positions[t];
+    return true;
+  }
+  const int b0 = segment_of_warp(a.cu, a.B, t_first);
+  const int first_start = a.cu[b0];
+  const int bound = a.cu[min((int64_t)b0 + 1 + lane, (int64_t)a.B)];     // repeats cu[B] past the end
+  int mine = 0;
+  for (int k = 0; k < n_tok; ++k) {
+    const int c = __popc(__ballot_sync(0xffffffffu, bound <= t_first + k));
+    if (t_first + k == t) mine = c;
+  }
+  int start = __shfl_sync(0xffffffffu, bound, max(mine - 1, 0)), end = __shfl_sync(0xffffffffu, bound, min(mine, 31));
+  int seg = b0 + mine;
+  if (mine == 0) start = first_start;
+  if (mine == 32) {
+    seg = segment_of_thread(a.cu, a.B, t);
+    start = a.cu[seg];
+    end = a.cu[seg + 1];
+  }
+  if (seg >= a.B || start > t || end <= t || start < 0) {
     flag_device(a.status, kDevCheck);
     return false;
   }
-  pos = t - start + (a.pos0 ? a.pos0[b] : 0);
+  pos = t - start + (a.pos0 ? a.pos0[seg] : 0);
   return true;
 }
 
-// Shared: pos[tb] (int64), ok[tb] (int), then the tile's table: pairs of
-// (cos, sin) as float4 {c0, s0, c1, s1}, the four of a lane's eight pairs
-// rot/16 apart, so that the lanes of a group read consecutive words.
-struct Tile {
-  int64_t* pos;
-  int* ok;
-  float4* cs;
-};
-__host__ __device__ __forceinline__ int table_offset(int tb) { return (tb * 12 + 15) & ~15; }
-__device__ __forceinline__ Tile tile_of(unsigned char* smem, int tb) {
-  Tile s;
-  s.pos = reinterpret_cast<int64_t*>(smem);
-  s.ok = reinterpret_cast<int*>(smem + tb * 8);
-  s.cs = reinterpret_cast<float4*>(smem + table_offset(tb));
-  return s;
-}
-
-// With nothing to rotate the positions are not read (and may be NULL).
-__device__ void fill_tile(const Args& a, const Tile& s, int64_t t0, int n) {
-  if (a.rot == 0 || a.positions) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      s.ok[i] = 1;
-      s.pos[i] = a.rot == 0 ? 0 : a.positions[t0 + i];
-    }
-  } else if (n <= kWarps) {
-    // few tokens: one per warp, 32 probes a step (the latency of a search is
-    // what a decoding step waits for: 2 steps instead of 8 for 256 segments)
-    const int i = threadIdx.x >> 5;
-    if (i < n) {
-      const int b = segment_of_warp(a.cu, a.B, t0 + i);
-      if ((threadIdx.x & 31) == 0) {
-        int64_t p = 0;
-        s.ok[i] = position_in(a, t0 + i, b, p);
-        s.pos[i] = p;
-      }
-    }
-  } else {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      int64_t p = 0;
-      s.ok[i] = position_in(a, t0 + i, segment_of_thread(a.cu, a.B, t0 + i), p);
-      s.pos[i] = p;
-    }
-  }
-  __syncthreads();
-  const int quarter = a.rot >> 2;               // float4 words of one token
-  const int lanes = a.rot >> 4;
-  for (int e = threadIdx.x; e < n * quarter; e += kThreads) {
-    const int tok = e / quarter, w = e - tok * quarter;
-    const int q = w / lanes, i = w - q * lanes;  // word q of lane i: pairs 8 i + 2 q, + 1
-    const uint64_t p = (uint64_t)s.pos[tok];
-    float v[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint64_t frac = p * a.turns[8 * i + 2 * q + h];
-      float sn, cn;
-      sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &sn, &cn);   // 2^-31: half turns
-      v[2 * h] = cn * a.scale;
-      v[2 * h + 1] = sn * a.scale;
-    }
-    s.cs[e] = make_float4(v[0], v[1], v[2], v[3]);
-  }
-  __syncthreads();
-}
-
-// A lane's place: its group's token within the tile and first head, and the
-// columns of its two chunks.
+// A lane's columns.
 template <int LP, bool kInter>
 struct Lane {
-  int i, tok, h0, hg, ca, cb;
+  int i, g, ca, cb;
   bool on, rotated;
-  __device__ __forceinline__ Lane(const Args& a, const Side& p) {
+  __device__ __forceinline__ Lane(const Args& a) {
     i = threadIdx.x % LP;
-    const int g = threadIdx.x / LP;
-    hg = 1 << p.hg_log2;
-    tok = g >> p.hg_log2;
-    h0 = g & (hg - 1);
+    g = threadIdx.x % 32 / LP;
     on = 16 * i < a.d;
     rotated = 16 * i < a.rot;
     if (!kInter && rotated) {
@@ -153,21 +118,30 @@ struct Lane {
       cb = 16 * i + 8;
     }
   }
-  // cosines and sines of the lane's eight pairs (1 and 0 where nothing turns)
-  __device__ __forceinline__ void angles(const Args& a, const Tile& s, float (&c)[8], float (&sn)[8]) const {
+  // cosines and sines of the lane's eight pairs at pos (1 and 0 where nothing turns)
+  __device__ __forceinline__ void angles(const Args& a, int64_t pos, float (&c)[8], float (&s)[8]) const {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 w = rotated ? s.cs[tok * (a.rot >> 2) + q * (a.rot >> 4) + i] : make_float4(1.f, 0.f, 1.f, 0.f);
-      c[2 * q] = w.x;
-      sn[2 * q] = w.y;
-      c[2 * q + 1] = w.z;
-      sn[2 * q + 1] = w.w;
+    for (int e = 0; e < 8; ++e) {
+      c[e] = 1.f;
+      s[e] = 0.f;
+    }
+    if (!rotated) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t frac = (uint64_t)pos * a.turns[8 * i + e];
+      sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31: half turns
+      c[e] *= a.scale;
+      s[e] *= a.scale;
     }
   }
+  __device__ __forceinline__ void gamma(const float* p, float (&v)[16]) const {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 1.f;
+    if (!p || !on) return;
+    load8(p + ca, v);
+    load8(p + cb, v + 8);
+  }
 };
-// Element indices (0..15: chunk a, then chunk b) of pair e's two parts.
-template <bool kInter> __device__ constexpr int part_a(int e) { return kInter ? 2 * e : e; }
-template <bool kInter> __device__ constexpr int part_b(int e) { return kInter ? 2 * e + 1 : e + 8; }
 
 template <int LP>
 __device__ __forceinline__ float group_sum(float v) {
@@ -176,259 +150,386 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// One row's two chunks as loaded, and as fp32.
-template <typename T> struct Raw;
-template <> struct Raw<bf16> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const bf16* x, int ca, int cb) {
-    a = *reinterpret_cast<const uint4*>(x + ca);
-    b = *reinterpret_cast<const uint4*>(x + cb);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[16]) const {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-};
-template <> struct Raw<float> {
-  float4 a[4];
-  __device__ __forceinline__ void load(const float* x, int ca, int cb) {
-    a[0] = *reinterpret_cast<const float4*>(x + ca);
-    a[1] = *reinterpret_cast<const float4*>(x + ca + 4);
-    a[2] = *reinterpret_cast<const float4*>(x + cb);
-    a[3] = *reinterpret_cast<const float4*>(x + cb + 4);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __device__ __forceinline__ void get(float (&v)[16]) const {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[4 * e] = a[e].x;
-      v[4 * e + 1] = a[e].y;
-      v[4 * e + 2] = a[e].z;
-      v[4 * e + 3] = a[e].w;
-    }
-  }
-};
+// The thread's own words of the ring: 16-byte word w of slot s at
+// (s * words + w) * kThreads + thread, so that a warp's accesses are
+// consecutive.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <typename T, int LP, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const Args a) {
-  constexpr int kBatch = sizeof(T) == 2 ? 3 : 2;        // rows in flight per group
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int sd = blockIdx.x >= a.side[0].ctas;
-  const Side& p = a.side[sd];
-  const Lane<LP, kInter> me(a, p);
-  const int tb = kThreads / LP >> p.hg_log2;
-  const int64_t t0 = (int64_t)(blockIdx.x - (sd ? a.side[0].ctas : 0)) * tb;
-  const int n = (int)min64(tb, a.T - t0);
-  const Tile s = tile_of(smem, tb);
-  const bool here = me.on && me.tok < n;
-  const T* x = static_cast<const T*>(p.x) + (t0 + me.tok) * p.xs;
-  Raw<T> raw[kBatch];
-  auto load = [&](int h) {
+template <typename T>
+__device__ __forceinline__ void copy_row(uint32_t dst, const T* x, int ca, int cb) {
+  constexpr int kHalf = 8 * sizeof(T) / 16;          // 16-byte words of a chunk
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      raw[k].zero();
-      if (here && h + k * me.hg < p.H) raw[k].load(x + (int64_t)(h + k * me.hg) * a.d, me.ca, me.cb);
-    }
-  };
-  pdl_wait();
-  load(me.h0);
-  fill_tile(a, s, t0, n);
-  // pair e: out_a = r (x_a m[0] - x_b m[1]), out_b = r (x_a m[2] + x_b m[3])
-  float m[8][4];
-  const bool norm = p.gamma != nullptr;
-  {
-    float c[8], sn[8], gm[16];
-    if (here) {
-      me.angles(a, s, c, sn);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = sn[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) gm[e] = 1.f;
-    if (norm && me.on) {
-      Raw<float> g;
-      g.load(p.gamma, me.ca, me.cb);
-      g.get(gm);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float ga = gm[part_a<kInter>(e)], gb = gm[part_b<kInter>(e)];
-      m[e][0] = ga * c[e];
-      m[e][1] = gb * sn[e];
-      m[e][2] = ga * sn[e];
-      m[e][3] = gb * c[e];
-    }
+  for (int w = 0; w < kHalf; ++w) {
+    copy16(dst + w * kThreads * 16, x + ca + w * (16 / sizeof(T)));
+    copy16(dst + (kHalf + w) * kThreads * 16, x + cb + w * (16 / sizeof(T)));
   }
-  const bool write = here && s.ok[me.tok];
-  T* o = static_cast<T*>(p.out) + (t0 + me.tok) * p.os;
-  // the loop's bounds are the warp's: its groups may hold different first heads
-  for (int hb = 0; hb < p.H; hb += kBatch * me.hg) {
-    const int h = hb + me.h0;
-    if (hb) load(h);
+}
+template <typename T>
+__device__ __forceinline__ void read_row(const uint4* src, float (&v)[16]) {
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      float v[16];
-      raw[k].get(v);
-      float r = 1.f;
-      if (norm) {
-        float ss = 0.f;
+    for (int w = 0; w < 2; ++w) {
+      const uint4 x = src[w * kThreads];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
-        r = rsqrtf(group_sum<LP>(ss) * a.inv_d + a.eps);
+      for (int e = 0; e < 4; ++e) {
+        v[8 * w + 2 * e] = tc::bf16lo(u[e]);
+        v[8 * w + 2 * e + 1] = tc::bf16hi(u[e]);
       }
-      float w[16];
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int ia = part_a<kInter>(e), ib = part_b<kInter>(e);
-        w[ia] = r * (v[ia] * m[e][0] - v[ib] * m[e][1]);
-        w[ib] = r * (v[ia] * m[e][2] + v[ib] * m[e][3]);
-      }
-      if (write && h + k * me.hg < p.H) {
-        T* y = o + (int64_t)(h + k * me.hg) * a.d;
-        store8(y + me.ca, w);
-        store8(y + me.cb, w + 8);
-      }
+    for (int w = 0; w < 4; ++w) {
+      const uint4 x = src[w * kThreads];
+      v[4 * w] = __uint_as_float(x.x);
+      v[4 * w + 1] = __uint_as_float(x.y);
+      v[4 * w + 2] = __uint_as_float(x.z);
+      v[4 * w + 3] = __uint_as_float(x.w);
     }
   }
 }
 
+// sum of v[e]^2, or of u[e] v[e]
+__device__ __forceinline__ float dot16(const float (&u)[16], const float (&v)[16]) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) ffma2(u[e], u[e + 1], v[e], v[e + 1], s0, s1, s0, s1);
+  return s0 + s1;
+}
+
+// out = the rotation of v by per-pair factors: for pair (a, b) of eight,
+// out_a = v_a f[.] + v_b f[.], in packed pairs.  m holds, for the half layout
+// and the two pairs e, e + 1 at a time: {aa, aa'}, {ab, ab'}, {ba, ba'},
+// {bb, bb'}; for the interleaved one and pair e: {aa, bb}, {ab, ba}.
+template <bool kInter>
+__device__ __forceinline__ void turn(const float (&v)[16], const float (&m)[32], float (&w)[16]) {
+  if constexpr (kInter) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x, y;
+      fmul2(v[2 * e + 1], v[2 * e], m[4 * e + 2], m[4 * e + 3], x, y);
+      ffma2(v[2 * e], v[2 * e + 1], m[4 * e], m[4 * e + 1], x, y, w[2 * e], w[2 * e + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float x, y;
+      fmul2(v[8 + e], v[9 + e], m[4 * e + 2], m[4 * e + 3], x, y);
+      ffma2(v[e], v[e + 1], m[4 * e], m[4 * e + 1], x, y, w[e], w[e + 1]);
+      fmul2(v[e], v[e + 1], m[4 * e + 4], m[4 * e + 5], x, y);
+      ffma2(v[8 + e], v[9 + e], m[4 * e + 6], m[4 * e + 7], x, y, w[8 + e], w[9 + e]);
+    }
+  }
+}
+
+// The same for a lane behind the rotated columns: each value by its own
+// factor, so that an infinity stays in its column.
+template <bool kInter>
+__device__ __forceinline__ void pass(const float (&v)[16], const float (&m)[32], float (&w)[16]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (kInter) {
+      w[2 * e] = v[2 * e] * m[4 * e];
+      w[2 * e + 1] = v[2 * e + 1] * m[4 * e + 1];
+    } else {
+      const int b = 4 * (e & ~1) + (e & 1);
+      w[e] = v[e] * m[b];
+      w[8 + e] = v[8 + e] * m[b + 6];
+    }
+  }
+}
+
+// A warp's steps [lo, hi) of the line.
+__device__ __forceinline__ void warp_steps(const Args& a, int64_t& lo, int64_t& hi) {
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  lo = w * a.per_warp + min64(w, a.extra);
+  hi = lo + a.per_warp + (w < a.extra ? 1 : 0);
+}
+
+template <typename T> struct Ring {          // forward: one row a step
+  static constexpr int kWords = sizeof(T);   // 16-byte words of a row per lane
+  static constexpr int kSlots = 16 / sizeof(T);
+  static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
+};
+
 template <typename T, int LP, bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
-  constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int sd = blockIdx.x >= a.side[0].ctas;
-  const Side& p = a.side[sd];
-  const Lane<LP, kInter> me(a, p);
-  const int tb = kThreads / LP >> p.hg_log2;
-  const Tile s = tile_of(smem, tb);
-  const bool norm = p.gamma != nullptr;
-  float gm[16], acc[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    gm[e] = 1.f;
-    acc[e] = 0.f;
-  }
+__global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
+  using R = Ring<T>;
+  extern __shared__ __align__(16) uint4 ring[];
+  constexpr int kTok = 32 / LP;
+  const Lane<LP, kInter> me(a);
+  int64_t lo, hi;
+  warp_steps(a, lo, hi);
+  if (lo >= hi) return;
+  const int heads = a.side[0].H + a.side[1].H;
+  int64_t tg = lo / heads;                   // the warp's tokens: tg * kTok, ...
+  int h = (int)(lo - tg * heads);
   pdl_wait();
-  pdl_trigger();
-  if (norm && me.on) {
-    Raw<float> g;
-    g.load(p.gamma, me.ca, me.cb);
-    g.get(gm);
-  }
-  for (int64_t t0 = (int64_t)(blockIdx.x - (sd ? a.side[0].ctas : 0)) * tb; t0 < a.T; t0 += (int64_t)p.ctas * tb) {
-    const int n = (int)min64(tb, a.T - t0);
-    const bool here = me.on && me.tok < n;
-    const T* u = static_cast<const T*>(p.up) + (t0 + me.tok) * p.us;
-    const T* x = static_cast<const T*>(p.x) + (t0 + me.tok) * p.xs;
-    Raw<T> ru[kBatch], rx[kBatch];
-    auto load = [&](int h) {
+  // the copies' place runs kSlots steps ahead
+  int64_t pt = tg * kTok + me.g;
+  int ph = h;
+  auto copy = [&](int64_t step, int slot) {
+    if (step < hi) {
+      if (me.on && pt < a.T) {
+        const bool k = ph >= a.side[0].H;
+        const Side& p = a.side[k];
+        copy_row(tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x),
+                 static_cast<const T*>(p.x) + pt * p.xs + (int64_t)(ph - (k ? a.side[0].H : 0)) * a.d, me.ca, me.cb);
+      }
+      if (++ph == heads) {
+        ph = 0;
+        pt += kTok;
+      }
+    }
+    copy_commit();
+  };
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        ru[k].zero();
-        rx[k].zero();
-        if (here && h + k * me.hg < p.H) {
-          const int64_t at = (int64_t)(h + k * me.hg) * a.d;
-          ru[k].load(u + at, me.ca, me.cb);
-          if (norm) rx[k].load(x + at, me.ca, me.cb);
+  for (int s = 0; s < R::kSlots; ++s) copy(lo + s, s);
+  float c[8], sn[8], m[32];
+  bool fresh = true, write = false;
+  int slot = 0;
+  for (int64_t step = lo; step < hi; ++step) {
+    const int64_t t = tg * kTok + me.g;
+    if (fresh || h == 0) {                   // new tokens
+      int64_t pos;
+      write = lane_position(a, min64(t, a.T - 1), tg * kTok, (int)min64(kTok, a.T - tg * kTok), pos) && me.on &&
+              t < a.T;
+      me.angles(a, pos, c, sn);
+    }
+    const int sd = h >= a.side[0].H;
+    const Side& p = a.side[sd];
+    if (fresh || h == 0 || h == a.side[0].H) {
+      float gm[16];
+      me.gamma(p.gamma, gm);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float ga = gm[kInter ? 2 * e : e], gb = gm[kInter ? 2 * e + 1 : 8 + e];
+        if constexpr (kInter) {
+          m[4 * e] = ga * c[e];
+          m[4 * e + 1] = gb * c[e];
+          m[4 * e + 2] = -gb * sn[e];
+          m[4 * e + 3] = ga * sn[e];
+        } else {
+          const int b = 4 * (e & ~1) + (e & 1);
+          m[b] = ga * c[e];
+          m[b + 2] = -gb * sn[e];
+          m[b + 4] = ga * sn[e];
+          m[b + 6] = gb * c[e];
         }
       }
-    };
-    load(me.h0);
-    __syncthreads();                         // the tile of the step before is read out
-    fill_tile(a, s, t0, n);
-    float c[8], sn[8];
-    if (here) {
-      me.angles(a, s, c, sn);
+      fresh = false;
+    }
+    copy_wait<R::kSlots - 1>();
+    float v[16], w[16];
+    if (me.on && t < a.T) {
+      read_row<T>(ring + slot * R::kWords * kThreads + threadIdx.x, v);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = sn[e] = 0.f;
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
     }
-    const bool write = here && s.ok[me.tok];
-    T* o = static_cast<T*>(p.out) + (t0 + me.tok) * p.os;
-    for (int hb = 0; hb < p.H; hb += kBatch * me.hg) {
-      const int h = hb + me.h0;
-      if (hb) load(h);
+    if (me.rotated) turn<kInter>(v, m, w);
+    else pass<kInter>(v, m, w);
+    if (p.gamma) {
+      const float r = rsqrtf(group_sum<LP>(dot16(v, v)) * a.inv_d + a.eps);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        float v[16], g[16];
-        ru[k].get(v);
+      for (int e = 0; e < 16; e += 2) fmul2(w[e], w[e + 1], r, r, w[e], w[e + 1]);
+    }
+    copy(step + R::kSlots, slot);
+    slot = slot + 1 == R::kSlots ? 0 : slot + 1;
+    if (write) {
+      T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)(h - (sd ? a.side[0].H : 0)) * a.d;
+      store8(y + me.ca, w);
+      store8(y + me.cb, w + 8);
+    }
+    if (++h == heads) {
+      h = 0;
+      ++tg;
+    }
+  }
+}
+
+template <typename T> struct RingBwd {       // backward: the upstream row and the input's
+  static constexpr int kWords = 2 * sizeof(T);
+  static constexpr int kSlots = sizeof(T) == 2 ? 4 : 3;
+  static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
+};
+
+// The backward's line is all steps of q, then all of k: a warp sums dgamma of
+// one side in registers and puts it away when it comes to the other.
+template <typename T, int LP, bool kInter>
+__global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
+  using R = RingBwd<T>;
+  extern __shared__ __align__(16) uint4 ring[];
+  constexpr int kTok = 32 / LP;
+  float* red = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(ring) + R::kBytes);   // [kWarps][2][d]
+  const Lane<LP, kInter> me(a);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (a.partial) {
+    for (int e = lane; e < 2 * a.d; e += 32) red[warp * 2 * a.d + e] = 0.f;
+    __syncwarp();
+  }
+  int64_t lo, hi;
+  warp_steps(a, lo, hi);
+  float acc[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int ia = part_a<kInter>(e), ib = part_b<kInter>(e);
-          g[ia] = v[ia] * c[e] + v[ib] * sn[e];
-          g[ib] = v[ib] * c[e] - v[ia] * sn[e];
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  auto put_away = [&](int sd) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float v = acc[e];
+#pragma unroll
+      for (int x = 16; x >= LP; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+      if (lane < LP && me.on) red[(warp * 2 + sd) * a.d + (e < 8 ? me.ca + e : me.cb + e - 8)] = v;
+      acc[e] = 0.f;
+    }
+  };
+  int sd = lo >= a.side_steps;
+  int64_t at = lo - (sd ? a.side_steps : 0);
+  int H = a.side[sd].H;
+  int64_t tg = lo < hi ? at / H : 0;
+  int h = lo < hi ? (int)(at - tg * H) : 0;
+  int psd = sd, ph = h, pH = H;
+  int64_t pt = tg * kTok + me.g;
+  const int64_t tgs = (a.T + kTok - 1) / kTok;
+  auto copy = [&](int64_t step, int slot) {
+    if (step < hi) {
+      if (me.on && pt < a.T) {
+        const Side& p = a.side[psd];
+        const uint32_t dst = tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x);
+        copy_row(dst, static_cast<const T*>(p.up) + pt * p.us + (int64_t)ph * a.d, me.ca, me.cb);
+        if (p.gamma)
+          copy_row(dst + R::kWords / 2 * kThreads * 16, static_cast<const T*>(p.x) + pt * p.xs + (int64_t)ph * a.d,
+                   me.ca, me.cb);
+      }
+      if (++ph == pH) {
+        ph = 0;
+        pt += kTok;
+        if (pt - me.g >= tgs * kTok) {       // the first side is done
+          psd = 1;
+          pH = a.side[1].H;
+          pt = me.g;
         }
-        if (norm) {
-          rx[k].get(v);
-          float ss = 0.f;
+      }
+    }
+    copy_commit();
+  };
 #pragma unroll
-          for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
-          const float r = rsqrtf(group_sum<LP>(ss) * a.inv_d + a.eps);
-          float hx = 0.f;
-          const float keep = write ? r : 0.f;        // a token in no segment adds nothing
+  for (int s = 0; s < R::kSlots; ++s) copy(lo + s, s);
+  float c[8], sn[8], gm[16];
+  bool fresh = true, write = false;
+  int slot = 0;
+  for (int64_t step = lo; step < hi; ++step) {
+    const int64_t t = tg * kTok + me.g;
+    const Side& p = a.side[sd];
+    if (fresh || h == 0) {
+      int64_t pos;
+      write = lane_position(a, min64(t, a.T - 1), tg * kTok, (int)min64(kTok, a.T - tg * kTok), pos) && me.on &&
+              t < a.T;
+      me.angles(a, pos, c, sn);
+      if (fresh || tg == 0) me.gamma(p.gamma, gm);
+      fresh = false;
+    }
+    copy_wait<R::kSlots - 1>();
+    const uint4* row = ring + slot * R::kWords * kThreads + threadIdx.x;
+    float v[16], g[16];
+    const bool here = me.on && t < a.T;
+    if (here) {
+      read_row<T>(row, v);
+    } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[e] *= keep;
-            acc[e] = fmaf(g[e], v[e], acc[e]);
-            g[e] *= gm[e];
-            hx = fmaf(g[e], v[e], hx);
-          }
-          const float mean = group_sum<LP>(hx) * a.inv_d;
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    }
+    // the transposed rotation
+    if (!me.rotated) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) g[e] = r * (g[e] - v[e] * mean);
-        }
-        if (write && h + k * me.hg < p.H) {
-          T* y = o + (int64_t)(h + k * me.hg) * a.d;
-          store8(y + me.ca, g);
-          store8(y + me.cb, g + 8);
-        }
+      for (int e = 0; e < 16; ++e) g[e] = v[e];
+    } else if constexpr (kInter) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float x, y;
+        fmul2(v[2 * e + 1], v[2 * e], sn[e], -sn[e], x, y);
+        ffma2(v[2 * e], v[2 * e + 1], c[e], c[e], x, y, g[2 * e], g[2 * e + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        float x, y;
+        fmul2(v[8 + e], v[9 + e], sn[e], sn[e + 1], x, y);
+        ffma2(v[e], v[e + 1], c[e], c[e + 1], x, y, g[e], g[e + 1]);
+        fmul2(v[e], v[e + 1], -sn[e], -sn[e + 1], x, y);
+        ffma2(v[8 + e], v[9 + e], c[e], c[e + 1], x, y, g[8 + e], g[9 + e]);
+      }
+    }
+    if (p.gamma) {
+      if (here) {
+        read_row<T>(row + R::kWords / 2 * kThreads, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      }
+      const float r = rsqrtf(group_sum<LP>(dot16(v, v)) * a.inv_d + a.eps);
+      const float keep = write ? r : 0.f;            // a token in no segment adds nothing
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        fmul2(v[e], v[e + 1], keep, keep, v[e], v[e + 1]);
+        ffma2(g[e], g[e + 1], v[e], v[e + 1], acc[e], acc[e + 1], acc[e], acc[e + 1]);
+        fmul2(g[e], g[e + 1], gm[e], gm[e + 1], g[e], g[e + 1]);
+      }
+      const float mean = -group_sum<LP>(dot16(g, v)) * a.inv_d;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        ffma2(v[e], v[e + 1], mean, mean, g[e], g[e + 1], g[e], g[e + 1]);
+        fmul2(g[e], g[e + 1], r, r, g[e], g[e + 1]);
+      }
+    }
+    copy(step + R::kSlots, slot);
+    slot = slot + 1 == R::kSlots ? 0 : slot + 1;
+    if (write) {
+      T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)h * a.d;
+      store8(y + me.ca, g);
+      store8(y + me.cb, g + 8);
+    }
+    if (++h == H) {
+      h = 0;
+      if (++tg == tgs && step + 1 < hi) {            // the first side is done
+        if (a.partial) put_away(0);
+        sd = 1;
+        H = a.side[1].H;
+        tg = 0;
       }
     }
   }
   if (!a.partial) return;
-  // dgamma: the groups of a warp by shuffle, the warps through shared memory
+  if (lo < hi) put_away(sd);
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);          // [kWarps][d]
-  const int warp = threadIdx.x / 32;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float v = acc[e];
-#pragma unroll
-    for (int m = 16; m >= LP; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    if ((threadIdx.x & 31) < LP && me.on) red[warp * a.d + (e < 8 ? me.ca + e : me.cb + e - 8)] = v;
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+  for (int e = threadIdx.x; e < 2 * a.d; e += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w * a.d + c];
-    a.partial[(int64_t)blockIdx.x * a.d + c] = v;
+    for (int w = 0; w < kWarps; ++w) v += red[w * 2 * a.d + e];
+    a.partial[(int64_t)blockIdx.x * 2 * a.d + e] = v;
   }
 }
 
-// dgamma of side blockIdx.y: the sum of its CTAs' partials, in CTA order
+// dgamma of side blockIdx.y: the sum of the CTAs' partials, in CTA order
 // within each of 32 strides, then across the strides.
-__global__ void __launch_bounds__(1024) rope_dgamma_kernel(const float* partial, int parts_q, int parts_k, int d,
-                                                           float* dq_gamma, float* dk_gamma) {
+__global__ void __launch_bounds__(1024) rope_dgamma_kernel(const float* partial, int parts, int d, float* dq_gamma,
+                                                           float* dk_gamma) {
   __shared__ float red[32][33];
   const int col = threadIdx.x % 32, c = blockIdx.x * 32 + col, w = threadIdx.x / 32, sd = blockIdx.y;
   float* out = sd ? dk_gamma : dq_gamma;
   pdl_wait();
   if (!out) return;
-  const int first = sd ? parts_q : 0, end = first + (sd ? parts_k : parts_q);
   float v = 0.f;
   if (c < d) {
-#pragma unroll 4
-    for (int p = first + w; p < end; p += 32) v += partial[(int64_t)p * d + c];
+#pragma unroll 8
+    for (int p = w; p < parts; p += 32) v += partial[((int64_t)p * 2 + sd) * d + c];
   }
   red[w][col] = v;
   __syncthreads();
@@ -446,31 +547,35 @@ int group_lanes(int d) {
 }
 
 template <typename T, int LP, bool kInter>
-cudaError_t run(const Args& a, bool bwd, int grid, size_t smem, cudaStream_t s) {
-  return launch_pdl(bwd ? rope_bwd_kernel<T, LP, kInter> : rope_fwd_kernel<T, LP, kInter>, dim3(grid), dim3(kThreads),
-                    smem, s, a);
+cudaError_t run(const Args& a, bool bwd, int grid, cudaStream_t s) {
+  auto kern = bwd ? rope_bwd_kernel<T, LP, kInter> : rope_fwd_kernel<T, LP, kInter>;
+  const size_t smem = bwd ? RingBwd<T>::kBytes + (a.partial ? (size_t)kWarps * 2 * a.d * sizeof(float) : 0)
+                          : Ring<T>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
 }
 
 template <typename T, bool kInter>
-cudaError_t run_lp(const Args& a, bool bwd, int grid, size_t smem, cudaStream_t s) {
+cudaError_t run_lp(const Args& a, bool bwd, int grid, cudaStream_t s) {
   switch (group_lanes(a.d)) {
-    case 1: return run<T, 1, kInter>(a, bwd, grid, smem, s);
-    case 2: return run<T, 2, kInter>(a, bwd, grid, smem, s);
-    case 4: return run<T, 4, kInter>(a, bwd, grid, smem, s);
-    case 8: return run<T, 8, kInter>(a, bwd, grid, smem, s);
-    default: return run<T, 16, kInter>(a, bwd, grid, smem, s);
+    case 1: return run<T, 1, kInter>(a, bwd, grid, s);
+    case 2: return run<T, 2, kInter>(a, bwd, grid, s);
+    case 4: return run<T, 4, kInter>(a, bwd, grid, s);
+    case 8: return run<T, 8, kInter>(a, bwd, grid, s);
+    default: return run<T, 16, kInter>(a, bwd, grid, s);
   }
 }
 
 }  // namespace
 
-size_t qk_rope_bwd_workspace_bytes(int d) { return (size_t)kRopeMaxParts * (size_t)d * sizeof(float); }
+size_t qk_rope_bwd_workspace_bytes(int d) { return (size_t)kRopeMaxCtas * 2 * (size_t)d * sizeof(float); }
 
 cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* workspace, unsigned int* status,
                            cudaStream_t s) {
   Args a = {};
-  a.side[0] = {p.q, p.dq_out, p.q_out, p.q_stride, p.dq_out_stride, p.q_out_stride, p.q_gamma, p.H_q, 0, 0};
-  a.side[1] = {p.k, p.dk_out, p.k_out, p.k_stride, p.dk_out_stride, p.k_out_stride, p.k_gamma, p.H_k, 0, 0};
+  a.side[0] = {p.q, p.dq_out, p.q_out, p.q_stride, p.dq_out_stride, p.q_out_stride, p.q_gamma, p.H_q};
+  a.side[1] = {p.k, p.dk_out, p.k_out, p.k_stride, p.dk_out_stride, p.k_out_stride, p.k_gamma, p.H_k};
   a.T = p.T;
   a.d = p.d;
   a.rot = p.rot_dim;
@@ -485,35 +590,22 @@ cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* w
   a.status = status;
   const bool norm = p.q_gamma || p.k_gamma;
   a.partial = bwd && norm ? workspace : nullptr;
-  const int groups = kThreads / group_lanes(p.d), sms = sm_count();
-  size_t smem = bwd ? (size_t)kWarps * p.d * sizeof(float) : 0;
-  for (Side& sd : a.side) {
-    if (sd.H == 0 || p.T == 0) continue;
-    // Groups per token: few, so that a group walks three heads or more with
-    // one token's angles, unless the CTAs would then not fill the SMs twice.
-    int lg = 0;
-    while ((2 << lg) <= groups && (2 << lg) * 3 <= sd.H) ++lg;
-    while ((2 << lg) <= groups && (1 << lg) < sd.H && p.T < (int64_t)2 * sms * (groups >> lg)) ++lg;
-    const int tb = groups >> lg;
-    const int64_t tiles = (p.T + tb - 1) / tb;
-    sd.hg_log2 = lg;
-    // The backward's CTAs stay (their sums of dgamma are what is added up at
-    // the end): four per SM between the sides, by their heads.
-    sd.ctas = (int)(bwd ? max64(1, min64(tiles, (int64_t)sms * 4 * sd.H / (p.H_q + p.H_k))) : tiles);
-    const size_t need = (size_t)table_offset(tb) + (size_t)tb * (p.rot_dim / 4) * 16;
-    if (smem < need) smem = need;
-  }
-  const int grid = a.side[0].ctas + a.side[1].ctas;
+  const int tok = 32 / group_lanes(p.d);
+  const int64_t groups = (p.T + tok - 1) / tok, steps = groups * (p.H_q + p.H_k);
+  a.side_steps = groups * p.H_q;
+  const int grid = (int)min64((steps + kWarps - 1) / kWarps, min64((int64_t)2 * sm_count(), kRopeMaxCtas));
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
+    a.per_warp = steps / ((int64_t)grid * kWarps);
+    a.extra = steps % ((int64_t)grid * kWarps);
     if (dt == NT_BF16)
-      e = p.interleaved ? run_lp<bf16, true>(a, bwd, grid, smem, s) : run_lp<bf16, false>(a, bwd, grid, smem, s);
+      e = p.interleaved ? run_lp<bf16, true>(a, bwd, grid, s) : run_lp<bf16, false>(a, bwd, grid, s);
     else
-      e = p.interleaved ? run_lp<float, true>(a, bwd, grid, smem, s) : run_lp<float, false>(a, bwd, grid, smem, s);
+      e = p.interleaved ? run_lp<float, true>(a, bwd, grid, s) : run_lp<float, false>(a, bwd, grid, s);
   }
   if (e != cudaSuccess || !bwd || !norm) return e;
-  return launch_pdl(rope_dgamma_kernel, dim3((p.d + 31) / 32, 2), dim3(1024), 0, s, (const float*)workspace,
-                    a.side[0].ctas, a.side[1].ctas, p.d, p.dq_gamma, p.dk_gamma);
+  return launch_pdl(rope_dgamma_kernel, dim3((p.d + 31) / 32, 2), dim3(1024), 0, s, (const float*)workspace, grid, p.d,
+                    p.dq_gamma, p.dk_gamma);
 }
 
 }  // namespace nt
