@@ -16,16 +16,19 @@
 // Both directions are bound by HBM, and at about ten operations an element
 // not by much, so the layout keeps loads in flight without holding registers
 // or waiting at barriers.  A row (one head of one token) is a group of LP
-// lanes, a lane two 8-element chunks: both halves of its eight pairs in
-// either layout.  A warp takes 32 / LP tokens at a time and walks their
-// heads, one row per group and step; the steps of the whole call are one line
-// that the warps share out evenly.  Each thread copies its own chunks of the
-// rows kSlots steps ahead into its own words of shared memory (cp.async), so
-// nothing but its own copies is ever waited for, and 128 KB per SM are in
-// flight.  A warp forms its tokens' cosines and sines itself when it comes to
-// new tokens (a tenth of the work of their heads), and keeps them, in the
-// forward multiplied by gamma, in registers.  Everything between the load and
-// the one rounding of the store is fp32, in packed pairs.
+// lanes, a lane one eighth or less of it: 16 elements in 16-byte words spread
+// over the row so that the words of neighbouring lanes are neighbours, and so
+// that a lane holds both columns of its eight pairs in either layout.  A warp
+// takes units of 32 / LP tokens and some consecutive heads of q or of k, one
+// row per group and step.  Units are dealt out in order, a round at a time:
+// all warps work in one region of memory (giving each warp a range of its own
+// costs a tenth of the bandwidth), and the unit's heads are chosen so that
+// the rounds come out even.  Each thread copies its own words of the rows
+// kSlots steps ahead into its own words of shared memory (cp.async), so
+// nothing but its own copies is ever waited for.  A warp forms its tokens'
+// cosines and sines itself and keeps them, in the forward multiplied by
+// gamma, in registers.  Everything between the load and the one rounding of
+// the store is fp32, in packed pairs.
 #include "tc_ptx.cuh"
 
 namespace nt {
@@ -50,8 +53,8 @@ struct Side {
 struct Args {
   Side side[2];
   int64_t T;
-  int64_t per_warp, extra;   // steps of a warp, and how many warps take one more
-  int64_t side_steps;        // backward: steps of the first side
+  uint32_t units[2];         // of each side: token groups x parts of its heads
+  int parts[2], unit_heads;  // parts of a side's heads, heads of a part
   int d, rot, B;
   float inv_d, eps, scale;
   const int32_t* cu;
@@ -100,24 +103,23 @@ __device__ __forceinline__ bool lane_position(const Args& a, int64_t t, int64_t 
   return true;
 }
 
-// A lane's columns.
-template <int LP, bool kInter>
+// A lane's columns: element e of 16 is column col(e / V) + e % V, V the
+// elements of a 16-byte word.  The lanes of the rotated part come first.
+template <typename T, int LP, bool kInter>
 struct Lane {
-  int i, g, ca, cb;
+  static constexpr int V = 16 / sizeof(T), W = 16 / V;
+  int i, g, col0, step;
   bool on, rotated;
   __device__ __forceinline__ Lane(const Args& a) {
     i = threadIdx.x % LP;
     g = threadIdx.x % 32 / LP;
     on = 16 * i < a.d;
     rotated = 16 * i < a.rot;
-    if (!kInter && rotated) {
-      ca = 8 * i;
-      cb = (a.rot >> 1) + 8 * i;
-    } else {
-      ca = 16 * i;
-      cb = 16 * i + 8;
-    }
+    const int first = rotated ? 0 : a.rot, width = rotated ? a.rot : a.d - a.rot;
+    col0 = first + V * (i - first / 16);
+    step = width / W;
   }
+  __device__ __forceinline__ int col(int w) const { return col0 + w * step; }
   // cosines and sines of the lane's eight pairs at pos (1 and 0 where nothing turns)
   __device__ __forceinline__ void angles(const Args& a, int64_t pos, float (&c)[8], float (&s)[8]) const {
 #pragma unroll
@@ -128,8 +130,15 @@ struct Lane {
     if (!rotated) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint64_t frac = (uint64_t)pos * a.turns[8 * i + e];
-      sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31: half turns
+      // the pair's first column: element e (half), element 2 e (interleaved)
+      const int j = kInter ? (col(2 * e / V) + 2 * e % V) / 2 : col(e / V) + e % V;
+      const float frac = (float)(int32_t)(((uint64_t)pos * a.turns[j]) >> 32);     // in 2^-32 turns, [-1/2, 1/2)
+      // For bf16 the hardware's sine and cosine do: within [-pi, pi] they are
+      // off by 2^-21 at most, an eighth of a percent of the half step (2^-9)
+      // that the output is rounded by, and cost an eighth of the exact ones,
+      // which fp32 takes.
+      if constexpr (sizeof(T) == 2) __sincosf(frac * 1.4629180792671596e-9f, &s[e], &c[e]);    // 2 pi 2^-32
+      else sincospif(frac * 4.656612873077393e-10f, &s[e], &c[e]);                            // 2^-31: half turns
       c[e] *= a.scale;
       s[e] *= a.scale;
     }
@@ -138,8 +147,35 @@ struct Lane {
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = 1.f;
     if (!p || !on) return;
-    load8(p + ca, v);
-    load8(p + cb, v + 8);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + col(e / V) + e % V);
+      v[e] = x.x;
+      v[e + 1] = x.y;
+      v[e + 2] = x.z;
+      v[e + 3] = x.w;
+    }
+  }
+  // copy the lane's words of a row into its ring words, 16 bytes each
+  __device__ __forceinline__ void copy(uint32_t dst, const T* x) const {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
+                   ::"r"(dst + w * kThreads * 16), "l"(x + col(w)) : "memory");
+  }
+  __device__ __forceinline__ void store(T* y, const float (&v)[16]) const {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint4 x;
+      if constexpr (sizeof(T) == 2) {
+        x = make_uint4(tc::pack_bf16x2(v[8 * w], v[8 * w + 1]), tc::pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
+                       tc::pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), tc::pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+      } else {
+        x = make_uint4(__float_as_uint(v[4 * w]), __float_as_uint(v[4 * w + 1]), __float_as_uint(v[4 * w + 2]),
+                       __float_as_uint(v[4 * w + 3]));
+      }
+      *reinterpret_cast<uint4*>(y + col(w)) = x;
+    }
   }
 };
 
@@ -153,22 +189,10 @@ __device__ __forceinline__ float group_sum(float v) {
 // The thread's own words of the ring: 16-byte word w of slot s at
 // (s * words + w) * kThreads + thread, so that a warp's accesses are
 // consecutive.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <typename T>
-__device__ __forceinline__ void copy_row(uint32_t dst, const T* x, int ca, int cb) {
-  constexpr int kHalf = 8 * sizeof(T) / 16;          // 16-byte words of a chunk
-#pragma unroll
-  for (int w = 0; w < kHalf; ++w) {
-    copy16(dst + w * kThreads * 16, x + ca + w * (16 / sizeof(T)));
-    copy16(dst + (kHalf + w) * kThreads * 16, x + cb + w * (16 / sizeof(T)));
-  }
-}
 template <typename T>
 __device__ __forceinline__ void read_row(const uint4* src, float (&v)[16]) {
   if constexpr (sizeof(T) == 2) {
@@ -244,16 +268,39 @@ __device__ __forceinline__ void pass(const float (&v)[16], const float (&m)[32],
   }
 }
 
-// A warp's steps [lo, hi) of the line.
-__device__ __forceinline__ void warp_steps(const Args& a, int64_t& lo, int64_t& hi) {
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  lo = w * a.per_warp + min64(w, a.extra);
-  hi = lo + a.per_warp + (w < a.extra ? 1 : 0);
-}
+// The warp's place among its units: warp w of n takes units w, w + n, ... of
+// the line (q's units, then k's).
+struct Place {
+  uint32_t u, n;         // unit, warps
+  int sd, h, h_end;      // side; head, end of the unit's heads
+  uint32_t tg;           // token group
+  bool more;
+  __device__ __forceinline__ Place(const Args& a) {
+    n = gridDim.x * kWarps;
+    u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    set(a);
+  }
+  __device__ __forceinline__ void set(const Args& a) {
+    more = u < a.units[0] + a.units[1];
+    if (!more) return;
+    sd = u >= a.units[0];
+    const uint32_t v = u - (sd ? a.units[0] : 0);
+    tg = v / (uint32_t)a.parts[sd];
+    h = (int)(v - tg * a.parts[sd]) * a.unit_heads;
+    h_end = min(h + a.unit_heads, a.side[sd].H);
+  }
+  // the next row; true if it is a new unit's (or there is none)
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (++h < h_end) return false;
+    u += n;
+    set(a);
+    return true;
+  }
+};
 
 template <typename T> struct Ring {          // forward: one row a step
   static constexpr int kWords = sizeof(T);   // 16-byte words of a row per lane
-  static constexpr int kSlots = 16 / sizeof(T);
+  static constexpr int kSlots = 8 / sizeof(T);
   static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
 };
 
@@ -262,49 +309,35 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
   using R = Ring<T>;
   extern __shared__ __align__(16) uint4 ring[];
   constexpr int kTok = 32 / LP;
-  const Lane<LP, kInter> me(a);
-  int64_t lo, hi;
-  warp_steps(a, lo, hi);
-  if (lo >= hi) return;
-  const int heads = a.side[0].H + a.side[1].H;
-  int64_t tg = lo / heads;                   // the warp's tokens: tg * kTok, ...
-  int h = (int)(lo - tg * heads);
+  const Lane<T, LP, kInter> me(a);
+  Place at(a), ahead(a);                     // the row in hand, and the row to copy, kSlots further
   pdl_wait();
-  // the copies' place runs kSlots steps ahead
-  int64_t pt = tg * kTok + me.g;
-  int ph = h;
-  auto copy = [&](int64_t step, int slot) {
-    if (step < hi) {
-      if (me.on && pt < a.T) {
-        const bool k = ph >= a.side[0].H;
-        const Side& p = a.side[k];
-        copy_row(tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x),
-                 static_cast<const T*>(p.x) + pt * p.xs + (int64_t)(ph - (k ? a.side[0].H : 0)) * a.d, me.ca, me.cb);
+  auto copy = [&](int slot) {
+    if (ahead.more) {
+      const int64_t t = (int64_t)ahead.tg * kTok + me.g;
+      if (me.on && t < a.T) {
+        const Side& p = a.side[ahead.sd];
+        me.copy(tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x),
+                static_cast<const T*>(p.x) + t * p.xs + (int64_t)ahead.h * a.d);
       }
-      if (++ph == heads) {
-        ph = 0;
-        pt += kTok;
-      }
+      ahead.next(a);
     }
     copy_commit();
   };
 #pragma unroll
-  for (int s = 0; s < R::kSlots; ++s) copy(lo + s, s);
-  float c[8], sn[8], m[32];
+  for (int s = 0; s < R::kSlots; ++s) copy(s);
+  float m[32];
   bool fresh = true, write = false;
   int slot = 0;
-  for (int64_t step = lo; step < hi; ++step) {
-    const int64_t t = tg * kTok + me.g;
-    if (fresh || h == 0) {                   // new tokens
+  while (at.more) {
+    const Side& p = a.side[at.sd];
+    const int64_t first = (int64_t)at.tg * kTok, t = first + me.g;
+    const bool here = me.on && t < a.T;
+    if (fresh) {
       int64_t pos;
-      write = lane_position(a, min64(t, a.T - 1), tg * kTok, (int)min64(kTok, a.T - tg * kTok), pos) && me.on &&
-              t < a.T;
+      write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && here;
+      float c[8], sn[8], gm[16];
       me.angles(a, pos, c, sn);
-    }
-    const int sd = h >= a.side[0].H;
-    const Side& p = a.side[sd];
-    if (fresh || h == 0 || h == a.side[0].H) {
-      float gm[16];
       me.gamma(p.gamma, gm);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -322,11 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
           m[b + 6] = gb * c[e];
         }
       }
-      fresh = false;
     }
     copy_wait<R::kSlots - 1>();
     float v[16], w[16];
-    if (me.on && t < a.T) {
+    if (here) {
       read_row<T>(ring + slot * R::kWords * kThreads + threadIdx.x, v);
     } else {
 #pragma unroll
@@ -339,44 +371,53 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
 #pragma unroll
       for (int e = 0; e < 16; e += 2) fmul2(w[e], w[e + 1], r, r, w[e], w[e + 1]);
     }
-    copy(step + R::kSlots, slot);
+    copy(slot);
     slot = slot + 1 == R::kSlots ? 0 : slot + 1;
-    if (write) {
-      T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)(h - (sd ? a.side[0].H : 0)) * a.d;
-      store8(y + me.ca, w);
-      store8(y + me.cb, w + 8);
-    }
-    if (++h == heads) {
-      h = 0;
-      ++tg;
-    }
+    if (write) me.store(static_cast<T*>(p.out) + t * p.os + (int64_t)at.h * a.d, w);
+    fresh = at.next(a);
   }
 }
 
 template <typename T> struct RingBwd {       // backward: the upstream row and the input's
   static constexpr int kWords = 2 * sizeof(T);
-  static constexpr int kSlots = sizeof(T) == 2 ? 4 : 3;
+  static constexpr int kSlots = sizeof(T) == 2 ? 3 : 2;
   static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
 };
 
-// The backward's line is all steps of q, then all of k: a warp sums dgamma of
-// one side in registers and puts it away when it comes to the other.
+// A warp comes to k's units after its last of q: it sums dgamma of one side
+// in registers and puts it away when it comes to the other.
 template <typename T, int LP, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
   using R = RingBwd<T>;
   extern __shared__ __align__(16) uint4 ring[];
   constexpr int kTok = 32 / LP;
   float* red = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(ring) + R::kBytes);   // [kWarps][2][d]
-  const Lane<LP, kInter> me(a);
+  const Lane<T, LP, kInter> me(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Place at(a), ahead(a);
   pdl_wait();
   pdl_trigger();
+  auto copy = [&](int slot) {
+    if (ahead.more) {
+      const int64_t t = (int64_t)ahead.tg * kTok + me.g;
+      if (me.on && t < a.T) {
+        const Side& p = a.side[ahead.sd];
+        const uint32_t dst = tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x);
+        me.copy(dst, static_cast<const T*>(p.up) + t * p.us + (int64_t)ahead.h * a.d);
+        if (p.gamma)
+          me.copy(dst + R::kWords / 2 * kThreads * 16,
+                  static_cast<const T*>(p.x) + t * p.xs + (int64_t)ahead.h * a.d);
+      }
+      ahead.next(a);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < R::kSlots; ++s) copy(s);
   if (a.partial) {
     for (int e = lane; e < 2 * a.d; e += 32) red[warp * 2 * a.d + e] = 0.f;
     __syncwarp();
   }
-  int64_t lo, hi;
-  warp_steps(a, lo, hi);
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -386,60 +427,31 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
       float v = acc[e];
 #pragma unroll
       for (int x = 16; x >= LP; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-      if (lane < LP && me.on) red[(warp * 2 + sd) * a.d + (e < 8 ? me.ca + e : me.cb + e - 8)] = v;
+      if (lane < LP && me.on) red[(warp * 2 + sd) * a.d + me.col(e / me.V) + e % me.V] = v;
       acc[e] = 0.f;
     }
   };
-  int sd = lo >= a.side_steps;
-  int64_t at = lo - (sd ? a.side_steps : 0);
-  int H = a.side[sd].H;
-  int64_t tg = lo < hi ? at / H : 0;
-  int h = lo < hi ? (int)(at - tg * H) : 0;
-  int psd = sd, ph = h, pH = H;
-  int64_t pt = tg * kTok + me.g;
-  const int64_t tgs = (a.T + kTok - 1) / kTok;
-  auto copy = [&](int64_t step, int slot) {
-    if (step < hi) {
-      if (me.on && pt < a.T) {
-        const Side& p = a.side[psd];
-        const uint32_t dst = tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x);
-        copy_row(dst, static_cast<const T*>(p.up) + pt * p.us + (int64_t)ph * a.d, me.ca, me.cb);
-        if (p.gamma)
-          copy_row(dst + R::kWords / 2 * kThreads * 16, static_cast<const T*>(p.x) + pt * p.xs + (int64_t)ph * a.d,
-                   me.ca, me.cb);
-      }
-      if (++ph == pH) {
-        ph = 0;
-        pt += kTok;
-        if (pt - me.g >= tgs * kTok) {       // the first side is done
-          psd = 1;
-          pH = a.side[1].H;
-          pt = me.g;
-        }
-      }
-    }
-    copy_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < R::kSlots; ++s) copy(lo + s, s);
   float c[8], sn[8], gm[16];
+  int sd = -1;                               // the side acc and gm are of
   bool fresh = true, write = false;
   int slot = 0;
-  for (int64_t step = lo; step < hi; ++step) {
-    const int64_t t = tg * kTok + me.g;
-    const Side& p = a.side[sd];
-    if (fresh || h == 0) {
+  while (at.more) {
+    const Side& p = a.side[at.sd];
+    const int64_t first = (int64_t)at.tg * kTok, t = first + me.g;
+    const bool here = me.on && t < a.T;
+    if (fresh) {
       int64_t pos;
-      write = lane_position(a, min64(t, a.T - 1), tg * kTok, (int)min64(kTok, a.T - tg * kTok), pos) && me.on &&
-              t < a.T;
+      write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && here;
       me.angles(a, pos, c, sn);
-      if (fresh || tg == 0) me.gamma(p.gamma, gm);
-      fresh = false;
+      if (sd != at.sd) {
+        if (sd >= 0 && a.partial) put_away(sd);
+        sd = at.sd;
+        me.gamma(p.gamma, gm);
+      }
     }
     copy_wait<R::kSlots - 1>();
     const uint4* row = ring + slot * R::kWords * kThreads + threadIdx.x;
     float v[16], g[16];
-    const bool here = me.on && t < a.T;
     if (here) {
       read_row<T>(row, v);
     } else {
@@ -489,25 +501,13 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
         fmul2(g[e], g[e + 1], r, r, g[e], g[e + 1]);
       }
     }
-    copy(step + R::kSlots, slot);
+    copy(slot);
     slot = slot + 1 == R::kSlots ? 0 : slot + 1;
-    if (write) {
-      T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)h * a.d;
-      store8(y + me.ca, g);
-      store8(y + me.cb, g + 8);
-    }
-    if (++h == H) {
-      h = 0;
-      if (++tg == tgs && step + 1 < hi) {            // the first side is done
-        if (a.partial) put_away(0);
-        sd = 1;
-        H = a.side[1].H;
-        tg = 0;
-      }
-    }
+    if (write) me.store(static_cast<T*>(p.out) + t * p.os + (int64_t)at.h * a.d, g);
+    fresh = at.next(a);
   }
   if (!a.partial) return;
-  if (lo < hi) put_away(sd);
+  if (sd >= 0) put_away(sd);
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * a.d; e += kThreads) {
     float v = 0.f;
@@ -591,13 +591,30 @@ cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* w
   const bool norm = p.q_gamma || p.k_gamma;
   a.partial = bwd && norm ? workspace : nullptr;
   const int tok = 32 / group_lanes(p.d);
-  const int64_t groups = (p.T + tok - 1) / tok, steps = groups * (p.H_q + p.H_k);
-  a.side_steps = groups * p.H_q;
-  const int grid = (int)min64((steps + kWarps - 1) / kWarps, min64((int64_t)2 * sm_count(), kRopeMaxCtas));
+  const int64_t groups = (p.T + tok - 1) / tok, warps = min64((int64_t)2 * sm_count(), kRopeMaxCtas) * kWarps;
+  // The heads of a unit: the number that gives the fewest steps, the rounds
+  // of units times a unit's heads and about three steps' worth of work for its
+  // tokens' angles.  (Unit counts stay below 2^31: a unit is 512 elements of
+  // q or k at least, and 2^31 of those are 2 TB.)
+  const int most = max(p.H_q, p.H_k);
+  int64_t best = 0;
+  for (int hu = 1; hu <= most; hu = hu == 64 ? max(most, 65) : hu + 1) {
+    const int64_t units = groups * ((p.H_q + hu - 1) / hu + (p.H_k + hu - 1) / hu);
+    const int64_t cost = (units + warps - 1) / warps * (hu + 3);
+    if (units > 0x7fffffffLL || (best && cost >= best)) continue;
+    best = cost;
+    a.unit_heads = hu;
+  }
+  int64_t total = 0;
+  for (int sd = 0; sd < 2 && best; ++sd) {
+    a.parts[sd] = max(1, (a.side[sd].H + a.unit_heads - 1) / a.unit_heads);
+    a.units[sd] = a.side[sd].H ? (uint32_t)(groups * a.parts[sd]) : 0;
+    total += a.units[sd];
+  }
+  if (total == 0 && p.T > 0 && most > 0) return cudaErrorInvalidValue;
+  const int grid = (int)min64((total + kWarps - 1) / kWarps, warps / kWarps);
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
-    a.per_warp = steps / ((int64_t)grid * kWarps);
-    a.extra = steps % ((int64_t)grid * kWarps);
     if (dt == NT_BF16)
       e = p.interleaved ? run_lp<bf16, true>(a, bwd, grid, s) : run_lp<bf16, false>(a, bwd, grid, s);
     else
