@@ -9,10 +9,9 @@
 //
 // Two producer warps walk the CTA's share of the batch (paged_plan.cuh), 64
 // keys at a time, tiles alternating: one box of R = gcd(page_size, 64) keys
-// per lane, its page looked up a tile ahead, into a ring of stages in the
-// 128-byte swizzle.  (One warp takes about 1,100 cycles for a tile and 85
-// more for each box after the fourth: more than HBM takes for 64 keys of
-// d = 64.)  A third warp copies the items' query rows.  Eight
+// per lane into a ring of stages in the 128-byte swizzle.  (A copy takes its
+// warp about 85 cycles to issue, so one warp alone could not keep up with HBM
+// for 64 keys of d = 64 in pages of 16: eight boxes in 700 cycles.)  A third warp copies the items' query rows.  Eight
 // consumer warps take 16 keys each, four to a stage, stages alternating
 // between the two fours, every warp with its own running maximum, sum and
 // output.  A warp's part is
@@ -27,8 +26,10 @@
 // matrix loads of a 32 KB stage take about a tenth of the time HBM takes to
 // deliver it.
 //
-// At the end of a segment the eight warps merge through shared memory, and
-// either write the output or leave a partial result for the join.
+// At the end of a segment the eight warps leave their results in shared
+// memory for a fourth kind of warp, which merges them and writes the output
+// or a partial result for the join, while the eight go on: with short
+// sequences the merge is as long as the segment's tiles.
 #include "paged_plan.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,7 +42,7 @@ constexpr int kTile = 64;                   // keys per stage, and per unit of t
 constexpr int kConsumers = 8;               // warps
 constexpr int kProducers = 2;               // warps, tiles alternating
 constexpr int kQSlots = 4;                  // items whose query rows are in flight or in use
-constexpr int kThreads = (kConsumers + kProducers + 1) * 32;
+constexpr int kThreads = (kConsumers + kProducers + 2) * 32;
 
 template <int D, int NT>
 struct Cfg {
@@ -50,9 +51,13 @@ struct Cfg {
   static constexpr uint32_t kStage = 2 * kSide;
   static constexpr int kRedStride = D + 4;                    // floats: keeps the merge's writes conflict-free
   static constexpr uint32_t kRed = kConsumers * kHeads * kRedStride * 4;
+  static constexpr int kRedBufs = D * NT <= 128 ? 2 : 1;      // segments whose results wait for the merge
+  // The merge: one warp of its own, or, where it is four times the work, the
+  // eight together (G = 16, d = 128: 78 us for a batch that took 104 with one).
+  static constexpr int kMergeWarps = NT == 1 ? 1 : kConsumers;
   static constexpr uint32_t kQBytes = kHeads * D * 2;
-  static constexpr int kExtra = D == 64 ? 3 : 2;               // an item's cost beside its tiles, in tiles
-  static constexpr uint32_t kFixed = kRed + kQSlots * kQBytes + 2048 /* statistics, barriers, plan */;
+  static constexpr int kExtra = D == 64 || NT == 2 ? 3 : 2;   // an item's cost beside its tiles, in tiles
+  static constexpr uint32_t kFixed = kRedBufs * kRed + kQSlots * kQBytes + 4096 /* statistics, barriers, plan */;
   // An even number: a stage is then always the same four warps' and they see
   // every phase of its barriers.  (With an odd number a warp would wait on a
   // phase whose predecessor it never waited for, which parity cannot tell
@@ -63,12 +68,12 @@ struct Cfg {
 };
 
 struct Ctl {
-  uint64_t full[16], empty[16], q_full[kQSlots], q_empty[kQSlots];
-  float m[kConsumers][16], l[kConsumers][16];
+  uint64_t full[16], empty[16], q_full[kQSlots], q_empty[kQSlots], red_full[2], red_empty[2];
+  float m[2][kConsumers][16], l[2][kConsumers][16];
   PagedPlanShared plan;
   int abort;
 };
-static_assert(sizeof(Ctl) <= 2048, "control block");
+static_assert(sizeof(Ctl) <= 4096, "control block");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -101,6 +106,63 @@ struct TcArgs {
   unsigned int* status;
 };
 
+// The merge of a segment's eight warps, and its output or partial result: the
+// caller is thread `first` of `step`.
+template <int D, int NT>
+__device__ __forceinline__ void merge_segment(const TcArgs& a, const PagedWalk& w, const Ctl* ctl, const float* red,
+                                              int buf, int first, int step) {
+  using C = Cfg<D, NT>;
+  constexpr int kHeads = C::kHeads;
+  const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
+  const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
+  const int nh = min(kHeads, a.G - h0);
+  const bool whole = w.begins && w.ends;
+  const int64_t pslot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
+  const int64_t hq = (int64_t)kvh * a.G + h0;
+  const float(*sm)[16] = ctl->m[buf];
+  const float(*sl)[16] = ctl->l[buf];
+  // a lane's four columns of a head; two passes at a time, to overlap their reads
+#pragma unroll 2
+  for (int e = first; e < nh * (D / 4); e += step) {
+    const int h = e / (D / 4), c = e % (D / 4) * 4;
+    float f[kConsumers], mm = -INFINITY;
+    float4 v[kConsumers];
+#pragma unroll
+    for (int x = 0; x < kConsumers; ++x) {
+      f[x] = sm[x][h];
+      mm = fmaxf(mm, f[x]);
+      v[x] = sl[x][h] == -1.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : *reinterpret_cast<const float4*>(red + buf * (C::kRed / 4) +
+                                                                 (x * kHeads + h) * C::kRedStride + c);
+    }
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kConsumers; ++x) {
+  const float lx = sl[x][h];
+  const float fx = lx == -1.f ? 0.f : ex2_approx(f[x] - base);
+      ll += fx * lx;
+      oo.x += fx * v[x].x;
+      oo.y += fx * v[x].y;
+      oo.z += fx * v[x].z;
+      oo.w += fx * v[x].w;
+    }
+    if (whole) {
+  const float inv = 1.f / ll;
+  const uint2 out = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
+      *reinterpret_cast<uint2*>(a.o + ((int64_t)w.seg_b * a.H + hq + h) * D + c) = out;
+      if (a.lse && c == 0) a.lse[(hq + h) * a.B + w.seg_b] = (mm + log2f(ll)) * 0.6931471805599453f;
+    } else {
+      *reinterpret_cast<float4*>(part.o + (pslot * a.heads + h) * D + c) = oo;
+      if (c == 0) {
+        part.ml[(pslot * a.heads + h) * 2] = mm;
+        part.ml[(pslot * a.heads + h) * 2 + 1] = ll;
+      }
+    }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -111,7 +173,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* stages = smem;
   float* red = reinterpret_cast<float*>(smem + S * C::kStage);
-  uint8_t* qbuf = reinterpret_cast<uint8_t*>(red) + C::kRed;
+  uint8_t* qbuf = reinterpret_cast<uint8_t*>(red) + C::kRedBufs * C::kRed;
   Ctl* ctl = reinterpret_cast<Ctl*>(qbuf + kQSlots * C::kQBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t cap = min64((int64_t)a.max_pages * a.page_size, 0x7fffffff);
@@ -125,6 +187,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], kConsumers);
+    }
+    for (int i = 0; i < C::kRedBufs; ++i) {
+      mbar_init(&ctl->red_full[i], kConsumers);
+      mbar_init(&ctl->red_empty[i], C::kMergeWarps);
     }
     ctl->abort = 0;
     fence_mbar_init();
@@ -140,7 +206,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   PagedWalk w;
   w.init(&ctl->plan, a.lengths, cap, kTile, C::kExtra, a.whole);
 
-  if (warp >= kConsumers + kProducers) {
+  if (warp == kConsumers + kProducers) {
     // ---- query rows, item by item ------------------------------------------
     uint32_t segs = 0;
     while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
@@ -160,6 +226,30 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         mbar_wait(&ctl->q_full[i % kQSlots], (i / kQSlots) & 1, nullptr, a.status);
     return;
   }
+  if (warp == kConsumers + kProducers + 1) {
+    // ---- merge: the consumers' results of a segment ------------------------------
+    uint32_t segs = 0;
+    int64_t open_id = -1, open_parts = 0;             // the item left unfinished
+    while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      if (C::kMergeWarps == 1) {
+        const int buf = segs % C::kRedBufs;
+        if (!mbar_wait_warp(&ctl->red_full[buf], (segs / C::kRedBufs) & 1, &ctl->abort, a.status)) break;
+        merge_segment<D, NT>(a, w, ctl, red, buf, lane, 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
+        ++segs;
+      }
+      if (w.begins && !w.ends) {
+        open_id = (int64_t)w.seg_b * a.items + w.seg_item;
+        open_parts = w.parts(&ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
+      }
+    }
+    if (lane == 0) {
+      part.id[2 * blockIdx.x] = open_id;
+      part.id[2 * blockIdx.x + 1] = open_parts;
+    }
+    return;
+  }
   if (warp >= kConsumers) {
     // ---- producers: tiles warp - kConsumers, + kProducers, ... ----------------
     const uint32_t me = warp - kConsumers;
@@ -168,74 +258,75 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     const bool has_box = side < 2;
     const CUtensorMap* map = side ? &vmap : &kmap;
     const uint32_t dst = side * C::kSide + rb * a.box * (2 * D);
-    const uint32_t ps = a.page_size, step_pg = kProducers * kTile / ps, step_row = kProducers * kTile % ps;
-    // The walk runs one of the warp's tiles ahead of the copies, so that the
-    // page lookup's latency passes behind a tile's wait.
-    uint32_t seg_it = 0;                              // the segment's first tile in the CTA's order
-    int64_t t = 0;
-    uint32_t pg = 0, row = 0;                         // of this lane's box of tile t
     const int32_t* trow = nullptr;
-    bool more = true;
-    auto advance = [&](bool start) {
-      bool jump = start;
-      if (!start) {
-        t += kProducers;
-        pg += step_pg;
-        row += step_row;
-        if (row >= ps) {
+    uint32_t pages = 0;                               // of the sequence
+    const uint32_t ps = a.page_size, step_pg = kProducers * kTile / ps, step_row = kProducers * kTile % ps;
+    // The block table is read 32 entries at a time, a lane each, and one such
+    // window ahead, so that a lookup is a shuffle.  The window stays when the
+    // next segment starts on the same pages: the sequence's next head.
+    uint32_t win = 0;                                 // its first page index
+    int cur = -1, nxt = -1, wb = -1;                  // entries win + lane, win + 32 + lane; sequence
+    auto entry = [&](uint32_t i) { return i < pages ? trow[i] : -1; };
+    uint32_t seg_it = 0, last = 0;                    // the segment's first tile in the CTA's order
+    bool ok = true;
+    while (ok && w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      int64_t t = w.t0 + ((me - seg_it) & (kProducers - 1));
+      if (t < w.t1) {
+        const int kvh = w.seg_item / a.hgroups;
+        trow = a.table + (int64_t)w.seg_b * a.max_pages;
+        pages = ((uint32_t)w.seg_len + ps - 1) / ps;
+        const uint32_t key0 = (uint32_t)t * kTile, pg0 = key0 / ps;
+        uint32_t row = key0 - pg0 * ps + rb * a.box, pg = pg0;      // of this lane's box
+        while (row >= ps) {
           row -= ps;
           ++pg;
         }
-        jump = t >= w.t1;
-      }
-      while (jump) {
-        if (!start) seg_it += (uint32_t)(w.t1 - w.t0);
-        start = false;
-        if (!w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
-          more = false;
-          return;
+        uint32_t first = pg0, first_row = key0 - pg0 * ps;          // of the tile's first key
+        if (wb != w.seg_b || win != pg0) {
+          wb = w.seg_b;
+          win = pg0;
+          cur = entry(win + lane);
+          nxt = entry(win + 32 + lane);
         }
-        t = w.t0 + ((me - seg_it) & (kProducers - 1));
-        jump = t >= w.t1;
-        if (!jump) {
-          const uint32_t key = (uint32_t)t * kTile + rb * a.box;
-          pg = key / ps;
-          row = key - pg * ps;
-          trow = a.table + (int64_t)w.seg_b * a.max_pages;
+        for (; t < w.t1; t += kProducers) {
+          if (first - win >= 32) {
+            win += 32;
+            cur = nxt;
+            nxt = entry(win + 32 + lane);
+          }
+          const uint32_t at = pg - win;
+          const int id0 = __shfl_sync(0xffffffffu, cur, at & 31), id1 = __shfl_sync(0xffffffffu, nxt, at & 31);
+          const int page = at < 32 ? id0 : id1;
+          const bool now = has_box && t * kTile + rb * a.box < w.seg_len;
+          int z = page * a.Hkv + kvh;
+          if (now && (uint32_t)page >= (uint32_t)a.n_pages) {
+            flag_device(a.status, kDevCheck);
+            z = a.n_pages * a.Hkv;                    // outside the map: reads as zeros
+          }
+          const uint32_t it = seg_it + (uint32_t)(t - w.t0);
+          const int st = it % S;
+          ok = mbar_wait_warp(&ctl->empty[st], ((it / S) & 1) ^ 1, &ctl->abort, a.status);
+          if (!ok) break;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, now));
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * a.box * (2 * D));
+          __syncwarp();
+          if (now) tma_load_4d(stages + st * C::kStage + dst, map, &ctl->full[st], 0, (int)row, 0, z);
+          last = it + 1;
+          pg += step_pg;
+          row += step_row;
+          if (row >= ps) {
+            row -= ps;
+            ++pg;
+          }
+          first += step_pg;
+          first_row += step_row;
+          if (first_row >= ps) {
+            first_row -= ps;
+            ++first;
+          }
         }
       }
-    };
-    auto page_of = [&]() -> int {                     // this lane's page of tile t, -1 if it loads nothing
-      if (!more || !has_box || t * kTile + rb * a.box >= w.seg_len) return -1;
-      return trow[pg];
-    };
-    auto loads = [&]() { return more && has_box && t * kTile + rb * a.box < w.seg_len; };
-    advance(true);
-    bool mine = loads();
-    int id = page_of();
-    uint32_t last = 0;
-    bool ok = true;
-    while (more) {
-      const uint32_t it = seg_it + (uint32_t)(t - w.t0);
-      const int y = (int)row, kvh = w.seg_item / a.hgroups;
-      const bool now = mine;
-      const int page = id;
-      advance(false);
-      mine = loads();
-      id = page_of();
-      int z = page * a.Hkv + kvh;
-      if (now && (uint32_t)page >= (uint32_t)a.n_pages) {
-        flag_device(a.status, kDevCheck);
-        z = a.n_pages * a.Hkv;                        // outside the map: reads as zeros
-      }
-      const int st = it % S;
-      ok = mbar_wait_warp(&ctl->empty[st], ((it / S) & 1) ^ 1, &ctl->abort, a.status);
-      if (!ok) break;
-      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, now));
-      if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * a.box * (2 * D));
-      __syncwarp();
-      if (now) tma_load_4d(stages + st * C::kStage + dst, map, &ctl->full[st], 0, y, 0, z);
-      last = it + 1;
+      seg_it += (uint32_t)(w.t1 - w.t0);
     }
     if (!ok && lane == 0)                             // given up: the copies in flight land first
       for (uint32_t i = 0; i < (uint32_t)S && i < last; ++i)
@@ -262,13 +353,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   const uint32_t row_off = row_at(mrow);
   const uint32_t xr = ((((uint32_t)lane >> 3) & 1) ^ (mrow & 7)) << 4;
   uint32_t it = 0, segs = 0;
-  int64_t open_id = -1, open_parts = 0;      // the item left unfinished
-  bool ok = true;                // a warp that gave up still meets the others at the merges
-  while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
-    const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
-    const int nh = min(kHeads, a.G - h0);
+  bool ok = true;
+  while (ok && w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+    const int nh = min(kHeads, a.G - (w.seg_item % a.hgroups) * kHeads);
     const int slot = segs % kQSlots;
-    if (ok) ok = mbar_wait_warp(&ctl->q_full[slot], (segs / kQSlots) & 1, &ctl->abort, a.status);
+    ok = mbar_wait_warp(&ctl->q_full[slot], (segs / kQSlots) & 1, &ctl->abort, a.status);
+    if (!ok) break;
     uint32_t qa[D / 16][4];
     {
       const uint32_t* qrow = reinterpret_cast<const uint32_t*>(qbuf + slot * C::kQBytes);
@@ -297,9 +387,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     for (int64_t t = w.t0; t < w.t1; ++t, ++it) {
       if ((it & 1) != (uint32_t)grp) continue;
       const int st = it % S;
-      if (ok) ok = mbar_wait_warp(&ctl->full[st], (it / S) & 1, &ctl->abort, a.status);
+      ok = mbar_wait_warp(&ctl->full[st], (it / S) & 1, &ctl->abort, a.status);
+      if (!ok) break;
       const int left = (int)min64(w.seg_len - t * kTile - slice * 16, 16);     // keys of this slice
-      if (ok && left > 0) {
+      if (left > 0) {
         active = true;
         const uint32_t kbase = smem_u32(stages + st * C::kStage), vbase = kbase + C::kSide;
         if (left < 16) {
@@ -311,13 +402,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           }
           __syncwarp();
         }
-        float s[2][4] = {};
+        float s[2][4] = {}, s2[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t kb[4];
           ldsm4(kbase + (ks >> 2) * hs + row_off + ((((uint32_t)ks & 3) << 5) ^ xr), kb);
-          mma16816(s[0], qa[ks], kb[0], kb[1]);
-          mma16816(s[1], qa[ks], kb[2], kb[3]);
+          mma16816(ks & 1 ? s2[0] : s[0], qa[ks], kb[0], kb[1]);
+          mma16816(ks & 1 ? s2[1] : s[1], qa[ks], kb[2], kb[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[0][c] += s2[0][c];
+          s[1][c] += s2[1][c];
         }
         uint32_t pb[NT][2];
         float corr[NT];
@@ -373,14 +469,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[st]);
     }
-    // ---- merge the warps -------------------------------------------------------
+    if (!ok) break;
+    // ---- the warp's result, for the merge --------------------------------------
+    const int buf = (segs - 1) % C::kRedBufs;
+    ok = mbar_wait_warp(&ctl->red_empty[buf], (((segs - 1) / C::kRedBufs) & 1) ^ 1, &ctl->abort, a.status);
+    if (!ok) break;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
       l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
       if (tq == 0) {
-        ctl->m[warp][n * 8 + g] = m[n];
-        ctl->l[warp][n * 8 + g] = active ? l[n] : -1.f;      // -1: no keys, nothing to add
+        ctl->m[buf][warp][n * 8 + g] = m[n];
+        ctl->l[buf][warp][n * 8 + g] = active ? l[n] : -1.f;      // -1: no keys, nothing to add
       }
     }
     if (active) {
@@ -390,7 +490,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         for (int c = 0; c < 2; ++c) {
           const int h = n * 8 + 2 * tq + c;
           if (h >= nh) continue;
-          float* r = red + (warp * kHeads + h) * C::kRedStride + g;
+          float* r = red + buf * (C::kRed / 4) + (warp * kHeads + h) * C::kRedStride + g;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             r[i * 16] = o[n][i][c];
@@ -398,52 +498,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           }
         }
     }
-    named_bar_sync(1, kConsumers * 32);
-    const bool whole = w.begins && w.ends;
-    const int64_t pslot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
-    const int64_t hq = (int64_t)kvh * a.G + h0;
-    for (int e = threadIdx.x; e < nh * (D / 4); e += kConsumers * 32) {
-      const int h = e / (D / 4), c = e % (D / 4) * 4;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kConsumers; ++x) mm = fmaxf(mm, ctl->m[x][h]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int x = 0; x < kConsumers; ++x) {
-        const float lx = ctl->l[x][h];
-        if (lx == -1.f) continue;
-        const float f = ex2_approx(ctl->m[x][h] - base);
-        const float4 v = *reinterpret_cast<const float4*>(red + (x * kHeads + h) * C::kRedStride + c);
-        ll += f * lx;
-        oo.x += f * v.x;
-        oo.y += f * v.y;
-        oo.z += f * v.z;
-        oo.w += f * v.w;
-      }
-      if (whole) {
-        const float inv = 1.f / ll;
-        uint2 out = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
-        *reinterpret_cast<uint2*>(a.o + ((int64_t)w.seg_b * a.H + hq + h) * D + c) = out;
-        if (a.lse && c == 0) a.lse[(hq + h) * a.B + w.seg_b] = (mm + log2f(ll)) * 0.6931471805599453f;
-      } else {
-        *reinterpret_cast<float4*>(part.o + (pslot * a.heads + h) * D + c) = oo;
-        if (c == 0) {
-          part.ml[(pslot * a.heads + h) * 2] = mm;
-          part.ml[(pslot * a.heads + h) * 2 + 1] = ll;
-        }
-      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->red_full[buf]);
+    if (C::kMergeWarps > 1) {
+      ok = mbar_wait_warp(&ctl->red_full[buf], ((segs - 1) / C::kRedBufs) & 1, &ctl->abort, a.status);
+      if (!ok) break;
+      merge_segment<D, NT>(a, w, ctl, red, buf, threadIdx.x, kConsumers * 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
     }
-    if (w.begins && !w.ends) {
-      open_id = (int64_t)w.seg_b * a.items + w.seg_item;
-      open_parts = w.parts(&ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
-    }
-    named_bar_sync(1, kConsumers * 32);
-  }
-  if (threadIdx.x == 0) {
-    part.id[2 * blockIdx.x] = open_id;
-    part.id[2 * blockIdx.x + 1] = open_parts;
   }
 }
 
