@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
                                                               unsigned int* status) {
   constexpr int N = D / 32;          // elements of a row per lane
   constexpr int KB = 32 / GP;        // keys of a batch
-  __shared__ PagedPlanShared plan;
+  __shared__ PagedPlan plan;
   __shared__ float red_o[kWarps][GP][D];
   __shared__ float red_m[kWarps][GP], red_l[kWarps][GP];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
       for (int h = threadIdx.x; h < p.H; h += kThreads) p.lse[(int64_t)h * p.B + b] = -INFINITY;
   }
   PagedWalk w;
-  w.init(&plan, p.lengths, cap, kTile, kExtra, whole_items);
+  w.init(plan, p.lengths, p.B, cap, kTile, kExtra, whole_items);
   const int ps = p.pool.page_size;
   const int my_key = lane / GP;
   int64_t open_id = -1, open_parts = 0;      // the item left unfinished
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnPro
     }
     if (w.begins && !w.ends) {
       open_id = (int64_t)w.seg_b * items + w.seg_item;
-      open_parts = w.parts(&plan, kExtra, blockIdx.x, gridDim.x);
+      open_parts = w.parts(plan, kExtra, blockIdx.x, gridDim.x);
     }
     __syncthreads();
   }
@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnProblem 
   constexpr int kLanes = D / 4, kRows = 256 / kLanes;
   __shared__ float4 red[kRows][kLanes];
   __shared__ float red_m[kRows], red_l[kRows];
+  pdl_trigger();                                  // the next call may set itself up; it waits for this one's end
   pdl_wait();
   const int stride = min(heads, G);
   const PagedPartials part = paged_partials(p.workspace, ctas, stride);

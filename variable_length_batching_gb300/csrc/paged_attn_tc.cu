@@ -70,7 +70,7 @@ struct Cfg {
 struct Ctl {
   uint64_t full[16], empty[16], q_full[kQSlots], q_empty[kQSlots], red_full[2], red_empty[2];
   float m[2][kConsumers][16], l[2][kConsumers][16];
-  PagedPlanShared plan;
+  PagedPlan plan;
   int abort;
 };
 static_assert(sizeof(Ctl) <= 4096, "control block");
@@ -179,32 +179,28 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   const int64_t cap = min64((int64_t)a.max_pages * a.page_size, 0x7fffffff);
   const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 4);
-    }
-    for (int i = 0; i < kQSlots; ++i) {
-      mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], kConsumers);
-    }
-    for (int i = 0; i < C::kRedBufs; ++i) {
-      mbar_init(&ctl->red_full[i], kConsumers);
-      mbar_init(&ctl->red_empty[i], C::kMergeWarps);
-    }
-    ctl->abort = 0;
-    fence_mbar_init();
-    prefetch_tmap(&kmap);
-    prefetch_tmap(&vmap);
+  // a lane to each barrier
+  if (threadIdx.x < S) {
+    mbar_init(&ctl->full[threadIdx.x], 1);
+    mbar_init(&ctl->empty[threadIdx.x], 4);
   }
+  if (threadIdx.x < kQSlots) {
+    mbar_init(&ctl->q_full[threadIdx.x], 1);
+    mbar_init(&ctl->q_empty[threadIdx.x], kConsumers);
+  }
+  if (threadIdx.x < C::kRedBufs) {
+    mbar_init(&ctl->red_full[threadIdx.x], kConsumers);
+    mbar_init(&ctl->red_empty[threadIdx.x], C::kMergeWarps);
+  }
+  if (threadIdx.x == 0) ctl->abort = 0;
+  if (threadIdx.x < 32) fence_mbar_init();
+  if (threadIdx.x == 32) prefetch_tmap(&kmap);
+  if (threadIdx.x == 64) prefetch_tmap(&vmap);
   pdl_wait();
   pdl_trigger();
-  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status,
-             kThreads);
-  __syncthreads();
-
+  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status, kThreads);
   PagedWalk w;
-  w.init(&ctl->plan, a.lengths, cap, kTile, C::kExtra, a.whole);
+  w.init(ctl->plan, a.lengths, a.B, cap, kTile, C::kExtra, a.whole);
 
   if (warp == kConsumers + kProducers) {
     // ---- query rows, item by item ------------------------------------------
@@ -241,7 +237,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
       }
       if (w.begins && !w.ends) {
         open_id = (int64_t)w.seg_b * a.items + w.seg_item;
-        open_parts = w.parts(&ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
+        open_parts = w.parts(ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
       }
     }
     if (lane == 0) {

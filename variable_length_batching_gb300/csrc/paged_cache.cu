@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kThreads) paged_write_kernel(const WriteArgs a
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int n = (int)min64(a.tokens, a.T - t0);
   pdl_wait();
+  pdl_trigger();
   if (n <= kThreads / 32) {
     if (warp < n) {
       const int b = segment_of_warp(a.cu, a.B, t0 + warp);
@@ -102,6 +103,8 @@ constexpr int kCopyBytes = 16384;      // bytes of a page a CTA moves
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) paged_copy_kernel(const __grid_constant__ CopyArgs<N> a) {
+  pdl_wait();
+  pdl_trigger();
   const int i = blockIdx.y;
   uint8_t* pool = a.pool[blockIdx.z];
   const int64_t lo = (int64_t)blockIdx.x * kCopyBytes, hi = min64(lo + kCopyBytes, a.page_bytes);
@@ -123,8 +126,7 @@ cudaError_t copy_pages(const PagedPool& p, const int32_t* src, const int32_t* ds
     a.dst[i] = dst[i];
   }
   const dim3 grid((unsigned)((a.page_bytes + kCopyBytes - 1) / kCopyBytes), n, 2);
-  paged_copy_kernel<N><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(paged_copy_kernel<N>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

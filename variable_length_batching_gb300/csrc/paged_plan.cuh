@@ -20,10 +20,10 @@ namespace nt {
 // An item costs more than its tiles (query rows, merge, output): it counts as
 // `extra` tiles more, in front of its first.  A CTA whose share ends among
 // those takes nothing of the item.
-struct PagedPlanShared {
+struct PagedPlan {
   int64_t warp_sum[32];
   int64_t total, lo, hi;   // units of the call, this CTA's range
-  int64_t start;           // first unit of sequence b0
+  int64_t start;           // first unit of sequence b0, which holds lo
   int b0;
 };
 
@@ -41,17 +41,22 @@ __device__ __forceinline__ int64_t paged_tiles(int len, int tile) { return (len 
 __device__ __forceinline__ int64_t paged_units(int len, int tile, int items, int extra) {
   return len > 0 ? (paged_tiles(len, tile) + extra) * items : 0;
 }
+// floor(a / b), in 32 bits where that does (a 64-bit division takes a hundred
+// cycles, and every CTA waits for three of them before its first load)
+__device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // CTAs that share the units, and the first unit of CTA c of them.
 __device__ __forceinline__ int64_t paged_ctas(int64_t total, int ctas) { return max64(1, min64(ctas, total)); }
-__device__ __forceinline__ int64_t paged_first(int64_t total, int64_t n, int64_t c) {
-  return total / n * c + total % n * c / n;
-}
+__device__ __forceinline__ int64_t paged_first(int64_t total, int64_t n, int64_t c) { return paged_div(total * c, n); }
 
 // Every thread of the CTA calls this (nthreads a multiple of 32, at most
-// 1024): each sums a strip of the sequences, the strips are scanned, and the
-// thread whose strip holds the CTA's first unit walks to its sequence.
-__device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, int items, int tile, int extra, int cta,
-                                  int ctas, PagedPlanShared* s, unsigned int* status, int nthreads) {
+// 1024): each sums a strip of the sequences (for up to nthreads of them one
+// coalesced load, whose latency is most of what this costs), the strips are
+// scanned, and the thread whose strip holds the CTA's first unit walks to its
+// sequence.
+__device__ __forceinline__ void paged_plan(const int32_t* lengths, int B, int64_t cap, int items, int tile, int extra,
+                                           int cta, int ctas, PagedPlan* s, unsigned int* status, int nthreads) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = nthreads >> 5;
   const int strip = (B + nthreads - 1) / nthreads;
   const int b_lo = min(B, tid * strip), b_hi = min(B, b_lo + strip);
@@ -67,20 +72,23 @@ __device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, in
   __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += s->warp_sum[w];
-    total += s->warp_sum[w];
+    const int64_t x = s->warp_sum[w];
+    if (w < warp) before += x;
+    total += x;
   }
   // with fewer units than CTAs the last CTAs get none, so that no CTA without
   // work lies between two that share an item
   const int64_t n = paged_ctas(total, ctas), c = min64(cta, n), c1 = min64(cta + 1, n);
-  const int64_t lo = paged_first(total, n, c), hi = paged_first(total, n, c1);
+  const int64_t lo = paged_first(total, n, c);
   int64_t at = before + inc - sum;
   if (lo >= at && lo < at + sum) {
     int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const int64_t w = paged_units(paged_length(lengths, b, cap, nullptr), tile, items, extra);
-      if (lo < at + w) break;
-      at += w;
+    if (strip > 1) {
+      for (; b < b_hi; ++b) {
+        const int64_t w = paged_units(paged_length(lengths, b, cap, nullptr), tile, items, extra);
+        if (lo < at + w) break;
+        at += w;
+      }
     }
     s->b0 = b;
     s->start = at;
@@ -88,7 +96,7 @@ __device__ inline void paged_plan(const int32_t* lengths, int B, int64_t cap, in
   if (tid == 0) {
     s->total = total;
     s->lo = lo;
-    s->hi = hi;
+    s->hi = paged_first(total, n, c1);
   }
   __syncthreads();
 }
@@ -99,6 +107,7 @@ struct PagedWalk {
   bool whole;
   int64_t left;           // units of the range not yet handed out
   int b, item, len;
+  int len_after;          // of sequence b + 1, loaded when b was reached
   int64_t units;          // of an item of sequence b
   int64_t unit;           // of the item, where the next segment starts
   // the current segment: tiles [t0, t1) of item seg_item of sequence seg_b
@@ -106,16 +115,17 @@ struct PagedWalk {
   int64_t t0, t1;
   bool begins, ends;
 
-  __device__ __forceinline__ void init(const PagedPlanShared* s, const int32_t* lengths, int64_t cap, int tile_keys,
-                                       int extra, bool whole_items) {
+  __device__ __forceinline__ void init(const PagedPlan& s, const int32_t* lengths, int B, int64_t cap,
+                                       int tile_keys, int extra, bool whole_items) {
     whole = whole_items;
-    left = s->hi - s->lo;
+    left = s.hi - s.lo;
     if (left <= 0) return;
-    b = s->b0;
+    b = s.b0;
     len = paged_length(lengths, b, cap, nullptr);
+    len_after = b + 1 < B ? paged_length(lengths, b + 1, cap, nullptr) : 0;
     units = paged_tiles(len, tile_keys) + extra;
-    const int64_t off = s->lo - s->start;
-    item = (int)(off / units);
+    const int64_t off = s.lo - s.start;
+    item = (int)paged_div(off, units);
     unit = off - item * units;
     if (whole && unit > 0) {
       left -= units - unit;
@@ -131,7 +141,8 @@ struct PagedWalk {
         item = 0;
         do {                              // the range holds a further unit, so a longer sequence follows
           if (++b >= B) return false;
-          len = paged_length(lengths, b, cap, nullptr);
+          len = len_after;
+          len_after = b + 1 < B ? paged_length(lengths, b + 1, cap, nullptr) : 0;
         } while (len == 0);
         units = paged_tiles(len, tile_keys) + extra;
       }
@@ -153,9 +164,9 @@ struct PagedWalk {
   // begins its item and does not end it (so the range ends inside it): the
   // item ends at unit e of the call, and CTA c starts in front of e when
   // floor(total c / n) < e.
-  __device__ __forceinline__ int parts(const PagedPlanShared* s, int extra, int cta, int ctas) const {
-    const int64_t n = paged_ctas(s->total, ctas), e = s->hi + units - (t1 + extra);
-    return (int)((e * n + s->total - 1) / s->total) - cta;
+  __device__ __forceinline__ int parts(const PagedPlan& s, int extra, int cta, int ctas) const {
+    const int64_t n = paged_ctas(s.total, ctas), e = s.hi + units - (t1 + extra);
+    return (int)paged_div(e * n + s.total - 1, s.total) - cta;
   }
 };
 

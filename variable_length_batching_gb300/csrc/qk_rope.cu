@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
   const Lane<T, LP, kInter> me(a);
   Place at(a), ahead(a);                     // the row in hand, and the row to copy, kSlots further
   pdl_wait();
+  pdl_trigger();
   auto copy = [&](int slot) {
     if (ahead.more) {
       const int64_t t = (int64_t)ahead.tg * kTok + me.g;
