@@ -405,9 +405,9 @@ constexpr int kPagedMaxCtas = 512;      // CTAs of the split, at most (two parti
 constexpr int kPagedMaxHeads = 16;      // query heads of one item, at most
 size_t paged_attn_workspace_bytes(int G, int d);
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
-// The tensor-core kernel: bf16, d = 64 or 128, pages of a multiple of 8.
-bool paged_attn_tc_supported(nt_dtype dt, const PagedAttnProblem& p);
-cudaError_t launch_paged_attn_tc(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
+// The TMA-fed kernel: pages of a multiple of 8 positions.
+bool paged_attn_tma_supported(const PagedAttnProblem& p);
+cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 
 bool attn_simt_supported(int d);
 cudaError_t launch_attn_simt(nt_dtype dt, const AttnProblem& p, unsigned int* status, cudaStream_t s);

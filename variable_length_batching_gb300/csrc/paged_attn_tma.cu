@@ -1,0 +1,757 @@
+// Attention of one new token per sequence over a paged key/value cache whose
+// pages hold a multiple of 8 positions.
+//
+// The floor is the cache's bytes: 2 len H_kv d elements read once, for G
+// multiply-adds per element (G query heads to a key head), so the kernel is
+// a stream of TMA loads and everything else has to hide behind it.  One CTA
+// per SM holds 128 to 160 KB of key/value tiles in flight (what a latency of
+// about 1 us at the SM's share of the bandwidth needs, three times over).
+//
+// Two producer warps walk the CTA's share of the batch (paged_plan.cuh) tile
+// by tile, alternating: one box of R = gcd(page_size, 64, tile) keys per lane
+// into a ring of stages.  (A copy takes its warp about 85 cycles to issue, so
+// one warp alone could not keep up with HBM for 64 keys of d = 64 in pages of
+// 16: eight boxes in 700 cycles.)  A third warp copies the items' query rows.
+// Eight consumer warps take 16 keys of a tile each, every warp with its own
+// running maximum, sum and output.
+//
+// bf16 (boxes in the 128-byte swizzle; 64-byte for d = 32): a warp's part is
+//   S = Q K^T      (heads x 16 keys; rows beyond the item's heads are zero)
+//   P = exp2(S - max), rounded to bf16 for the product (the sum keeps fp32)
+//   O^T += V^T P^T (d x heads): S's accumulator layout is the B operand's, so
+//                  P goes from registers to the product, and V^T comes from
+//                  the tile by transposed matrix loads.
+// These are mma.sync products of 16 rows: a decode item has at most 16 query
+// rows where a tcgen05 tile has 64 at least, and its accumulators' round trip
+// through TMEM would be longer than the whole product.  The products and
+// matrix loads of a 32 KB stage take about a tenth of the time HBM takes to
+// deliver it.
+//
+// fp32 (plain rows): a key's row lies across the lanes; the lanes' partial
+// dot products of 32 (key, head) pairs are reduced together (butterfly32),
+// which leaves one score per lane.
+//
+// At the end of a segment the eight warps leave their results in shared
+// memory for a fourth kind of warp, which merges them and writes the output
+// or a partial result for the join, while the eight go on: with short
+// sequences the merge is as long as the segment's tiles.
+#include "paged_plan.cuh"
+#include "tc_ptx.cuh"
+
+namespace nt {
+namespace {
+
+using namespace tc;
+
+constexpr int kConsumers = 8;               // warps
+constexpr int kProducers = 2;               // warps, tiles alternating
+constexpr int kQSlots = 4;                  // items whose query rows are in flight or in use
+constexpr int kThreads = (kConsumers + kProducers + 2) * 32;
+
+// HP: query heads of an item, at most, and what the registers are laid out
+// for: 8 or 16 in bf16 (one or two accumulator tiles), 1, 2, 4 or 8 in fp32.
+template <typename T, int D, int HP>
+struct Cfg {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  // keys per stage, and per unit of the split: 16 KB of bf16 (32 at d = 128), 32 of fp32
+  static constexpr int kTile = kBf16 ? (D == 32 ? 128 : 64) : 4096 / D;
+  static constexpr int kSlices = kTile / 16;                  // warps that share a stage
+  static constexpr int kGroups = kConsumers / kSlices;        // stages worked on at once
+  static constexpr uint32_t kRow = D * sizeof(T);             // bytes of a key's row
+  static constexpr uint32_t kSide = kTile * kRow;             // K or V of a stage
+  static constexpr uint32_t kStage = 2 * kSide;
+  static constexpr int kRedStride = D + 4;                    // floats: keeps the merge's writes conflict-free
+  static constexpr uint32_t kRed = kConsumers * HP * kRedStride * 4;
+  static constexpr int kRedBufs = HP * D <= 1024 ? 2 : 1;     // segments whose results wait for the merge
+  // The merge: one warp of its own, or, where it is four times the work, the
+  // eight together (G = 16, d = 128: 78 us for a batch that took 104 with one).
+  static constexpr int kMergeWarps = HP == 16 ? kConsumers : 1;
+  static constexpr uint32_t kQBytes = HP * kRow;
+  static constexpr int kExtra = HP == 16 ? 3 : 2;             // an item's cost beside its tiles, in tiles
+  static constexpr uint32_t kFixed = kRedBufs * kRed + kQSlots * kQBytes + 4096 /* statistics, barriers, plan */;
+  // A multiple of the groups and of the producers: a stage is then always the
+  // same warps' and they see every phase of its barriers.  (Otherwise a warp
+  // would wait on a phase whose predecessor it never waited for, which parity
+  // cannot tell apart from the phase before that.)
+  static constexpr int kRound = kGroups > kProducers ? kGroups : kProducers;
+  static constexpr int kFit = (int)((226 * 1024 - 1024 - kFixed) / kStage);
+  static constexpr int kStages = (kFit < 16 ? kFit : 16) / kRound * kRound;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kFixed;
+  static_assert(kStages >= 4 && kStages % kGroups == 0 && kStages % kProducers == 0 && kSmem <= 227 * 1024,
+                "shared memory");
+};
+
+struct Ctl {
+  uint64_t full[16], empty[16], q_full[kQSlots], q_empty[kQSlots], red_full[2], red_empty[2];
+  float m[2][kConsumers][16], l[2][kConsumers][16];
+  PagedPlan plan;
+  int abort;
+};
+static_assert(sizeof(Ctl) <= 4096, "control block");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// v[i] summed over the lanes, for i = this lane: halves the array and the
+// lane distance together (31 shuffles for 32 sums).
+__device__ __forceinline__ float butterfly32(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float give = up ? v[i] : v[i + m];
+      const float keep = up ? v[i + m] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+    }
+  }
+  return v[0];
+}
+
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[N]) {
+  if constexpr (N == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x; x[1] = v.y;
+  } else {
+    x[0] = *p;
+  }
+}
+
+struct TmaArgs {
+  const void* q;
+  int64_t q_stride;
+  const int32_t* table;
+  const int32_t* lengths;
+  void* o;
+  float* lse;
+  void* workspace;
+  int B, H, G, Hkv, max_pages, page_size, n_pages;
+  int items, hgroups, heads;      // head items per sequence; item slots of the partials
+  bool whole;                     // items are not split
+  int box;                        // keys per box: gcd(page_size, 64)
+  float scale_log2;
+  unsigned int* status;
+};
+
+// A consumer warp's part of a segment: its query rows, running maxima, sums
+// and outputs, and what it does with its 16 keys of a tile.
+template <typename T, int D, int HP>
+struct Worker;
+
+// bf16: matrix products.
+template <int D, int HP>
+struct Worker<bf16, D, HP> {
+  using C = Cfg<bf16, D, HP>;
+  static constexpr int NT = HP / 8;
+  static constexpr uint32_t kBoxRow = D < 64 ? D * 2 : 128;   // bytes of a key in a box's columns
+  uint32_t qa[D / 16][4];
+  float m[NT], l[NT], o[NT][D / 16][4];
+  int g, tq;                       // accumulator row (head) and column pair
+  uint32_t hs, row_off, xr;        // a box's next 64 columns; this lane's row in the matrix loads; its swizzle
+  int box, slice;
+
+  __device__ __forceinline__ uint32_t row_at(int r) const {
+    return (uint32_t)(r / box) * box * C::kRow + r % box * kBoxRow;
+  }
+  __device__ __forceinline__ Worker(const TmaArgs& a, int slice_) {
+    const int lane = threadIdx.x & 31;
+    g = lane >> 2;
+    tq = lane & 3;
+    box = a.box;
+    slice = slice_;
+    hs = a.box * 128;
+    const int mrow = slice * 16 + ((lane >> 4) << 3) + (lane & 7);
+    row_off = row_at(mrow);
+    const int sw = D < 64 ? (mrow >> 1) & 3 : mrow & 7;
+    xr = (((lane >> 3) & 1) ^ sw) << 4;
+  }
+  __device__ __forceinline__ void load_q(const uint8_t* rows, int nh) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(rows);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qa[ks][0] = g < nh ? q[(g * D + ks * 16) / 2 + tq] : 0u;
+      qa[ks][2] = g < nh ? q[(g * D + ks * 16 + 8) / 2 + tq] : 0u;
+      qa[ks][1] = NT == 2 && g + 8 < nh ? q[((g + 8) * D + ks * 16) / 2 + tq] : 0u;
+      qa[ks][3] = NT == 2 && g + 8 < nh ? q[((g + 8) * D + ks * 16 + 8) / 2 + tq] : 0u;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+    }
+  }
+  // the first `left` of the slice's keys
+  __device__ __forceinline__ void tile(uint8_t* stage, int left, float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t kbase = smem_u32(stage), vbase = kbase + C::kSide;
+    if (left < 16) {
+      // rows behind the last key may hold anything: zeros instead, so that a probability of 0 adds 0
+      for (int e = lane; e < (16 - left) * (D / 8); e += 32) {
+        const int row = slice * 16 + left + e / (D / 8), ch = e % (D / 8);
+        *reinterpret_cast<uint4*>(stage + C::kSide + row_at(row) + (ch >> 3) * hs + (ch & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+    // two chains for each eight keys
+    float s[2][4] = {}, s2[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t kb[4];
+      ldsm4(kbase + (ks >> 2) * hs + row_off + ((((uint32_t)ks & 3) << 5) ^ xr), kb);
+      mma16816(ks & 1 ? s2[0] : s[0], qa[ks], kb[0], kb[1]);
+      mma16816(ks & 1 ? s2[1] : s[1], qa[ks], kb[2], kb[3]);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      s[0][c] += s2[0][c];
+      s[1][c] += s2[1][c];
+    }
+    uint32_t pb[NT][2];
+    float corr[NT];
+    bool moved = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float v[4] = {s[0][2 * n] * scale_log2, s[0][2 * n + 1] * scale_log2, s[1][2 * n] * scale_log2,
+                    s[1][2 * n + 1] * scale_log2};
+      if (left < 16) {
+        if (2 * tq >= left) v[0] = -INFINITY;
+        if (2 * tq + 1 >= left) v[1] = -INFINITY;
+        if (8 + 2 * tq >= left) v[2] = -INFINITY;
+        if (9 + 2 * tq >= left) v[3] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[n], mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      moved |= mn > m[n];
+      corr[n] = ex2_approx(m[n] - base);
+      m[n] = mn;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = ex2_approx(v[c] - base);
+      l[n] = l[n] * corr[n] + (v[0] + v[1]) + (v[2] + v[3]);
+      pb[n][0] = pack_bf16x2(v[0], v[1]);
+      pb[n][1] = pack_bf16x2(v[2], v[3]);
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+      // the output's columns are heads 2 tq and 2 tq + 1: their factors sit in those rows' lanes
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float c0 = __shfl_sync(0xffffffffu, corr[n], 8 * tq);
+        const float c1 = __shfl_sync(0xffffffffu, corr[n], 8 * tq + 4);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[n][i][0] *= c0;
+          o[n][i][1] *= c1;
+          o[n][i][2] *= c0;
+          o[n][i][3] *= c1;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t va[4];
+      ldsm4_t(vbase + (i >> 2) * hs + row_off + ((((uint32_t)i & 3) << 5) ^ xr), va);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816(o[n][i], va, pb[n][0], pb[n][1]);
+    }
+    if (left < 16) fence_async_shared();       // the zeros, before the next copy into this stage
+  }
+  // the warp's result: maxima and sums (-1: no keys, nothing to add), outputs [HP][kRedStride]
+  __device__ __forceinline__ void result(float* rm, float* rl, float* ro, int nh, bool active) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+      if (tq == 0) {
+        rm[n * 8 + g] = m[n];
+        rl[n * 8 + g] = active ? l[n] : -1.f;
+      }
+    }
+    if (!active) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = n * 8 + 2 * tq + c;
+        if (h >= nh) continue;
+        float* r = ro + h * C::kRedStride + g;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          r[i * 16] = o[n][i][c];
+          r[i * 16 + 8] = o[n][i][c + 2];
+        }
+      }
+  }
+};
+
+// fp32: D / 32 elements of a row per lane, batches of KB keys x HP heads.
+template <int D, int HP>
+struct Worker<float, D, HP> {
+  using C = Cfg<float, D, HP>;
+  static constexpr int N = D / 32, KB = 32 / HP < 16 ? 32 / HP : 16;
+  float q[HP][N], o[HP][N];
+  float m, l;                      // of head lane % HP
+  int slice;
+
+  __device__ __forceinline__ Worker(const TmaArgs&, int slice_) : slice(slice_) {}
+  __device__ __forceinline__ void load_q(const uint8_t* rows, int nh) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) q[h][c] = o[h][c] = 0.f;
+      if (h < nh) load_row<N>(reinterpret_cast<const float*>(rows) + h * D + lane * N, q[h]);
+    }
+    m = -INFINITY;
+    l = 0.f;
+  }
+  __device__ __forceinline__ void tile(const uint8_t* stage, int left, float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    const float* k = reinterpret_cast<const float*>(stage) + slice * 16 * D + lane * N;
+    const float* v = k + C::kSide / 4;
+#pragma unroll
+    for (int b = 0; b < 16; b += KB) {
+      if (b >= left) break;
+      float s[32];
+#pragma unroll
+      for (int j = 0; j < 32 / HP; ++j) {
+        float x[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) x[c] = 0.f;
+        if (j < KB && b + j < left) load_row<N>(k + (b + j) * D, x);
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          float d = 0.f;
+#pragma unroll
+          for (int c = 0; c < N; ++c) d = fmaf(q[h][c], x[c], d);
+          s[j * HP + h] = d;
+        }
+      }
+      float sc = butterfly32(s) * scale_log2;        // of key b + lane / HP, head lane % HP
+      if (lane / HP >= KB || b + lane / HP >= left) sc = -INFINITY;
+      float mx = sc;
+#pragma unroll
+      for (int d = HP; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float mn = fmaxf(m, mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m - base), pr = exp2f(sc - base);
+      float sum = pr;
+#pragma unroll
+      for (int d = HP; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const bool moved = mn > m;
+      l = l * corr + sum;
+      m = mn;
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float ch = __shfl_sync(0xffffffffu, corr, h);
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[h][c] *= ch;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        if (b + j >= left) break;                    // rows behind the last key may hold anything
+        float x[N];
+        load_row<N>(v + (b + j) * D, x);
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float pj = __shfl_sync(0xffffffffu, pr, j * HP + h);
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[h][c] = fmaf(pj, x[c], o[h][c]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void result(float* rm, float* rl, float* ro, int nh, bool active) {
+    const int lane = threadIdx.x & 31;
+    if (lane < HP) {
+      rm[lane] = m;
+      rl[lane] = active ? l : -1.f;
+    }
+    if (!active) return;
+#pragma unroll
+    for (int h = 0; h < HP; ++h)
+      if (h < nh)
+#pragma unroll
+        for (int c = 0; c < N; ++c) ro[h * C::kRedStride + lane * N + c] = o[h][c];
+  }
+};
+
+// The merge of a segment's eight warps, and its output or partial result: the
+// caller is thread `first` of `step`.
+template <typename T, int D, int HP>
+__device__ __forceinline__ void merge_segment(const TmaArgs& a, const PagedWalk& w, const Ctl* ctl, const float* red,
+                                              int buf, int first, int step) {
+  using C = Cfg<T, D, HP>;
+  constexpr int kHeads = HP;
+  const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
+  const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
+  const int nh = min(kHeads, a.G - h0);
+  const bool whole = w.begins && w.ends;
+  const int64_t pslot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
+  const int64_t hq = (int64_t)kvh * a.G + h0;
+  const float(*sm)[16] = ctl->m[buf];
+  const float(*sl)[16] = ctl->l[buf];
+  // a lane's four columns of a head; two passes at a time, to overlap their reads
+#pragma unroll 2
+  for (int e = first; e < nh * (D / 4); e += step) {
+    const int h = e / (D / 4), c = e % (D / 4) * 4;
+    float f[kConsumers], mm = -INFINITY;
+    float4 v[kConsumers];
+#pragma unroll
+    for (int x = 0; x < kConsumers; ++x) {
+      f[x] = sm[x][h];
+      mm = fmaxf(mm, f[x]);
+      v[x] = sl[x][h] == -1.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : *reinterpret_cast<const float4*>(red + buf * (C::kRed / 4) +
+                                                                 (x * kHeads + h) * C::kRedStride + c);
+    }
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kConsumers; ++x) {
+      const float lx = sl[x][h];
+      const float fx = lx == -1.f ? 0.f : ex2_approx(f[x] - base);
+      ll += fx * lx;
+      oo.x += fx * v[x].x;
+      oo.y += fx * v[x].y;
+      oo.z += fx * v[x].z;
+      oo.w += fx * v[x].w;
+    }
+    if (whole) {
+      const float inv = 1.f / ll;
+      T* out = static_cast<T*>(a.o) + ((int64_t)w.seg_b * a.H + hq + h) * D + c;
+      if constexpr (C::kBf16)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv),
+                                                    pack_bf16x2(oo.z * inv, oo.w * inv));
+      else
+        *reinterpret_cast<float4*>(out) = make_float4(oo.x * inv, oo.y * inv, oo.z * inv, oo.w * inv);
+      if (a.lse && c == 0) a.lse[(hq + h) * a.B + w.seg_b] = (mm + log2f(ll)) * 0.6931471805599453f;
+    } else {
+      *reinterpret_cast<float4*>(part.o + (pslot * a.heads + h) * D + c) = oo;
+      if (c == 0) {
+        part.ml[(pslot * a.heads + h) * 2] = mm;
+        part.ml[(pslot * a.heads + h) * 2 + 1] = ll;
+      }
+    }
+  }
+}
+
+template <typename T, int D, int HP>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const TmaArgs a) {
+  using C = Cfg<T, D, HP>;
+  constexpr int kHeads = HP, S = C::kStages, kTile = C::kTile;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* stages = smem;
+  float* red = reinterpret_cast<float*>(smem + S * C::kStage);
+  uint8_t* qbuf = reinterpret_cast<uint8_t*>(red) + C::kRedBufs * C::kRed;
+  Ctl* ctl = reinterpret_cast<Ctl*>(qbuf + kQSlots * C::kQBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t cap = min64((int64_t)a.max_pages * a.page_size, 0x7fffffff);
+  const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
+
+  // a lane to each barrier
+  if (threadIdx.x < S) {
+    mbar_init(&ctl->full[threadIdx.x], 1);
+    mbar_init(&ctl->empty[threadIdx.x], C::kSlices);
+  }
+  if (threadIdx.x < kQSlots) {
+    mbar_init(&ctl->q_full[threadIdx.x], 1);
+    mbar_init(&ctl->q_empty[threadIdx.x], kConsumers);
+  }
+  if (threadIdx.x < C::kRedBufs) {
+    mbar_init(&ctl->red_full[threadIdx.x], kConsumers);
+    mbar_init(&ctl->red_empty[threadIdx.x], C::kMergeWarps);
+  }
+  if (threadIdx.x == 0) ctl->abort = 0;
+  if (threadIdx.x < 32) fence_mbar_init();
+  if (threadIdx.x == 32) prefetch_tmap(&kmap);
+  if (threadIdx.x == 64) prefetch_tmap(&vmap);
+  pdl_wait();
+  pdl_trigger();
+  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status, kThreads);
+  PagedWalk w;
+  w.init(ctl->plan, a.lengths, a.B, cap, kTile, C::kExtra, a.whole);
+
+  if (warp == kConsumers + kProducers) {
+    // ---- query rows, item by item ------------------------------------------
+    uint32_t segs = 0;
+    while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      const int slot = segs % kQSlots;
+      if (!mbar_wait_warp(&ctl->q_empty[slot], ((segs / kQSlots) & 1) ^ 1, &ctl->abort, a.status)) break;
+      const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
+      const uint32_t bytes = min(kHeads, a.G - h0) * C::kRow;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl->q_full[slot], bytes);
+        bulk_load(qbuf + slot * C::kQBytes,
+                  static_cast<const T*>(a.q) + w.seg_b * a.q_stride + (int64_t)(kvh * a.G + h0) * D, bytes,
+                  &ctl->q_full[slot]);
+      }
+      ++segs;
+    }
+    if (ctl->abort && lane == 0)                      // given up: the copies in flight land first
+      for (uint32_t i = segs > kQSlots ? segs - kQSlots : 0; i < segs; ++i)
+        mbar_wait(&ctl->q_full[i % kQSlots], (i / kQSlots) & 1, nullptr, a.status);
+    return;
+  }
+  if (warp == kConsumers + kProducers + 1) {
+    // ---- merge: the consumers' results of a segment ------------------------------
+    uint32_t segs = 0;
+    int64_t open_id = -1, open_parts = 0;             // the item left unfinished
+    while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      if (C::kMergeWarps == 1) {
+        const int buf = segs % C::kRedBufs;
+        if (!mbar_wait_warp(&ctl->red_full[buf], (segs / C::kRedBufs) & 1, &ctl->abort, a.status)) break;
+        merge_segment<T, D, HP>(a, w, ctl, red, buf, lane, 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
+        ++segs;
+      }
+      if (w.begins && !w.ends) {
+        open_id = (int64_t)w.seg_b * a.items + w.seg_item;
+        open_parts = w.parts(ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
+      }
+    }
+    if (lane == 0) {
+      part.id[2 * blockIdx.x] = open_id;
+      part.id[2 * blockIdx.x + 1] = open_parts;
+    }
+    return;
+  }
+  if (warp >= kConsumers) {
+    // ---- producers: tiles warp - kConsumers, + kProducers, ... ----------------
+    const uint32_t me = warp - kConsumers;
+    const uint32_t rows = kTile / a.box;              // boxes down a tile
+    const uint32_t rb = lane % rows, side = lane / rows;
+    const bool has_box = side < 2;
+    const CUtensorMap* map = side ? &vmap : &kmap;
+    const uint32_t dst = side * C::kSide + rb * a.box * C::kRow;
+    const int32_t* trow = nullptr;
+    uint32_t pages = 0;                               // of the sequence
+    const uint32_t ps = a.page_size, step_pg = kProducers * kTile / ps, step_row = kProducers * kTile % ps;
+    // The block table is read 32 entries at a time, a lane each, and one such
+    // window ahead, so that a lookup is a shuffle.  The window stays when the
+    // next segment starts on the same pages: the sequence's next head.
+    uint32_t win = 0;                                 // its first page index
+    int cur = -1, nxt = -1, wb = -1;                  // entries win + lane, win + 32 + lane; sequence
+    auto entry = [&](uint32_t i) { return i < pages ? trow[i] : -1; };
+    uint32_t seg_it = 0, last = 0;                    // the segment's first tile in the CTA's order
+    bool ok = true;
+    while (ok && w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+      int64_t t = w.t0 + ((me - seg_it) & (kProducers - 1));
+      if (t < w.t1) {
+        const int kvh = w.seg_item / a.hgroups;
+        trow = a.table + (int64_t)w.seg_b * a.max_pages;
+        pages = ((uint32_t)w.seg_len + ps - 1) / ps;
+        const uint32_t key0 = (uint32_t)t * kTile, pg0 = key0 / ps;
+        uint32_t row = key0 - pg0 * ps + rb * a.box, pg = pg0;      // of this lane's box
+        while (row >= ps) {
+          row -= ps;
+          ++pg;
+        }
+        uint32_t first = pg0, first_row = key0 - pg0 * ps;          // of the tile's first key
+        if (wb != w.seg_b || win != pg0) {
+          wb = w.seg_b;
+          win = pg0;
+          cur = entry(win + lane);
+          nxt = entry(win + 32 + lane);
+        }
+        for (; t < w.t1; t += kProducers) {
+          if (first - win >= 32) {
+            win += 32;
+            cur = nxt;
+            nxt = entry(win + 32 + lane);
+          }
+          const uint32_t at = pg - win;
+          const int id0 = __shfl_sync(0xffffffffu, cur, at & 31), id1 = __shfl_sync(0xffffffffu, nxt, at & 31);
+          const int page = at < 32 ? id0 : id1;
+          const bool now = has_box && t * kTile + rb * a.box < w.seg_len;
+          int z = page * a.Hkv + kvh;
+          if (now && (uint32_t)page >= (uint32_t)a.n_pages) {
+            flag_device(a.status, kDevCheck);
+            z = a.n_pages * a.Hkv;                    // outside the map: reads as zeros
+          }
+          const uint32_t it = seg_it + (uint32_t)(t - w.t0);
+          const int st = it % S;
+          ok = mbar_wait_warp(&ctl->empty[st], ((it / S) & 1) ^ 1, &ctl->abort, a.status);
+          if (!ok) break;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, now));
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * a.box * C::kRow);
+          __syncwarp();
+          if (now) tma_load_4d(stages + st * C::kStage + dst, map, &ctl->full[st], 0, (int)row, 0, z);
+          last = it + 1;
+          pg += step_pg;
+          row += step_row;
+          if (row >= ps) {
+            row -= ps;
+            ++pg;
+          }
+          first += step_pg;
+          first_row += step_row;
+          if (first_row >= ps) {
+            first_row -= ps;
+            ++first;
+          }
+        }
+      }
+      seg_it += (uint32_t)(w.t1 - w.t0);
+    }
+    if (!ok && lane == 0)                             // given up: the copies in flight land first
+      for (uint32_t i = 0; i < (uint32_t)S && i < last; ++i)
+        if (((last - 1 - i) & (kProducers - 1)) == me)
+          mbar_wait(&ctl->full[(last - 1 - i) % S], ((last - 1 - i) / S) & 1, nullptr, a.status);
+    return;
+  }
+
+  // ---- consumers -------------------------------------------------------------
+  // sequences with no key: zeros
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (paged_length(a.lengths, b, cap, nullptr) != 0) continue;
+    for (int e = threadIdx.x; e < a.H * D; e += kConsumers * 32)
+      static_cast<T*>(a.o)[(int64_t)b * a.H * D + e] = from_f32<T>(0.f);
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.H; h += kConsumers * 32) a.lse[(int64_t)h * a.B + b] = -INFINITY;
+  }
+  const int grp = warp / C::kSlices, slice = warp % C::kSlices;
+  Worker<T, D, HP> me(a, slice);
+  uint32_t it = 0, segs = 0;
+  bool ok = true;
+  while (ok && w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
+    const int nh = min(kHeads, a.G - (w.seg_item % a.hgroups) * kHeads);
+    const int slot = segs % kQSlots, buf = segs % C::kRedBufs;
+    ok = mbar_wait_warp(&ctl->q_full[slot], (segs / kQSlots) & 1, &ctl->abort, a.status);
+    if (!ok) break;
+    me.load_q(qbuf + slot * C::kQBytes, nh);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+    bool active = false;
+    for (int64_t t = w.t0; t < w.t1; ++t, ++it) {
+      if (it % C::kGroups != (uint32_t)grp) continue;
+      const int st = it % S;
+      ok = mbar_wait_warp(&ctl->full[st], (it / S) & 1, &ctl->abort, a.status);
+      if (!ok) break;
+      const int left = (int)min64(w.seg_len - t * kTile - slice * 16, 16);     // keys of this slice
+      if (left > 0) {
+        active = true;
+        me.tile(stages + st * C::kStage, left, a.scale_log2);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->empty[st]);
+    }
+    if (!ok) break;
+    ok = mbar_wait_warp(&ctl->red_empty[buf], ((segs / C::kRedBufs) & 1) ^ 1, &ctl->abort, a.status);
+    if (!ok) break;
+    me.result(ctl->m[buf][warp], ctl->l[buf][warp], red + buf * (C::kRed / 4) + warp * kHeads * C::kRedStride, nh,
+              active);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->red_full[buf]);
+    if (C::kMergeWarps > 1) {
+      ok = mbar_wait_warp(&ctl->red_full[buf], (segs / C::kRedBufs) & 1, &ctl->abort, a.status);
+      if (!ok) break;
+      merge_segment<T, D, HP>(a, w, ctl, red, buf, threadIdx.x, kConsumers * 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
+    }
+    ++segs;
+  }
+}
+
+template <typename T, int D, int HP>
+cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
+  using C = Cfg<T, D, HP>;
+  TmaArgs a;
+  a.q = p.q;
+  a.q_stride = p.q_stride;
+  a.table = p.table;
+  a.lengths = p.lengths;
+  a.o = p.o;
+  a.lse = p.lse;
+  a.workspace = p.workspace;
+  a.B = p.B;
+  a.H = p.H;
+  a.G = p.H / p.pool.H;
+  a.Hkv = p.pool.H;
+  a.max_pages = p.max_pages;
+  a.page_size = p.pool.page_size;
+  a.n_pages = p.pool.n_pages;
+  a.hgroups = (a.G + HP - 1) / HP;
+  a.items = a.Hkv * a.hgroups;
+  a.heads = min(HP, a.G);
+  a.whole = paged_whole_items(p, sizeof(T));
+  a.box = min(64, C::kTile);
+  while (a.page_size % a.box) a.box >>= 1;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.status = status;
+  CUtensorMap maps[2];
+  // bf16: a page's rows as 64-column parts, so that one swizzled box holds them all; fp32: plain rows
+  constexpr uint32_t kCols = C::kBf16 && D > 64 ? 64 : D;
+  const uint64_t rows = (uint64_t)a.page_size;
+  const uint64_t dims[4] = {kCols, rows, D / kCols, (uint64_t)a.n_pages * a.Hkv};
+  const uint64_t strides[3] = {C::kRow, kCols * sizeof(T), C::kRow * rows};
+  const uint32_t box[4] = {kCols, (uint32_t)a.box, D / kCols, 1};
+  constexpr CUtensorMapSwizzle kSwizzle = !C::kBf16 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                          : D == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  for (int i = 0; i < 2; ++i)
+    if (!make_tmap(&maps[i], C::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, kSwizzle,
+                   i ? p.pool.v : p.pool.k, 4, dims, strides, box))
+      return cudaErrorInvalidValue;
+  const int ctas = min(sm_count(), kPagedMaxCtas);
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tma_kernel<T, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_tma_kernel<T, D, HP>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[0], maps[1], a);
+  if (e != cudaSuccess || a.whole) return e;
+  return launch_paged_join(C::kBf16 ? NT_BF16 : NT_F32, p, ctas, a.items, HP, s);
+}
+
+template <int D>
+cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
+  const int G = p.H / p.pool.H;
+  if (dt == NT_BF16) return G <= 8 ? run<bf16, D, 8>(p, status, s) : run<bf16, D, 16>(p, status, s);
+  if (G == 1) return run<float, D, 1>(p, status, s);
+  if (G == 2) return run<float, D, 2>(p, status, s);
+  if (G <= 4) return run<float, D, 4>(p, status, s);
+  return run<float, D, 8>(p, status, s);
+}
+
+}  // namespace
+
+bool paged_attn_tma_supported(const PagedAttnProblem& p) {
+  return (p.d == 32 || p.d == 64 || p.d == 128) && p.pool.page_size % 8 == 0 && p.pool.n_pages > 0;
+}
+
+cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
+  if (p.d == 32) return run_d<32>(dt, p, status, s);
+  if (p.d == 64) return run_d<64>(dt, p, status, s);
+  return run_d<128>(dt, p, status, s);
+}
+
+}  // namespace nt

@@ -385,7 +385,9 @@ __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w &
 
 }  // namespace tc
 
-// Host: TMA tensor maps over bf16 tensors with the 128-byte swizzle.
+// Host: TMA tensor maps; over bf16 tensors with the 128-byte swizzle.
+bool make_tmap(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* ptr, int rank,
+               const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box);
 bool make_tmap_bf16(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
 // Row-major [outer, inner] matrix, box {64 (inner), rows}.
