@@ -35,8 +35,20 @@ bool make_tmap(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle sw
     es[i] = 1;
   }
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides_bytes[i];
-  return fn(map, type, rank, const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(map, type, rank, const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    // The encoder is a driver call and wants a current context, which a
+    // thread that has made no runtime call yet does not have (autograd's
+    // backward thread, for one).  Setting the thread's device gives it one.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    r = encode();
+  }
+  return r == CUDA_SUCCESS;
 }
 
 bool make_tmap_bf16(CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
