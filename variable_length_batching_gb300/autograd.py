@@ -13,7 +13,11 @@ forward: nt_pair_broadcast, nt_pair_transition, nt_pair_reduce; the
 backward: nt_pair_block_backward, whose gradients are fp32 and are returned
 in the dtype of each input).  ``varlen_attention`` is non-causal or causal
 self-attention over cu_seqlens segments (the forward keeps the natural-log
-LSE; the backward is nt_varlen_attn_bwd).
+LSE; the backward is nt_varlen_attn_bwd).  ``qk_norm_rope`` gives packed
+queries and keys their norms and positions before it (nt_qk_norm_rope; the
+backward is nt_qk_norm_rope_bwd):
+
+    q, k = qk_norm_rope(q, k, turns, cu_seqlens=cu_seqlens, q_gamma=g_q, k_gamma=g_k)
 """
 from __future__ import annotations
 
@@ -84,3 +88,34 @@ def varlen_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
                      causal: bool = False, scale: Optional[float] = None):
     """Self-attention within each cu_seqlens segment, with autograd."""
     return VarlenAttention.apply(q, k, v, cu_seqlens, max_len, causal, scale)
+
+
+class QKNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0, eps, interleaved, rot_scale):
+        q_out, k_out = nt.nt_qk_norm_rope(q, k, turns, cu_seqlens=cu_seqlens, positions=positions, pos0=pos0,
+                                          q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, interleaved=interleaved,
+                                          rot_scale=rot_scale)
+        ctx.save_for_backward(q if q_gamma is not None else None, k if k_gamma is not None else None, turns, q_gamma,
+                              k_gamma, cu_seqlens, positions, pos0)
+        ctx.args = eps, interleaved, rot_scale
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0 = ctx.saved_tensors
+        eps, interleaved, rot_scale = ctx.args
+        dq, dk, dqg, dkg = nt.nt_qk_norm_rope_bwd(dq_out.contiguous(), dk_out.contiguous(), turns, q=q, k=k,
+                                                  cu_seqlens=cu_seqlens, positions=positions, pos0=pos0,
+                                                  q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, interleaved=interleaved,
+                                                  rot_scale=rot_scale)
+        return dq, dk, None, dqg, dkg, None, None, None, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, turns: Optional[torch.Tensor], cu_seqlens=None, positions=None,
+                 pos0=None, q_gamma: Optional[torch.Tensor] = None, k_gamma: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0):
+    """Per-head norm and rotary positions of packed q and k with autograd
+    (:func:`nt.nt_qk_norm_rope`): returns (q_out, k_out), ready for
+    :func:`varlen_attention`.  The gammas are fp32 leaves."""
+    return QKNormRope.apply(q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0, eps, interleaved, rot_scale)

@@ -69,7 +69,7 @@ __device__ __forceinline__ float butterfly(float (&v)[32]) {
 }
 
 template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnProblem p, int items, int hgroups,
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const PagedAttnProblem p, int items, int hgroups,
                                                               int G, bool whole_items, float scale_log2,
                                                               unsigned int* status) {
   constexpr int N = D / 32;          // elements of a row per lane

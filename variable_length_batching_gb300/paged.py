@@ -1,0 +1,214 @@
+"""A paged key/value cache for answering one token at a time.
+
+:class:`PageTable` is the host side: which pages hold which sequence, what is
+free, what is shared.  Sequences are added, extended, forked (the copy shares
+its pages; the first write into a shared page gets its own copy of it), freed
+and compacted (the pages in use moved to the front of the pool).  It moves no
+data itself: what has to be copied comes back as a list of pages.
+
+:class:`PagedCache` joins it with the pages on the device (``nt.KVPages``) and
+the library's calls: a step names its sequences and how many tokens each
+gains, writes their keys and values (``nt_paged_write``) and attends with one
+query token per sequence (``nt_paged_attn``); forks and compaction copy pages
+(``nt_paged_copy``).
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Dict, List, Optional, Sequence, Tuple
+
+import torch
+
+from . import nt
+
+Copies = List[Tuple[int, int]]
+
+
+class OutOfPages(RuntimeError):
+    """The pool has not enough free pages; nothing was changed."""
+
+
+class PageTable:
+    """Pages [0, n_pages) of ``page_size`` positions and the sequences in them."""
+
+    def __init__(self, n_pages: int, page_size: int):
+        if n_pages < 0 or page_size < 1:
+            raise ValueError("n_pages >= 0 and page_size >= 1")
+        self.n_pages, self.page_size = n_pages, page_size
+        self.refs = [0] * n_pages
+        self.free_pages = list(range(n_pages - 1, -1, -1))      # taken from the end: low pages first
+        self.pages: Dict[int, List[int]] = {}                   # of each sequence, in order
+        self.length: Dict[int, int] = {}
+        self._next = 0
+
+    def add(self) -> int:
+        """A new, empty sequence's id."""
+        seq = self._next
+        self._next += 1
+        self.pages[seq], self.length[seq] = [], 0
+        return seq
+
+    def _known(self, seq: int):
+        if seq not in self.pages:
+            raise KeyError(f"no sequence {seq}")
+
+    def _drop(self, page: int):
+        self.refs[page] -= 1
+        if self.refs[page] == 0:
+            self.free_pages.append(page)
+
+    def extend(self, seqs: Sequence[int], counts: Sequence[int]) -> Copies:
+        """Room for counts[i] more positions in each of ``seqs`` (distinct).
+        Returns the (source, destination) pages to copy before they are
+        written: the partly filled last pages that other sequences share.
+        Raises OutOfPages with nothing changed."""
+        if len(seqs) != len(counts) or len(set(seqs)) != len(seqs):
+            raise ValueError("one count per sequence, each sequence once")
+        # what each needs: new pages, and a page of its own in place of a shared one.  When all sharers of a
+        # page extend in one call, the last one left keeps it.
+        need, left = 0, {}
+        own = []
+        for s, n in zip(seqs, counts):
+            self._known(s)
+            if n < 0:
+                raise ValueError("counts must be >= 0")
+            have = len(self.pages[s])
+            copy = False
+            if n > 0 and self.length[s] % self.page_size:
+                last = self.pages[s][-1]
+                refs = left.setdefault(last, self.refs[last])
+                copy = refs > 1
+                if copy:
+                    left[last] = refs - 1
+            own.append(copy)
+            need += -(-(self.length[s] + n) // self.page_size) - have + copy
+        if need > len(self.free_pages):
+            raise OutOfPages(f"{need} pages needed, {len(self.free_pages)} free")
+        copies = []
+        for s, n, copy in zip(seqs, counts, own):
+            pages = self.pages[s]
+            if copy:
+                dst = self.free_pages.pop()
+                copies.append((pages[-1], dst))
+                self.refs[dst] = 1
+                self.refs[pages[-1]] -= 1                       # stays in use: another sequence holds it
+                pages[-1] = dst
+            self.length[s] += n
+            while len(pages) * self.page_size < self.length[s]:
+                page = self.free_pages.pop()
+                self.refs[page] = 1
+                pages.append(page)
+        return copies
+
+    def fork(self, seq: int) -> int:
+        """A new sequence with the same positions, sharing ``seq``'s pages."""
+        self._known(seq)
+        new = self.add()
+        self.pages[new], self.length[new] = list(self.pages[seq]), self.length[seq]
+        for p in self.pages[new]:
+            self.refs[p] += 1
+        return new
+
+    def free(self, seq: int) -> None:
+        """Ends a sequence; pages no other sequence shares become free."""
+        self._known(seq)
+        for p in self.pages.pop(seq):
+            self._drop(p)
+        del self.length[seq]
+
+    def compact(self) -> Copies:
+        """Moves the pages in use to [0, pages in use): returns the (source,
+        destination) pages to copy.  No page is both a source and a
+        destination."""
+        used = sum(r > 0 for r in self.refs)
+        holes = [p for p in range(used) if self.refs[p] == 0]
+        moved = [p for p in range(used, self.n_pages) if self.refs[p] > 0]
+        to = dict(zip(moved, holes))
+        for src, dst in to.items():
+            self.refs[dst], self.refs[src] = self.refs[src], 0
+        for s, pages in self.pages.items():
+            self.pages[s] = [to.get(p, p) for p in pages]
+        self.free_pages = list(range(self.n_pages - 1, used - 1, -1))
+        return list(to.items())
+
+
+@dataclass
+class Step:
+    """One step's sequences as the calls take them: packed offsets of the new
+    tokens, the lengths before and after, and the block table."""
+    seqs: List[int]
+    cu_seqlens: torch.Tensor     # [B + 1] of the new tokens
+    pos0: torch.Tensor           # [B] positions before the step
+    lengths: torch.Tensor        # [B] positions with the step's
+    block_table: torch.Tensor    # [B, max_pages]
+    max_new: int                 # longest of the new segments
+
+
+class PagedCache:
+    """Keys and values of many sequences in pages on the device."""
+
+    def __init__(self, n_pages: int, page_size: int, H_kv: int, d: int, dtype: torch.dtype = torch.bfloat16,
+                 device="cuda"):
+        shape = (n_pages, H_kv, page_size, d)
+        self.table = PageTable(n_pages, page_size)
+        self.pages = nt.KVPages(torch.empty(shape, dtype=dtype, device=device),
+                                torch.empty(shape, dtype=dtype, device=device))
+        self._workspace: Optional[torch.Tensor] = None
+
+    def add(self) -> int:
+        return self.table.add()
+
+    def fork(self, seq: int) -> int:
+        return self.table.fork(seq)
+
+    def free(self, seq: int) -> None:
+        self.table.free(seq)
+
+    def _copy(self, copies: Copies, stream=None) -> None:
+        if copies:
+            src, dst = torch.tensor(copies, dtype=torch.int32).T.contiguous()
+            nt.nt_paged_copy(self.pages, src, dst, stream=stream)
+
+    def compact(self, stream=None) -> None:
+        """The pages in use moved to the front of the pool.  Steps taken
+        before hold the old places."""
+        self._copy(self.table.compact(), stream)
+
+    def step(self, seqs: Sequence[int], counts: Sequence[int], stream=None) -> Step:
+        """Makes room for counts[i] new tokens of seqs[i] and returns the
+        step's device arrays (one copy from pinned memory).  Counts of 1 make
+        a decoding step, larger ones a prefill."""
+        copies = self.table.extend(seqs, counts)
+        self._copy(copies, stream)
+        B = len(seqs)
+        lists = [self.table.pages[s] for s in seqs]
+        after = [self.table.length[s] for s in seqs]
+        width = max([len(p) for p in lists] + [1])
+        cu = [0]
+        for n in counts:
+            cu.append(cu[-1] + n)
+        flat = cu + [a - n for a, n in zip(after, counts)] + after
+        head = len(flat) + (-len(flat)) % 4
+        flat += [0] * (head - len(flat))
+        for p in lists:
+            flat += p + [-1] * (width - len(p))
+        host = torch.tensor(flat, dtype=torch.int32).pin_memory()
+        dev = self.pages.device
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            arr = host.to(dev, non_blocking=True)
+        return Step(list(seqs), arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
+                    arr[head:].view(B, width), max(list(counts) + [0]))
+
+    def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+        """The step's new keys and values, packed (tokens, H_kv, d)."""
+        nt.nt_paged_write(self.pages, k, v, step.cu_seqlens, step.block_table, pos0=step.pos0, stream=stream)
+
+    def attend(self, step: Step, q: torch.Tensor, scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """One query token per sequence, q (B, H, d), over all its positions.
+        Calls on several streams at once need caches (and so workspaces) of
+        their own."""
+        need = nt.nt_paged_attn_workspace_bytes(q.shape[1], self.pages.H_kv, self.pages.d)
+        if self._workspace is None or self._workspace.numel() < need:
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
+        return nt.nt_paged_attn(self.pages, q, step.block_table, step.lengths, scale=scale,
+                                workspace=self._workspace, stream=stream)[0]
