@@ -246,19 +246,33 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnProblem 
   const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = row; i < n; i += kRows) {
-    const int64_t s = (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * stride + g;
-    const float2 ml = *reinterpret_cast<const float2*>(part.ml + s * 2);
-    const float4 v = *reinterpret_cast<const float4*>(part.o + s * D + 4 * lane);
-    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - base), fi = exp2f(ml.x - base);
-    m = mn;
-    l = l * f + ml.y * fi;
-    o.x = o.x * f + v.x * fi;
-    o.y = o.y * f + v.y * fi;
-    o.z = o.z * f + v.z * fi;
-    o.w = o.w * f + v.w * fi;
+  // kBatch partials' loads at a time: one latency for up to kBatch * kRows of them
+  constexpr int kBatch = 4;
+  for (int i0 = row; i0 < n; i0 += kBatch * kRows) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kRows;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const int64_t s = (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * stride + g;
+        ml[k] = *reinterpret_cast<const float2*>(part.ml + s * 2);
+        v[k] = *reinterpret_cast<const float4*>(part.o + s * D + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float mn = fmaxf(m, ml[k].x), base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m - base), fi = exp2f(ml[k].x - base);
+      m = mn;
+      l = l * f + ml[k].y * fi;
+      o.x = o.x * f + v[k].x * fi;
+      o.y = o.y * f + v[k].y * fi;
+      o.z = o.z * f + v[k].z * fi;
+      o.w = o.w * f + v[k].w * fi;
+    }
   }
   red[row][lane] = o;
   if (lane == 0) {

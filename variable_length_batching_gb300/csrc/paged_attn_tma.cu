@@ -724,8 +724,7 @@ cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s)
                    i ? p.pool.v : p.pool.k, 4, dims, strides, box))
       return cudaErrorInvalidValue;
   const int ctas = min(sm_count(), kPagedMaxCtas);
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_tma_kernel<T, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmem);
+  cudaError_t e = allow_smem_once<paged_attn_tma_kernel<T, D, HP>>(C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_attn_tma_kernel<T, D, HP>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[0], maps[1], a);
   if (e != cudaSuccess || a.whole) return e;

@@ -13,6 +13,22 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWriteTokens = 32;      // tokens a CTA of the write takes, at most
 
+// Division of x < 2^22 by a constant: floor(x m / 2^s), m = ceil(2^s / d), is
+// exact while x (m d - 2^s) < 2^s, and m d - 2^s < d <= 2^21.
+struct Divisor {
+  uint32_t d, m;
+  int s;
+  __host__ explicit Divisor(uint32_t d_ = 1) : d(d_), m(0), s(0) {
+    if (d > (1u << 21)) return;          // m = 0: divide
+    while ((1u << s) < d) ++s;
+    s += 22;                             // d 2^22 <= 2^s: x (m d - 2^s) < 2^22 d <= 2^s
+    m = (uint32_t)(((1ull << s) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t x) const {
+    return m && x < (1u << 22) ? (uint32_t)((uint64_t)x * m >> s) : x / d;
+  }
+};
+
 struct WriteArgs {
   const uint8_t* src[2];              // k, v
   uint8_t* pool[2];
@@ -20,6 +36,7 @@ struct WriteArgs {
   int64_t T;
   int n_pages, page_size, H, row_bytes, B, max_pages;
   int tokens;                         // tokens a CTA takes
+  Divisor by_words, by_row;           // 16-byte words of a token's keys, of a row
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* table;
@@ -43,11 +60,11 @@ __device__ __forceinline__ int64_t write_offset(const WriteArgs& a, int64_t t, i
   return off;
 }
 
-// A warp copies a token's keys, then its values: 16 bytes a lane, kUnroll
-// loads in flight.  The rows of a token are contiguous at the source; each
-// head's row goes to its own place in the page.
+// The rows of a token are contiguous at the source; each head's row goes to
+// its own place in the page.  The CTA's keys, then its values, are one run of
+// 16-byte words over its threads, kUnroll loads in flight: 24 KB per CTA.
 __global__ void __launch_bounds__(kThreads) paged_write_kernel(const WriteArgs a) {
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = 6;
   __shared__ int64_t dst[kWriteTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
@@ -64,28 +81,27 @@ __global__ void __launch_bounds__(kThreads) paged_write_kernel(const WriteArgs a
       dst[i] = write_offset(a, t0 + i, segment_of_thread(a.cu, a.B, t0 + i));
   }
   __syncthreads();
-  const int row_words = a.row_bytes / 16, words = a.H * row_words;
+  const uint32_t words = a.H * (a.row_bytes / 16), total = 2 * n * words;
   const int64_t head_bytes = (int64_t)a.page_size * a.row_bytes;
-  // units of kUnroll x 32 words of one side of one token, over the warps
-  const int per = (words + 32 * kUnroll - 1) / (32 * kUnroll), units = n * 2 * per;
-  for (int u = warp; u < units; u += kThreads / 32) {
-    const int tok = u / (2 * per), rest = u - tok * 2 * per;
-    const int sd = rest >= per, w0 = (rest - sd * per) * 32 * kUnroll + lane;
-    const int64_t off = dst[tok];
-    if (off < 0) continue;
-    const uint8_t* src = a.src[sd] + (t0 + tok) * a.stride[sd];
-    uint8_t* out = a.pool[sd] + off;
+  for (uint32_t e0 = threadIdx.x; e0 < total; e0 += kThreads * kUnroll) {
     uint4 x[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      if (w0 + 32 * k < words) x[k] = *reinterpret_cast<const uint4*>(src + (int64_t)(w0 + 32 * k) * 16);
+    uint8_t* to[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int w = w0 + 32 * k;
-      if (w >= words) continue;
-      const int h = w / row_words, c = w - h * row_words;
-      *reinterpret_cast<uint4*>(out + h * head_bytes + c * 16) = x[k];
+      const uint32_t e = e0 + k * kThreads;
+      to[k] = nullptr;
+      if (e >= total) continue;
+      const int sd = e >= total / 2;
+      const uint32_t r = e - (sd ? total / 2 : 0);
+      const uint32_t tok = a.by_words.div(r), w = r - tok * words;
+      const uint32_t h = a.by_row.div(w), c = w - h * (a.row_bytes / 16);
+      if (dst[tok] < 0) continue;
+      x[k] = *reinterpret_cast<const uint4*>(a.src[sd] + (t0 + tok) * a.stride[sd] + (int64_t)w * 16);
+      to[k] = a.pool[sd] + dst[tok] + h * head_bytes + c * 16;
     }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (to[k]) *reinterpret_cast<uint4*>(to[k]) = x[k];
   }
 }
 
@@ -153,9 +169,13 @@ cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stri
   a.pos0 = pos0;
   a.table = table;
   a.status = status;
-  // one token per CTA until that fills the SMs four times
+  a.by_words = Divisor(p.H * (p.row_bytes / 16));
+  a.by_row = Divisor(p.row_bytes / 16);
+  // one token per CTA until that fills the SMs four times; at most 2^22 words
   a.tokens = 1;
-  while (a.tokens < kWriteTokens && T >= (int64_t)sm_count() * 4 * a.tokens * 2) a.tokens <<= 1;
+  while (a.tokens < kWriteTokens && T >= (int64_t)sm_count() * 4 * a.tokens * 2 &&
+         (int64_t)a.by_words.d * a.tokens * 4 <= (1 << 22))
+    a.tokens <<= 1;
   return launch_pdl(paged_write_kernel, dim3((unsigned)((T + a.tokens - 1) / a.tokens)), dim3(kThreads), 0, s, a);
 }
 

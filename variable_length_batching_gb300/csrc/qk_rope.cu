@@ -549,12 +549,13 @@ int group_lanes(int d) {
 
 template <typename T, int LP, bool kInter>
 cudaError_t run(const Args& a, bool bwd, int grid, cudaStream_t s) {
-  auto kern = bwd ? rope_bwd_kernel<T, LP, kInter> : rope_fwd_kernel<T, LP, kInter>;
-  const size_t smem = bwd ? RingBwd<T>::kBytes + (a.partial ? (size_t)kWarps * 2 * a.d * sizeof(float) : 0)
-                          : Ring<T>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static_assert(Ring<T>::kBytes <= 48 * 1024, "needs no opt-in");
+  if (!bwd) return launch_pdl(rope_fwd_kernel<T, LP, kInter>, dim3(grid), dim3(kThreads), Ring<T>::kBytes, s, a);
+  const size_t sums = (size_t)kWarps * 2 * sizeof(float);         // per column
+  const cudaError_t e = allow_smem_once<rope_bwd_kernel<T, LP, kInter>>(RingBwd<T>::kBytes + sums * 16 * LP);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+  return launch_pdl(rope_bwd_kernel<T, LP, kInter>, dim3(grid), dim3(kThreads),
+                    RingBwd<T>::kBytes + (a.partial ? sums * a.d : 0), s, a);
 }
 
 template <typename T, bool kInter>
@@ -598,8 +599,9 @@ cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* w
   // tokens' angles.  (Unit counts stay below 2^31: a unit is 512 elements of
   // q or k at least, and 2^31 of those are 2 TB.)
   const int most = max(p.H_q, p.H_k);
+  const bool one_round = groups * (p.H_q + p.H_k) <= warps;        // one head to a unit
   int64_t best = 0;
-  for (int hu = 1; hu <= most; hu = hu == 64 ? max(most, 65) : hu + 1) {
+  for (int hu = 1; hu <= (one_round ? min(most, 1) : most); hu = hu == 64 ? max(most, 65) : hu + 1) {
     const int64_t units = groups * ((p.H_q + hu - 1) / hu + (p.H_k + hu - 1) / hu);
     const int64_t cost = (units + warps - 1) / warps * (hu + 3);
     if (units > 0x7fffffffLL || (best && cost >= best)) continue;

@@ -726,14 +726,14 @@ def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns:
     qp, qs = _tokens(q, index, dt, "q")
     kp, ks = _tokens(k, index, dt, "k")
     if q_out is None and q is not None:
-        q_out = torch.empty((T, H_q, d), dtype=dt, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qo, qos = q_out.data_ptr(), H_q * d
     else:
         if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
             raise ValueError("q_out must have q's shape")
         qo, qos = _tokens(q_out, index, dt, "q_out")
     if k_out is None and k is not None:
-        k_out = torch.empty((T, H_k, d), dtype=dt, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         ko, kos = k_out.data_ptr(), H_k * d
     else:
         if (k is None) != (k_out is None) or (k is not None and k.shape != k_out.shape):
@@ -782,10 +782,10 @@ def nt_qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.T
     uq, uqs = _tokens(dq_out, index, dt, "dq_out")
     uk, uks = _tokens(dk_out, index, dt, "dk_out")
     if dq_out is not None:
-        dq = torch.empty((T, H_q, d), dtype=dt, device=dev)
+        dq = torch.empty_like(dq_out, memory_format=torch.contiguous_format)
         dqp = dq.data_ptr()
     if dk_out is not None:
-        dk = torch.empty((T, H_k, d), dtype=dt, device=dev)
+        dk = torch.empty_like(dk_out, memory_format=torch.contiguous_format)
         dkp = dk.data_ptr()
     if workspace is not None:
         wsp, ws_bytes = _on(workspace, index, None, "workspace"), workspace.numel() * workspace.element_size()
@@ -871,7 +871,7 @@ def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, le
     qp, qs = _tokens(q, index, dt, "q")
     tab, max_pages = _table(block_table, B, index)
     if out is None:
-        out = torch.empty((B, H, d), dtype=dt, device=pages.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if want_lse and lse is None:
