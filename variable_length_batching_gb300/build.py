@@ -1,4 +1,5 @@
-"""In-tree build of ``libnt.so`` for sm_103a with nvcc.
+"""In-tree build of ``libnt.so`` for sm_103a with nvcc, and of the compiled
+part of its Python binding (``_nt_binding``, host code only) with g++.
 
 Each ``csrc/*.cu`` translation unit compiles in parallel to an object under
 ``_build/``; the objects link into ``libnt.so`` beside this file with the
@@ -15,6 +16,9 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +26,8 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnt.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_nt_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 STAMP = os.path.join(BUILD, "stamp.txt")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,8 +52,9 @@ def _digest() -> str:
     h = hashlib.sha256()
     h.update(platform.machine().encode())
     h.update(" ".join(CFLAGS).encode())
+    h.update(f"{sys.version} {torch.__version__}".encode())
     files = sources() + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
-    files.append(os.path.join(INCLUDE, "nt.h"))
+    files += [BINDING_SRC, os.path.join(INCLUDE, "nt.h")]
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
@@ -64,18 +71,35 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _compile_binding() -> None:
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libnt.so; returns its path."""
+    """Compile and link libnt.so and the binding; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(STAMP):
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(STAMP):
         with open(STAMP) as f:
             if f.read().strip() == digest:
                 return LIB
     srcs = sources()
-    jobs = min(len(srcs), max(1, os.cpu_count() or 1))
+    jobs = min(len(srcs) + 1, max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, extra_flags), srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH_FLAGS + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

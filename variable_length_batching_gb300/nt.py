@@ -4,6 +4,8 @@ Argument marshalling only: torch tensors supply device memory and the
 current CUDA stream; every step of the block and of varlen attention runs in
 the library's kernels.  Functions keep the C names.  If ``libnt.so`` is
 missing or a call fails, an exception is raised -- there is no other path.
+The calls of a decoding step (norm and rope, paged write, copy and attention)
+pass their arguments through a compiled module, the others through ctypes.
 """
 from __future__ import annotations
 
@@ -620,94 +622,28 @@ def nt_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", fa
     return t if device is None else t.to(device)
 
 
-def _refuse(t, index: int, dtype, name: str):
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    raise ValueError(f"{name} must be contiguous")
+_binding = None
 
 
-def _on(t: Optional[torch.Tensor], index: int, dtype, name: str):
-    """Address of a contiguous tensor that must live on CUDA device ``index``
-    (None -> NULL)."""
-    if t is None:
-        return None
-    if t.get_device() != index or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
-        _refuse(t, index, dtype, name)
-    return t.data_ptr()
+def _calls():
+    """The compiled marshalling of the calls below (``csrc/binding.cpp``),
+    bound to the loaded library; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        try:
+            from . import _nt_binding as b
+        except ImportError as e:
+            raise RuntimeError("the binding is not built; run `python -m variable_length_batching_gb300.build`") from e
+        b.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "nt_qk_norm_rope", "nt_qk_norm_rope_bwd", "nt_qk_norm_rope_bwd_workspace_bytes", "nt_paged_write",
+            "nt_paged_copy", "nt_paged_attn", "nt_paged_attn_workspace_bytes")))
+        _binding = b
+    return _binding
 
 
-def _tokens(t: Optional[torch.Tensor], index: int, dtype, name: str):
-    """(address, token stride) of packed tokens (T, H, d) whose heads are
-    contiguous within a token; tokens may be any stride apart."""
-    if t is None:
-        return None, 0
-    if t.get_device() != index or t.dtype is not dtype:
-        _refuse(t, index, dtype, name)
-    T, H, d = t.shape
-    if t.is_contiguous():
-        return t.data_ptr(), H * d
-    stride, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), stride if T > 1 else H * d
-
-
-def _cuda_index(t: torch.Tensor) -> int:
-    i = t.get_device()
-    if i < 0:
-        raise ValueError("expected CUDA tensors")
-    return i
-
-
-def _run(name: str, index: int, stream, *args):
-    """One call of the library on CUDA device ``index``, which is made current
-    while it runs, on its current stream (or ``stream``)."""
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        st = getattr(_lib or lib(), name)(*args, s)
-    else:
-        with torch.cuda.device(index):
-            st = getattr(_lib or lib(), name)(*args, s)
-    if st != 0:
-        _check(st, name)
-
-
-def _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma):
-    """Shapes, device and position arguments of the rope calls."""
-    t = q if q is not None else k
-    if t is None:
-        raise ValueError("q or k is needed")
-    if t.dim() != 3:
-        raise ValueError("q and k must be (tokens, heads, d)")
-    T, _, d = t.shape
-    H_q = 0 if q is None else q.shape[1]
-    H_k = 0
-    if k is not None:
-        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != d:
-            raise ValueError("q and k must share their tokens and head width")
-        H_k = k.shape[1]
-    B = 0
-    if positions is not None:
-        if cu_seqlens is not None or pos0 is not None:
-            raise ValueError("give positions or cu_seqlens (with pos0), not both")
-        if positions.numel() != T:
-            raise ValueError("one position per token")
-    elif cu_seqlens is not None:
-        B = cu_seqlens.numel() - 1
-        if B < 0:
-            raise ValueError("cu_seqlens has B + 1 entries")
-    if pos0 is not None and (cu_seqlens is None or pos0.numel() != B):
-        raise ValueError("pos0 is one start per cu_seqlens segment")
-    if (q_gamma is not None and q_gamma.numel() != d) or (k_gamma is not None and k_gamma.numel() != d):
-        raise ValueError("gammas must have d entries")
-    index = _cuda_index(t)
-    i32 = torch.int32
-    tail = (_on(cu_seqlens, index, i32, "cu_seqlens"), B, _on(pos0, index, i32, "pos0"),
-            _on(positions, index, i32, "positions"), _on(turns, index, torch.int64, "turns"),
-            0 if turns is None else 2 * turns.numel())
-    return T, H_q, H_k, d, index, t.dtype, tail
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns: Optional[torch.Tensor],
@@ -722,27 +658,11 @@ def nt_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns:
     segment, or are given as ``positions``.  ``turns`` from nt_rope_turns
     sets the rotated columns (None: norm only).  q and k may be slices of a
     fused projection; ``q_out=q, k_out=k`` works in place."""
-    T, H_q, H_k, d, index, dt, tail = _rope_args(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
-    qp, qs = _tokens(q, index, dt, "q")
-    kp, ks = _tokens(k, index, dt, "k")
-    if q_out is None and q is not None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        qo, qos = q_out.data_ptr(), H_q * d
-    else:
-        if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
-            raise ValueError("q_out must have q's shape")
-        qo, qos = _tokens(q_out, index, dt, "q_out")
-    if k_out is None and k is not None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        ko, kos = k_out.data_ptr(), H_k * d
-    else:
-        if (k is None) != (k_out is None) or (k is not None and k.shape != k_out.shape):
-            raise ValueError("k_out must have k's shape")
-        ko, kos = _tokens(k_out, index, dt, "k_out")
-    f32 = torch.float32
-    _run("nt_qk_norm_rope", index, stream, _dtype(q if q is not None else k), qp, qs, kp, ks, T, H_q, H_k, d,
-         _on(q_gamma, index, f32, "q_gamma"), _on(k_gamma, index, f32, "k_gamma"), eps, *tail,
-         1 if interleaved else 0, rot_scale, qo, qos, ko, kos)
+    st, q_out, k_out = (_binding or _calls()).qk_norm_rope(q, k, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma,
+                                                           eps, interleaved, rot_scale, q_out, k_out,
+                                                           _handle(stream))
+    if st:
+        _check(st, "nt_qk_norm_rope")
     return q_out, k_out
 
 
@@ -761,40 +681,11 @@ def nt_qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.T
     (dq, dk, dq_gamma, dk_gamma), the gammas' in fp32, None where there is no
     input.  ``q`` and ``k`` are the forward's inputs, needed for the sides
     that have a gamma."""
-    T, H_q, H_k, d, index, dt, tail = _rope_args(dq_out, dk_out, turns, cu_seqlens, positions, pos0, q_gamma, k_gamma)
-    f32 = torch.float32
-    dev = (dq_out if dq_out is not None else dk_out).device
-    dq = dk = dqg = dkg = None
-    qp = kp = dqp = dkp = dqgp = dkgp = wsp = None
-    qs = ks = ws_bytes = 0
-    if q_gamma is not None:
-        if q is None or dq_out is None or q.shape != dq_out.shape:
-            raise ValueError("q's norm needs q and its upstream gradient, of one shape")
-        qp, qs = _tokens(q, index, dt, "q")
-        dqg = torch.empty(d, dtype=f32, device=dev)
-        dqgp = dqg.data_ptr()
-    if k_gamma is not None:
-        if k is None or dk_out is None or k.shape != dk_out.shape:
-            raise ValueError("k's norm needs k and its upstream gradient, of one shape")
-        kp, ks = _tokens(k, index, dt, "k")
-        dkg = torch.empty(d, dtype=f32, device=dev)
-        dkgp = dkg.data_ptr()
-    uq, uqs = _tokens(dq_out, index, dt, "dq_out")
-    uk, uks = _tokens(dk_out, index, dt, "dk_out")
-    if dq_out is not None:
-        dq = torch.empty_like(dq_out, memory_format=torch.contiguous_format)
-        dqp = dq.data_ptr()
-    if dk_out is not None:
-        dk = torch.empty_like(dk_out, memory_format=torch.contiguous_format)
-        dkp = dk.data_ptr()
-    if workspace is not None:
-        wsp, ws_bytes = _on(workspace, index, None, "workspace"), workspace.numel() * workspace.element_size()
-    elif dqg is not None or dkg is not None:
-        workspace = torch.empty(nt_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
-        wsp, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _run("nt_qk_norm_rope_bwd", index, stream, _dtype(dq_out if dq_out is not None else dk_out), uq, uqs, uk, uks,
-         qp, qs, kp, ks, T, H_q, H_k, d, _on(q_gamma, index, f32, "q_gamma"), _on(k_gamma, index, f32, "k_gamma"),
-         eps, *tail, 1 if interleaved else 0, rot_scale, dqp, H_q * d, dkp, H_k * d, dqgp, dkgp, wsp, ws_bytes)
+    st, dq, dk, dqg, dkg = (_binding or _calls()).qk_norm_rope_bwd(dq_out, dk_out, turns, q, k, cu_seqlens, positions,
+                                                                   pos0, q_gamma, k_gamma, eps, interleaved,
+                                                                   rot_scale, workspace, _handle(stream))
+    if st:
+        _check(st, "nt_qk_norm_rope_bwd")
     return dq, dk, dqg, dkg
 
 
@@ -805,18 +696,16 @@ class KVPages:
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must share the shape (n_pages, H_kv, page_size, d), dtype and device")
+        if not k.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous")
         self.k, self.v = k, v
-        self.device, self.dtype, self.index = k.device, k.dtype, _cuda_index(k)
+        self.device, self.dtype, self.index = k.device, k.dtype, k.get_device()
         self.n_pages, self.H_kv, self.page_size, self.d = k.shape
-        self.c = nt_kv_pages(_on(k, self.index, k.dtype, "k") or None, _on(v, self.index, k.dtype, "v") or None,
-                             self.n_pages, self.page_size, self.H_kv, self.d, _dtype(k))
-        self.ref = ctypes.byref(self.c)
-
-
-def _table(block_table: torch.Tensor, B: int, index: int):
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be (B = {B}, max_pages)")
-    return _on(block_table, index, torch.int32, "block_table"), block_table.shape[1]
+        self.c = nt_kv_pages(k.data_ptr() or None, v.data_ptr() or None, self.n_pages, self.page_size, self.H_kv,
+                             self.d, _dtype(k))
+        self.address = ctypes.addressof(self.c)
 
 
 def nt_paged_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -824,30 +713,18 @@ def nt_paged_write(pages: KVPages, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     """Keys and values of packed tokens (T, H_kv, d) into their sequences'
     pages: token t of ``cu_seqlens`` segment b goes to position
     pos0[b] + t - cu[b] (``pos0`` None: 0) of row b of ``block_table``."""
-    index, dt = pages.index, pages.dtype
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != pages.H_kv or k.shape[2] != pages.d:
-        raise ValueError("k and v must be (T, H_kv, d) of the pages")
-    B = cu_seqlens.numel() - 1
-    if pos0 is not None and pos0.numel() != B:
-        raise ValueError("pos0 is one start per cu_seqlens segment")
-    kp, ks = _tokens(k, index, dt, "k")
-    vp, vs = _tokens(v, index, dt, "v")
-    tab, max_pages = _table(block_table, B, index)
-    i32 = torch.int32
-    _run("nt_paged_write", index, stream, pages.ref, kp, ks, vp, vs, k.shape[0],
-         _on(cu_seqlens, index, i32, "cu_seqlens"), B, _on(pos0, index, i32, "pos0"), tab, max_pages)
+    st, = (_binding or _calls()).paged_write(pages.address, pages.index, k, v, cu_seqlens, block_table, pos0,
+                                             _handle(stream))
+    if st:
+        _check(st, "nt_paged_write")
 
 
 def nt_paged_copy(pages: KVPages, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Page src[i] copied over page dst[i] (int32 HOST tensors): no page
     twice in dst, none in both."""
-    if src.is_cuda or dst.is_cuda:
-        raise ValueError("src and dst are host tensors")
-    if src.dtype is not torch.int32 or dst.dtype is not torch.int32 or src.dim() != 1 or src.shape != dst.shape:
-        raise ValueError("src and dst must be int32, one entry per copy")
-    if not (src.is_contiguous() and dst.is_contiguous()):
-        raise ValueError("src and dst must be contiguous")
-    _run("nt_paged_copy", pages.index, stream, pages.ref, src.data_ptr(), dst.data_ptr(), src.numel())
+    st, = (_binding or _calls()).paged_copy(pages.address, pages.index, src, dst, _handle(stream))
+    if st:
+        _check(st, "nt_paged_copy")
 
 
 def nt_paged_attn_workspace_bytes(H: int, H_kv: int, d: int) -> int:
@@ -862,29 +739,10 @@ def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, le
     lengths[b] positions of its paged cache; H a multiple of H_kv.  Returns
     (o, lse [H, B] or None).  ``workspace``: nt_paged_attn_workspace_bytes()
     bytes (None allocates them per call)."""
-    index, dt, d = pages.index, pages.dtype, pages.d
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q must be (B, H, d) with the pages' d")
-    B, H, _ = q.shape
-    if lengths.numel() != B:
-        raise ValueError("one length per sequence")
-    qp, qs = _tokens(q, index, dt, "q")
-    tab, max_pages = _table(block_table, B, index)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if want_lse and lse is None:
-        lse = torch.empty((H, B), dtype=torch.float32, device=pages.device)
-    if lse is not None and (lse.dim() != 2 or lse.shape[0] != H or lse.shape[1] != B):
-        raise ValueError("lse must be (H, B)")
-    if workspace is None:
-        workspace = torch.empty(nt_paged_attn_workspace_bytes(H, pages.H_kv, d), dtype=torch.uint8,
-                                device=pages.device)
-    _run("nt_paged_attn", index, stream, pages.ref, qp, qs, B, H, tab, max_pages,
-         _on(lengths, index, torch.int32, "lengths"), d ** -0.5 if scale is None else scale,
-         _on(out, index, dt, "out"), _on(lse, index, torch.float32, "lse"), _on(workspace, index, None, "workspace"),
-         workspace.numel() * workspace.element_size())
+    st, out, lse = (_binding or _calls()).paged_attn(pages.address, pages.index, q, block_table, lengths, scale, out,
+                                                     lse, want_lse, workspace, _handle(stream))
+    if st:
+        _check(st, "nt_paged_attn")
     return out, lse
 
 
