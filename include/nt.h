@@ -709,7 +709,7 @@ nt_status nt_qk_norm_rope_bwd(nt_dtype dtype, const void* dq_out, int64_t dq_out
  * is in the callers' block tables, [B, max_pages] int32 on the device:
  * position x of sequence b is row x % page_size of page
  * d_block_table[b * max_pages + x / page_size].  Sequences may share pages.
- * Entries behind a sequence's last position are never read.
+ * Entries behind a sequence's last position are never used.
  *   n_pages >= 0, page_size in [1, 65536], H_kv >= 1, d * element size a
  *   multiple of 16; k, v 16-byte aligned (NULL if n_pages = 0).
  */

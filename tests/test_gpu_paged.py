@@ -117,8 +117,11 @@ def test_captured_copy_keeps_its_list(nt):
 
 # ---- attention --------------------------------------------------------------
 
-def _attn_case(nt, lens, page, H, Hk, d, dtype, seed=0, scale=None, edit=None, want_lse=True):
+def _attn_case(nt, lens, page, H, Hk, d, dtype, seed=0, scale=None, edit=None, want_lse=True, wide=0):
+    """``wide``: unused columns of the block table, which say how long the
+    contexts may get (the call chooses its kernel by that)."""
     kp, vp, table = make_pool(lens, page, Hk, d, dtype, seed)
+    table = torch.nn.functional.pad(table, (0, wide), value=-1)
     q = (2 * _rand(seed + 100, len(lens), H, d)).to(dtype)
     if edit:
         edit(kp, vp, table, q)
@@ -163,20 +166,46 @@ SHAPES = [  # lens, page, H, Hk, d
 ]
 
 
+@pytest.mark.parametrize("room", ["exact", "1024", "wide"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("shape", SHAPES)
-def test_attn(nt, shape, dtype):
+def test_attn(nt, shape, dtype, room):
+    """Every shape with a table as wide as its longest context, and with
+    wider ones."""
+    lens, page, H, Hk, d = shape
+    wide = {"exact": 0, "1024": max(0, 1024 // page - -(-max(lens) // page)), "wide": -(-5000 // page)}[room]
+    inputs, o, lse = _attn_case(nt, lens, page, H, Hk, d, dtype, wide=wide)
+    _check(inputs, o, lse, lens, dtype)
+
+
+# contexts of a few positions, where a table of few pages is all there is
+SHORT = [  # lens, page, H, Hk, d
+    ([1, 0, 3, 16, 17, 128, 127, 64], 16, 12, 12, 64),
+    ([5, 33, 0, 0, 90], 8, 32, 2, 128),              # 16 heads to a key head
+    ([5, 33, 0, 0, 90], 24, 48, 2, 32),              # 24
+    ([128] * 3, 128, 7, 1, 64),
+    ([9, 100], 1, 3, 1, 64),                         # pages of one position
+    ([9, 100, 31], 5, 10, 5, 32),
+    ([1, 2, 3, 4] * 300, 2, 4, 2, 64),               # more items than warps
+    ([0] * 5, 16, 8, 1, 128),
+    ([77, 1, 120, 16, 15], 40, 6, 3, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", SHORT)
+def test_attn_short(nt, shape, dtype):
     lens, page, H, Hk, d = shape
     inputs, o, lse = _attn_case(nt, lens, page, H, Hk, d, dtype)
     _check(inputs, o, lse, lens, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("page", [16, 12])
-def test_attn_nothing_behind_the_end(nt, dtype, page):
+@pytest.mark.parametrize("page,lens,wide", [(16, [1, 5, 17, 70, 131], 400), (12, [1, 5, 17, 70, 131], 400),
+                                            (16, [1, 5, 17, 70, 111], 0), (12, [1, 5, 17, 70, 111], 0)])
+def test_attn_nothing_behind_the_end(nt, dtype, page, lens, wide):
     """NaN and infinities in the cache's rows behind the last position, in
     spare pages and in the table's unused entries reach no output."""
-    lens = [1, 5, 17, 70, 131]
 
     def edit(kp, vp, table, q):
         used = torch.zeros(kp.shape[0], kp.shape[2], dtype=torch.bool)
@@ -189,7 +218,7 @@ def test_attn_nothing_behind_the_end(nt, dtype, page):
         vp[mask & (torch.arange(kp.shape[3]) % 2 == 0)] = math.nan
         table[table < 0] = 1 << 30
 
-    inputs, o, lse = _attn_case(nt, lens, page, 8, 2, 64, dtype, edit=edit)
+    inputs, o, lse = _attn_case(nt, lens, page, 8, 2, 64, dtype, edit=edit, wide=wide)
     _check(inputs, o, lse, lens, dtype)
 
 
@@ -234,12 +263,14 @@ def test_attn_empty_batch(nt):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length"])
-def test_attn_flags_bad_tables(nt, what, dtype):
+@pytest.mark.parametrize("page", [16, 12])
+@pytest.mark.parametrize("scale_up", [1, 30])
+def test_attn_flags_bad_tables(nt, what, dtype, page, scale_up):
     """A page outside the pool reads as zeros, a length beyond the table as
     the table's, a negative one as 0; each is flagged and the other sequences
     keep their results."""
-    lens = [40, 20]
-    kp, vp, table = make_pool(lens, 16, 1, 64, dtype, 3)
+    lens = [40 * scale_up, 20 * scale_up]
+    kp, vp, table = make_pool(lens, page, 1, 64, dtype, 3)
     q = _rand(4, 2, 2, 64, dtype=dtype)
     t2, l2 = table.clone(), list(lens)
     if what == "page":
@@ -247,7 +278,7 @@ def test_attn_flags_bad_tables(nt, what, dtype):
     elif what == "negative page":
         t2[0, 1] = -5
     elif what == "length":
-        l2[0] = 49
+        l2[0] = table.shape[1] * page + 1
     else:
         l2[0] = -1
     pages = nt.KVPages(kp.to(DEV), vp.to(DEV))
@@ -257,16 +288,17 @@ def test_attn_flags_bad_tables(nt, what, dtype):
     assert ei.value.status == 6
     ro, _, mag, cond = paged_attn(kp, vp, q, table, lens)
     err = (o.double().cpu() - ro).abs()[1]
-    assert bool((err <= attn_bound(ro, mag, cond, 40, dtype)[1] + 1e-38).all())
+    assert bool((err <= attn_bound(ro, mag, cond, max(lens), dtype)[1] + 1e-38).all())
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attn_captured_follows_lengths(nt, dtype):
+@pytest.mark.parametrize("cap", [900, 112])
+def test_attn_captured_follows_lengths(nt, dtype, cap):
     """A captured call replayed with other lengths and queries gives what a
     direct call gives, bit for bit; a second captured call with a workspace
     of its own does too."""
     page, H, Hk, d = 16, 8, 2, 64
-    kp, vp, table = make_pool([900, 900, 900], page, Hk, d, dtype, 1)
+    kp, vp, table = make_pool([cap] * 3, page, Hk, d, dtype, 1)
     pages = nt.KVPages(kp.to(DEV), vp.to(DEV))
     table = table.to(DEV)
     q = torch.zeros(3, H, d, dtype=dtype, device=DEV)
@@ -280,7 +312,7 @@ def test_attn_captured_follows_lengths(nt, dtype):
             outs.append(nt.nt_paged_attn(pages, q, table, lens, workspace=w, want_lse=True))
         graphs.append(g)
     for ls in ([900, 3, 0], [17, 900, 64], [0, 0, 0], [256, 255, 899]):
-        lens.copy_(torch.tensor(ls, dtype=torch.int32))
+        lens.copy_(torch.tensor(ls, dtype=torch.int32).clamp(max=cap))
         q.normal_()
         for w in ws:
             w.fill_(255)

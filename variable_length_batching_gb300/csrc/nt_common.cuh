@@ -423,6 +423,11 @@ constexpr int kPagedMaxCtas = 512;      // CTAs of the split, at most (two parti
 constexpr int kPagedMaxHeads = 16;      // query heads of one item, at most
 size_t paged_attn_workspace_bytes(int G, int d);
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
+// One warp per sequence and key head, for tables of at most kPagedShortKeys
+// positions.
+constexpr int kPagedShortKeys = 128;
+bool paged_attn_short_chosen(nt_dtype dt, const PagedAttnProblem& p);
+cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 // The TMA-fed kernel: pages of a multiple of 8 positions.
 bool paged_attn_tma_supported(const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);

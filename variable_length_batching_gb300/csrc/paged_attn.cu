@@ -359,6 +359,7 @@ cudaError_t launch_paged_join(nt_dtype dt, const PagedAttnProblem& p, int ctas, 
 
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
+  if (paged_attn_short_chosen(dt, p)) return launch_paged_attn_short(dt, p, status, s);
   if (paged_attn_tma_supported(p)) return launch_paged_attn_tma(dt, p, status, s);
   return dt == NT_BF16 ? run_d<bf16>(p, status, s) : run_d<float>(p, status, s);
 }
