@@ -108,11 +108,16 @@ __device__ __forceinline__ bool lane_position(const Args& a, int64_t t, int64_t 
 template <typename T, int LP, bool kInter>
 struct Lane {
   static constexpr int V = 16 / sizeof(T), W = 16 / V;
-  int i, g, col0, step;
+  static constexpr int kRow = LP * 16 * sizeof(T);                // bytes of a row, at most
+  static constexpr int kSide = kRow >= 128 ? 1 : 128 / kRow;      // rows of one token in a step, side by side
+  static constexpr int kTok = 32 / LP / kSide;                    // tokens of a step
+  int i, tok, h_off, col0, step;
   bool on, rotated;
   __device__ __forceinline__ Lane(const Args& a) {
     i = threadIdx.x % LP;
-    g = threadIdx.x % 32 / LP;
+    const int g = threadIdx.x % 32 / LP;
+    tok = g / kSide;
+    h_off = g % kSide;
     on = 16 * i < a.d;
     rotated = 16 * i < a.rot;
     const int first = rotated ? 0 : a.rot, width = rotated ? a.rot : a.d - a.rot;
@@ -156,12 +161,13 @@ struct Lane {
       v[e + 3] = x.w;
     }
   }
-  // copy the lane's words of a row into its ring words, 16 bytes each
+  // copy the lane's words of a row into its ring words, 16 bytes each; x and
+  // y point at its first column
   __device__ __forceinline__ void copy(uint32_t dst, const T* x) const {
 #pragma unroll
     for (int w = 0; w < W; ++w)
       asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
-                   ::"r"(dst + w * kThreads * 16), "l"(x + col(w)) : "memory");
+                   ::"r"(dst + w * kThreads * 16), "l"(x + w * step) : "memory");
   }
   __device__ __forceinline__ void store(T* y, const float (&v)[16]) const {
 #pragma unroll
@@ -174,7 +180,7 @@ struct Lane {
         x = make_uint4(__float_as_uint(v[4 * w]), __float_as_uint(v[4 * w + 1]), __float_as_uint(v[4 * w + 2]),
                        __float_as_uint(v[4 * w + 3]));
       }
-      *reinterpret_cast<uint4*>(y + col(w)) = x;
+      *reinterpret_cast<uint4*>(y + w * step) = x;
     }
   }
 };
@@ -289,54 +295,78 @@ struct Place {
     h = (int)(v - tg * a.parts[sd]) * a.unit_heads;
     h_end = min(h + a.unit_heads, a.side[sd].H);
   }
-  // the next row; true if it is a new unit's (or there is none)
-  __device__ __forceinline__ bool next(const Args& a) {
-    if (++h < h_end) return false;
+  __device__ __forceinline__ void next(const Args& a) {
     u += n;
     set(a);
-    return true;
   }
 };
 
+// How many steps ahead rows are copied: few.  More than about 48 KB in flight
+// on an SM is slower, not faster (the stream's forward with four slots 72 us,
+// three 69; its backward with three 101, two 98).
 template <typename T> struct Ring {          // forward: one row a step
   static constexpr int kWords = sizeof(T);   // 16-byte words of a row per lane
-  static constexpr int kSlots = 8 / sizeof(T);
+  static constexpr int kSlots = sizeof(T) == 2 ? 3 : 2;
   static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
 };
 
+// The inner loops hold everything of a unit in registers and step pointers:
+// with four warps a scheduler, instructions are the next bound (157 a row and
+// lane; 240 with the addresses formed anew each step).
 template <typename T, int LP, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
   using R = Ring<T>;
+  constexpr uint32_t kSlotWords = R::kWords * kThreads;
   extern __shared__ __align__(16) uint4 ring[];
-  constexpr int kTok = 32 / LP;
-  const Lane<T, LP, kInter> me(a);
-  Place at(a), ahead(a);                     // the row in hand, and the row to copy, kSlots further
+  using L = Lane<T, LP, kInter>;
+  constexpr int kTok = L::kTok;
+  const L me(a);
+  Place at(a), ahead(a);                     // the unit in hand, and the unit to copy, kSlots rows further
   pdl_wait();
   pdl_trigger();
-  auto copy = [&](int slot) {
-    if (ahead.more) {
-      const int64_t t = (int64_t)ahead.tg * kTok + me.g;
-      if (me.on && t < a.T) {
-        const Side& p = a.side[ahead.sd];
-        me.copy(tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x),
-                static_cast<const T*>(p.x) + t * p.xs + (int64_t)ahead.h * a.d);
+  const T* px = nullptr;                     // the next row to copy, and how many the unit has left
+  int pn = 0;
+  bool pon = false;
+  auto enter = [&] {
+    if (!ahead.more) return;
+    const Side& p = a.side[ahead.sd];
+    const int64_t t = (int64_t)ahead.tg * kTok + me.tok;
+    pon = me.on && t < a.T;
+    px = static_cast<const T*>(p.x) + t * p.xs + (int64_t)(ahead.h + me.h_off) * a.d + me.col0;
+    pn = ahead.h_end - ahead.h;
+  };
+  enter();
+  uint32_t so = threadIdx.x;                 // this thread's first word of the slot in hand
+  auto copy = [&] {
+    if (pn > 0) {
+      if (pon && me.h_off < pn) me.copy(tc::smem_u32(ring + so), px);
+      px += a.d * L::kSide;
+      if ((pn -= L::kSide) <= 0) {
+        ahead.next(a);
+        enter();
       }
-      ahead.next(a);
     }
     copy_commit();
+    so = so + kSlotWords >= R::kSlots * kSlotWords ? threadIdx.x : so + kSlotWords;
   };
 #pragma unroll
-  for (int s = 0; s < R::kSlots; ++s) copy(s);
-  float m[32];
-  bool fresh = true, write = false;
-  int slot = 0;
+  for (int s = 0; s < R::kSlots; ++s) {
+    // lanes beyond the head's columns copy nothing and add zeros to its sums
+    if (!me.on)
+#pragma unroll
+      for (int w = 0; w < R::kWords; ++w) ring[so + w * kThreads] = make_uint4(0, 0, 0, 0);
+    copy();
+  }
   while (at.more) {
     const Side& p = a.side[at.sd];
-    const int64_t first = (int64_t)at.tg * kTok, t = first + me.g;
-    const bool here = me.on && t < a.T;
-    if (fresh) {
-      int64_t pos;
-      write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && here;
+    const int64_t first = (int64_t)at.tg * kTok, t = first + me.tok;
+    int64_t pos;
+    const bool write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && me.on &&
+                       t < a.T;
+    const bool norm = p.gamma != nullptr;
+    T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)(at.h + me.h_off) * a.d + me.col0;
+    float m[32];
+    {
       float c[8], sn[8], gm[16];
       me.angles(a, pos, c, sn);
       me.gamma(p.gamma, gm);
@@ -357,31 +387,28 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
         }
       }
     }
-    copy_wait<R::kSlots - 1>();
-    float v[16], w[16];
-    if (here) {
-      read_row<T>(ring + slot * R::kWords * kThreads + threadIdx.x, v);
-    } else {
+    for (int n = at.h_end - at.h; n > 0; n -= L::kSide) {
+      copy_wait<R::kSlots - 1>();
+      float v[16], w[16];
+      read_row<T>(ring + so, v);
+      if (me.rotated) turn<kInter>(v, m, w);
+      else pass<kInter>(v, m, w);
+      if (norm) {
+        const float r = rsqrtf(fmaf(group_sum<LP>(dot16(v, v)), a.inv_d, a.eps));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int e = 0; e < 16; e += 2) fmul2(w[e], w[e + 1], r, r, w[e], w[e + 1]);
+      }
+      copy();
+      if (write && me.h_off < n) me.store(y, w);
+      y += a.d * L::kSide;
     }
-    if (me.rotated) turn<kInter>(v, m, w);
-    else pass<kInter>(v, m, w);
-    if (p.gamma) {
-      const float r = rsqrtf(group_sum<LP>(dot16(v, v)) * a.inv_d + a.eps);
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) fmul2(w[e], w[e + 1], r, r, w[e], w[e + 1]);
-    }
-    copy(slot);
-    slot = slot + 1 == R::kSlots ? 0 : slot + 1;
-    if (write) me.store(static_cast<T*>(p.out) + t * p.os + (int64_t)at.h * a.d, w);
-    fresh = at.next(a);
+    at.next(a);
   }
 }
 
 template <typename T> struct RingBwd {       // backward: the upstream row and the input's
   static constexpr int kWords = 2 * sizeof(T);
-  static constexpr int kSlots = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kSlots = 2;
   static constexpr size_t kBytes = (size_t)kSlots * kWords * 16 * kThreads;
 };
 
@@ -391,30 +418,54 @@ template <typename T, int LP, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
   using R = RingBwd<T>;
   extern __shared__ __align__(16) uint4 ring[];
-  constexpr int kTok = 32 / LP;
+  using L = Lane<T, LP, kInter>;
+  constexpr int kTok = L::kTok;
   float* red = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(ring) + R::kBytes);   // [kWarps][2][d]
-  const Lane<T, LP, kInter> me(a);
+  constexpr uint32_t kSlotWords = R::kWords * kThreads;
+  const L me(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Place at(a), ahead(a);
   pdl_wait();
   pdl_trigger();
-  auto copy = [&](int slot) {
-    if (ahead.more) {
-      const int64_t t = (int64_t)ahead.tg * kTok + me.g;
-      if (me.on && t < a.T) {
-        const Side& p = a.side[ahead.sd];
-        const uint32_t dst = tc::smem_u32(ring + slot * R::kWords * kThreads + threadIdx.x);
-        me.copy(dst, static_cast<const T*>(p.up) + t * p.us + (int64_t)ahead.h * a.d);
-        if (p.gamma)
-          me.copy(dst + R::kWords / 2 * kThreads * 16,
-                  static_cast<const T*>(p.x) + t * p.xs + (int64_t)ahead.h * a.d);
+  const T *px = nullptr, *pu = nullptr;      // the next rows to copy, and how many the unit has left
+  int pn = 0;
+  bool pon = false, pnorm = false;
+  auto enter = [&] {
+    if (!ahead.more) return;
+    const Side& p = a.side[ahead.sd];
+    const int64_t t = (int64_t)ahead.tg * kTok + me.tok, in = (int64_t)(ahead.h + me.h_off) * a.d + me.col0;
+    pon = me.on && t < a.T;
+    pnorm = p.gamma != nullptr;
+    pu = static_cast<const T*>(p.up) + t * p.us + in;
+    px = static_cast<const T*>(p.x) + t * p.xs + in;
+    pn = ahead.h_end - ahead.h;
+  };
+  enter();
+  uint32_t so = threadIdx.x;
+  auto copy = [&] {
+    if (pn > 0) {
+      if (pon && me.h_off < pn) {
+        const uint32_t dst = tc::smem_u32(ring + so);
+        me.copy(dst, pu);
+        if (pnorm) me.copy(dst + R::kWords / 2 * kThreads * 16, px);
       }
-      ahead.next(a);
+      pu += a.d * L::kSide;
+      px += a.d * L::kSide;
+      if ((pn -= L::kSide) <= 0) {
+        ahead.next(a);
+        enter();
+      }
     }
     copy_commit();
+    so = so + kSlotWords >= R::kSlots * kSlotWords ? threadIdx.x : so + kSlotWords;
   };
 #pragma unroll
-  for (int s = 0; s < R::kSlots; ++s) copy(s);
+  for (int s = 0; s < R::kSlots; ++s) {
+    // what no copy fills (lanes beyond the head's columns, tokens beyond the last) has to be finite
+#pragma unroll
+    for (int w = 0; w < R::kWords; ++w) ring[so + w * kThreads] = make_uint4(0, 0, 0, 0);
+    copy();
+  }
   if (a.partial) {
     for (int e = lane; e < 2 * a.d; e += 32) red[warp * 2 * a.d + e] = 0.f;
     __syncwarp();
@@ -432,80 +483,71 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
       acc[e] = 0.f;
     }
   };
-  float c[8], sn[8], gm[16];
+  float gm[16];
   int sd = -1;                               // the side acc and gm are of
-  bool fresh = true, write = false;
-  int slot = 0;
   while (at.more) {
     const Side& p = a.side[at.sd];
-    const int64_t first = (int64_t)at.tg * kTok, t = first + me.g;
-    const bool here = me.on && t < a.T;
-    if (fresh) {
-      int64_t pos;
-      write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && here;
-      me.angles(a, pos, c, sn);
-      if (sd != at.sd) {
-        if (sd >= 0 && a.partial) put_away(sd);
-        sd = at.sd;
-        me.gamma(p.gamma, gm);
-      }
+    const int64_t first = (int64_t)at.tg * kTok, t = first + me.tok;
+    int64_t pos;
+    const bool write = lane_position(a, min64(t, a.T - 1), first, (int)min64(kTok, a.T - first), pos) && me.on &&
+                       t < a.T;
+    const bool norm = p.gamma != nullptr;
+    T* y = static_cast<T*>(p.out) + t * p.os + (int64_t)(at.h + me.h_off) * a.d + me.col0;
+    float c[8], sn[8];
+    me.angles(a, pos, c, sn);
+    if (sd != at.sd) {
+      if (sd >= 0 && a.partial) put_away(sd);
+      sd = at.sd;
+      me.gamma(p.gamma, gm);
     }
-    copy_wait<R::kSlots - 1>();
-    const uint4* row = ring + slot * R::kWords * kThreads + threadIdx.x;
-    float v[16], g[16];
-    if (here) {
-      read_row<T>(row, v);
-    } else {
+    for (int n = at.h_end - at.h; n > 0; n -= L::kSide) {
+      copy_wait<R::kSlots - 1>();
+      const bool live = write && me.h_off < n;
+      float v[16], g[16];
+      read_row<T>(ring + so, v);
+      // the transposed rotation
+      if (!me.rotated) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    }
-    // the transposed rotation
-    if (!me.rotated) {
+        for (int e = 0; e < 16; ++e) g[e] = v[e];
+      } else if constexpr (kInter) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) g[e] = v[e];
-    } else if constexpr (kInter) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float x, y;
-        fmul2(v[2 * e + 1], v[2 * e], sn[e], -sn[e], x, y);
-        ffma2(v[2 * e], v[2 * e + 1], c[e], c[e], x, y, g[2 * e], g[2 * e + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float x, y;
-        fmul2(v[8 + e], v[9 + e], sn[e], sn[e + 1], x, y);
-        ffma2(v[e], v[e + 1], c[e], c[e + 1], x, y, g[e], g[e + 1]);
-        fmul2(v[e], v[e + 1], -sn[e], -sn[e + 1], x, y);
-        ffma2(v[8 + e], v[9 + e], c[e], c[e + 1], x, y, g[8 + e], g[9 + e]);
-      }
-    }
-    if (p.gamma) {
-      if (here) {
-        read_row<T>(row + R::kWords / 2 * kThreads, v);
+        for (int e = 0; e < 8; ++e) {
+          float x, z;
+          fmul2(v[2 * e + 1], v[2 * e], sn[e], -sn[e], x, z);
+          ffma2(v[2 * e], v[2 * e + 1], c[e], c[e], x, z, g[2 * e], g[2 * e + 1]);
+        }
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int e = 0; e < 8; e += 2) {
+          float x, z;
+          fmul2(v[8 + e], v[9 + e], sn[e], sn[e + 1], x, z);
+          ffma2(v[e], v[e + 1], c[e], c[e + 1], x, z, g[e], g[e + 1]);
+          fmul2(v[e], v[e + 1], -sn[e], -sn[e + 1], x, z);
+          ffma2(v[8 + e], v[9 + e], c[e], c[e + 1], x, z, g[8 + e], g[9 + e]);
+        }
       }
-      const float r = rsqrtf(group_sum<LP>(dot16(v, v)) * a.inv_d + a.eps);
-      const float keep = write ? r : 0.f;            // a token in no segment adds nothing
+      if (norm) {
+        read_row<T>(ring + so + R::kWords / 2 * kThreads, v);
+        const float r = rsqrtf(fmaf(group_sum<LP>(dot16(v, v)), a.inv_d, a.eps));
+        const float keep = live ? r : 0.f;             // a row that is not there adds nothing
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        fmul2(v[e], v[e + 1], keep, keep, v[e], v[e + 1]);
-        ffma2(g[e], g[e + 1], v[e], v[e + 1], acc[e], acc[e + 1], acc[e], acc[e + 1]);
-        fmul2(g[e], g[e + 1], gm[e], gm[e + 1], g[e], g[e + 1]);
-      }
-      const float mean = -group_sum<LP>(dot16(g, v)) * a.inv_d;
+        for (int e = 0; e < 16; e += 2) {
+          fmul2(v[e], v[e + 1], keep, keep, v[e], v[e + 1]);
+          ffma2(g[e], g[e + 1], v[e], v[e + 1], acc[e], acc[e + 1], acc[e], acc[e + 1]);
+          fmul2(g[e], g[e + 1], gm[e], gm[e + 1], g[e], g[e + 1]);
+        }
+        const float mean = -group_sum<LP>(dot16(g, v)) * a.inv_d;
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        ffma2(v[e], v[e + 1], mean, mean, g[e], g[e + 1], g[e], g[e + 1]);
-        fmul2(g[e], g[e + 1], r, r, g[e], g[e + 1]);
+        for (int e = 0; e < 16; e += 2) {
+          ffma2(v[e], v[e + 1], mean, mean, g[e], g[e + 1], g[e], g[e + 1]);
+          fmul2(g[e], g[e + 1], r, r, g[e], g[e + 1]);
+        }
       }
+      copy();
+      if (live) me.store(y, g);
+      y += a.d * L::kSide;
     }
-    copy(slot);
-    slot = slot + 1 == R::kSlots ? 0 : slot + 1;
-    if (write) me.store(static_cast<T*>(p.out) + t * p.os + (int64_t)at.h * a.d, g);
-    fresh = at.next(a);
+    at.next(a);
   }
   if (!a.partial) return;
   if (sd >= 0) put_away(sd);
@@ -592,18 +634,22 @@ cudaError_t launch_qk_rope(nt_dtype dt, const RopeProblem& p, bool bwd, float* w
   a.status = status;
   const bool norm = p.q_gamma || p.k_gamma;
   a.partial = bwd && norm ? workspace : nullptr;
-  const int tok = 32 / group_lanes(p.d);
+  // as in Lane
+  const int LP = group_lanes(p.d), row = LP * 16 * (dt == NT_BF16 ? 2 : 4), side = row >= 128 ? 1 : 128 / row;
+  const int tok = 32 / LP / side;
   const int64_t groups = (p.T + tok - 1) / tok, warps = min64((int64_t)2 * sm_count(), kRopeMaxCtas) * kWarps;
-  // The heads of a unit: the number that gives the fewest steps, the rounds
-  // of units times a unit's heads and about three steps' worth of work for its
-  // tokens' angles.  (Unit counts stay below 2^31: a unit is 512 elements of
-  // q or k at least, and 2^31 of those are 2 TB.)
-  const int most = max(p.H_q, p.H_k);
-  const bool one_round = groups * (p.H_q + p.H_k) <= warps;        // one head to a unit
+  // The heads of a unit, a multiple of the rows side by side: the number that
+  // gives the fewest steps, the rounds of units times a unit's steps and about
+  // three steps' worth of work for its tokens' angles.  (Unit counts stay
+  // below 2^31: a unit is 512 bytes of q or k at least, and 2^31 of those are
+  // 1 TB.)
+  const int most = (max(p.H_q, p.H_k) + side - 1) / side;          // steps of a token group, at most
+  const bool one_round = groups * ((p.H_q + side - 1) / side + (p.H_k + side - 1) / side) <= warps;
   int64_t best = 0;
-  for (int hu = 1; hu <= (one_round ? min(most, 1) : most); hu = hu == 64 ? max(most, 65) : hu + 1) {
+  for (int st = 1; st <= (one_round ? min(most, 1) : most); st = st == 64 ? max(most, 65) : st + 1) {
+    const int hu = st * side;
     const int64_t units = groups * ((p.H_q + hu - 1) / hu + (p.H_k + hu - 1) / hu);
-    const int64_t cost = (units + warps - 1) / warps * (hu + 3);
+    const int64_t cost = (units + warps - 1) / warps * (st + 3);
     if (units > 0x7fffffffLL || (best && cost >= best)) continue;
     best = cost;
     a.unit_heads = hu;
