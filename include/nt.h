@@ -652,7 +652,8 @@ nt_status nt_rope_turns(int32_t rot_dim, double base, int32_t scaling, double fa
  *                 and d_pos0 NULL; or d_cu_seqlens [B+1] int32 as in
  *                 nt_varlen_attn, token t of segment b at position
  *                 t - cu[b] + d_pos0[b] (d_pos0 [B] int32 or NULL for 0: for
- *                 decoding, the tokens already in the cache).  A token that
+ *                 decoding, the tokens already in the cache), B at most
+ *                 2^30.  A token that
  *                 the offsets place in no segment is flagged
  *                 (NT_ERR_DEVICE_CHECK) and not written.
  *   d_turns       [rot_dim / 2] device, from nt_rope_turns.
@@ -732,7 +733,7 @@ typedef struct nt_kv_pages {
  *                 v_stride elements apart (>= H_kv * d, multiples of 8 bf16 /
  *                 4 fp32 elements).
  *   d_cu_seqlens  [B+1] int32, as in nt_varlen_attn.   d_pos0 [B] or NULL.
- *   d_block_table [B, max_pages] int32.
+ *   d_block_table [B, max_pages] int32.   B at most 2^30.
  * Two tokens of one call may not share a position of a page (a page that
  * several sequences share must be copied before one of them writes to it).
  * A token outside every segment, a negative position, one beyond max_pages,
@@ -771,8 +772,9 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  * value are in the cache already (nt_paged_write comes first).
  *   q             [B, H, d] in the pages' dtype, sequences q_stride elements
  *                 apart (>= H * d, a multiple of 8 bf16 / 4 fp32 elements).
- *   H             a multiple of H_kv.   d in {32, 64, 128}.  B * max_pages *
- *                 page_size * H at most 1e15 (NT_ERR_OVERFLOW).
+ *   H             a multiple of H_kv.   d in {32, 64, 128}.  B at most
+ *                 2^30 and B * max_pages * page_size * H at most 1e13
+ *                 (NT_ERR_OVERFLOW).
  *   d_block_table [B, max_pages] int32.
  *   d_lengths     [B] int32, the positions of each sequence that are attended
  *                 to; 0 gives o = 0 and lse = -inf.  Lengths are read on the
@@ -782,7 +784,8 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  *                 (NT_ERR_DEVICE_CHECK).
  *   scale         finite and > 0.
  *   o             [B, H, d] contiguous, out.   lse [H, B] fp32 natural-log
- *                 log-sum-exp of the scaled scores, or NULL.
+ *                 log-sum-exp of the scaled scores, or NULL.  Neither may
+ *                 overlap an input.
  *   workspace     >= nt_paged_attn_workspace_bytes(H, H_kv, d) bytes, 16-byte aligned.
  * The softmax statistics and sums are fp32; bf16 probabilities are rounded to
  * bf16 before they multiply the values where tensor cores form the product.

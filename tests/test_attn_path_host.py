@@ -167,6 +167,18 @@ def test_attn_refusals(lib):
     assert lib.nt_paged_attn_workspace_bytes(4, 3, 64) == 0 and lib.nt_paged_attn_workspace_bytes(4, 2, 48) == 0
 
 
+def test_limits_of_segments_and_of_a_batch(lib):
+    """Counts the kernels' indexes could not hold."""
+    far = (1 << 30) + 1
+    assert _rope(lib, B=far) == OVERFLOW and _rope_bwd(lib, B=far) == OVERFLOW
+    p = ctypes.byref(_pages())
+    assert lib.nt_paged_write(p, FAKE, 128, FAKE, 128, 1, FAKE, far, None, FAKE, 4, None) == OVERFLOW
+    attn = lambda B, pages: lib.nt_paged_attn(p, FAKE, 256, B, 4, FAKE, pages, FAKE, 0.125, FAKE, None, FAKE, 1 << 30,
+                                              None)
+    assert attn(far, 0) == OVERFLOW
+    assert attn(1 << 30, 1 << 8) == OVERFLOW           # 2^30 * 2^8 pages of 16 * 4 heads
+
+
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
     q = torch.zeros(4, 2, 64)
     with pytest.raises(ValueError):

@@ -230,3 +230,58 @@ def test_cache_full(mods):
         cache.step([b], [1])
     cache.free(a)
     cache.step([b], [12])
+
+
+def test_one_side_alone(mods):
+    """Queries without keys through autograd: the gradients of the call with both."""
+    nt, ag, _ = mods
+    q, k = (torch.randn(50, h, 64, device=DEV, dtype=BF, requires_grad=True) for h in (4, 2))
+    g = torch.rand(64, device=DEV, requires_grad=True)
+    turns, cu, up = nt.nt_rope_turns(64, device=DEV), _cu([20, 30]), torch.randn(50, 4, 64, device=DEV, dtype=BF)
+    alone, none = ag.qk_norm_rope(q, None, turns, cu_seqlens=cu, q_gamma=g)
+    assert none is None
+    got = torch.autograd.grad(alone, (q, g), up)
+    both = ag.qk_norm_rope(q, k, turns, cu_seqlens=cu, q_gamma=g, k_gamma=g.detach())[0]
+    assert torch.equal(alone, both)
+    want = torch.autograd.grad(both, (q, g), up)
+    assert torch.equal(got[0], want[0])
+    # the gammas' sums run over the rows in another order: T H roundings of the sum of magnitudes at most
+    y = torch.nn.functional.rms_norm(q.detach().double(), (64,)).abs().amax() * up.double().abs().sum((0, 1)).sum()
+    assert float((got[1] - want[1]).abs().max()) <= 200 * 2.0 ** -24 * float(y)
+
+
+def test_step_is_not_captured(mods):
+    _, _, paged = mods
+    cache = paged.PagedCache(4, 16, 1, 64, device=DEV)
+    a = cache.add()
+    x = torch.zeros(1, device=DEV)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        x.add_(1)
+        with pytest.raises(RuntimeError):
+            cache.step([a], [1])
+    assert cache.table.length[a] == 0
+
+
+def test_cache_on_two_streams(mods):
+    """Steps attended to on two streams at once, and in a graph replayed
+    beside them, share nothing but the pages."""
+    nt, _, paged = mods
+    cache = paged.PagedCache(600, 16, 2, 64, device=DEV)
+    seqs = [cache.add() for _ in range(4)]
+    lens = [4000, 1, 2300, 2600]
+    step = cache.step(seqs, lens)
+    k, v = (torch.randn(sum(lens), 2, 64, device=DEV, dtype=BF) for _ in range(2))
+    cache.write(step, k, v)
+    q = [torch.randn(4, 8, 64, device=DEV, dtype=BF) for _ in range(3)]
+    want = [cache.attend(step, x) for x in q]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = cache.attend(step, q[2])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+        got = [cache.attend(step, x, stream=s) for x, s in zip(q, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got + [replayed], want + [want[2]]))

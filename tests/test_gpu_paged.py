@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from _attn_path import attn_bound, make_pool, paged_attn
+from _attn_path import HALF_STEP, attn_bound, make_pool, paged_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -394,3 +394,30 @@ def test_attn_far_page_offsets(nt):
     assert torch.equal(k[0], k[far]) and torch.equal(v[0], v[far])
     ro, _, mag, cond = paged_attn(k[far:].cpu(), v[far:].cpu(), q.cpu(), torch.tensor([[0]]), [5])
     assert bool(((o.double().cpu() - ro).abs() <= attn_bound(ro, mag, cond, 5, BF)).all())
+
+
+@pytest.mark.parametrize("page,dtype", [(65536, BF), (65535, F32)])
+def test_attn_longest_context(nt, page, dtype):
+    """2^31 - 1 positions (one page many times over): counts of keys and tiles
+    next to the end of 32 bits.  Against fp64 over the page's rows, each as
+    often as it is attended to.  A sum of n roundings in turn is off by n
+    steps of 2^-24 at most (2^-23 on the tensor cores, which may cut): a warp
+    adds 32 lanes' keys in turn, 2^31 / (8 warps x 152) of them at most one by
+    one (fp32), 16 at a time (bf16)."""
+    n, d = 2 ** 31 - 1, 32
+    k, v, q = (_rand(i, *s, dtype=dtype) for i, s in enumerate([(1, 1, page, d), (1, 1, page, d), (1, 1, d)]))
+    v = v.abs()
+    entries = -(-n // page)
+    table = torch.zeros(1, entries, dtype=torch.int32, device=DEV)
+    o, lse = nt.nt_paged_attn(nt.KVPages(k.to(DEV), v.to(DEV)), q.to(DEV), table, _i32([n]), want_lse=True)
+    nt.nt_device_status()
+    last = n - (entries - 1) * page                    # rows of the last page that count
+    times = torch.full((page,), float(entries - 1), dtype=torch.float64)
+    times[:last] += 1
+    s = k[0, 0].double() @ q[0, 0].double() * d ** -0.5
+    w = times * torch.exp(s - s.max())
+    ro, rl = (w @ v[0, 0].double()) / w.sum(), float(s.max() + torch.log(w.sum()))
+    added = n / (8 * 152) / (16 if dtype == BF else 1)
+    rel = added * (2.0 ** -23 + 2.0 ** -24) + 2 * HALF_STEP[dtype]       # output and sum; P's and o's rounding in bf16
+    assert bool(((o[0, 0].double().cpu() - ro).abs() <= rel * ro).all())
+    assert abs(float(lse) - rl) <= rel

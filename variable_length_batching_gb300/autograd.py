@@ -105,14 +105,15 @@ class QKNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0 = ctx.saved_tensors
         eps, interleaved, rot_scale = ctx.args
-        dq, dk, dqg, dkg = nt.nt_qk_norm_rope_bwd(dq_out.contiguous(), dk_out.contiguous(), turns, q=q, k=k,
+        dq_out, dk_out = (None if g is None else g.contiguous() for g in (dq_out, dk_out))
+        dq, dk, dqg, dkg = nt.nt_qk_norm_rope_bwd(dq_out, dk_out, turns, q=q, k=k,
                                                   cu_seqlens=cu_seqlens, positions=positions, pos0=pos0,
                                                   q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, interleaved=interleaved,
                                                   rot_scale=rot_scale)
         return dq, dk, None, dqg, dkg, None, None, None, None, None, None
 
 
-def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, turns: Optional[torch.Tensor], cu_seqlens=None, positions=None,
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns: Optional[torch.Tensor], cu_seqlens=None, positions=None,
                  pos0=None, q_gamma: Optional[torch.Tensor] = None, k_gamma: Optional[torch.Tensor] = None,
                  eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0):
     """Per-head norm and rotary positions of packed q and k with autograd

@@ -94,6 +94,11 @@ int32_t dtype_of(at::ScalarType t) {
   refuse(std::string("unsupported dtype ") + type_name(t));
 }
 
+int32_t flag(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v;
+}
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -127,6 +132,18 @@ T like(const T& t) { return at::empty(t.sizes(), t.options()); }
 T bytes(size_t n, const T& t) { return at::empty({(int64_t)n}, t.options().dtype(at::kByte)); }
 void* data(const T& t) { return t.defined() ? t.data_ptr() : nullptr; }
 bool same_shape(const T& a, const T& b) { return a.defined() == b.defined() && (!a.defined() || a.sizes() == b.sizes()); }
+
+// The interpreter's lock is not held across a C call: a launch waits where the
+// device's queue is full, possibly for work that needs the lock.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... A>
+int unlocked(F f, A... args) {
+  const Unlocked u;
+  return f(args...);
+}
 
 PyObject* result(int status, std::initializer_list<const T*> outs) {
   PyObject* r = PyTuple_New(1 + outs.size());
@@ -214,9 +231,9 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
   if (!k_out.defined() && k.defined()) k_out = like(k);
   if (!same_shape(q, q_out) || !same_shape(k, k_out)) refuse("outputs must have their inputs' shapes");
   const Tokens qo = tokens(q_out, r.index, r.type, "q_out"), ko = tokens(k_out, r.index, r.type, "k_out");
-  const int st = f_rope((nt_dtype)dt, qt.p, qt.stride, kt.p, kt.stride, r.n, (int32_t)r.H_q, (int32_t)r.H_k,
+  const int st = unlocked(f_rope, (nt_dtype)dt, qt.p, qt.stride, kt.p, kt.stride, r.n, (int32_t)r.H_q, (int32_t)r.H_k,
                         (int32_t)r.d, r.qg, r.kg, (float)number(a[8]), r.cu, r.B, r.pos0, r.positions, r.turns, r.rot,
-                        PyObject_IsTrue(a[9]), (float)number(a[10]), qo.p, qo.stride, ko.p, ko.stride, call.stream);
+                        flag(a[9]), (float)number(a[10]), qo.p, qo.stride, ko.p, ko.stride, call.stream);
   return result(st, {&q_out, &k_out});
 }
 
@@ -248,9 +265,9 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a, Py_ssize_t n) {
   } else if (qg.defined() || kg.defined()) {
     ws = bytes(f_rope_bwd_ws((int32_t)r.d), uq.defined() ? uq : uk);
   }
-  const int st = f_rope_bwd((nt_dtype)dt, uqt.p, uqt.stride, ukt.p, ukt.stride, qt.p, qt.stride, kt.p, kt.stride, r.n,
+  const int st = unlocked(f_rope_bwd, (nt_dtype)dt, uqt.p, uqt.stride, ukt.p, ukt.stride, qt.p, qt.stride, kt.p, kt.stride, r.n,
                             (int32_t)r.H_q, (int32_t)r.H_k, (int32_t)r.d, r.qg, r.kg, (float)number(a[10]), r.cu, r.B,
-                            r.pos0, r.positions, r.turns, r.rot, PyObject_IsTrue(a[11]), (float)number(a[12]),
+                            r.pos0, r.positions, r.turns, r.rot, flag(a[11]), (float)number(a[12]),
                             data(dq), r.H_q * r.d, data(dk), r.H_k * r.d, static_cast<float*>(data(dqg)),
                             static_cast<float*>(data(dkg)), data(ws), ws.defined() ? ws.nbytes() : 0, call.stream);
   return result(st, {&dq, &dk, &dqg, &dkg});
@@ -290,7 +307,7 @@ PyObject* paged_write(PyObject* const* a, Py_ssize_t n) {
   const int32_t* table = block_table(need(a[5], "block_table"), B, g.index, max_pages);
   const void *c = flat(cu, g.index, at::kInt, "cu_seqlens"), *p0 = flat(pos0, g.index, at::kInt, "pos0");
   Call call(g.index, a[7]);
-  const int st = f_write(g.p, kt.p, kt.stride, vt.p, vt.stride, k.size(0), static_cast<const int32_t*>(c), B,
+  const int st = unlocked(f_write, g.p, kt.p, kt.stride, vt.p, vt.stride, k.size(0), static_cast<const int32_t*>(c), B,
                          static_cast<const int32_t*>(p0), table, max_pages, call.stream);
   return result(st, {});
 }
@@ -305,7 +322,7 @@ PyObject* paged_copy(PyObject* const* a, Py_ssize_t n) {
     refuse("src and dst must be int32, one entry per copy");
   if (!src.is_contiguous() || !dst.is_contiguous()) refuse("src and dst must be contiguous");
   Call call(g.index, a[4]);
-  const int st = f_copy(g.p, static_cast<const int32_t*>(src.data_ptr()), static_cast<const int32_t*>(dst.data_ptr()),
+  const int st = unlocked(f_copy, g.p, static_cast<const int32_t*>(src.data_ptr()), static_cast<const int32_t*>(dst.data_ptr()),
                         src.numel(), call.stream);
   return result(st, {});
 }
@@ -328,7 +345,7 @@ PyObject* paged_attn(PyObject* const* a, Py_ssize_t n) {
   T out = tensor(a[6], "out"), lse = tensor(a[7], "lse"), ws = tensor(a[9], "workspace");
   if (!out.defined()) out = like(q);
   else if (out.sizes() != q.sizes()) refuse("out must have q's shape");
-  if (!lse.defined() && PyObject_IsTrue(a[8])) lse = at::empty({H, B}, q.options().dtype(at::kFloat));
+  if (!lse.defined() && flag(a[8])) lse = at::empty({H, B}, q.options().dtype(at::kFloat));
   if (lse.defined() && (lse.dim() != 2 || lse.size(0) != H || lse.size(1) != B)) refuse("lse must be (H, B)");
   if (ws.defined()) {
     on_device(ws, g.index, "workspace");
@@ -337,7 +354,7 @@ PyObject* paged_attn(PyObject* const* a, Py_ssize_t n) {
     ws = bytes(f_attn_ws((int32_t)H, g.p->H_kv, d), q);
   }
   const float scale = a[5] == Py_None ? 1.0f / std::sqrt((float)d) : (float)number(a[5]);
-  const int st = f_attn(g.p, qt.p, qt.stride, (int32_t)B, (int32_t)H, table, max_pages,
+  const int st = unlocked(f_attn, g.p, qt.p, qt.stride, (int32_t)B, (int32_t)H, table, max_pages,
                         static_cast<const int32_t*>(len), scale, flat(out, g.index, g.type, "out"),
                         static_cast<float*>(flat(lse, g.index, at::kFloat, "lse")), data(ws), ws.nbytes(),
                         call.stream);

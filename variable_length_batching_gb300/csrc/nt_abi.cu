@@ -160,6 +160,9 @@ nt_status pair_transition(const nt_partition* part, nt_dtype dtype, const void* 
                           b2, stream);
 }
 
+// The kernels' searches and strides over segments add to a segment's index.
+constexpr int32_t kMaxSegments = 1 << 30;
+
 // Sizes, strides, positions and pointers that nt_qk_norm_rope and its
 // backward share.
 nt_status check_rope(nt_dtype dtype, int64_t T, int32_t H_q, int32_t H_k, int32_t d, float eps,
@@ -170,6 +173,7 @@ nt_status check_rope(nt_dtype dtype, int64_t T, int32_t H_q, int32_t H_k, int32_
     return fail(NT_ERR_INVALID, "bad sizes T=%lld H_q=%d H_k=%d d=%d B=%d rot_dim=%d", (long long)T, H_q, H_k, d, B,
                 rot_dim);
   if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 segments", B);
   if (H_q > 65536 || H_k > 65536) return fail(NT_ERR_UNSUPPORTED, "H_q=%d, H_k=%d: at most 65536 heads", H_q, H_k);
   if (d % 16 || d > 256) return fail(NT_ERR_UNSUPPORTED, "head width d=%d must be a multiple of 16 up to 256", d);
   if (rot_dim > d) return fail(NT_ERR_INVALID, "rot_dim=%d > d=%d", rot_dim, d);
@@ -1069,6 +1073,7 @@ nt_status nt_paged_write(const nt_kv_pages* pages, const void* k, int64_t k_stri
   if (st != NT_OK) return st;
   if (T < 0 || B < 0) return fail(NT_ERR_INVALID, "bad sizes T=%lld B=%d", (long long)T, B);
   if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 segments", B);
   st = check_table(d_block_table, max_pages, B);
   if (st == NT_OK) st = check_tokens(pages->dtype, "k", k, k_stride, T, pages->H_kv, pages->d);
   if (st == NT_OK) st = check_tokens(pages->dtype, "v", v, v_stride, T, pages->H_kv, pages->d);
@@ -1126,6 +1131,7 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   nt_status st = check_pages(pages);
   if (st != NT_OK) return st;
   if (B < 0 || H <= 0) return fail(NT_ERR_INVALID, "bad sizes B=%d H=%d", B, H);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
   if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
   if (pages->d != 32 && pages->d != 64 && pages->d != 128)
     return fail(NT_ERR_UNSUPPORTED, "head width d=%d (32, 64 or 128)", pages->d);
@@ -1137,8 +1143,8 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(d_lengths) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(NT_ERR_INVALID, "d_lengths or lse misaligned");
-  if ((double)B * max_pages * pages->page_size * H > 1e15)
-    return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e15",
+  if ((double)B * max_pages * pages->page_size * H > 1e13)
+    return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e13",
                 (double)B * max_pages * pages->page_size * H);
   const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
   if (B > 0 && workspace_bytes < need)

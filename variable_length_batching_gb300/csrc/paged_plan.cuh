@@ -35,7 +35,8 @@ __device__ __forceinline__ int paged_length(const int32_t* lengths, int b, int64
   }
   return n;
 }
-__device__ __forceinline__ int64_t paged_tiles(int len, int tile) { return (len + tile - 1) / tile; }
+// (unsigned: len + tile passes 2^31 for the longest)
+__device__ __forceinline__ int64_t paged_tiles(int len, int tile) { return ((uint32_t)len + tile - 1) / tile; }
 
 // Units of a sequence's items.
 __device__ __forceinline__ int64_t paged_units(int len, int tile, int items, int extra) {

@@ -153,7 +153,6 @@ class PagedCache:
         self.table = PageTable(n_pages, page_size)
         self.pages = nt.KVPages(torch.empty(shape, dtype=dtype, device=device),
                                 torch.empty(shape, dtype=dtype, device=device))
-        self._workspace: Optional[torch.Tensor] = None
 
     def add(self) -> int:
         return self.table.add()
@@ -177,7 +176,12 @@ class PagedCache:
     def step(self, seqs: Sequence[int], counts: Sequence[int], stream=None) -> Step:
         """Makes room for counts[i] new tokens of seqs[i] and returns the
         step's device arrays (one copy from pinned memory).  Counts of 1 make
-        a decoding step, larger ones a prefill."""
+        a decoding step, larger ones a prefill.  Not while a graph is being
+        captured: a replay would not make room again."""
+        on = stream if stream is not None else torch.cuda.current_stream(self.pages.device)
+        with torch.cuda.stream(on):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a step makes room on the host: take it outside the capture")
         copies = self.table.extend(seqs, counts)
         self._copy(copies, stream)
         B = len(seqs)
@@ -194,7 +198,7 @@ class PagedCache:
             flat += p + [-1] * (width - len(p))
         host = torch.tensor(flat, dtype=torch.int32).pin_memory()
         dev = self.pages.device
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+        with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
         return Step(list(seqs), arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
                     arr[head:].view(B, width), max(list(counts) + [0]))
@@ -204,11 +208,5 @@ class PagedCache:
         nt.nt_paged_write(self.pages, k, v, step.cu_seqlens, step.block_table, pos0=step.pos0, stream=stream)
 
     def attend(self, step: Step, q: torch.Tensor, scale: Optional[float] = None, stream=None) -> torch.Tensor:
-        """One query token per sequence, q (B, H, d), over all its positions.
-        Calls on several streams at once need caches (and so workspaces) of
-        their own."""
-        need = nt.nt_paged_attn_workspace_bytes(q.shape[1], self.pages.H_kv, self.pages.d)
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
-        return nt.nt_paged_attn(self.pages, q, step.block_table, step.lengths, scale=scale,
-                                workspace=self._workspace, stream=stream)[0]
+        """One query token per sequence, q (B, H, d), over all its positions."""
+        return nt.nt_paged_attn(self.pages, q, step.block_table, step.lengths, scale=scale, stream=stream)[0]
