@@ -176,6 +176,9 @@ def test_limits_of_segments_and_of_a_batch(lib):
     attn = lambda B, pages: lib.nt_paged_attn(p, FAKE, 256, B, 4, FAKE, pages, FAKE, 0.125, FAKE, None, FAKE, 1 << 30,
                                               None)
     assert attn(far, 0) == OVERFLOW
+    odd = ctypes.byref(_pages(page_size=12))
+    assert lib.nt_paged_attn(odd, FAKE, 256, 1, 4, FAKE, (1 << 24) // 12 + 1, FAKE, 0.125, FAKE, None, FAKE, 1 << 30,
+                             None) == UNSUPPORTED
     assert attn(1 << 30, 1 << 8) == OVERFLOW           # 2^30 * 2^8 pages of 16 * 4 heads
 
 

@@ -178,6 +178,27 @@ def test_attn(nt, shape, dtype, room):
     _check(inputs, o, lse, lens, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] % 8 == 0])
+def test_attn_long_tables(nt, shape, dtype):
+    """Tables made for contexts of 200,000 positions: the kernel that long
+    contexts take, at every shape."""
+    lens, page, H, Hk, d = shape
+    inputs, o, lse = _attn_case(nt, lens, page, H, Hk, d, dtype, wide=200000 // page)
+    _check(inputs, o, lse, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [16, 10])
+@pytest.mark.parametrize("B", [1, 2, 3, 5, 9, 20, 40, 90])
+def test_attn_cluster_sizes(nt, B, page, dtype):
+    """Batches of few items, which are spread over more CTAs the fewer they
+    are; lengths around the slices' and the CTAs' ends."""
+    lens = [[1, 15, 16, 17, 255, 256, 257, 0, 1000, 1553, 1537, 96, 97, 500][i % 14] for i in range(B - 1)] + [1600]
+    inputs, o, lse = _attn_case(nt, lens, page, 8, 2, 64, dtype, seed=B)
+    _check(inputs, o, lse, lens, dtype)
+
+
 # contexts of a few positions, where a table of few pages is all there is
 SHORT = [  # lens, page, H, Hk, d
     ([1, 0, 3, 16, 17, 128, 127, 64], 16, 12, 12, 64),
@@ -396,7 +417,7 @@ def test_attn_far_page_offsets(nt):
     assert bool(((o.double().cpu() - ro).abs() <= attn_bound(ro, mag, cond, 5, BF)).all())
 
 
-@pytest.mark.parametrize("page,dtype", [(65536, BF), (65535, F32)])
+@pytest.mark.parametrize("page,dtype", [(65536, BF), (65528, F32)])
 def test_attn_longest_context(nt, page, dtype):
     """2^31 - 1 positions (one page many times over): counts of keys and tiles
     next to the end of 32 bits.  Against fp64 over the page's rows, each as

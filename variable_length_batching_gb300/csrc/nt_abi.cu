@@ -1146,6 +1146,9 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   if ((double)B * max_pages * pages->page_size * H > 1e13)
     return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e13",
                 (double)B * max_pages * pages->page_size * H);
+  // (the kernel for other pages has few warps to a sequence, whose fp32 sums run in turn)
+  if (B > 0 && pages->page_size % 8 && (int64_t)max_pages * pages->page_size > (1 << 24))
+    return fail(NT_ERR_UNSUPPORTED, "tables of more than 2^24 positions need pages of a multiple of 8");
   const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
   if (B > 0 && workspace_bytes < need)
     return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);

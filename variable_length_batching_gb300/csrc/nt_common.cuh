@@ -135,8 +135,9 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 // Lets a kernel take `bytes` of dynamic shared memory, asked for once per
 // device (the attribute stays set, and asking again is host time on every
-// call).  `bytes` is the most the kernel is launched with.
-template <auto kKernel>
+// call).  `bytes` is the most the kernel is launched with.  kClusters: and of
+// clusters of more than 8 CTAs.
+template <auto kKernel, bool kClusters = false>
 cudaError_t allow_smem_once(size_t bytes) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -145,6 +146,8 @@ cudaError_t allow_smem_once(size_t bytes) {
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (kClusters && e == cudaSuccess)
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -423,13 +426,31 @@ constexpr int kPagedMaxCtas = 512;      // CTAs of the split, at most (two parti
 constexpr int kPagedMaxHeads = 16;      // query heads of one item, at most
 size_t paged_attn_workspace_bytes(int G, int d);
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
-// One warp per sequence and key head, for tables of at most kPagedShortKeys
-// positions.
+// Positions a table holds, at most.
+inline int64_t paged_cap(const PagedAttnProblem& p) {
+  return min64((int64_t)p.max_pages * p.pool.page_size, 0x7fffffff);
+}
+// Items (a sequence's key head with up to `heads` of its query heads).
+inline int64_t paged_items(const PagedAttnProblem& p, int heads) {
+  return (int64_t)p.B * p.pool.H * ((p.H / p.pool.H + heads - 1) / heads);
+}
+// What the estimates take the lengths' mean to be, as a part of the longest
+// that the tables hold (the lengths are known on the device only): one
+// sequence that long, the others of a ragged batch 0.35 of it.
+inline double paged_mean_part(const PagedAttnProblem& p) { return 0.35 + 0.65 / p.B; }
+// The three kernels, each with its estimate of the call's time in
+// microseconds (infinite where it does not take the call).
+// A warp per item, for tables of at most kPagedShortKeys positions.
 constexpr int kPagedShortKeys = 128;
-bool paged_attn_short_chosen(nt_dtype dt, const PagedAttnProblem& p);
+double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
-// The TMA-fed kernel: pages of a multiple of 8 positions.
-bool paged_attn_tma_supported(const PagedAttnProblem& p);
+// A cluster of CTAs per item; any page size.
+double paged_attn_spread_us(nt_dtype dt, const PagedAttnProblem& p, int* cluster);
+cudaError_t launch_paged_attn_spread(nt_dtype dt, const PagedAttnProblem& p, int cluster, unsigned int* status,
+                                     cudaStream_t s);
+// The batch's tiles dealt out evenly to the SMs by TMA; pages of a multiple of
+// 8 positions.
+double paged_attn_tma_us(nt_dtype dt, const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 
 bool attn_simt_supported(int d);

@@ -48,16 +48,10 @@ struct ShortArgs {
   unsigned int* status;
 };
 
-__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-
 template <typename T, int D, int HP>
 __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32)) paged_attn_short_kernel(const ShortArgs a) {
   using C = Cfg<T, D, HP>;
   constexpr int kWarps = C::kWarps;
-  constexpr int kChunks = C::kRow / 16;            // 16-byte words of a row
-  constexpr int kRowsAt = 32 / kChunks < 1 ? 1 : 32 / kChunks;      // rows a warp copies at once
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * C::kWarpBytes;
@@ -101,22 +95,8 @@ __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32)) paged_attn_short
       const int id = __shfl_sync(0xffffffffu, ids, (pg - win) & 31);
       const bool in = key < len, good = id >= 0 && id < a.n_pages;
       if (in && !good) flag_device(a.status, kDevCheck);
-      int64_t row = in && good ? ((int64_t)id * a.Hkv + kvh) * ps + (key - pg * ps) : -1;
-      const uint32_t dst = smem_u32(ring + slot * C::kSlot);
-      const uint8_t* src[2] = {static_cast<const uint8_t*>(a.k), static_cast<const uint8_t*>(a.v)};
-#pragma unroll
-      for (int r0 = 0; r0 < 16; r0 += kRowsAt) {
-        const int r = r0 + (kRowsAt > 1 ? lane / kChunks : 0), c = lane % kChunks;
-        const int64_t at = __shfl_sync(0xffffffffu, row, r);
-        // bf16: 64-column halves of 16 rows, swizzled as the worker reads them
-        uint32_t to;
-        if constexpr (!C::kBf16) to = r * C::kRow + c * 16;
-        else if constexpr (D == 32) to = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        else to = (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-#pragma unroll
-        for (int sd = 0; sd < 2; ++sd)
-          copy16_or_zero(dst + sd * C::kSide + to, src[sd] + (at < 0 ? 0 : at * C::kRow + c * 16), at >= 0);
-      }
+      const int64_t row = in && good ? ((int64_t)id * a.Hkv + kvh) * ps + (key - pg * ps) : -1;
+      copy_slice<T, D>(smem_u32(ring + slot * C::kSlot), a.k, a.v, row);
       kb += 16;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -202,25 +182,14 @@ cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, 
 
 }  // namespace
 
-// Short tables, where this kernel is the faster: it takes about 1.0 us and,
-// for every round of items on its warps, 1.6 us and 1.05 us a slice of 16
-// keys; the tile kernel 3.8 us and, for every round of items on the SMs, 0.6
-// us and 0.75 us a 32 KB of keys and values (twice that with 16 heads).
-// Measured at d = 128, four heads to a key head: 240 items of 60 keys 6.9 us
-// here and 7.9 there, 512 of 128 keys 11.6 and 13.1; but 64 of 100 keys 9.7
-// and 6.9, 256 of 128 keys 11.0 and 8.5.
-bool paged_attn_short_chosen(nt_dtype dt, const PagedAttnProblem& p) {
-  const int64_t cap = (int64_t)p.max_pages * p.pool.page_size;
-  if (cap > kPagedShortKeys || p.pool.n_pages == 0) return false;
-  if (p.pool.page_size % 8) return true;           // the tile kernel does not take these
-  const int G = p.H / p.pool.H, es = dt == NT_BF16 ? 2 : 4;
-  const int HP = dt == NT_BF16 && G > 8 ? 16 : 8;
-  const int64_t items = (int64_t)p.B * p.pool.H * ((G + HP - 1) / HP), sms = sm_count();
-  const int64_t warps = sms * (dt == NT_BF16 ? 12 : p.d == 128 ? 6 : 12);
-  const double here = 1.0 + (double)((items + warps - 1) / warps) * (1.6 + 1.05 * (double)((cap + 15) / 16));
-  const double tiles = 3.8 + (double)((items + sms - 1) / sms) *
-                                 (0.6 + 0.75 * (double)(cap * p.d * es * 2) / 32768) * (HP == 16 ? 2 : 1);
-  return here <= tiles;
+// About 1.0 us and, for every round of items on the warps, 1.6 us and 1.05 us
+// a slice of 16 keys.
+double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p) {
+  const int64_t cap = paged_cap(p);
+  if (cap > kPagedShortKeys || p.pool.n_pages == 0) return INFINITY;
+  const int64_t warps = sm_count() * (dt == NT_BF16 || p.d < 128 ? 12 : 6);
+  const int64_t items = paged_items(p, dt == NT_BF16 && p.H / p.pool.H > 8 ? 16 : 8);
+  return 1.0 + (double)((items + warps - 1) / warps) * (1.6 + 1.05 * (double)((cap + 15) / 16));
 }
 
 cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {

@@ -1,6 +1,6 @@
 // What a warp does with 16 keys of a paged cache and up to HP query heads of
-// one key head: scores, a running softmax, outputs.  Used by the two kernels
-// that stage the keys in shared memory.
+// one key head: scores, a running softmax, outputs.  Used by the kernels of
+// paged attention, which differ in how the keys come to shared memory.
 #pragma once
 
 #include "tc_ptx.cuh"
@@ -354,6 +354,34 @@ struct Worker<float, D, HP> {
         for (int c = 0; c < N; ++c) ro[h * kRedStride + lane * N + c] = o[h][c];
   }
 };
+
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// A warp copies 16 keys and their values into a slot that its Worker (box 16)
+// reads, row by row with cp.async, so any page size will do.  `row`: of lane
+// i < 16 the pool's row of key i, negative for zeros.
+template <typename T, int D>
+__device__ __forceinline__ void copy_slice(uint32_t dst, const void* k, const void* v, int64_t row) {
+  constexpr uint32_t kRow = D * sizeof(T);
+  constexpr int kChunks = kRow / 16;                                // 16-byte words of a row
+  constexpr int kRowsAt = 32 / kChunks < 1 ? 1 : 32 / kChunks;      // rows a warp copies at once
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r0 = 0; r0 < 16; r0 += kRowsAt) {
+    const int r = r0 + (kRowsAt > 1 ? lane / kChunks : 0), c = lane % kChunks;
+    const int64_t at = __shfl_sync(0xffffffffu, row, r);
+    // bf16: 64-column halves of 16 rows, swizzled as the worker reads them
+    uint32_t to;
+    if constexpr (sizeof(T) == 4) to = r * kRow + c * 16;
+    else if constexpr (D == 32) to = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    else to = (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    const int64_t from = at < 0 ? 0 : at * kRow + c * 16;
+    copy16_or_zero(dst + to, static_cast<const uint8_t*>(k) + from, at >= 0);
+    copy16_or_zero(dst + 16 * kRow + to, static_cast<const uint8_t*>(v) + from, at >= 0);
+  }
+}
 
 }  // namespace paged
 }  // namespace nt
