@@ -24,11 +24,12 @@ struct Cfg {
   static constexpr uint32_t kRow = D * sizeof(T);
   static constexpr uint32_t kSide = 16 * kRow;                     // keys or values of a slice
   static constexpr uint32_t kSlot = 2 * kSide;
-  static constexpr uint32_t kOut = kBf16 ? HP * kRow : 0;          // the output, rows gathered
+  static constexpr uint32_t kOut = HP * kRow;                      // bf16: the output's rows; fp32: the query's
+  static constexpr uint32_t kScratch = Worker<T, D, HP>::kScratch;
   // few slots, many warps: 12 to 24 on an SM (6 in fp32 with d = 128)
   static constexpr int kSlots = D == 128 || (!kBf16 && D == 64) ? 2 : 3;
   static constexpr int kWarps = !kBf16 && D == 128 ? 6 : 4;
-  static constexpr uint32_t kWarpBytes = kSlots * kSlot + kOut;
+  static constexpr uint32_t kWarpBytes = (kSlots * kSlot + kOut + kScratch + 127) / 128 * 128;
   static constexpr uint32_t kSmem = kWarps * kWarpBytes;
   static constexpr int kPerSm = (int)(225 * 1024 / (kSmem + 1024)) < 6 ? (int)(225 * 1024 / (kSmem + 1024)) : 6;
   static_assert(kWarpBytes % 128 == 0 && kPerSm >= 1 && kSmem <= 227 * 1024, "shared memory");
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32)) paged_attn_short
   for (int s = 0; s < C::kSlots; ++s) copy(s);
 
   // ---- the items ------------------------------------------------------------------
-  Worker<T, D, HP> me(16, 0);
+  Worker<T, D, HP> me(16, 0, ring + C::kSlots * C::kSlot + C::kOut);
   int slot = 0;
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < total; item += step) {
     const int b = (int)paged_div(item, a.items), j = (int)(item - (int64_t)b * a.items);
@@ -118,7 +119,14 @@ __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32)) paged_attn_short
       if (a.lse && lane < nh) a.lse[(hq + lane) * a.B + b] = -INFINITY;
       continue;
     }
-    me.load_q(static_cast<const T*>(a.q) + b * a.q_stride + hq * D, nh);
+    const T* q = static_cast<const T*>(a.q) + b * a.q_stride + hq * D;
+    if constexpr (Worker<T, D, HP>::kKeepsQ) {
+      for (int e = lane; e < nh * (D / 4); e += 32)
+        reinterpret_cast<float4*>(out_rows)[e] = reinterpret_cast<const float4*>(q)[e];
+      __syncwarp();
+      q = out_rows;
+    }
+    me.load_q(q, nh);
     for (int k0 = 0; k0 < n; k0 += 16) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kSlots - 1) : "memory");
       __syncwarp();
@@ -128,15 +136,7 @@ __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32)) paged_attn_short
       slot = slot + 1 == C::kSlots ? 0 : slot + 1;
     }
     me.finish(out_rows, o, nh);
-    if (a.lse) {
-      const float v = me.head_lse();
-      const int h = me.head_of_lane();
-      if (h >= 0 && h < nh) a.lse[(hq + h) * a.B + b] = v;
-      if constexpr (C::kBf16 && HP == 16) {
-        const float v1 = me.head_lse1();
-        if (h >= 0 && h + 8 < nh) a.lse[(hq + h + 8) * a.B + b] = v1;
-      }
-    }
+    if (a.lse) me.store_lse(a.lse + hq * a.B + b, a.B, nh);
   }
 }
 

@@ -33,8 +33,9 @@ struct Cfg {
   static constexpr int kWarps = kRow <= 128 ? 8 : kRow == 256 ? 6 : 3;
   static constexpr int kSlots = kRow <= 128 ? 3 : 2;
   static constexpr uint32_t kWarpBytes = kSlots * kSlot;
-  static constexpr uint32_t kPart = HP * D * 4;                    // the CTA's output
-  static constexpr uint32_t kSmem = kWarps * kWarpBytes + kPart;
+  static constexpr uint32_t kPart = HP * D * 4;                    // the CTA's output; before, fp32: its query rows
+  static constexpr uint32_t kScratch = Worker<T, D, HP>::kScratch; // of a warp
+  static constexpr uint32_t kSmem = kWarps * (kWarpBytes + kScratch) + kPart;
   static constexpr int kRedStride = D + 4;
   static_assert(HP * kRedStride * 4 <= kWarpBytes && kSmem <= 111 * 1024, "shared memory");
 };
@@ -159,8 +160,15 @@ __global__ void __launch_bounds__((Cfg<T, D, HP>::kWarps * 32), 2) paged_attn_sp
     Place at[C::kSlots];
   #pragma unroll
     for (int s = 0; s < C::kSlots; ++s) at[s] = place(first + s * step);
-    Worker<T, D, HP> me(16, 0);
-    me.load_q(static_cast<const T*>(a.q) + b * a.q_stride + hq * D, nh);
+    Worker<T, D, HP> me(16, 0, smem + kWarps * C::kWarpBytes + C::kPart + warp * C::kScratch);
+    const T* q = static_cast<const T*>(a.q) + b * a.q_stride + hq * D;
+    if constexpr (Worker<T, D, HP>::kKeepsQ) {
+      for (int e = threadIdx.x; e < nh * kCols; e += kWarps * 32)
+        reinterpret_cast<float4*>(part_o)[e] = reinterpret_cast<const float4*>(q)[e];
+      __syncthreads();
+      q = part_o;
+    }
+    me.load_q(q, nh);
   #pragma unroll
     for (int s = 0; s < C::kSlots; ++s) copy(s, first + s * step, at[s]);
     Place ahead = place(first + C::kSlots * step);            // of the next slice to copy
@@ -328,17 +336,22 @@ double estimate(const PagedAttnProblem& p, int* cluster) {
   return fmax(best, 3.8 + bytes / 6.8e6);
 }
 
-// f<T, D, HP>() for the problem's types and sizes.
+template <typename T_, int D_, int HP_>
+struct Types {
+  using T = T_;
+  static constexpr int D = D_, HP = HP_;
+};
+// f(Types) for the problem's type and sizes.
 template <typename F>
 auto with_types(nt_dtype dt, const PagedAttnProblem& p, const F& f) {
   const int G = p.H / p.pool.H;
   auto heads = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt == NT_BF16) return G <= 8 ? f.template operator()<bf16, D, 8>() : f.template operator()<bf16, D, 16>();
-    if (G == 1) return f.template operator()<float, D, 1>();
-    if (G == 2) return f.template operator()<float, D, 2>();
-    if (G <= 4) return f.template operator()<float, D, 4>();
-    return f.template operator()<float, D, 8>();
+    if (dt == NT_BF16) return G <= 8 ? f(Types<bf16, D, 8>()) : f(Types<bf16, D, 16>());
+    if (G == 1) return f(Types<float, D, 1>());
+    if (G == 2) return f(Types<float, D, 2>());
+    if (G <= 4) return f(Types<float, D, 4>());
+    return f(Types<float, D, 8>());
   };
   if (p.d == 32) return heads(std::integral_constant<int, 32>());
   if (p.d == 64) return heads(std::integral_constant<int, 64>());
@@ -348,11 +361,17 @@ auto with_types(nt_dtype dt, const PagedAttnProblem& p, const F& f) {
 }  // namespace
 
 double paged_attn_spread_us(nt_dtype dt, const PagedAttnProblem& p, int* cluster) {
-  return with_types(dt, p, [&]<typename T, int D, int HP>() { return estimate<T, D, HP>(p, cluster); });
+  return with_types(dt, p, [&](auto k) {
+    using K = decltype(k);
+    return estimate<typename K::T, K::D, K::HP>(p, cluster);
+  });
 }
 cudaError_t launch_paged_attn_spread(nt_dtype dt, const PagedAttnProblem& p, int cluster, unsigned int* status,
                                      cudaStream_t s) {
-  return with_types(dt, p, [&]<typename T, int D, int HP>() { return run<T, D, HP>(p, cluster, status, s); });
+  return with_types(dt, p, [&](auto k) {
+    using K = decltype(k);
+    return run<typename K::T, K::D, K::HP>(p, cluster, status, s);
+  });
 }
 
 }  // namespace nt

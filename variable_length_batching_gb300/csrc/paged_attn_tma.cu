@@ -27,9 +27,8 @@
 // matrix loads of a 32 KB stage take about a tenth of the time HBM takes to
 // deliver it.
 //
-// fp32 (plain rows): a key's row lies across the lanes; the lanes' partial
-// dot products of 32 (key, head) pairs are reduced together (butterfly32),
-// which leaves one score per lane.
+// fp32: packed multiply-adds, a key's columns in two lanes for the scores,
+// four columns of the output in each lane (paged_worker.cuh).
 //
 // At the end of a segment the eight warps leave their results in shared
 // memory for a fourth kind of warp, which merges them and writes the output
@@ -68,7 +67,8 @@ struct Cfg {
   static constexpr int kMergeWarps = HP == 16 ? kConsumers : 1;
   static constexpr uint32_t kQBytes = HP * kRow;
   static constexpr int kExtra = HP == 16 ? 3 : 2;             // an item's cost beside its tiles, in tiles
-  static constexpr uint32_t kFixed = kRedBufs * kRed + kQSlots * kQBytes + 4096 /* statistics, barriers, plan */;
+  static constexpr uint32_t kScratch = kConsumers * Worker<T, D, HP>::kScratch;
+  static constexpr uint32_t kFixed = kRedBufs * kRed + kQSlots * kQBytes + kScratch + 4096 /* statistics, barriers, plan */;
   // A multiple of the groups and of the producers: a stage is then always the
   // same warps' and they see every phase of its barriers.  (Otherwise a warp
   // would wait on a phase whose predecessor it never waited for, which parity
@@ -177,7 +177,8 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   uint8_t* stages = smem;
   float* red = reinterpret_cast<float*>(smem + S * C::kStage);
   uint8_t* qbuf = reinterpret_cast<uint8_t*>(red) + C::kRedBufs * C::kRed;
-  Ctl* ctl = reinterpret_cast<Ctl*>(qbuf + kQSlots * C::kQBytes);
+  uint8_t* scratch = qbuf + kQSlots * C::kQBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(scratch + C::kScratch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t cap = min64((int64_t)a.max_pages * a.page_size, 0x7fffffff);
   const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
@@ -345,7 +346,8 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       for (int h = threadIdx.x; h < a.H; h += kConsumers * 32) a.lse[(int64_t)h * a.B + b] = -INFINITY;
   }
   const int grp = warp / C::kSlices, slice = warp % C::kSlices;
-  Worker<T, D, HP> me(a.box, slice);
+  using W = Worker<T, D, HP>;
+  W me(a.box, slice, scratch + warp * W::kScratch);
   uint32_t it = 0, segs = 0;
   bool ok = true;
   while (ok && w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
@@ -355,7 +357,7 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     if (!ok) break;
     me.load_q(qbuf + slot * C::kQBytes, nh);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+    if (!W::kKeepsQ && lane == 0) mbar_arrive(&ctl->q_empty[slot]);
     bool active = false;
     for (int64_t t = w.t0; t < w.t1; ++t, ++it) {
       if (it % C::kGroups != (uint32_t)grp) continue;
@@ -371,6 +373,7 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       if (lane == 0) mbar_arrive(&ctl->empty[st]);
     }
     if (!ok) break;
+    if (W::kKeepsQ && lane == 0) mbar_arrive(&ctl->q_empty[slot]);
     ok = mbar_wait_warp(&ctl->red_empty[buf], ((segs / C::kRedBufs) & 1) ^ 1, &ctl->abort, a.status);
     if (!ok) break;
     me.result(ctl->m[buf][warp], ctl->l[buf][warp], red + buf * (C::kRed / 4) + warp * kHeads * C::kRedStride, nh,
@@ -415,14 +418,13 @@ cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s)
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.status = status;
   CUtensorMap maps[2];
-  // bf16: a page's rows as 64-column parts, so that one swizzled box holds them all; fp32: plain rows
-  constexpr uint32_t kCols = C::kBf16 && D > 64 ? 64 : D;
+  // a page's rows as 128-byte parts (64 for bf16 rows of 32), so that one swizzled box holds them all
+  constexpr uint32_t kCols = C::kRow < 128 ? D : 128 / sizeof(T);
   const uint64_t rows = (uint64_t)a.page_size;
   const uint64_t dims[4] = {kCols, rows, D / kCols, (uint64_t)a.n_pages * a.Hkv};
   const uint64_t strides[3] = {C::kRow, kCols * sizeof(T), C::kRow * rows};
   const uint32_t box[4] = {kCols, (uint32_t)a.box, D / kCols, 1};
-  constexpr CUtensorMapSwizzle kSwizzle = !C::kBf16 ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                          : D == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  constexpr CUtensorMapSwizzle kSwizzle = C::kRow < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   for (int i = 0; i < 2; ++i)
     if (!make_tmap(&maps[i], C::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, kSwizzle,
                    i ? p.pool.v : p.pool.k, 4, dims, strides, box))

@@ -25,46 +25,27 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// v[i] summed over the lanes, for i = this lane: halves the array and the
-// lane distance together (31 shuffles for 32 sums).
-__device__ __forceinline__ float butterfly32(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    const bool up = lane & m;
-#pragma unroll
-    for (int i = 0; i < m; ++i) {
-      const float give = up ? v[i] : v[i + m];
-      const float keep = up ? v[i + m] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-    }
-  }
-  return v[0];
-}
-
-template <int N>
-__device__ __forceinline__ void load_row(const float* p, float (&x)[N]) {
-  if constexpr (N == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else if constexpr (N == 2) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x[0] = v.x; x[1] = v.y;
-  } else {
-    x[0] = *p;
-  }
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 // A warp's query rows, running maxima, sums and outputs.  Its keys lie in a
-// stage: rows of kRow bytes, the values `side` bytes behind the keys; bf16
-// rows in boxes of `box` keys by 64 columns with the 128-byte swizzle (64-byte
-// for D = 32), fp32 rows plain.
+// stage, the values `side` bytes behind the keys, in boxes of `box` keys by
+// 128 bytes of their rows (64 for bf16 rows of 32) with the 128-byte (64-byte)
+// swizzle.  kScratch: bytes of shared memory a warp needs beside the stage.
+// kKeepsQ: whether the query rows stay where they are read from (then in
+// shared memory) until the item's end.
 template <typename T, int D, int HP>
 struct Worker;
 
 // bf16: matrix products.
 template <int D, int HP>
 struct Worker<bf16, D, HP> {
+  static constexpr uint32_t kScratch = 0;
+  static constexpr bool kKeepsQ = false;
   static constexpr int NT = HP / 8;
   static constexpr uint32_t kRow = D * 2;
   static constexpr int kRedStride = D + 4;      // floats: keeps the result's writes conflict-free
@@ -78,7 +59,7 @@ struct Worker<bf16, D, HP> {
   __device__ __forceinline__ uint32_t row_at(int r) const {
     return (uint32_t)(r / box) * box * kRow + r % box * kBoxRow;
   }
-  __device__ __forceinline__ Worker(int box_, int slice_) {
+  __device__ __forceinline__ Worker(int box_, int slice_, void*) {
     const int lane = threadIdx.x & 31;
     g = lane >> 2;
     tq = lane & 3;
@@ -189,8 +170,7 @@ struct Worker<bf16, D, HP> {
     if (left < 16) fence_async_shared();       // the zeros, before the next copy into this stage
   }
   // The whole item's output from this warp alone: rows [nh][D] at o, gathered
-  // in `rows` (shared, HP x D); and, after it, the heads' log-sum-exps: this
-  // lane's head (lanes with tq = 0), and head + 8.
+  // in `rows` (shared, HP x D).
   __device__ __forceinline__ void finish(bf16* rows, bf16* o_, int nh) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -213,9 +193,12 @@ struct Worker<bf16, D, HP> {
       reinterpret_cast<uint4*>(o_)[e] = reinterpret_cast<const uint4*>(rows)[e];
     __syncwarp();
   }
-  __device__ __forceinline__ int head_of_lane() const { return tq == 0 ? g : -1; }
-  __device__ __forceinline__ float head_lse() const { return (m[0] + log2f(l[0])) * 0.6931471805599453f; }
-  __device__ __forceinline__ float head_lse1() const { return (m[NT - 1] + log2f(l[NT - 1])) * 0.6931471805599453f; }
+  // the heads' log-sum-exps, after finish
+  __device__ __forceinline__ void store_lse(float* lse, int64_t stride, int nh) const {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (tq == 0 && n * 8 + g < nh) lse[(n * 8 + g) * stride] = (m[n] + log2f(l[n])) * 0.6931471805599453f;
+  }
   // the warp's result: maxima and sums (-1: no keys, nothing to add), outputs [HP][kRedStride]
   __device__ __forceinline__ void result(float* rm, float* rl, float* ro, int nh, bool active) {
 #pragma unroll
@@ -244,114 +227,181 @@ struct Worker<bf16, D, HP> {
   }
 };
 
-// fp32: D / 32 elements of a row per lane, batches of KB keys x HP heads.
+// fp32, on the CUDA cores, in packed pairs.  Scores: a lane has one key and
+// half of its columns against all heads, whose rows it reads as broadcasts;
+// the halves are added, and each half of the warp keeps every other head.
+// Outputs: a lane has four columns of all heads and every kGroups-th key, the
+// probabilities read as broadcasts from the warp's scratch.  (Columns across the
+// lanes and sums by shuffles take 31 shuffles for 32 scores, and one more for
+// every probability and head: the ragged batch of 64 with 8 key heads of 64 and
+// eight heads to each takes 102 us that way, 64 this, with d = 32 and one 49
+// and 32.)
 template <int D, int HP>
 struct Worker<float, D, HP> {
+  static constexpr uint32_t kScratch = 16 * HP * 4;
+  static constexpr bool kKeepsQ = true;
   static constexpr uint32_t kRow = D * 4;
   static constexpr int kRedStride = D + 4;
-  static constexpr int N = D / 32, KB = 32 / HP < 16 ? 32 / HP : 16;
-  float q[HP][N], o[HP][N];
-  float m, l;                      // of head lane % HP
-  int slice;
+  static constexpr int kMine = HP > 1 ? HP / 2 : 1;      // heads whose softmax this lane keeps: 2 i + half
+  static constexpr int kGroups = 128 / D;                // keys side by side in the output's product
+  static constexpr int kAcc = D == 128 ? 8 : 4;          // sums a dot product is split into
+  float m[kMine], l[kMine], o[HP][4];                    // l: of this lane's keys
+  const float* q;
+  float* p;                                              // probabilities [16][HP]
+  int slice, half, grp;
+  uint32_t hs, k_off, k_x, v_off, v_x, v_jump;
 
-  __device__ __forceinline__ Worker(int, int slice_) : slice(slice_) {}
-  __device__ __forceinline__ void load_q(const void* rows, int nh) {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ Worker(int box, int slice_, void* scratch) : p(static_cast<float*>(scratch)), slice(slice_) {
+    const int lane = threadIdx.x & 31, c = lane % (D / 4);
+    half = lane >> 4;
+    grp = lane / (D / 4);
+    hs = box * 128;                                      // to a box's next 32 columns
+    auto row_at = [&](int r) { return (uint32_t)(r / box) * box * kRow + r % box * 128; };
+    k_off = row_at(slice * 16 + (lane & 15)) + half * (D / 64) * hs;
+    k_x = ((D == 32 ? half * 4 : 0) ^ (lane & 7)) << 4;
+    v_off = row_at(slice * 16) + (c >> 3) * hs + grp * 128;
+    v_x = ((c & 7) ^ grp) << 4;
+    v_jump = box == 8 ? 8 * kRow : 1024;                 // to the slice's second eight rows
+  }
+  // HP query rows (those behind the item's heads may hold anything)
+  __device__ __forceinline__ void load_q(const void* rows, int) {
+    q = static_cast<const float*>(rows);
 #pragma unroll
-    for (int h = 0; h < HP; ++h) {
-#pragma unroll
-      for (int c = 0; c < N; ++c) q[h][c] = o[h][c] = 0.f;
-      if (h < nh) load_row<N>(reinterpret_cast<const float*>(rows) + h * D + lane * N, q[h]);
+    for (int i = 0; i < kMine; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
     }
-    m = -INFINITY;
-    l = 0.f;
+#pragma unroll
+    for (int h = 0; h < HP; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[h][c] = 0.f;
   }
   __device__ __forceinline__ void tile(const uint8_t* stage, uint32_t side, int left, float scale_log2) {
-    const int lane = threadIdx.x & 31;
-    const float* k = reinterpret_cast<const float*>(stage) + slice * 16 * D + lane * N;
-    const float* v = k + side / 4;
+    const int lane = threadIdx.x & 31, key = lane & 15;
+    const uint32_t k = smem_u32(stage) + k_off, v = smem_u32(stage) + side + v_off, qs = smem_u32(q + half * (D / 2));
+    float acc[HP][kAcc] = {};
 #pragma unroll
-    for (int b = 0; b < 16; b += KB) {
-      if (b >= left) break;
-      float s[32];
+    for (int i = 0; i < D / 8; ++i) {
+      const float4 x = lds4(k + (i >> 3) * hs + (((i & 7) << 4) ^ k_x));
+      const int a = kAcc == 8 ? (i & 1) * 4 : 0;
 #pragma unroll
-      for (int j = 0; j < 32 / HP; ++j) {
-        float x[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) x[c] = 0.f;
-        if (j < KB && b + j < left) load_row<N>(k + (b + j) * D, x);
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          float d = 0.f;
-#pragma unroll
-          for (int c = 0; c < N; ++c) d = fmaf(q[h][c], x[c], d);
-          s[j * HP + h] = d;
-        }
-      }
-      float sc = butterfly32(s) * scale_log2;        // of key b + lane / HP, head lane % HP
-      if (lane / HP >= KB || b + lane / HP >= left) sc = -INFINITY;
-      float mx = sc;
-#pragma unroll
-      for (int d = HP; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float mn = fmaxf(m, mx);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float corr = exp2f(m - base), pr = exp2f(sc - base);
-      float sum = pr;
-#pragma unroll
-      for (int d = HP; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const bool moved = mn > m;
-      l = l * corr + sum;
-      m = mn;
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          const float ch = __shfl_sync(0xffffffffu, corr, h);
-#pragma unroll
-          for (int c = 0; c < N; ++c) o[h][c] *= ch;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        if (b + j >= left) break;                    // rows behind the last key may hold anything
-        float x[N];
-        load_row<N>(v + (b + j) * D, x);
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          const float pj = __shfl_sync(0xffffffffu, pr, j * HP + h);
-#pragma unroll
-          for (int c = 0; c < N; ++c) o[h][c] = fmaf(pj, x[c], o[h][c]);
-        }
+      for (int h = 0; h < HP; ++h) {
+        const float4 y = lds4(qs + (h * D + 4 * i) * 4);
+        ffma2(x.x, x.y, y.x, y.y, acc[h][a], acc[h][a + 1], acc[h][a], acc[h][a + 1]);
+        ffma2(x.z, x.w, y.z, y.w, acc[h][a + 2], acc[h][a + 3], acc[h][a + 2], acc[h][a + 3]);
       }
     }
+    float s[HP];
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+      s[h] = (acc[h][0] + acc[h][1]) + (acc[h][2] + acc[h][3]);
+      if constexpr (kAcc == 8) s[h] += (acc[h][4] + acc[h][5]) + (acc[h][6] + acc[h][7]);
+    }
+    float corr[kMine];
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      float t;
+      if constexpr (HP == 1) t = s[0] + __shfl_xor_sync(0xffffffffu, s[0], 16);
+      else t = (half ? s[2 * i + 1] : s[2 * i]) + __shfl_xor_sync(0xffffffffu, half ? s[2 * i] : s[2 * i + 1], 16);
+      t = key < left ? t * scale_log2 : -INFINITY;       // rows behind the last key may hold anything
+      float mx = t;
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+      moved |= mn > m[i];
+      corr[i] = exp2f(m[i] - base);
+      m[i] = mn;
+      const float pr = exp2f(t - base);
+      l[i] = l[i] * corr[i] + pr;
+      if (HP > 1 || half == 0) p[key * HP + (HP > 1 ? 2 * i + half : 0)] = pr;
+    }
+    __syncwarp();
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        const float c = __shfl_sync(0xffffffffu, corr[h / 2], (h & 1) * 16);
+        fmul2(o[h][0], o[h][1], c, c, o[h][0], o[h][1]);
+        fmul2(o[h][2], o[h][3], c, c, o[h][2], o[h][3]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += kGroups) {              // key j + grp
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j + grp < left) x = lds4(v + (j >> 3) * v_jump + (j & 7) * 128 + (v_x ^ ((j & 7) << 4)));
+      float pr[HP];
+      const float* pk = p + (j + grp) * HP;
+      if constexpr (HP == 1) {
+        pr[0] = *pk;
+      } else if constexpr (HP == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(pk);
+        pr[0] = y.x;
+        pr[1] = y.y;
+      } else {
+#pragma unroll
+        for (int h = 0; h < HP; h += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(pk + h);
+          pr[h] = y.x;
+          pr[h + 1] = y.y;
+          pr[h + 2] = y.z;
+          pr[h + 3] = y.w;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        ffma2(x.x, x.y, pr[h], pr[h], o[h][0], o[h][1], o[h][0], o[h][1]);
+        ffma2(x.z, x.w, pr[h], pr[h], o[h][2], o[h][3], o[h][2], o[h][3]);
+      }
+    }
+    __syncwarp();                                        // the scratch is free again
+  }
+  // the sums over all keys, in every lane that keeps or holds them
+  __device__ __forceinline__ void gather() {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+#pragma unroll
+    for (int x = D / 4; x < 32; x <<= 1)
+#pragma unroll
+      for (int h = 0; h < HP; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[h][c] += __shfl_xor_sync(0xffffffffu, o[h][c], x);
   }
   __device__ __forceinline__ void finish(float*, float* o_, int nh) {
     const int lane = threadIdx.x & 31;
+    gather();
 #pragma unroll
     for (int h = 0; h < HP; ++h) {
-      const float inv = 1.f / __shfl_sync(0xffffffffu, l, h);
-      if (h < nh) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) o_[h * D + lane * N + c] = o[h][c] * inv;
-      }
+      const float inv = 1.f / __shfl_sync(0xffffffffu, l[h / 2], (h & 1) * 16);
+      if (h < nh && lane < D / 4)
+        *reinterpret_cast<float4*>(o_ + h * D + 4 * lane) =
+            make_float4(o[h][0] * inv, o[h][1] * inv, o[h][2] * inv, o[h][3] * inv);
     }
   }
-  __device__ __forceinline__ int head_of_lane() const {
-    const int lane = threadIdx.x & 31;
-    return lane < HP ? lane : -1;
+  __device__ __forceinline__ void store_lse(float* lse, int64_t stride, int nh) const {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int h = 2 * i + half;
+      if ((threadIdx.x & 15) == 0 && h < nh) lse[h * stride] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
+    }
   }
-  __device__ __forceinline__ float head_lse() const { return (m + log2f(l)) * 0.6931471805599453f; }
   __device__ __forceinline__ void result(float* rm, float* rl, float* ro, int nh, bool active) {
     const int lane = threadIdx.x & 31;
-    if (lane < HP) {
-      rm[lane] = m;
-      rl[lane] = active ? l : -1.f;
+    gather();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int h = 2 * i + half;
+      if ((lane & 15) == 0 && h < HP) {
+        rm[h] = m[i];
+        rl[h] = active ? l[i] : -1.f;
+      }
     }
-    if (!active) return;
+    if (!active || lane >= D / 4) return;
 #pragma unroll
     for (int h = 0; h < HP; ++h)
       if (h < nh)
-#pragma unroll
-        for (int c = 0; c < N; ++c) ro[h * kRedStride + lane * N + c] = o[h][c];
+        *reinterpret_cast<float4*>(ro + h * kRedStride + 4 * lane) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
   }
 };
 
@@ -372,10 +422,8 @@ __device__ __forceinline__ void copy_slice(uint32_t dst, const void* k, const vo
   for (int r0 = 0; r0 < 16; r0 += kRowsAt) {
     const int r = r0 + (kRowsAt > 1 ? lane / kChunks : 0), c = lane % kChunks;
     const int64_t at = __shfl_sync(0xffffffffu, row, r);
-    // bf16: 64-column halves of 16 rows, swizzled as the worker reads them
     uint32_t to;
-    if constexpr (sizeof(T) == 4) to = r * kRow + c * 16;
-    else if constexpr (D == 32) to = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    if constexpr (kRow == 64) to = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
     else to = (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     const int64_t from = at < 0 ? 0 : at * kRow + c * 16;
     copy16_or_zero(dst + to, static_cast<const uint8_t*>(k) + from, at >= 0);
