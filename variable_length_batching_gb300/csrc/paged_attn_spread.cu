@@ -316,7 +316,7 @@ template <typename T, int D, int HP>
 double estimate(const PagedAttnProblem& p, int* cluster) {
   using C = Cfg<T, D, HP>;
   const double first = HP == 16 ? 5.0 : C::kRow <= 128 ? 3.9 : 4.1;
-  const double t = C::kBf16 ? (HP == 16 ? 1.35 : D == 128 ? 0.9 : D == 64 ? 0.75 : 0.6) : (D == 128 ? 2.0 : 1.5) * (HP == 8 ? 1.5 : 1);
+  const double t = C::kBf16 ? (HP == 16 ? 1.35 : D == 128 ? 0.9 : D == 64 ? 0.75 : 0.6) : (D == 128 ? 2.0 : D == 64 ? 1.5 : 0.9) * (HP == 8 ? 1.5 : 1);
   const int64_t items = paged_items(p, HP), cap = paged_cap(p), slices = (cap + 15) / 16;
   double best = INFINITY;
   *cluster = 1;
