@@ -441,7 +441,7 @@ inline double paged_mean_part(const PagedAttnProblem& p) { return 0.35 + 0.65 / 
 // The three kernels, each with its estimate of the call's time in
 // microseconds (infinite where it does not take the call).
 // A warp per item, for tables of at most kPagedShortKeys positions.
-constexpr int kPagedShortKeys = 128;
+constexpr int kPagedShortKeys = 1024;
 double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 // A cluster of CTAs per item; any page size.

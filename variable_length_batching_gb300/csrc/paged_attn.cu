@@ -117,18 +117,14 @@ cudaError_t launch_paged_join(nt_dtype dt, const PagedAttnProblem& p, int ctas, 
   return dt == NT_BF16 ? join<bf16>(p, ctas, items, heads, s) : join<float>(p, ctas, items, heads, s);
 }
 
-// The kernel with the least estimated time, by the sizes of the tables.  The
-// tile kernel alone keeps its time when a few sequences are much longer than
-// the others, so a batch goes to the clusters only with a fifth to spare (16
-// contexts of up to 4,688 keys, most of them far shorter, 8 key heads of 128:
-// 17.6 us there, 27.4 here; all of 4,000: 46.9 and 41.9).
+// The kernel with the least estimated time, by the sizes of the tables.
 cudaError_t launch_paged_attn(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
   int cluster = 1;
   const double apart = paged_attn_short_us(dt, p), tiles = paged_attn_tma_us(dt, p);
   const double spread = paged_attn_spread_us(dt, p, &cluster);
   if (apart <= tiles && apart <= spread) return launch_paged_attn_short(dt, p, status, s);
-  if (spread < tiles * (p.B > 1 ? 0.8 : 1)) return launch_paged_attn_spread(dt, p, cluster, status, s);
+  if (spread < tiles) return launch_paged_attn_spread(dt, p, cluster, status, s);
   return launch_paged_attn_tma(dt, p, status, s);
 }
 

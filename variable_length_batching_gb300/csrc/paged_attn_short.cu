@@ -1,5 +1,5 @@
-// Attention of one new token per sequence over short paged contexts: one warp
-// per item (a sequence's key head with up to HP of its query heads).
+// Attention of one new token per sequence over many short paged contexts: one
+// warp per item (a sequence's key head with up to HP of its query heads).
 //
 // With block tables of a few pages there is nothing to split and little to
 // stream; what an item costs is the chain length -> pages -> keys -> scores ->
@@ -183,14 +183,18 @@ cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, 
 
 }  // namespace
 
-// About 1.0 us and, for every round of items on the warps, 1.6 us and 1.05 us
-// a slice of 16 keys.
+// About 1 us, 1.6 us an item and t a slice of 16 keys, more when all warps are
+// busy; as long as the longest item, or as the warps' shares.
 double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p) {
   const int64_t cap = paged_cap(p);
   if (cap > kPagedShortKeys || p.pool.n_pages == 0) return INFINITY;
-  const int64_t warps = sm_count() * (dt == NT_BF16 || p.d < 128 ? 12 : 6);
-  const int64_t items = paged_items(p, dt == NT_BF16 && p.H / p.pool.H > 8 ? 16 : 8);
-  return 1.0 + (double)((items + warps - 1) / warps) * (1.6 + 1.05 * (double)((cap + 15) / 16));
+  const int G = p.H / p.pool.H, HP = dt == NT_BF16 && G > 8 ? 16 : 8;
+  const double rounds = (double)paged_items(p, HP) / (double)(sm_count() * (dt == NT_BF16 || p.d < 128 ? 12 : 6));
+  const double t = (dt == NT_F32 ? (p.d == 128 ? 1.65 : 0.9) : HP == 16 ? 0.95 : 0.85) +
+                   (p.d == 128 && (HP == 16 || dt == NT_F32) ? 1.0 : 0.5) * fmin(1, rounds);
+  const double keys = (double)((cap + 15) / 16) * t;
+  const double bytes = (double)p.B * p.pool.H * cap * p.d * 2 * (dt == NT_BF16 ? 2 : 4) * paged_mean_part(p);
+  return fmax(1.0 + fmax(1.6 + keys, rounds * (1.6 + keys * paged_mean_part(p))), 3.8 + bytes / 6.1e6);
 }
 
 cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {

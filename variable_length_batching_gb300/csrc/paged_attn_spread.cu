@@ -310,13 +310,16 @@ cudaError_t run(const PagedAttnProblem& p, int cluster, unsigned int* status, cu
 
 // Estimated time (us) and the cluster's size.  A CTA takes about 4 us with one
 // round of slices on its warps, and t for each further one.  The clusters that
-// fit on the device at once (two CTAs on an SM) run together; each later wave
-// takes a little more than the first.  HBM gives 6.8 TB/s.
+// fit on the device at once (two CTAs on an SM) run together.  A batch waits for
+// its longest items, so theirs count a quarter more: 16 contexts of up to 4,688
+// keys, most of them far shorter, 8 key heads of 128, take 27.4 us here and
+// 17.6 on the tile kernel, which deals them out evenly; all of 4,000 41.9 and
+// 46.9.  HBM gives 6.8 TB/s.
 template <typename T, int D, int HP>
 double estimate(const PagedAttnProblem& p, int* cluster) {
   using C = Cfg<T, D, HP>;
   const double first = HP == 16 ? 5.0 : C::kRow <= 128 ? 3.9 : 4.1;
-  const double t = C::kBf16 ? (HP == 16 ? 1.35 : D == 128 ? 0.9 : D == 64 ? 0.75 : 0.6) : (D == 128 ? 2.0 : D == 64 ? 1.5 : 0.9) * (HP == 8 ? 1.5 : 1);
+  const double t = C::kBf16 ? (HP == 16 ? 1.35 : D == 128 ? 0.9 : D == 64 ? 0.75 : 0.6) : (D == 128 ? 1.7 : D == 64 ? 1.3 : 0.9) * (HP == 8 ? 1.5 : 1);
   const int64_t items = paged_items(p, HP), cap = paged_cap(p), slices = (cap + 15) / 16;
   double best = INFINITY;
   *cluster = 1;
@@ -326,7 +329,7 @@ double estimate(const PagedAttnProblem& p, int* cluster) {
     if (fit <= 0) continue;
     const double waves = (double)((items + fit - 1) / fit);
     const double rounds = fmax(1, (double)((slices + c * C::kWarps - 1) / (c * C::kWarps)));
-    const double more = (rounds - 1) * t, us = first + more + (waves - 1) * (5.3 + 1.2 * more);
+    const double more = (rounds - 1) * t, us = first + more * (p.B > 1 ? 1.25 : 1) + (waves - 1) * (5.3 + more);
     if (us < best) {
       best = us;
       *cluster = c;

@@ -452,20 +452,19 @@ cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, 
 
 }  // namespace
 
-// Items kept whole: about 5 us and, for every round of them on the SMs, 0.6
-// us and 0.75 us a 32 KB of keys and values, twice that with 16 heads.  Split:
-// 8 us (the plan, the ragged end, the join; 11 with 16 heads) and 6.1 TB/s, an
-// item's own cost counted as 64 to 96 KB.
+// An item costs an SM 0.5 us and 1.4 ns for each of its outputs.  Items kept
+// whole: about 5 us and, for every round of them on the SMs, that and 0.75 us
+// a 32 KB of keys and values.  Split: 8 us (the plan, the ragged end, the
+// join; 11 with 16 heads), their cost, and 6.1 TB/s.
 double paged_attn_tma_us(nt_dtype dt, const PagedAttnProblem& p) {
   if (p.pool.page_size % 8 || p.pool.n_pages == 0) return INFINITY;
-  const int es = dt == NT_BF16 ? 2 : 4, HP = dt == NT_BF16 && p.H / p.pool.H > 8 ? 16 : 8;
-  const int64_t items = paged_items(p, HP), sms = sm_count();
-  const double item_bytes = (double)paged_cap(p) * p.d * es * 2;
+  const int es = dt == NT_BF16 ? 2 : 4, G = p.H / p.pool.H, HP = dt == NT_BF16 && G > 8 ? 16 : 8;
+  const double rounds = (double)paged_items(p, HP) / sm_count(), own = 0.5 + 0.0014 * min(G, HP) * p.d;
+  const double keys = (double)paged_cap(p) * p.d * es * 2, mean = paged_mean_part(p);
   if (paged_whole_items(p, es))
-    return (p.d == 128 ? 5.3 : 4.3) +
-           (double)((items + sms - 1) / sms) * (0.6 + 0.75 * item_bytes / 32768) * (HP == 16 ? 2 : 1);
-  const double bytes = (double)p.B * p.pool.H * item_bytes * paged_mean_part(p);
-  return (HP == 16 ? 11 : p.d == 128 ? 8.5 : 8) + (bytes + (double)items * (HP == 16 ? 98304 : 65536)) / 6.1e6;
+    return (p.d == 128 ? 4.8 : 4.3) + own + 0.75 * keys / 32768 +
+           fmax(0, rounds - 1) * (own + 0.75 * keys / 32768 * mean);
+  return (HP == 16 ? 11 : p.d == 128 ? 8.5 : 8) + rounds * own + (double)p.B * p.pool.H * keys * mean / 6.1e6;
 }
 
 cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
