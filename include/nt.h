@@ -789,8 +789,9 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  *                 overlap an input.
  *   workspace     >= nt_paged_attn_workspace_bytes(H, H_kv, d) bytes, 16-byte aligned.
  * The softmax statistics and sums are fp32; bf16 probabilities are rounded to
- * bf16 before they multiply the values where tensor cores form the product.
- * Results do not depend on scheduling.  Asynchronous.
+ * bf16 before they multiply the values.  Results do not depend on scheduling;
+ * their rounding may depend on B and max_pages, by which the kernel is chosen.
+ * Asynchronous.
  */
 nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,
                         const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,

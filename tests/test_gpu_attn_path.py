@@ -3,6 +3,7 @@
 varlen attention, then one token at a time over the paged cache, with forks,
 frees and compaction on the way)."""
 import math
+import os
 
 import numpy as np
 import pytest
@@ -285,3 +286,40 @@ def test_cache_on_two_streams(mods):
         got = [cache.attend(step, x, stream=s) for x, s in zip(q, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got + [replayed], want + [want[2]]))
+
+
+def test_first_calls_captured():
+    """A process whose first calls of the library are captured ones: what a
+    kernel has to be allowed or asked first goes on under a capture."""
+    import subprocess
+    import sys
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    code = """
+import torch
+from variable_length_batching_gb300 import nt
+D, B = "cuda", torch.bfloat16
+pages = nt.KVPages(torch.randn(640, 2, 16, 64, device=D, dtype=B), torch.randn(640, 2, 16, 64, device=D, dtype=B))
+q, k = torch.randn(3, 8, 64, device=D, dtype=B), torch.randn(3, 2, 64, device=D, dtype=B)
+turns, gamma = nt.nt_rope_turns(64, device=D), torch.ones(64, device=D)
+cu, one = (torch.tensor(x, dtype=torch.int32, device=D) for x in ([0, 1, 2, 3], [700, 30, 0]))
+tables = [torch.arange(3 * w, dtype=torch.int32, device=D).reshape(3, w) % 640 for w in (2, 50, 12500)]
+
+def step():
+    a, b = nt.nt_qk_norm_rope(q, k, turns, cu_seqlens=cu, pos0=one, q_gamma=gamma, k_gamma=gamma)
+    g = nt.nt_qk_norm_rope_bwd(a, b, turns, q=q, k=k, cu_seqlens=cu, pos0=one, q_gamma=gamma, k_gamma=gamma)
+    o = [nt.nt_paged_attn(pages, a, t, one.clamp(max=16 * t.shape[1]), want_lse=True) for t in tables]
+    return [a, b, *g] + [x for y in o for x in y]
+
+s = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=s):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, step()))
+nt.nt_device_status()
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -258,10 +258,9 @@ cudaLaunchConfig_t spread_config(int cluster, cudaLaunchAttribute (&attr)[2]) {
 // Clusters that run at once, asked for once per device (GPCs differ in size,
 // so it is not the SMs' number over the cluster's).  0 if that fails.
 template <typename T, int D, int HP>
-int clusters_fit(int cluster) {
+int clusters_fit(int dev, int cluster) {
   static std::atomic<int> known[64][kMaxCluster + 1];                // plus 1; 0: not asked yet
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = 0;
   if (dev < 64 && (n = known[dev][cluster].load(std::memory_order_relaxed)) > 0) return n - 1;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = spread_config<T, D, HP>(cluster, attr);
@@ -323,9 +322,11 @@ double estimate(const PagedAttnProblem& p, int* cluster) {
   const int64_t items = paged_items(p, HP), cap = paged_cap(p), slices = (cap + 15) / 16;
   double best = INFINITY;
   *cluster = 1;
+  int dev = 64;                                                      // 64: asked for every time
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
   for (int c = 1; c <= kMaxCluster; ++c) {
     if (c > 1 && (int64_t)(c - 1) * C::kWarps >= slices) break;    // the CTAs before it have them all
-    const int64_t fit = c > 1 ? clusters_fit<T, D, HP>(c) : max(clusters_fit<T, D, HP>(1), 1);
+    const int64_t fit = c > 1 ? clusters_fit<T, D, HP>(dev, c) : max(clusters_fit<T, D, HP>(dev, 1), 1);
     if (fit <= 0) continue;
     const double waves = (double)((items + fit - 1) / fit);
     const double rounds = fmax(1, (double)((slices + c * C::kWarps - 1) / (c * C::kWarps)));
