@@ -11,7 +11,7 @@
 // that the caller does not give are allocated on the call's stream.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -128,8 +128,13 @@ struct Call {
   }
 };
 
-T like(const T& t) { return at::empty(t.sizes(), t.options()); }
-T bytes(size_t n, const T& t) { return at::empty({(int64_t)n}, t.options().dtype(at::kByte)); }
+// A new contiguous tensor, without the dispatcher's way to the allocator.
+T fresh(at::IntArrayRef sizes, at::ScalarType type, int index) {
+  return T(at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)),
+                                  std::nullopt));
+}
+T like(const T& t) { return fresh(t.sizes(), t.scalar_type(), t.get_device()); }
+T bytes(size_t n, const T& t) { return fresh({(int64_t)n}, at::kByte, t.get_device()); }
 void* data(const T& t) { return t.defined() ? t.data_ptr() : nullptr; }
 bool same_shape(const T& a, const T& b) { return a.defined() == b.defined() && (!a.defined() || a.sizes() == b.sizes()); }
 
@@ -257,8 +262,8 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a, Py_ssize_t n) {
   T dq, dk, dqg, dkg, ws = tensor(a[13], "workspace");
   if (uq.defined()) dq = like(uq);
   if (uk.defined()) dk = like(uk);
-  if (qg.defined()) dqg = at::empty({r.d}, qg.options());
-  if (kg.defined()) dkg = at::empty({r.d}, kg.options());
+  if (qg.defined()) dqg = like(qg);
+  if (kg.defined()) dkg = like(kg);
   if (ws.defined()) {
     on_device(ws, r.index, "workspace");
     if (!ws.is_contiguous()) refuse("workspace must be contiguous");
@@ -345,7 +350,7 @@ PyObject* paged_attn(PyObject* const* a, Py_ssize_t n) {
   T out = tensor(a[6], "out"), lse = tensor(a[7], "lse"), ws = tensor(a[9], "workspace");
   if (!out.defined()) out = like(q);
   else if (out.sizes() != q.sizes()) refuse("out must have q's shape");
-  if (!lse.defined() && flag(a[8])) lse = at::empty({H, B}, q.options().dtype(at::kFloat));
+  if (!lse.defined() && flag(a[8])) lse = fresh({H, B}, at::kFloat, g.index);
   if (lse.defined() && (lse.dim() != 2 || lse.size(0) != H || lse.size(1) != B)) refuse("lse must be (H, B)");
   if (ws.defined()) {
     on_device(ws, g.index, "workspace");
