@@ -303,3 +303,13 @@ def test_side_stream(nt):
 def test_layout_columns():
     a, b = columns(8, True)
     assert a.tolist() == [0, 2, 4, 6] and b.tolist() == [1, 3, 5, 7]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", range(16, 257, 16))
+def test_every_width(nt, d, dtype):
+    """Every head width, whole and a part rotated: forward and gradients."""
+    for rot, inter in ((d, False), (max(16, d // 32 * 16), True)):
+        case = ([33, 0, 5, 1], [4, 0, 90, 1000], 3, 2, d, rot, inter, True, True, {}, 1.0)
+        test_forward(nt, case, dtype)
+        test_backward(nt, case, dtype)

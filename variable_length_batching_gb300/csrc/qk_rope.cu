@@ -16,13 +16,13 @@
 // Both directions are bound by HBM (65,536 tokens of 12 + 12 heads of 64 in
 // bf16: forward 68.6 us, 86% of the measured copy rate, backward 97 us, 92%;
 // 16,384 of 32 + 8 of 128: 55.3 and 80.8 us, 89% and 92%), and at about ten
-// operations an element not by much, so the layout keeps loads in flight without holding registers
-// or waiting at barriers.  A row (one head of one token) is a group of LP
-// lanes, a lane one eighth or less of it: 16 elements in 16-byte words spread
+// operations an element not by much, so the layout keeps loads in flight
+// without holding registers or waiting at barriers.  A row (one head of one
+// token) is a group of LP lanes, 16 elements to a lane in 16-byte words spread
 // over the row so that the words of neighbouring lanes are neighbours, and so
 // that a lane holds both columns of its eight pairs in either layout.  A warp
-// takes units of 32 / LP tokens and some consecutive heads of q or of k, one
-// row per group and step.  Units are dealt out in order, a round at a time:
+// takes units of some tokens and consecutive heads of q or of k, one row per
+// group and step.  Units are dealt out in order, a round at a time:
 // all warps work in one region of memory (giving each warp a range of its own
 // costs a tenth of the bandwidth), and the unit's heads are chosen so that
 // the rounds come out even.  Each thread copies its own words of the rows
@@ -110,18 +110,21 @@ __device__ __forceinline__ bool lane_position(const Args& a, int64_t t, int64_t 
 template <typename T, int LP, bool kInter>
 struct Lane {
   static constexpr int V = 16 / sizeof(T), W = 16 / V;
+  static constexpr int kGroups = 32 / LP;                         // a warp's (lanes behind the last one idle)
   static constexpr int kRow = LP * 16 * sizeof(T);                // bytes of a row, at most
   static constexpr int kSide = kRow >= 128 ? 1 : 128 / kRow;      // rows of one token in a step, side by side
-  static constexpr int kTok = 32 / LP / kSide;                    // tokens of a step
+  static constexpr int kTok = kGroups / kSide;                    // tokens of a step
   int i, tok, h_off, col0, step;
   bool on, rotated;
   __device__ __forceinline__ Lane(const Args& a) {
-    i = threadIdx.x % LP;
-    const int g = threadIdx.x % 32 / LP;
+    const int lane = threadIdx.x & 31;
+    const bool idle = lane >= kGroups * LP;
+    const int g = idle ? 0 : lane / LP;
+    i = lane % LP;
     tok = g / kSide;
     h_off = g % kSide;
-    on = 16 * i < a.d;
-    rotated = 16 * i < a.rot;
+    on = !idle && 16 * i < a.d;
+    rotated = !idle && 16 * i < a.rot;
     const int first = rotated ? 0 : a.rot, width = rotated ? a.rot : a.d - a.rot;
     col0 = first + V * (i - first / 16);
     step = width / W;
@@ -187,11 +190,34 @@ struct Lane {
   }
 };
 
+// v summed over a row's lanes, in one order for all of them.
 template <int LP>
 __device__ __forceinline__ float group_sum(float v) {
+  if constexpr ((LP & (LP - 1)) == 0) {
 #pragma unroll
-  for (int m = LP / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
+    for (int m = LP / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  } else {
+    const int first = (threadIdx.x & 31) / LP * LP;
+    float s = 0.f;
+#pragma unroll
+    for (int m = 0; m < LP; ++m) s += __shfl_sync(0xffffffffu, v, min(first + m, 31));
+    return s;
+  }
+}
+// v summed over a warp's rows, for lanes below LP.
+template <int LP>
+__device__ __forceinline__ float rows_sum(float v) {
+  if constexpr ((LP & (LP - 1)) == 0) {
+#pragma unroll
+    for (int m = 16; m >= LP; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  } else {
+    float s = v;
+#pragma unroll
+    for (int g = 1; g < 32 / LP; ++g) s += __shfl_sync(0xffffffffu, v, ((threadIdx.x & 31) + g * LP) & 31);
+    return s;
+  }
 }
 
 // The thread's own words of the ring: 16-byte word w of slot s at
@@ -478,9 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
   auto put_away = [&](int sd) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float v = acc[e];
-#pragma unroll
-      for (int x = 16; x >= LP; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+      const float v = rows_sum<LP>(acc[e]);
       if (lane < LP && me.on) red[(warp * 2 + sd) * a.d + me.col(e / me.V) + e % me.V] = v;
       acc[e] = 0.f;
     }
@@ -585,10 +609,14 @@ __global__ void __launch_bounds__(1024) rope_dgamma_kernel(const float* partial,
   if (col == 0 && blockIdx.x * 32 + w < d) out[blockIdx.x * 32 + w] = v;
 }
 
+// Lanes of a row: those that leave the fewest of a warp's idle (d = 80: five,
+// 30 lanes of 32 at work instead of 20 with eight, 38.5 -> 33.1 us for 30,000
+// tokens of 15 heads; d = 160: ten, 71.7 -> 54.3 for 25,000 of 18).
 int group_lanes(int d) {
-  int lp = 1;
-  while (16 * lp < d) lp <<= 1;
-  return lp;
+  int best = 16;
+  for (int lp : {10, 8, 6, 5, 4, 2, 1})
+    if (16 * lp >= d && 32 / lp > 32 / best) best = lp;
+  return best;
 }
 
 template <typename T, int LP, bool kInter>
@@ -608,6 +636,9 @@ cudaError_t run_lp(const Args& a, bool bwd, int grid, cudaStream_t s) {
     case 1: return run<T, 1, kInter>(a, bwd, grid, s);
     case 2: return run<T, 2, kInter>(a, bwd, grid, s);
     case 4: return run<T, 4, kInter>(a, bwd, grid, s);
+    case 5: return run<T, 5, kInter>(a, bwd, grid, s);
+    case 6: return run<T, 6, kInter>(a, bwd, grid, s);
+    case 10: return run<T, 10, kInter>(a, bwd, grid, s);
     case 8: return run<T, 8, kInter>(a, bwd, grid, s);
     default: return run<T, 16, kInter>(a, bwd, grid, s);
   }
