@@ -323,3 +323,38 @@ nt.nt_device_status()
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads(mods):
+    """Calls from two host threads at once, each on a stream of its own."""
+    import threading
+    nt, _, _ = mods
+    pages = nt.KVPages(*(torch.randn(300, 2, 16, 64, device=DEV, dtype=BF) for _ in range(2)))
+    table = torch.arange(300, dtype=torch.int32, device=DEV).reshape(3, 100)
+    q = torch.randn(3, 8, 64, device=DEV, dtype=BF)
+    turns, cu = nt.nt_rope_turns(64, device=DEV), _cu([1, 1, 1])
+    lens = torch.tensor([1600, 3, 700], dtype=torch.int32, device=DEV)
+
+    def step(stream=None):
+        a, _ = nt.nt_qk_norm_rope(q, None, turns, cu_seqlens=cu, pos0=lens, stream=stream)
+        return a, nt.nt_paged_attn(pages, a, table, lens, stream=stream)[0]
+
+    want = step()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                got = step(s)
+                if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    nt.nt_device_status()
+    assert not bad
