@@ -184,7 +184,9 @@ cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, 
 }  // namespace
 
 // About 1 us, 1.6 us an item and t a slice of 16 keys, more when all warps are
-// busy; as long as the longest item, or as the warps' shares.
+// busy; as long as the longest item, or as the warps' shares.  (200 contexts
+// with 12 heads of 64, of up to 200 keys: 19 us here, 24 on the tile kernel;
+// of up to 1,000: 73 and 55.)
 double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p) {
   const int64_t cap = paged_cap(p);
   if (cap > kPagedShortKeys || p.pool.n_pages == 0) return INFINITY;
