@@ -14,7 +14,7 @@
 //   dgamma = sum g x r,  h = g gamma,  dx = r (h - x r mean(h x r)).
 //
 // Both directions are bound by HBM (65,536 tokens of 12 + 12 heads of 64 in
-// bf16: forward 66.1 us, 90% of the measured copy rate, backward 97 us, 92%;
+// bf16: forward 68.6 us, 86% of the measured copy rate, backward 97 us, 92%;
 // 16,384 of 32 + 8 of 128: 55.3 and 80.8 us, 89% and 92%), and at about ten
 // operations an element not by much, so the layout keeps loads in flight
 // without holding registers or waiting at barriers.  A row (one head of one
@@ -167,18 +167,12 @@ struct Lane {
     }
   }
   // copy the lane's words of a row into its ring words, 16 bytes each; x and
-  // y point at its first column.  kPair: L2 may fetch the line beside it too.
-  template <bool kPair>
+  // y point at its first column
   __device__ __forceinline__ void copy(uint32_t dst, const T* x) const {
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if constexpr (kPair)
-        asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
-                     ::"r"(dst + w * kThreads * 16), "l"(x + w * step) : "memory");
-      else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                     ::"r"(dst + w * kThreads * 16), "l"(x + w * step) : "memory");
-    }
+    for (int w = 0; w < W; ++w)
+      asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
+                   ::"r"(dst + w * kThreads * 16), "l"(x + w * step) : "memory");
   }
   __device__ __forceinline__ void store(T* y, const float (&v)[16]) const {
 #pragma unroll
@@ -373,10 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_fwd_kernel(const Args a) {
   uint32_t so = threadIdx.x;                 // this thread's first word of the slot in hand
   auto copy = [&] {
     if (pn > 0) {
-      // (where a row is a line, the next step fetches the one beside it: the
-      // stream's forward 69.1 us with pairs, 66.1 without; other widths gain
-      // about 1% by them, the backward 3%)
-      if (pon && me.h_off < pn) me.template copy<L::kRow != 128>(tc::smem_u32(ring + so), px);
+      if (pon && me.h_off < pn) me.copy(tc::smem_u32(ring + so), px);
       px += a.d * L::kSide;
       if ((pn -= L::kSide) <= 0) {
         ahead.next(a);
@@ -483,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
     if (pn > 0) {
       if (pon && me.h_off < pn) {
         const uint32_t dst = tc::smem_u32(ring + so);
-        me.template copy<true>(dst, pu);
-        if (pnorm) me.template copy<true>(dst + R::kWords / 2 * kThreads * 16, px);
+        me.copy(dst, pu);
+        if (pnorm) me.copy(dst + R::kWords / 2 * kThreads * 16, px);
       }
       pu += a.d * L::kSide;
       px += a.d * L::kSide;
