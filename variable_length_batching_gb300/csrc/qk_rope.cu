@@ -14,8 +14,8 @@
 //   dgamma = sum g x r,  h = g gamma,  dx = r (h - x r mean(h x r)).
 //
 // Both directions are bound by HBM (65,536 tokens of 12 + 12 heads of 64 in
-// bf16: forward 68.6 us, 86% of the measured copy rate, backward 97 us, 92%;
-// 16,384 of 32 + 8 of 128: 55.3 and 80.8 us, 89% and 92%), and at about ten
+// bf16: forward 66 to 69 us, 86 to 90% of the measured copy rate, backward 97,
+// 92%; 16,384 of 32 + 8 of 128: 55.3 and 80.8, 89% and 92%), and at about ten
 // operations an element not by much, so the layout keeps loads in flight
 // without holding registers or waiting at barriers.  A row (one head of one
 // token) is a group of LP lanes, 16 elements to a lane in 16-byte words spread
