@@ -48,11 +48,12 @@ using namespace paged;
 constexpr int kConsumers = 8;               // warps
 constexpr int kProducers = 2;               // warps, tiles alternating
 constexpr int kQSlots = 4;                  // items whose query rows are in flight or in use
-constexpr int kThreads = (kConsumers + kProducers + 2) * 32;
+constexpr int kOthers = kConsumers + kProducers + 1;       // warps beside the merge's
 
 // HP: query heads of an item, at most, and what the registers are laid out
 // for: 8 or 16 in bf16 (one or two accumulator tiles), 1, 2, 4 or 8 in fp32.
-template <typename T, int D, int HP>
+// MW: warps that merge, 0 for the eight together.
+template <typename T, int D, int HP, int MW>
 struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   // keys per stage, and per unit of the split: 16 KB of bf16 (32 at d = 128), 32 of fp32
@@ -65,9 +66,7 @@ struct Cfg {
   static constexpr int kRedStride = D + 4;                    // floats: keeps the merge's writes conflict-free
   static constexpr uint32_t kRed = kConsumers * HP * kRedStride * 4;
   static constexpr int kRedBufs = HP * D <= 1024 ? 2 : 1;     // segments whose results wait for the merge
-  // The merge: one warp of its own, or, where it is four times the work, the
-  // eight together (G = 16, d = 128: 78 us for a batch that took 104 with one).
-  static constexpr int kMergeWarps = HP == 16 ? kConsumers : 1;
+  static constexpr int kThreads = (kOthers + (MW ? MW : 1)) * 32;
   static constexpr uint32_t kQBytes = HP * kRow;
   static constexpr int kExtra = HP == 16 ? 3 : 2;             // an item's cost beside its tiles, in tiles
   static constexpr uint32_t kScratch = kConsumers * Worker<T, D, HP>::kScratch;
@@ -110,10 +109,10 @@ struct TmaArgs {
 
 // The merge of a segment's eight warps, and its output or partial result: the
 // caller is thread `first` of `step`.
-template <typename T, int D, int HP>
+template <typename T, int D, int HP, int MW>
 __device__ __forceinline__ void merge_segment(const TmaArgs& a, const PagedWalk& w, const Ctl* ctl, const float* red,
                                               int buf, int first, int step) {
-  using C = Cfg<T, D, HP>;
+  using C = Cfg<T, D, HP, MW>;
   constexpr int kHeads = HP;
   const PagedPartials part = paged_partials(a.workspace, gridDim.x, a.heads);
   const int kvh = w.seg_item / a.hgroups, h0 = (w.seg_item % a.hgroups) * kHeads;
@@ -169,11 +168,11 @@ __device__ __forceinline__ void merge_segment(const TmaArgs& a, const PagedWalk&
   }
 }
 
-template <typename T, int D, int HP>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int D, int HP, int MW>
+__global__ void __launch_bounds__((Cfg<T, D, HP, MW>::kThreads), 1)
 paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const TmaArgs a) {
-  using C = Cfg<T, D, HP>;
+  using C = Cfg<T, D, HP, MW>;
   constexpr int kHeads = HP, S = C::kStages, kTile = C::kTile;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -197,7 +196,7 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   }
   if (threadIdx.x < C::kRedBufs) {
     mbar_init(&ctl->red_full[threadIdx.x], kConsumers);
-    mbar_init(&ctl->red_empty[threadIdx.x], C::kMergeWarps);
+    mbar_init(&ctl->red_empty[threadIdx.x], MW ? MW : kConsumers);
   }
   if (threadIdx.x == 0) ctl->abort = 0;
   if (threadIdx.x < 32) fence_mbar_init();
@@ -205,11 +204,11 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   if (threadIdx.x == 64) prefetch_tmap(&vmap);
   pdl_wait();
   pdl_trigger();
-  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status, kThreads);
+  paged_plan(a.lengths, a.B, cap, a.items, kTile, C::kExtra, blockIdx.x, gridDim.x, &ctl->plan, a.status, C::kThreads);
   PagedWalk w;
   w.init(ctl->plan, a.lengths, a.B, cap, kTile, C::kExtra, a.whole);
 
-  if (warp == kConsumers + kProducers) {
+  if (warp == kOthers - 1) {
     // ---- query rows, item by item ------------------------------------------
     uint32_t segs = 0;
     while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
@@ -230,15 +229,15 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         mbar_wait(&ctl->q_full[i % kQSlots], (i / kQSlots) & 1, nullptr, a.status);
     return;
   }
-  if (warp == kConsumers + kProducers + 1) {
+  if (warp >= kOthers) {
     // ---- merge: the consumers' results of a segment ------------------------------
     uint32_t segs = 0;
     int64_t open_id = -1, open_parts = 0;             // the item left unfinished
     while (w.next(a.lengths, a.B, cap, a.items, kTile, C::kExtra)) {
-      if (C::kMergeWarps == 1) {
+      if (MW > 0) {
         const int buf = segs % C::kRedBufs;
         if (!mbar_wait_warp(&ctl->red_full[buf], (segs / C::kRedBufs) & 1, &ctl->abort, a.status)) break;
-        merge_segment<T, D, HP>(a, w, ctl, red, buf, lane, 32);
+        merge_segment<T, D, HP, MW>(a, w, ctl, red, buf, threadIdx.x - kOthers * 32, MW * 32);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
         ++segs;
@@ -248,7 +247,7 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         open_parts = w.parts(ctl->plan, C::kExtra, blockIdx.x, gridDim.x);
       }
     }
-    if (lane == 0) {
+    if (threadIdx.x == kOthers * 32) {
       part.id[2 * blockIdx.x] = open_id;
       part.id[2 * blockIdx.x + 1] = open_parts;
     }
@@ -383,10 +382,10 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
               active);
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->red_full[buf]);
-    if (C::kMergeWarps > 1) {
+    if (MW == 0) {
       ok = mbar_wait_warp(&ctl->red_full[buf], (segs / C::kRedBufs) & 1, &ctl->abort, a.status);
       if (!ok) break;
-      merge_segment<T, D, HP>(a, w, ctl, red, buf, threadIdx.x, kConsumers * 32);
+      merge_segment<T, D, HP, MW>(a, w, ctl, red, buf, threadIdx.x, kConsumers * 32);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->red_empty[buf]);
     }
@@ -394,9 +393,9 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   }
 }
 
-template <typename T, int D, int HP>
+template <typename T, int D, int HP, int MW>
 cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
-  using C = Cfg<T, D, HP>;
+  using C = Cfg<T, D, HP, MW>;
   TmaArgs a;
   a.q = p.q;
   a.q_stride = p.q_stride;
@@ -433,9 +432,9 @@ cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s)
                    i ? p.pool.v : p.pool.k, 4, dims, strides, box))
       return cudaErrorInvalidValue;
   const int ctas = min(sm_count(), kPagedMaxCtas);
-  cudaError_t e = allow_smem_once<paged_attn_tma_kernel<T, D, HP>>(C::kSmem);
+  cudaError_t e = allow_smem_once<paged_attn_tma_kernel<T, D, HP, MW>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attn_tma_kernel<T, D, HP>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[0], maps[1], a);
+  e = launch_pdl(paged_attn_tma_kernel<T, D, HP, MW>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, maps[0], maps[1], a);
   if (e != cudaSuccess || a.whole) return e;
   return launch_paged_join(C::kBf16 ? NT_BF16 : NT_F32, p, ctas, a.items, HP, s);
 }
@@ -443,11 +442,19 @@ cudaError_t run(const PagedAttnProblem& p, unsigned int* status, cudaStream_t s)
 template <int D>
 cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s) {
   const int G = p.H / p.pool.H;
-  if (dt == NT_BF16) return G <= 8 ? run<bf16, D, 8>(p, status, s) : run<bf16, D, 16>(p, status, s);
-  if (G == 1) return run<float, D, 1>(p, status, s);
-  if (G == 2) return run<float, D, 2>(p, status, s);
-  if (G <= 4) return run<float, D, 4>(p, status, s);
-  return run<float, D, 8>(p, status, s);
+  // The merge: one warp of its own; two for more than four heads (the ragged
+  // batch of 64 with 8 heads to a key head of 128: 65.7 us with one, 60.1 with
+  // two; with four heads 57.3 and 57.4, and many short contexts lose 4%, as the
+  // registers have to do for 13 warps); the eight together for more than eight
+  // (16 heads: 78 us where one alone took 104).
+  if (dt == NT_BF16) {
+    if (G <= 4) return run<bf16, D, 8, 1>(p, status, s);
+    return G <= 8 ? run<bf16, D, 8, 2>(p, status, s) : run<bf16, D, 16, 0>(p, status, s);
+  }
+  if (G == 1) return run<float, D, 1, 1>(p, status, s);
+  if (G == 2) return run<float, D, 2, 1>(p, status, s);
+  if (G <= 4) return run<float, D, 4, 1>(p, status, s);
+  return run<float, D, 8, 1>(p, status, s);
 }
 
 }  // namespace
