@@ -788,9 +788,10 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  *                 log-sum-exp of the scaled scores, or NULL.  Neither may
  *                 overlap an input.
  *   workspace     >= nt_paged_attn_workspace_bytes(H, H_kv, d) bytes, 16-byte aligned.
- * The softmax statistics and sums are fp32; bf16 probabilities are rounded to
- * bf16 before they multiply the values.  Results do not depend on scheduling;
- * their rounding may depend on B and max_pages, by which the kernel is chosen.
+ * The softmax statistics and sums are fp32; in bf16 a probability multiplies
+ * the values as the sum of two bf16, 2^-15 of it at most away from it.  Results
+ * do not depend on scheduling; their rounding may depend on B and max_pages, by
+ * which the kernel is chosen.
  * Asynchronous.
  */
 nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,

@@ -91,6 +91,17 @@ struct Worker<bf16, D, HP> {
         for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
     }
   }
+  // Probabilities x, y >= 0 as the sums of two bf16, off by 2^-15 of them at
+  // most (one bf16 would be off by 2^-8, which shows in the output).  The upper
+  // part is the largest bf16 below the value, so that both are positive: an
+  // infinite value in the cache gives the infinity that x times it is, and a
+  // lower part of 0 or below would make it NaN.
+  static __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const uint32_t a = (max(__float_as_uint(x), 1u) - 1) & 0xffff0000u;
+    const uint32_t b = (max(__float_as_uint(y), 1u) - 1) & 0xffff0000u;
+    hi = __byte_perm(a, b, 0x7632);
+    lo = pack_bf16x2(x - __uint_as_float(a), y - __uint_as_float(b));
+  }
   // the first `left` of the slice's keys
   __device__ __forceinline__ void tile(uint8_t* stage, uint32_t side, int left, float scale_log2) {
     const int lane = threadIdx.x & 31;
@@ -118,7 +129,7 @@ struct Worker<bf16, D, HP> {
       s[0][c] += s2[0][c];
       s[1][c] += s2[1][c];
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2], pl[NT][2];
     float corr[NT];
     bool moved = false;
 #pragma unroll
@@ -142,8 +153,8 @@ struct Worker<bf16, D, HP> {
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] = ex2_approx(v[c] - base);
       l[n] = l[n] * corr[n] + (v[0] + v[1]) + (v[2] + v[3]);
-      pb[n][0] = pack_bf16x2(v[0], v[1]);
-      pb[n][1] = pack_bf16x2(v[2], v[3]);
+      split(v[0], v[1], pb[n][0], pl[n][0]);
+      split(v[2], v[3], pb[n][1], pl[n][1]);
     }
     if (__any_sync(0xffffffffu, moved)) {
       // the output's columns are heads 2 tq and 2 tq + 1: their factors sit in those rows' lanes
@@ -160,12 +171,20 @@ struct Worker<bf16, D, HP> {
         }
       }
     }
+    // two column blocks at a time: a product does not wait for the one before it
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      uint32_t va[4];
-      ldsm4_t(vbase + (i >> 2) * hs + row_off + ((((uint32_t)i & 3) << 5) ^ xr), va);
+    for (int i = 0; i < D / 16; i += 2) {
+      uint32_t va[2][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816(o[n][i], va, pb[n][0], pb[n][1]);
+      for (int k = 0; k < 2; ++k)
+        ldsm4_t(vbase + ((i + k) >> 2) * hs + row_off + ((((uint32_t)(i + k) & 3) << 5) ^ xr), va[k]);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816(o[n][i + k], va[k], part ? pl[n][0] : pb[n][0], part ? pl[n][1] : pb[n][1]);
     }
     if (left < 16) fence_async_shared();       // the zeros, before the next copy into this stage
   }
