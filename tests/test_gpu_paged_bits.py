@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from _attn_path import HALF_STEP, U32, paged_attn
-from test_gpu_paged import DEV, SHAPES, SHORT, _attn_case, _i32, nt  # noqa: F401
+from test_gpu_paged import SHAPES, SHORT, _attn_case, nt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
