@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
   };
 #pragma unroll
   for (int s = 0; s < R::kSlots; ++s) {
-    // what no copy fills (lanes beyond the head's columns, tokens beyond the last) has to be finite
+    // lanes beyond the head's columns copy nothing and add zeros to its sums
 #pragma unroll
     for (int w = 0; w < R::kWords; ++w) ring[so + w * kThreads] = make_uint4(0, 0, 0, 0);
     copy();
@@ -554,8 +554,19 @@ __global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const Args a) {
       }
       if (norm) {
         read_row<T>(ring + so + R::kWords / 2 * kThreads, v);
+        // A row that is not there (a token beyond the last, a head beyond the unit's: its words are an earlier
+        // row's, the other side's perhaps), or that the offsets place nowhere, adds nothing.  Zeros, not a factor
+        // of zero, which would let NaN and infinities through.
+        if (__any_sync(0xffffffffu, me.on && !live)) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            v[e] = live ? v[e] : 0.f;
+            g[e] = live ? g[e] : 0.f;
+          }
+        }
         const float r = rsqrtf(fmaf(group_sum<LP>(dot16(v, v)), a.inv_d, a.eps));
-        const float keep = live ? r : 0.f;             // a row that is not there adds nothing
+        // eps 0 and a row of zeros: r is infinite, and a row that is not there has nothing to multiply by it
+        const float keep = live ? r : 0.f;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           fmul2(v[e], v[e + 1], keep, keep, v[e], v[e + 1]);
