@@ -1,0 +1,67 @@
+"""The autograd Functions around the library's calls, without a GPU: the calls
+are stood in for by torch operations on detached tensors, as opaque to
+autograd as the library's are."""
+import pytest
+import torch
+
+from variable_length_batching_gb300 import autograd as ag
+
+
+@pytest.fixture
+def rope(monkeypatch):
+    """y = x^2 gamma for either side in place of the norm and rotation."""
+    def fwd(q, k, turns, q_gamma=None, k_gamma=None, **_):
+        one = lambda x, g: None if x is None else x.detach() ** 2 * (1 if g is None else g.detach())
+        return one(q, q_gamma), one(k, k_gamma)
+
+    def bwd(uq, uk, turns, q=None, k=None, q_gamma=None, k_gamma=None, **_):
+        def one(u, x, g):
+            if u is None or g is None:
+                return None if u is None else u.detach().clone(), None
+            u, x, g = (t.detach() for t in (u, x, g))
+            return 2 * u * x * g, (u * x * x).sum((0, 1))
+        (dq, dqg), (dk, dkg) = one(uq, q, q_gamma), one(uk, k, k_gamma)
+        return dq, dk, dqg, dkg
+
+    monkeypatch.setattr(ag.nt, "nt_qk_norm_rope", fwd)
+    monkeypatch.setattr(ag.nt, "nt_qk_norm_rope_bwd", bwd)
+
+
+def _leaves():
+    gen = torch.Generator().manual_seed(1)
+    q, k = (torch.randn(5, h, 8, generator=gen, requires_grad=True) for h in (2, 1))
+    return q, k, torch.rand(8, generator=gen, requires_grad=True)
+
+
+@pytest.mark.parametrize("upstream", ["constant", "of the outputs", "a leaf"])
+def test_second_derivatives_of_rope_raise(rope, upstream):
+    q, k, g = _leaves()
+    qo, ko = ag.qk_norm_rope(q, k, None, q_gamma=g, k_gamma=g)
+    if upstream == "constant":
+        grads = torch.autograd.grad(qo.sum() + ko.sum(), (q, k, g), create_graph=True)
+    elif upstream == "of the outputs":
+        grads = torch.autograd.grad((qo ** 2).sum() + (ko ** 2).sum(), (q, k, g), create_graph=True)
+    else:
+        u = torch.ones_like(qo, requires_grad=True)
+        grads = torch.autograd.grad(qo, (q, g), u, create_graph=True)
+    for x in grads:
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            ((x ** 2).sum() + (q ** 2).sum()).backward(retain_graph=True)
+
+
+def test_second_derivatives_without_a_norm_raise_too(rope):
+    """Linear in q, but the upstream gradient's derivative would be lost."""
+    q, k, _ = _leaves()
+    qo, _ = ag.qk_norm_rope(q, k, None)
+    dq, = torch.autograd.grad((qo ** 2).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        dq.sum().backward()
+
+
+def test_first_derivatives_with_create_graph(rope):
+    """The graph may be asked for as long as nobody differentiates it."""
+    q, k, g = _leaves()
+    run = lambda **kw: torch.autograd.grad(sum((y ** 2).sum() for y in ag.qk_norm_rope(q, k, None, q_gamma=g)),
+                                           (q, k, g), **kw)
+    for a, b in zip(run(create_graph=True), run()):
+        assert torch.equal(a, b) and a.requires_grad and not b.requires_grad

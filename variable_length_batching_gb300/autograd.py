@@ -29,6 +29,35 @@ import torch
 from . import nt
 
 
+class _FirstOnly(torch.autograd.Function):
+    """Passes gradients on; raises when they are differentiated."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):
+        ctx.name = name
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has first derivatives only")
+
+
+def _first_only(name, grads, *of):
+    """The gradients a Function's backward returns, computed by the library
+    from the tensors ``of``.  The calls are opaque to autograd, so with
+    create_graph the gradients would pass for constants; here they depend on
+    ``of`` through a node that raises.  (torch's once_differentiable looks at
+    the upstream gradients only, and lets a constant one through.)"""
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in of):
+        return grads
+    at = [i for i, g in enumerate(grads) if g is not None]
+    kept = _FirstOnly.apply(name, len(at), *(grads[i] for i in at), *of)
+    out = list(grads)
+    for i, g in zip(at, kept):
+        out[i] = g
+    return tuple(out)
+
+
 class PairBlock(torch.autograd.Function):
     @staticmethod
     def forward(ctx, part, s, W_a, W_b, ln_gamma, ln_beta, W1, b1, W2, b2, W_g, b_g, ln_eps):
@@ -105,11 +134,12 @@ class QKNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0 = ctx.saved_tensors
         eps, interleaved, rot_scale = ctx.args
-        dq_out, dk_out = (None if g is None else g.contiguous() for g in (dq_out, dk_out))
-        dq, dk, dqg, dkg = nt.nt_qk_norm_rope_bwd(dq_out, dk_out, turns, q=q, k=k,
+        uq, uk = (None if g is None else g.contiguous() for g in (dq_out, dk_out))
+        dq, dk, dqg, dkg = nt.nt_qk_norm_rope_bwd(uq, uk, turns, q=q, k=k,
                                                   cu_seqlens=cu_seqlens, positions=positions, pos0=pos0,
                                                   q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, interleaved=interleaved,
                                                   rot_scale=rot_scale)
+        dq, dk, dqg, dkg = _first_only("qk_norm_rope", (dq, dk, dqg, dkg), dq_out, dk_out, q, k, q_gamma, k_gamma)
         return dq, dk, None, dqg, dkg, None, None, None, None, None, None
 
 
@@ -118,5 +148,6 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], turns: Op
                  eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0):
     """Per-head norm and rotary positions of packed q and k with autograd
     (:func:`nt.nt_qk_norm_rope`): returns (q_out, k_out), ready for
-    :func:`varlen_attention`.  The gammas are fp32 leaves."""
+    :func:`varlen_attention`.  The gammas are fp32 leaves.  First derivatives
+    only: differentiating the gradients raises."""
     return QKNormRope.apply(q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0, eps, interleaved, rot_scale)
