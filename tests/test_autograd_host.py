@@ -65,3 +65,30 @@ def test_first_derivatives_with_create_graph(rope):
                                            (q, k, g), **kw)
     for a, b in zip(run(create_graph=True), run()):
         assert torch.equal(a, b) and a.requires_grad and not b.requires_grad
+
+
+def test_second_derivatives_of_varlen_attention_raise(monkeypatch):
+    monkeypatch.setattr(ag.nt, "nt_varlen_attn_qk", lambda q, k, v, *a, **kw: (q.detach() * k * v, q.detach().sum(-1)))
+    monkeypatch.setattr(ag.nt, "nt_varlen_attn_bwd",
+                        lambda q, k, v, o, d_o, *a, **kw: tuple(t.detach() * d_o.detach() for t in (k * v, q * v, q * k)))
+    q, k, v = (torch.randn(5, 2, 8, requires_grad=True) for _ in range(3))
+    run = lambda **kw: torch.autograd.grad(ag.varlen_attention(q, k, v, torch.tensor([0, 5]), 5).sum(), (q, k, v), **kw)
+    for x in run(create_graph=True):
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            x.sum().backward(retain_graph=True)
+    assert all(not x.requires_grad for x in run())
+
+
+def test_second_derivatives_of_the_block_raise(monkeypatch):
+    names = ("ds", "dW_a", "dW_b", "dgamma", "dbeta", "dW1", "db1", "dW2", "db2", "dW_g", "db_g")
+    monkeypatch.setattr(ag.nt, "block_forward", lambda part, s, w, ln_eps: (s.detach() * 2, s.detach(), s.detach() * 3))
+    monkeypatch.setattr(ag.nt, "nt_pair_block_backward",
+                        lambda *a, **kw: {n: torch.ones(4, 4) for n in names})
+    w = [torch.ones(4, 4, requires_grad=True) for _ in names]
+    w[6] = None                                                   # no b1
+    run = lambda **kw: torch.autograd.grad(sum(y.sum() for y in ag.pair_block(None, *w)), [t for t in w if t is not None],
+                                           **kw)
+    for x in run(create_graph=True):
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            x.sum().backward(retain_graph=True)
+    assert all(not x.requires_grad for x in run())

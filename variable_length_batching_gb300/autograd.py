@@ -84,15 +84,18 @@ class PairBlock(torch.autograd.Function):
             ds_out = torch.zeros(s.shape[0], W_g.shape[0], dtype=torch.float32, device=s.device)
         g = nt.nt_pair_block_backward(ctx.part, s, w, m, f32(ds_out), f32(dz_t), ln_eps=ctx.ln_eps)
         like = lambda grad, t: grad.to(t.dtype)
-        return (None, like(g["ds"], s), like(g["dW_a"], W_a), like(g["dW_b"], W_b), like(g["dgamma"], ln_gamma),
-                like(g["dbeta"], ln_beta), like(g["dW1"], W1), like(g["db1"], b1) if has_b1 else None,
-                like(g["dW2"], W2), like(g["db2"], b2) if has_b2 else None, like(g["dW_g"], W_g),
-                like(g["db_g"], b_g) if has_bg else None, None)
+        grads = (like(g["ds"], s), like(g["dW_a"], W_a), like(g["dW_b"], W_b), like(g["dgamma"], ln_gamma),
+                 like(g["dbeta"], ln_beta), like(g["dW1"], W1), like(g["db1"], b1) if has_b1 else None,
+                 like(g["dW2"], W2), like(g["db2"], b2) if has_b2 else None, like(g["dW_g"], W_g),
+                 like(g["db_g"], b_g) if has_bg else None)
+        return (None, *_first_only("pair_block", grads, dz_t, ds_out, s, W_a, W_b, ln_gamma, ln_beta, W1, b1, W2, b2,
+                                   W_g, b_g), None)
 
 
 def pair_block(part: "nt.Partition", s: torch.Tensor, W_a, W_b, ln_gamma, ln_beta, W1, b1, W2, b2, W_g, b_g,
                ln_eps: float = 1e-5):
-    """The ReLU block of Eq. 1 with autograd: returns (z~, s_out)."""
+    """The ReLU block of Eq. 1 with autograd: returns (z~, s_out).  First
+    derivatives only: differentiating the gradients raises."""
     return PairBlock.apply(part, s, W_a, W_b, ln_gamma, ln_beta, W1, b1, W2, b2, W_g, b_g, ln_eps)
 
 
@@ -110,12 +113,14 @@ class VarlenAttention(torch.autograd.Function):
         q, k, v, o, lse, cu = ctx.saved_tensors
         dq, dk, dv = nt.nt_varlen_attn_bwd(q, k, v, o, d_o.to(q.dtype).contiguous(), lse, cu, None, ctx.max_len,
                                            scale=ctx.scale, causal=ctx.causal)
+        dq, dk, dv = _first_only("varlen_attention", (dq, dk, dv), d_o, q, k, v)
         return dq, dk, dv, None, None, None, None
 
 
 def varlen_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int,
                      causal: bool = False, scale: Optional[float] = None):
-    """Self-attention within each cu_seqlens segment, with autograd."""
+    """Self-attention within each cu_seqlens segment, with autograd.  First
+    derivatives only: differentiating the gradients raises."""
     return VarlenAttention.apply(q, k, v, cu_seqlens, max_len, causal, scale)
 
 
