@@ -16,6 +16,8 @@ def rope(monkeypatch):
 
     def bwd(uq, uk, turns, q=None, k=None, q_gamma=None, k_gamma=None, **_):
         def one(u, x, g):
+            if g is not None and (u is None or x is None):
+                raise ValueError("a norm needs its side and its upstream gradient")      # as the library does
             if u is None or g is None:
                 return None if u is None else u.detach().clone(), None
             u, x, g = (t.detach() for t in (u, x, g))
@@ -92,3 +94,13 @@ def test_second_derivatives_of_the_block_raise(monkeypatch):
         with pytest.raises(RuntimeError, match="first derivatives only"):
             x.sum().backward(retain_graph=True)
     assert all(not x.requires_grad for x in run())
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_a_gamma_without_its_side_takes_no_part(rope, side):
+    x, _, g = _leaves()
+    other = torch.rand(8, requires_grad=True)
+    gammas = (g, other) if side == 0 else (other, g)
+    out = ag.qk_norm_rope(*((x, None) if side == 0 else (None, x)), None, q_gamma=gammas[0], k_gamma=gammas[1])[side]
+    dx, dg, none = torch.autograd.grad(out.sum(), (x, g, other), allow_unused=True)
+    assert none is None and torch.equal(dx, (2 * x * g).detach()) and dg is not None

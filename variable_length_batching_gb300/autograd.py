@@ -127,6 +127,8 @@ def varlen_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
 class QKNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, turns, q_gamma, k_gamma, cu_seqlens, positions, pos0, eps, interleaved, rot_scale):
+        q_gamma = None if q is None else q_gamma       # a gamma without its side takes no part
+        k_gamma = None if k is None else k_gamma
         q_out, k_out = nt.nt_qk_norm_rope(q, k, turns, cu_seqlens=cu_seqlens, positions=positions, pos0=pos0,
                                           q_gamma=q_gamma, k_gamma=k_gamma, eps=eps, interleaved=interleaved,
                                           rot_scale=rot_scale)
