@@ -774,8 +774,10 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  *                 apart (>= H * d, a multiple of 8 bf16 / 4 fp32 elements).
  *   H             a multiple of H_kv.   d in {32, 64, 128}.  B at most
  *                 2^30 and B * max_pages * page_size * H at most 1e13
- *                 (NT_ERR_OVERFLOW); max_pages * page_size at most 2^24 for
- *                 pages that are not a multiple of 8 (NT_ERR_UNSUPPORTED).
+ *                 (NT_ERR_OVERFLOW).  Tables of more than 2^24 positions
+ *                 (max_pages * page_size, up to 2^31 - 1 of them): pages of a
+ *                 multiple of 8, and B * H_kv * ceil(G / 8) * positions at
+ *                 most 2^31 (NT_ERR_UNSUPPORTED).
  *   d_block_table [B, max_pages] int32.
  *   d_lengths     [B] int32, the positions of each sequence that are attended
  *                 to; 0 gives o = 0 and lse = -inf.  Lengths are read on the

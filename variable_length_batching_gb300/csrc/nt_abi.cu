@@ -1146,9 +1146,19 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   if ((double)B * max_pages * pages->page_size * H > 1e13)
     return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e13",
                 (double)B * max_pages * pages->page_size * H);
-  // (the kernel for other pages has few warps to a sequence, whose fp32 sums run in turn)
-  if (B > 0 && pages->page_size % 8 && (int64_t)max_pages * pages->page_size > (1 << 24))
-    return fail(NT_ERR_UNSUPPORTED, "tables of more than 2^24 positions need pages of a multiple of 8");
+  // The longest part of a context that one SM reads: its fp32 sums run in turn, and the warps that fetch queries
+  // and merge wait for all of it, 2 s at most (2^24 keys of 1 KB at an SM's part of HBM's rate: 0.4 s).  Pages of a
+  // multiple of 8 are dealt out to the SMs evenly, so there 2^31 positions in all do (128 SMs and more).
+  constexpr int64_t kPositions = 1 << 24;
+  const int64_t cap = min64((int64_t)max_pages * pages->page_size, 0x7fffffff);
+  if (B > 0 && cap > kPositions) {
+    const int G = H / pages->H_kv;
+    if (pages->page_size % 8)
+      return fail(NT_ERR_UNSUPPORTED, "tables of more than 2^24 positions need pages of a multiple of 8");
+    if ((double)B * pages->H_kv * ((G + 7) / 8) * cap > 128.0 * kPositions)
+      return fail(NT_ERR_UNSUPPORTED, "B * H_kv * ceil(G / 8) * positions = %g: at most 2^31 with tables of more than 2^24",
+                  (double)B * pages->H_kv * ((G + 7) / 8) * cap);
+  }
   const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
   if (B > 0 && workspace_bytes < need)
     return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
