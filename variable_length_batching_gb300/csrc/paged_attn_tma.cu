@@ -226,7 +226,8 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       }
       ++segs;
     }
-    if (ctl->abort && lane == 0)                      // given up: the copies in flight land first
+    // no copy may land after the CTA is gone: not where a wait was given up, here or by another warp
+    if (lane == 0)
       for (uint32_t i = segs > kQSlots ? segs - kQSlots : 0; i < segs; ++i)
         mbar_wait(&ctl->q_full[i % kQSlots], (i / kQSlots) & 1, nullptr, a.status);
     return;
@@ -333,7 +334,7 @@ paged_attn_tma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       }
       seg_it += (uint32_t)(w.t1 - w.t0);
     }
-    if (!ok && lane == 0)                             // given up: the copies in flight land first
+    if (lane == 0)                                    // as for the query rows
       for (uint32_t i = 0; i < (uint32_t)S && i < last; ++i)
         if (((last - 1 - i) & (kProducers - 1)) == me)
           mbar_wait(&ctl->full[(last - 1 - i) % S], ((last - 1 - i) / S) & 1, nullptr, a.status);
