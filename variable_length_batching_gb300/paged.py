@@ -100,6 +100,20 @@ class PageTable:
                 pages.append(page)
         return copies
 
+    def retract(self, seqs: Sequence[int], counts: Sequence[int], copies: Copies) -> None:
+        """Takes back the call of :meth:`extend` before it, which had these
+        arguments and returned ``copies``: the table is as it was."""
+        copied = {dst: src for src, dst in copies}
+        for s, n in zip(reversed(seqs), reversed(counts)):
+            pages = self.pages[s]
+            self.length[s] -= n
+            while len(pages) > -(-self.length[s] // self.page_size):
+                self._drop(pages.pop())
+            if pages and pages[-1] in copied:
+                dst, pages[-1] = pages[-1], copied[pages[-1]]
+                self.refs[pages[-1]] += 1
+                self._drop(dst)
+
     def fork(self, seq: int) -> int:
         """A new sequence with the same positions, sharing ``seq``'s pages."""
         self._known(seq)
@@ -171,7 +185,13 @@ class PagedCache:
     def compact(self, stream=None) -> None:
         """The pages in use moved to the front of the pool.  Steps taken
         before hold the old places."""
-        self._copy(self.table.compact(), stream)
+        t = self.table
+        before = list(t.refs), list(t.free_pages), {s: list(p) for s, p in t.pages.items()}
+        try:
+            self._copy(t.compact(), stream)
+        except BaseException:
+            t.refs, t.free_pages, t.pages = before
+            raise
 
     def step(self, seqs: Sequence[int], counts: Sequence[int], stream=None) -> Step:
         """Makes room for counts[i] new tokens of seqs[i] and returns the
@@ -182,8 +202,16 @@ class PagedCache:
         with torch.cuda.stream(on):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a step makes room on the host: take it outside the capture")
+        seqs, counts = list(seqs), list(counts)
         copies = self.table.extend(seqs, counts)
-        self._copy(copies, stream)
+        try:
+            self._copy(copies, stream)
+            return self._arrays(seqs, counts, on)
+        except BaseException:
+            self.table.retract(seqs, counts, copies)      # no room is made for a step that was not taken
+            raise
+
+    def _arrays(self, seqs: List[int], counts: List[int], on) -> Step:
         B = len(seqs)
         lists = [self.table.pages[s] for s in seqs]
         after = [self.table.length[s] for s in seqs]
@@ -200,8 +228,8 @@ class PagedCache:
         dev = self.pages.device
         with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
-        return Step(list(seqs), arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
-                    arr[head:].view(B, width), max(list(counts) + [0]))
+        return Step(seqs, arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
+                    arr[head:].view(B, width), max(counts + [0]))
 
     def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """The step's new keys and values, packed (tokens, H_kv, d)."""
