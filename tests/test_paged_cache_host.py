@@ -98,3 +98,16 @@ def test_a_compaction_that_fails_moves_nothing(cache):
     cache.fail = None
     cache.compact()
     assert len(cache.copied) == 3 and sorted(cache.table.pages[b]) == [0, 1, 2]
+
+
+def test_neither_is_captured(cache):
+    """What changes the table now and the pages at a replay is refused."""
+    a, b = cache.add(), cache.add()
+    cache.step([a, b], [9, 9])
+    cache.free(a)
+    before = _state(cache.table)
+    cache.capturing = True
+    for call in (cache.compact, lambda: cache.step([b], [1])):
+        with pytest.raises(RuntimeError, match="capture"):
+            call()
+    assert _state(cache.table) == before and cache.copied == []

@@ -182,9 +182,19 @@ class PagedCache:
             src, dst = torch.tensor(copies, dtype=torch.int32).T.contiguous()
             nt.nt_paged_copy(self.pages, src, dst, stream=stream)
 
+    def _on(self, stream, what: str):
+        """The call's stream, which may not be capturing."""
+        on = stream if stream is not None else torch.cuda.current_stream(self.pages.device)
+        with torch.cuda.stream(on):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"{what} on the host: take it outside the capture")
+        return on
+
     def compact(self, stream=None) -> None:
         """The pages in use moved to the front of the pool.  Steps taken
-        before hold the old places."""
+        before hold the old places.  Not while a graph is being captured: the
+        table would change now and the pages at a replay."""
+        self._on(stream, "compaction moves pages")
         t = self.table
         before = list(t.refs), list(t.free_pages), {s: list(p) for s, p in t.pages.items()}
         try:
@@ -198,10 +208,7 @@ class PagedCache:
         step's device arrays (one copy from pinned memory).  Counts of 1 make
         a decoding step, larger ones a prefill.  Not while a graph is being
         captured: a replay would not make room again."""
-        on = stream if stream is not None else torch.cuda.current_stream(self.pages.device)
-        with torch.cuda.stream(on):
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("a step makes room on the host: take it outside the capture")
+        on = self._on(stream, "a step makes room")
         seqs, counts = list(seqs), list(counts)
         copies = self.table.extend(seqs, counts)
         try:
