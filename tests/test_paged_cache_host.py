@@ -111,3 +111,18 @@ def test_neither_is_captured(cache):
         with pytest.raises(RuntimeError, match="capture"):
             call()
     assert _state(cache.table) == before and cache.copied == []
+
+
+def test_a_write_is_the_whole_step(cache, monkeypatch):
+    """Fewer tokens than the step made room for would leave positions that
+    are attended to and were never written."""
+    written = []
+    monkeypatch.setattr(paged.nt, "nt_paged_write", lambda pages, k, v, *a, **kw: written.append(k.shape[0]))
+    a, b = cache.add(), cache.add()
+    step = cache.step([a, b], [5, 2])
+    kv = lambda n: torch.zeros(n, 1, 8)
+    for n in (0, 6, 8):
+        with pytest.raises(ValueError, match="7 new tokens"):
+            cache.write(step, kv(n), kv(n))
+    cache.write(step, kv(7), kv(7))
+    assert written == [7]

@@ -156,6 +156,7 @@ class Step:
     lengths: torch.Tensor        # [B] positions with the step's
     block_table: torch.Tensor    # [B, max_pages]
     max_new: int                 # longest of the new segments
+    tokens: int                  # new tokens of all of them
 
 
 class PagedCache:
@@ -236,10 +237,13 @@ class PagedCache:
         with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
         return Step(seqs, arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
-                    arr[head:].view(B, width), max(counts + [0]))
+                    arr[head:].view(B, width), max(counts + [0]), cu[-1])
 
     def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
-        """The step's new keys and values, packed (tokens, H_kv, d)."""
+        """The step's new keys and values, packed (tokens, H_kv, d): all of
+        them, or positions that were never written would be attended to."""
+        if k.shape[0] != step.tokens:
+            raise ValueError(f"the step has {step.tokens} new tokens, k and v have {k.shape[0]}")
         nt.nt_paged_write(self.pages, k, v, step.cu_seqlens, step.block_table, pos0=step.pos0, stream=stream)
 
     def attend(self, step: Step, q: torch.Tensor, scale: Optional[float] = None, stream=None) -> torch.Tensor:
