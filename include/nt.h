@@ -823,6 +823,21 @@ nt_status nt_device_status(void* stream);
 nt_status nt_selftest_bounded_wait(int32_t mode, uint64_t delay_ns, uint64_t limit_ns, int64_t* d_result,
                                    void* stream);
 
+/*
+ * nt_selftest_paged_attn -- nt_paged_attn by a kernel that the caller names,
+ * so that each can be tested at every size it takes, not only where the call
+ * chooses it: 0 a warp per item (a sequence's key head with up to 8 or 16 of
+ * its query heads), 1 a cluster of CTAs per item (`cluster` of them, in
+ * [1, 12], or 0 for the call's own estimate), 2 the batch's tiles dealt out to
+ * the SMs.  NT_ERR_UNSUPPORTED where that kernel does not take the call
+ * (0: tables of more than 1,024 positions; 2: pages that are not a multiple of
+ * 8; either: no pages); everything else as in nt_paged_attn.
+ */
+nt_status nt_selftest_paged_attn(int32_t kernel, int32_t cluster, const nt_kv_pages* pages, const void* q,
+                                 int64_t q_stride, int32_t B, int32_t H, const int32_t* d_block_table,
+                                 int32_t max_pages, const int32_t* d_lengths, float scale, void* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* nt_status_str(nt_status s);
 

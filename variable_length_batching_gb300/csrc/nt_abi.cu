@@ -231,6 +231,48 @@ nt_status check_table(const int32_t* table, int32_t max_pages, int32_t B) {
   return NT_OK;
 }
 
+// What nt_paged_attn refuses, and else the problem it runs.
+nt_status check_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,
+                           const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,
+                           void* o, float* lse, void* workspace, size_t workspace_bytes, PagedAttnProblem* p) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (B < 0 || H <= 0) return fail(NT_ERR_INVALID, "bad sizes B=%d H=%d", B, H);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
+  if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
+  if (pages->d != 32 && pages->d != 64 && pages->d != 128)
+    return fail(NT_ERR_UNSUPPORTED, "head width d=%d (32, 64 or 128)", pages->d);
+  if (!(scale > 0.f) || std::isinf(scale)) return fail(NT_ERR_INVALID, "scale must be finite and > 0");
+  st = check_table(d_block_table, max_pages, B);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "q", q, q_stride, B, H, pages->d);
+  if (st != NT_OK) return st;
+  if (B > 0 && (!d_lengths || !o || !workspace)) return fail(NT_ERR_INVALID, "NULL pointer");
+  if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(d_lengths) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(NT_ERR_INVALID, "d_lengths or lse misaligned");
+  if ((double)B * max_pages * pages->page_size * H > 1e13)
+    return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e13",
+                (double)B * max_pages * pages->page_size * H);
+  // The longest part of a context that one SM reads: its fp32 sums run in turn, and the warps that fetch queries
+  // and merge wait for all of it, 2 s at most (2^24 keys of 1 KB at an SM's part of HBM's rate: 0.4 s).  Pages of a
+  // multiple of 8 are dealt out to the SMs evenly, so there 2^31 positions in all do (128 SMs and more).
+  constexpr int64_t kPositions = 1 << 24;
+  const int64_t cap = min64((int64_t)max_pages * pages->page_size, 0x7fffffff);
+  if (B > 0 && cap > kPositions) {
+    const int G = H / pages->H_kv;
+    if (pages->page_size % 8)
+      return fail(NT_ERR_UNSUPPORTED, "tables of more than 2^24 positions need pages of a multiple of 8");
+    if ((double)B * pages->H_kv * ((G + 7) / 8) * cap > 128.0 * kPositions)
+      return fail(NT_ERR_UNSUPPORTED, "B * H_kv * ceil(G / 8) * positions = %g: at most 2^31 with tables of more than 2^24",
+                  (double)B * pages->H_kv * ((G + 7) / 8) * cap);
+  }
+  const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
+  if (B > 0 && workspace_bytes < need)
+    return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  *p = {pool_of(pages), q, q_stride, B, H, pages->d, d_block_table, max_pages, d_lengths, scale, o, lse, workspace};
+  return NT_OK;
+}
+
 // u = s_left W_a^T (T rows), v = s_right W_b^T (T_cols rows), fp32.
 cudaError_t project_uv(const nt_partition* part, nt_dtype dtype, const void* s_left, const void* s_right,
                        int32_t C_s, const void* W_a, const void* W_b, int32_t C_z, float* u, float* v,
@@ -1128,44 +1170,34 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d) {
 nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int32_t B, int32_t H,
                         const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,
                         void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  nt_status st = check_pages(pages);
-  if (st != NT_OK) return st;
-  if (B < 0 || H <= 0) return fail(NT_ERR_INVALID, "bad sizes B=%d H=%d", B, H);
-  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
-  if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
-  if (pages->d != 32 && pages->d != 64 && pages->d != 128)
-    return fail(NT_ERR_UNSUPPORTED, "head width d=%d (32, 64 or 128)", pages->d);
-  if (!(scale > 0.f) || std::isinf(scale)) return fail(NT_ERR_INVALID, "scale must be finite and > 0");
-  st = check_table(d_block_table, max_pages, B);
-  if (st == NT_OK) st = check_tokens(pages->dtype, "q", q, q_stride, B, H, pages->d);
-  if (st != NT_OK) return st;
-  if (B > 0 && (!d_lengths || !o || !workspace)) return fail(NT_ERR_INVALID, "NULL pointer");
-  if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(d_lengths) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return fail(NT_ERR_INVALID, "d_lengths or lse misaligned");
-  if ((double)B * max_pages * pages->page_size * H > 1e13)
-    return fail(NT_ERR_OVERFLOW, "B * max_pages * page_size * H = %g: at most 1e13",
-                (double)B * max_pages * pages->page_size * H);
-  // The longest part of a context that one SM reads: its fp32 sums run in turn, and the warps that fetch queries
-  // and merge wait for all of it, 2 s at most (2^24 keys of 1 KB at an SM's part of HBM's rate: 0.4 s).  Pages of a
-  // multiple of 8 are dealt out to the SMs evenly, so there 2^31 positions in all do (128 SMs and more).
-  constexpr int64_t kPositions = 1 << 24;
-  const int64_t cap = min64((int64_t)max_pages * pages->page_size, 0x7fffffff);
-  if (B > 0 && cap > kPositions) {
-    const int G = H / pages->H_kv;
-    if (pages->page_size % 8)
-      return fail(NT_ERR_UNSUPPORTED, "tables of more than 2^24 positions need pages of a multiple of 8");
-    if ((double)B * pages->H_kv * ((G + 7) / 8) * cap > 128.0 * kPositions)
-      return fail(NT_ERR_UNSUPPORTED, "B * H_kv * ceil(G / 8) * positions = %g: at most 2^31 with tables of more than 2^24",
-                  (double)B * pages->H_kv * ((G + 7) / 8) * cap);
-  }
-  const size_t need = paged_attn_workspace_bytes(H / pages->H_kv, pages->d);
-  if (B > 0 && workspace_bytes < need)
-    return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
-  if (B == 0) return NT_OK;
-  const PagedAttnProblem p = {pool_of(pages), q, q_stride, B, H, pages->d, d_block_table, max_pages, d_lengths,
-                              scale, o, lse, workspace};
+  PagedAttnProblem p;
+  const nt_status st = check_paged_attn(pages, q, q_stride, B, H, d_block_table, max_pages, d_lengths, scale, o, lse,
+                                        workspace, workspace_bytes, &p);
+  if (st != NT_OK || B == 0) return st;
   const cudaError_t e = launch_paged_attn(pages->dtype, p, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return NT_OK;
+}
+
+nt_status nt_selftest_paged_attn(int32_t kernel, int32_t cluster, const nt_kv_pages* pages, const void* q,
+                                 int64_t q_stride, int32_t B, int32_t H, const int32_t* d_block_table,
+                                 int32_t max_pages, const int32_t* d_lengths, float scale, void* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (kernel < 0 || kernel > 2) return fail(NT_ERR_INVALID, "kernel %d (0, 1 or 2)", kernel);
+  if (cluster < 0 || cluster > kPagedMaxCluster || (cluster && kernel != 1))
+    return fail(NT_ERR_INVALID, "cluster %d: 0, or 1 to %d for kernel 1", cluster, kPagedMaxCluster);
+  PagedAttnProblem p;
+  const nt_status st = check_paged_attn(pages, q, q_stride, B, H, d_block_table, max_pages, d_lengths, scale, o, lse,
+                                        workspace, workspace_bytes, &p);
+  if (st != NT_OK || B == 0) return st;
+  if ((kernel == 0 && std::isinf(paged_attn_short_us(pages->dtype, p))) ||
+      (kernel == 2 && std::isinf(paged_attn_tma_us(pages->dtype, p))))
+    return fail(NT_ERR_UNSUPPORTED, "kernel %d does not take this call", kernel);
+  if (kernel == 1 && cluster == 0) paged_attn_spread_us(pages->dtype, p, &cluster);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = kernel == 0   ? launch_paged_attn_short(pages->dtype, p, status_word(), s)
+                        : kernel == 1 ? launch_paged_attn_spread(pages->dtype, p, cluster, status_word(), s)
+                                      : launch_paged_attn_tma(pages->dtype, p, status_word(), s);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return NT_OK;
 }

@@ -445,6 +445,7 @@ constexpr int kPagedShortKeys = 1024;
 double paged_attn_short_us(nt_dtype dt, const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_short(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
 // A cluster of CTAs per item; any page size.
+constexpr int kPagedMaxCluster = 12;    // CTAs (beyond 12 fewer of them run at once than there are SMs for)
 double paged_attn_spread_us(nt_dtype dt, const PagedAttnProblem& p, int* cluster);
 cudaError_t launch_paged_attn_spread(nt_dtype dt, const PagedAttnProblem& p, int cluster, unsigned int* status,
                                      cudaStream_t s);

@@ -21,7 +21,7 @@ namespace {
 
 using namespace paged;
 
-constexpr int kMaxCluster = 12;              // CTAs (beyond 12 fewer of them run at once than there are SMs for)
+constexpr int kMaxCluster = kPagedMaxCluster;
 constexpr int64_t kMaxClusters = 1 << 24;    // of a launch
 
 template <typename T, int D, int HP>

@@ -96,6 +96,7 @@ SIGNATURES = {
     "nt_paged_copy": (_I32, [_PG, _P, _P, _I64, _P]),
     "nt_paged_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "nt_paged_attn": (_I32, [_PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
+    "nt_selftest_paged_attn": (_I32, [_I32, _I32, _PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_device_status": (_I32, [_P]),
     "nt_selftest_bounded_wait": (_I32, [_I32, ctypes.c_uint64, ctypes.c_uint64, _P, _P]),
     "nt_status_str": (ctypes.c_char_p, [_I32]),
@@ -766,6 +767,31 @@ def nt_selftest_bounded_wait(mode: int, delay_ns: int, limit_ns: int, result: Op
     st = lib().nt_selftest_bounded_wait(int(mode), int(delay_ns), int(limit_ns), _ptr(result), _stream(stream))
     _check(st, "nt_selftest_bounded_wait")
     return result
+
+
+def nt_selftest_paged_attn(kernel: int, pages: KVPages, q: torch.Tensor, block_table: torch.Tensor,
+                           lengths: torch.Tensor, scale: Optional[float] = None, cluster: int = 0,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """nt_paged_attn by kernel 0 (a warp per item), 1 (a cluster of CTAs per
+    item, ``cluster`` of them or as the call would) or 2 (tiles dealt out), for
+    tests of each.  q (B, H, d), block_table and lengths contiguous.  Returns
+    (o, lse)."""
+    B, H, d = q.shape
+    if q.dtype != pages.dtype or block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+        raise ValueError("q in the pages' dtype, block_table and lengths int32")
+    if d != pages.d or block_table.shape[0] != B or lengths.numel() != B:
+        raise ValueError("q must be (B, H, d) with the pages' d, block_table (B, max_pages), lengths (B)")
+    if not all(t.is_cuda and t.is_contiguous() for t in (q, block_table, lengths)):
+        raise ValueError("expected contiguous CUDA tensors")
+    o, lse = torch.empty_like(q), torch.empty(H, B, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(nt_paged_attn_workspace_bytes(H, pages.H_kv, d), dtype=torch.uint8, device=q.device)
+    st = lib().nt_selftest_paged_attn(int(kernel), int(cluster), ctypes.byref(pages.c), _ptr(q), H * d, B, H,
+                                      _ptr(block_table), block_table.shape[1], _ptr(lengths),
+                                      d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(workspace),
+                                      workspace.nbytes, _stream(stream))
+    _check(st, "nt_selftest_paged_attn")
+    return o, lse
 
 
 def nt_pair_block_fused(part: Partition, s_left: torch.Tensor, s_right: torch.Tensor, w, W3=None, b3=None,
