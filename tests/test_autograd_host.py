@@ -96,6 +96,23 @@ def test_second_derivatives_of_the_block_raise(monkeypatch):
     assert all(not x.requires_grad for x in run())
 
 
+def test_gradients_with_create_graph_can_be_changed_in_place(rope):
+    """As those of torch's own operations can: scaled, accumulated, clipped."""
+    q, k, g = _leaves()
+    loss = lambda: sum((y ** 2).sum() for y in ag.qk_norm_rope(q, k, None, q_gamma=g))
+    want = [2 * x for x in torch.autograd.grad(loss(), (q, k, g))]
+    grads = torch.autograd.grad(loss(), (q, k, g), create_graph=True)
+    for x, y in zip(grads, want):
+        assert torch.equal(x.mul_(2), y)
+    with torch.no_grad():
+        for x, y in zip(grads, want):
+            assert torch.equal(x.mul_(0.5).mul_(2), y)
+    for _ in range(2):
+        loss().backward(create_graph=True)
+    for x, y in zip((q, k, g), want):
+        assert torch.allclose(x.grad, y)
+
+
 @pytest.mark.parametrize("side", [0, 1])
 def test_a_gamma_without_its_side_takes_no_part(rope, side):
     x, _, g = _leaves()

@@ -30,12 +30,13 @@ from . import nt
 
 
 class _FirstOnly(torch.autograd.Function):
-    """Passes gradients on; raises when they are differentiated."""
+    """Passes gradients on, as copies (views of its inputs could not be
+    changed in place); raises when they are differentiated."""
 
     @staticmethod
     def forward(ctx, name, n, *tensors):
         ctx.name = name
-        return tensors[:n]
+        return tuple(t.clone() for t in tensors[:n])
 
     @staticmethod
     def backward(ctx, *_):
