@@ -664,7 +664,9 @@ nt_status nt_rope_turns(int32_t rot_dim, double base, int32_t scaling, double fa
  *   q_out, k_out  [T, H, d], tokens q_out_stride / k_out_stride elements
  *                 apart; may equal q / k with the same stride (in place),
  *                 otherwise must not overlap any input.
- * fp32 arithmetic, one rounding to the I/O dtype at the end.  Asynchronous.
+ * fp32 arithmetic, one rounding to the I/O dtype at the end; in bf16 the sines
+ * and cosines are the hardware's, off by 2^-20 at most, so that before its
+ * rounding an output is off by that part of |y_a| + |y_b|.  Asynchronous.
  */
 nt_status nt_qk_norm_rope(nt_dtype dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                           int64_t T, int32_t H_q, int32_t H_k, int32_t d, const float* q_gamma,
@@ -778,7 +780,9 @@ size_t nt_paged_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d);
  *                 (max_pages * page_size, up to 2^31 - 1 of them): pages of a
  *                 multiple of 8, and B * H_kv * ceil(G / 8) * positions at
  *                 most 2^31 (NT_ERR_UNSUPPORTED).
- *   d_block_table [B, max_pages] int32.
+ *   d_block_table [B, max_pages] int32.  Its width is what the call knows of
+ *                 the lengths and chooses its kernel by: cut to the longest
+ *                 context, short ones are faster.
  *   d_lengths     [B] int32, the positions of each sequence that are attended
  *                 to; 0 gives o = 0 and lse = -inf.  Lengths are read on the
  *                 device only: a captured call follows them.  A negative

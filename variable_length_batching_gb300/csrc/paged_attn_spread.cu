@@ -9,8 +9,8 @@
 // filled row by row with cp.async, and no barrier while it has slices.  Then
 // the warps' results are merged in the CTA, and the CTAs' through distributed
 // shared memory, each CTA joining its share of the output columns, in place
-// of a second launch.  A context of 777 keys and 12 heads of 64 takes 4.1 us
-// (8.0 on the tile kernel), four of 4,000 with 8 key heads of 128 13.6 (17.8).
+// of a second launch.  A context of 777 keys and 12 heads of 64 takes 4.2 us
+// (8.3 on the tile kernel), four of 4,000 with 8 key heads of 128 14.1 (18.3).
 #include <type_traits>
 
 #include "paged_plan.cuh"
@@ -312,7 +312,7 @@ cudaError_t run(const PagedAttnProblem& p, int cluster, unsigned int* status, cu
 // fit on the device at once (two CTAs on an SM) run together.  A batch waits for
 // its longest items, so theirs count a quarter more: 16 contexts of up to 4,688
 // keys, most of them far shorter, 8 key heads of 128, take 27.4 us here and
-// 17.6 on the tile kernel, which deals them out evenly; all of 4,000 41.9 and
+// 17.6 on the tile kernel, which deals them out evenly; all of 4,000 42.7 and
 // 46.9.  HBM gives 6.8 TB/s.
 template <typename T, int D, int HP>
 double estimate(const PagedAttnProblem& p, int* cluster) {

@@ -7,7 +7,7 @@
 // per SM holds 128 to 160 KB of key/value tiles in flight (what a latency of
 // about 1 us at the SM's share of the bandwidth needs, three times over).
 // Four contexts of 120,000 keys with 8 key heads of 128 take 279 us in bf16
-// (104% of the measured copy rate), 64 of 16 to 8,192 keys 56 us (82%), in
+// (104% of the measured copy rate), 64 of 16 to 8,192 keys 57 us (82%), in
 // fp32 106 (87%).
 //
 // Two producer warps walk the CTA's share of the batch (paged_plan.cuh) tile
@@ -449,7 +449,8 @@ cudaError_t run_d(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, 
   // batch of 64 with 8 heads to a key head of 128: 65.7 us with one, 60.1 with
   // two; with four heads 57.3 and 57.4, and many short contexts lose 4%, as the
   // registers have to do for 13 warps); the eight together for more than eight
-  // (16 heads: 78 us where one alone took 104).
+  // (16 heads: 78 us where one alone took 104; the probabilities' second
+  // product adds 2 to 5% to these).
   if (dt == NT_BF16) {
     if (G <= 4) return run<bf16, D, 8, 1>(p, status, s);
     return G <= 8 ? run<bf16, D, 8, 2>(p, status, s) : run<bf16, D, 16, 0>(p, status, s);

@@ -14,8 +14,9 @@
 //   dgamma = sum g x r,  h = g gamma,  dx = r (h - x r mean(h x r)).
 //
 // Both directions are bound by HBM (65,536 tokens of 12 + 12 heads of 64 in
-// bf16: forward 66 to 69 us, 86 to 90% of the measured copy rate, backward 97,
-// 92%; 16,384 of 32 + 8 of 128: 55.3 and 80.8, 89% and 92%), and at about ten
+// bf16: forward 66 to 69 us, 86 to 90% of the measured copy rate, backward 96,
+// 93%; 16,384 of 32 + 8 of 128: 53.3 and 78.9, 93% and 94%; in fp32 forward 110,
+// 90%, and 30,000 of 12 + 12 of 64 67.8, 80%), and at about ten
 // operations an element not by much, so the layout keeps loads in flight
 // without holding registers or waiting at barriers.  A row (one head of one
 // token) is a group of LP lanes, 16 elements to a lane in 16-byte words spread
@@ -144,9 +145,9 @@ struct Lane {
       const int j = kInter ? (col(2 * e / V) + 2 * e % V) / 2 : col(e / V) + e % V;
       const float frac = (float)(int32_t)(((uint64_t)pos * a.turns[j]) >> 32);     // in 2^-32 turns, [-1/2, 1/2)
       // For bf16 the hardware's sine and cosine do: within [-pi, pi] they are
-      // off by 2^-21 at most, an eighth of a percent of the half step (2^-9)
-      // that the output is rounded by, and cost an eighth of the exact ones,
-      // which fp32 takes.
+      // off by 2^-21, with the angle's rounding by 2^-20 at most, a 4,096th of
+      // the half step (2^-8) that an output as large as its pair is rounded by,
+      // and cost an eighth of the exact ones, which fp32 takes.
       if constexpr (sizeof(T) == 2) __sincosf(frac * 1.4629180792671596e-9f, &s[e], &c[e]);    // 2 pi 2^-32
       else sincospif(frac * 4.656612873077393e-10f, &s[e], &c[e]);                            // 2^-31: half turns
       c[e] *= a.scale;

@@ -737,8 +737,9 @@ def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, le
                   lse: Optional[torch.Tensor] = None, want_lse: bool = False,
                   workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of one new token per sequence, q (B, H, d), over the first
-    lengths[b] positions of its paged cache; H a multiple of H_kv.  Returns
-    (o, lse [H, B] or None).  ``workspace``: nt_paged_attn_workspace_bytes()
+    lengths[b] positions of its paged cache; H a multiple of H_kv, d 32, 64 or
+    128.  The kernel is chosen by ``block_table``'s width: cut to the longest
+    context, short ones are faster.  Returns (o, lse [H, B] or None).  ``workspace``: nt_paged_attn_workspace_bytes()
     bytes (None allocates them per call)."""
     st, out, lse = (_binding or _calls()).paged_attn(pages.address, pages.index, q, block_table, lengths, scale, out,
                                                      lse, want_lse, workspace, _handle(stream))
