@@ -804,6 +804,148 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
                         const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths, float scale,
                         void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * nt_paged_write_slots -- nt_paged_write with each token's place given: token
+ * t goes to position d_slots[t] of the pool, page d_slots[t] / page_size, row
+ * d_slots[t] % page_size (nt_paged_resize makes such a map, one for all layers
+ * of a step).  -1 writes nothing (tokens that only fill up a captured batch);
+ * any other slot outside the pool is flagged (NT_ERR_DEVICE_CHECK) and not
+ * written.
+ *   k, v          as in nt_paged_write.   d_slots [T] int64.
+ * No two tokens of one call may share a slot.  Asynchronous.
+ */
+nt_status nt_paged_write_slots(const nt_kv_pages* pages, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int64_t T, const int64_t* d_slots, void* stream);
+
+/*
+ * nt_paged_resize -- block tables and slot maps on the device, from lengths:
+ * row b of the table is brought from d_lengths[b] positions to
+ * d_new_lengths[b].  Rows that shrink give their last pages back to a stack of
+ * free pages, then rows that grow take theirs from its top.  Nothing is read
+ * on the host, so a captured step makes room again at every replay.
+ *   d_new_lengths [B] int32, in [0, max_pages * page_size]: one outside is
+ *                 flagged (NT_ERR_DEVICE_CHECK) and its row left as it is, as
+ *                 is a row whose present length is outside.
+ *   d_block_table [B, max_pages] int32, in and out: entries of pages given
+ *                 back become -1; entries behind are not touched.
+ *   d_lengths     [B] int32, in and out.
+ *   d_free_pages  [n_pages] int32 and d_n_free [1] int32, in and out: the
+ *                 stack.  The released page of rank r and the taken one of
+ *                 rank k (rows in order, a row's pages in order) have the
+ *                 place n_free + released - 1 - rank, so lengths that go back
+ *                 to what they were leave table and stack as they were.  A
+ *                 stack whose count is outside [0, n_pages], or would be, is
+ *                 flagged (NT_ERR_DEVICE_CHECK) and nothing is changed.
+ *   d_cu_seqlens  [B+1] int32 out: offsets of the tokens that rows gain.
+ *   d_pos0        [B] int32 out: the lengths before.
+ *   d_slots       [T] int64 out: where token t of them goes, page * page_size +
+ *                 offset; -1 behind the last.  T is the room the caller has;
+ *                 T = 0 with NULL where nothing grows.
+ *   d_lacking     [2] int32 out: free pages that are missing, and tokens that
+ *                 do not fit T.  Where one is not 0 nothing is changed:
+ *                 d_cu_seqlens is 0, all slots -1, and d_pos0 the lengths.
+ *   page_size in [1, 65536]; B at most 2^30.  No page may belong to two rows
+ * (a table that shares pages is the host's to keep).  Two calls on one state
+ * must not overlap.  Asynchronous.
+ */
+nt_status nt_paged_resize(const int32_t* d_new_lengths, int32_t B, int32_t page_size, int32_t* d_block_table,
+                          int32_t max_pages, int32_t* d_lengths, int32_t* d_free_pages, int32_t n_pages,
+                          int32_t* d_n_free, int32_t* d_cu_seqlens, int32_t* d_pos0, int64_t* d_slots, int64_t T,
+                          int32_t* d_lacking, void* stream);
+
+/*
+ * nt_draft_tree -- the masks and positions of trees of drafted tokens: token i
+ * of segment b hangs on token d_parents[cu[b] + i] of its segment, an earlier
+ * one, or (-1) on the context.
+ *   d_parents     [T] int32: in [-1, i); others are flagged
+ *                 (NT_ERR_DEVICE_CHECK) and read as -1.
+ *   d_cu_seqlens  [B+1] int32; a segment of more than max_new tokens, or
+ *                 outside [0, T], is flagged and not written.   B at most 2^30.
+ *   max_new       longest segment, in [1, 256].
+ *   d_bits        [T, ceil(max_new / 64)] int64 out: bit j % 64 of word j / 64
+ *                 is set where the token sees token j of its segment: itself
+ *                 and those it hangs on, all the way up.
+ *   d_pos0        [B] int32 or NULL for 0: the position of a token that hangs
+ *                 on the context.
+ *   d_positions   [T] int32 out, or NULL: pos0 and the number of tokens above
+ *                 (for nt_qk_norm_rope).
+ * Tokens behind the last segment get no bits and position 0.  Asynchronous.
+ */
+nt_status nt_draft_tree(const int32_t* d_parents, const int32_t* d_cu_seqlens, int32_t B, int64_t T, int32_t max_new,
+                        const int32_t* d_pos0, int64_t* d_bits, int32_t* d_positions, void* stream);
+
+/*
+ * nt_paged_keep -- the accepted ones of a sequence's drafted tokens moved up:
+ * keys and values at position d_pos0[b] + d_kept[i] go to d_pos0[b] + i - cu[b],
+ * for every i in [cu[b], cu[b + 1]).
+ *   d_kept        [K] int32: within a segment growing, and at least 0, so that
+ *                 nothing is overwritten before it is read; an entry that is
+ *                 not is flagged (NT_ERR_DEVICE_CHECK) and not moved.
+ *   d_cu_kept     [B+1] int32 offsets; a segment outside [0, K] is flagged and
+ *                 not moved.   d_pos0 [B] int32, >= 0.   B at most 2^30.
+ *   d_block_table [B, max_pages] int32; a position outside the table, or a page
+ *                 outside [0, n_pages), is flagged and not moved.
+ * Pages behind the last kept token are the caller's to give back
+ * (nt_paged_resize).  No page that is written may belong to two rows.
+ * Asynchronous.
+ */
+nt_status nt_paged_keep(const nt_kv_pages* pages, const int32_t* d_kept, int64_t K, const int32_t* d_cu_kept, int32_t B,
+                        const int32_t* d_block_table, int32_t max_pages, const int32_t* d_pos0, void* stream);
+
+/* Bytes of device workspace nt_paged_tree_attn needs for H query heads on
+ * H_kv key heads of width d and up to max_new new tokens (partial results of
+ * items split over CTAs; at most 130 MiB, whatever the batch and the lengths).
+ * 0 for sizes the call refuses.  Calls that may overlap on the GPU need
+ * workspaces of their own; nothing needs clearing. */
+size_t nt_paged_tree_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d, int32_t max_new);
+
+/*
+ * nt_paged_tree_attn -- attention of several new tokens per sequence over its
+ * paged cache: a tree of drafted tokens, or a piece of a prompt,
+ *     o[t, h, :] = sum_x softmax_x(scale q[t, h] . K[x, h / G]) V[x, h / G]
+ * with G = H / H_kv, over the positions x that token t sees: all before the
+ * sequence's new tokens, and of the new tokens those that its mask names.  The
+ * new tokens' own keys and values are in the cache already, in packed order
+ * behind the context (nt_paged_write comes first).
+ *   q             [T, H, d] packed, in the pages' dtype, tokens q_stride
+ *                 elements apart (>= H * d, a multiple of 8 bf16 / 4 fp32
+ *                 elements).
+ *   H             a multiple of H_kv.   d in {32, 64, 128}.
+ *   d_cu_seqlens  [B+1] int32: sequence b's n_b = cu[b+1] - cu[b] new tokens, 0
+ *                 to max_new of them.   B at most 2^30.
+ *   max_new       in [0, 256].
+ *   d_block_table [B, max_pages] int32.   max_pages * page_size at most 2^24
+ *                 (NT_ERR_UNSUPPORTED), times T * H at most 1e15
+ *                 (NT_ERR_OVERFLOW).
+ *   d_lengths     [B] int32: positions of each sequence, the new tokens' among
+ *                 them (>= n_b).  A sequence whose length or offsets do not fit
+ *                 (negative, beyond max_pages * page_size, n_b > max_new) is
+ *                 flagged (NT_ERR_DEVICE_CHECK) and its outputs are not
+ *                 written; a page outside [0, n_pages) is flagged and read as
+ *                 zeros.
+ *   d_bits        [T, ceil(max_new / 64)] int64, as nt_draft_tree writes them
+ *                 (any mask will do; bits behind the segment's end are not
+ *                 read), or NULL: every new token sees itself and those before
+ *                 it.  A token that sees no position gets o = 0 and lse = -inf.
+ *                 A value at a position that a token does not see is not part
+ *                 of its sum, finite or not.
+ *   scale         finite and > 0.
+ *   o             [T, H, d] contiguous, out: tokens in no segment are left as
+ *                 they are.   lse [H, T] fp32 natural-log log-sum-exp of the
+ *                 scaled scores, or NULL.  Neither may overlap an input.
+ *   workspace     >= nt_paged_tree_attn_workspace_bytes(H, H_kv, d, max_new)
+ *                 bytes, 16-byte aligned.
+ * Softmax statistics and sums are fp32; in bf16 a probability multiplies the
+ * values as the sum of two bf16, 2^-15 of it at most away from it.  Results do
+ * not depend on scheduling; their rounding may depend on B and max_new.
+ * Asynchronous; nothing is read on the host, so a captured call follows
+ * lengths, offsets and masks from replay to replay.
+ */
+nt_status nt_paged_tree_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int64_t T, int32_t H,
+                             const int32_t* d_cu_seqlens, int32_t B, int32_t max_new, const int32_t* d_block_table,
+                             int32_t max_pages, const int32_t* d_lengths, const int64_t* d_bits, float scale, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device status word set by
  * device-side checks (bounded waits that ran out: NT_ERR_TIMEOUT; failed data
  * checks: NT_ERR_DEVICE_CHECK).  NT_OK if nothing was flagged. */

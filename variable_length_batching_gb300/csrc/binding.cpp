@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <optional>
 #include <string>
@@ -32,6 +33,12 @@ decltype(&nt_paged_write) f_write;
 decltype(&nt_paged_copy) f_copy;
 decltype(&nt_paged_attn) f_attn;
 decltype(&nt_paged_attn_workspace_bytes) f_attn_ws;
+decltype(&nt_paged_write_slots) f_write_slots;
+decltype(&nt_paged_resize) f_resize;
+decltype(&nt_draft_tree) f_tree;
+decltype(&nt_paged_keep) f_keep;
+decltype(&nt_paged_tree_attn) f_tree_attn;
+decltype(&nt_paged_tree_attn_workspace_bytes) f_tree_attn_ws;
 
 // A mismatch: ValueError with this text.
 struct Mismatch {
@@ -366,11 +373,142 @@ PyObject* paged_attn(PyObject* const* a, Py_ssize_t n) {
   return result(st, {&out, &lse});
 }
 
+int32_t* ints(const T& t, int index, const char* name) { return static_cast<int32_t*>(flat(t, index, at::kInt, name)); }
+int32_t int32_of(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  if (v < -0x80000000LL || v > 0x7fffffffLL) refuse(std::string(name) + " beyond 32 bits");
+  return (int32_t)v;
+}
+int32_t segments(const T& cu, const char* name) {
+  if (cu.numel() < 1 || cu.numel() > 0x7fffffff) refuse(std::string(name) + " has B + 1 entries");
+  return (int32_t)(cu.numel() - 1);
+}
+
+// pages, device, k, v, slots, stream
+PyObject* paged_write_slots(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 6);
+  const Pages g(a[0], a[1]);
+  const T &k = need(a[2], "k"), &v = need(a[3], "v"), &slots = need(a[4], "slots");
+  if (k.dim() != 3 || k.sizes() != v.sizes() || k.size(1) != g.p->H_kv || k.size(2) != g.p->d)
+    refuse("k and v must be (T, H_kv, d) of the pages");
+  if (slots.numel() != k.size(0)) refuse("one slot per token");
+  const Tokens kt = tokens(k, g.index, g.type, "k"), vt = tokens(v, g.index, g.type, "v");
+  const void* s = flat(slots, g.index, at::kLong, "slots");
+  Call call(g.index, a[5]);
+  const int st = unlocked(f_write_slots, g.p, kt.p, kt.stride, vt.p, vt.stride, k.size(0),
+                          static_cast<const int64_t*>(s), call.stream);
+  return result(st, {});
+}
+
+// block_table, lengths, free_pages, n_free, page_size, new_lengths, tokens, stream
+PyObject* paged_resize(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 8);
+  const T &table = need(a[0], "block_table"), &lengths = need(a[1], "lengths"), &free_pages = need(a[2], "free_pages"),
+          &n_free = need(a[3], "n_free"), &now = need(a[5], "new_lengths");
+  if (!table.is_cuda()) refuse("expected CUDA tensors");
+  const int index = table.get_device();
+  const int64_t B = lengths.numel(), tokens = integer(a[6]);
+  if (B > 0x7ffffffe || free_pages.numel() > 0x7fffffff) refuse("sizes beyond 32 bits");
+  if (now.numel() != B) refuse("one new length per row");
+  if (n_free.numel() != 1) refuse("n_free has one entry");
+  if (tokens < 0) refuse("tokens must be >= 0");
+  int32_t max_pages;
+  int32_t* t = const_cast<int32_t*>(block_table(table, B, index, max_pages));
+  int32_t *len = ints(lengths, index, "lengths"), *f = ints(free_pages, index, "free_pages"),
+          *nf = ints(n_free, index, "n_free"), *nl = ints(now, index, "new_lengths");
+  const int32_t page_size = int32_of(a[4], "page_size");
+  Call call(index, a[7]);
+  const T cu = fresh({B + 1}, at::kInt, index), pos0 = fresh({B}, at::kInt, index),
+          slots = fresh({tokens}, at::kLong, index), lacking = fresh({2}, at::kInt, index);
+  const int st = unlocked(f_resize, nl, (int32_t)B, page_size, t, max_pages, len, f, (int32_t)free_pages.numel(), nf,
+                          static_cast<int32_t*>(data(cu)), static_cast<int32_t*>(data(pos0)),
+                          static_cast<int64_t*>(data(slots)), tokens, static_cast<int32_t*>(data(lacking)), call.stream);
+  return result(st, {&cu, &pos0, &slots, &lacking});
+}
+
+// parents, cu_seqlens, max_new, pos0, bits, positions, stream
+PyObject* draft_tree(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 7);
+  const T &parents = need(a[0], "parents"), &cu = need(a[1], "cu_seqlens"), &pos0 = tensor(a[3], "pos0");
+  if (!parents.is_cuda()) refuse("expected CUDA tensors");
+  if (parents.dim() != 1) refuse("parents must be (tokens)");
+  const int index = parents.get_device();
+  const int64_t tokens = parents.numel();
+  const int32_t B = segments(cu, "cu_seqlens"), max_new = int32_of(a[2], "max_new");
+  if (pos0.defined() && pos0.numel() != B) refuse("pos0 is one start per cu_seqlens segment");
+  const int32_t *p = ints(parents, index, "parents"), *c = ints(cu, index, "cu_seqlens"), *p0 = ints(pos0, index, "pos0");
+  Call call(index, a[6]);
+  T bits = tensor(a[4], "bits"), positions = tensor(a[5], "positions");
+  const int64_t words = ((int64_t)max_new + 63) / 64;
+  if (!bits.defined()) bits = fresh({tokens, std::max<int64_t>(words, 0)}, at::kLong, index);
+  else if (bits.dim() != 2 || bits.size(0) != tokens || bits.size(1) != words)
+    refuse("bits must be (tokens, ceil(max_new / 64))");
+  if (!positions.defined()) positions = fresh({tokens}, at::kInt, index);
+  else if (positions.numel() != tokens) refuse("one position per token");
+  const int st = unlocked(f_tree, p, c, B, tokens, max_new, p0, static_cast<int64_t*>(flat(bits, index, at::kLong, "bits")),
+                          ints(positions, index, "positions"), call.stream);
+  return result(st, {&bits, &positions});
+}
+
+// pages, device, kept, cu_kept, block_table, pos0, stream
+PyObject* paged_keep(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 7);
+  const Pages g(a[0], a[1]);
+  const T &kept = need(a[2], "kept"), &cu = need(a[3], "cu_kept"), &pos0 = need(a[5], "pos0");
+  const int32_t B = segments(cu, "cu_kept");
+  if (pos0.numel() != B) refuse("pos0 is one start per cu_kept segment");
+  int32_t max_pages;
+  const int32_t* table = block_table(need(a[4], "block_table"), B, g.index, max_pages);
+  const int32_t *k = ints(kept, g.index, "kept"), *c = ints(cu, g.index, "cu_kept"), *p0 = ints(pos0, g.index, "pos0");
+  Call call(g.index, a[6]);
+  const int st = unlocked(f_keep, g.p, k, kept.numel(), c, B, table, max_pages, p0, call.stream);
+  return result(st, {});
+}
+
+// pages, device, q, cu_seqlens, block_table, lengths, max_new, bits, scale, out, lse, want_lse, workspace, stream
+PyObject* paged_tree_attn(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 14);
+  const Pages g(a[0], a[1]);
+  const int32_t d = g.p->d;
+  const T &q = need(a[2], "q"), &cu = need(a[3], "cu_seqlens"), &lengths = need(a[5], "lengths"), &bits = tensor(a[7], "bits");
+  if (q.dim() != 3 || q.size(2) != d) refuse("q must be (tokens, H, d) with the pages' d");
+  const int64_t tokens_ = q.size(0), H = q.size(1);
+  if (H > 0x7fffffff) refuse("sizes beyond 32 bits");
+  const int32_t B = segments(cu, "cu_seqlens"), max_new = int32_of(a[6], "max_new");
+  if (lengths.numel() != B) refuse("one length per sequence");
+  if (bits.defined() && (bits.dim() != 2 || bits.size(0) != tokens_ || bits.size(1) != ((int64_t)max_new + 63) / 64))
+    refuse("bits must be (tokens, ceil(max_new / 64))");
+  const Tokens qt = tokens(q, g.index, g.type, "q");
+  int32_t max_pages;
+  const int32_t* table = block_table(need(a[4], "block_table"), B, g.index, max_pages);
+  const int32_t *c = ints(cu, g.index, "cu_seqlens"), *len = ints(lengths, g.index, "lengths");
+  const int64_t* mask = static_cast<const int64_t*>(flat(bits, g.index, at::kLong, "bits"));
+  Call call(g.index, a[13]);
+  T out = tensor(a[9], "out"), lse = tensor(a[10], "lse"), ws = tensor(a[12], "workspace");
+  if (!out.defined()) out = like(q);
+  else if (out.sizes() != q.sizes()) refuse("out must have q's shape");
+  if (!lse.defined() && flag(a[11])) lse = fresh({H, tokens_}, at::kFloat, g.index);
+  if (lse.defined() && (lse.dim() != 2 || lse.size(0) != H || lse.size(1) != tokens_)) refuse("lse must be (H, tokens)");
+  if (ws.defined()) {
+    on_device(ws, g.index, "workspace");
+    if (!ws.is_contiguous()) refuse("workspace must be contiguous");
+  } else {
+    ws = bytes(f_tree_attn_ws((int32_t)H, g.p->H_kv, d, max_new), q);
+  }
+  const float scale = a[8] == Py_None ? 1.0f / std::sqrt((float)d) : (float)number(a[8]);
+  const int st = unlocked(f_tree_attn, g.p, qt.p, qt.stride, tokens_, (int32_t)H, c, B, max_new, table, max_pages, len,
+                          mask, scale, flat(out, g.index, g.type, "out"),
+                          static_cast<float*>(flat(lse, g.index, at::kFloat, "lse")), data(ws), ws.nbytes(),
+                          call.stream);
+  return result(st, {&out, &lse});
+}
+
 // Addresses of the C functions, in this order.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  arity(n, 7);
-  void* p[7];
-  for (int i = 0; i < 7; ++i) {
+  constexpr int kFunctions = 13;
+  arity(n, kFunctions);
+  void* p[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) refuse("a function's address is needed");
   }
@@ -381,6 +519,12 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   f_copy = reinterpret_cast<decltype(f_copy)>(p[4]);
   f_attn = reinterpret_cast<decltype(f_attn)>(p[5]);
   f_attn_ws = reinterpret_cast<decltype(f_attn_ws)>(p[6]);
+  f_write_slots = reinterpret_cast<decltype(f_write_slots)>(p[7]);
+  f_resize = reinterpret_cast<decltype(f_resize)>(p[8]);
+  f_tree = reinterpret_cast<decltype(f_tree)>(p[9]);
+  f_keep = reinterpret_cast<decltype(f_keep)>(p[10]);
+  f_tree_attn = reinterpret_cast<decltype(f_tree_attn)>(p[11]);
+  f_tree_attn_ws = reinterpret_cast<decltype(f_tree_attn_ws)>(p[12]);
   Py_RETURN_NONE;
 }
 
@@ -409,6 +553,11 @@ PyMethodDef kMethods[] = {
     {"paged_write", method<paged_write>(), METH_FASTCALL, nullptr},
     {"paged_copy", method<paged_copy>(), METH_FASTCALL, nullptr},
     {"paged_attn", method<paged_attn>(), METH_FASTCALL, nullptr},
+    {"paged_write_slots", method<paged_write_slots>(), METH_FASTCALL, nullptr},
+    {"paged_resize", method<paged_resize>(), METH_FASTCALL, nullptr},
+    {"draft_tree", method<draft_tree>(), METH_FASTCALL, nullptr},
+    {"paged_keep", method<paged_keep>(), METH_FASTCALL, nullptr},
+    {"paged_tree_attn", method<paged_tree_attn>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_nt_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,182 @@
+// Attention of drafted tokens over a paged cache, any page size, head width
+// 32, 64 or 128, bf16 and fp32: the general kernel.
+//
+// Work, split and partial results as draft_plan.cuh says.  An item has up to
+// 64 rows (tokens times query heads of one key head); a tile is 64 keys, whose
+// rows are fetched one by one through the block table with cp.async, a tile
+// ahead.  Each row keeps a running maximum, sum and output:
+//   S = Q K^T,  m' = max(m, scale S),  P = 2^(scale S - m'),
+//   l = l 2^(m - m') + sum P,  O = O 2^(m - m') + P V
+// with the scores that a row does not see at -infinity.  bf16: matrix products
+// of 16 rows a warp, P as the sum of two bf16 (one would be off by 2^-8 of P,
+// which shows in the output).  fp32: packed multiply-adds, 4 x 4 scores and 4
+// x D / 16 outputs to a thread.
+//
+// A value that is not finite may stand at a key that only some of the rows
+// see, and 0 times it is not 0; such values are taken out of the tile and
+// added to the rows that do see them (only where new tokens are: older keys
+// are seen by all).
+#include "draft_plan.cuh"
+#include "draft_worker.cuh"
+
+namespace nt {
+namespace {
+
+using namespace draft;
+
+constexpr int kRows = 64, kKeys = 64;
+
+template <typename T, int D>
+struct Cfg {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kThreads = kBf16 ? 128 : 256;
+  static constexpr uint32_t kRow = D * sizeof(T);
+  static constexpr uint32_t kSide = kKeys * kRow;
+  static constexpr uint32_t kScratch = kBf16 ? 0 : kRows * kRow + kRows * (kKeys + 4) * 4;   // queries, probabilities
+  static constexpr uint32_t kSmem = 4 * kSide + kScratch;
+};
+
+struct RowsArgs {
+  DraftBatch a;
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  void* workspace;
+  bool whole;
+  float scale_log2;
+};
+
+struct Shared {
+  PagedPlan plan;
+  int64_t off[2][kKeys];       // byte offsets in the pool of a tile's rows, -1 none
+  unsigned long long bad;      // keys of the tile with values that are not finite
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__((Cfg<T, D>::kThreads)) draft_rows_kernel(const RowsArgs p) {
+  using C = Cfg<T, D>;
+  using W = Rows<T, D>;
+  constexpr int kThreads = C::kThreads, kChunks = D * (int)sizeof(T) / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Shared sh;
+  const DraftBatch& a = p.a;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  draft_plan(a, kKeys, 1, blockIdx.x, gridDim.x, &sh.plan, kThreads);
+  DraftWalk w;
+  w.init(a, sh.plan, kKeys, 1, p.whole);
+  const DraftPartials part = draft_partials(p.workspace, gridDim.x, kRows);
+  int4 open = make_int4(-1, 0, 0, 0);
+  const int64_t head_bytes = (int64_t)a.page_size * C::kRow;
+  W me(smem + 4 * C::kSide);
+
+  while (w.next(a, kKeys, 1)) {
+    const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+    auto rows_of = [&](int64_t t) {                // offsets of tile t's rows
+      if (tid < kKeys) {
+        const int64_t x = t * kKeys + tid;
+        int64_t off = -1;
+        if (x < w.seq.len) {
+          const int pg = (int)(x / a.page_size);
+          const int id = a.table[(int64_t)w.seg_b * a.max_pages + pg];
+          if ((unsigned)id < (unsigned)a.n_pages)
+            off = ((int64_t)id * a.Hkv + it.kvh) * head_bytes + (x - (int64_t)pg * a.page_size) * C::kRow;
+          else
+            flag_device(a.status, kDevCheck);
+        }
+        sh.off[t & 1][tid] = off;
+      }
+    };
+    auto fetch = [&](int64_t t) {
+      uint8_t* st = smem + (t & 1) * 2 * C::kSide;
+      for (int e = tid; e < 2 * kKeys * kChunks; e += kThreads) {
+        const int side = e / (kKeys * kChunks), r = e / kChunks % kKeys, c = e % kChunks;
+        const int64_t off = sh.off[t & 1][r];
+        uint8_t* to = st + side * C::kSide + swizzled<C::kRow>(r, c);
+        if (off >= 0) cp_async16(to, static_cast<const uint8_t*>(side ? p.v : p.k) + off + c * 16);
+        else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+      }
+      cp_async_commit();
+    };
+    __syncthreads();
+    rows_of(w.t0);
+    me.load_q(static_cast<const T*>(p.q), p.q_stride, w.seq.first + it.i0, it.kvh * a.G + it.h0, it.ni, it.nh);
+    __syncthreads();
+    fetch(w.t0);
+    for (int64_t t = w.t0; t < w.t1; ++t) {
+      if (t + 1 < w.t1) rows_of(t + 1);
+      if (tid == 0) sh.bad = 0;
+      __syncthreads();
+      if (t + 1 < w.t1) fetch(t + 1);
+      else cp_async_commit();
+      cp_async_wait1();
+      __syncthreads();
+      uint8_t* st = smem + (t & 1) * 2 * C::kSide;
+      const int64_t x0 = t * kKeys;
+      const int ctx = w.seq.len - w.seq.n;
+      const bool all = x0 + kKeys <= ctx;          // every row sees every key
+      if (!all) {
+        for (int e = tid; e < kKeys * kChunks; e += kThreads)
+          if (clear_bad<T>(st + C::kSide + swizzled<C::kRow>(e / kChunks, e % kChunks)))
+            atomicOr(&sh.bad, 1ull << (e / kChunks));
+        __syncthreads();
+      }
+      me.tile(a, w.seq, it, st, st + C::kSide, x0, all, p.scale_log2);
+      if (!all && sh.bad) {
+        const uint64_t bad = sh.bad;
+        me.add_bad(a, w.seq, it, x0, bad, static_cast<const uint8_t*>(p.v), sh.off[t & 1]);
+      }
+      __syncthreads();
+    }
+    cp_async_wait0();
+    const bool whole = w.begins && w.ends;
+    if (whole) {
+      me.store(a, w.seq, it, static_cast<T*>(p.o), p.lse);
+    } else {
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
+      me.store_part(part.ml + slot * kRows * 2, part.o + slot * kRows * D);
+    }
+    if (w.begins && !w.ends)
+      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(sh.plan, 1, blockIdx.x, gridDim.x));
+  }
+  if (tid == 0) part.open[blockIdx.x] = open;
+}
+
+template <typename T, int D>
+cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
+  using C = Cfg<T, D>;
+  RowsArgs r = {};
+  r.a = draft_batch(p, kRows, 1, status);
+  r.q = p.q;
+  r.q_stride = p.q_stride;
+  r.k = p.pool.k;
+  r.v = p.pool.v;
+  r.o = p.o;
+  r.lse = p.lse;
+  r.workspace = p.workspace;
+  r.whole = false;
+  r.scale_log2 = p.scale * 1.4426950408889634f;
+  const int per_sm = C::kSmem <= 110 * 1024 ? 2 : 1, ctas = min(per_sm * sm_count(), kPagedMaxCtas);
+  cudaError_t e = allow_smem_once<draft_rows_kernel<T, D>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(draft_rows_kernel<T, D>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, r);
+  if (e != cudaSuccess) return e;
+  return launch_draft_join(C::kBf16 ? NT_BF16 : NT_F32, r.a, D, ctas, kRows, p.workspace, p.o, p.lse, s);
+}
+
+}  // namespace
+
+cudaError_t launch_draft_rows(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
+  if (dt == NT_BF16) {
+    if (p.d == 32) return run<bf16, 32>(p, status, s);
+    return p.d == 64 ? run<bf16, 64>(p, status, s) : run<bf16, 128>(p, status, s);
+  }
+  if (p.d == 32) return run<float, 32>(p, status, s);
+  return p.d == 64 ? run<float, 64>(p, status, s) : run<float, 128>(p, status, s);
+}
+
+}  // namespace nt

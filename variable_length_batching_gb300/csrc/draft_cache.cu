@@ -1,0 +1,398 @@
+// What a step with drafted tokens needs around its attention: block tables
+// and slot maps from request lengths, the tree's masks and positions, and the
+// accepted tokens' keys and values moved up.  All three are latencies: a
+// launch, and a few dependent loads.
+#include "nt_common.cuh"
+
+namespace nt {
+namespace {
+
+// ---- block tables and slot maps -------------------------------------------------
+//
+// One cluster of CTAs for the whole call, so that a phase may read what the one
+// before it wrote with no second launch: the scan of what each row releases,
+// takes and adds; then the released pages, then the taken ones, then the
+// slots.  Every CTA scans all rows (their lengths are a load that all do at
+// once), a thread a strip of them; pages and tokens are then dealt out one by
+// one over all threads, however they lie in the rows.
+constexpr int kResizeThreads = 512;
+constexpr int kResizeCtas = 8;
+
+struct ResizeArgs {
+  const int32_t* new_lengths;
+  int32_t* lengths;
+  int32_t* table;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* cu;
+  int32_t* pos0;
+  int64_t* slots;
+  int32_t* lacking;
+  int B, page_size, max_pages, n_pages;
+  int64_t T, cap;
+  unsigned int* status;
+};
+
+struct Change {
+  int old, now;             // positions before and after
+  int have, want;           // pages
+};
+__device__ __forceinline__ Change change_of(const ResizeArgs& a, int b, unsigned int* status) {
+  Change c;
+  c.old = a.lengths[b];
+  c.now = a.new_lengths[b];
+  if (c.old < 0 || c.old > a.cap || c.now < 0 || c.now > a.cap) {
+    flag_device(status, kDevCheck);
+    c.now = c.old;          // left as it is, and without pages to move
+    c.have = c.want = 0;
+    return c;
+  }
+  c.have = (int)(((int64_t)c.old + a.page_size - 1) / a.page_size);
+  c.want = (int)(((int64_t)c.now + a.page_size - 1) / a.page_size);
+  return c;
+}
+struct Sums {
+  int64_t rel, take, add;   // pages released and taken, tokens added
+  __device__ __forceinline__ void operator+=(const Sums& o) {
+    rel += o.rel;
+    take += o.take;
+    add += o.add;
+  }
+};
+__device__ __forceinline__ Sums sums_of(const Change& c) {
+  return {max(c.have - c.want, 0), max(c.want - c.have, 0), max((int64_t)c.now - c.old, (int64_t)0)};
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const ResizeArgs a) {
+  __shared__ Sums warp_sum[kResizeThreads / 32];
+  __shared__ Sums ahead[kResizeThreads];           // of the rows in front of a thread's strip
+  __shared__ Change one[kResizeThreads];           // strips of one row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  // the scan of what rows release, take and add, every CTA for itself
+  const int strip = (int)(((int64_t)a.B + kResizeThreads - 1) / kResizeThreads);
+  const int b_lo = (int)min64(a.B, (int64_t)tid * strip), b_hi = (int)min64(a.B, (int64_t)b_lo + strip);
+  Sums mine = {0, 0, 0};
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Change c = change_of(a, b, cta == 0 ? a.status : nullptr);
+    if (strip == 1) one[tid] = c;
+    mine += sums_of(c);
+  }
+  Sums inc = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const Sums o = {__shfl_up_sync(0xffffffffu, inc.rel, m), __shfl_up_sync(0xffffffffu, inc.take, m),
+                    __shfl_up_sync(0xffffffffu, inc.add, m)};
+    if (lane >= m) inc += o;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  const int nf = *a.n_free;
+  __syncthreads();
+  Sums before = {inc.rel - mine.rel, inc.take - mine.take, inc.add - mine.add}, total = {0, 0, 0};
+  for (int w = 0; w < kResizeThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  ahead[tid] = before;
+  const bool broken = nf < 0 || nf > a.n_pages || nf + total.rel > a.n_pages;
+  const int64_t lack = max64(0, total.take - total.rel - max(nf, 0)), over = max64(0, total.add - a.T);
+  const bool none = broken || lack > 0 || over > 0;
+  cluster_sync_all();                    // every CTA has read what is written from here on
+  if (cta == 0 && tid == 0) {
+    if (broken) flag_device(a.status, kDevCheck);
+    a.lacking[0] = (int)min64(lack, 0x7fffffff);
+    a.lacking[1] = (int)min64(over, 0x7fffffff);
+    if (!none) *a.n_free = (int)(nf + total.rel - total.take);
+    a.cu[a.B] = none ? 0 : (int)total.add;
+  }
+  {
+    Sums at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const Change c = strip == 1 ? one[tid] : change_of(a, b, nullptr);
+      if (b % ctas == cta) {
+        a.cu[b] = none ? 0 : (int)at.add;
+        a.pos0[b] = c.old;
+        if (strip == 1 && !none) a.lengths[b] = c.now;
+      }
+      at += sums_of(c);
+    }
+  }
+  const int64_t me = (int64_t)cta * kResizeThreads + tid, all = (int64_t)ctas * kResizeThreads;
+  if (none) {
+    for (int64_t t = me; t < a.T; t += all) a.slots[t] = -1;
+    return;
+  }
+  // The row whose share of a sum holds `rank`: its strip by a search, the row
+  // by a walk through the strip.
+  auto row_of = [&](int64_t Sums::*what, int64_t rank, int64_t& off, Change& c) {
+    int lo = 0, hi = kResizeThreads - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (ahead[mid].*what <= rank) lo = mid; else hi = mid - 1;
+    }
+    off = rank - ahead[lo].*what;
+    if (strip == 1) {
+      c = one[lo];
+      return lo;
+    }
+    int b = lo * strip;
+    for (;; ++b) {
+      c = change_of(a, b, nullptr);
+      const int64_t n = sums_of(c).*what;
+      if (off < n) return b;
+      off -= n;
+    }
+  };
+  // released pages: the first of them ends on top of the stack
+  const int64_t top = nf + total.rel - 1;
+  for (int64_t r = me; r < total.rel; r += all) {
+    int64_t off;
+    Change c;
+    const int b = row_of(&Sums::rel, r, off, c);
+    int32_t* e = a.table + (int64_t)b * a.max_pages + c.want + off;
+    a.free_pages[top - r] = *e;
+    *e = -1;
+  }
+  if (total.take > 0) {
+    if (total.rel > 0) cluster_sync_all();
+    for (int64_t r = me; r < total.take; r += all) {
+      int64_t off;
+      Change c;
+      const int b = row_of(&Sums::take, r, off, c);
+      a.table[(int64_t)b * a.max_pages + c.have + off] = a.free_pages[top - r];
+    }
+  }
+  if (total.take > 0 || strip > 1) cluster_sync_all();
+  for (int64_t t = me; t < a.T; t += all) {
+    int64_t slot = -1;
+    if (t < total.add) {
+      int64_t off;
+      Change c;
+      const int b = row_of(&Sums::add, t, off, c);
+      const int64_t x = c.old + off;
+      slot = (int64_t)a.table[(int64_t)b * a.max_pages + x / a.page_size] * a.page_size + x % a.page_size;
+    }
+    a.slots[t] = slot;
+  }
+  if (strip > 1) {
+    cluster_sync_all();                  // nobody reads the old lengths any more
+    for (int64_t b = me; b < a.B; b += all) a.lengths[b] = change_of(a, (int)b, nullptr).now;
+  }
+}
+
+// ---- the tree's masks and positions ---------------------------------------------
+//
+// A CTA to a sequence, a thread to a token.  In round r a token adds what the
+// token 2^r above it has gathered, so a path of 256 takes eight rounds.
+constexpr int kTreeThreads = kDraftMaxNew;
+
+__global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t* parents, const int32_t* cu, int64_t T,
+                                                                  int max_new, const int32_t* pos0, int64_t* bits,
+                                                                  int32_t* positions, unsigned int* status) {
+  __shared__ unsigned long long words[2][kTreeThreads][kDraftMaxNew / 64];
+  __shared__ int up[2][kTreeThreads], depth[2][kTreeThreads];
+  const int b = blockIdx.x, i = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int lo = cu[b], hi = cu[b + 1], n = hi - lo, W = (max_new + 63) / 64;
+  if (b == gridDim.x - 1)                          // tokens that only fill up the batch
+    for (int64_t t = max(hi, 0) + i; t < T; t += blockDim.x) {
+      if (positions) positions[t] = 0;
+      for (int w = 0; w < W; ++w) bits[t * W + w] = 0;
+    }
+  if (lo < 0 || hi < lo || hi > T || n > max_new) {
+    if (i == 0) flag_device(status, kDevCheck);
+    return;
+  }
+  if (n == 0) return;
+  if (i < n) {
+    int p = parents[(int64_t)lo + i];
+    if (p >= i || p < -1) {
+      flag_device(status, kDevCheck);
+      p = -1;
+    }
+    up[0][i] = p;
+    depth[0][i] = p >= 0;
+    for (int w = 0; w < W; ++w) words[0][i][w] = w == i >> 6 ? 1ull << (i & 63) : 0;
+  }
+  int from = 0;
+  for (int reach = 1; reach < n; reach <<= 1) {
+    __syncthreads();
+    if (i < n) {
+      const int p = up[from][i];
+      up[from ^ 1][i] = p >= 0 ? up[from][p] : -1;
+      depth[from ^ 1][i] = depth[from][i] + (p >= 0 ? depth[from][p] : 0);
+      for (int w = 0; w < W; ++w) words[from ^ 1][i][w] = words[from][i][w] | (p >= 0 ? words[from][p][w] : 0);
+    }
+    from ^= 1;
+  }
+  if (i >= n) return;
+  if (positions) positions[(int64_t)lo + i] = (pos0 ? pos0[b] : 0) + depth[from][i];
+  for (int w = 0; w < W; ++w) bits[((int64_t)lo + i) * W + w] = (int64_t)words[from][i][w];
+}
+
+// ---- the accepted tokens moved up ---------------------------------------------------
+//
+// Kept token i of a sequence goes from position pos0 + kept[i] to pos0 + i.
+// The indices grow, so kept[i] >= i: a CTA that moves a run of tokens, all
+// read before any is written, and then the next run, reads nothing that it
+// has written.  CTAs have a sequence, a range of its heads and a side each.
+constexpr int kKeepThreads = 256;
+constexpr int kKeepUnroll = 4;
+
+struct KeepArgs {
+  uint8_t* pool[2];
+  const int32_t* kept;
+  const int32_t* cu;
+  const int32_t* table;
+  const int32_t* pos0;
+  int64_t K;
+  int n_pages, page_size, H, row_bytes, B, max_pages;
+  int heads;                // of a CTA
+  unsigned int* status;
+};
+
+__device__ __forceinline__ int64_t keep_offset(const KeepArgs& a, int b, int64_t x) {
+  if (x < 0 || x >= (int64_t)a.max_pages * a.page_size) return -1;
+  const int pg = (int)(x / a.page_size);
+  const int id = a.table[(int64_t)b * a.max_pages + pg];
+  if (id < 0 || id >= a.n_pages) return -1;
+  return ((int64_t)id * a.H * a.page_size + (x - (int64_t)pg * a.page_size)) * a.row_bytes;
+}
+
+__global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepArgs a) {
+  __shared__ int64_t from[kKeepThreads], to[kKeepThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int side = blockIdx.y & 1, h0 = (int)(blockIdx.y >> 1) * a.heads, nh = min(a.heads, a.H - h0);
+  const int words = a.row_bytes / 16, per = nh * words;            // 16-byte words of a token
+  const int run = max(1, kKeepThreads * kKeepUnroll / per);        // tokens read before any is written
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    if (lo < 0 || hi < lo || hi > a.K) {
+      if (threadIdx.x == 0) flag_device(a.status, kDevCheck);
+      continue;
+    }
+    const int64_t p0 = a.pos0[b];
+    for (int i0 = lo; i0 < hi; i0 += kKeepThreads) {
+      const int n = min(kKeepThreads, hi - i0);
+      __syncthreads();
+      if (threadIdx.x < n) {
+        const int i = i0 + threadIdx.x, k = a.kept[i];
+        int64_t s = -1, d = -1;
+        if (k < i - lo || (i > lo && k <= a.kept[i - 1]) || p0 < 0) {
+          flag_device(a.status, kDevCheck);
+        } else if (k > i - lo) {
+          s = keep_offset(a, b, p0 + k);
+          d = keep_offset(a, b, p0 + i - lo);
+          if (s < 0 || d < 0) flag_device(a.status, kDevCheck);
+        }
+        from[threadIdx.x] = d < 0 ? -1 : s;
+        to[threadIdx.x] = d;
+      }
+      __syncthreads();
+      for (int r = 0; r < n; r += run) {
+        const int total = min(run, n - r) * per;
+        for (int e0 = 0; e0 < total; e0 += kKeepThreads * kKeepUnroll) {   // one pass, but for very wide tokens
+          uint4 v[kKeepUnroll];
+          uint8_t* at[kKeepUnroll];
+#pragma unroll
+          for (int u = 0; u < kKeepUnroll; ++u) {
+            const int e = e0 + u * kKeepThreads + threadIdx.x;
+            at[u] = nullptr;
+            if (e >= total) continue;
+            const int t = r + e / per, w = e % per;
+            if (from[t] < 0) continue;
+            const int64_t off = ((int64_t)(h0 + w / words) * a.page_size) * a.row_bytes + (w % words) * 16;
+            v[u] = *reinterpret_cast<const uint4*>(a.pool[side] + from[t] + off);
+            at[u] = a.pool[side] + to[t] + off;
+          }
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < kKeepUnroll; ++u)
+            if (at[u]) *reinterpret_cast<uint4*>(at[u]) = v[u];
+          __syncthreads();
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_resize(const int32_t* new_lengths, int B, int page_size, int32_t* table, int max_pages,
+                                int32_t* lengths, int32_t* free_pages, int n_pages, int32_t* n_free, int32_t* cu,
+                                int32_t* pos0, int64_t* slots, int64_t T, int32_t* lacking, unsigned int* status,
+                                cudaStream_t s) {
+  ResizeArgs a;
+  a.new_lengths = new_lengths;
+  a.lengths = lengths;
+  a.table = table;
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  a.cu = cu;
+  a.pos0 = pos0;
+  a.slots = slots;
+  a.lacking = lacking;
+  a.B = B;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.T = T;
+  a.cap = min64((int64_t)max_pages * page_size, 0x7fffffff);
+  a.status = status;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kResizeCtas);
+  cfg.blockDim = dim3(kResizeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kResizeCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_resize_kernel, a);
+}
+
+cudaError_t launch_draft_tree(const int32_t* parents, const int32_t* cu, int B, int64_t T, int max_new,
+                              const int32_t* pos0, int64_t* bits, int32_t* positions, unsigned int* status,
+                              cudaStream_t s) {
+  if (B == 0 || T == 0) return cudaSuccess;
+  return launch_pdl(draft_tree_kernel, dim3(B), dim3((max_new + 31) / 32 * 32), 0, s, parents, cu, T, max_new, pos0,
+                    bits, positions, status);
+}
+
+cudaError_t launch_paged_keep(const PagedPool& p, const int32_t* kept, int64_t K, const int32_t* cu, int B,
+                              const int32_t* table, int max_pages, const int32_t* pos0, unsigned int* status,
+                              cudaStream_t s) {
+  if (B == 0 || K == 0) return cudaSuccess;
+  KeepArgs a;
+  a.pool[0] = static_cast<uint8_t*>(p.k);
+  a.pool[1] = static_cast<uint8_t*>(p.v);
+  a.kept = kept;
+  a.cu = cu;
+  a.table = table;
+  a.pos0 = pos0;
+  a.K = K;
+  a.n_pages = p.n_pages;
+  a.page_size = p.page_size;
+  a.H = p.H;
+  a.row_bytes = p.row_bytes;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.heads = min(p.H, max(1, kKeepThreads * kKeepUnroll / 32 * 16 / p.row_bytes));     // 32 tokens in flight
+  while ((p.H + a.heads - 1) / a.heads > 32767) a.heads *= 2;
+  a.status = status;
+  const int groups = (p.H + a.heads - 1) / a.heads;
+  return launch_pdl(paged_keep_kernel, dim3(min(B, 65536), 2 * groups), dim3(kKeepThreads), 0, s, a);
+}
+
+}  // namespace nt

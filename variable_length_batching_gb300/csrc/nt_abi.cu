@@ -273,6 +273,46 @@ nt_status check_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_st
   return NT_OK;
 }
 
+// What nt_paged_tree_attn refuses, and else the problem it runs.
+nt_status check_tree_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int64_t T, int32_t H,
+                          const int32_t* d_cu_seqlens, int32_t B, int32_t max_new, const int32_t* d_block_table,
+                          int32_t max_pages, const int32_t* d_lengths, const int64_t* d_bits, float scale, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes, DraftProblem* p) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (B < 0 || T < 0 || H <= 0 || max_new < 0)
+    return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld H=%d max_new=%d", B, (long long)T, H, max_new);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
+  if (max_new > kDraftMaxNew) return fail(NT_ERR_UNSUPPORTED, "max_new=%d: at most %d", max_new, kDraftMaxNew);
+  if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
+  if (pages->d != 32 && pages->d != 64 && pages->d != 128)
+    return fail(NT_ERR_UNSUPPORTED, "head width d=%d (32, 64 or 128)", pages->d);
+  if (!(scale > 0.f) || std::isinf(scale)) return fail(NT_ERR_INVALID, "scale must be finite and > 0");
+  st = check_table(d_block_table, max_pages, B);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "q", q, q_stride, T, H, pages->d);
+  if (st != NT_OK) return st;
+  if (T > 0 && (B == 0 || !d_cu_seqlens)) return fail(NT_ERR_INVALID, "T > 0 with no segments");
+  if (T > 0 && (!d_lengths || !o || !workspace)) return fail(NT_ERR_INVALID, "NULL pointer");
+  if (!aligned16(o) || !aligned16(workspace)) return fail(NT_ERR_INVALID, "pointers must be 16-byte aligned");
+  const void* words[] = {d_cu_seqlens, d_lengths, lse};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return fail(NT_ERR_INVALID, "misaligned pointer");
+  if (reinterpret_cast<uintptr_t>(d_bits) & 7u) return fail(NT_ERR_INVALID, "d_bits misaligned");
+  const int G = H / pages->H_kv;
+  if ((double)T * G * pages->H_kv * max_pages * pages->page_size > 1e15)
+    return fail(NT_ERR_OVERFLOW, "T * H * max_pages * page_size = %g: at most 1e15",
+                (double)T * H * max_pages * pages->page_size);
+  if ((int64_t)max_pages * pages->page_size > (1 << 24))
+    return fail(NT_ERR_UNSUPPORTED, "tables of at most 2^24 positions");
+  const size_t need = draft_workspace_bytes(pages->d);
+  if (T > 0 && workspace_bytes < need)
+    return fail(NT_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  *p = {pool_of(pages), q, q_stride, T, d_cu_seqlens, B, H, pages->d, max_new, d_block_table, max_pages, d_lengths,
+        d_bits, scale, o, lse, workspace};
+  return NT_OK;
+}
+
 // u = s_left W_a^T (T rows), v = s_right W_b^T (T_cols rows), fp32.
 cudaError_t project_uv(const nt_partition* part, nt_dtype dtype, const void* s_left, const void* s_right,
                        int32_t C_s, const void* W_a, const void* W_b, int32_t C_z, float* u, float* v,
@@ -1126,9 +1166,89 @@ nt_status nt_paged_write(const nt_kv_pages* pages, const void* k, int64_t k_stri
   if (T == 0) return NT_OK;
   const int64_t es = (int64_t)esize(pages->dtype);
   const cudaError_t e = launch_paged_write(pool_of(pages), k, k_stride * es, v, v_stride * es, T, d_cu_seqlens, B,
-                                           d_pos0, d_block_table, max_pages, status_word(),
+                                           d_pos0, d_block_table, max_pages, nullptr, status_word(),
                                            static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged write launch");
+  return NT_OK;
+}
+
+nt_status nt_paged_write_slots(const nt_kv_pages* pages, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int64_t T, const int64_t* d_slots, void* stream) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (T < 0) return fail(NT_ERR_INVALID, "bad size T=%lld", (long long)T);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  st = check_tokens(pages->dtype, "k", k, k_stride, T, pages->H_kv, pages->d);
+  if (st == NT_OK) st = check_tokens(pages->dtype, "v", v, v_stride, T, pages->H_kv, pages->d);
+  if (st != NT_OK) return st;
+  if (T == 0) return NT_OK;
+  if (!d_slots) return fail(NT_ERR_INVALID, "d_slots is NULL");
+  if (reinterpret_cast<uintptr_t>(d_slots) & 7u) return fail(NT_ERR_INVALID, "d_slots misaligned");
+  const int64_t es = (int64_t)esize(pages->dtype);
+  const cudaError_t e = launch_paged_write(pool_of(pages), k, k_stride * es, v, v_stride * es, T, nullptr, 0, nullptr,
+                                           nullptr, 0, d_slots, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged write launch");
+  return NT_OK;
+}
+
+nt_status nt_paged_resize(const int32_t* d_new_lengths, int32_t B, int32_t page_size, int32_t* d_block_table,
+                          int32_t max_pages, int32_t* d_lengths, int32_t* d_free_pages, int32_t n_pages,
+                          int32_t* d_n_free, int32_t* d_cu_seqlens, int32_t* d_pos0, int64_t* d_slots, int64_t T,
+                          int32_t* d_lacking, void* stream) {
+  if (B < 0 || T < 0 || n_pages < 0 || page_size < 1 || page_size > 65536)
+    return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld n_pages=%d page_size=%d", B, (long long)T, n_pages, page_size);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
+  const nt_status st = check_table(d_block_table, max_pages, B);
+  if (st != NT_OK) return st;
+  if (!d_n_free || !d_cu_seqlens || !d_lacking || (B > 0 && (!d_new_lengths || !d_lengths || !d_pos0)) ||
+      (n_pages > 0 && !d_free_pages) || (T > 0 && !d_slots))
+    return fail(NT_ERR_INVALID, "NULL pointer");
+  const void* words[] = {d_new_lengths, d_lengths, d_free_pages, d_n_free, d_cu_seqlens, d_pos0, d_lacking};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return fail(NT_ERR_INVALID, "misaligned pointer");
+  if (reinterpret_cast<uintptr_t>(d_slots) & 7u) return fail(NT_ERR_INVALID, "d_slots misaligned");
+  const cudaError_t e = launch_paged_resize(d_new_lengths, B, page_size, d_block_table, max_pages, d_lengths,
+                                            d_free_pages, n_pages, d_n_free, d_cu_seqlens, d_pos0, d_slots, T,
+                                            d_lacking, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block table launch");
+  return NT_OK;
+}
+
+nt_status nt_draft_tree(const int32_t* d_parents, const int32_t* d_cu_seqlens, int32_t B, int64_t T, int32_t max_new,
+                        const int32_t* d_pos0, int64_t* d_bits, int32_t* d_positions, void* stream) {
+  if (B < 0 || T < 0 || max_new < 1) return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld max_new=%d", B, (long long)T, max_new);
+  if (max_new > kDraftMaxNew) return fail(NT_ERR_UNSUPPORTED, "max_new=%d: at most %d", max_new, kDraftMaxNew);
+  if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 segments", B);
+  if (T > 0 && (B == 0 || !d_cu_seqlens)) return fail(NT_ERR_INVALID, "T > 0 with no segments");
+  if (T > 0 && (!d_parents || !d_bits)) return fail(NT_ERR_INVALID, "NULL pointer");
+  const void* words[] = {d_parents, d_cu_seqlens, d_pos0, d_positions};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return fail(NT_ERR_INVALID, "misaligned pointer");
+  if (reinterpret_cast<uintptr_t>(d_bits) & 7u) return fail(NT_ERR_INVALID, "d_bits misaligned");
+  const cudaError_t e = launch_draft_tree(d_parents, d_cu_seqlens, B, T, max_new, d_pos0, d_bits, d_positions,
+                                          status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft tree launch");
+  return NT_OK;
+}
+
+nt_status nt_paged_keep(const nt_kv_pages* pages, const int32_t* d_kept, int64_t K, const int32_t* d_cu_kept, int32_t B,
+                        const int32_t* d_block_table, int32_t max_pages, const int32_t* d_pos0, void* stream) {
+  nt_status st = check_pages(pages);
+  if (st != NT_OK) return st;
+  if (B < 0 || K < 0) return fail(NT_ERR_INVALID, "bad sizes B=%d K=%lld", B, (long long)K);
+  if (K > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "K = %lld: token counts must fit int32", (long long)K);
+  if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 segments", B);
+  st = check_table(d_block_table, max_pages, B);
+  if (st != NT_OK) return st;
+  if (K > 0 && (B == 0 || !d_cu_kept || !d_kept || !d_pos0)) return fail(NT_ERR_INVALID, "K > 0 with a NULL pointer or no segments");
+  const void* words[] = {d_kept, d_cu_kept, d_pos0};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return fail(NT_ERR_INVALID, "misaligned pointer");
+  const cudaError_t e = launch_paged_keep(pool_of(pages), d_kept, K, d_cu_kept, B, d_block_table, max_pages, d_pos0,
+                                          status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kept tokens launch");
   return NT_OK;
 }
 
@@ -1176,6 +1296,25 @@ nt_status nt_paged_attn(const nt_kv_pages* pages, const void* q, int64_t q_strid
   if (st != NT_OK || B == 0) return st;
   const cudaError_t e = launch_paged_attn(pages->dtype, p, status_word(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return NT_OK;
+}
+
+size_t nt_paged_tree_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d, int32_t max_new) {
+  if (H <= 0 || H_kv <= 0 || H % H_kv || (d != 32 && d != 64 && d != 128) || max_new < 0 || max_new > kDraftMaxNew)
+    return 0;
+  return draft_workspace_bytes(d);
+}
+
+nt_status nt_paged_tree_attn(const nt_kv_pages* pages, const void* q, int64_t q_stride, int64_t T, int32_t H,
+                             const int32_t* d_cu_seqlens, int32_t B, int32_t max_new, const int32_t* d_block_table,
+                             int32_t max_pages, const int32_t* d_lengths, const int64_t* d_bits, float scale, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  DraftProblem p;
+  const nt_status st = check_tree_attn(pages, q, q_stride, T, H, d_cu_seqlens, B, max_new, d_block_table, max_pages,
+                                       d_lengths, d_bits, scale, o, lse, workspace, workspace_bytes, &p);
+  if (st != NT_OK || T == 0 || max_new == 0) return st;
+  const cudaError_t e = launch_draft_attn(pages->dtype, p, status_word(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return NT_OK;
 }
 

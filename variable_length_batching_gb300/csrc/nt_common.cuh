@@ -405,7 +405,8 @@ struct PagedPool {
 };
 cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stride_bytes, const void* v,
                                int64_t v_stride_bytes, int64_t T, const int32_t* cu, int B, const int32_t* pos0,
-                               const int32_t* table, int max_pages, unsigned int* status, cudaStream_t s);
+                               const int32_t* table, int max_pages, const int64_t* slots, unsigned int* status,
+                               cudaStream_t s);
 cudaError_t launch_paged_copy(const PagedPool& p, const int32_t* src, const int32_t* dst, int64_t n, cudaStream_t s);
 
 // One query token per sequence over a paged cache.
@@ -453,6 +454,43 @@ cudaError_t launch_paged_attn_spread(nt_dtype dt, const PagedAttnProblem& p, int
 // 8 positions.
 double paged_attn_tma_us(nt_dtype dt, const PagedAttnProblem& p);
 cudaError_t launch_paged_attn_tma(nt_dtype dt, const PagedAttnProblem& p, unsigned int* status, cudaStream_t s);
+
+// Several new tokens per sequence (drafted ones, or a piece of a prompt) over a
+// paged cache.
+constexpr int kDraftMaxNew = 256;       // new tokens of a sequence, at most
+struct DraftProblem {
+  PagedPool pool;
+  const void* q;          // [T] tokens of [H, d], q_stride elements apart
+  int64_t q_stride, T;
+  const int32_t* cu;      // [B + 1]
+  int B, H, d, max_new;
+  const int32_t* table;   // [B, max_pages]
+  int max_pages;
+  const int32_t* lengths;
+  const int64_t* bits;    // [T, ceil(max_new / 64)] or NULL
+  float scale;
+  void* o;                // [T, H, d]
+  float* lse;             // [H, T] or NULL
+  void* workspace;
+};
+struct DraftBatch;
+// The batch for items of up to `rows` rows times `groups`.
+DraftBatch draft_batch(const DraftProblem& p, int rows, int groups, unsigned int* status);
+size_t draft_workspace_bytes(int d);
+cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
+// Any page size, a CTA to 64 rows.
+cudaError_t launch_draft_rows(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
+
+cudaError_t launch_paged_resize(const int32_t* new_lengths, int B, int page_size, int32_t* table, int max_pages,
+                                int32_t* lengths, int32_t* free_pages, int n_pages, int32_t* n_free, int32_t* cu,
+                                int32_t* pos0, int64_t* slots, int64_t T, int32_t* lacking, unsigned int* status,
+                                cudaStream_t s);
+cudaError_t launch_draft_tree(const int32_t* parents, const int32_t* cu, int B, int64_t T, int max_new,
+                              const int32_t* pos0, int64_t* bits, int32_t* positions, unsigned int* status,
+                              cudaStream_t s);
+cudaError_t launch_paged_keep(const PagedPool& p, const int32_t* kept, int64_t K, const int32_t* cu, int B,
+                              const int32_t* table, int max_pages, const int32_t* pos0, unsigned int* status,
+                              cudaStream_t s);
 
 bool attn_simt_supported(int d);
 cudaError_t launch_attn_simt(nt_dtype dt, const AttnProblem& p, unsigned int* status, cudaStream_t s);

@@ -42,6 +42,7 @@ struct WriteArgs {
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* table;
+  const int64_t* slots;               // the tokens' places, where they are given
   unsigned int* status;
 };
 
@@ -62,6 +63,17 @@ __device__ __forceinline__ int64_t write_offset(const WriteArgs& a, int64_t t, i
   return off;
 }
 
+// The same of a token whose place is given; -1 (not flagged) for none.
+__device__ __forceinline__ int64_t slot_offset(const WriteArgs& a, int64_t t) {
+  const int64_t slot = a.slots[t];
+  if (slot < 0 || slot >= (int64_t)a.n_pages * a.page_size) {
+    if (slot != -1) flag_device(a.status, kDevCheck);
+    return -1;
+  }
+  const int64_t id = slot / a.page_size;
+  return (id * a.H * a.page_size + (slot - id * a.page_size)) * a.row_bytes;
+}
+
 // The rows of a token are contiguous at the source; each head's row goes to
 // its own place in the page.  The CTA's keys, then its values, are one run of
 // 16-byte words over its threads, kUnroll loads in flight: 24 KB per CTA.
@@ -73,7 +85,9 @@ __global__ void __launch_bounds__(kThreads) paged_write_kernel(const WriteArgs a
   const int n = (int)min64(a.tokens, a.T - t0);
   pdl_wait();
   pdl_trigger();
-  if (n <= kThreads / 32) {
+  if (a.slots) {
+    if (threadIdx.x < n) dst[threadIdx.x] = slot_offset(a, t0 + threadIdx.x);
+  } else if (n <= kThreads / 32) {
     if (warp < n) {
       const int b = segment_of_warp(a.cu, a.B, t0 + warp);
       if (lane == 0) dst[warp] = write_offset(a, t0 + warp, b);
@@ -153,7 +167,7 @@ cudaError_t copy_pages(const PagedPool& p, const int32_t* src, const int32_t* ds
 
 cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                                int64_t T, const int32_t* cu, int B, const int32_t* pos0, const int32_t* table,
-                               int max_pages, unsigned int* status, cudaStream_t s) {
+                               int max_pages, const int64_t* slots, unsigned int* status, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   WriteArgs a = {};
   a.src[0] = static_cast<const uint8_t*>(k);
@@ -172,6 +186,7 @@ cudaError_t launch_paged_write(const PagedPool& p, const void* k, int64_t k_stri
   a.cu = cu;
   a.pos0 = pos0;
   a.table = table;
+  a.slots = slots;
   a.status = status;
   a.by_words = Divisor(p.H * (p.row_bytes / 16));
   a.by_row = Divisor(p.row_bytes / 16);

@@ -4,8 +4,8 @@ Argument marshalling only: torch tensors supply device memory and the
 current CUDA stream; every step of the block and of varlen attention runs in
 the library's kernels.  Functions keep the C names.  If ``libnt.so`` is
 missing or a call fails, an exception is raised -- there is no other path.
-The calls of a decoding step (norm and rope, paged write, copy and attention)
-pass their arguments through a compiled module, the others through ctypes.
+The calls of a decoding step (norm and rope, paged write, copy and attention,
+those of drafted tokens) pass their arguments through a compiled module, the others through ctypes.
 """
 from __future__ import annotations
 
@@ -96,6 +96,12 @@ SIGNATURES = {
     "nt_paged_copy": (_I32, [_PG, _P, _P, _I64, _P]),
     "nt_paged_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "nt_paged_attn": (_I32, [_PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
+    "nt_paged_write_slots": (_I32, [_PG, _P, _I64, _P, _I64, _I64, _P, _P]),
+    "nt_paged_resize": (_I32, [_P, _I32, _I32, _P, _I32, _P, _P, _I32, _P, _P, _P, _P, _I64, _P, _P]),
+    "nt_draft_tree": (_I32, [_P, _P, _I32, _I64, _I32, _P, _P, _P, _P]),
+    "nt_paged_keep": (_I32, [_PG, _P, _I64, _P, _I32, _P, _I32, _P, _P]),
+    "nt_paged_tree_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "nt_paged_tree_attn": (_I32, [_PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_selftest_paged_attn": (_I32, [_I32, _I32, _PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_device_status": (_I32, [_P]),
     "nt_selftest_bounded_wait": (_I32, [_I32, ctypes.c_uint64, ctypes.c_uint64, _P, _P]),
@@ -638,7 +644,8 @@ def _calls():
             raise RuntimeError("the binding is not built; run `python -m variable_length_batching_gb300.build`") from e
         b.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
             "nt_qk_norm_rope", "nt_qk_norm_rope_bwd", "nt_qk_norm_rope_bwd_workspace_bytes", "nt_paged_write",
-            "nt_paged_copy", "nt_paged_attn", "nt_paged_attn_workspace_bytes")))
+            "nt_paged_copy", "nt_paged_attn", "nt_paged_attn_workspace_bytes", "nt_paged_write_slots", "nt_paged_resize",
+            "nt_draft_tree", "nt_paged_keep", "nt_paged_tree_attn", "nt_paged_tree_attn_workspace_bytes")))
         _binding = b
     return _binding
 
@@ -745,6 +752,82 @@ def nt_paged_attn(pages: KVPages, q: torch.Tensor, block_table: torch.Tensor, le
                                                      lse, want_lse, workspace, _handle(stream))
     if st:
         _check(st, "nt_paged_attn")
+    return out, lse
+
+
+def nt_paged_write_slots(pages: KVPages, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Keys and values of tokens (T, H_kv, d) to the positions of the pool
+    that ``slots`` (T) int64 names (nt_paged_resize's); -1 writes nothing."""
+    st, = (_binding or _calls()).paged_write_slots(pages.address, pages.index, k, v, slots, _handle(stream))
+    if st:
+        _check(st, "nt_paged_write_slots")
+
+
+def nt_paged_resize(block_table: torch.Tensor, lengths: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
+                    page_size: int, new_lengths: torch.Tensor, tokens: int = 0, stream=None):
+    """A block table kept on the device, brought to ``new_lengths`` (B):
+    pages of the rows that shrink go back to the stack ``free_pages`` (of
+    ``n_free`` (1)), rows that grow take theirs from it; ``block_table`` (B,
+    max_pages), ``lengths`` (B) and the stack, all int32, are changed in place.
+    Returns (cu_seqlens (B + 1) and slots (``tokens``) int64 of the tokens
+    that rows gain, pos0 (B) between them: the lengths before; lacking (2):
+    pages, and room in ``tokens``, that were missing; if either was, nothing
+    is changed): (cu_seqlens, pos0, slots, lacking)."""
+    st, cu, pos0, slots, lacking = (_binding or _calls()).paged_resize(block_table, lengths, free_pages, n_free,
+                                                                       page_size, new_lengths, tokens,
+                                                                       _handle(stream))
+    if st:
+        _check(st, "nt_paged_resize")
+    return cu, pos0, slots, lacking
+
+
+def nt_draft_tree(parents: torch.Tensor, cu_seqlens: torch.Tensor, max_new: int, pos0: Optional[torch.Tensor] = None,
+                  bits: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, stream=None):
+    """Masks and positions of trees of drafted tokens: token i of a segment
+    hangs on its token parents[i], an earlier one, or (-1) on the context.
+    Returns (bits (T, ceil(max_new / 64)) int64: the tokens of its segment
+    that a token sees; positions (T): pos0 and the tokens above it); tokens
+    behind the last segment get 0 of both."""
+    st, bits, positions = (_binding or _calls()).draft_tree(parents, cu_seqlens, max_new, pos0, bits, positions,
+                                                            _handle(stream))
+    if st:
+        _check(st, "nt_draft_tree")
+    return bits, positions
+
+
+def nt_paged_keep(pages: KVPages, kept: torch.Tensor, cu_kept: torch.Tensor, block_table: torch.Tensor,
+                  pos0: torch.Tensor, stream=None) -> None:
+    """The accepted drafted tokens' keys and values moved up: of sequence b,
+    those at position pos0[b] + kept[i] to pos0[b] + i - cu_kept[b], for i in
+    its ``cu_kept`` segment; ``kept`` grows within a segment."""
+    st, = (_binding or _calls()).paged_keep(pages.address, pages.index, kept, cu_kept, block_table, pos0,
+                                            _handle(stream))
+    if st:
+        _check(st, "nt_paged_keep")
+
+
+def nt_paged_tree_attn_workspace_bytes(H: int, H_kv: int, d: int, max_new: int) -> int:
+    return int(lib().nt_paged_tree_attn_workspace_bytes(int(H), int(H_kv), int(d), int(max_new)))
+
+
+def nt_paged_tree_attn(pages: KVPages, q: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
+                       lengths: torch.Tensor, max_new: int, bits: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of several new tokens per sequence, packed q (T, H, d), over
+    its paged cache of lengths[b] positions, whose last ones are the new
+    tokens': a tree of drafted tokens (``bits`` from nt_draft_tree), or a
+    chain or a piece of a prompt (None: a token sees itself and those before
+    it).  Up to ``max_new`` (at most 256) new tokens per sequence; d 32, 64 or
+    128.  Returns (o, lse [H, T] or None); tokens in no ``cu_seqlens`` segment
+    are left as they are.  ``workspace``: nt_paged_tree_attn_workspace_bytes()
+    bytes (None allocates them per call)."""
+    st, out, lse = (_binding or _calls()).paged_tree_attn(pages.address, pages.index, q, cu_seqlens, block_table,
+                                                          lengths, max_new, bits, scale, out, lse, want_lse,
+                                                          workspace, _handle(stream))
+    if st:
+        _check(st, "nt_paged_tree_attn")
     return out, lse
 
 
