@@ -52,6 +52,20 @@ def call(nt, c, scale=None, want_lse=True, **kw):
     return o, lse
 
 
+def call_kernel(nt, c, kernel, scale=None):
+    """The same by a kernel by name; None where it does not take the call."""
+    pages = nt.KVPages(c["kp"].to(DEV), c["vp"].to(DEV))
+    bits = None if c["bits"] is None else c["bits"].to(DEV)
+    try:
+        got = nt.nt_selftest_paged_tree_attn(kernel, pages, c["q"].to(DEV), _cu(c["ns"]), c["table"].to(DEV),
+                                             _i32(c["lens"]), c["max_new"], bits=bits, scale=scale)
+    except nt.NTError as e:
+        assert e.status == 2 and kernel == 1
+        return None
+    nt.nt_device_status()
+    return got
+
+
 def check(c, o, lse, scale=None):
     ro, rl, mag, cond = tree_attn(c["kp"], c["vp"], c["q"], c["ns"], c["table"], c["lens"], c["bits"], scale)
     n = max(c["lens"] + [0])
@@ -101,3 +115,8 @@ def test_tree_attn(nt, shape, dtype, kind):
     ctx, ns, page, H, Hk, d = SHAPES[shape]
     c = make_case(ctx, ns, page, H, Hk, d, dtype, kind, seed=shape)
     check(c, *call(nt, c))
+    for kernel in (0, 1):
+        got = call_kernel(nt, c, kernel)
+        assert (got is not None) == (kernel == 0 or (dtype == BF and d > 32 and page % 8 == 0 and H // Hk <= 128))
+        if got:
+            check(c, *got)

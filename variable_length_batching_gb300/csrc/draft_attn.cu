@@ -23,12 +23,12 @@ __global__ void __launch_bounds__(256) draft_join_kernel(const DraftBatch a, int
   const DraftPartials part = draft_partials(workspace, ctas, rows);
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 open = part.open[c0];
-  if (open.x < 0) return;
+  if (open.x < 0 || open.x >= a.B) return;
   const DraftSeq seq = draft_seq(a, open.x, nullptr);
   const DraftItem it = draft_item(a, seq.n, open.y, open.z);
   const int row = blockIdx.y * 8 + warp;
   if (row >= it.ni * it.nh) return;
-  const int n = open.w;                            // partial i: slot 1 of c0, then slot 0 of c0 + i
+  const int n = min(open.w, ctas - c0);            // partial i: slot 1 of c0, then slot 0 of c0 + i
   float m = -INFINITY, l = 0.f, acc[kCols] = {};
   for (int i0 = 0; i0 < n; i0 += kBatch) {
     float2 ml[kBatch];
@@ -123,7 +123,7 @@ cudaError_t launch_draft_join(nt_dtype dt, const DraftBatch& a, int d, int ctas,
 }
 
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
-  return launch_draft_rows(dt, p, status, s);
+  return draft_tc_supported(dt, p) ? launch_draft_tc(p, status, s) : launch_draft_rows(dt, p, status, s);
 }
 
 }  // namespace nt

@@ -478,6 +478,10 @@ struct DraftBatch;
 DraftBatch draft_batch(const DraftProblem& p, int rows, int groups, unsigned int* status);
 size_t draft_workspace_bytes(int d);
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
+// bf16 at d = 64 and 128, pages of a multiple of 8 positions, at most 128
+// query heads to a key head.
+bool draft_tc_supported(nt_dtype dt, const DraftProblem& p);
+cudaError_t launch_draft_tc(const DraftProblem& p, unsigned int* status, cudaStream_t s);
 // Any page size, a CTA to 64 rows.
 cudaError_t launch_draft_rows(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
 

@@ -102,6 +102,8 @@ SIGNATURES = {
     "nt_paged_keep": (_I32, [_PG, _P, _I64, _P, _I32, _P, _I32, _P, _P]),
     "nt_paged_tree_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "nt_paged_tree_attn": (_I32, [_PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P, _P, _SZ, _P]),
+    "nt_selftest_paged_tree_attn": (_I32, [_I32, _PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P,
+                                           _P, _SZ, _P]),
     "nt_selftest_paged_attn": (_I32, [_I32, _I32, _PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_device_status": (_I32, [_P]),
     "nt_selftest_bounded_wait": (_I32, [_I32, ctypes.c_uint64, ctypes.c_uint64, _P, _P]),
@@ -875,6 +877,32 @@ def nt_selftest_paged_attn(kernel: int, pages: KVPages, q: torch.Tensor, block_t
                                       d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(workspace),
                                       workspace.nbytes, _stream(stream))
     _check(st, "nt_selftest_paged_attn")
+    return o, lse
+
+
+def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu_seqlens: torch.Tensor,
+                                block_table: torch.Tensor, lengths: torch.Tensor, max_new: int,
+                                bits: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None):
+    """nt_paged_tree_attn by kernel 0 (the general one) or 1 (the tensor
+    cores'), for tests of each; contiguous tensors.  Returns (o, lse)."""
+    T, H, d = q.shape
+    B = cu_seqlens.numel() - 1
+    if q.dtype != pages.dtype or any(t.dtype != torch.int32 for t in (cu_seqlens, block_table, lengths)):
+        raise ValueError("q in the pages' dtype, cu_seqlens, block_table and lengths int32")
+    if d != pages.d or block_table.shape[0] != B or lengths.numel() != B:
+        raise ValueError("q must be (tokens, H, d) with the pages' d, block_table (B, max_pages), lengths (B)")
+    if bits is not None and (bits.dtype != torch.int64 or tuple(bits.shape) != (T, -(-max_new // 64))):
+        raise ValueError("bits must be int64 (tokens, ceil(max_new / 64))")
+    o, lse = torch.empty_like(q), torch.empty(H, T, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(nt_paged_tree_attn_workspace_bytes(H, pages.H_kv, d, max_new), dtype=torch.uint8,
+                                device=q.device)
+    st = lib().nt_selftest_paged_tree_attn(int(kernel), ctypes.byref(pages.c), _ptr(q), H * d, T, H, _ptr(cu_seqlens), B,
+                                           int(max_new), _ptr(block_table), block_table.shape[1], _ptr(lengths),
+                                           _ptr(bits), d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse),
+                                           _ptr(workspace), workspace.nbytes, _stream(stream))
+    _check(st, "nt_selftest_paged_tree_attn")
     return o, lse
 
 
