@@ -12,20 +12,24 @@
 // CTAs are joined by a second kernel.
 //
 // A step is one row tile against one key tile:
-//   S = Q K^T           (128 x 128; one of kBufs buffers in TMEM)
+//   S = Q K^T           (128 x 128 in TMEM)
 //   P = 2^(scale S - m) as the sum of two bf16, written over S
 //   O += P V            (two products, P from TMEM; O stays in TMEM)
-// Warps: 0 to 7 softmax, 8 issues the products, 9 and 10 fetch keys and
-// values, 11 queries.  A row's 128 scores belong to two threads (warps w and
-// w + 4), 64 each, which tell one another their maxima; a thread keeps its
-// scores in registers from S to P.  The products of step s + 1 run under the
-// softmax of step s, and the fetches under both.  The running maximum m moves
-// only when a tile's exceeds it by 8 (a factor of 256, which fp32 sums and the
-// bf16 parts of P bear), so O is rescaled on few tiles.
+// Steps alternate between two streams, each with its S, its O and its
+// softmax warps, a row to a thread: with two row tiles a stream is a row tile;
+// with one, the streams take every other key tile, and their sums are joined
+// in the end.  So the products of one stream run under the softmax of the
+// other, and the fetches under both.  Warps: 0 to 3 and 4 to 7 softmax, 8 issues
+// Q K^T and 11 P V, each as soon as its operands are there (one warp for both
+// took over 1,000 cycles a step to find out which), 9 fetches queries and keys,
+// 10 values.  The running
+// maximum m moves only when a tile's exceeds it by 8 (a factor of 256, which
+// fp32 sums and the bf16 parts of P bear), so O is rescaled on few tiles.
 //
 // Two bf16 for P: one would be off by 2^-8 of P, which shows in the output.
-// The upper part is cut from P (1 - 2^-10), so that both parts are positive:
-// an infinite value in the cache then gives the infinity that P times it is.
+// The upper part is P cut short, the lower P (1 + 2^-20) less that, so that
+// both are positive: an infinite value in the cache then gives the infinity
+// that P times it is.
 //
 // Tiles behind the context (new tokens, the last key) are the only ones with a
 // mask, and with rows of V that a product may not read as they are: those
@@ -40,9 +44,10 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kSoftmax = 8;                         // warps
+constexpr int kSoftmax = 8;                         // warps, four to a stream
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;                     // S of stream g at 128 g, O at kColO + D g
 
 template <int D, int R>
 struct Cfg {
@@ -54,23 +59,20 @@ struct Cfg {
   static constexpr int kFit = (int)((227 * 1024 - kCtl - kQBufs * kQ) / kTile);
   static constexpr int kK = kFit / 2, kV = kFit - kK;              // stages of keys and of values
   static constexpr uint32_t kSmem = kQBufs * kQ + (kK + kV) * kTile + kCtl;
-  static constexpr int kFitBufs = (512 - R * D) / 128;
-  static constexpr int kBufs = kFitBufs > 3 ? 3 : kFitBufs;        // of S
-  static constexpr uint32_t kColO = kBufs * 128;
   static constexpr int kExtra = 1;                                 // an item's cost beside its tiles, in tiles
-  static_assert(kK >= 2 && kBufs >= 2 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kK >= 2 && kSmem <= 227 * 1024, "shared memory");
 };
 
 constexpr int kMaxStages = 7, kSpecial = 3;         // tiles behind the context, at most: 127 + 256 keys
 struct Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[3], p_full[3], pv_done[3], o_free, mma_done;
-  uint64_t pair[4][2];                              // two warps of the same rows
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free, s_end, pv_end;  // [2]: of a stream
+  uint64_t pair[4];                                 // two warps of the same rows
   uint32_t tmem_base;
   int abort;
   unsigned int bad[3][kSpecial * 4 + 1];            // of three segments in turn: keys, and whether any
-  float word[2][2][kRows];                          // what the two threads of a row tell one another
+  float2 word[2][kRows];                            // maximum and sum of a row in a stream
   PagedPlan plan;
 };
 static_assert(sizeof(Ctl) <= 3072, "control block");
@@ -98,12 +100,55 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// mbar_wait, whose clock is read only after some tries; by one thread, and by
+// a warp.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort, status));
+}
+
+// Columns [c, c + 32) of what was taken out of the segment's tiles, added to
+// the outputs of new token i where it sees them.
+__device__ __forceinline__ void add_bad(const DraftBatch& a, const DraftWalk& w, const DraftItem& it, int i,
+                                        const unsigned int* bad, const uint8_t* v, int c, int d, float (&ov)[32]) {
+  const int64_t t0 = (w.seq.len - w.seq.n) / kKeys;
+  for (int64_t t = max64(w.t0, t0); t < w.t1; ++t)
+    for (int k = 0; k < 4; ++k) {
+      const unsigned int there = bad[(int)(t - t0) * 4 + k];
+      if (!there) continue;
+      const int64_t x0 = t * kKeys + k * 32;
+      unsigned int todo = there & (unsigned int)draft_sees(a, w.seq, i, x0);
+      for (; todo; todo &= todo - 1) {
+        const int64_t x = x0 + __ffs(todo) - 1;
+        const int pg = (int)(x / a.page_size), id = a.table[(int64_t)w.seg_b * a.max_pages + pg];
+        if ((unsigned)id >= (unsigned)a.n_pages) continue;
+        const uint4* vr = reinterpret_cast<const uint4*>(
+            v + ((((int64_t)id * a.Hkv + it.kvh) * a.page_size + (x - (int64_t)pg * a.page_size)) * d + c) * 2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 q = vr[u];
+          const uint32_t z[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            ov[8 * u + 2 * y] += draft::if_bad(bf16lo(z[y]));
+            ov[8 * u + 2 * y + 1] += draft::if_bad(bf16hi(z[y]));
+          }
+        }
+      }
+    }
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const TcArgs p) {
   using C = Cfg<D, R>;
-  constexpr int NB = C::kBufs, kE = C::kExtra, kPartRows = R * kRows;
+  constexpr int kE = C::kExtra, kPartRows = R * kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const DraftBatch& a = p.a;
   if (smem_u32(smem) & 1023) {                      // the swizzled tiles need it
@@ -131,25 +176,26 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       mbar_init(&ctl->v_full[i], 1);
       mbar_init(&ctl->v_empty[i], 1);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], kSoftmax);
+      mbar_init(&ctl->p_full[i], kSoftmax / 2);
       mbar_init(&ctl->pv_done[i], 1);
+    }
+    for (int i = 0; i < 3; ++i)
       for (int k = 0; k <= kSpecial * 4; ++k) ctl->bad[i][k] = 0;
-    }
     mbar_init(&ctl->o_free, kSoftmax);
-    mbar_init(&ctl->mma_done, 1);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&ctl->pair[i][0], 2);
-      mbar_init(&ctl->pair[i][1], 2);
-    }
+    mbar_init(&ctl->s_end, 1);
+    mbar_init(&ctl->pv_end, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl->pair[i], 2);
     ctl->abort = 0;
     fence_mbar_init();
     fence_async_shared();
   }
-  if (threadIdx.x == 9 * 32) prefetch_tmap(&kmap);
+  if (threadIdx.x == 9 * 32) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+  }
   if (threadIdx.x == 10 * 32) prefetch_tmap(&vmap);
-  if (threadIdx.x == 11 * 32) prefetch_tmap(&qmap);
   if (warp == 8) tmem_alloc(&ctl->tmem_base, kTmemCols);
   pdl_wait();
   pdl_trigger();
@@ -161,28 +207,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
   w.init(a, ctl->plan, kKeys, kE, p.whole);
   const int tile_tokens = a.tokens / R;             // of a row tile
 
-  if (warp == 11) {
-    // ---- queries, item by item ------------------------------------------------
-    if (lane == 0) {
-      uint32_t segs = 0;
-      while (w.next(a, kKeys, kE)) {
-        const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
-        const int slot = segs % C::kQBufs, tiles = it.ni > tile_tokens ? R : 1;
-        if (!mbar_wait(&ctl->q_empty[slot], ((segs / C::kQBufs) & 1) ^ 1, abort, a.status)) break;
-        const uint32_t rows = tile_tokens * a.heads;
-        mbar_arrive_expect_tx(&ctl->q_full[slot], tiles * (D / 64) * rows * 128);
-        for (int r = 0; r < tiles; ++r)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sq + slot * C::kQ + r * C::kTile + h * C::kHalf, &qmap, &ctl->q_full[slot], h * 64,
-                        it.kvh * a.G, w.seq.first + it.i0 + r * tile_tokens);
-        ++segs;
-      }
-      // no copy may land after the CTA is gone
-      for (uint32_t i = segs > C::kQBufs ? segs - C::kQBufs : 0; i < segs; ++i)
-        mbar_wait(&ctl->q_full[i % C::kQBufs], (i / C::kQBufs) & 1, nullptr, a.status);
-    }
-  } else if (warp == 9 || warp == 10) {
-    // ---- keys (warp 9) and values (10): a lane to each box of a tile -----------------
+  if (warp == 9 || warp == 10) {
+    // ---- queries and keys (warp 9), values (10): a lane to each box of a tile ----------
     const bool vals = warp == 10;
     const CUtensorMap* map = vals ? &vmap : &kmap;
     uint64_t* full = vals ? ctl->v_full : ctl->k_full;
@@ -192,7 +218,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     const int boxes = kKeys / p.box, rb = lane % boxes, half = lane / boxes;
     const bool mine = half < D / 64;
     const uint32_t dst = half * C::kHalf + rb * p.box * 128, ps = a.page_size;
-    uint32_t n = 0;                                 // tiles fetched
+    uint32_t n = 0, segs = 0;                       // tiles and queries fetched
     bool ok = true;
     while (ok && w.next(a, kKeys, kE)) {
       const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
@@ -203,6 +229,19 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         return mine && t < w.t1 && x < (uint32_t)w.seq.len ? row[x / ps] : -1;
       };
       int next = page_of(w.t0);
+      if (!vals) {
+        const int slot = segs % C::kQBufs, tiles = it.ni > tile_tokens ? R : 1;
+        ok = wait(&ctl->q_empty[slot], ((segs / C::kQBufs) & 1) ^ 1, abort, a.status);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl->q_full[slot], tiles * (D / 64) * tile_tokens * a.heads * 128);
+          for (int r = 0; r < tiles; ++r)
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sq + slot * C::kQ + r * C::kTile + h * C::kHalf, &qmap, &ctl->q_full[slot], h * 64,
+                          it.kvh * a.G, w.seq.first + it.i0 + r * tile_tokens);
+        }
+        ++segs;
+      }
       for (int64_t t = w.t0; t < w.t1; ++t, ++n) {
         const uint32_t x = (uint32_t)t * kKeys + rb * p.box;
         const bool now = mine && x < (uint32_t)w.seq.len;
@@ -214,7 +253,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           z = a.n_pages * a.Hkv;                    // outside the map: reads as zeros
         }
         const int st = n % S;
-        ok = mbar_wait_warp(&empty[st], ((n / S) & 1) ^ 1, abort, a.status);
+        ok = wait(&empty[st], ((n / S) & 1) ^ 1, abort, a.status);
         if (!ok) break;
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, now));
         if (lane == 0) mbar_arrive_expect_tx(&full[st], count * p.box * 128);
@@ -222,141 +261,137 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (now) tma_load_3d(ring + st * C::kTile + dst, map, &full[st], half * 64, (int)(x % ps), z);
       }
     }
-    if (lane == 0)
+    // no copy may land after the CTA is gone
+    if (lane == 0) {
       for (uint32_t i = n > (uint32_t)S ? n - S : 0; i < n; ++i)
         mbar_wait(&full[i % S], (i / S) & 1, nullptr, a.status);
+      for (uint32_t i = segs > C::kQBufs ? segs - C::kQBufs : 0; i < segs; ++i)
+        mbar_wait(&ctl->q_full[i % C::kQBufs], (i / C::kQBufs) & 1, nullptr, a.status);
+    }
   } else if (warp == 8) {
-    // ---- products --------------------------------------------------------------------
-    // S of a step is issued kBufs - 1 steps before its P V.
-    struct Pending {
-      uint32_t s, tile;
-      int r, parts;                                 // row tile; 16-key parts
-      bool first, last;                             // of the segment's tiles; of the tile's row tiles
-    };
-    const uint32_t id_s = idesc_bf16_f32(128, kKeys);
-    const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);   // V MN-major
-    const uint32_t qb = smem_u32(sq), kb = smem_u32(sk), vb = smem_u32(sv);
-    const bool leader = elect_one();
-    constexpr int kAhead = NB - 1;
-    Pending ring[kAhead];
-    uint32_t s = 0, done = 0, tile = 0, segs = 0, seg_done = 0;
-    bool ok = true;
-    auto pv = [&](const Pending& x) {
-      const int buf = x.s % NB, st = x.tile % C::kV;
-      if (x.r == 0 && !mbar_wait_warp(&ctl->v_full[st], (x.tile / C::kV) & 1, abort, a.status)) return false;
-      if (!mbar_wait_warp(&ctl->p_full[buf], (x.s / NB) & 1, abort, a.status)) return false;
-      if (x.first && x.r == 0) {                    // the output of the segment before has been read
-        if (seg_done > 0 && !mbar_wait_warp(&ctl->o_free, (seg_done - 1) & 1, abort, a.status)) return false;
-        ++seg_done;
-      }
-      tc_fence_after();
-      if (leader) {
-        const uint32_t v0 = vb + st * C::kTile, d = tmem + C::kColO + x.r * D, pc = tmem + buf * 128;
-        for (int k = 0; k < x.parts; ++k) {
-          const uint64_t vd = sdesc_mn(v0 + k * 2048, C::kHalf);
-          const uint32_t at = pc + (k >> 2) * 64 + (k & 3) * 8;
-          mma_bf16_ts(d, at, vd, id_o, !x.first || k > 0);
-          mma_bf16_ts(d, at + 32, vd, id_o, 1u);
-        }
-        mma_commit(&ctl->pv_done[buf]);
-        if (x.last) mma_commit(&ctl->v_empty[st]);
-      }
-      __syncwarp();
-      return true;
-    };
-    while (ok && w.next(a, kKeys, kE)) {
-      const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
-      const int slot = segs % C::kQBufs, tiles = it.ni > tile_tokens ? R : 1;
-      if (C::kQBufs == 1)                           // the queries' copy waits for nothing but S: do not hold up P V
-        for (; ok && done < s; ++done) ok = pv(ring[done % kAhead]);
-      ok = ok && mbar_wait_warp(&ctl->q_full[slot], (segs / C::kQBufs) & 1, abort, a.status);
-      for (int64_t t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        const int st = tile % C::kK;
-        ok = mbar_wait_warp(&ctl->k_full[st], (tile / C::kK) & 1, abort, a.status);
-        const int parts = (int)(min64(kKeys, w.seq.len - t * kKeys) + 15) / 16;
-        for (int r = 0; ok && r < tiles; ++r, ++s) {
-          const int buf = s % NB;
-          if (s >= NB) ok = mbar_wait_warp(&ctl->pv_done[buf], ((s / NB) - 1) & 1, abort, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint32_t q0 = qb + slot * C::kQ + r * C::kTile, k0 = kb + st * C::kTile;
+    // ---- S = Q K^T: step s of the CTA is stream s & 1's ------------------------------------
+    if (elect_one()) {
+      const uint32_t id_s = idesc_bf16_f32(128, kKeys);
+      const uint64_t q_desc = sdesc_k128(smem_u32(sq)), k_desc = sdesc_k128(smem_u32(sk));
+      uint32_t s = 0, st = 0, ph = 0, segs = 0;
+      bool ok = true;
+      while (ok && w.next(a, kKeys, kE)) {
+        const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+        const int slot = segs % C::kQBufs, tiles = it.ni > tile_tokens ? R : 1;
+        ok = wait_one(&ctl->q_full[slot], (segs / C::kQBufs) & 1, abort, a.status);
+        for (int t = (int)(w.t1 - w.t0); ok && t > 0; --t) {
+          ok = wait_one(&ctl->k_full[st], ph, abort, a.status);
+          const uint64_t k0 = k_desc + st * (C::kTile >> 4);
+          uint64_t q0 = q_desc + slot * (C::kQ >> 4);
+          for (int r = tiles; ok && r > 0; --r, ++s, q0 += C::kTile >> 4) {
+            const uint32_t g = s & 1;
+            if (s >= 2 && !(ok = wait_one(&ctl->pv_done[g], ((s >> 1) - 1) & 1, abort, a.status))) break;
+            tc_fence_after();
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
-              mma_bf16(tmem + buf * 128, sdesc_k128(q0 + off), sdesc_k128(k0 + off), id_s, k > 0);
+              const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+              mma_bf16(tmem + g * kKeys, q0 + off, k0 + off, id_s, k > 0);
             }
-            mma_commit(&ctl->s_full[buf]);
-            if (r == tiles - 1) {
-              mma_commit(&ctl->k_empty[st]);
-              if (t == w.t1 - 1) mma_commit(&ctl->q_empty[slot]);
-            }
+            mma_commit(&ctl->s_full[g]);
           }
-          __syncwarp();
-          if (s - done == (uint32_t)kAhead) {
-            ok = pv(ring[done % kAhead]);
-            ++done;
-            if (!ok) break;
-          }
-          ring[s % kAhead] = {s, tile, r, parts, t == w.t0, r == tiles - 1};
+          if (!ok) break;
+          mma_commit(&ctl->k_empty[st]);
+          if (t == 1) mma_commit(&ctl->q_empty[slot]);
+          if (++st == C::kK) st = 0, ph ^= 1;
         }
+        ++segs;
       }
-      ++segs;
+      mma_commit(&ctl->s_end);
+      mbar_wait(&ctl->s_end, 0, nullptr, a.status);
     }
-    for (; ok && done < s; ++done) ok = pv(ring[done % kAhead]);
-    if (leader) mma_commit(&ctl->mma_done);
-    __syncwarp();
-    mbar_wait_warp(&ctl->mma_done, 0, nullptr, a.status);
+  } else if (warp == 11) {
+    // ---- O += P V ----------------------------------------------------------------------------
+    if (elect_one()) {
+      const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);   // V MN-major
+      const uint64_t v_desc = sdesc_mn(smem_u32(sv), C::kHalf);
+      uint32_t s = 0, st = 0, ph = 0, segs = 0;
+      bool ok = true;
+      while (ok && w.next(a, kKeys, kE)) {
+        const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+        const int tiles = it.ni > tile_tokens ? R : 1, tiles_k = (int)(w.t1 - w.t0);
+        for (int t = 0; ok && t < tiles_k; ++t) {
+          ok = wait_one(&ctl->v_full[st], ph, abort, a.status);
+          const uint64_t v0 = v_desc + st * (C::kTile >> 4);
+          for (int r = 0; ok && r < tiles; ++r, ++s) {
+            const uint32_t g = s & 1;
+            ok = wait_one(&ctl->p_full[g], (s >> 1) & 1, abort, a.status);
+            // the output of the segment before has been read
+            if (ok && t == 0 && r == 0 && segs > 0) ok = wait_one(&ctl->o_free, (segs - 1) & 1, abort, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + kColO + g * D, pc = tmem + g * kKeys, add = tiles == 1 ? t > 1 : t > 0;
+            const int left = w.seq.len - (int)(w.t0 + t) * kKeys;
+            if (left >= kKeys) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k) {
+                const uint32_t at = pc + (k >> 1) * 32 + (k & 1) * 8;
+                mma_bf16_ts(d, at, v0 + k * (2048 >> 4), id_o, k > 0 ? 1u : add);
+                mma_bf16_ts(d, at + 16, v0 + k * (2048 >> 4), id_o, 1u);
+              }
+            } else {
+              for (int k = 0; k * 16 < left; ++k) {
+                const uint32_t at = pc + (k >> 1) * 32 + (k & 1) * 8;
+                mma_bf16_ts(d, at, v0 + k * (2048 >> 4), id_o, k > 0 ? 1u : add);
+                mma_bf16_ts(d, at + 16, v0 + k * (2048 >> 4), id_o, 1u);
+              }
+            }
+            mma_commit(&ctl->pv_done[g]);
+          }
+          if (!ok) break;
+          mma_commit(&ctl->v_empty[st]);
+          if (++st == C::kV) st = 0, ph ^= 1;
+        }
+        ++segs;
+      }
+      mma_commit(&ctl->pv_end);
+      mbar_wait(&ctl->pv_end, 0, nullptr, a.status);
+    }
   } else {
     // ---- softmax --------------------------------------------------------------------------
-    const int quad = warp & 3, side = warp >> 2, row = quad * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int quad = warp & 3, g = warp >> 2, row = quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), s_at = lanes + g * kKeys;
     const DraftPartials part = draft_partials(p.workspace, gridDim.x, kPartRows);
+    const int tok = row / a.heads;                  // the row's token in its row tile
     int4 open = make_int4(-1, 0, 0, 0);
-    uint32_t s = 0, tile = 0, segs = 0, told = 0;
+    uint32_t s0 = 0, tile0 = 0, segs = 0, told = 0;                // steps and tiles before the segment
     bool ok = true;
-    // the other thread of the row tells its value for this one's
-    auto tell = [&](float mine, float& other) {
-      ctl->word[told & 1][side][row] = mine;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->pair[quad][told & 1]);
-      if (!mbar_wait_warp(&ctl->pair[quad][told & 1], (told >> 1) & 1, abort, a.status)) return false;
-      other = ctl->word[told & 1][side ^ 1][row];
-      ++told;
-      return true;
-    };
     while (ok && w.next(a, kKeys, kE)) {
       const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
-      const int tiles = it.ni > tile_tokens ? R : 1;
-      const int tok = row / a.heads, ctx = w.seq.len - w.seq.n;   // the row's token in its row tile
+      const int tiles = it.ni > tile_tokens ? R : 1, ctx = w.seq.len - w.seq.n;
+      const int e = g ^ (s0 & 1);                   // this stream's first step of the segment, and its row tile
+      const int i = it.i0 + (tiles == 1 ? 0 : e * tile_tokens) + tok;
+      const bool valid = tok < tile_tokens && i < it.i0 + it.ni;
+      const bool live = __any_sync(0xffffffffu, valid);
       unsigned int* bad = ctl->bad[segs % 3];
-      if (threadIdx.x == 0)                         // nobody is in the segment before the last any more
-        for (int k = 0; k <= kSpecial * 4; ++k) ctl->bad[(segs + 1) % 3][k] = 0;
-      float m[R], l[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-      }
-      for (int64_t t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        const int64_t x0 = t * kKeys + side * 64;
+      float m = -INFINITY, l = 0.f;
+      const int64_t step = tiles == 1 ? 2 : 1, t_first = w.t0 + (tiles == 1 ? e : 0);
+      uint32_t s = s0 + e;
+      for (int64_t t = t_first; t < w.t1; t += step, s += 2) {
         const bool special = t * kKeys + kKeys > ctx;
-        for (int r = 0; ok && r < tiles; ++r, ++s) {
-          const int buf = s % NB, i = it.i0 + r * tile_tokens + tok;
-          const bool valid = tok < tile_tokens && i < it.i0 + it.ni;
-          const bool live = __any_sync(0xffffffffu, valid);
-          ok = mbar_wait_warp(&ctl->s_full[buf], (s / NB) & 1, abort, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (live) {
-            const uint32_t s_at = lanes + buf * 128 + side * 64, o_at = lanes + C::kColO + r * D + side * (D / 2);
+        ok = wait(&ctl->s_full[g], (s >> 1) & 1, abort, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          uint64_t see[2] = {~0ull, ~0ull};
+          if (special) {
+            see[0] = valid ? draft_sees(a, w.seq, i, t * kKeys) : 0;
+            see[1] = valid ? draft_sees(a, w.seq, i, t * kKeys + 64) : 0;
+            __syncwarp();
+          }
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
             float x[64];
-            tmem_ld64_sync(s_at, x);
+            tmem_ld64_sync(s_at + 64 * h, x);
             if (special) {
-              const uint64_t see = valid ? draft_sees(a, w.seq, i, x0) : 0;
 #pragma unroll
               for (int c = 0; c < 64; ++c)
-                if (!(see >> c & 1)) x[c] = -INFINITY;
+                if (!((h ? see[1] : see[0]) >> c & 1)) x[c] = -INFINITY;
             }
             float pm[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -368,136 +403,137 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
             pm[0] = max3(pm[0], x[60], x[61]);
             pm[1] = max3(pm[1], x[62], x[63]);
-            float mx = valid ? fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) : -INFINITY, other;
-            ok = tell(mx, other);
-            if (!ok) break;
-            const float cand = fmaxf(mx, other) * p.scale_log2;
-            float mr = R == 1 || r == 0 ? m[0] : m[R - 1], lr = R == 1 || r == 0 ? l[0] : l[R - 1];
-            float corr = 1.f;
-            const bool move = cand > mr + 8.f;
-            if (move) {
-              corr = ex2_approx(mr - cand);         // 0 on the first tile
-              mr = cand;
-            }
-            if (t > w.t0 && __any_sync(0xffffffffu, move)) {
-              const uint32_t before = s - tiles;    // the step whose P V this row tile's output waits for
-              ok = mbar_wait_warp(&ctl->pv_done[before % NB], (before / NB) & 1, abort, a.status);
-              if (!ok) break;
-              tc_fence_after();
+            mx = max3(mx, max3(pm[0], pm[1], pm[2]), pm[3]);
+          }
+          const float cand = valid ? mx * p.scale_log2 : -INFINITY;
+          float corr = 1.f;
+          const bool move = cand > m + 8.f;
+          if (move) {
+            corr = ex2_approx(m - cand);            // 0 on the first tile
+            m = cand;
+          }
+          if (t > t_first && __any_sync(0xffffffffu, move)) {
+            // the stream's P V before this step has completed: S was issued after that
 #pragma unroll 1
-              for (int c = 0; c < D / 2; c += 32) {
-                float ov[32];
-                tmem_ld32_sync(o_at + c, ov);
+            for (int c = 0; c < D; c += 32) {
+              float ov[32];
+              tmem_ld32_sync(lanes + kColO + g * D + c, ov);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] *= corr;
-                tmem_st32(o_at + c, ov);
-              }
-              tmem_st_wait();
+              for (int y = 0; y < 32; ++y) ov[y] *= corr;
+              tmem_st32(lanes + kColO + g * D + c, ov);
             }
-            const float base = mr == -INFINITY ? 0.f : mr;
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t hi[32], lo[32];
+            tmem_st_wait();
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            float x[32];
+            uint32_t pw[32];                        // upper parts, then lower parts
+            tmem_ld32_sync(s_at + c0, x);
+            if (special) {
+              const uint32_t there = (uint32_t)((c0 < 64 ? see[0] : see[1]) >> (c0 & 32));
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              float e0, e1, c0, c1, r0, r1;
+              for (int c = 0; c < 32; ++c)
+                if (!(there >> c & 1)) x[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              float e0, e1, r0, r1;
               ffma2(x[c], x[c + 1], p.scale_log2, p.scale_log2, -base, -base, e0, e1);
               e0 = ex2_approx(e0);
               e1 = ex2_approx(e1);
               if ((c >> 1) & 1) fadd2(ps[2], ps[3], e0, e1, ps[2], ps[3]);
               else fadd2(ps[0], ps[1], e0, e1, ps[0], ps[1]);
-              constexpr float kBelow = 1.f - 1.f / 1024;
-              fmul2(e0, e1, kBelow, kBelow, c0, c1);
-              hi[c / 2] = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
-              ffma2(bf16lo(hi[c / 2]), bf16hi(hi[c / 2]), -1.f, -1.f, e0, e1, r0, r1);
-              lo[c / 2] = pack_bf16x2(r0, r1);
+              pw[c / 2] = __byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632);
+              constexpr float kAbove = 1.f + 1.f / (1 << 20);
+              ffma2(e0, e1, kAbove, kAbove, __uint_as_float((__float_as_uint(e0) & 0xffff0000u) ^ 0x80000000u),
+                    __uint_as_float((__float_as_uint(e1) & 0xffff0000u) ^ 0x80000000u), r0, r1);
+              pw[16 + c / 2] = pack_bf16x2(r0, r1);
             }
-            lr = lr * corr + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-            if (R == 1 || r == 0) m[0] = mr, l[0] = lr;
-            else m[R - 1] = mr, l[R - 1] = lr;
-            __syncwarp();
-            tmem_st32(s_at, reinterpret_cast<const float*>(hi));
-            tmem_st32(s_at + 32, reinterpret_cast<const float*>(lo));
-            tmem_st_wait();
+            tmem_st32(s_at + c0, reinterpret_cast<const float*>(pw));
           }
-          if (special && r == 0) {
-            // V as the product may read it
-            const int st = tile % C::kV;
-            ok = mbar_wait_warp(&ctl->v_full[st], (tile / C::kV) & 1, abort, a.status);
-            if (!ok) break;
-            const int left = (int)min64(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
-            uint8_t* v0 = sv + st * C::kTile;
-            for (int e = threadIdx.x; e < end * (D / 8); e += kSoftmax * 32) {
-              const int key = e / (D / 8), c = e % (D / 8);
-              uint8_t* at = v0 + (c >> 3) * C::kHalf + key * 128 + (c & 7) * 16;
-              if (key >= left) {
-                *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-              } else if (draft::clear_bad<bf16>(at)) {
-                const int k = (int)(t - ctx / kKeys) * kKeys + key;
-                atomicOr(&bad[k >> 5], 1u << (k & 31));
-                bad[kSpecial * 4] = 1;
-              }
-            }
-            fence_async_shared();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->p_full[buf]);
+          l = l * corr + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          tmem_st_wait();
         }
+        if (special && (tiles == 1 || e == 0)) {
+          // V as the product may read it
+          const uint32_t tile = tile0 + (uint32_t)(t - w.t0);
+          const int st = tile % C::kV;
+          ok = wait(&ctl->v_full[st], (tile / C::kV) & 1, abort, a.status);
+          if (!ok) break;
+          const int left = (int)min64(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
+          uint8_t* v0 = sv + st * C::kTile;
+          for (int e = threadIdx.x & 127; e < end * (D / 8); e += 128) {
+            const int key = e / (D / 8), c = e % (D / 8);
+            uint8_t* at = v0 + (c >> 3) * C::kHalf + key * 128 + (c & 7) * 16;
+            if (key >= left) {
+              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+            } else if (draft::clear_bad<bf16>(at)) {
+              const int k = (int)(t - ctx / kKeys) * kKeys + key;
+              atomicOr(&bad[k >> 5], 1u << (k & 31));
+              bad[kSpecial * 4] = 1;
+            }
+          }
+          fence_async_shared();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[g]);
       }
       if (!ok) break;
       // ---- the segment's output: complete with its last P V
-      const uint32_t last = s - 1;
-      ok = mbar_wait_warp(&ctl->pv_done[last % NB], (last / NB) & 1, abort, a.status);
+      const uint32_t steps = (uint32_t)(w.t1 - w.t0) * tiles, mine = s - 2, other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
+      const bool some = t_first < w.t1, join = tiles == 1 && (steps > 1 || !some);
+      // its own last P V first: the other stream's then has no phase but its last to wait for
+      if (some) ok = wait(&ctl->pv_done[g], (mine >> 1) & 1, abort, a.status);
+      if (ok && join) ok = wait(&ctl->pv_done[g ^ 1], (other >> 1) & 1, abort, a.status);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = w.begins && w.ends, odd = bad[kSpecial * 4] != 0;
-      const int64_t pslot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
-#pragma unroll 1
-      for (int r = 0; ok && r < tiles; ++r) {
-        const int i = it.i0 + r * tile_tokens + tok, h = it.kvh * a.G + row % a.heads;
-        const bool valid = tok < tile_tokens && i < it.i0 + it.ni;
-        if (!__any_sync(0xffffffffu, valid)) continue;
-        const float mr = R == 1 || r == 0 ? m[0] : m[R - 1], lr = R == 1 || r == 0 ? l[0] : l[R - 1];
-        float lo;
-        ok = tell(lr, lo);
-        if (!ok) break;
-        const float ll = side ? lo + lr : lr + lo;
+      if (live) {
+        float f = 1.f, f_other = 0.f;               // of this stream's sums, and of the other's
+        if (tiles == 1) {
+          ctl->word[g][row] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->pair[quad]);
+          ok = wait(&ctl->pair[quad], told & 1, abort, a.status);
+          if (!ok) break;
+          ++told;
+          const float2 o = ctl->word[g ^ 1][row];
+          const float mm = fmaxf(m, o.x), base = mm == -INFINITY ? 0.f : mm;
+          f = ex2_approx(m - base);
+          f_other = ex2_approx(o.x - base);
+          const float own = l * f, others = o.y * f_other;
+          l = own + others;
+          m = mm;
+        }
+        const bool whole = w.begins && w.ends, odd = bad[kSpecial * 4] != 0;
+        const int h = it.kvh * a.G + row % a.heads;
         const int64_t tt = (int64_t)w.seq.first + i;
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0)) * kPartRows + (i - it.i0) * a.heads + row % a.heads;
         const bool any = valid && draft_sees_any(a, w.seq, i);
-        const float inv = any ? 1.f / ll : 0.f;
+        const float inv = any ? 1.f / l : 0.f;
+        // with one row tile the streams' threads of a row share its columns
+        const int c_lo = tiles == 1 ? e * (D / 2) : 0, c_hi = tiles == 1 ? c_lo + D / 2 : D;
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
+        for (int c = c_lo; c < c_hi; c += 32) {
           float ov[32];
           __syncwarp();
-          tmem_ld32_sync(lanes + C::kColO + r * D + side * (D / 2) + c, ov);
-          if (valid && odd) {
-            for (int64_t t = max64(w.t0, ctx / kKeys); t < w.t1; ++t)
-              for (int k = 0; k < 4; ++k) {
-                const unsigned int there = bad[(int)(t - ctx / kKeys) * 4 + k];
-                if (!there) continue;
-                const int64_t x0 = t * kKeys + k * 32;
-                unsigned int todo = there & (unsigned int)draft_sees(a, w.seq, i, x0);
-                for (; todo; todo &= todo - 1) {
-                  const int64_t x = x0 + __ffs(todo) - 1;
-                  const int pg = (int)(x / a.page_size), id = a.table[(int64_t)w.seg_b * a.max_pages + pg];
-                  const uint4* vr = reinterpret_cast<const uint4*>(
-                      p.v + ((((int64_t)id * a.Hkv + it.kvh) * a.page_size + (x - (int64_t)pg * a.page_size)) * D +
-                             side * (D / 2) + c) * 2);
+          if (some) {
+            tmem_ld32_sync(lanes + kColO + g * D + c, ov);
+          } else {
 #pragma unroll
-                  for (int u = 0; u < 4; ++u) {
-                    const uint4 q = vr[u];
-                    const uint32_t z[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                      ov[8 * u + 2 * y] += draft::if_bad(bf16lo(z[y]));
-                      ov[8 * u + 2 * y + 1] += draft::if_bad(bf16hi(z[y]));
-                    }
-                  }
-                }
-              }
+            for (int y = 0; y < 32; ++y) ov[y] = 0.f;
           }
+          if (join) {
+            float x[32];
+            tmem_ld32_sync(lanes + kColO + (g ^ 1) * D + c, x);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) ov[y] = ov[y] * f + x[y] * f_other;
+          }
+          if (valid && odd) add_bad(a, w, it, i, bad, p.v, c, D, ov);
           if (valid && whole) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<bf16*>(p.o) + (tt * a.H + h) * D + side * (D / 2) + c);
+            uint4* to = reinterpret_cast<uint4*>(static_cast<bf16*>(p.o) + (tt * a.H + h) * D + c);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint4 x;
@@ -508,21 +544,25 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
               to[u] = any ? x : make_uint4(0, 0, 0, 0);
             }
           } else if (valid) {
-            const int64_t slot = pslot * kPartRows + r * tile_tokens * a.heads + row;
-            float4* to = reinterpret_cast<float4*>(part.o + slot * D + side * (D / 2) + c);
+            float4* to = reinterpret_cast<float4*>(part.o + slot * D + c);
 #pragma unroll
             for (int u = 0; u < 8; ++u) to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
-            if (side == 0 && c == 0) *reinterpret_cast<float2*>(part.ml + slot * 2) = make_float2(mr, ll);
           }
         }
-        if (whole && valid && side == 0 && p.lse) p.lse[(int64_t)h * a.T + tt] = draft::row_lse(mr, ll, any);
+        if (valid && (tiles != 1 || e == 0)) {
+          if (!whole) *reinterpret_cast<float2*>(part.ml + slot * 2) = make_float2(m, l);
+          else if (p.lse) p.lse[(int64_t)h * a.T + tt] = draft::row_lse(m, l, any);
+        }
       }
-      if (!ok) break;
+      if (threadIdx.x == 0)                         // of the segment before, which nobody is in any more
+        for (int k = 0; k <= kSpecial * 4; ++k) ctl->bad[(segs + 2) % 3][k] = 0;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free);
       if (w.begins && !w.ends)
         open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(ctl->plan, kE, blockIdx.x, gridDim.x));
+      s0 += steps;
+      tile0 += (uint32_t)(w.t1 - w.t0);
       ++segs;
     }
     if (threadIdx.x == 0) part.open[blockIdx.x] = open;
