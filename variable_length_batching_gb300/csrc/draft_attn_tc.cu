@@ -67,7 +67,7 @@ constexpr int kMaxStages = 7, kSpecial = 3;         // tiles behind the context,
 struct Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free, s_end, pv_end;  // [2]: of a stream
+  uint64_t s_full[2], p_full[2][2], pv_done[2], o_free, s_end, pv_end;   // of a stream; P: of each half of its keys
   uint64_t pair[4];                                 // two warps of the same rows
   uint32_t tmem_base;
   int abort;
@@ -178,7 +178,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], kSoftmax / 2);
+      mbar_init(&ctl->p_full[i][0], kSoftmax / 2);
+      mbar_init(&ctl->p_full[i][1], kSoftmax / 2);
       mbar_init(&ctl->pv_done[i], 1);
     }
     for (int i = 0; i < 3; ++i)
@@ -319,26 +320,32 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           const uint64_t v0 = v_desc + st * (C::kTile >> 4);
           for (int r = 0; ok && r < tiles; ++r, ++s) {
             const uint32_t g = s & 1;
-            ok = wait_one(&ctl->p_full[g], (s >> 1) & 1, abort, a.status);
+            ok = wait_one(&ctl->p_full[g][0], (s >> 1) & 1, abort, a.status);
             // the output of the segment before has been read
             if (ok && t == 0 && r == 0 && segs > 0) ok = wait_one(&ctl->o_free, (segs - 1) & 1, abort, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + kColO + g * D, pc = tmem + g * kKeys, add = tiles == 1 ? t > 1 : t > 0;
             const int left = w.seq.len - (int)(w.t0 + t) * kKeys;
+            auto part = [&](int k) {                // 16 keys
+              const uint32_t at = pc + (k >> 1) * 32 + (k & 1) * 8;
+              mma_bf16_ts(d, at, v0 + k * (2048 >> 4), id_o, k > 0 ? 1u : add);
+              mma_bf16_ts(d, at + 16, v0 + k * (2048 >> 4), id_o, 1u);
+            };
             if (left >= kKeys) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k) {
-                const uint32_t at = pc + (k >> 1) * 32 + (k & 1) * 8;
-                mma_bf16_ts(d, at, v0 + k * (2048 >> 4), id_o, k > 0 ? 1u : add);
-                mma_bf16_ts(d, at + 16, v0 + k * (2048 >> 4), id_o, 1u);
-              }
+              for (int k = 0; k < kKeys / 32; ++k) part(k);
             } else {
-              for (int k = 0; k * 16 < left; ++k) {
-                const uint32_t at = pc + (k >> 1) * 32 + (k & 1) * 8;
-                mma_bf16_ts(d, at, v0 + k * (2048 >> 4), id_o, k > 0 ? 1u : add);
-                mma_bf16_ts(d, at + 16, v0 + k * (2048 >> 4), id_o, 1u);
-              }
+              for (int k = 0; k < kKeys / 32 && k * 16 < left; ++k) part(k);
+            }
+            ok = wait_one(&ctl->p_full[g][1], (s >> 1) & 1, abort, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (left >= kKeys) {
+#pragma unroll
+              for (int k = kKeys / 32; k < kKeys / 16; ++k) part(k);
+            } else {
+              for (int k = kKeys / 32; k * 16 < left; ++k) part(k);
             }
             mma_commit(&ctl->pv_done[g]);
           }
@@ -369,9 +376,9 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       const bool live = __any_sync(0xffffffffu, valid);
       unsigned int* bad = ctl->bad[segs % 3];
       float m = -INFINITY, l = 0.f;
-      const int64_t step = tiles == 1 ? 2 : 1, t_first = w.t0 + (tiles == 1 ? e : 0);
+      const int t_lo = (int)w.t0, t_hi = (int)w.t1, step = tiles == 1 ? 2 : 1, t_first = t_lo + (tiles == 1 ? e : 0);
       uint32_t s = s0 + e;
-      for (int64_t t = t_first; t < w.t1; t += step, s += 2) {
+      for (int t = t_first; t < t_hi; t += step, s += 2) {
         const bool special = t * kKeys + kKeys > ctx;
         ok = wait(&ctl->s_full[g], (s >> 1) & 1, abort, a.status);
         if (!ok) break;
@@ -452,17 +459,23 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
               pw[16 + c / 2] = pack_bf16x2(r0, r1);
             }
             tmem_st32(s_at + c0, reinterpret_cast<const float*>(pw));
+            if (c0 == 32 && !special) {             // the product of these may begin
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl->p_full[g][0]);
+            }
           }
           l = l * corr + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
           tmem_st_wait();
         }
         if (special && (tiles == 1 || e == 0)) {
           // V as the product may read it
-          const uint32_t tile = tile0 + (uint32_t)(t - w.t0);
+          const uint32_t tile = tile0 + (uint32_t)(t - t_lo);
           const int st = tile % C::kV;
           ok = wait(&ctl->v_full[st], (tile / C::kV) & 1, abort, a.status);
           if (!ok) break;
-          const int left = (int)min64(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
+          const int left = min(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
           uint8_t* v0 = sv + st * C::kTile;
           for (int e = threadIdx.x & 127; e < end * (D / 8); e += 128) {
             const int key = e / (D / 8), c = e % (D / 8);
@@ -470,7 +483,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             if (key >= left) {
               *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
             } else if (draft::clear_bad<bf16>(at)) {
-              const int k = (int)(t - ctx / kKeys) * kKeys + key;
+              const int k = (t - ctx / kKeys) * kKeys + key;
               atomicOr(&bad[k >> 5], 1u << (k & 31));
               bad[kSpecial * 4] = 1;
             }
@@ -479,12 +492,15 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[g]);
+        if (lane == 0) {
+          if (special || !live) mbar_arrive(&ctl->p_full[g][0]);
+          mbar_arrive(&ctl->p_full[g][1]);
+        }
       }
       if (!ok) break;
       // ---- the segment's output: complete with its last P V
-      const uint32_t steps = (uint32_t)(w.t1 - w.t0) * tiles, mine = s - 2, other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
-      const bool some = t_first < w.t1, join = tiles == 1 && (steps > 1 || !some);
+      const uint32_t steps = (uint32_t)(t_hi - t_lo) * tiles, mine = s - 2, other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
+      const bool some = t_first < t_hi, join = tiles == 1 && (steps > 1 || !some);
       // its own last P V first: the other stream's then has no phase but its last to wait for
       if (some) ok = wait(&ctl->pv_done[g], (mine >> 1) & 1, abort, a.status);
       if (ok && join) ok = wait(&ctl->pv_done[g ^ 1], (other >> 1) & 1, abort, a.status);
@@ -562,7 +578,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       if (w.begins && !w.ends)
         open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(ctl->plan, kE, blockIdx.x, gridDim.x));
       s0 += steps;
-      tile0 += (uint32_t)(w.t1 - w.t0);
+      tile0 += (uint32_t)(t_hi - t_lo);
       ++segs;
     }
     if (threadIdx.x == 0) part.open[blockIdx.x] = open;
