@@ -123,7 +123,10 @@ cudaError_t launch_draft_join(nt_dtype dt, const DraftBatch& a, int d, int ctas,
 }
 
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
-  return draft_tc_supported(dt, p) ? launch_draft_tc(p, status, s) : launch_draft_rows(dt, p, status, s);
+  const int64_t rows = (int64_t)p.max_new * (p.H / p.pool.H);
+  const bool tc = draft_tc_supported(dt, p);
+  if (draft_slices_supported(dt, p) && (rows <= 64 || !tc)) return launch_draft_slices(p, status, s);
+  return tc ? launch_draft_tc(p, status, s) : launch_draft_rows(dt, p, status, s);
 }
 
 }  // namespace nt

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__((Cfg<T, D>::kThreads)) draft_rows_kernel(const
   W me(smem + 4 * C::kSide);
 
   while (w.next(a, kKeys, 1)) {
-    const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+    const DraftItem& it = w.it;
     auto rows_of = [&](int64_t t) {                // offsets of tile t's rows
       if (tid < kKeys) {
         const int64_t x = t * kKeys + tid;

@@ -222,7 +222,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint32_t n = 0, segs = 0;                       // tiles and queries fetched
     bool ok = true;
     while (ok && w.next(a, kKeys, kE)) {
-      const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+      const DraftItem& it = w.it;
       const int32_t* row = a.table + (int64_t)w.seg_b * a.max_pages;
       // the table is read a tile ahead
       auto page_of = [&](int64_t t) {
@@ -277,7 +277,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       uint32_t s = 0, st = 0, ph = 0, segs = 0;
       bool ok = true;
       while (ok && w.next(a, kKeys, kE)) {
-        const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+        const DraftItem& it = w.it;
         const int slot = segs % C::kQBufs, tiles = it.ni > tile_tokens ? R : 1;
         ok = wait_one(&ctl->q_full[slot], (segs / C::kQBufs) & 1, abort, a.status);
         for (int t = (int)(w.t1 - w.t0); ok && t > 0; --t) {
@@ -313,7 +313,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       uint32_t s = 0, st = 0, ph = 0, segs = 0;
       bool ok = true;
       while (ok && w.next(a, kKeys, kE)) {
-        const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+        const DraftItem& it = w.it;
         const int tiles = it.ni > tile_tokens ? R : 1, tiles_k = (int)(w.t1 - w.t0);
         for (int t = 0; ok && t < tiles_k; ++t) {
           ok = wait_one(&ctl->v_full[st], ph, abort, a.status);
@@ -368,7 +368,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint32_t s0 = 0, tile0 = 0, segs = 0, told = 0;                // steps and tiles before the segment
     bool ok = true;
     while (ok && w.next(a, kKeys, kE)) {
-      const DraftItem it = draft_item(a, w.seq.n, w.seg_item, w.seg_items);
+      const DraftItem& it = w.it;
       const int tiles = it.ni > tile_tokens ? R : 1, ctx = w.seq.len - w.seq.n;
       const int e = g ^ (s0 & 1);                   // this stream's first step of the segment, and its row tile
       const int i = it.i0 + (tiles == 1 ? 0 : e * tile_tokens) + tok;
@@ -376,6 +376,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       const bool live = __any_sync(0xffffffffu, valid);
       unsigned int* bad = ctl->bad[segs % 3];
       float m = -INFINITY, l = 0.f;
+      DraftMask mask;
+      mask.read(a, w.seq, i, valid);
       const int t_lo = (int)w.t0, t_hi = (int)w.t1, step = tiles == 1 ? 2 : 1, t_first = t_lo + (tiles == 1 ? e : 0);
       uint32_t s = s0 + e;
       for (int t = t_first; t < t_hi; t += step, s += 2) {
@@ -386,8 +388,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (live) {
           uint64_t see[2] = {~0ull, ~0ull};
           if (special) {
-            see[0] = valid ? draft_sees(a, w.seq, i, t * kKeys) : 0;
-            see[1] = valid ? draft_sees(a, w.seq, i, t * kKeys + 64) : 0;
+            see[0] = valid ? mask.sees(a, w.seq, i, t * kKeys) : 0;
+            see[1] = valid ? mask.sees(a, w.seq, i, t * kKeys + 64) : 0;
             __syncwarp();
           }
           float mx = -INFINITY;
@@ -477,8 +479,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           if (!ok) break;
           const int left = min(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
           uint8_t* v0 = sv + st * C::kTile;
-          for (int e = threadIdx.x & 127; e < end * (D / 8); e += 128) {
-            const int key = e / (D / 8), c = e % (D / 8);
+          for (int y = max(0, ctx - t * kKeys) * (D / 8) + (threadIdx.x & 127); y < end * (D / 8); y += 128) {
+            const int key = y / (D / 8), c = y % (D / 8);
             uint8_t* at = v0 + (c >> 3) * C::kHalf + key * 128 + (c & 7) * 16;
             if (key >= left) {
               *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
@@ -500,15 +502,16 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       if (!ok) break;
       // ---- the segment's output: complete with its last P V
       const uint32_t steps = (uint32_t)(t_hi - t_lo) * tiles, mine = s - 2, other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
-      const bool some = t_first < t_hi, join = tiles == 1 && (steps > 1 || !some);
+      const bool some = t_first < t_hi, join = tiles == 1 && steps > 1;
       // its own last P V first: the other stream's then has no phase but its last to wait for
+      // (a stream without a step has nothing to do, so that items of one tile follow each other in turns)
       if (some) ok = wait(&ctl->pv_done[g], (mine >> 1) & 1, abort, a.status);
       if (ok && join) ok = wait(&ctl->pv_done[g ^ 1], (other >> 1) & 1, abort, a.status);
       if (!ok) break;
       tc_fence_after();
-      if (live) {
+      if (live && some) {
         float f = 1.f, f_other = 0.f;               // of this stream's sums, and of the other's
-        if (tiles == 1) {
+        if (join) {
           ctl->word[g][row] = make_float2(m, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->pair[quad]);
@@ -524,23 +527,18 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           m = mm;
         }
         const bool whole = w.begins && w.ends, odd = bad[kSpecial * 4] != 0;
-        const int h = it.kvh * a.G + row % a.heads;
+        const int h = it.kvh * a.G + row - tok * a.heads;
         const int64_t tt = (int64_t)w.seq.first + i;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0)) * kPartRows + (i - it.i0) * a.heads + row % a.heads;
-        const bool any = valid && draft_sees_any(a, w.seq, i);
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0)) * kPartRows + (i - it.i0 - tok) * a.heads + row;
+        const bool any = valid && mask.sees_any(a, w.seq);
         const float inv = any ? 1.f / l : 0.f;
-        // with one row tile the streams' threads of a row share its columns
-        const int c_lo = tiles == 1 ? e * (D / 2) : 0, c_hi = tiles == 1 ? c_lo + D / 2 : D;
+        // joined, the streams' threads of a row share its columns
+        const int c_lo = join ? e * (D / 2) : 0, c_hi = join ? c_lo + D / 2 : D;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
           float ov[32];
           __syncwarp();
-          if (some) {
-            tmem_ld32_sync(lanes + kColO + g * D + c, ov);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) ov[y] = 0.f;
-          }
+          tmem_ld32_sync(lanes + kColO + g * D + c, ov);
           if (join) {
             float x[32];
             tmem_ld32_sync(lanes + kColO + (g ^ 1) * D + c, x);
@@ -565,7 +563,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             for (int u = 0; u < 8; ++u) to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
           }
         }
-        if (valid && (tiles != 1 || e == 0)) {
+        if (valid && (!join || e == 0)) {
           if (!whole) *reinterpret_cast<float2*>(part.ml + slot * 2) = make_float2(m, l);
           else if (p.lse) p.lse[(int64_t)h * a.T + tt] = draft::row_lse(m, l, any);
         }

@@ -35,16 +35,18 @@ struct DraftBatch {
 struct DraftSeq {
   int len, n, first;        // first: its first token in the packed batch
 };
-__device__ __forceinline__ DraftSeq draft_seq(const DraftBatch& a, int b, unsigned int* status) {
+__device__ __forceinline__ DraftSeq draft_seq(const DraftBatch& a, int first, int hi, int len, unsigned int* status) {
   DraftSeq s;
-  s.first = a.cu[b];
-  const int hi = a.cu[b + 1];
-  s.len = a.lengths[b];
-  const bool bad = s.first < 0 || hi < s.first || hi > a.T || (int64_t)hi - s.first > a.max_new ||
-                   s.len < hi - s.first || s.len > a.cap;
+  s.first = first;
+  s.len = len;
+  const bool bad = first < 0 || hi < first || hi > a.T || (int64_t)hi - first > a.max_new || len < hi - first ||
+                   len > a.cap;
   if (bad) flag_device(status, kDevCheck);
-  s.n = bad ? 0 : hi - s.first;
+  s.n = bad ? 0 : hi - first;
   return s;
+}
+__device__ __forceinline__ DraftSeq draft_seq(const DraftBatch& a, int b, unsigned int* status) {
+  return draft_seq(a, a.cu[b], a.cu[b + 1], a.lengths[b], status);
 }
 __device__ __forceinline__ int draft_items(const DraftBatch& a, int n) {
   return a.Hkv * a.hgroups * ((n + a.tokens - 1) / a.tokens);
@@ -99,61 +101,109 @@ __device__ __forceinline__ void draft_plan(const DraftBatch& a, int tile, int ex
   __syncthreads();
 }
 
+// What an item of a sequence is.
+struct DraftItem {
+  int kvh, h0, nh;          // key head; first of its query heads, and how many
+  int i0, ni;               // first token, and how many
+};
+__device__ __forceinline__ DraftItem draft_item(const DraftBatch& a, int n, int kvh, int hgroup, int group) {
+  DraftItem it;
+  it.kvh = kvh;
+  it.h0 = hgroup * a.heads;
+  it.nh = min(a.heads, a.G - it.h0);
+  it.i0 = group * a.tokens;
+  it.ni = min(a.tokens, n - it.i0);
+  return it;
+}
+__device__ __forceinline__ DraftItem draft_item(const DraftBatch& a, int n, int item, int items) {
+  const int groups = items / (a.Hkv * a.hgroups), head = item / groups, kvh = head / a.hgroups;
+  return draft_item(a, n, kvh, head - kvh * a.hgroups, item - head * groups);
+}
+
 // Walks a CTA's range segment by segment; as PagedWalk.
 struct DraftWalk {
   bool whole;
   int64_t left;           // units of the range not yet handed out
   int b, item, items;
   DraftSeq cur;
-  int64_t units;          // of an item of sequence b
-  int64_t unit;           // of the item, where the next segment starts
-  // the current segment: tiles [t0, t1) of item seg_item of sequence b's
+  int next_lo, next_hi, next_len;         // of sequence b + 1, loaded when b was reached
+  int units;              // of an item of sequence b
+  int unit;               // of the item, where the next segment starts
+  int kvh, hgroup, group, groups;         // of the item: key head, group of its query heads, group of tokens of how many
+  // the current segment: tiles [t0, t1) of item `it` (seg_item) of sequence seg_b
   DraftSeq seq;
+  DraftItem it;
   int seg_b, seg_item, seg_items;
-  int64_t t0, t1;
+  int t0, t1;
   bool begins, ends;
 
+  __device__ __forceinline__ void load_next(const DraftBatch& a) {
+    const bool there = b + 1 < a.B;
+    next_lo = there ? a.cu[b + 1] : 0;
+    next_hi = there ? a.cu[b + 2] : 0;
+    next_len = there ? a.lengths[b + 1] : 0;
+  }
+  __device__ __forceinline__ void sequence(const DraftBatch& a, int tile, int extra) {
+    groups = (cur.n + a.tokens - 1) / a.tokens;
+    items = a.Hkv * a.hgroups * groups;
+    units = (int)paged_tiles(cur.len, tile) + extra;
+  }
+  __device__ __forceinline__ void step_item(const DraftBatch& a) {
+    ++item;
+    if (++group == groups) {
+      group = 0;
+      if (++hgroup == a.hgroups) {
+        hgroup = 0;
+        ++kvh;
+      }
+    }
+  }
   __device__ __forceinline__ void init(const DraftBatch& a, const PagedPlan& s, int tile, int extra, bool whole_items) {
     whole = whole_items;
     left = s.hi - s.lo;
     if (left <= 0) return;
     b = s.b0;
     cur = draft_seq(a, b, nullptr);
-    items = draft_items(a, cur.n);
-    units = paged_tiles(cur.len, tile) + extra;
+    load_next(a);
+    sequence(a, tile, extra);
     const int64_t off = s.lo - s.start;
     item = (int)paged_div(off, units);
-    unit = off - item * units;
+    unit = (int)(off - (int64_t)item * units);
+    const int head = item / groups;
+    group = item - head * groups;
+    kvh = head / a.hgroups;
+    hgroup = head - kvh * a.hgroups;
     if (whole && unit > 0) {
       left -= units - unit;
       unit = 0;
-      ++item;
+      step_item(a);
     }
   }
   __device__ __forceinline__ bool next(const DraftBatch& a, int tile, int extra) {
     do {
       if (left <= 0) return false;
       if (item == items) {
-        item = 0;
         do {                              // the range holds a further unit, so a sequence with tokens follows
           if (++b >= a.B) return false;
-          cur = draft_seq(a, b, nullptr);
+          cur = draft_seq(a, next_lo, next_hi, next_len, nullptr);
+          load_next(a);
         } while (cur.n == 0);
-        items = draft_items(a, cur.n);
-        units = paged_tiles(cur.len, tile) + extra;
+        item = group = hgroup = kvh = 0;
+        sequence(a, tile, extra);
       }
-      const int64_t end = whole ? units : min64(units, unit + left);
+      const int end = whole ? units : (int)min64(units, unit + left);
       seg_b = b;
       seg_item = item;
       seg_items = items;
       seq = cur;
-      t0 = max64(0, unit - extra);
+      it = draft_item(a, cur.n, kvh, hgroup, group);
+      t0 = max(0, unit - extra);
       t1 = end - extra;
       begins = t0 == 0;
       ends = end == units;
       left -= end - unit;
       unit = 0;
-      ++item;
+      step_item(a);
     } while (t1 <= t0);                   // nothing but the item's extra units
     return true;
   }
@@ -163,23 +213,6 @@ struct DraftWalk {
     return (int)paged_div(e * n + s.total - 1, s.total) - cta;
   }
 };
-
-// What an item of a sequence is.
-struct DraftItem {
-  int kvh, h0, nh;          // key head; first of its query heads, and how many
-  int i0, ni;               // first token, and how many
-};
-__device__ __forceinline__ DraftItem draft_item(const DraftBatch& a, int n, int item, int items) {
-  const int groups = items / (a.Hkv * a.hgroups);
-  const int rest = item / groups;
-  DraftItem it;
-  it.i0 = (item - rest * groups) * a.tokens;
-  it.ni = min(a.tokens, n - it.i0);
-  it.kvh = rest / a.hgroups;
-  it.h0 = (rest - it.kvh * a.hgroups) * a.heads;
-  it.nh = min(a.heads, a.G - it.h0);
-  return it;
-}
 
 // The keys that new token i of a sequence sees among positions [x, x + 64), a
 // bit each.  x may lie behind the sequence's end.
@@ -200,6 +233,44 @@ __device__ __forceinline__ uint64_t draft_sees(const DraftBatch& a, const DraftS
   if (sh && k + 1 < a.words) m |= (uint64_t)w[k + 1] << (64 - sh);
   return there & m;
 }
+// The same from the token's mask words, read before.
+struct DraftMask {
+  uint64_t w[kDraftMaxNew / 64];
+  __device__ __forceinline__ void read(const DraftBatch& a, const DraftSeq& s, int i, bool there) {
+#pragma unroll
+    for (int k = 0; k < kDraftMaxNew / 64; ++k)
+      w[k] = there && a.bits && k < a.words ? (uint64_t)a.bits[((int64_t)s.first + i) * a.words + k] : 0;
+  }
+  __device__ __forceinline__ uint64_t sees(const DraftBatch& a, const DraftSeq& s, int i, int x) const {
+    const int left = s.len - x, j = x - (s.len - s.n);
+    if (left <= 0) return 0;
+    const uint64_t all = left < 64 ? (1ull << left) - 1 : ~0ull;
+    if (j <= -64) return all;
+    if (!a.bits) {
+      const int upto = i - j;
+      return upto < 0 ? 0 : upto >= 63 ? all : all & ((2ull << upto) - 1);
+    }
+    if (j < 0) return all & ((1ull << -j) - 1 | w[0] << -j);
+    const int k = j >> 6, sh = j & 63;
+    uint64_t m = 0;
+#pragma unroll
+    for (int y = 0; y < kDraftMaxNew / 64; ++y) {
+      if (y == k) m |= w[y] >> sh;
+      if (y == k + 1 && sh) m |= w[y] << (64 - sh);
+    }
+    return all & m;
+  }
+  __device__ __forceinline__ bool sees_any(const DraftBatch& a, const DraftSeq& s) const {
+    if (s.len > s.n || !a.bits) return true;
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < kDraftMaxNew / 64; ++k) {
+      const int n = s.n - 64 * k;
+      if (n > 0 && (w[k] & (n < 64 ? (1ull << n) - 1 : ~0ull))) any = true;
+    }
+    return any;
+  }
+};
 // Whether it sees any.
 __device__ __forceinline__ bool draft_sees_any(const DraftBatch& a, const DraftSeq& s, int i) {
   if (s.len > s.n || !a.bits) return true;

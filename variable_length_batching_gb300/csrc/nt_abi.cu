@@ -1346,16 +1346,17 @@ nt_status nt_selftest_paged_tree_attn(int32_t kernel, const nt_kv_pages* pages, 
                                       const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths,
                                       const int64_t* d_bits, float scale, void* o, float* lse, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-  if (kernel < 0 || kernel > 1) return fail(NT_ERR_INVALID, "kernel %d (0 or 1)", kernel);
+  if (kernel < 0 || kernel > 2) return fail(NT_ERR_INVALID, "kernel %d (0, 1 or 2)", kernel);
   DraftProblem p;
   const nt_status st = check_tree_attn(pages, q, q_stride, T, H, d_cu_seqlens, B, max_new, d_block_table, max_pages,
                                        d_lengths, d_bits, scale, o, lse, workspace, workspace_bytes, &p);
   if (st != NT_OK || T == 0 || max_new == 0) return st;
-  if (kernel == 1 && !draft_tc_supported(pages->dtype, p))
+  if ((kernel == 1 && !draft_tc_supported(pages->dtype, p)) || (kernel == 2 && !draft_slices_supported(pages->dtype, p)))
     return fail(NT_ERR_UNSUPPORTED, "kernel %d does not take this call", kernel);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = kernel ? launch_draft_tc(p, status_word(), s)
-                               : launch_draft_rows(pages->dtype, p, status_word(), s);
+  const cudaError_t e = kernel == 2   ? launch_draft_slices(p, status_word(), s)
+                        : kernel == 1 ? launch_draft_tc(p, status_word(), s)
+                                      : launch_draft_rows(pages->dtype, p, status_word(), s);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return NT_OK;
 }

@@ -482,6 +482,10 @@ cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* 
 // query heads to a key head.
 bool draft_tc_supported(nt_dtype dt, const DraftProblem& p);
 cudaError_t launch_draft_tc(const DraftProblem& p, unsigned int* status, cudaStream_t s);
+// bf16, pages of a multiple of 8 positions, few rows (64 of them read the keys
+// once).
+bool draft_slices_supported(nt_dtype dt, const DraftProblem& p);
+cudaError_t launch_draft_slices(const DraftProblem& p, unsigned int* status, cudaStream_t s);
 // Any page size, a CTA to 64 rows.
 cudaError_t launch_draft_rows(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
 

@@ -884,8 +884,8 @@ def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu
                                 block_table: torch.Tensor, lengths: torch.Tensor, max_new: int,
                                 bits: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                                 workspace: Optional[torch.Tensor] = None, stream=None):
-    """nt_paged_tree_attn by kernel 0 (the general one) or 1 (the tensor
-    cores'), for tests of each; contiguous tensors.  Returns (o, lse)."""
+    """nt_paged_tree_attn by kernel 0 (the general one), 1 (in tensor
+    memory) or 2 (few rows), for tests of each; contiguous tensors.  Returns (o, lse)."""
     T, H, d = q.shape
     B = cu_seqlens.numel() - 1
     if q.dtype != pages.dtype or any(t.dtype != torch.int32 for t in (cu_seqlens, block_table, lengths)):
