@@ -52,13 +52,13 @@ def call(nt, c, scale=None, want_lse=True, **kw):
     return o, lse
 
 
-def call_kernel(nt, c, kernel, scale=None):
+def call_kernel(nt, c, kernel, scale=None, cluster=0):
     """The same by a kernel by name; None where it does not take the call."""
     pages = nt.KVPages(c["kp"].to(DEV), c["vp"].to(DEV))
     bits = None if c["bits"] is None else c["bits"].to(DEV)
     try:
         got = nt.nt_selftest_paged_tree_attn(kernel, pages, c["q"].to(DEV), _cu(c["ns"]), c["table"].to(DEV),
-                                             _i32(c["lens"]), c["max_new"], bits=bits, scale=scale)
+                                             _i32(c["lens"]), c["max_new"], bits=bits, scale=scale, cluster=cluster)
     except nt.NTError as e:
         assert e.status == 2 and kernel
         return None
@@ -115,8 +115,9 @@ def test_tree_attn(nt, shape, dtype, kind):
     ctx, ns, page, H, Hk, d = SHAPES[shape]
     c = make_case(ctx, ns, page, H, Hk, d, dtype, kind, seed=shape)
     check(c, *call(nt, c))
-    takes = {0: True, 1: dtype == BF and d > 32 and page % 8 == 0 and H // Hk <= 128, 2: dtype == BF and page % 8 == 0}
-    for kernel in (0, 1, 2):
+    takes = {0: True, 1: dtype == BF and d > 32 and page % 8 == 0 and H // Hk <= 128, 2: dtype == BF and page % 8 == 0,
+             3: True}
+    for kernel in (0, 1, 2, 3):
         got = call_kernel(nt, c, kernel)
         assert (got is not None) == takes[kernel]
         if got:

@@ -140,6 +140,15 @@ T fresh(at::IntArrayRef sizes, at::ScalarType type, int index) {
   return T(at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)),
                                   std::nullopt));
 }
+// n elements of another type over a part of a tensor's memory.
+T part(const T& all, int64_t at, int64_t n, at::ScalarType type) {
+  T t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                 c10::scalarTypeToTypeMeta(type));
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(at / (int64_t)c10::elementSize(type));
+  impl->set_sizes_contiguous({n});
+  return t;
+}
 T like(const T& t) { return fresh(t.sizes(), t.scalar_type(), t.get_device()); }
 T bytes(size_t n, const T& t) { return fresh({(int64_t)n}, at::kByte, t.get_device()); }
 void* data(const T& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -418,8 +427,11 @@ PyObject* paged_resize(PyObject* const* a, Py_ssize_t n) {
           *nf = ints(n_free, index, "n_free"), *nl = ints(now, index, "new_lengths");
   const int32_t page_size = int32_of(a[4], "page_size");
   Call call(index, a[7]);
-  const T cu = fresh({B + 1}, at::kInt, index), pos0 = fresh({B}, at::kInt, index),
-          slots = fresh({tokens}, at::kLong, index), lacking = fresh({2}, at::kInt, index);
+  // one allocation for the four outputs, each a tensor over its part of it
+  const int64_t ints_at = 8 * tokens;
+  const T all = fresh({ints_at + 4 * (2 * B + 3)}, at::kByte, index);
+  const T slots = part(all, 0, tokens, at::kLong), cu = part(all, ints_at, B + 1, at::kInt),
+          pos0 = part(all, ints_at + 4 * (B + 1), B, at::kInt), lacking = part(all, ints_at + 4 * (2 * B + 1), 2, at::kInt);
   const int st = unlocked(f_resize, nl, (int32_t)B, page_size, t, max_pages, len, f, (int32_t)free_pages.numel(), nf,
                           static_cast<int32_t*>(data(cu)), static_cast<int32_t*>(data(pos0)),
                           static_cast<int64_t*>(data(slots)), tokens, static_cast<int32_t*>(data(lacking)), call.stream);

@@ -29,8 +29,6 @@ using namespace draft;
 constexpr int kConsumers = 8;               // warps
 constexpr int kProducers = 2;               // warps, tiles alternating
 constexpr int kThreads = (kConsumers + kProducers + 1) * 32;
-constexpr int kWords = kDraftMaxNew / 64;
-constexpr int kBadWords = 10;               // new tokens, from the 16 keys that the first of them is in
 
 template <int D, int RG>
 struct Cfg {
@@ -42,7 +40,7 @@ struct Cfg {
   static constexpr int kTurns = kUnits > kSlices ? 1 : kSlices / kUnits;           // slices of a stage to a warp
   static constexpr uint32_t kRow = D * 2;
   static constexpr uint32_t kSide = kTile * kRow, kStage = 2 * kSide;
-  static constexpr int kRedStride = D + 4;                    // floats: keeps the results' writes conflict-free
+  static constexpr int kRedStride = Slice<D, 0>::kRedStride;
   static constexpr uint32_t kRed = kUnits * kRows * kRedStride * 4;
   static constexpr int kQSlots = 4 / RG > 2 ? 4 / RG : 2;     // items whose queries are in flight or in use
   static constexpr uint32_t kQBytes = kRows * kRow, kMask = kRows * kWords * 8;
@@ -74,159 +72,6 @@ struct SliceArgs {
   bool whole;                     // items are not split
   int box;                        // keys per box
   float scale_log2;
-};
-
-// Keys [x, x + 16) that a row sees, from its mask words in shared memory.
-__device__ __forceinline__ uint32_t sees16(const DraftBatch& a, const DraftSeq& s, int i, const unsigned long long* words,
-                                           int x) {
-  const int left = s.len - x, j = x - (s.len - s.n);
-  const uint32_t there = left >= 16 ? 0xffffu : (1u << max(left, 0)) - 1;
-  if (j <= -16) return there;
-  if (!a.bits) {
-    const int upto = i - j;                         // the last one seen, from x
-    return upto < 0 ? 0 : upto >= 15 ? there : there & ((2u << upto) - 1);
-  }
-  if (j < 0) return there & ((1u << -j) - 1 | (uint32_t)(words[0] << -j));
-  const int k = j >> 6, sh = j & 63;
-  uint64_t m = k < a.words ? words[k] >> sh : 0;
-  if (sh && k + 1 < a.words) m |= words[k + 1] << (64 - sh);
-  return there & (uint32_t)m;
-}
-
-// A warp's 16 rows and their running statistics; a lane has two, g and g + 8.
-template <int D, int RG>
-struct Part {
-  using C = Cfg<D, RG>;
-  static constexpr uint32_t kBoxRow = D < 64 ? D * 2 : 128;   // bytes of a key in a box's columns
-  uint32_t qa[D / 16][4];
-  float m[2], l[2], o[D / 8][4];
-  int g, tq;
-  uint32_t hs;                     // to a box's next 64 columns
-  int box;                         // a power of two
-
-  __device__ __forceinline__ explicit Part(int box_) : box(box_) {
-    const int lane = threadIdx.x & 31;
-    g = lane >> 2;
-    tq = lane & 3;
-    hs = box * 128;
-  }
-  __device__ __forceinline__ uint32_t row_at(int r) const {
-    return (uint32_t)(r & -box) * C::kRow + (r & (box - 1)) * kBoxRow;
-  }
-  __device__ __forceinline__ static int swizzle(int r) { return D < 64 ? (r >> 1) & 3 : r & 7; }
-  // rows `first` to first + 15 of the item's, as TMA laid them down (those behind its last hold anything)
-  __device__ __forceinline__ void load_q(uint32_t rows, int first) {
-    const int lane = threadIdx.x & 31, row = first + (lane & 15);
-    const uint32_t at = rows + row * kBoxRow, x = ((lane >> 4) ^ swizzle(row)) << 4;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      ldsm4(at + (ks >> 2) * C::kRows * 128 + ((((uint32_t)ks & 3) << 5) ^ x), qa[ks]);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-  }
-  // Slice `slice` of the stage; `all`: every row sees every key, else the rows' masks in `see`.
-  __device__ __forceinline__ void tile(uint32_t kbase, int slice, bool all, const uint32_t (&see)[2], float scale_log2) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t vbase = kbase + C::kSide;
-    const int krow = slice * 16 + ((lane >> 4) << 3) + (lane & 7), vrow = slice * 16 + (lane & 15);
-    const uint32_t k_at = kbase + row_at(krow), v_at = vbase + row_at(vrow);
-    const uint32_t kx = (((lane >> 3) & 1) ^ swizzle(krow)) << 4, vx = ((lane >> 4) ^ swizzle(vrow)) << 4;
-    // two chains for each eight keys
-    float s[2][4] = {}, s2[2][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t b[4];
-      ldsm4(k_at + (ks >> 2) * hs + ((((uint32_t)ks & 3) << 5) ^ kx), b);
-      mma16816(ks & 1 ? s2[0] : s[0], qa[ks], b[0], b[1]);
-      mma16816(ks & 1 ? s2[1] : s[1], qa[ks], b[2], b[3]);
-    }
-    uint32_t ph[4], pl[4];
-    float corr[2];
-    bool moved = false;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float v[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[c] = (s[c >> 1][2 * r + (c & 1)] + s2[c >> 1][2 * r + (c & 1)]) * scale_log2;
-        if (!all && !(see[r] >> ((c >> 1) * 8 + 2 * tq + (c & 1)) & 1)) v[c] = -INFINITY;
-      }
-      float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
-      moved |= mn > m[r];
-      corr[r] = ex2_approx(m[r] - base);
-      m[r] = mn;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = ex2_approx(v[c] - base);
-      l[r] = l[r] * corr[r] + (v[0] + v[1]) + (v[2] + v[3]);
-      Worker<bf16, D, 8>::split(v[0], v[1], ph[r], pl[r]);
-      Worker<bf16, D, 8>::split(v[2], v[3], ph[2 + r], pl[2 + r]);
-    }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= corr[0];
-        o[i][1] *= corr[0];
-        o[i][2] *= corr[1];
-        o[i][3] *= corr[1];
-      }
-    }
-    // two column blocks at a time: a product does not wait for the one before it
-#pragma unroll
-    for (int i = 0; i < D / 16; i += 2) {
-      uint32_t b[2][4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        ldsm4_t(v_at + ((i + k) >> 2) * hs + ((((uint32_t)(i + k) & 3) << 5) ^ vx), b[k]);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mma16816(o[2 * (i + k)], part ? pl : ph, b[k][0], b[k][1]);
-          mma16816(o[2 * (i + k) + 1], part ? pl : ph, b[k][2], b[k][3]);
-        }
-    }
-  }
-  // V of a slice as the products may read it: rows behind the last key become zeros, values that are not finite are
-  // taken out (their keys in `found`).
-  __device__ __forceinline__ uint32_t clean(uint8_t* stage, int slice, int left) const {
-    const int lane = threadIdx.x & 31;
-    uint32_t found = 0;
-    for (int e = lane; e < 16 * (D / 8); e += 32) {
-      const int key = e / (D / 8), ch = e % (D / 8);
-      uint8_t* at = stage + C::kSide + row_at(slice * 16 + key) + (ch >> 3) * hs + (ch & 7) * 16;
-      if (key >= left) *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-      else if (clear_bad<bf16>(at)) found |= 1u << key;
-    }
-    __syncwarp();
-    return __reduce_or_sync(0xffffffffu, found);
-  }
-  // the warp's results: maxima and sums (-1: no keys, nothing to add), outputs [16][kRedStride]
-  __device__ __forceinline__ void result(float* rm, float* rl, float* ro, bool active) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (tq == 0) {
-        rm[g + 8 * r] = m[r];
-        rl[g + 8 * r] = active ? l[r] : -1.f;
-      }
-      if (!active) continue;
-      float* to = ro + (g + 8 * r) * C::kRedStride + 2 * tq;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-    }
-  }
 };
 
 template <int D, int RG>
@@ -383,7 +228,7 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
   // ---- consumers -------------------------------------------------------------
   const int rg = warp % RG, unit = warp / RG;
   const int grp = C::kGroups > 1 ? unit / C::kSlices : 0, slice0 = C::kGroups > 1 ? unit % C::kSlices : unit;
-  Part<D, RG> me(p.box);
+  Slice<D, C::kSide> me(p.box);
   // a row's token: floor(row / heads), exact for rows of up to 64 (an item of part of a key head's query heads has one)
   const uint32_t by_heads = (65535 + a.heads) / a.heads;
   auto token_of = [&](int row) { return a.hgroups > 1 ? 0 : (int)(row * by_heads >> 16); };
@@ -399,7 +244,7 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     ok = mbar_wait_warp(&ctl->q_full[slot], (segs / C::kQSlots) & 1, &ctl->abort, a.status);
     if (!ok) break;
     const bool live = rg * 16 < rows;
-    if (live) me.load_q(smem_u32(qbuf + slot * C::kQBytes), rg * 16);
+    if (live) me.load_q(smem_u32(qbuf + slot * C::kQBytes), rg * 16, C::kRows * 128);
     const int r0 = rg * 16 + me.g, i0 = token_of(r0), i1 = token_of(r0 + 8);
     bool active = false;
     for (int64_t t = w.t0; t < w.t1; ++t, ++it) {

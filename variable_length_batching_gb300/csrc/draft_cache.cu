@@ -14,9 +14,11 @@ namespace {
 // takes and adds; then the released pages, then the taken ones, then the
 // slots.  Every CTA scans all rows (their lengths are a load that all do at
 // once), a thread a strip of them; pages and tokens are then dealt out one by
-// one over all threads, however they lie in the rows.
+// one over all threads, however they lie in the rows, several searches side
+// by side (one after the other 512 prompts of 65,000 tokens took 12.3 us).
 constexpr int kResizeThreads = 512;
 constexpr int kResizeCtas = 8;
+constexpr int kResizeUnroll = 4;
 
 struct ResizeArgs {
   const int32_t* new_lengths;
@@ -37,6 +39,9 @@ struct Change {
   int old, now;             // positions before and after
   int have, want;           // pages
 };
+__device__ __forceinline__ int pages_of(const ResizeArgs& a, int n) {
+  return (int)(((uint32_t)n + (uint32_t)a.page_size - 1) / (uint32_t)a.page_size);
+}
 __device__ __forceinline__ Change change_of(const ResizeArgs& a, int b, unsigned int* status) {
   Change c;
   c.old = a.lengths[b];
@@ -47,8 +52,8 @@ __device__ __forceinline__ Change change_of(const ResizeArgs& a, int b, unsigned
     c.have = c.want = 0;
     return c;
   }
-  c.have = (int)(((int64_t)c.old + a.page_size - 1) / a.page_size);
-  c.want = (int)(((int64_t)c.now + a.page_size - 1) / a.page_size);
+  c.have = pages_of(a, c.old);
+  c.want = pages_of(a, c.now);
   return c;
 }
 struct Sums {
@@ -68,9 +73,10 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const ResizeArgs a) {
+  enum { kRel, kTake, kAdd };
   __shared__ Sums warp_sum[kResizeThreads / 32];
-  __shared__ Sums ahead[kResizeThreads];           // of the rows in front of a thread's strip
-  __shared__ Change one[kResizeThreads];           // strips of one row
+  __shared__ int ahead[3][kResizeThreads];         // released, taken, added in the rows in front of a thread's strip
+  __shared__ int old_of[kResizeThreads], have_of[kResizeThreads], want_of[kResizeThreads];     // strips of one row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = gridDim.x, cta = blockIdx.x;
   pdl_wait();
@@ -78,12 +84,16 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
   // the scan of what rows release, take and add, every CTA for itself
   const int strip = (int)(((int64_t)a.B + kResizeThreads - 1) / kResizeThreads);
   const int b_lo = (int)min64(a.B, (int64_t)tid * strip), b_hi = (int)min64(a.B, (int64_t)b_lo + strip);
+  const int nf = *a.n_free;
   Sums mine = {0, 0, 0};
+  Change one = {};
   for (int b = b_lo; b < b_hi; ++b) {
-    const Change c = change_of(a, b, cta == 0 ? a.status : nullptr);
-    if (strip == 1) one[tid] = c;
-    mine += sums_of(c);
+    one = change_of(a, b, cta == 0 ? a.status : nullptr);
+    mine += sums_of(one);
   }
+  old_of[tid] = one.old;
+  have_of[tid] = one.have;
+  want_of[tid] = one.want;
   Sums inc = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -92,17 +102,20 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
     if (lane >= m) inc += o;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  const int nf = *a.n_free;
   __syncthreads();
   Sums before = {inc.rel - mine.rel, inc.take - mine.take, inc.add - mine.add}, total = {0, 0, 0};
+#pragma unroll
   for (int w = 0; w < kResizeThreads / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  ahead[tid] = before;
   const bool broken = nf < 0 || nf > a.n_pages || nf + total.rel > a.n_pages;
   const int64_t lack = max64(0, total.take - total.rel - max(nf, 0)), over = max64(0, total.add - a.T);
   const bool none = broken || lack > 0 || over > 0;
+  // (below 2^31 unless nothing is done)
+  ahead[kRel][tid] = (int)before.rel;
+  ahead[kTake][tid] = (int)before.take;
+  ahead[kAdd][tid] = (int)before.add;
   cluster_sync_all();                    // every CTA has read what is written from here on
   if (cta == 0 && tid == 0) {
     if (broken) flag_device(a.status, kDevCheck);
@@ -114,7 +127,7 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
   {
     Sums at = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      const Change c = strip == 1 ? one[tid] : change_of(a, b, nullptr);
+      const Change c = strip == 1 ? one : change_of(a, b, nullptr);
       if (b % ctas == cta) {
         a.cu[b] = none ? 0 : (int)at.add;
         a.pos0[b] = c.old;
@@ -123,63 +136,77 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
       at += sums_of(c);
     }
   }
-  const int64_t me = (int64_t)cta * kResizeThreads + tid, all = (int64_t)ctas * kResizeThreads;
+  const uint32_t me = cta * kResizeThreads + tid, all = ctas * kResizeThreads;
+  const uint32_t T = (uint32_t)a.T;
   if (none) {
-    for (int64_t t = me; t < a.T; t += all) a.slots[t] = -1;
+    for (uint32_t t = me; t < T; t += all) a.slots[t] = -1;
     return;
   }
-  // The row whose share of a sum holds `rank`: its strip by a search, the row
-  // by a walk through the strip.
-  auto row_of = [&](int64_t Sums::*what, int64_t rank, int64_t& off, Change& c) {
-    int lo = 0, hi = kResizeThreads - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (ahead[mid].*what <= rank) lo = mid; else hi = mid - 1;
-    }
-    off = rank - ahead[lo].*what;
+  // The strips that hold ranks r[k] of a sum, and the places in them.
+  auto strips_of = [&](int what, const uint32_t (&r)[kResizeUnroll], int (&lo)[kResizeUnroll]) {
+#pragma unroll
+    for (int k = 0; k < kResizeUnroll; ++k) lo[k] = 0;
+#pragma unroll
+    for (int step = kResizeThreads / 2; step > 0; step >>= 1)
+#pragma unroll
+      for (int k = 0; k < kResizeUnroll; ++k)
+        if (ahead[what][lo[k] + step] <= (int)r[k]) lo[k] += step;
+  };
+  // The row in a strip, its lengths before and the place in its share of the sum.
+  auto row_of = [&](int what, int lo, uint32_t rank, int& off, Change& c) {
+    off = (int)rank - ahead[what][lo];
     if (strip == 1) {
-      c = one[lo];
+      c.old = old_of[lo];
+      c.have = have_of[lo];
+      c.want = want_of[lo];
       return lo;
     }
-    int b = lo * strip;
-    for (;; ++b) {
+    for (int b = lo * strip;; ++b) {
       c = change_of(a, b, nullptr);
-      const int64_t n = sums_of(c).*what;
+      const Sums s = sums_of(c);
+      const int n = (int)(what == kRel ? s.rel : what == kTake ? s.take : s.add);
       if (off < n) return b;
       off -= n;
     }
   };
   // released pages: the first of them ends on top of the stack
   const int64_t top = nf + total.rel - 1;
-  for (int64_t r = me; r < total.rel; r += all) {
-    int64_t off;
-    Change c;
-    const int b = row_of(&Sums::rel, r, off, c);
+  const uint32_t rel = (uint32_t)total.rel, take = (uint32_t)total.take, add = (uint32_t)total.add;
+  auto moves = [&](int what, uint32_t count, auto f) {
+    for (uint32_t r0 = me; r0 < count; r0 += all * kResizeUnroll) {
+      uint32_t r[kResizeUnroll];
+      int lo[kResizeUnroll];
+#pragma unroll
+      for (int k = 0; k < kResizeUnroll; ++k) r[k] = min(r0 + k * all, count - 1);
+      strips_of(what, r, lo);
+#pragma unroll
+      for (int k = 0; k < kResizeUnroll; ++k) {
+        if (r0 + k * all >= count) break;
+        int off;
+        Change c;
+        const int b = row_of(what, lo[k], r[k], off, c);
+        f(r[k], b, off, c);
+      }
+    }
+  };
+  moves(kRel, rel, [&](uint32_t r, int b, int off, const Change& c) {
     int32_t* e = a.table + (int64_t)b * a.max_pages + c.want + off;
     a.free_pages[top - r] = *e;
     *e = -1;
-  }
-  if (total.take > 0) {
-    if (total.rel > 0) cluster_sync_all();
-    for (int64_t r = me; r < total.take; r += all) {
-      int64_t off;
-      Change c;
-      const int b = row_of(&Sums::take, r, off, c);
+  });
+  if (take > 0) {
+    if (rel > 0) cluster_sync_all();
+    moves(kTake, take, [&](uint32_t r, int b, int off, const Change& c) {
       a.table[(int64_t)b * a.max_pages + c.have + off] = a.free_pages[top - r];
-    }
+    });
   }
-  if (total.take > 0 || strip > 1) cluster_sync_all();
-  for (int64_t t = me; t < a.T; t += all) {
-    int64_t slot = -1;
-    if (t < total.add) {
-      int64_t off;
-      Change c;
-      const int b = row_of(&Sums::add, t, off, c);
-      const int64_t x = c.old + off;
-      slot = (int64_t)a.table[(int64_t)b * a.max_pages + x / a.page_size] * a.page_size + x % a.page_size;
-    }
-    a.slots[t] = slot;
-  }
+  if (take > 0 || strip > 1) cluster_sync_all();
+  const uint32_t ps = a.page_size;
+  moves(kAdd, add, [&](uint32_t t, int b, int off, const Change& c) {
+    const uint32_t x = (uint32_t)c.old + off, pg = x / ps;
+    a.slots[t] = (int64_t)a.table[(int64_t)b * a.max_pages + pg] * ps + (x - pg * ps);
+  });
+  for (uint32_t t = add + me; t < T; t += all) a.slots[t] = -1;
   if (strip > 1) {
     cluster_sync_all();                  // nobody reads the old lengths any more
     for (int64_t b = me; b < a.B; b += all) a.lengths[b] = change_of(a, (int)b, nullptr).now;
@@ -189,18 +216,23 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
 // ---- the tree's masks and positions ---------------------------------------------
 //
 // A CTA to a sequence, a thread to a token.  In round r a token adds what the
-// token 2^r above it has gathered, so a path of 256 takes eight rounds.
+// token 2^r above it has gathered, so a path of 256 takes eight rounds.  A
+// token's own words stay in registers; W words, so that they are moved whole.
 constexpr int kTreeThreads = kDraftMaxNew;
 
+template <int W>
 __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t* parents, const int32_t* cu, int64_t T,
                                                                   int max_new, const int32_t* pos0, int64_t* bits,
                                                                   int32_t* positions, unsigned int* status) {
-  __shared__ unsigned long long words[2][kTreeThreads][kDraftMaxNew / 64];
-  __shared__ int up[2][kTreeThreads], depth[2][kTreeThreads];
+  struct alignas(W % 2 ? 8 : 16) Words {
+    unsigned long long w[W];
+  };
+  __shared__ Words words[2][64 * W];
+  __shared__ int2 above[2][64 * W];                // the next one to ask, and the tokens in between
   const int b = blockIdx.x, i = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int lo = cu[b], hi = cu[b + 1], n = hi - lo, W = (max_new + 63) / 64;
+  const int lo = cu[b], hi = cu[b + 1], n = hi - lo, start = pos0 ? pos0[b] : 0;
   if (b == gridDim.x - 1)                          // tokens that only fill up the batch
     for (int64_t t = max(hi, 0) + i; t < T; t += blockDim.x) {
       if (positions) positions[t] = 0;
@@ -210,31 +242,42 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
     if (i == 0) flag_device(status, kDevCheck);
     return;
   }
-  if (n == 0) return;
+  Words mine;
+  int2 up = make_int2(-1, 0);
   if (i < n) {
-    int p = parents[(int64_t)lo + i];
-    if (p >= i || p < -1) {
+    up.x = parents[(int64_t)lo + i];
+    if (up.x >= i || up.x < -1) {
       flag_device(status, kDevCheck);
-      p = -1;
+      up.x = -1;
     }
-    up[0][i] = p;
-    depth[0][i] = p >= 0;
-    for (int w = 0; w < W; ++w) words[0][i][w] = w == i >> 6 ? 1ull << (i & 63) : 0;
+    up.y = up.x >= 0;
   }
-  int from = 0;
-  for (int reach = 1; reach < n; reach <<= 1) {
-    __syncthreads();
-    if (i < n) {
-      const int p = up[from][i];
-      up[from ^ 1][i] = p >= 0 ? up[from][p] : -1;
-      depth[from ^ 1][i] = depth[from][i] + (p >= 0 ? depth[from][p] : 0);
-      for (int w = 0; w < W; ++w) words[from ^ 1][i][w] = words[from][i][w] | (p >= 0 ? words[from][p][w] : 0);
+#pragma unroll
+  for (int w = 0; w < W; ++w) mine.w[w] = w == i >> 6 ? 1ull << (i & 63) : 0;
+  for (int reach = 1, at = 0; reach < n; reach <<= 1, at ^= 1) {
+    words[at][i] = mine;
+    above[at][i] = up;
+    if (!__syncthreads_or(up.x >= 0)) break;       // (everybody has asked all the way up)
+    if (up.x >= 0) {
+      const Words theirs = words[at][up.x];
+      const int2 next = above[at][up.x];
+#pragma unroll
+      for (int w = 0; w < W; ++w) mine.w[w] |= theirs.w[w];
+      up = make_int2(next.x, up.y + next.y);
     }
-    from ^= 1;
   }
   if (i >= n) return;
-  if (positions) positions[(int64_t)lo + i] = (pos0 ? pos0[b] : 0) + depth[from][i];
-  for (int w = 0; w < W; ++w) bits[((int64_t)lo + i) * W + w] = (int64_t)words[from][i][w];
+  if (positions) positions[(int64_t)lo + i] = start + up.y;
+  if constexpr (W % 2 == 0) {
+    ulonglong2* to = reinterpret_cast<ulonglong2*>(bits + ((int64_t)lo + i) * W);
+    if ((reinterpret_cast<uintptr_t>(bits) & 15) == 0) {
+#pragma unroll
+      for (int w = 0; w < W; w += 2) to[w / 2] = make_ulonglong2(mine.w[w], mine.w[w + 1]);
+      return;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < W; ++w) bits[((int64_t)lo + i) * W + w] = (int64_t)mine.w[w];
 }
 
 // ---- the accepted tokens moved up ---------------------------------------------------
@@ -244,7 +287,7 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
 // read before any is written, and then the next run, reads nothing that it
 // has written.  CTAs have a sequence, a range of its heads and a side each.
 constexpr int kKeepThreads = 256;
-constexpr int kKeepUnroll = 4;
+constexpr int kKeepUnroll = 8;
 
 struct KeepArgs {
   uint8_t* pool[2];
@@ -266,11 +309,12 @@ __device__ __forceinline__ int64_t keep_offset(const KeepArgs& a, int b, int64_t
   return ((int64_t)id * a.H * a.page_size + (x - (int64_t)pg * a.page_size)) * a.row_bytes;
 }
 
-__global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepArgs a) {
+__global__ void __launch_bounds__(kKeepThreads, 4) paged_keep_kernel(const KeepArgs a) {
   __shared__ int64_t from[kKeepThreads], to[kKeepThreads];
   pdl_wait();
   pdl_trigger();
   const int side = blockIdx.y & 1, h0 = (int)(blockIdx.y >> 1) * a.heads, nh = min(a.heads, a.H - h0);
+  uint8_t* const pool = side ? a.pool[1] : a.pool[0];
   const int words = a.row_bytes / 16, per = nh * words;            // 16-byte words of a token
   const int run = max(1, kKeepThreads * kKeepUnroll / per);        // tokens read before any is written
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -310,8 +354,8 @@ __global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepArgs
             const int t = r + e / per, w = e % per;
             if (from[t] < 0) continue;
             const int64_t off = ((int64_t)(h0 + w / words) * a.page_size) * a.row_bytes + (w % words) * 16;
-            v[u] = *reinterpret_cast<const uint4*>(a.pool[side] + from[t] + off);
-            at[u] = a.pool[side] + to[t] + off;
+            v[u] = *reinterpret_cast<const uint4*>(pool + from[t] + off);
+            at[u] = pool + to[t] + off;
           }
           __syncthreads();
 #pragma unroll
@@ -366,8 +410,13 @@ cudaError_t launch_draft_tree(const int32_t* parents, const int32_t* cu, int B, 
                               const int32_t* pos0, int64_t* bits, int32_t* positions, unsigned int* status,
                               cudaStream_t s) {
   if (B == 0 || T == 0) return cudaSuccess;
-  return launch_pdl(draft_tree_kernel, dim3(B), dim3((max_new + 31) / 32 * 32), 0, s, parents, cu, T, max_new, pos0,
-                    bits, positions, status);
+  const dim3 grid(B), block((max_new + 31) / 32 * 32);
+  switch ((max_new + 63) / 64) {
+    case 1: return launch_pdl(draft_tree_kernel<1>, grid, block, 0, s, parents, cu, T, max_new, pos0, bits, positions, status);
+    case 2: return launch_pdl(draft_tree_kernel<2>, grid, block, 0, s, parents, cu, T, max_new, pos0, bits, positions, status);
+    case 3: return launch_pdl(draft_tree_kernel<3>, grid, block, 0, s, parents, cu, T, max_new, pos0, bits, positions, status);
+    default: return launch_pdl(draft_tree_kernel<4>, grid, block, 0, s, parents, cu, T, max_new, pos0, bits, positions, status);
+  }
 }
 
 cudaError_t launch_paged_keep(const PagedPool& p, const int32_t* kept, int64_t K, const int32_t* cu, int B,
@@ -388,7 +437,7 @@ cudaError_t launch_paged_keep(const PagedPool& p, const int32_t* kept, int64_t K
   a.row_bytes = p.row_bytes;
   a.B = B;
   a.max_pages = max_pages;
-  a.heads = min(p.H, max(1, kKeepThreads * kKeepUnroll / 32 * 16 / p.row_bytes));     // 32 tokens in flight
+  a.heads = min(p.H, max(1, kKeepThreads * kKeepUnroll / 64 * 16 / p.row_bytes));     // 64 tokens in flight
   while ((p.H + a.heads - 1) / a.heads > 32767) a.heads *= 2;
   a.status = status;
   const int groups = (p.H + a.heads - 1) / a.heads;

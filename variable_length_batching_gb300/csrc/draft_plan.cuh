@@ -48,6 +48,10 @@ __device__ __forceinline__ DraftSeq draft_seq(const DraftBatch& a, int first, in
 __device__ __forceinline__ DraftSeq draft_seq(const DraftBatch& a, int b, unsigned int* status) {
   return draft_seq(a, a.cu[b], a.cu[b + 1], a.lengths[b], status);
 }
+// Items of a sequence, and the most of any.
+inline int draft_items_most(const DraftBatch& a) {
+  return a.Hkv * a.hgroups * ((a.max_new + a.tokens - 1) / a.tokens);
+}
 __device__ __forceinline__ int draft_items(const DraftBatch& a, int n) {
   return a.Hkv * a.hgroups * ((n + a.tokens - 1) / a.tokens);
 }

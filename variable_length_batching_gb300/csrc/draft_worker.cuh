@@ -1,5 +1,6 @@
-// What the threads of the general kernel for drafted tokens do with a tile of
-// 64 keys and up to 64 rows: scores, a running softmax, outputs.
+// What the threads of the kernels for drafted tokens do with keys and rows:
+// scores, a running softmax, outputs.  Rows: 64 keys and up to 64 rows to a CTA
+// (the general kernel).  Slice: 16 keys and 16 rows to a warp.
 #pragma once
 
 #include "draft_plan.cuh"
@@ -387,6 +388,182 @@ struct Rows<float, D> {
       const int row = 4 * y + r;
       if (x == 0) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m[r], l[r]);
       put(po + row * D, r, 1.f);
+    }
+  }
+};
+
+// ---- slices of 16 keys -------------------------------------------------------------
+
+constexpr int kWords = kDraftMaxNew / 64;
+constexpr int kBadWords = 10;               // new tokens, from the 16 keys that the first of them is in
+
+// Keys [x, x + 16) that a row sees, from its mask words in shared memory.
+__device__ __forceinline__ uint32_t sees16(const DraftBatch& a, const DraftSeq& s, int i, const unsigned long long* words,
+                                           int x) {
+  const int left = s.len - x, j = x - (s.len - s.n);
+  const uint32_t there = left >= 16 ? 0xffffu : (1u << max(left, 0)) - 1;
+  if (j <= -16) return there;
+  if (!a.bits) {
+    const int upto = i - j;                         // the last one seen, from x
+    return upto < 0 ? 0 : upto >= 15 ? there : there & ((2u << upto) - 1);
+  }
+  if (j < 0) return there & ((1u << -j) - 1 | (uint32_t)(words[0] << -j));
+  const int k = j >> 6, sh = j & 63;
+  uint64_t m = k < a.words ? words[k] >> sh : 0;
+  if (sh && k + 1 < a.words) m |= words[k + 1] << (64 - sh);
+  return there & (uint32_t)m;
+}
+
+// A warp's 16 rows and their running statistics; a lane has two, g and g + 8.
+// The warp's keys lie in a stage as those of paged_worker.cuh, the values kSide bytes behind them.
+template <int D, uint32_t kSide>
+struct Slice {
+  static constexpr uint32_t kRow = D * 2;
+  static constexpr int kRedStride = D + 4;      // floats: keeps the results' writes conflict-free
+  static constexpr uint32_t kBoxRow = D < 64 ? D * 2 : 128;   // bytes of a key in a box's columns
+  uint32_t qa[D / 16][4];
+  float m[2], l[2], o[D / 8][4];
+  int g, tq;
+  uint32_t hs;                     // to a box's next 64 columns
+  int box;                         // a power of two
+
+  __device__ __forceinline__ explicit Slice(int box_) : box(box_) {
+    const int lane = threadIdx.x & 31;
+    g = lane >> 2;
+    tq = lane & 3;
+    hs = box * 128;
+  }
+  __device__ __forceinline__ uint32_t row_at(int r) const {
+    return (uint32_t)(r & -box) * kRow + (r & (box - 1)) * kBoxRow;
+  }
+  __device__ __forceinline__ static int swizzle(int r) { return D < 64 ? (r >> 1) & 3 : r & 7; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+  }
+  // rows `first` to first + 15 of the item's, as TMA laid them down, 64 columns `part` bytes behind the 64 before (rows
+  // behind the item's last hold anything)
+  __device__ __forceinline__ void load_q(uint32_t rows, int first, int part) {
+    const int lane = threadIdx.x & 31, row = first + (lane & 15);
+    const uint32_t at = rows + row * kBoxRow, x = ((lane >> 4) ^ swizzle(row)) << 4;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      ldsm4(at + (ks >> 2) * part + ((((uint32_t)ks & 3) << 5) ^ x), qa[ks]);
+    clear();
+  }
+  // the same from two rows in memory, NULL for none
+  __device__ __forceinline__ void load_q(const bf16* row0, const bf16* row1) {
+    const uint32_t *q0 = reinterpret_cast<const uint32_t*>(row0), *q1 = reinterpret_cast<const uint32_t*>(row1);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qa[ks][0] = q0 ? q0[ks * 8 + tq] : 0u;
+      qa[ks][1] = q1 ? q1[ks * 8 + tq] : 0u;
+      qa[ks][2] = q0 ? q0[ks * 8 + 4 + tq] : 0u;
+      qa[ks][3] = q1 ? q1[ks * 8 + 4 + tq] : 0u;
+    }
+    clear();
+  }
+  // Slice `slice` of the stage; `all`: every row sees every key, else the rows' masks in `see`.
+  __device__ __forceinline__ void tile(uint32_t kbase, int slice, bool all, const uint32_t (&see)[2], float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t vbase = kbase + kSide;
+    const int krow = slice * 16 + ((lane >> 4) << 3) + (lane & 7), vrow = slice * 16 + (lane & 15);
+    const uint32_t k_at = kbase + row_at(krow), v_at = vbase + row_at(vrow);
+    const uint32_t kx = (((lane >> 3) & 1) ^ swizzle(krow)) << 4, vx = ((lane >> 4) ^ swizzle(vrow)) << 4;
+    // two chains for each eight keys
+    float s[2][4] = {}, s2[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t b[4];
+      ldsm4(k_at + (ks >> 2) * hs + ((((uint32_t)ks & 3) << 5) ^ kx), b);
+      mma16816(ks & 1 ? s2[0] : s[0], qa[ks], b[0], b[1]);
+      mma16816(ks & 1 ? s2[1] : s[1], qa[ks], b[2], b[3]);
+    }
+    uint32_t ph[4], pl[4];
+    float corr[2];
+    bool moved = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] = (s[c >> 1][2 * r + (c & 1)] + s2[c >> 1][2 * r + (c & 1)]) * scale_log2;
+        if (!all && !(see[r] >> ((c >> 1) * 8 + 2 * tq + (c & 1)) & 1)) v[c] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
+      moved |= mn > m[r];
+      corr[r] = ex2_approx(m[r] - base);
+      m[r] = mn;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = ex2_approx(v[c] - base);
+      l[r] = l[r] * corr[r] + (v[0] + v[1]) + (v[2] + v[3]);
+      Worker<bf16, D, 8>::split(v[0], v[1], ph[r], pl[r]);
+      Worker<bf16, D, 8>::split(v[2], v[3], ph[2 + r], pl[2 + r]);
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= corr[0];
+        o[i][1] *= corr[0];
+        o[i][2] *= corr[1];
+        o[i][3] *= corr[1];
+      }
+    }
+    // two column blocks at a time: a product does not wait for the one before it
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 2) {
+      uint32_t b[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        ldsm4_t(v_at + ((i + k) >> 2) * hs + ((((uint32_t)(i + k) & 3) << 5) ^ vx), b[k]);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mma16816(o[2 * (i + k)], part ? pl : ph, b[k][0], b[k][1]);
+          mma16816(o[2 * (i + k) + 1], part ? pl : ph, b[k][2], b[k][3]);
+        }
+    }
+  }
+  // V of a slice as the products may read it: rows behind the last key become zeros, values that are not finite are
+  // taken out (their keys in `found`).
+  __device__ __forceinline__ uint32_t clean(uint8_t* stage, int slice, int left) const {
+    const int lane = threadIdx.x & 31;
+    uint32_t found = 0;
+    for (int e = lane; e < 16 * (D / 8); e += 32) {
+      const int key = e / (D / 8), ch = e % (D / 8);
+      uint8_t* at = stage + kSide + row_at(slice * 16 + key) + (ch >> 3) * hs + (ch & 7) * 16;
+      if (key >= left) *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+      else if (clear_bad<bf16>(at)) found |= 1u << key;
+    }
+    __syncwarp();
+    return __reduce_or_sync(0xffffffffu, found);
+  }
+  // the warp's results: maxima and sums (-1: no keys, nothing to add), outputs [16][kRedStride]
+  __device__ __forceinline__ void result(float* rm, float* rl, float* ro, bool active) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (tq == 0) {
+        rm[g + 8 * r] = m[r];
+        rl[g + 8 * r] = active ? l[r] : -1.f;
+      }
+      if (!active) continue;
+      float* to = ro + (g + 8 * r) * kRedStride + 2 * tq;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
     }
   }
 };

@@ -1341,20 +1341,24 @@ nt_status nt_selftest_paged_attn(int32_t kernel, int32_t cluster, const nt_kv_pa
   return NT_OK;
 }
 
-nt_status nt_selftest_paged_tree_attn(int32_t kernel, const nt_kv_pages* pages, const void* q, int64_t q_stride,
+nt_status nt_selftest_paged_tree_attn(int32_t kernel, int32_t cluster, const nt_kv_pages* pages, const void* q, int64_t q_stride,
                                       int64_t T, int32_t H, const int32_t* d_cu_seqlens, int32_t B, int32_t max_new,
                                       const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths,
                                       const int64_t* d_bits, float scale, void* o, float* lse, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-  if (kernel < 0 || kernel > 2) return fail(NT_ERR_INVALID, "kernel %d (0, 1 or 2)", kernel);
+  if (kernel < 0 || kernel > 3) return fail(NT_ERR_INVALID, "kernel %d (0 to 3)", kernel);
+  if (cluster < 0 || cluster > kPagedMaxCluster || (cluster && kernel != 3))
+    return fail(NT_ERR_INVALID, "cluster %d: 0, or 1 to %d for kernel 3", cluster, kPagedMaxCluster);
   DraftProblem p;
   const nt_status st = check_tree_attn(pages, q, q_stride, T, H, d_cu_seqlens, B, max_new, d_block_table, max_pages,
                                        d_lengths, d_bits, scale, o, lse, workspace, workspace_bytes, &p);
   if (st != NT_OK || T == 0 || max_new == 0) return st;
   if ((kernel == 1 && !draft_tc_supported(pages->dtype, p)) || (kernel == 2 && !draft_slices_supported(pages->dtype, p)))
     return fail(NT_ERR_UNSUPPORTED, "kernel %d does not take this call", kernel);
+  if (kernel == 3 && cluster == 0) draft_spread_us(pages->dtype, p, &cluster);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = kernel == 2   ? launch_draft_slices(p, status_word(), s)
+  const cudaError_t e = kernel == 3   ? launch_draft_spread(pages->dtype, p, cluster, status_word(), s)
+                        : kernel == 2 ? launch_draft_slices(p, status_word(), s)
                         : kernel == 1 ? launch_draft_tc(p, status_word(), s)
                                       : launch_draft_rows(pages->dtype, p, status_word(), s);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");

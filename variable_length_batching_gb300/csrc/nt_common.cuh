@@ -486,6 +486,9 @@ cudaError_t launch_draft_tc(const DraftProblem& p, unsigned int* status, cudaStr
 // once).
 bool draft_slices_supported(nt_dtype dt, const DraftProblem& p);
 cudaError_t launch_draft_slices(const DraftProblem& p, unsigned int* status, cudaStream_t s);
+// A cluster of CTAs per item, any page size and type; its estimated time in us.
+double draft_spread_us(nt_dtype dt, const DraftProblem& p, int* cluster);
+cudaError_t launch_draft_spread(nt_dtype dt, const DraftProblem& p, int cluster, unsigned int* status, cudaStream_t s);
 // Any page size, a CTA to 64 rows.
 cudaError_t launch_draft_rows(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
 

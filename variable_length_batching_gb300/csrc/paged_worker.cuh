@@ -295,7 +295,10 @@ struct Worker<float, D, HP> {
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[h][c] = 0.f;
   }
-  __device__ __forceinline__ void tile(const uint8_t* stage, uint32_t side, int left, float scale_log2) {
+  // kMasked: `see` has a bit for each key of the slice that rows 2 i + half see
+  template <bool kMasked = false>
+  __device__ __forceinline__ void tile(const uint8_t* stage, uint32_t side, int left, float scale_log2,
+                                       const uint32_t* see = nullptr) {
     const int lane = threadIdx.x & 31, key = lane & 15;
     const uint32_t k = smem_u32(stage) + k_off, v = smem_u32(stage) + side + v_off, qs = smem_u32(q + half * (D / 2));
     float acc[HP][kAcc] = {};
@@ -323,7 +326,8 @@ struct Worker<float, D, HP> {
       float t;
       if constexpr (HP == 1) t = s[0] + __shfl_xor_sync(0xffffffffu, s[0], 16);
       else t = (half ? s[2 * i + 1] : s[2 * i]) + __shfl_xor_sync(0xffffffffu, half ? s[2 * i] : s[2 * i + 1], 16);
-      t = key < left ? t * scale_log2 : -INFINITY;       // rows behind the last key may hold anything
+      const bool seen = kMasked ? see[i] >> key & 1 : key < left;
+      t = seen ? t * scale_log2 : -INFINITY;             // rows behind the last key may hold anything
       float mx = t;
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));

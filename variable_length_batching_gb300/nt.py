@@ -102,7 +102,7 @@ SIGNATURES = {
     "nt_paged_keep": (_I32, [_PG, _P, _I64, _P, _I32, _P, _I32, _P, _P]),
     "nt_paged_tree_attn_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "nt_paged_tree_attn": (_I32, [_PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P, _P, _SZ, _P]),
-    "nt_selftest_paged_tree_attn": (_I32, [_I32, _PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P,
+    "nt_selftest_paged_tree_attn": (_I32, [_I32, _I32, _PG, _P, _I64, _I64, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _F, _P, _P,
                                            _P, _SZ, _P]),
     "nt_selftest_paged_attn": (_I32, [_I32, _I32, _PG, _P, _I64, _I32, _I32, _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
     "nt_device_status": (_I32, [_P]),
@@ -883,9 +883,10 @@ def nt_selftest_paged_attn(kernel: int, pages: KVPages, q: torch.Tensor, block_t
 def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu_seqlens: torch.Tensor,
                                 block_table: torch.Tensor, lengths: torch.Tensor, max_new: int,
                                 bits: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                                workspace: Optional[torch.Tensor] = None, stream=None):
+                                cluster: int = 0, workspace: Optional[torch.Tensor] = None, stream=None):
     """nt_paged_tree_attn by kernel 0 (the general one), 1 (in tensor
-    memory) or 2 (few rows), for tests of each; contiguous tensors.  Returns (o, lse)."""
+    memory), 2 (few rows) or 3 (a cluster of CTAs per item, ``cluster`` of
+    them or as the call would), for tests of each; contiguous tensors.  Returns (o, lse)."""
     T, H, d = q.shape
     B = cu_seqlens.numel() - 1
     if q.dtype != pages.dtype or any(t.dtype != torch.int32 for t in (cu_seqlens, block_table, lengths)):
@@ -898,7 +899,7 @@ def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu
     if workspace is None:
         workspace = torch.empty(nt_paged_tree_attn_workspace_bytes(H, pages.H_kv, d, max_new), dtype=torch.uint8,
                                 device=q.device)
-    st = lib().nt_selftest_paged_tree_attn(int(kernel), ctypes.byref(pages.c), _ptr(q), H * d, T, H, _ptr(cu_seqlens), B,
+    st = lib().nt_selftest_paged_tree_attn(int(kernel), int(cluster), ctypes.byref(pages.c), _ptr(q), H * d, T, H, _ptr(cu_seqlens), B,
                                            int(max_new), _ptr(block_table), block_table.shape[1], _ptr(lengths),
                                            _ptr(bits), d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse),
                                            _ptr(workspace), workspace.nbytes, _stream(stream))
