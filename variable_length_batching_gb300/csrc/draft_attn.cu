@@ -112,6 +112,8 @@ DraftBatch draft_batch(const DraftProblem& p, int rows, int groups, unsigned int
   a.heads = min(a.G, rows);
   a.hgroups = (a.G + a.heads - 1) / a.heads;
   a.tokens = max(1, rows / a.heads) * groups;
+  // units are counted in tiles of 32 keys at least, with at most 16 more to an item
+  a.few = p.B <= kPlanFew && (double)p.B * draft_items_most(a) * ((double)a.cap / 32 + 17) < 2e9;
   a.status = status;
   return a;
 }

@@ -34,6 +34,7 @@ struct Cfg {
   static constexpr uint32_t kSide = kKeys * kRow;
   static constexpr uint32_t kScratch = kBf16 ? 0 : kRows * kRow + kRows * (kKeys + 4) * 4;   // queries, probabilities
   static constexpr uint32_t kSmem = 4 * kSide + kScratch;
+  static constexpr int kPerSm = kSmem <= 110 * 1024 ? 2 : 1;       // CTAs
 };
 
 struct RowsArgs {
@@ -50,13 +51,13 @@ struct RowsArgs {
 };
 
 struct Shared {
-  PagedPlan plan;
+  DraftPlanSums plan;
   int64_t off[2][kKeys];       // byte offsets in the pool of a tile's rows, -1 none
   unsigned long long bad;      // keys of the tile with values that are not finite
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__((Cfg<T, D>::kThreads)) draft_rows_kernel(const RowsArgs p) {
+__global__ void __launch_bounds__((Cfg<T, D>::kThreads), (Cfg<T, D>::kPerSm)) draft_rows_kernel(const RowsArgs p) {
   using C = Cfg<T, D>;
   using W = Rows<T, D>;
   constexpr int kThreads = C::kThreads, kChunks = D * (int)sizeof(T) / 16;
@@ -66,9 +67,9 @@ __global__ void __launch_bounds__((Cfg<T, D>::kThreads)) draft_rows_kernel(const
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  draft_plan(a, kKeys, 1, blockIdx.x, gridDim.x, &sh.plan, kThreads);
+  const DraftPlan plan = draft_plan(a, kKeys, 1, blockIdx.x, gridDim.x, &sh.plan, kThreads);
   DraftWalk w;
-  w.init(a, sh.plan, kKeys, 1, p.whole);
+  w.init(a, plan, kKeys, 1, p.whole);
   const DraftPartials part = draft_partials(p.workspace, gridDim.x, kRows);
   int4 open = make_int4(-1, 0, 0, 0);
   const int64_t head_bytes = (int64_t)a.page_size * C::kRow;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__((Cfg<T, D>::kThreads)) draft_rows_kernel(const
       me.store_part(part.ml + slot * kRows * 2, part.o + slot * kRows * D);
     }
     if (w.begins && !w.ends)
-      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(sh.plan, 1, blockIdx.x, gridDim.x));
+      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, 1, blockIdx.x));
   }
   if (tid == 0) part.open[blockIdx.x] = open;
 }
@@ -160,7 +161,7 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   r.workspace = p.workspace;
   r.whole = false;
   r.scale_log2 = p.scale * 1.4426950408889634f;
-  const int per_sm = C::kSmem <= 110 * 1024 ? 2 : 1, ctas = min(per_sm * sm_count(), kPagedMaxCtas);
+  const int ctas = min(C::kPerSm * sm_count(), kPagedMaxCtas);
   cudaError_t e = allow_smem_once<draft_rows_kernel<T, D>>(C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(draft_rows_kernel<T, D>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, r);

@@ -58,7 +58,7 @@ struct Ctl {
   uint64_t full[16], empty[16], q_full[4], q_empty[4], red_full;
   float m[kConsumers][16], l[kConsumers][16];       // of a unit's rows
   unsigned int bad[2][kBadWords + 1];               // of two segments in turn: keys, and whether any
-  PagedPlan plan;
+  DraftPlanSums plan;
   int abort;
 };
 static_assert(sizeof(Ctl) <= 4096, "control block");
@@ -111,9 +111,10 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
   if (threadIdx.x == 64) prefetch_tmap(&vmap);
   pdl_wait();
   pdl_trigger();
-  draft_plan(a, kTile, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
+  __syncthreads();
+  const DraftPlan plan = draft_plan(a, kTile, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
   DraftWalk w;
-  w.init(a, ctl->plan, kTile, kE, p.whole);
+  w.init(a, plan, kTile, kE, p.whole);
 
   if (warp == kConsumers + kProducers) {
     // ---- query rows and mask words, item by item ----------------------------------
@@ -362,7 +363,7 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     if (threadIdx.x == 0)                             // everybody has read it; the segment after the next writes it
       for (int k = 0; k <= kBadWords; ++k) bad[k] = 0;
     if (w.begins && !w.ends)
-      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(ctl->plan, kE, blockIdx.x, gridDim.x));
+      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, kE, blockIdx.x));
     ++segs;
   }
   if (threadIdx.x == 0) part.open[blockIdx.x] = open;

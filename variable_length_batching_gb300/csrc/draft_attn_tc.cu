@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kFit = (int)((227 * 1024 - kCtl - kQBufs * kQ) / kTile);
   static constexpr int kK = kFit / 2, kV = kFit - kK;              // stages of keys and of values
   static constexpr uint32_t kSmem = kQBufs * kQ + (kK + kV) * kTile + kCtl;
-  static constexpr int kExtra = 1;                                 // an item's cost beside its tiles, in tiles
+  static constexpr int kExtra = D == 64 ? 3 : 2;                   // an item's cost beside its tiles, in tiles
   static_assert(kK >= 2 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -73,7 +73,7 @@ struct Ctl {
   int abort;
   unsigned int bad[3][kSpecial * 4 + 1];            // of three segments in turn: keys, and whether any
   float2 word[2][kRows];                            // maximum and sum of a row in a stream
-  PagedPlan plan;
+  DraftPlanSums plan;
 };
 static_assert(sizeof(Ctl) <= 3072, "control block");
 
@@ -85,6 +85,7 @@ struct TcArgs {
   void* workspace;
   bool whole;                     // items are not split
   int box;                        // keys per box: the largest power of two that divides page_size, 128 at most
+  int page_shift;                 // of a page_size that is a power of two, else -1
   float scale_log2;
 };
 
@@ -201,11 +202,12 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
   pdl_wait();
   pdl_trigger();
   tc_fence_before();
-  draft_plan(a, kKeys, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  const DraftPlan plan = draft_plan(a, kKeys, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
   DraftWalk w;
-  w.init(a, ctl->plan, kKeys, kE, p.whole);
+  w.init(a, plan, kKeys, kE, p.whole);
   const int tile_tokens = a.tokens / R;             // of a row tile
 
   if (warp == 9 || warp == 10) {
@@ -227,7 +229,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       // the table is read a tile ahead
       auto page_of = [&](int64_t t) {
         const uint32_t x = (uint32_t)t * kKeys + rb * p.box;
-        return mine && t < w.t1 && x < (uint32_t)w.seq.len ? row[x / ps] : -1;
+        return mine && t < w.t1 && x < (uint32_t)w.seq.len ? row[p.page_shift >= 0 ? x >> p.page_shift : x / ps] : -1;
       };
       int next = page_of(w.t0);
       if (!vals) {
@@ -259,7 +261,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, now));
         if (lane == 0) mbar_arrive_expect_tx(&full[st], count * p.box * 128);
         __syncwarp();
-        if (now) tma_load_3d(ring + st * C::kTile + dst, map, &full[st], half * 64, (int)(x % ps), z);
+        if (now) tma_load_3d(ring + st * C::kTile + dst, map, &full[st], half * 64, (int)(p.page_shift >= 0 ? x & (ps - 1) : x % ps), z);
       }
     }
     // no copy may land after the CTA is gone
@@ -574,7 +576,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free);
       if (w.begins && !w.ends)
-        open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(ctl->plan, kE, blockIdx.x, gridDim.x));
+        open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, kE, blockIdx.x));
       s0 += steps;
       tile0 += (uint32_t)(t_hi - t_lo);
       ++segs;
@@ -604,6 +606,9 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   r.whole = false;
   r.box = kKeys;
   while (p.pool.page_size % r.box) r.box >>= 1;
+  r.page_shift = -1;
+  for (int k = 0; k <= 16; ++k)
+    if (p.pool.page_size == 1 << k) r.page_shift = k;
   r.scale_log2 = p.scale * 1.4426950408889634f;
   CUtensorMap maps[3];
   {

@@ -27,6 +27,7 @@ struct DraftBatch {
   int H, G, Hkv;
   int heads, hgroups;       // query heads of an item, and groups of them to a key head
   int tokens;               // of an item
+  bool few;                 // few enough sequences and units for a warp to plan
   unsigned int* status;
 };
 
@@ -53,16 +54,91 @@ inline int draft_items_most(const DraftBatch& a) {
   return a.Hkv * a.hgroups * ((a.max_new + a.tokens - 1) / a.tokens);
 }
 __device__ __forceinline__ int draft_items(const DraftBatch& a, int n) {
-  return a.Hkv * a.hgroups * ((n + a.tokens - 1) / a.tokens);
+  return a.Hkv * a.hgroups * (n <= a.tokens ? 1 : (n + a.tokens - 1) / a.tokens);
 }
 __device__ __forceinline__ int64_t draft_units(const DraftBatch& a, const DraftSeq& s, int tile, int extra) {
   return s.n > 0 ? (paged_tiles(s.len, tile) + extra) * draft_items(a, s.n) : 0;
 }
 
+// The units of the call dealt out to n CTAs: CTA c has per of them, one more for
+// the first rem CTAs.
+struct DraftPlan {
+  int64_t total, per, rem;
+  int64_t lo, hi;           // this CTA's
+  int64_t start;            // first unit of sequence b0, which holds lo
+  int n, b0;
+  DraftSeq seq;             // sequence b0
+  __device__ __forceinline__ void deal(int64_t total_, int cta, int ctas) {
+    total = total_;
+    n = (int)min64(ctas, total);                   // with fewer units than CTAs the last ones get none
+    per = n ? paged_div(total, n) : 0;
+    rem = total - per * n;
+    lo = cta < n ? per * cta + min64(cta, rem) : total;
+    hi = cta < n ? lo + per + (cta < rem) : total;
+  }
+  // The CTA that has unit u.
+  __device__ __forceinline__ int cta_of(int64_t u) const {
+    const int64_t longer = rem * (per + 1);
+    return (int)(u < longer ? paged_div(u, per + 1) : rem + paged_div(u - longer, per));
+  }
+};
+struct DraftPlanSums {
+  int64_t warp_sum[32];
+  int64_t start;
+  int b0;
+};
+
+// By a warp alone, without a barrier: batches of at most 128 sequences whose
+// units are below 2^31 (a.few).  Every lane gets the plan.
+constexpr int kPlanFew = 128;
+__device__ __forceinline__ DraftPlan draft_plan_warp(const DraftBatch& a, int tile, int extra, int cta, int ctas,
+                                                     unsigned int* status) {
+  const int lane = threadIdx.x & 31, strip = (a.B + 31) >> 5, b_lo = lane * strip;
+  DraftSeq q[kPlanFew / 32];
+  int u[kPlanFew / 32], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanFew / 32; ++k) {
+    u[k] = 0;
+    if (k < strip && b_lo + k < a.B) {
+      q[k] = draft_seq(a, b_lo + k, status);
+      u[k] = (int)draft_units(a, q[k], tile, extra);
+    }
+    sum += u[k];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += o;
+  }
+  DraftPlan p;
+  p.deal(__shfl_sync(0xffffffffu, inc, 31), cta, ctas);
+  int at = inc - sum, b = -1;
+  DraftSeq s = {0, 0, 0};
+  const int lo = (int)p.lo;
+#pragma unroll
+  for (int k = 0; k < kPlanFew / 32; ++k) {
+    if (b < 0 && lo >= at && lo < at + u[k]) {
+      b = b_lo + k;
+      s = q[k];
+    } else if (b < 0) {
+      at += u[k];
+    }
+  }
+  const unsigned int who = __ballot_sync(0xffffffffu, b >= 0);
+  const int from = who ? __ffs(who) - 1 : 0;
+  p.b0 = __shfl_sync(0xffffffffu, b, from);
+  p.start = __shfl_sync(0xffffffffu, at, from);
+  p.seq.first = __shfl_sync(0xffffffffu, s.first, from);
+  p.seq.len = __shfl_sync(0xffffffffu, s.len, from);
+  p.seq.n = __shfl_sync(0xffffffffu, s.n, from);
+  return p;
+}
+
 // Every thread of the CTA calls this (nthreads a multiple of 32, at most
 // 1024); as paged_plan.
-__device__ __forceinline__ void draft_plan(const DraftBatch& a, int tile, int extra, int cta, int ctas, PagedPlan* s,
-                                           int nthreads) {
+__device__ __forceinline__ DraftPlan draft_plan_cta(const DraftBatch& a, int tile, int extra, int cta, int ctas,
+                                                    DraftPlanSums* s, int nthreads) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = nthreads >> 5;
   const int strip = (a.B + nthreads - 1) / nthreads;
   const int b_lo = (int)min64(a.B, (int64_t)tid * strip), b_hi = (int)min64(a.B, (int64_t)b_lo + strip);
@@ -82,27 +158,31 @@ __device__ __forceinline__ void draft_plan(const DraftBatch& a, int tile, int ex
     if (w < warp) before += x;
     total += x;
   }
-  const int64_t n = paged_ctas(total, ctas), c = min64(cta, n), c1 = min64(cta + 1, n);
-  const int64_t lo = paged_first(total, n, c);
+  DraftPlan p;
+  p.deal(total, cta, ctas);
   int64_t at = before + inc - sum;
-  if (lo >= at && lo < at + sum) {
+  if (p.lo >= at && p.lo < at + sum) {
     int b = b_lo;
     if (strip > 1) {
       for (; b < b_hi; ++b) {
         const int64_t w = draft_units(a, draft_seq(a, b, nullptr), tile, extra);
-        if (lo < at + w) break;
+        if (p.lo < at + w) break;
         at += w;
       }
     }
     s->b0 = b;
     s->start = at;
   }
-  if (tid == 0) {
-    s->total = total;
-    s->lo = lo;
-    s->hi = paged_first(total, n, c1);
-  }
   __syncthreads();
+  p.b0 = s->b0;
+  p.start = s->start;
+  if (p.lo < p.hi) p.seq = draft_seq(a, p.b0, nullptr);
+  return p;
+}
+__device__ __forceinline__ DraftPlan draft_plan(const DraftBatch& a, int tile, int extra, int cta, int ctas,
+                                                DraftPlanSums* s, int nthreads) {
+  if (a.few) return draft_plan_warp(a, tile, extra, cta, ctas, threadIdx.x < 32 ? a.status : nullptr);
+  return draft_plan_cta(a, tile, extra, cta, ctas, s, nthreads);
 }
 
 // What an item of a sequence is.
@@ -148,7 +228,7 @@ struct DraftWalk {
     next_len = there ? a.lengths[b + 1] : 0;
   }
   __device__ __forceinline__ void sequence(const DraftBatch& a, int tile, int extra) {
-    groups = (cur.n + a.tokens - 1) / a.tokens;
+    groups = cur.n <= a.tokens ? 1 : (cur.n + a.tokens - 1) / a.tokens;
     items = a.Hkv * a.hgroups * groups;
     units = (int)paged_tiles(cur.len, tile) + extra;
   }
@@ -162,21 +242,25 @@ struct DraftWalk {
       }
     }
   }
-  __device__ __forceinline__ void init(const DraftBatch& a, const PagedPlan& s, int tile, int extra, bool whole_items) {
+  __device__ __forceinline__ void init(const DraftBatch& a, const DraftPlan& s, int tile, int extra, bool whole_items) {
     whole = whole_items;
     left = s.hi - s.lo;
     if (left <= 0) return;
     b = s.b0;
-    cur = draft_seq(a, b, nullptr);
+    cur = s.seq;
     load_next(a);
     sequence(a, tile, extra);
     const int64_t off = s.lo - s.start;
-    item = (int)paged_div(off, units);
-    unit = (int)(off - (int64_t)item * units);
-    const int head = item / groups;
-    group = item - head * groups;
-    kvh = head / a.hgroups;
-    hgroup = head - kvh * a.hgroups;
+    item = kvh = hgroup = group = 0;
+    unit = (int)off;
+    if (off >= units) {
+      item = (int)paged_div(off, units);
+      unit = (int)(off - (int64_t)item * units);
+      const int head = item / groups;
+      group = item - head * groups;
+      kvh = head / a.hgroups;
+      hgroup = head - kvh * a.hgroups;
+    }
     if (whole && unit > 0) {
       left -= units - unit;
       unit = 0;
@@ -211,10 +295,9 @@ struct DraftWalk {
     } while (t1 <= t0);                   // nothing but the item's extra units
     return true;
   }
-  // CTAs that take tiles of the current segment's item, where it begins and does not end; as PagedWalk::parts
-  __device__ __forceinline__ int parts(const PagedPlan& s, int extra, int cta, int ctas) const {
-    const int64_t n = paged_ctas(s.total, ctas), e = s.hi + units - (t1 + extra);
-    return (int)paged_div(e * n + s.total - 1, s.total) - cta;
+  // CTAs that take tiles of the current segment's item, where it begins and does not end (so the range ends inside it)
+  __device__ __forceinline__ int parts(const DraftPlan& s, int extra, int cta) const {
+    return s.cta_of(s.hi + units - (t1 + extra) - 1) - cta + 1;
   }
 };
 
