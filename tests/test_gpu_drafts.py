@@ -115,8 +115,8 @@ def test_tree_attn(nt, shape, dtype, kind):
     ctx, ns, page, H, Hk, d = SHAPES[shape]
     c = make_case(ctx, ns, page, H, Hk, d, dtype, kind, seed=shape)
     check(c, *call(nt, c))
-    takes = {0: True, 1: dtype == BF and d > 32 and page % 8 == 0 and H // Hk <= 128, 2: dtype == BF and page % 8 == 0,
-             3: True}
+    takes = {0: True, 1: dtype == BF and d > 32 and page % 8 == 0 and H // Hk <= 128,
+             2: dtype == BF and d < 128 and page % 8 == 0, 3: True}
     for kernel in (0, 1, 2, 3):
         got = call_kernel(nt, c, kernel)
         assert (got is not None) == takes[kernel]

@@ -6,82 +6,151 @@
 // tokens, and of these the ones that the tree's mask names (without one:
 // itself and those before it).
 #include "draft_plan.cuh"
+#include "tc_ptx.cuh"
 
 namespace nt {
 namespace {
 
-// One CTA per (CTA of the split, eight rows): joins the item that CTA began
-// and left unfinished, whose rest is the slots 0 of the CTAs after it.  A warp
-// has a row, a lane D / 32 columns of it; partials are added in order with a
-// running maximum, eight loads at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) draft_join_kernel(const DraftBatch a, int ctas, int rows, void* workspace,
-                                                         T* o, float* lse) {
-  constexpr int kCols = D / 32, kBatch = 8;
+// Joins the items that CTAs of the split began and left unfinished: the rest of
+// CTA c0's is the slots 0 of the CTAs after it.  A lane has four columns of a
+// row, so a warp takes 128 / D rows at once; partials are added in order with a
+// running maximum, kBatch loads at a time.  L2's latency bounds it.  kShared:
+// a CTA's warps share rows, each with an eighth of their partials, and
+// blockIdx.x counts the unfinished items; for few rows of few items, which have
+// many partials each.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+struct JoinRow {
+  static constexpr int kBatch = 4;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float mi, float li, const float4& v) {
+    const float mn = fmaxf(m, mi), base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - base), fi = exp2f(mi - base);
+    m = mn;
+    l = l * f + li * fi;
+    acc.x = acc.x * f + v.x * fi;
+    acc.y = acc.y * f + v.y * fi;
+    acc.z = acc.z * f + v.z * fi;
+    acc.w = acc.w * f + v.w * fi;
+  }
+  // Partials [from, to) of a row at these columns: partial i is slot 1 of c0, then slot 0 of c0 + i.
+  __device__ __forceinline__ void partials(const DraftPartials& part, int c0, int rows, int row, int col, int from,
+                                           int to) {
+    for (int i0 = from; i0 < to; i0 += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < to) {
+          const int64_t s = (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + row;
+          ml[k] = *reinterpret_cast<const float2*>(part.ml + s * 2);
+          v[k] = *reinterpret_cast<const float4*>(part.o + s * D + col);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) add(ml[k].x, ml[k].y, v[k]);
+    }
+  }
+};
+
+template <typename T, int D, bool kShared>
+__global__ void __launch_bounds__(kJoinWarps * 32, kShared ? 4 : 6) draft_join_kernel(const DraftBatch a, int ctas, int rows,
+                                                                        void* workspace, T* o, float* lse) {
+  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;
+  __shared__ int which;
+  __shared__ float4 sv[kJoinWarps][32];
+  __shared__ float2 sml[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
   const DraftPartials part = draft_partials(workspace, ctas, rows);
-  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % kLanes * 4;
+  int c0 = blockIdx.x;
+  if constexpr (kShared) {                          // the blockIdx.x-th CTA that left one
+    constexpr int kMost = kPagedMaxCtas / (kJoinWarps * 32);
+    __shared__ int counts[kMost * kJoinWarps];
+    unsigned int left[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int c = k * kJoinWarps * 32 + threadIdx.x;
+      left[k] = __ballot_sync(0xffffffffu, c < ctas && part.open[c].x >= 0);
+      if (lane == 0) counts[k * kJoinWarps + warp] = __popc(left[k]);
+    }
+    if (threadIdx.x == 0) which = -1;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      int rank = __popc(left[k] & ((1u << lane) - 1));
+      for (int w = 0; w < k * kJoinWarps + warp; ++w) rank += counts[w];
+      if ((left[k] >> lane & 1) && rank == (int)blockIdx.x) which = k * kJoinWarps * 32 + threadIdx.x;
+    }
+    __syncthreads();
+    c0 = which;
+    if (c0 < 0) return;
+  }
   const int4 open = part.open[c0];
   if (open.x < 0 || open.x >= a.B) return;
   const DraftSeq seq = draft_seq(a, open.x, nullptr);
   const DraftItem it = draft_item(a, seq.n, open.y, open.z);
-  const int row = blockIdx.y * 8 + warp;
-  if (row >= it.ni * it.nh) return;
-  const int n = min(open.w, ctas - c0);            // partial i: slot 1 of c0, then slot 0 of c0 + i
-  float m = -INFINITY, l = 0.f, acc[kCols] = {};
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    float2 ml[kBatch];
-    float v[kBatch][kCols];
+  const int n = min(open.w, ctas - c0), all = it.ni * it.nh;
+  const int row = (kShared ? blockIdx.y : blockIdx.y * kJoinWarps + warp) * kAtOnce + lane / kLanes;
+  JoinRow<D> r;
+  if constexpr (kShared) {
+    const int share = (n + kJoinWarps - 1) / kJoinWarps;
+    if (row < all) r.partials(part, c0, rows, row, col, min(n, warp * share), min(n, (warp + 1) * share));
+    sv[warp][lane] = r.acc;
+    sml[warp][lane] = make_float2(r.m, r.l);
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k;
-      ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) v[k][c] = 0.f;
-      if (i < n) {
-        const int64_t s = (int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + row;
-        ml[k] = *reinterpret_cast<const float2*>(part.ml + s * 2);
-        const float* from = part.o + s * D + kCols * lane;
-        if constexpr (kCols == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(from);
-          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-        } else if constexpr (kCols == 2) {
-          const float2 x = *reinterpret_cast<const float2*>(from);
-          v[k][0] = x.x, v[k][1] = x.y;
-        } else {
-          v[k][0] = *from;
-        }
-      }
+      for (int w = 1; w < kJoinWarps; ++w) r.add(sml[w][lane].x, sml[w][lane].y, sv[w][lane]);
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float mn = fmaxf(m, ml[k].x), base = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m - base), fi = exp2f(ml[k].x - base);
-      m = mn;
-      l = l * f + ml[k].y * fi;
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[c] = acc[c] * f + v[k][c] * fi;
-    }
+    if (warp > 0) return;
+  } else if (row < all) {
+    r.partials(part, c0, rows, row, col, 0, n);
   }
+  if (row >= all) return;
   const int i = it.i0 + row / it.nh, h = it.kvh * a.G + it.h0 + row % it.nh;
   const int64_t t = (int64_t)seq.first + i;
   const bool any = draft_sees_any(a, seq, i);
-  T* to = o + (t * a.H + h) * D + kCols * lane;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) to[c] = from_f32<T>(any ? acc[c] / l : 0.f);
-  if (lse && lane == 0) lse[(int64_t)h * a.T + t] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  T* to = o + (t * a.H + h) * D + col;
+  const float out[4] = {any ? r.acc.x / r.l : 0.f, any ? r.acc.y / r.l : 0.f, any ? r.acc.z / r.l : 0.f,
+                        any ? r.acc.w / r.l : 0.f};
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(tc::pack_bf16x2(out[0], out[1]), tc::pack_bf16x2(out[2], out[3]));
+  } else {
+    *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[2], out[3]);
+  }
+  if (lse && col == 0) lse[(int64_t)h * a.T + t] = any ? (r.m + log2f(r.l)) * 0.6931471805599453f : -INFINITY;
 }
 
+template <typename T, int D>
+cudaError_t join_d(const DraftBatch& a, int ctas, int rows, void* ws, void* o, float* lse, cudaStream_t s) {
+  constexpr int kAtOnce = 128 / D;
+  const int most = min(a.tokens, a.max_new) * a.heads;     // rows of any item
+  const int64_t items = (int64_t)a.B * draft_items_most(a);
+  T* out = static_cast<T*>(o);
+  // Sixteen partials or more to an item, in rows that leave warps without one.
+  // Two items of 48 and more partials, 53 rows of d = 128: the call 21.8 us,
+  // 18.4 so; below sixteen the search for the item costs as much (12 items of 13: 0.8 us more).
+  const int64_t shared = items * ((most + kAtOnce - 1) / kAtOnce);
+  if (items * 16 <= ctas && shared <= 4 * ctas)
+    return launch_pdl(draft_join_kernel<T, D, true>, dim3((unsigned)items, (most + kAtOnce - 1) / kAtOnce),
+                      dim3(kJoinWarps * 32), 0, s, a, ctas, rows, ws, out, lse);
+  const int y = (most + kAtOnce * kJoinWarps - 1) / (kAtOnce * kJoinWarps);
+  return launch_pdl(draft_join_kernel<T, D, false>, dim3(ctas, y), dim3(kJoinWarps * 32), 0, s, a, ctas, rows, ws, out,
+                    lse);
+}
 template <typename T>
 cudaError_t join(const DraftBatch& a, int d, int ctas, int rows, void* ws, void* o, float* lse, cudaStream_t s) {
-  const int most = min(a.tokens, a.max_new) * a.heads;     // rows of any item
-  const dim3 grid(ctas, (most + 7) / 8), block(256);
-  T* out = static_cast<T*>(o);
   switch (d) {
-    case 32: return launch_pdl(draft_join_kernel<T, 32>, grid, block, 0, s, a, ctas, rows, ws, out, lse);
-    case 64: return launch_pdl(draft_join_kernel<T, 64>, grid, block, 0, s, a, ctas, rows, ws, out, lse);
-    default: return launch_pdl(draft_join_kernel<T, 128>, grid, block, 0, s, a, ctas, rows, ws, out, lse);
+    case 32: return join_d<T, 32>(a, ctas, rows, ws, o, lse, s);
+    case 64: return join_d<T, 64>(a, ctas, rows, ws, o, lse, s);
+    default: return join_d<T, 128>(a, ctas, rows, ws, o, lse, s);
   }
 }
 
@@ -124,11 +193,67 @@ cudaError_t launch_draft_join(nt_dtype dt, const DraftBatch& a, int d, int ctas,
                        : join<float>(a, d, ctas, rows, workspace, o, lse, s);
 }
 
+namespace {
+
+// Rates of a kernel that deals tiles of keys out to `ctas` CTAs, and the
+// estimated time (us) of a call: what it costs whatever it does, and a CTA's
+// share of the tiles and of the items.
+struct Rates {
+  double first, tile, item;
+};
+double split_us(const DraftProblem& p, int rows, int groups, int keys, int ctas, const Rates& r) {
+  const DraftBatch a = draft_batch(p, rows, groups, nullptr);
+  const double items = p.B * draft_items_mean(p, a), tiles = items * (draft_mean_keys(p, a) / keys + 0.5);
+  return r.first + fmax(tiles / ctas, 1) * r.tile + items / ctas * r.item;
+}
+
+}  // namespace
+
+double draft_mean_keys(const DraftProblem& p, const DraftBatch& a) { return p.B == 1 ? a.cap : 0.4 * a.cap; }
+double draft_items_mean(const DraftProblem& p, const DraftBatch& a) {
+  const double heads = (double)a.Hkv * a.hgroups, n = (double)p.T / p.B, most = (p.max_new + a.tokens - 1) / a.tokens;
+  return heads * (most <= 1 || n >= p.max_new ? most : fmin(most, fmax(1, n / a.tokens + 0.5)));
+}
+
+// The call takes the kernel with the least estimated time.  Lengths are on the
+// device, so the estimates go by what the host knows: the tables' size (one
+// sequence fills its table, several 0.4 of it), the tokens and the heads.  The
+// rates were fitted to 2,500 random calls of up to 128 sequences, on which this
+// choice costs 1 to 3% over the best kernel of each (geometric mean; without the
+// spread kernel 11 to 24%, the tensor-memory kernel 14 to 18 at d = 64 and 128,
+// the slices 2.2 at d = 32 and 0.8 at 64, the rows kernel 3 to 7 in bf16 and 27
+// to 51 in fp32).
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
+  constexpr Rates kRowsRates[2][3] = {{{7.3, 1.85, 2.9}, {8.2, 2.5, 3.0}, {8.3, 4.0, 4.5}},
+                                      {{6.5, 5.4, 5.9}, {7.1, 8.9, 5.8}, {1.3, 18.0, 16.3}}};
+  constexpr Rates kTcRates[2][2] = {{{11.0, 1.08, 2.5}, {14.9, 2.2, 5.5}}, {{11.2, 1.6, 2.4}, {17.7, 3.1, 6.5}}};
+  constexpr Rates kSliceRates[2][3] = {{{7.8, 0.52, 1.7}, {7.8, 0.99, 1.7}, {7.8, 1.75, 1.7}},
+                                       {{8.9, 0.40, 2.1}, {8.9, 0.58, 2.1}, {8.9, 1.47, 2.1}}};
+  const int sms = min(sm_count(), kPagedMaxCtas), w = p.d == 32 ? 0 : p.d == 64 ? 1 : 2;
   const int64_t rows = (int64_t)p.max_new * (p.H / p.pool.H);
-  const bool tc = draft_tc_supported(dt, p);
-  if (draft_slices_supported(dt, p) && (rows <= 64 || !tc)) return launch_draft_slices(p, status, s);
-  return tc ? launch_draft_tc(p, status, s) : launch_draft_rows(dt, p, status, s);
+  int cluster;
+  double best = draft_spread_us(dt, p, &cluster);
+  enum { kSpread, kRowsOf64, kTc, kSlices } kernel = kSpread;
+  auto consider = [&](decltype(kernel) k, double us) {
+    if (us >= best) return;
+    best = us;
+    kernel = k;
+  };
+  consider(kRowsOf64, split_us(p, 64, 1, 64, 2 * sms, kRowsRates[dt != NT_BF16][w]));
+  if (draft_tc_supported(dt, p)) {
+    const int two = rows > 128;
+    consider(kTc, split_us(p, 128, 1 + two, 128, sms, kTcRates[p.d == 128][two]));
+  }
+  if (draft_slices_supported(dt, p)) {
+    const int g = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+    consider(kSlices, split_us(p, 16 << g, 1, w ? 64 : 128, sms, kSliceRates[w][g]));
+  }
+  switch (kernel) {
+    case kSpread: return launch_draft_spread(dt, p, cluster, status, s);
+    case kTc: return launch_draft_tc(p, status, s);
+    case kSlices: return launch_draft_slices(p, status, s);
+    default: return launch_draft_rows(dt, p, status, s);
+  }
 }
 
 }  // namespace nt

@@ -46,7 +46,6 @@ struct RowsArgs {
   void* o;
   float* lse;
   void* workspace;
-  bool whole;
   float scale_log2;
 };
 
@@ -69,7 +68,7 @@ __global__ void __launch_bounds__((Cfg<T, D>::kThreads), (Cfg<T, D>::kPerSm)) dr
   pdl_trigger();
   const DraftPlan plan = draft_plan(a, kKeys, 1, blockIdx.x, gridDim.x, &sh.plan, kThreads);
   DraftWalk w;
-  w.init(a, plan, kKeys, 1, p.whole);
+  w.init(a, plan, kKeys, 1);
   const DraftPartials part = draft_partials(p.workspace, gridDim.x, kRows);
   int4 open = make_int4(-1, 0, 0, 0);
   const int64_t head_bytes = (int64_t)a.page_size * C::kRow;
@@ -159,7 +158,6 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   r.o = p.o;
   r.lse = p.lse;
   r.workspace = p.workspace;
-  r.whole = false;
   r.scale_log2 = p.scale * 1.4426950408889634f;
   const int ctas = min(C::kPerSm * sm_count(), kPagedMaxCtas);
   cudaError_t e = allow_smem_once<draft_rows_kernel<T, D>>(C::kSmem);

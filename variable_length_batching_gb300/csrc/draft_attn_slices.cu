@@ -69,7 +69,6 @@ struct SliceArgs {
   bf16* o;
   float* lse;
   void* workspace;
-  bool whole;                     // items are not split
   int box;                        // keys per box
   float scale_log2;
 };
@@ -114,7 +113,7 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
   __syncthreads();
   const DraftPlan plan = draft_plan(a, kTile, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
   DraftWalk w;
-  w.init(a, plan, kTile, kE, p.whole);
+  w.init(a, plan, kTile, kE);
 
   if (warp == kConsumers + kProducers) {
     // ---- query rows and mask words, item by item ----------------------------------
@@ -378,7 +377,6 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   r.o = static_cast<bf16*>(p.o);
   r.lse = p.lse;
   r.workspace = p.workspace;
-  r.whole = false;
   r.box = C::kTile < 64 ? C::kTile : 64;
   while (p.pool.page_size % r.box) r.box >>= 1;
   r.scale_log2 = p.scale * 1.4426950408889634f;
@@ -402,7 +400,7 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   cudaError_t e = allow_smem_once<draft_slices_kernel<D, RG>>(C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(draft_slices_kernel<D, RG>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[2], maps[0], maps[1], r);
-  if (e != cudaSuccess || r.whole) return e;
+  if (e != cudaSuccess) return e;
   return launch_draft_join(NT_BF16, r.a, D, ctas, C::kRows, p.workspace, p.o, p.lse, s);
 }
 
@@ -416,12 +414,11 @@ cudaError_t run_d(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
 }  // namespace
 
 bool draft_slices_supported(nt_dtype dt, const DraftProblem& p) {
-  return dt == NT_BF16 && p.pool.page_size % 8 == 0 && p.pool.n_pages > 0;
+  return dt == NT_BF16 && p.d <= 64 && p.pool.page_size % 8 == 0 && p.pool.n_pages > 0;
 }
 
 cudaError_t launch_draft_slices(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
-  if (p.d == 32) return run_d<32>(p, status, s);
-  return p.d == 64 ? run_d<64>(p, status, s) : run_d<128>(p, status, s);
+  return p.d == 32 ? run_d<32>(p, status, s) : run_d<64>(p, status, s);
 }
 
 }  // namespace nt

@@ -392,14 +392,22 @@ cudaError_t run(const DraftProblem& p, int cluster, unsigned int* status, cudaSt
   return cudaLaunchKernelEx(&cfg, draft_spread_kernel<T, D>, r);
 }
 
-// Estimated time (us) and the cluster's size, from the tables' sizes; as
-// paged_attn_spread.cu's.
+// Estimated time (us) and the cluster's size.  A cluster's time beside its
+// slices of keys, a warp's slice while it waits for no other, a further wave of
+// clusters, and a slice of every resident warp where the SMs are full; fitted
+// with the other kernels' rates (draft_attn.cu).
 template <typename T, int D>
 double estimate(const DraftProblem& p, int* cluster) {
   using C = Cfg<T, D>;
-  const double first = 5.0, t = C::kBf16 ? 1.35 : (D == 128 ? 2.5 : D == 64 ? 2.0 : 1.4);
+  constexpr int w = D == 32 ? 0 : D == 64 ? 1 : 2;
+  constexpr double kFirst = C::kBf16 ? (w == 0 ? 5.9 : w == 1 ? 6.7 : 8.4) : (w == 0 ? 7.9 : w == 1 ? 7.7 : 8.9);
+  constexpr double kSlice = C::kBf16 ? (w == 0 ? 0.85 : w == 1 ? 0.97 : 1.22) : (w == 0 ? 1.9 : w == 1 ? 2.4 : 1.9);
+  constexpr double kWave = C::kBf16 ? (w == 0 ? 4.1 : w == 1 ? 4.3 : 5.6) : (w == 0 ? 6.3 : w == 1 ? 5.2 : 5.5);
+  constexpr double kLoaded = C::kBf16 ? (w == 0 ? 1.06 : w == 1 ? 2.1 : 2.9) : (w == 0 ? 2.4 : w == 1 ? 3.4 : 4.2);
   const DraftBatch a = draft_batch(p, C::kRows, 1, nullptr);
   const int64_t items = (int64_t)p.B * draft_items_most(a), slices = (a.cap + 15) / 16;
+  const double all = p.B * draft_items_mean(p, a) * (draft_mean_keys(p, a) / 16 + 0.5);
+  const double load = all / (2.0 * sm_count() * C::kWarps) * kLoaded;
   double best = INFINITY;
   *cluster = 1;
   int dev = 64;                                                      // 64: asked for every time
@@ -410,7 +418,7 @@ double estimate(const DraftProblem& p, int* cluster) {
     if (fit <= 0) continue;
     const double waves = (double)((items + fit - 1) / fit);
     const double rounds = fmax(1, (double)((slices + c * C::kWarps - 1) / (c * C::kWarps)));
-    const double more = (rounds - 1) * t, us = first + more * (p.B > 1 ? 1.25 : 1) + (waves - 1) * (5.3 + more);
+    const double us = kFirst + fmax((rounds - 1) * kSlice, load) + (waves - 1) * kWave;
     if (us < best) {
       best = us;
       *cluster = c;

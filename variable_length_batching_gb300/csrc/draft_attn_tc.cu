@@ -83,7 +83,6 @@ struct TcArgs {
   void* o;
   float* lse;
   void* workspace;
-  bool whole;                     // items are not split
   int box;                        // keys per box: the largest power of two that divides page_size, 128 at most
   int page_shift;                 // of a page_size that is a power of two, else -1
   float scale_log2;
@@ -207,7 +206,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
   const uint32_t tmem = ctl->tmem_base;
   const DraftPlan plan = draft_plan(a, kKeys, kE, blockIdx.x, gridDim.x, &ctl->plan, kThreads);
   DraftWalk w;
-  w.init(a, plan, kKeys, kE, p.whole);
+  w.init(a, plan, kKeys, kE);
   const int tile_tokens = a.tokens / R;             // of a row tile
 
   if (warp == 9 || warp == 10) {
@@ -603,7 +602,6 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   r.o = p.o;
   r.lse = p.lse;
   r.workspace = p.workspace;
-  r.whole = false;
   r.box = kKeys;
   while (p.pool.page_size % r.box) r.box >>= 1;
   r.page_shift = -1;
@@ -627,7 +625,7 @@ cudaError_t run(const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   cudaError_t e = allow_smem_once<draft_tc_kernel<D, R>>(C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(draft_tc_kernel<D, R>, dim3(ctas), dim3(kThreads), C::kSmem, s, maps[0], maps[1], maps[2], r);
-  if (e != cudaSuccess || r.whole) return e;
+  if (e != cudaSuccess) return e;
   return launch_draft_join(NT_BF16, r.a, D, ctas, R * kRows, p.workspace, p.o, p.lse, s);
 }
 

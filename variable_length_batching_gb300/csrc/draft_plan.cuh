@@ -206,7 +206,6 @@ __device__ __forceinline__ DraftItem draft_item(const DraftBatch& a, int n, int 
 
 // Walks a CTA's range segment by segment; as PagedWalk.
 struct DraftWalk {
-  bool whole;
   int64_t left;           // units of the range not yet handed out
   int b, item, items;
   DraftSeq cur;
@@ -242,8 +241,7 @@ struct DraftWalk {
       }
     }
   }
-  __device__ __forceinline__ void init(const DraftBatch& a, const DraftPlan& s, int tile, int extra, bool whole_items) {
-    whole = whole_items;
+  __device__ __forceinline__ void init(const DraftBatch& a, const DraftPlan& s, int tile, int extra) {
     left = s.hi - s.lo;
     if (left <= 0) return;
     b = s.b0;
@@ -261,11 +259,6 @@ struct DraftWalk {
       kvh = head / a.hgroups;
       hgroup = head - kvh * a.hgroups;
     }
-    if (whole && unit > 0) {
-      left -= units - unit;
-      unit = 0;
-      step_item(a);
-    }
   }
   __device__ __forceinline__ bool next(const DraftBatch& a, int tile, int extra) {
     do {
@@ -279,7 +272,7 @@ struct DraftWalk {
         item = group = hgroup = kvh = 0;
         sequence(a, tile, extra);
       }
-      const int end = whole ? units : (int)min64(units, unit + left);
+      const int end = (int)min64(units, unit + left);
       seg_b = b;
       seg_item = item;
       seg_items = items;

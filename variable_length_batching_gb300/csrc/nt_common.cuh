@@ -476,14 +476,17 @@ struct DraftProblem {
 struct DraftBatch;
 // The batch for items of up to `rows` rows times `groups`.
 DraftBatch draft_batch(const DraftProblem& p, int rows, int groups, unsigned int* status);
+// For estimates from what the host knows: keys of a sequence and its items, on average.
+double draft_mean_keys(const DraftProblem& p, const DraftBatch& a);
+double draft_items_mean(const DraftProblem& p, const DraftBatch& a);
 size_t draft_workspace_bytes(int d);
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s);
 // bf16 at d = 64 and 128, pages of a multiple of 8 positions, at most 128
 // query heads to a key head.
 bool draft_tc_supported(nt_dtype dt, const DraftProblem& p);
 cudaError_t launch_draft_tc(const DraftProblem& p, unsigned int* status, cudaStream_t s);
-// bf16, pages of a multiple of 8 positions, few rows (64 of them read the keys
-// once).
+// bf16 at d = 32 and 64, pages of a multiple of 8 positions, few rows (64 of
+// them read the keys once).
 bool draft_slices_supported(nt_dtype dt, const DraftProblem& p);
 cudaError_t launch_draft_slices(const DraftProblem& p, unsigned int* status, cudaStream_t s);
 // A cluster of CTAs per item, any page size and type; its estimated time in us.
