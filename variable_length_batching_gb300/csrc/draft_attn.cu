@@ -218,36 +218,38 @@ double draft_items_mean(const DraftProblem& p, const DraftBatch& a) {
 // The call takes the kernel with the least estimated time.  Lengths are on the
 // device, so the estimates go by what the host knows: the tables' size (one
 // sequence fills its table, several 0.4 of it), the tokens and the heads.  The
-// rates were fitted to 2,500 random calls of up to 128 sequences, on which this
+// rates were fitted to 4,000 random calls of up to 128 sequences, on which this
 // choice costs 1 to 3% over the best kernel of each (geometric mean; without the
-// spread kernel 11 to 24%, the tensor-memory kernel 14 to 18 at d = 64 and 128,
-// the slices 2.2 at d = 32 and 0.8 at 64, the rows kernel 3 to 7 in bf16 and 27
-// to 51 in fp32).
+// spread kernel 7 to 16%, the tensor-memory kernel 14 to 16 at d = 64 and 128,
+// the slices 1.6 at d = 32 and 0.7 at 64, the rows kernel 4 in bf16 and 35 to 51
+// in fp32).
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
-  constexpr Rates kRowsRates[2][3] = {{{7.3, 1.85, 2.9}, {8.2, 2.5, 3.0}, {8.3, 4.0, 4.5}},
-                                      {{6.5, 5.4, 5.9}, {7.1, 8.9, 5.8}, {1.3, 18.0, 16.3}}};
-  constexpr Rates kTcRates[2][2] = {{{11.0, 1.08, 2.5}, {14.9, 2.2, 5.5}}, {{11.2, 1.6, 2.4}, {17.7, 3.1, 6.5}}};
-  constexpr Rates kSliceRates[2][3] = {{{7.8, 0.52, 1.7}, {7.8, 0.99, 1.7}, {7.8, 1.75, 1.7}},
-                                       {{8.9, 0.40, 2.1}, {8.9, 0.58, 2.1}, {8.9, 1.47, 2.1}}};
+  constexpr Rates kRowsBf16[3] = {{7.2, 1.75, 2.9}, {7.7, 2.4, 3.0}, {8.5, 3.85, 4.6}};
+  constexpr Rates kRowsF32[3][3] = {{{7.6, 2.1, 4.7}, {7.6, 3.2, 4.7}, {7.6, 5.5, 4.7}},
+                                    {{7.9, 3.25, 5.3}, {7.9, 5.3, 5.3}, {7.9, 9.2, 5.3}},
+                                    {{9.1, 3.95, 6.2}, {9.1, 5.6, 6.2}, {9.1, 9.3, 6.2}}};
+  constexpr Rates kTcRates[2][2] = {{{10.9, 1.06, 2.4}, {13.8, 2.1, 6.5}}, {{11.0, 1.7, 2.5}, {17.3, 3.1, 7.1}}};
+  constexpr Rates kSliceRates[2][3] = {{{7.8, 0.53, 2.3}, {7.8, 0.92, 2.3}, {7.8, 1.66, 2.3}},
+                                       {{8.2, 0.40, 2.5}, {8.2, 0.59, 2.5}, {8.2, 1.58, 2.5}}};
   const int sms = min(sm_count(), kPagedMaxCtas), w = p.d == 32 ? 0 : p.d == 64 ? 1 : 2;
   const int64_t rows = (int64_t)p.max_new * (p.H / p.pool.H);
+  const int group = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
   int cluster;
   double best = draft_spread_us(dt, p, &cluster);
-  enum { kSpread, kRowsOf64, kTc, kSlices } kernel = kSpread;
+  enum { kSpread, kRows, kTc, kSlices } kernel = kSpread;
   auto consider = [&](decltype(kernel) k, double us) {
     if (us >= best) return;
     best = us;
     kernel = k;
   };
-  consider(kRowsOf64, split_us(p, 64, 1, 64, 2 * sms, kRowsRates[dt != NT_BF16][w]));
+  if (dt == NT_BF16) consider(kRows, split_us(p, 64, 1, 64, 2 * sms, kRowsBf16[w]));
+  else consider(kRows, split_us(p, 16 << group, 1, 64, p.d == 128 ? sms : 2 * sms, kRowsF32[w][group]));
   if (draft_tc_supported(dt, p)) {
     const int two = rows > 128;
     consider(kTc, split_us(p, 128, 1 + two, 128, sms, kTcRates[p.d == 128][two]));
   }
-  if (draft_slices_supported(dt, p)) {
-    const int g = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
-    consider(kSlices, split_us(p, 16 << g, 1, w ? 64 : 128, sms, kSliceRates[w][g]));
-  }
+  if (draft_slices_supported(dt, p))
+    consider(kSlices, split_us(p, 16 << group, 1, w ? 64 : 128, sms, kSliceRates[w][group]));
   switch (kernel) {
     case kSpread: return launch_draft_spread(dt, p, cluster, status, s);
     case kTc: return launch_draft_tc(p, status, s);

@@ -8,8 +8,8 @@
 // of slots filled row by row with cp.async; the warps' results are merged in
 // the CTA, and the CTAs' through distributed shared memory.  A sequence has as
 // many items as max_new may need; clusters whose tokens are not there leave at
-// once.  One context of 777 keys, eight tokens and 12 heads of 64: 5.0 us, 9.7
-// on the kernels that deal tiles out.
+// once.  One context of 777 keys, eight tokens and 12 heads of 64: 6.2 us, 9.7
+// to 11.5 on the kernels that deal tiles out.
 #include <atomic>
 #include <type_traits>
 
@@ -400,10 +400,10 @@ template <typename T, int D>
 double estimate(const DraftProblem& p, int* cluster) {
   using C = Cfg<T, D>;
   constexpr int w = D == 32 ? 0 : D == 64 ? 1 : 2;
-  constexpr double kFirst = C::kBf16 ? (w == 0 ? 5.9 : w == 1 ? 6.7 : 8.4) : (w == 0 ? 7.9 : w == 1 ? 7.7 : 8.9);
-  constexpr double kSlice = C::kBf16 ? (w == 0 ? 0.85 : w == 1 ? 0.97 : 1.22) : (w == 0 ? 1.9 : w == 1 ? 2.4 : 1.9);
-  constexpr double kWave = C::kBf16 ? (w == 0 ? 4.1 : w == 1 ? 4.3 : 5.6) : (w == 0 ? 6.3 : w == 1 ? 5.2 : 5.5);
-  constexpr double kLoaded = C::kBf16 ? (w == 0 ? 1.06 : w == 1 ? 2.1 : 2.9) : (w == 0 ? 2.4 : w == 1 ? 3.4 : 4.2);
+  constexpr double kFirst = C::kBf16 ? (w == 0 ? 5.8 : w == 1 ? 6.7 : 8.6) : (w == 0 ? 8.0 : w == 1 ? 7.6 : 9.1);
+  constexpr double kSlice = C::kBf16 ? (w == 0 ? 0.82 : w == 1 ? 1.06 : 1.14) : (w == 0 ? 1.7 : w == 1 ? 1.84 : 2.27);
+  constexpr double kWave = C::kBf16 ? (w == 0 ? 3.6 : w == 1 ? 4.2 : 6.1) : (w == 0 ? 4.5 : w == 1 ? 5.3 : 5.4);
+  constexpr double kLoaded = C::kBf16 ? (w == 0 ? 1.35 : w == 1 ? 2.4 : 3.05) : (w == 0 ? 3.8 : w == 1 ? 3.6 : 4.3);
   const DraftBatch a = draft_batch(p, C::kRows, 1, nullptr);
   const int64_t items = (int64_t)p.B * draft_items_most(a), slices = (a.cap + 15) / 16;
   const double all = p.B * draft_items_mean(p, a) * (draft_mean_keys(p, a) / 16 + 0.5);

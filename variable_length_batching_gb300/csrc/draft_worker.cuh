@@ -51,12 +51,13 @@ __device__ __forceinline__ float row_lse(float m, float l, bool any) {
   return any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <typename T, int D>
+// kGroups groups of threads have the same 64 / kGroups rows and as many of the tile's keys each.
+template <typename T, int D, int kGroups = 1>
 struct Rows;
 
 // bf16: warp w has rows 16 w to 16 w + 15; a lane two of them, g and g + 8.
 template <int D>
-struct Rows<bf16, D> {
+struct Rows<bf16, D, 1> {
   uint32_t qa[D / 16][4];
   float m[2], l[2], o[D / 8][4];
   int g, tq, row0;
@@ -67,6 +68,7 @@ struct Rows<bf16, D> {
     tq = lane & 3;
     row0 = (threadIdx.x >> 5) * 16;
   }
+  __device__ __forceinline__ void merge(float*) {}
   __device__ __forceinline__ void load_q(const bf16* q, int64_t stride, int64_t token, int head, int ni, int nh) {
     const uint32_t* at[2];
 #pragma unroll
@@ -225,21 +227,24 @@ struct Rows<bf16, D> {
 
 // fp32: thread (y, x) of 16 x 16 has rows 4 y to 4 y + 3, of the scores the
 // keys x + 16 j, of the outputs the columns kVec x + 16 kVec i.
-template <int D>
-struct Rows<float, D> {
-  static constexpr int kVec = D == 32 ? 2 : 4, kParts = D / (16 * kVec), kStride = 68;
+template <int D, int kGroups>
+struct Rows<float, D, kGroups> {
+  static constexpr int kM = 64 / kGroups, kJ = 4 / kGroups;          // rows; keys of a thread
+  static constexpr int kVec = D == 32 ? 2 : 4, kParts = D / (16 * kVec), kStride = kM + 4;
   float m[4], l[4], o[4][D / 16];
   float *qs, *ps;
-  int y, x;
+  int y, x, group, key0;
 
   __device__ __forceinline__ explicit Rows(void* scratch) {
     qs = static_cast<float*>(scratch);
-    ps = qs + 64 * D;
-    y = threadIdx.x >> 4;
+    ps = qs + kM * D + (threadIdx.x >> 4) * 4 * kStride;
+    y = (threadIdx.x >> 4) % (kM / 4);
+    group = (threadIdx.x >> 4) / (kM / 4);
+    key0 = group * kM;
     x = threadIdx.x & 15;
   }
   __device__ __forceinline__ void load_q(const float* q, int64_t stride, int64_t token, int head, int ni, int nh) {
-    for (int e = threadIdx.x; e < 64 * (D / 4); e += 256) {
+    for (int e = threadIdx.x; e < kM * (D / 4); e += 256) {
       const int row = e / (D / 4), c = e % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < ni * nh)
@@ -258,17 +263,23 @@ struct Rows<float, D> {
                                        const uint8_t* ks_, const uint8_t* vs_, int64_t x0, bool all, float scale_log2) {
     const int rows = it.ni * it.nh;
     if ((y & ~1) * 4 >= rows) return;                       // the whole warp's rows
-    float2 s2[4][4];
+    uint64_t see[4];                                        // read while the scores are computed
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * y + r;
+      see[r] = all ? ~0ull : row < rows ? draft_sees(a, seq, it.i0 + row / it.nh, x0) : 0;
+    }
+    float2 s2[4][kJ];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s2[r][j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < kJ; ++j) s2[r][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int c = 0; c < D / 4; ++c) {
-      float4 kq[4], qq[4];
+      float4 kq[kJ], qq[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = x + 16 * j;
+      for (int j = 0; j < kJ; ++j) {
+        const int key = key0 + x + 16 * j;
         kq[j] = *reinterpret_cast<const float4*>(ks_ + swizzled<D * 4>(key, c));
       }
 #pragma unroll
@@ -276,20 +287,17 @@ struct Rows<float, D> {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kJ; ++j) {
           ffma2(qq[r].x, qq[r].y, kq[j].x, kq[j].y, s2[r][j].x, s2[r][j].y, s2[r][j].x, s2[r][j].y);
           ffma2(qq[r].z, qq[r].w, kq[j].z, kq[j].w, s2[r][j].x, s2[r][j].y, s2[r][j].x, s2[r][j].y);
         }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 4 * y + r;
-      uint64_t see = ~0ull;
-      if (!all) see = row < rows ? draft_sees(a, seq, it.i0 + row / it.nh, x0) : 0;
-      float s[4], mx = -INFINITY;
+      float s[kJ], mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = all || (see >> (x + 16 * j) & 1) ? (s2[r][j].x + s2[r][j].y) * scale_log2 : -INFINITY;
+      for (int j = 0; j < kJ; ++j) {
+        s[j] = all || (see[r] >> (key0 + x + 16 * j) & 1) ? (s2[r][j].x + s2[r][j].y) * scale_log2 : -INFINITY;
         mx = fmaxf(mx, s[j]);
       }
 #pragma unroll
@@ -299,10 +307,10 @@ struct Rows<float, D> {
       m[r] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kJ; ++j) {
         s[j] = ex2_approx(s[j] - base);
         sum += s[j];
-        ps[row * kStride + x + 16 * j] = s[j];
+        ps[r * kStride + x + 16 * j] = s[j];
       }
       l[r] = l[r] * corr + sum;
 #pragma unroll
@@ -310,13 +318,13 @@ struct Rows<float, D> {
     }
     __syncwarp();                                           // a warp reads the rows that it wrote
 #pragma unroll 2
-    for (int k4 = 0; k4 < 16; ++k4) {
+    for (int k4 = 0; k4 < kM / 4; ++k4) {
       float4 pr[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pr[r] = *reinterpret_cast<const float4*>(ps + (4 * y + r) * kStride + 4 * k4);
+      for (int r = 0; r < 4; ++r) pr[r] = *reinterpret_cast<const float4*>(ps + r * kStride + 4 * k4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int key = 4 * k4 + k;
+        const int key = key0 + 4 * k4 + k;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           const int col = kVec * x + 16 * kVec * i;
@@ -343,6 +351,7 @@ struct Rows<float, D> {
   }
   __device__ __forceinline__ void add_bad(const DraftBatch& a, const DraftSeq& seq, const DraftItem& it, int64_t x0,
                                        uint64_t bad, const uint8_t* v, const int64_t* off) {
+    if constexpr (kGroups > 1) bad &= ((1ull << kM) - 1) << key0;
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * y + r;
       if (row >= it.ni * it.nh) continue;
@@ -360,20 +369,53 @@ struct Rows<float, D> {
 #pragma unroll
       for (int k = 1; k < 16; k <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
   }
+  // The groups' results into the first one's; `red` has room for 64 rows.
+  __device__ __forceinline__ void merge(float* red) {
+    sum_up();
+    if constexpr (kGroups > 1) {
+      float2* ml = reinterpret_cast<float2*>(red + 64 * D);
+      if (group > 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = group * kM + 4 * y + r;
+          put(red + at * D, r, 1.f);
+          if (x == 0) ml[at] = make_float2(m[r], l[r]);
+        }
+      }
+      __syncthreads();
+      if (group > 0) return;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        for (int k = 1; k < kGroups; ++k) {
+          const int at = k * kM + 4 * y + r;
+          const float2 other = ml[at];
+          const float mn = fmaxf(m[r], other.x), base = mn == -INFINITY ? 0.f : mn;
+          const float f = ex2_approx(m[r] - base), fo = ex2_approx(other.x - base);
+          m[r] = mn;
+          l[r] = l[r] * f + other.y * fo;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            o[r][c] = o[r][c] * f + red[at * D + kVec * x + 16 * kVec * (c / kVec) + c % kVec] * fo;
+        }
+    }
+  }
   __device__ __forceinline__ void put(float* row, int r, float f) const {
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) row[kVec * x + 16 * kVec * (c / kVec) + c % kVec] = o[r][c] * f;
   }
   __device__ __forceinline__ void store(const DraftBatch& a, const DraftSeq& seq, const DraftItem& it, float* out,
                                         float* lse) {
-    sum_up();
+    if (group > 0) return;
+    bool sees_any[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sees_any[r] = 4 * y + r < it.ni * it.nh && draft_sees_any(a, seq, it.i0 + (4 * y + r) / it.nh);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * y + r;
       if (row >= it.ni * it.nh) continue;
       const int i = row / it.nh, h = it.kvh * a.G + it.h0 + row % it.nh;
       const int64_t t = (int64_t)seq.first + it.i0 + i;
-      const bool any = draft_sees_any(a, seq, it.i0 + i);
+      const bool any = sees_any[r];
       if (!any)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
@@ -382,7 +424,7 @@ struct Rows<float, D> {
     }
   }
   __device__ __forceinline__ void store_part(float* ml, float* po) {
-    sum_up();
+    if (group > 0) return;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * y + r;
