@@ -883,10 +883,11 @@ def nt_selftest_paged_attn(kernel: int, pages: KVPages, q: torch.Tensor, block_t
 def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu_seqlens: torch.Tensor,
                                 block_table: torch.Tensor, lengths: torch.Tensor, max_new: int,
                                 bits: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                                cluster: int = 0, workspace: Optional[torch.Tensor] = None, stream=None):
+                                cluster: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None):
     """nt_paged_tree_attn by kernel 0 (the general one), 1 (in tensor
     memory), 2 (few rows) or 3 (a cluster of CTAs per item, ``cluster`` of
-    them or as the call would), for tests of each; contiguous tensors.  Returns (o, lse)."""
+    them or as the call would), for tests of each; all but q contiguous.  Returns (o, lse)."""
     T, H, d = q.shape
     B = cu_seqlens.numel() - 1
     if q.dtype != pages.dtype or any(t.dtype != torch.int32 for t in (cu_seqlens, block_table, lengths)):
@@ -895,16 +896,22 @@ def nt_selftest_paged_tree_attn(kernel: int, pages: KVPages, q: torch.Tensor, cu
         raise ValueError("q must be (tokens, H, d) with the pages' d, block_table (B, max_pages), lengths (B)")
     if bits is not None and (bits.dtype != torch.int64 or tuple(bits.shape) != (T, -(-max_new // 64))):
         raise ValueError("bits must be int64 (tokens, ceil(max_new / 64))")
-    o, lse = torch.empty_like(q), torch.empty(H, T, dtype=torch.float32, device=q.device)
+    if not q.is_cuda or q.stride(2) != 1 or q.stride(1) != d:
+        raise ValueError("q must be a CUDA tensor, its heads contiguous")
+    if out is None:
+        out = torch.empty(T, H, d, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(H, T, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = torch.empty(nt_paged_tree_attn_workspace_bytes(H, pages.H_kv, d, max_new), dtype=torch.uint8,
                                 device=q.device)
-    st = lib().nt_selftest_paged_tree_attn(int(kernel), int(cluster), ctypes.byref(pages.c), _ptr(q), H * d, T, H, _ptr(cu_seqlens), B,
+    st = lib().nt_selftest_paged_tree_attn(int(kernel), int(cluster), ctypes.byref(pages.c),
+                                           ctypes.c_void_p(q.data_ptr()), q.stride(0), T, H, _ptr(cu_seqlens), B,
                                            int(max_new), _ptr(block_table), block_table.shape[1], _ptr(lengths),
-                                           _ptr(bits), d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse),
+                                           _ptr(bits), d ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
                                            _ptr(workspace), workspace.nbytes, _stream(stream))
     _check(st, "nt_selftest_paged_tree_attn")
-    return o, lse
+    return out, lse
 
 
 def nt_pair_block_fused(part: Partition, s_left: torch.Tensor, s_right: torch.Tensor, w, W3=None, b3=None,

@@ -1,4 +1,5 @@
-"""A paged key/value cache for answering one token at a time.
+"""A paged key/value cache for answering one token at a time, or several that
+were drafted.
 
 :class:`PageTable` is the host side: which pages hold which sequence, what is
 free, what is shared.  Sequences are added, extended, forked (the copy shares
@@ -9,12 +10,17 @@ data itself: what has to be copied comes back as a list of pages.
 :class:`PagedCache` joins it with the pages on the device (``nt.KVPages``) and
 the library's calls: a step names its sequences and how many tokens each
 gains, writes their keys and values (``nt_paged_write``) and attends with one
-query token per sequence (``nt_paged_attn``); forks and compaction copy pages
-(``nt_paged_copy``).
+query token per sequence (``nt_paged_attn``), or with all the step's tokens, a
+tree of drafted ones or a piece of a prompt (``nt_paged_tree_attn``), of which it
+then keeps the accepted ones (``nt_paged_keep``); forks and compaction copy
+pages (``nt_paged_copy``).
+
+:class:`DevicePagedCache` has its table on the device: no step waits for the
+host, and a captured one follows the lengths from replay to replay.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
@@ -114,6 +120,20 @@ class PageTable:
                 self.refs[pages[-1]] += 1
                 self._drop(dst)
 
+    def shorten(self, seqs: Sequence[int], lengths: Sequence[int]) -> None:
+        """``seqs`` (distinct) cut to ``lengths``; pages that no position is
+        left in are given up."""
+        if len(seqs) != len(lengths) or len(set(seqs)) != len(seqs):
+            raise ValueError("one length per sequence, each sequence once")
+        for s, n in zip(seqs, lengths):
+            self._known(s)
+            if not 0 <= n <= self.length[s]:
+                raise ValueError(f"sequence {s} has {self.length[s]} positions, not {n}")
+        for s, n in zip(seqs, lengths):
+            self.length[s] = n
+            while len(self.pages[s]) > -(-n // self.page_size):
+                self._drop(self.pages[s].pop())
+
     def fork(self, seq: int) -> int:
         """A new sequence with the same positions, sharing ``seq``'s pages."""
         self._known(seq)
@@ -157,6 +177,8 @@ class Step:
     block_table: torch.Tensor    # [B, max_pages]
     max_new: int                 # longest of the new segments
     tokens: int                  # new tokens of all of them
+    counts: List[int] = field(default_factory=list)      # and of each
+    after: List[int] = field(default_factory=list)       # positions of each with the step's, as the host has them
 
 
 class PagedCache:
@@ -237,7 +259,7 @@ class PagedCache:
         with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
         return Step(seqs, arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
-                    arr[head:].view(B, width), max(counts + [0]), cu[-1])
+                    arr[head:].view(B, width), max(counts + [0]), cu[-1], counts, after)
 
     def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """The step's new keys and values, packed (tokens, H_kv, d): all of
@@ -249,3 +271,99 @@ class PagedCache:
     def attend(self, step: Step, q: torch.Tensor, scale: Optional[float] = None, stream=None) -> torch.Tensor:
         """One query token per sequence, q (B, H, d), over all its positions."""
         return nt.nt_paged_attn(self.pages, q, step.block_table, step.lengths, scale=scale, stream=stream)[0]
+
+    def attend_tree(self, step: Step, q: torch.Tensor, bits: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """All the step's tokens as queries, packed q (tokens, H, d): each over
+        the positions before the step and those of its sequence's new tokens
+        that ``bits`` (nt_draft_tree's) names; None: itself and those before
+        it."""
+        if q.shape[0] != step.tokens:
+            raise ValueError(f"the step has {step.tokens} new tokens, q has {q.shape[0]}")
+        return nt.nt_paged_tree_attn(self.pages, q, step.cu_seqlens, step.block_table, step.lengths, step.max_new,
+                                     bits=bits, scale=scale, stream=stream)[0]
+
+    def keep(self, step: Step, kept: Sequence[Sequence[int]], stream=None) -> None:
+        """Of the step's tokens only ``kept``: for each of its sequences the
+        accepted ones' numbers in the step, growing.  Their keys and values
+        move up, the rest of the step's positions are given up.  The step has
+        to be the last one of its sequences.  Not while a graph is being
+        captured."""
+        on = self._on(stream, "a step's positions are given up")
+        t, ps = self.table, self.table.page_size
+        if len(kept) != len(step.seqs) or len(step.counts) != len(step.seqs):
+            raise ValueError("one list of kept tokens per sequence")
+        flat, cu, lengths = [], [0], []
+        for s, n, after, ks in zip(step.seqs, step.counts, step.after, kept):
+            t._known(s)
+            ks = [int(k) for k in ks]
+            if t.length[s] != after:
+                raise ValueError(f"sequence {s} has changed since the step")
+            if any(k < 0 or k >= n for k in ks) or any(a >= b for a, b in zip(ks, ks[1:])):
+                raise ValueError(f"kept tokens of sequence {s}: growing numbers below {n}")
+            first = after - n
+            if any(k != i and t.refs[t.pages[s][(first + i) // ps]] > 1 for i, k in enumerate(ks)):
+                raise ValueError(f"sequence {s} was forked since the step")
+            flat += ks
+            cu.append(len(flat))
+            lengths.append(first + len(ks))
+        if any(k != i - cu[b] for b in range(len(kept)) for i, k in enumerate(flat[cu[b]:cu[b + 1]], cu[b])):
+            host = torch.tensor(cu + flat, dtype=torch.int32).pin_memory()
+            with torch.cuda.stream(on):
+                arr = host.to(self.pages.device, non_blocking=True)
+            nt.nt_paged_keep(self.pages, arr[len(cu):], arr[:len(cu)], step.block_table, step.pos0, stream=stream)
+        t.shorten(step.seqs, lengths)
+
+
+class DevicePagedCache:
+    """A paged cache of ``rows`` sequences whose block table, lengths and free
+    pages are on the device, for steps that never wait for the host, captured
+    ones among them.  A drafted step is
+
+        cu, pos0, slots, lacking = cache.resize(cache.lengths + counts, tokens)
+        bits, positions = nt.nt_draft_tree(parents, cu, max_new, pos0)
+        cache.write(k, v, slots)
+        o = cache.attend_tree(q, cu, max_new, bits)
+        cache.keep(kept, cu_kept, pos0)        # the accepted tokens
+        cache.resize(pos0 + n_kept)
+
+    with tensors on the device throughout.  Calls go in order on one stream:
+    each changes what the next one reads."""
+
+    def __init__(self, rows: int, max_pages: int, n_pages: int, page_size: int, H_kv: int, d: int,
+                 dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        shape = (n_pages, H_kv, page_size, d)
+        self.pages = nt.KVPages(torch.empty(shape, dtype=dtype, device=device),
+                                torch.empty(shape, dtype=dtype, device=device))
+        self.page_size = page_size
+        self.block_table = torch.full((rows, max_pages), -1, dtype=torch.int32, device=device)
+        self.lengths = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)   # from the end
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+
+    def resize(self, new_lengths: torch.Tensor, tokens: int = 0, stream=None):
+        """Every row brought to new_lengths (rows): (cu_seqlens, pos0, slots,
+        lacking) of the tokens that rows gain, as nt_paged_resize; where
+        ``lacking`` is not 0 nothing has changed."""
+        return nt.nt_paged_resize(self.block_table, self.lengths, self.free_pages, self.n_free, self.page_size,
+                                  new_lengths, tokens, stream=stream)
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """The gained tokens' keys and values, packed (tokens, H_kv, d)."""
+        nt.nt_paged_write_slots(self.pages, k, v, slots, stream=stream)
+
+    def attend(self, q: torch.Tensor, scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """One query token per row, q (rows, H, d), over all its positions."""
+        return nt.nt_paged_attn(self.pages, q, self.block_table, self.lengths, scale=scale, stream=stream)[0]
+
+    def attend_tree(self, q: torch.Tensor, cu_seqlens: torch.Tensor, max_new: int,
+                    bits: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """The gained tokens as queries, packed q (tokens, H, d), as
+        nt_paged_tree_attn."""
+        return nt.nt_paged_tree_attn(self.pages, q, cu_seqlens, self.block_table, self.lengths, max_new, bits=bits,
+                                     scale=scale, stream=stream)[0]
+
+    def keep(self, kept: torch.Tensor, cu_kept: torch.Tensor, pos0: torch.Tensor, stream=None) -> None:
+        """The accepted tokens' keys and values moved up behind pos0, as
+        nt_paged_keep; resize() then gives up the others'."""
+        nt.nt_paged_keep(self.pages, kept, cu_kept, self.block_table, pos0, stream=stream)
