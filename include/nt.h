@@ -937,7 +937,8 @@ size_t nt_paged_tree_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d, in
  *                 bytes, 16-byte aligned.
  * Softmax statistics and sums are fp32; in bf16 a probability multiplies the
  * values as the sum of two bf16, 2^-15 of it at most away from it.  Results do
- * not depend on scheduling; their rounding may depend on B and max_new.
+ * not depend on scheduling; their rounding may depend on the sizes of the call
+ * (B, T, max_new, max_pages, H, the page size), by which a kernel is chosen.
  * Asynchronous; nothing is read on the host, so a captured call follows
  * lengths, offsets and masks from replay to replay.
  */
@@ -988,13 +989,13 @@ nt_status nt_selftest_paged_attn(int32_t kernel, int32_t cluster, const nt_kv_pa
  * nt_selftest_paged_tree_attn -- nt_paged_tree_attn by a kernel that the
  * caller names, for tests of each: 0 the general one, 1 the one in tensor
  * memory (bf16, d 64 or 128, pages of a multiple of 8, at most 128 query heads
- * to a key head), 2 the one of few rows (bf16, pages of a multiple of 8), 3 a
- * cluster of CTAs per item (`cluster` of them, in [1, 12], or 0 for the call's
- * own estimate).
+ * to a key head), 2 the one of few rows (bf16, d 32 or 64, pages of a multiple
+ * of 8), 3 a cluster of CTAs per item (`cluster` of them, in [1, 12], or 0 for
+ * the call's own estimate).
  * NT_ERR_UNSUPPORTED where the kernel does not take the call.
  */
-nt_status nt_selftest_paged_tree_attn(int32_t kernel, int32_t cluster, const nt_kv_pages* pages, const void* q, int64_t q_stride,
-                                      int64_t T, int32_t H, const int32_t* d_cu_seqlens, int32_t B, int32_t max_new,
+nt_status nt_selftest_paged_tree_attn(int32_t kernel, int32_t cluster, const nt_kv_pages* pages, const void* q,
+                                      int64_t q_stride, int64_t T, int32_t H, const int32_t* d_cu_seqlens, int32_t B, int32_t max_new,
                                       const int32_t* d_block_table, int32_t max_pages, const int32_t* d_lengths,
                                       const int64_t* d_bits, float scale, void* o, float* lse, void* workspace,
                                       size_t workspace_bytes, void* stream);

@@ -1,5 +1,6 @@
 // Attention of drafted tokens over a paged cache, few rows to a key head (up to
-// 64 of tokens times query heads): bf16, pages of a multiple of 8 positions.
+// 64 of tokens times query heads): bf16 at d = 32 and 64, pages of a multiple of 8
+// positions.
 //
 // Up to some 50 rows the cache's bytes are the bound even for mma.sync, which
 // does 983 multiply-adds a cycle here (a key and its value take 3 d of them
@@ -10,9 +11,11 @@
 // 16 rows with a running maximum, sum and output of their own in registers;
 // no warp waits for another until the end of a segment, where their results are
 // merged.  The tensor-memory kernel (draft_attn_tc.cu) has 128 rows to a tile,
-// and two hand-offs between warps for every 128 keys; it takes over where more
-// rows than 64 pay for that (152 contexts of 8,000 keys, 16 rows: d = 64 69 us
-// there, d = 128 103).
+// and two hand-offs between warps for every 128 keys: it costs more where rows
+// are few (152 contexts of 8,000 keys, d = 64, 16 rows: 69 us there, 56 here; 32
+// rows 69 and 80), but has no d = 32 (44 us here, 105 on the general kernel), and at
+// d = 128 it was the faster one (64 contexts of up to 8,192 keys, up to 16 rows: 95 us
+// against 122).
 //
 // RG row groups of 16 (1, 2 or 4) share the eight warps with 8 / RG slices of
 // the keys.  A row's mask words are fetched with the queries.  Values that are
@@ -34,7 +37,7 @@ template <int D, int RG>
 struct Cfg {
   static constexpr int kRows = 16 * RG;
   static constexpr int kUnits = kConsumers / RG;              // warps of one row group
-  static constexpr int kTile = D == 32 ? 128 : D == 128 && RG == 4 ? 32 : 64;      // keys of a stage, 16 KB or so
+  static constexpr int kTile = D == 32 ? 128 : 64;            // keys of a stage, 16 KB
   static constexpr int kSlices = kTile / 16;
   static constexpr int kGroups = kUnits > kSlices ? kUnits / kSlices : 1;          // stages worked on at once
   static constexpr int kTurns = kUnits > kSlices ? 1 : kSlices / kUnits;           // slices of a stage to a warp
