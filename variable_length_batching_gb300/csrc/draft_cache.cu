@@ -285,9 +285,12 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
 // Kept token i of a sequence goes from position pos0 + kept[i] to pos0 + i.
 // The indices grow, so kept[i] >= i: a CTA that moves a run of tokens, all
 // read before any is written, and then the next run, reads nothing that it
-// has written.  CTAs have a sequence, a range of its heads and a side each.
+// has written.  CTAs have a sequence, a range of its heads and a side each; HBM
+// bounds a large batch (256 sequences, 35 tokens each of 8 heads of 256 bytes: 84 MB
+// in 17 us, four words in flight to a thread and 64 warps to an SM; eight and 32
+// took 20), the launch and four dependent loads a small one (16 sequences: 3.2).
 constexpr int kKeepThreads = 256;
-constexpr int kKeepUnroll = 8;
+constexpr int kKeepUnroll = 4;
 
 struct KeepArgs {
   uint8_t* pool[2];
@@ -309,7 +312,7 @@ __device__ __forceinline__ int64_t keep_offset(const KeepArgs& a, int b, int64_t
   return ((int64_t)id * a.H * a.page_size + (x - (int64_t)pg * a.page_size)) * a.row_bytes;
 }
 
-__global__ void __launch_bounds__(kKeepThreads, 4) paged_keep_kernel(const KeepArgs a) {
+__global__ void __launch_bounds__(kKeepThreads, 8) paged_keep_kernel(const KeepArgs a) {
   __shared__ int64_t from[kKeepThreads], to[kKeepThreads];
   pdl_wait();
   pdl_trigger();
@@ -437,7 +440,13 @@ cudaError_t launch_paged_keep(const PagedPool& p, const int32_t* kept, int64_t K
   a.row_bytes = p.row_bytes;
   a.B = B;
   a.max_pages = max_pages;
-  a.heads = min(p.H, max(1, kKeepThreads * kKeepUnroll / 64 * 16 / p.row_bytes));     // 64 tokens in flight
+  // Heads that make a run of what a sequence keeps on average: with fewer, short lists leave threads without work
+  // (246 sequences that keep one token of 12 heads of 512 bytes: 19.6 -> 3.9 us), with more, a list takes several
+  // runs.  Halved where that leaves SMs without a CTA.
+  const int64_t run = min64(64, (K + B - 1) / B);
+  const int64_t bytes = run * p.row_bytes;
+  a.heads = max(1, (int)min64(p.H, (kKeepThreads * kKeepUnroll * 16 + bytes / 2) / bytes));
+  while (a.heads > 1 && (int64_t)B * 2 * ((p.H + a.heads - 1) / a.heads) < 2 * sm_count()) a.heads = (a.heads + 1) / 2;
   while ((p.H + a.heads - 1) / a.heads > 32767) a.heads *= 2;
   a.status = status;
   const int groups = (p.H + a.heads - 1) / a.heads;
