@@ -334,3 +334,59 @@ def test_far_pages(nt, kernel, dtype, d):
         return
     nt.nt_device_status()
     check(c, o, lse)
+
+
+def test_calls_on_another_stream(nt):
+    """The calls of a drafted step queued on a side stream by argument, their
+    results allocated by the call."""
+    c = make_case([900, 3], [30, 8], 16, 8, 2, 64, BF, seed=2)
+    want = call(nt, c)[0]
+    kp, vp, q, table, bits = (c[k].to(DEV) for k in ("kp", "vp", "q", "table", "bits"))
+    cu, lens = _cu(c["ns"]), _i32(c["lens"])
+    parents = _i32([-1] * 38)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for _ in range(10):
+        got = nt.nt_paged_tree_attn(nt.KVPages(kp, vp), q, cu, table, lens, 30, bits=bits, stream=stream)[0]
+        own, pos = nt.nt_draft_tree(parents, cu, 30, stream=stream)
+        stream.synchronize()
+        assert torch.equal(got, want) and pos.tolist() == [0] * 38
+        assert own[:, 0].tolist() == [1 << i for i in range(30)] + [1 << i for i in range(8)]
+
+
+def test_binding_refusals(nt):
+    c = make_case([20, 3], [4, 2], 16, 4, 2, 64, BF, seed=2)
+    kp, vp, q, table, bits = (c[k].to(DEV) for k in ("kp", "vp", "q", "table", "bits"))
+    cu, lens, pages = _cu(c["ns"]), _i32(c["lens"]), nt.KVPages(kp, vp)
+    good = dict(q=q, cu=cu, table=table, lengths=lens, max_new=4, bits=bits)
+
+    def attend(**kw):
+        a = {**good, **kw}
+        extra = {k: a[k] for k in ("out", "lse", "workspace") if k in a}
+        return nt.nt_paged_tree_attn(pages, a["q"], a["cu"], a["table"], a["lengths"], a["max_new"], bits=a["bits"], **extra)
+
+    attend()
+    refused = [dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q.cpu()), dict(cu=cu.long()), dict(cu=cu[:2]),
+               dict(table=table.long()), dict(table=table[:1]), dict(table=table[0]), dict(lengths=lens[:1]),
+               dict(lengths=lens.float()), dict(bits=bits.int()), dict(bits=bits[:, :0]), dict(bits=bits[:3]),
+               dict(max_new=65), dict(max_new=-1), dict(max_new=257, bits=None), dict(out=torch.empty_like(q)[:3]),
+               dict(out=torch.empty_like(q).float()), dict(lse=torch.empty(4, 5, device=DEV)),
+               dict(workspace=torch.empty(16, dtype=torch.uint8, device=DEV)), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))]
+    for kw in refused:
+        with pytest.raises((ValueError, nt.NTError)):
+            attend(**kw)
+    kept, pos0 = _i32([0]), _i32([20, 3])
+    for call_ in (lambda: nt.nt_draft_tree(_i32([0] * 6).long(), cu, 4), lambda: nt.nt_draft_tree(_i32([-1] * 6), cu, 257),
+                  lambda: nt.nt_draft_tree(_i32([-1] * 6), cu, 0), lambda: nt.nt_draft_tree(_i32([-1] * 6), cu, 4, pos0[:1]),
+                  lambda: nt.nt_paged_keep(pages, kept.long(), _i32([0, 1, 1]), table, pos0),
+                  lambda: nt.nt_paged_keep(pages, kept, _i32([0, 1]), table, pos0),
+                  lambda: nt.nt_paged_keep(pages, kept, _i32([0, 1, 1]), table.cpu(), pos0),
+                  lambda: nt.nt_paged_write_slots(pages, kp[0].transpose(0, 1), kp[0].transpose(0, 1), torch.zeros(3, dtype=torch.int64, device=DEV)),
+                  lambda: nt.nt_paged_write_slots(pages, kp[:2, :, 0], vp[:2, :, 0], _i32([0, 1])),
+                  lambda: nt.nt_paged_resize(table, lens, _i32([0]), _i32([0]), 0, lens, 0),
+                  lambda: nt.nt_paged_resize(table, lens, _i32([0]), _i32([0]), 16, lens[:1], 0),
+                  lambda: nt.nt_paged_resize(table, lens.long(), _i32([0]), _i32([0]), 16, lens, 0),
+                  lambda: nt.nt_paged_resize(table, lens, _i32([0]), _i32([0]), 16, lens, -1)):
+        with pytest.raises((ValueError, nt.NTError)):
+            call_()
+    nt.nt_device_status()
