@@ -4,23 +4,29 @@
 // Work, split and partial results as draft_plan.cuh says.  An item has up to
 // 64 rows (tokens times query heads of one key head); a tile is 64 keys, whose
 // rows are fetched one by one through the block table with cp.async, a tile
-// ahead.  Each row keeps a running maximum, sum and output:
+// ahead; their pages are looked up two tiles ahead.  Each row keeps a running
+// maximum, sum and output:
 //   S = Q K^T,  m' = max(m, scale S),  P = 2^(scale S - m'),
 //   l = l 2^(m - m') + sum P,  O = O 2^(m - m') + P V
 // with the scores that a row does not see at -infinity.  bf16: matrix products
 // of 16 rows a warp, P as the sum of two bf16 (one would be off by 2^-8 of P,
-// which shows in the output).  fp32: packed multiply-adds, 4 x 4 scores and 4
-// x D / 16 outputs to a thread; with 32 rows or fewer, groups of threads take
-// a half or a quarter of a tile's keys each and merge their results at the end.
-// Barriers around each tile's fetch leave 27% of the issue slots busy.  fp32, 13
-// contexts of 5,120 keys, 24 rows to a key head, d = 64: 154 us; a page's place is
-// looked up two tiles ahead, masks before the scores (13 ragged contexts of up to
-// 5,000: 36.5 -> 33 us).
+// which shows in the output).  fp32: products of tf32 parts (draft_worker.cuh);
+// warps have 16 of 64, 32 or 16 rows and a half, a quarter or an eighth of a
+// tile's keys, and merge their results at the end.
+//
+// fp32, d = 64, 13 contexts of 5,120 keys, 24 rows to a key head: 123 us; packed
+// multiply-adds took 154 (three shared-memory cycles to each four multiply-adds of a
+// scheduler), most of the rest are the matrix instructions (32 x 64 x 64 x 2 of them three
+// times are 1,570 of a tile's 3,800 cycles).  bf16, d = 128, 152 contexts of 8,000, 64
+// rows: 203 us.  Whole rows by bulk copies were slower (a warp issues one every 100
+// cycles: bf16, d = 64, 110 us -> 161).
 //
 // A value that is not finite may stand at a key that only some of the rows
 // see, and 0 times it is not 0; such values are taken out of the tile and
 // added to the rows that do see them (only where new tokens are: older keys
 // are seen by all).
+#include <climits>
+
 #include "draft_plan.cuh"
 #include "draft_worker.cuh"
 
@@ -38,10 +44,10 @@ struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kThreads = kBf16 ? 128 : 256;
   static constexpr uint32_t kRow = D * sizeof(T);
-  static constexpr uint32_t kSide = kKeys * kRow;
-  static constexpr uint32_t kScratch = kBf16 ? 0 : kRows * kRow + 64 * (kKeys / kGroups + 4) * 4;   // queries, probabilities
+  static constexpr uint32_t kSide = kKeys * (kRow + 16);
+  static constexpr uint32_t kScratch = kBf16 ? 0 : 2 * kRows * kRow;        // two parts of the queries
   static constexpr uint32_t kSmem = 4 * kSide + kScratch;
-  static_assert(kGroups == 1 || (64 * D + 128) * 4 <= 4 * kSide, "results to merge");
+  static_assert(kBf16 || (128 * D + 256) * 4 <= 4 * kSide, "results to merge");
   static constexpr int kPerSm = kSmem <= 110 * 1024 ? 2 : 1;       // CTAs
 };
 
@@ -59,8 +65,8 @@ struct RowsArgs {
 
 struct Shared {
   DraftPlanSums plan;
-  int64_t off[3][kKeys];       // byte offsets in the pool of a tile's rows, -1 none
-  unsigned long long bad;      // keys of the tile with values that are not finite
+  int64_t off[2][kKeys];       // places in the pool of a tile's rows (of the next one's), -1 none
+  unsigned long long bad[2];   // keys of the tile (of the next one) with values that are not finite
 };
 
 template <typename T, int D, int kGroups>
@@ -83,76 +89,87 @@ __global__ void __launch_bounds__((Cfg<T, D, kGroups>::kThreads), (Cfg<T, D, kGr
   int4 open = make_int4(-1, 0, 0, 0);
   const int64_t head_bytes = (int64_t)a.page_size * C::kRow;
   W me(smem + 4 * C::kSide);
-
+  // The first 64 threads have a key of each tile: its page is looked up two tiles ahead, its place stored one ahead.
+  constexpr int kNone = INT_MIN;
+  auto page_of = [&](int t) {
+    const uint32_t x = (uint32_t)t * kKeys + tid;
+    return tid < kKeys && x < (uint32_t)w.seq.len
+               ? a.table[(int64_t)w.seg_b * a.max_pages + x / (uint32_t)a.page_size] : kNone;
+  };
+  auto place = [&](int t, int id) {
+    if (tid >= kKeys) return;
+    const uint32_t x = (uint32_t)t * kKeys + tid;
+    int64_t off = -1;
+    if ((unsigned)id < (unsigned)a.n_pages)
+      off = ((int64_t)id * a.Hkv + w.it.kvh) * head_bytes + (int64_t)(x % (uint32_t)a.page_size) * C::kRow;
+    else if (id != kNone)
+      flag_device(a.status, kDevCheck);
+    sh.off[t & 1][tid] = off;
+  };
+  // A thread has the same chunk of some rows, keys and values.
+  constexpr int kStep = kThreads / kChunks, kRowsEach = kKeys / kStep;
+  static_assert(kThreads % kChunks == 0 && kKeys % kStep == 0, "chunks of a thread");
+  const int my_row = tid / kChunks, chunk = tid % kChunks;
+  const uint32_t my_place = padded<C::kRow>(my_row, chunk);
+  auto fetch = [&](int t) {
+    const uint32_t to = smem_u32(smem) + (t & 1) * 2 * C::kSide + my_place;
+    int64_t off[kRowsEach];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) off[k] = sh.off[t & 1][my_row + k * kStep];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+      const bool there = off[k] >= 0;
+      const int64_t at = there ? off[k] + chunk * 16 : 0;
+      cp_async16(to + k * kStep * (C::kRow + 16), static_cast<const uint8_t*>(p.k) + at, there);
+      cp_async16(to + k * kStep * (C::kRow + 16) + C::kSide, static_cast<const uint8_t*>(p.v) + at, there);
+    }
+    cp_async_commit();
+  };
   while (w.next(a, kKeys, 1)) {
-    const DraftItem& it = w.it;
-    auto rows_of = [&](int t, int64_t* offs) {     // offsets of tile t's rows
-      if (tid < kKeys) {
-        const uint32_t x = (uint32_t)t * kKeys + tid;
-        int64_t off = -1;
-        if (x < (uint32_t)w.seq.len) {
-          const uint32_t pg = x / (uint32_t)a.page_size;
-          const int id = a.table[(int64_t)w.seg_b * a.max_pages + pg];
-          if ((unsigned)id < (unsigned)a.n_pages)
-            off = ((int64_t)id * a.Hkv + it.kvh) * head_bytes + (int64_t)(x - pg * a.page_size) * C::kRow;
-          else
-            flag_device(a.status, kDevCheck);
-        }
-        offs[tid] = off;
-      }
-    };
-    auto fetch = [&](int t, const int64_t* offs) {
-      uint8_t* st = smem + (t & 1) * 2 * C::kSide;
-      for (int e = tid; e < 2 * kKeys * kChunks; e += kThreads) {
-        const int side = e / (kKeys * kChunks), r = e / kChunks % kKeys, c = e % kChunks;
-        const int64_t off = offs[r];
-        uint8_t* to = st + side * C::kSide + swizzled<C::kRow>(r, c);
-        if (off >= 0) cp_async16(to, static_cast<const uint8_t*>(side ? p.v : p.k) + off + c * 16);
-        else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-      }
-      cp_async_commit();
-    };
     __syncthreads();
-    // a tile's offsets are looked up while the tile before the one before it is worked on
-    int64_t *off = sh.off[0], *off1 = sh.off[1], *off2 = sh.off[2];
-    rows_of(w.t0, off);
-    rows_of(w.t0 + 1, off1);
-    me.load_q(static_cast<const T*>(p.q), p.q_stride, w.seq.first + it.i0, it.kvh * a.G + it.h0, it.ni, it.nh);
+    if (tid < 2) sh.bad[tid] = 0;
+    const int first = page_of(w.t0), second = page_of(w.t0 + 1);
+    place(w.t0, first);
+    place(w.t0 + 1, second);
+    me.load_q(static_cast<const T*>(p.q), p.q_stride, w.seq.first + w.it.i0, w.it.kvh * a.G + w.it.h0, w.it.ni, w.it.nh);
     __syncthreads();
-    fetch(w.t0, off);
+    fetch(w.t0);
     for (int t = w.t0; t < w.t1; ++t) {
-      if (tid == 0) sh.bad = 0;
-      if (t + 1 < w.t1) fetch(t + 1, off1);
+      if (t + 1 < w.t1) fetch(t + 1);
       else cp_async_commit();
-      if (t + 2 < w.t1) rows_of(t + 2, off2);
+      const int ahead = page_of(t + 2);
       cp_async_wait1();
-      __syncthreads();
       uint8_t* st = smem + (t & 1) * 2 * C::kSide;
       const int64_t x0 = (int64_t)t * kKeys;
-      const int ctx = w.seq.len - w.seq.n;
-      const bool all = x0 + kKeys <= ctx;          // every row sees every key
-      if (!all) {
-        for (int e = tid; e < kKeys * kChunks; e += kThreads)
-          if (clear_bad<T>(st + C::kSide + swizzled<C::kRow>(e / kChunks, e % kChunks)))
-            atomicOr(&sh.bad, 1ull << (e / kChunks));
-        __syncthreads();
-      }
-      me.tile(a, w.seq, it, st, st + C::kSide, x0, all, p.scale_log2);
-      if (!all && sh.bad) {
-        const uint64_t bad = sh.bad;
-        me.add_bad(a, w.seq, it, x0, bad, static_cast<const uint8_t*>(p.v), off);
+      const bool all = x0 + kKeys <= w.seq.len - w.seq.n;        // every row sees every key
+      unsigned long long* bad = &sh.bad[t & 1];
+      if (!C::kBf16 || !all) {                     // in the chunks that this thread has fetched
+        uint8_t* mine = st + C::kSide + my_place;
+        uint4 v[kRowsEach];
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) v[k] = *reinterpret_cast<const uint4*>(mine + k * kStep * (C::kRow + 16));
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) any |= has_bad<T>(v[k]);
+        if (any) {
+          for (int k = 0; k < kRowsEach; ++k)
+            if (clear_bad<T>(mine + k * kStep * (C::kRow + 16))) atomicOr(bad, 1ull << (my_row + k * kStep));
+        }
       }
       __syncthreads();
-      int64_t* o3 = off;
-      off = off1;
-      off1 = off2;
-      off2 = o3;
+      if (tid == 0) sh.bad[(t & 1) ^ 1] = 0;
+      me.tile(a, w.seq, w.it, st, st + C::kSide, x0, all, p.scale_log2);
+      if (*bad) {
+        me.add_bad(a, w.seq, w.it, x0, *bad, static_cast<const uint8_t*>(p.v), sh.off[t & 1]);
+        __syncthreads();
+      }
+      place(t + 2, ahead);
+      __syncthreads();
     }
     cp_async_wait0();
     me.merge(reinterpret_cast<float*>(smem));
-    const bool whole = w.begins && w.ends;
-    if (whole) {
-      me.store(a, w.seq, it, static_cast<T*>(p.o), p.lse);
+    if (w.begins && w.ends) {
+      me.store(a, w.seq, w.it, static_cast<T*>(p.o), p.lse);
     } else {
       const int64_t slot = 2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0);
       me.store_part(part.ml + slot * kRows * 2, part.o + slot * kRows * D);

@@ -11,19 +11,19 @@ namespace draft {
 
 using namespace paged;
 
-__device__ __forceinline__ void cp_async16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+// 16 bytes, or zeros (nothing is read) where `there` is false.
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// Place of 16-byte chunk c of row r, so that eight rows' equal chunks, and a
-// row's eight neighbouring ones, lie in different banks.
+// Place of 16-byte chunk c of row r: rows lie 16 bytes further apart than they
+// are long, so that eight rows' equal chunks lie in different banks.
 template <uint32_t kRow>
-__device__ __forceinline__ uint32_t swizzled(int r, int c) {
-  const int x = kRow >= 128 ? r & 7 : (r >> 1) & 3;
-  return (uint32_t)r * kRow + ((c ^ x) << 4);
+__device__ __forceinline__ uint32_t padded(int r, int c) {
+  return (uint32_t)r * (kRow + 16) + (c << 4);
 }
 
 // Values of a chunk that are not finite become 0; true if there were any.
@@ -42,6 +42,16 @@ __device__ __forceinline__ bool clear_bad(uint8_t* chunk) {
     }
   }
   if (any) *reinterpret_cast<uint4*>(chunk) = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+template <typename T>
+__device__ __forceinline__ bool has_bad(const uint4& v) {
+  if (sizeof(T) == 4) {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m)) >= 0x7f800000u;
+  }
+  bool any = false;
+  for (uint32_t w : {v.x, v.y, v.z, v.w}) any |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
   return any;
 }
 __device__ __forceinline__ float if_bad(float v) { return fabsf(v) <= 3.402823466e38f ? 0.f : v; }
@@ -108,7 +118,7 @@ struct Rows<bf16, D, 1> {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t b[4];
-        ldsm4(kb_ + swizzled<D * 2>(j * 16 + krow, 2 * ks + kc), b);
+        ldsm4(kb_ + padded<D * 2>(j * 16 + krow, 2 * ks + kc), b);
         mma16816(s[2 * j], qa[ks], b[0], b[1]);
         mma16816(s[2 * j + 1], qa[ks], b[2], b[3]);
       }
@@ -162,7 +172,7 @@ struct Rows<bf16, D, 1> {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t b[4];
-        ldsm4_t(vb_ + swizzled<D * 2>(j * 16 + (lane & 15), 2 * i + (lane >> 4)), b);
+        ldsm4_t(vb_ + padded<D * 2>(j * 16 + (lane & 15), 2 * i + (lane >> 4)), b);
         mma16816(o[2 * i], ph, b[0], b[1]);
         mma16816(o[2 * i + 1], ph, b[2], b[3]);
         mma16816(o[2 * i], pl, b[0], b[1]);
@@ -225,210 +235,289 @@ struct Rows<bf16, D, 1> {
   }
 };
 
-// fp32: thread (y, x) of 16 x 16 has rows 4 y to 4 y + 3, of the scores the
-// keys x + 16 j, of the outputs the columns kVec x + 16 kVec i.
+// fp32 on the tensor cores: a value is the sum of two tf32 (11 bits each), and
+// a product the sum of three, upper by upper and upper by lower both ways.  Of
+// the two factors the one with fewer uses, q or p, is rounded to its upper part, so
+// that its lower part has either sign and what is left out, lower by lower, is
+// 2^-21 at most and 0 on average; k and v are cut.  A matrix instruction cuts
+// its sums to fp32 as well, a step each, so only 16 columns or one tile's keys are
+// summed in it, the lower products apart, and fp32 adds do the rest.
+struct Tf32 {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Tf32 tf32_cut(float x) {
+  Tf32 t;
+  t.hi = __float_as_uint(x) & 0xffffe000u;
+  t.lo = __float_as_uint(x - __uint_as_float(t.hi)) + 0x1000u;
+  return t;
+}
+__device__ __forceinline__ Tf32 tf32_round(float x) {      // |x| below 2^127
+  Tf32 t;
+  t.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  t.lo = __float_as_uint(x - __uint_as_float(t.hi)) + 0x1000u;
+  return t;
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// fp32: warp w has rows 16 (w % kRowGroups) to + 15 and the tile's keys of its
+// group; a lane two of the rows, g and g + 8, of the scores the keys 8 n + 2 tq
+// and + 1, of the outputs those columns.
 template <int D, int kGroups>
 struct Rows<float, D, kGroups> {
-  static constexpr int kM = 64 / kGroups, kJ = 4 / kGroups;          // rows; keys of a thread
-  static constexpr int kVec = D == 32 ? 2 : 4, kParts = D / (16 * kVec), kStride = kM + 4;
-  float m[4], l[4], o[4][D / 16];
-  float *qs, *ps;
-  int y, x, group, key0;
+  static constexpr int kM = 64 / kGroups, kRowGroups = kM / 16, kKeyGroups = 8 / kRowGroups, kN = 64 / kKeyGroups / 8;
+  float m[2], l[2], o[D / 8][4];
+  float4 *qh, *ql;                 // upper and lower parts of the queries, as the instruction takes them
+  int g, tq, lane, row0, group, key0;
 
   __device__ __forceinline__ explicit Rows(void* scratch) {
-    qs = static_cast<float*>(scratch);
-    ps = qs + kM * D + (threadIdx.x >> 4) * 4 * kStride;
-    y = (threadIdx.x >> 4) % (kM / 4);
-    group = (threadIdx.x >> 4) / (kM / 4);
-    key0 = group * kM;
-    x = threadIdx.x & 15;
+    lane = threadIdx.x & 31;
+    g = lane >> 2;
+    tq = lane & 3;
+    const int warp = threadIdx.x >> 5;
+    row0 = warp % kRowGroups * 16;
+    group = warp / kRowGroups;
+    key0 = group * 8 * kN;
+    qh = static_cast<float4*>(scratch);
+    ql = qh + kM * D / 4;
   }
   __device__ __forceinline__ void load_q(const float* q, int64_t stride, int64_t token, int head, int ni, int nh) {
-    for (int e = threadIdx.x; e < kM * (D / 4); e += 256) {
-      const int row = e / (D / 4), c = e % (D / 4);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < ni * nh)
-        v = *reinterpret_cast<const float4*>(q + (token + row / nh) * stride + (int64_t)(head + row % nh) * D + 4 * c);
-      *reinterpret_cast<float4*>(qs + row * D + 4 * c) = v;
+    for (int e = threadIdx.x; e < kM * D / 4; e += 256) {
+      const int ln = e & 31, ks = (e >> 5) % (D / 8), rg = (e >> 5) / (D / 8);
+      float hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = rg * 16 + (ln >> 2) + 8 * (i & 1), col = 8 * ks + (ln & 3) + 4 * (i >> 1);
+        const float v = row < ni * nh ? q[(token + row / nh) * stride + (int64_t)(head + row % nh) * D + col] : 0.f;
+        const Tf32 t = fabsf(v) < 1.7014118e38f ? tf32_round(v) : tf32_cut(v);
+        hi[i] = __uint_as_float(t.hi);
+        lo[i] = __uint_as_float(t.lo);
+        if (!(fabsf(v) <= 3.402823466e38f)) hi[i] = v, lo[i] = 0.f;
+      }
+      qh[e] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+      ql[e] = make_float4(lo[0], lo[1], lo[2], lo[3]);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int r = 0; r < 2; ++r) m[r] = -INFINITY, l[r] = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
+  }
+  // A score by plain multiply-adds, where the parts of an infinite key made NaN of it.
+  static __device__ __noinline__ float score(const float* q_hi, const float* q_lo, const uint8_t* ks_, int row, int key) {
+    float s = 0.f;
+    for (int c = 0; c < D; ++c) {
+      const int e = ((c / 8) * 32 + (row & 7) * 4 + (c & 3)) * 4 + (row >> 3) + (c & 4) / 2;
+      s = fmaf(q_hi[e] + q_lo[e], *reinterpret_cast<const float*>(ks_ + padded<D * 4>(key, c / 4) + (c & 3) * 4), s);
     }
+    return s;
   }
   __device__ __forceinline__ void tile(const DraftBatch& a, const DraftSeq& seq, const DraftItem& it,
                                        const uint8_t* ks_, const uint8_t* vs_, int64_t x0, bool all, float scale_log2) {
     const int rows = it.ni * it.nh;
-    if ((y & ~1) * 4 >= rows) return;                       // the whole warp's rows
-    uint64_t see[4];                                        // read while the scores are computed
+    if (row0 >= rows) return;                               // the whole warp's rows
+    uint64_t see[2];                                        // read while the scores are computed
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * y + r;
-      see[r] = all ? ~0ull : row < rows ? draft_sees(a, seq, it.i0 + row / it.nh, x0) : 0;
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      see[r] = all ? ~0ull : row < rows ? draft_sees(a, seq, it.i0 + row / it.nh, x0) >> key0 : 0;
     }
-    float2 s2[4][kJ];
+    float s[kN][4], sl[kN][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) s2[r][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int c = 0; c < D / 4; ++c) {
-      float4 kq[kJ], qq[4];
+      for (int i = 0; i < 4; ++i) s[n][i] = sl[n][i] = 0.f;
+    const float4 *qhi = qh + row0 * D / 4 + lane, *qlo = ql + row0 * D / 4 + lane;
+#pragma unroll 2
+    for (int k2 = 0; k2 < D / 16; ++k2) {
+      uint32_t ah[2][4], al[2][4];
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int key = key0 + x + 16 * j;
-        kq[j] = *reinterpret_cast<const float4*>(ks_ + swizzled<D * 4>(key, c));
+      for (int k = 0; k < 2; ++k) {
+        const float4 h = qhi[(2 * k2 + k) * 32], w = qlo[(2 * k2 + k) * 32];
+        ah[k][0] = __float_as_uint(h.x), ah[k][1] = __float_as_uint(h.y), ah[k][2] = __float_as_uint(h.z),
+        ah[k][3] = __float_as_uint(h.w);
+        al[k][0] = __float_as_uint(w.x), al[k][1] = __float_as_uint(w.y), al[k][2] = __float_as_uint(w.z),
+        al[k][3] = __float_as_uint(w.w);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) qq[r] = *reinterpret_cast<const float4*>(qs + (4 * y + r) * D + 4 * c);
+      for (int n = 0; n < kN; ++n) {
+        uint32_t kr[4];
+        ldsm4(smem_u32(ks_ + padded<D * 4>(key0 + 8 * n + (lane & 7), 4 * k2 + (lane >> 3))), kr);
+        Tf32 b[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int i = 0; i < 4; ++i) b[i] = tf32_cut(__uint_as_float(kr[i]));
+        float t[4] = {};
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          ffma2(qq[r].x, qq[r].y, kq[j].x, kq[j].y, s2[r][j].x, s2[r][j].y, s2[r][j].x, s2[r][j].y);
-          ffma2(qq[r].z, qq[r].w, kq[j].z, kq[j].w, s2[r][j].x, s2[r][j].y, s2[r][j].x, s2[r][j].y);
+        for (int k = 0; k < 2; ++k) {
+          mma_tf32(sl[n], al[k], b[2 * k].hi, b[2 * k + 1].hi);
+          mma_tf32(sl[n], ah[k], b[2 * k].lo, b[2 * k + 1].lo);
+          mma_tf32(t, ah[k], b[2 * k].hi, b[2 * k + 1].hi);
         }
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float s[kJ], mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        s[j] = all || (see[r] >> (key0 + x + 16 * j) & 1) ? (s2[r][j].x + s2[r][j].y) * scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[j]);
+        for (int i = 0; i < 4; ++i) s[n][i] += t[i];
       }
+    }
+    bool odd = false;
 #pragma unroll
-      for (int k = 1; k < 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[n][i] += sl[n][i];
+        odd |= s[n][i] != s[n][i] && (see[i >> 1] >> (8 * n + 2 * tq + (i & 1)) & 1);
+      }
+    if (odd) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (s[n][i] != s[n][i])
+            s[n][i] = score(reinterpret_cast<const float*>(qh + row0 * D / 4), reinterpret_cast<const float*>(ql + row0 * D / 4),
+                            ks_, g + 8 * (i >> 1), key0 + 8 * n + 2 * tq + (i & 1));
+    }
+    float corr[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float& x = s[n][2 * r + j];
+          x = all || (see[r] >> (8 * n + 2 * tq + j) & 1) ? x * scale_log2 : -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
-      const float corr = ex2_approx(m[r] - base);
+      corr[r] = ex2_approx(m[r] - base);
       m[r] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        s[j] = ex2_approx(s[j] - base);
-        sum += s[j];
-        ps[r * kStride + x + 16 * j] = s[j];
-      }
-      l[r] = l[r] * corr + sum;
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[r][c] *= corr;
-    }
-    __syncwarp();                                           // a warp reads the rows that it wrote
-#pragma unroll 2
-    for (int k4 = 0; k4 < kM / 4; ++k4) {
-      float4 pr[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) pr[r] = *reinterpret_cast<const float4*>(ps + r * kStride + 4 * k4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = key0 + 4 * k4 + k;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-          const int col = kVec * x + 16 * kVec * i;
-          const float* vp = reinterpret_cast<const float*>(vs_ + swizzled<D * 4>(key, col / 4)) + col % 4;
-          float v[kVec];
-          if constexpr (kVec == 4) {
-            const float4 t = *reinterpret_cast<const float4*>(vp);
-            v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-          } else {
-            const float2 t = *reinterpret_cast<const float2*>(vp);
-            v[0] = t.x, v[1] = t.y;
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float pk = k == 0 ? pr[r].x : k == 1 ? pr[r].y : k == 2 ? pr[r].z : pr[r].w;
-#pragma unroll
-            for (int c = 0; c < kVec; c += 2)
-              ffma2(pk, pk, v[c], v[c + 1], o[r][kVec * i + c], o[r][kVec * i + c + 1], o[r][kVec * i + c],
-                    o[r][kVec * i + c + 1]);
-          }
+        for (int j = 0; j < 2; ++j) {
+          s[n][2 * r + j] = ex2_approx(s[n][2 * r + j] - base);
+          sum += s[n][2 * r + j];
         }
+      l[r] = l[r] * corr[r] + sum;
+    }
+    uint32_t ph[kN][4], pl[kN][4];           // the keys' order in the instruction: 2 tq as column tq, 2 tq + 1 as tq + 4
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Tf32 t = tf32_round(s[n][i]);
+        const int at = (i & 1) * 2 + (i >> 1);
+        ph[n][at] = t.hi;
+        pl[n][at] = t.lo;
       }
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      float t[4] = {}, tl[4] = {};
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const int key = key0 + 8 * n + 2 * tq, chunk = 2 * c + (g >> 2), at = (g & 3) * 4;
+        const Tf32 b0 = tf32_cut(*reinterpret_cast<const float*>(vs_ + padded<D * 4>(key, chunk) + at));
+        const Tf32 b1 = tf32_cut(*reinterpret_cast<const float*>(vs_ + padded<D * 4>(key + 1, chunk) + at));
+        mma_tf32(tl, pl[n], b0.hi, b1.hi);
+        mma_tf32(tl, ph[n], b0.lo, b1.lo);
+        mma_tf32(t, ph[n], b0.hi, b1.hi);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][i] = o[c][i] * corr[i >> 1] + (t[i] + tl[i]);
     }
   }
   __device__ __forceinline__ void add_bad(const DraftBatch& a, const DraftSeq& seq, const DraftItem& it, int64_t x0,
                                        uint64_t bad, const uint8_t* v, const int64_t* off) {
-    if constexpr (kGroups > 1) bad &= ((1ull << kM) - 1) << key0;
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * y + r;
+    bad &= (kN == 8 ? ~0ull : (1ull << 8 * kN) - 1) << key0;
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
       if (row >= it.ni * it.nh) continue;
       uint64_t todo = bad & draft_sees(a, seq, it.i0 + row / it.nh, x0);
       for (; todo; todo &= todo - 1) {
         const float* vr = reinterpret_cast<const float*>(v + off[__ffsll(todo) - 1]);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[r][c] += if_bad(vr[kVec * x + 16 * kVec * (c / kVec) + c % kVec]);
+        for (int c = 0; c < D / 8; ++c) {
+          const float2 x = *reinterpret_cast<const float2*>(vr + 8 * c + 2 * tq);
+          const float y0 = if_bad(x.x), y1 = if_bad(x.y);
+          if (r == 0) o[c][0] += y0, o[c][1] += y1;
+          else o[c][2] += y0, o[c][3] += y1;
+        }
       }
     }
   }
-  __device__ __forceinline__ void sum_up() {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int k = 1; k < 16; k <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
-  }
-  // The groups' results into the first one's; `red` has room for 64 rows.
+  // The groups' results into the first one's; `red` has room for 128 rows of D and two.
   __device__ __forceinline__ void merge(float* red) {
-    sum_up();
-    if constexpr (kGroups > 1) {
-      float2* ml = reinterpret_cast<float2*>(red + 64 * D);
-      if (group > 0) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = group * kM + 4 * y + r;
-          put(red + at * D, r, 1.f);
-          if (x == 0) ml[at] = make_float2(m[r], l[r]);
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    float2* ml = reinterpret_cast<float2*>(red + 128 * D);
+    if (group > 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int at = group * kM + row0 + g + 8 * r;
+        put(red + at * D, r, 1.f);
+        if (tq == 0) ml[at] = make_float2(m[r], l[r]);
+      }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      for (int k = 1; k < kKeyGroups; ++k) {
+        const int at = k * kM + row0 + g + 8 * r;
+        const float2 other = ml[at];
+        const float mn = fmaxf(m[r], other.x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2_approx(m[r] - base), fo = ex2_approx(other.x - base);
+        m[r] = mn;
+        l[r] = l[r] * f + other.y * fo;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const float2 x = *reinterpret_cast<const float2*>(red + at * D + 8 * c + 2 * tq);
+          o[c][2 * r] = o[c][2 * r] * f + x.x * fo;
+          o[c][2 * r + 1] = o[c][2 * r + 1] * f + x.y * fo;
         }
       }
-      __syncthreads();
-      if (group > 0) return;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        for (int k = 1; k < kGroups; ++k) {
-          const int at = k * kM + 4 * y + r;
-          const float2 other = ml[at];
-          const float mn = fmaxf(m[r], other.x), base = mn == -INFINITY ? 0.f : mn;
-          const float f = ex2_approx(m[r] - base), fo = ex2_approx(other.x - base);
-          m[r] = mn;
-          l[r] = l[r] * f + other.y * fo;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            o[r][c] = o[r][c] * f + red[at * D + kVec * x + 16 * kVec * (c / kVec) + c % kVec] * fo;
-        }
-    }
   }
   __device__ __forceinline__ void put(float* row, int r, float f) const {
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) row[kVec * x + 16 * kVec * (c / kVec) + c % kVec] = o[r][c] * f;
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<float2*>(row + 8 * c + 2 * tq) = make_float2(o[c][2 * r] * f, o[c][2 * r + 1] * f);
   }
   __device__ __forceinline__ void store(const DraftBatch& a, const DraftSeq& seq, const DraftItem& it, float* out,
                                         float* lse) {
     if (group > 0) return;
-    bool sees_any[4];
+    bool sees_any[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sees_any[r] = 4 * y + r < it.ni * it.nh && draft_sees_any(a, seq, it.i0 + (4 * y + r) / it.nh);
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      sees_any[r] = row < it.ni * it.nh && draft_sees_any(a, seq, it.i0 + row / it.nh);
+    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * y + r;
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
       if (row >= it.ni * it.nh) continue;
       const int i = row / it.nh, h = it.kvh * a.G + it.h0 + row % it.nh;
       const int64_t t = (int64_t)seq.first + it.i0 + i;
-      const bool any = sees_any[r];
-      if (!any)
+      if (!sees_any[r])
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
-      put(out + (t * a.H + h) * D, r, any ? 1.f / l[r] : 0.f);
-      if (lse && x == 0) lse[(int64_t)h * a.T + t] = row_lse(m[r], l[r], any);
+        for (int c = 0; c < D / 8; ++c) o[c][2 * r] = o[c][2 * r + 1] = 0.f;
+      put(out + (t * a.H + h) * D, r, sees_any[r] ? 1.f / l[r] : 0.f);
+      if (lse && tq == 0) lse[(int64_t)h * a.T + t] = row_lse(m[r], l[r], sees_any[r]);
     }
   }
   __device__ __forceinline__ void store_part(float* ml, float* po) {
     if (group > 0) return;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * y + r;
-      if (x == 0) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m[r], l[r]);
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      if (tq == 0) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m[r], l[r]);
       put(po + row * D, r, 1.f);
     }
   }
