@@ -285,20 +285,38 @@ struct Rows<float, D, kGroups> {
     ql = qh + kM * D / 4;
   }
   __device__ __forceinline__ void load_q(const float* q, int64_t stride, int64_t token, int head, int ni, int nh) {
-    for (int e = threadIdx.x; e < kM * D / 4; e += 256) {
-      const int ln = e & 31, ks = (e >> 5) % (D / 8), rg = (e >> 5) / (D / 8);
-      float hi[4], lo[4];
+    constexpr int kAll = kM * D / 4, kTurns = (kAll + 255) / 256, kAtOnce = kTurns < 4 ? kTurns : 4;
+    for (int e0 = threadIdx.x; e0 < kAll; e0 += 256 * kAtOnce) {
+      float v[kAtOnce][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = rg * 16 + (ln >> 2) + 8 * (i & 1), col = 8 * ks + (ln & 3) + 4 * (i >> 1);
-        const float v = row < ni * nh ? q[(token + row / nh) * stride + (int64_t)(head + row % nh) * D + col] : 0.f;
-        const Tf32 t = fabsf(v) < 1.7014118e38f ? tf32_round(v) : tf32_cut(v);
-        hi[i] = __uint_as_float(t.hi);
-        lo[i] = __uint_as_float(t.lo);
-        if (!(fabsf(v) <= 3.402823466e38f)) hi[i] = v, lo[i] = 0.f;
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int at = (e0 >> 5) + 8 * k, ks = at % (D / 8);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = at / (D / 8) * 16 + g + 8 * r;
+          const bool there = row < ni * nh;
+          const float* from = q + (token + row / nh) * stride + (int64_t)(head + row % nh) * D + 8 * ks + tq;
+          v[k][r] = there ? from[0] : 0.f;
+          v[k][2 + r] = there ? from[4] : 0.f;
+        }
       }
-      qh[e] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-      ql[e] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        float hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = v[k][i];
+          const Tf32 t = fabsf(x) < 1.7014118e38f ? tf32_round(x) : tf32_cut(x);
+          hi[i] = __uint_as_float(t.hi);
+          lo[i] = __uint_as_float(t.lo);
+          if (!(fabsf(x) <= 3.402823466e38f)) hi[i] = x, lo[i] = 0.f;
+        }
+        const int e = e0 + 256 * k;
+        if (kAll % 256 == 0 || e < kAll) {
+          qh[e] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+          ql[e] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) m[r] = -INFINITY, l[r] = 0.f;
