@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from _drafts import tree_attn
 from test_gpu_drafts import BF, DEV, F32, _cu, _i32, call, call_kernel, check, make_case, nt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -390,3 +391,36 @@ def test_binding_refusals(nt):
         with pytest.raises((ValueError, nt.NTError)):
             call_()
     nt.nt_device_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [MIXED, WIDE, NARROW])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_infinite_keys(nt, kernel, shape, dtype):
+    """An infinite key in the context gives scores of -inf, weight 0, to the
+    heads whose query is negative there, and NaN to the others."""
+    b = max(i for i, (x, n) in enumerate(zip(shape["ctx"], shape["ns"])) if x > 4 and n)
+    first, n = sum(shape["ns"][:b]), shape["ns"][b]
+
+    def edit(kp, vp, table, q, bits):
+        page, row = at(shape, table, b, 3)
+        kp[page, 0, row, 2] = math.inf
+        q[:, :, 2] = torch.where(q[:, :, 2] == 0, torch.ones_like(q[:, :, 2]), q[:, :, 2])
+
+    c = make_case(**shape, dtype=dtype, seed=12, edit=edit)
+    got = by(nt, c, kernel)
+    if not got:
+        return
+    out = got[0].double().cpu()
+    G = shape["H"] // shape["Hk"]
+    up = torch.zeros(out.shape[:2], dtype=torch.bool)
+    up[first:first + n, :G] = c["q"][first:first + n, :G, 2] > 0
+    assert bool(torch.isnan(out[up]).all()) and bool(torch.isfinite(out[~up]).all())
+    # the others as if the key were not there: a copy whose key gives them a score of -10^4 or less
+    page, row = at(shape, c["table"], b, 3)
+    far = dict(c, kp=c["kp"].clone())
+    far["kp"][page, 0, row] = 0
+    far["kp"][page, 0, row, 2] = 3e38
+    plain = tree_attn(far["kp"], far["vp"], far["q"], far["ns"], far["table"], far["lens"], far["bits"])
+    err, scale = (out - plain[0]).abs()[~up], plain[0].abs().max()
+    assert float(err.max()) <= (2.0 ** -8 + 2.0 ** -12 if dtype == BF else 1e-5) * float(scale)

@@ -220,17 +220,17 @@ double draft_items_mean(const DraftProblem& p, const DraftBatch& a) {
 // sequence fills its table, several 0.4 of it), the tokens and the heads.  The
 // rates were fitted to 4,000 random calls of up to 128 sequences, on which this
 // choice costs 1 to 3% over the best kernel of each (geometric mean; without the
-// spread kernel 7 to 16%, the tensor-memory kernel 14 to 16 at d = 64 and 128,
-// the slices 1.6 at d = 32 and 0.7 at 64, the rows kernel 4 in bf16 and 35 to 51
-// in fp32).
+// spread kernel 6 to 16%, the tensor-memory kernel 10 to 12 at d = 64 and 128,
+// the slices 1.5 at d = 32 and 0.6 at 64, the rows kernel 6 to 11 in bf16 and 51
+// to 75 in fp32).
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
-  constexpr Rates kRowsBf16[3] = {{7.2, 1.75, 2.9}, {7.7, 2.4, 3.0}, {8.5, 3.85, 4.6}};
-  constexpr Rates kRowsF32[3][3] = {{{7.6, 2.1, 4.7}, {7.6, 3.2, 4.7}, {7.6, 5.5, 4.7}},
-                                    {{7.9, 3.25, 5.3}, {7.9, 5.3, 5.3}, {7.9, 9.2, 5.3}},
-                                    {{9.1, 3.95, 6.2}, {9.1, 5.6, 6.2}, {9.1, 9.3, 6.2}}};
-  constexpr Rates kTcRates[2][2] = {{{10.9, 1.06, 2.4}, {13.8, 2.1, 6.5}}, {{11.0, 1.7, 2.5}, {17.3, 3.1, 7.1}}};
-  constexpr Rates kSliceRates[2][3] = {{{7.8, 0.53, 2.3}, {7.8, 0.92, 2.3}, {7.8, 1.66, 2.3}},
-                                       {{8.2, 0.40, 2.5}, {8.2, 0.59, 2.5}, {8.2, 1.58, 2.5}}};
+  constexpr Rates kRowsBf16[3] = {{7.15, 1.47, 2.75}, {7.55, 2.0, 2.8}, {8.1, 3.1, 3.9}};
+  constexpr Rates kRowsF32[3][3] = {{{7.65, 1.72, 3.8}, {7.65, 2.34, 3.8}, {7.65, 4.1, 3.8}},
+                                    {{8.6, 2.74, 4.5}, {8.6, 4.0, 4.5}, {8.6, 7.4, 4.5}},
+                                    {{10.6, 3.1, 5.8}, {10.6, 4.0, 5.8}, {10.6, 7.1, 5.8}}};
+  constexpr Rates kTcRates[2][2] = {{{10.9, 1.06, 2.7}, {14.4, 2.2, 5.5}}, {{11.2, 1.66, 2.4}, {17.7, 3.1, 6.2}}};
+  constexpr Rates kSliceRates[2][3] = {{{7.5, 0.525, 2.4}, {7.5, 0.93, 2.4}, {7.5, 1.64, 2.4}},
+                                       {{8.45, 0.39, 2.6}, {8.45, 0.61, 2.6}, {8.45, 1.53, 2.6}}};
   const int sms = min(sm_count(), kPagedMaxCtas), w = p.d == 32 ? 0 : p.d == 64 ? 1 : 2;
   const int64_t rows = (int64_t)p.max_new * (p.H / p.pool.H);
   const int group = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;

@@ -400,10 +400,10 @@ template <typename T, int D>
 double estimate(const DraftProblem& p, int* cluster) {
   using C = Cfg<T, D>;
   constexpr int w = D == 32 ? 0 : D == 64 ? 1 : 2;
-  constexpr double kFirst = C::kBf16 ? (w == 0 ? 5.8 : w == 1 ? 6.7 : 8.6) : (w == 0 ? 8.0 : w == 1 ? 7.6 : 9.1);
-  constexpr double kSlice = C::kBf16 ? (w == 0 ? 0.82 : w == 1 ? 1.06 : 1.14) : (w == 0 ? 1.7 : w == 1 ? 1.84 : 2.27);
-  constexpr double kWave = C::kBf16 ? (w == 0 ? 3.6 : w == 1 ? 4.2 : 6.1) : (w == 0 ? 4.5 : w == 1 ? 5.3 : 5.4);
-  constexpr double kLoaded = C::kBf16 ? (w == 0 ? 1.35 : w == 1 ? 2.4 : 3.05) : (w == 0 ? 3.8 : w == 1 ? 3.6 : 4.3);
+  constexpr double kFirst = C::kBf16 ? (w == 0 ? 5.75 : w == 1 ? 6.66 : 8.45) : (w == 0 ? 8.0 : w == 1 ? 7.6 : 8.8);
+  constexpr double kSlice = C::kBf16 ? (w == 0 ? 0.89 : w == 1 ? 1.2 : 1.22) : (w == 0 ? 1.56 : w == 1 ? 2.46 : 1.83);
+  constexpr double kWave = C::kBf16 ? (w == 0 ? 3.9 : w == 1 ? 4.1 : 5.7) : (w == 0 ? 5.7 : w == 1 ? 4.4 : 4.76);
+  constexpr double kLoaded = C::kBf16 ? (w == 0 ? 1.09 : w == 1 ? 2.25 : 3.2) : (w == 0 ? 2.73 : w == 1 ? 3.9 : 4.46);
   const DraftBatch a = draft_batch(p, C::kRows, 1, nullptr);
   const int64_t items = (int64_t)p.B * draft_items_most(a), slices = (a.cap + 15) / 16;
   const double all = p.B * draft_items_mean(p, a) * (draft_mean_keys(p, a) / 16 + 0.5);
