@@ -141,12 +141,12 @@ T fresh(at::IntArrayRef sizes, at::ScalarType type, int index) {
                                   std::nullopt));
 }
 // n elements of another type over a part of a tensor's memory.
-T part(const T& all, int64_t at, int64_t n, at::ScalarType type) {
+T part(const T& all, int64_t at, at::IntArrayRef sizes, at::ScalarType type) {
   T t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
                                                  c10::scalarTypeToTypeMeta(type));
   c10::TensorImpl* impl = t.unsafeGetTensorImpl();
   impl->set_storage_offset(at / (int64_t)c10::elementSize(type));
-  impl->set_sizes_contiguous({n});
+  impl->set_sizes_contiguous(sizes);
   return t;
 }
 T like(const T& t) { return fresh(t.sizes(), t.scalar_type(), t.get_device()); }
@@ -430,8 +430,8 @@ PyObject* paged_resize(PyObject* const* a, Py_ssize_t n) {
   // one allocation for the four outputs, each a tensor over its part of it
   const int64_t ints_at = 8 * tokens;
   const T all = fresh({ints_at + 4 * (2 * B + 3)}, at::kByte, index);
-  const T slots = part(all, 0, tokens, at::kLong), cu = part(all, ints_at, B + 1, at::kInt),
-          pos0 = part(all, ints_at + 4 * (B + 1), B, at::kInt), lacking = part(all, ints_at + 4 * (2 * B + 1), 2, at::kInt);
+  const T slots = part(all, 0, {tokens}, at::kLong), cu = part(all, ints_at, {B + 1}, at::kInt),
+          pos0 = part(all, ints_at + 4 * (B + 1), {B}, at::kInt), lacking = part(all, ints_at + 4 * (2 * B + 1), {2}, at::kInt);
   const int st = unlocked(f_resize, nl, (int32_t)B, page_size, t, max_pages, len, f, (int32_t)free_pages.numel(), nf,
                           static_cast<int32_t*>(data(cu)), static_cast<int32_t*>(data(pos0)),
                           static_cast<int64_t*>(data(slots)), tokens, static_cast<int32_t*>(data(lacking)), call.stream);
@@ -452,6 +452,11 @@ PyObject* draft_tree(PyObject* const* a, Py_ssize_t n) {
   Call call(index, a[6]);
   T bits = tensor(a[4], "bits"), positions = tensor(a[5], "positions");
   const int64_t words = ((int64_t)max_new + 63) / 64;
+  if (!bits.defined() && !positions.defined() && words > 0) {        // one allocation for both
+    const T all = fresh({tokens * (8 * words + 4)}, at::kByte, index);
+    bits = part(all, 0, {tokens, words}, at::kLong);
+    positions = part(all, tokens * 8 * words, {tokens}, at::kInt);
+  }
   if (!bits.defined()) bits = fresh({tokens, std::max<int64_t>(words, 0)}, at::kLong, index);
   else if (bits.dim() != 2 || bits.size(0) != tokens || bits.size(1) != words)
     refuse("bits must be (tokens, ceil(max_new / 64))");
