@@ -2,6 +2,8 @@
 // and slot maps from request lengths, the tree's masks and positions, and the
 // accepted tokens' keys and values moved up.  All three are latencies: a
 // launch, and a few dependent loads.
+#include <atomic>
+
 #include "nt_common.cuh"
 
 namespace nt {
@@ -15,9 +17,11 @@ namespace {
 // slots.  Every CTA scans all rows (their lengths are a load that all do at
 // once), a thread a strip of them; pages and tokens are then dealt out one by
 // one over all threads, however they lie in the rows, several searches side
-// by side (one after the other 512 prompts of 65,000 tokens took 12.3 us).
+// by side.  512 prompts of 65,000 tokens and back: 25 us by one CTA, 16.5 by eight,
+// 12.0 by 16; 16 sequences and back: 13.2, 8.4 and 8.4, the launches, cluster barriers
+// and the loads between them.
 constexpr int kResizeThreads = 512;
-constexpr int kResizeCtas = 8;
+constexpr int kResizeCtas = 16, kResizePortable = 8;
 constexpr int kResizeUnroll = 4;
 
 struct ResizeArgs {
@@ -213,6 +217,39 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
   }
 }
 
+cudaLaunchConfig_t resize_config(int ctas, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kResizeThreads);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+// Asked for once per device: whether a cluster of 16 fits one.
+int resize_ctas() {
+  static std::atomic<int> known[64];
+  int dev = 64;
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n) return n;
+  int fit = 0;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = resize_config(kResizeCtas, attr);
+  if (allow_smem_once<paged_resize_kernel, true>(0) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&fit, paged_resize_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    fit = 0;
+  }
+  n = fit > 0 ? kResizeCtas : kResizePortable;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // ---- the tree's masks and positions ---------------------------------------------
 //
 // A CTA to a sequence, a thread to a token.  In round r a token adds what the
@@ -394,18 +431,9 @@ cudaError_t launch_paged_resize(const int32_t* new_lengths, int B, int page_size
   a.T = T;
   a.cap = min64((int64_t)max_pages * page_size, 0x7fffffff);
   a.status = status;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kResizeCtas);
-  cfg.blockDim = dim3(kResizeThreads);
-  cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kResizeCtas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cudaLaunchConfig_t cfg = resize_config(resize_ctas(), attr);
+  cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, paged_resize_kernel, a);
 }
 
