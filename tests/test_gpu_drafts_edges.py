@@ -424,3 +424,19 @@ def test_infinite_keys(nt, kernel, shape, dtype):
     plain = tree_attn(far["kp"], far["vp"], far["q"], far["ns"], far["table"], far["lens"], far["bits"])
     err, scale = (out - plain[0]).abs()[~up], plain[0].abs().max()
     assert float(err.max()) <= (2.0 ** -8 + 2.0 ** -12 if dtype == BF else 1e-5) * float(scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seed", range(8))
+def test_sequences_of_one_and_two_row_tiles(nt, seed, d):
+    """Tiles of sequences with more rows count for more when the batch is dealt
+    out, so shares begin and end inside tiles: from fewer tiles than SMs to
+    several to each."""
+    rng = np.random.default_rng(seed)
+    B = [1, 2, 5, 12, 30, 60, 150, 7][seed]
+    ns = [int(x) for x in rng.choice([0, 1, 31, 32, 33, 64, 65, 200], B)]
+    ctx = [int(x) for x in rng.integers(0, [3000, 900, 700, 500, 300, 200, 60, 5][seed], B)]
+    ns[0] = 40
+    c = make_case(ctx, ns, 16, 4, 1, d, BF, seed=seed)
+    check(c, *call_kernel(nt, c, 1))
+    check(c, *call(nt, c))

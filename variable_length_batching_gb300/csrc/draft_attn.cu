@@ -181,8 +181,9 @@ DraftBatch draft_batch(const DraftProblem& p, int rows, int groups, unsigned int
   a.heads = min(a.G, rows);
   a.hgroups = (a.G + a.heads - 1) / a.heads;
   a.tokens = max(1, rows / a.heads) * groups;
+  a.light = groups > 1 ? a.tokens / groups : 0;
   // units are counted in tiles of 32 keys at least, with at most 16 more to an item
-  a.few = p.B <= kPlanFew && (double)p.B * draft_items_most(a) * ((double)a.cap / 32 + 17) < 2e9;
+  a.few = p.B <= kPlanFew && (double)p.B * draft_items_most(a) * ((double)a.cap / 32 + 17) * draft_weight_most(a) < 2e9;
   a.status = status;
   return a;
 }
@@ -212,7 +213,7 @@ double split_us(const DraftProblem& p, int rows, int groups, int keys, int ctas,
 double draft_mean_keys(const DraftProblem& p, const DraftBatch& a) { return p.B == 1 ? a.cap : 0.4 * a.cap; }
 double draft_items_mean(const DraftProblem& p, const DraftBatch& a) {
   const double heads = (double)a.Hkv * a.hgroups, n = (double)p.T / p.B, most = (p.max_new + a.tokens - 1) / a.tokens;
-  return heads * (most <= 1 || n >= p.max_new ? most : fmin(most, fmax(1, n / a.tokens + 0.5)));
+  return heads * (most <= 1 || n >= p.max_new ? most : fmin(most, fmax(1, n / a.tokens + 0.75)));
 }
 
 // The call takes the kernel with the least estimated time.  Lengths are on the
@@ -245,8 +246,12 @@ cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* 
   if (dt == NT_BF16) consider(kRows, split_us(p, 64, 1, 64, 2 * sms, kRowsBf16[w]));
   else consider(kRows, split_us(p, 16 << group, 1, 64, p.d == 128 ? sms : 2 * sms, kRowsF32[w][group]));
   if (draft_tc_supported(dt, p)) {
-    const int two = rows > 128;
-    consider(kTc, split_us(p, 128, 1 + two, 128, sms, kTcRates[p.d == 128][two]));
+    const bool wide = p.d == 128;
+    Rates r = kTcRates[wide][rows > 128];
+    // two row tiles: sequences that need but one, at most those whose tokens leave the average below it, take less
+    if (rows > 128)
+      r.tile += (kTcRates[wide][0].tile - r.tile) * fmax(0, 1 - (double)p.T / p.B / (128 / min(128, p.H / p.pool.H)));
+    consider(kTc, split_us(p, 128, 1 + (rows > 128), 128, sms, r));
   }
   if (draft_slices_supported(dt, p))
     consider(kSlices, split_us(p, 16 << group, 1, w ? 64 : 128, sms, kSliceRates[w][group]));

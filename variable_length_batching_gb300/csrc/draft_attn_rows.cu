@@ -175,7 +175,7 @@ __global__ void __launch_bounds__((Cfg<T, D, kGroups>::kThreads), (Cfg<T, D, kGr
       me.store_part(part.ml + slot * kRows * 2, part.o + slot * kRows * D);
     }
     if (w.begins && !w.ends)
-      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, 1, blockIdx.x));
+      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, blockIdx.x));
   }
   if (tid == 0) part.open[blockIdx.x] = open;
 }

@@ -365,7 +365,7 @@ draft_slices_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     if (threadIdx.x == 0)                             // everybody has read it; the segment after the next writes it
       for (int k = 0; k <= kBadWords; ++k) bad[k] = 0;
     if (w.begins && !w.ends)
-      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, kE, blockIdx.x));
+      open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, blockIdx.x));
     ++segs;
   }
   if (threadIdx.x == 0) part.open[blockIdx.x] = open;

@@ -582,7 +582,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free);
       if (w.begins && !w.ends)
-        open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, kE, blockIdx.x));
+        open = make_int4(w.seg_b, w.seg_item, w.seg_items, w.parts(plan, blockIdx.x));
       s0 += steps;
       tile0 += (uint32_t)(t_hi - t_lo);
       ++segs;

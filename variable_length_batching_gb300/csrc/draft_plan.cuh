@@ -7,7 +7,10 @@
 // token per sequence (paged_plan.cuh), CTA c of n takes units
 // [c W / n, (c + 1) W / n) of the line, so that every CTA reads the same
 // number of keys however ragged the batch is, and lengths and offsets stay on
-// the device.  Here the items of a sequence are as many as its tokens need.
+// the device.  Here the items of a sequence are as many as its tokens need; and
+// where an item may have two row tiles over its keys, a tile of a sequence that
+// needs both counts 5 and one of another 3, as they take (152 contexts of 8,000,
+// d = 128: 178 us against 109), and belongs to the CTA that has its first unit.
 #pragma once
 
 #include "paged_plan.cuh"
@@ -27,6 +30,7 @@ struct DraftBatch {
   int H, G, Hkv;
   int heads, hgroups;       // query heads of an item, and groups of them to a key head
   int tokens;               // of an item
+  int light;                // tokens of one row tile, or 0: an item has but one
   bool few;                 // few enough sequences and units for a warp to plan
   unsigned int* status;
 };
@@ -56,8 +60,14 @@ inline int draft_items_most(const DraftBatch& a) {
 __device__ __forceinline__ int draft_items(const DraftBatch& a, int n) {
   return a.Hkv * a.hgroups * (n <= a.tokens ? 1 : (n + a.tokens - 1) / a.tokens);
 }
+constexpr int kHeavy = 5, kLight = 3;
+__host__ __device__ __forceinline__ int draft_weight_most(const DraftBatch& a) { return a.light ? kHeavy : 1; }
+// Units of a tile of a sequence of n new tokens.
+__device__ __forceinline__ int draft_weight(const DraftBatch& a, int n) {
+  return !a.light ? 1 : n > a.light ? kHeavy : kLight;
+}
 __device__ __forceinline__ int64_t draft_units(const DraftBatch& a, const DraftSeq& s, int tile, int extra) {
-  return s.n > 0 ? (paged_tiles(s.len, tile) + extra) * draft_items(a, s.n) : 0;
+  return s.n > 0 ? (paged_tiles(s.len, tile) + extra) * draft_items(a, s.n) * draft_weight(a, s.n) : 0;
 }
 
 // The units of the call dealt out to n CTAs: CTA c has per of them, one more for
@@ -68,9 +78,11 @@ struct DraftPlan {
   int64_t start;            // first unit of sequence b0, which holds lo
   int n, b0;
   DraftSeq seq;             // sequence b0
-  __device__ __forceinline__ void deal(int64_t total_, int cta, int ctas) {
+  // `least` units to a CTA, so that each has the first one of a tile; with fewer the last CTAs get none.
+  __device__ __forceinline__ void deal(int64_t total_, int least, int cta, int ctas) {
     total = total_;
-    n = (int)min64(ctas, total);                   // with fewer units than CTAs the last ones get none
+    n = (int)min64(ctas, total);
+    if (least > 1 && total > 0 && (int64_t)n * least > total) n = (int)max64(1, total / least);
     per = n ? paged_div(total, n) : 0;
     rem = total - per * n;
     lo = cta < n ? per * cta + min64(cta, rem) : total;
@@ -112,7 +124,7 @@ __device__ __forceinline__ DraftPlan draft_plan_warp(const DraftBatch& a, int ti
     if (lane >= m) inc += o;
   }
   DraftPlan p;
-  p.deal(__shfl_sync(0xffffffffu, inc, 31), cta, ctas);
+  p.deal(__shfl_sync(0xffffffffu, inc, 31), draft_weight_most(a), cta, ctas);
   int at = inc - sum, b = -1;
   DraftSeq s = {0, 0, 0};
   const int lo = (int)p.lo;
@@ -159,7 +171,7 @@ __device__ __forceinline__ DraftPlan draft_plan_cta(const DraftBatch& a, int til
     total += x;
   }
   DraftPlan p;
-  p.deal(total, cta, ctas);
+  p.deal(total, draft_weight_most(a), cta, ctas);
   int64_t at = before + inc - sum;
   if (p.lo >= at && p.lo < at + sum) {
     int b = b_lo;
@@ -210,6 +222,7 @@ struct DraftWalk {
   int b, item, items;
   DraftSeq cur;
   int next_lo, next_hi, next_len;         // of sequence b + 1, loaded when b was reached
+  int weight;             // units of a tile of sequence b
   int units;              // of an item of sequence b
   int unit;               // of the item, where the next segment starts
   int kvh, hgroup, group, groups;         // of the item: key head, group of its query heads, group of tokens of how many
@@ -218,6 +231,7 @@ struct DraftWalk {
   DraftItem it;
   int seg_b, seg_item, seg_items;
   int t0, t1;
+  int end;                // where it ends in the item, in units
   bool begins, ends;
 
   __device__ __forceinline__ void load_next(const DraftBatch& a) {
@@ -229,7 +243,8 @@ struct DraftWalk {
   __device__ __forceinline__ void sequence(const DraftBatch& a, int tile, int extra) {
     groups = cur.n <= a.tokens ? 1 : (cur.n + a.tokens - 1) / a.tokens;
     items = a.Hkv * a.hgroups * groups;
-    units = (int)paged_tiles(cur.len, tile) + extra;
+    weight = draft_weight(a, cur.n);
+    units = ((int)paged_tiles(cur.len, tile) + extra) * weight;
   }
   __device__ __forceinline__ void step_item(const DraftBatch& a) {
     ++item;
@@ -272,16 +287,21 @@ struct DraftWalk {
         item = group = hgroup = kvh = 0;
         sequence(a, tile, extra);
       }
-      const int end = (int)min64(units, unit + left);
+      end = (int)min64(units, unit + left);
       seg_b = b;
       seg_item = item;
       seg_items = items;
       seq = cur;
       it = draft_item(a, cur.n, kvh, hgroup, group);
-      t0 = max(0, unit - extra);
-      t1 = end - extra;
+      int from = unit, to = end;           // in tiles
+      if (weight > 1) {
+        from = (unit + weight - 1) / weight;
+        to = (end + weight - 1) / weight;
+      }
+      t0 = max(0, from - extra);
+      t1 = to - extra;
       begins = t0 == 0;
-      ends = end == units;
+      ends = to * weight >= units;
       left -= end - unit;
       unit = 0;
       step_item(a);
@@ -289,8 +309,8 @@ struct DraftWalk {
     return true;
   }
   // CTAs that take tiles of the current segment's item, where it begins and does not end (so the range ends inside it)
-  __device__ __forceinline__ int parts(const DraftPlan& s, int extra, int cta) const {
-    return s.cta_of(s.hi + units - (t1 + extra) - 1) - cta + 1;
+  __device__ __forceinline__ int parts(const DraftPlan& s, int cta) const {
+    return s.cta_of(s.hi + units - weight - end) - cta + 1;
   }
 };
 
