@@ -159,7 +159,7 @@ def test_flags(nt, kernel, dtype):
                 assert bool((out[rows][keep] == 7).all()) and bool((lse[:, rows][:, keep] == 7).all())
             elif cu[b] == 4 * b and cu[b + 1] == 4 * b + 4 and lens[b] == c["lens"][b]:
                 torch.testing.assert_close(out[rows].float(), good[0][rows].float(), rtol=2e-2, atol=2e-2)
-    for page in (-1, c["kp"].shape[0], 2 ** 31 - 1):
+    for page in (-1, c["kp"].shape[0], 2 ** 31 - 1, -2 ** 31):
         table = dev["table"].clone()
         table[1, 1] = page
         out, lse = run([0, 4, 8, 12, 16], c["lens"], table)

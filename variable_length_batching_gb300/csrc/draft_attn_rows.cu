@@ -94,7 +94,7 @@ __global__ void __launch_bounds__((Cfg<T, D, kGroups>::kThreads), (Cfg<T, D, kGr
   auto page_of = [&](int t) {
     const uint32_t x = (uint32_t)t * kKeys + tid;
     return tid < kKeys && x < (uint32_t)w.seq.len
-               ? a.table[(int64_t)w.seg_b * a.max_pages + x / (uint32_t)a.page_size] : kNone;
+               ? max(a.table[(int64_t)w.seg_b * a.max_pages + x / (uint32_t)a.page_size], -1) : kNone;
   };
   auto place = [&](int t, int id) {
     if (tid >= kKeys) return;

@@ -274,10 +274,10 @@ class PagedCache:
 
     def attend_tree(self, step: Step, q: torch.Tensor, bits: Optional[torch.Tensor] = None,
                     scale: Optional[float] = None, stream=None) -> torch.Tensor:
-        """All the step's tokens as queries, packed q (tokens, H, d): each over
-        the positions before the step and those of its sequence's new tokens
-        that ``bits`` (nt_draft_tree's) names; None: itself and those before
-        it."""
+        """All the step's tokens (at most 256 of a sequence) as queries, packed
+        q (tokens, H, d): each over the positions before the step and those of
+        its sequence's new tokens that ``bits`` (nt_draft_tree's) names; None:
+        itself and those before it."""
         if q.shape[0] != step.tokens:
             raise ValueError(f"the step has {step.tokens} new tokens, q has {q.shape[0]}")
         return nt.nt_paged_tree_attn(self.pages, q, step.cu_seqlens, step.block_table, step.lengths, step.max_new,
