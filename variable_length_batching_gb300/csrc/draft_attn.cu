@@ -59,8 +59,8 @@ struct JoinRow {
 };
 
 template <typename T, int D, bool kShared>
-__global__ void __launch_bounds__(kJoinWarps * 32, kShared ? 4 : 6) draft_join_kernel(const DraftBatch a, int ctas, int rows,
-                                                                        void* workspace, T* o, float* lse) {
+__global__ void __launch_bounds__(kJoinWarps * 32, kShared ? 4 : 6)
+    draft_join_kernel(const DraftBatch a, int ctas, int rows, void* workspace, T* o, float* lse) {
   constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;
   __shared__ int which;
   __shared__ float4 sv[kJoinWarps][32];

@@ -131,7 +131,8 @@ __global__ void __launch_bounds__((Cfg<T, D, kGroups>::kThreads), (Cfg<T, D, kGr
     const int first = page_of(w.t0), second = page_of(w.t0 + 1);
     place(w.t0, first);
     place(w.t0 + 1, second);
-    me.load_q(static_cast<const T*>(p.q), p.q_stride, w.seq.first + w.it.i0, w.it.kvh * a.G + w.it.h0, w.it.ni, w.it.nh);
+    me.load_q(static_cast<const T*>(p.q), p.q_stride, w.seq.first + w.it.i0, w.it.kvh * a.G + w.it.h0, w.it.ni,
+              w.it.nh);
     __syncthreads();
     fetch(w.t0);
     for (int t = w.t0; t < w.t1; ++t) {

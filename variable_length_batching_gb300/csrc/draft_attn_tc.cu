@@ -29,9 +29,9 @@
 // Measured: 152 contexts of 8,000 keys, 16 rows to a key head, 103 us at d = 128
 // (89% of the copy rate) and 69 at d = 64, where a row's 128 exponentials (1,550
 // cycles of a step's 2,900) are what a stream waits for; with 256 rows d = 128 178
-// and d = 64 141.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128: 331
-// us, 724 TFLOP/s of the result's products, three of which are made for two; a
-// product of 128 x 128 x 16 takes some 93 cycles here, 4,460 of a step's 5,250.
+// and d = 64 141.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128: 312
+// us, 768 TFLOP/s of the result's products, three of which are made for two; a
+// product of 128 x 128 x 16 takes some 93 cycles here, 4,460 of a step's 4,950.
 //
 // Two bf16 for P: one would be off by 2^-8 of P, which shows in the output.
 // The upper part is P cut short, the lower P (1 + 2^-20) less that, so that
@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr uint32_t kTile = kHalf * (D / 64);              // keys or values of a stage; a row tile of Q
   static constexpr int kQBufs = D == 128 && R == 2 ? 1 : 2;        // items whose queries are in flight or in use
   static constexpr uint32_t kQ = R * kTile;
-  static constexpr uint32_t kCtl = 3072;
+  static constexpr uint32_t kCtl = 2944;
   static constexpr int kFit = (int)((227 * 1024 - kCtl - kQBufs * kQ) / kTile);
   static constexpr int kK = kFit / 2, kV = kFit - kK;              // stages of keys and of values
   static constexpr uint32_t kSmem = kQBufs * kQ + (kK + kV) * kTile + kCtl;
@@ -83,7 +83,7 @@ struct Ctl {
   float2 word[2][kRows];                            // maximum and sum of a row in a stream
   DraftPlanSums plan;
 };
-static_assert(sizeof(Ctl) <= 3072, "control block");
+static_assert(sizeof(Ctl) <= 2944, "control block");
 
 struct TcArgs {
   DraftBatch a;
@@ -268,7 +268,9 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, now));
         if (lane == 0) mbar_arrive_expect_tx(&full[st], count * p.box * 128);
         __syncwarp();
-        if (now) tma_load_3d(ring + st * C::kTile + dst, map, &full[st], half * 64, (int)(p.page_shift >= 0 ? x & (ps - 1) : x % ps), z);
+        if (now)
+          tma_load_3d(ring + st * C::kTile + dst, map, &full[st], half * 64,
+                      (int)(p.page_shift >= 0 ? x & (ps - 1) : x % ps), z);
       }
     }
     // no copy may land after the CTA is gone
@@ -510,7 +512,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       }
       if (!ok) break;
       // ---- the segment's output: complete with its last P V
-      const uint32_t steps = (uint32_t)(t_hi - t_lo) * tiles, mine = s - 2, other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
+      const uint32_t steps = (uint32_t)(t_hi - t_lo) * tiles, mine = s - 2;
+      const uint32_t other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
       const bool some = t_first < t_hi, join = tiles == 1 && steps > 1;
       // its own last P V first: the other stream's then has no phase but its last to wait for
       // (a stream without a step has nothing to do, so that items of one tile follow each other in turns)
@@ -538,7 +541,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const bool whole = w.begins && w.ends, odd = bad[kSpecial * 4] != 0;
         const int h = it.kvh * a.G + row - tok * a.heads;
         const int64_t tt = (int64_t)w.seq.first + i;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0)) * kPartRows + (i - it.i0 - tok) * a.heads + row;
+        const int64_t slot =
+            (2 * (int64_t)blockIdx.x + (w.begins ? 1 : 0)) * kPartRows + (i - it.i0 - tok) * a.heads + row;
         const bool any = valid && mask.sees_any(a, w.seq);
         const float inv = any ? 1.f / l : 0.f;
         // joined, the streams' threads of a row share its columns

@@ -326,7 +326,8 @@ struct Rows<float, D, kGroups> {
       for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
   }
   // A score by plain multiply-adds, where the parts of an infinite key made NaN of it.
-  static __device__ __noinline__ float score(const float* q_hi, const float* q_lo, const uint8_t* ks_, int row, int key) {
+  static __device__ __noinline__ float score(const float* q_hi, const float* q_lo, const uint8_t* ks_, int row,
+                                             int key) {
     float s = 0.f;
     for (int c = 0; c < D; ++c) {
       const int e = ((c / 8) * 32 + (row & 7) * 4 + (c & 3)) * 4 + (row >> 3) + (c & 4) / 2;
@@ -393,8 +394,9 @@ struct Rows<float, D, kGroups> {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (s[n][i] != s[n][i])
-            s[n][i] = score(reinterpret_cast<const float*>(qh + row0 * D / 4), reinterpret_cast<const float*>(ql + row0 * D / 4),
-                            ks_, g + 8 * (i >> 1), key0 + 8 * n + 2 * tq + (i & 1));
+            s[n][i] = score(reinterpret_cast<const float*>(qh + row0 * D / 4),
+                            reinterpret_cast<const float*>(ql + row0 * D / 4), ks_, g + 8 * (i >> 1),
+                            key0 + 8 * n + 2 * tq + (i & 1));
     }
     float corr[2];
 #pragma unroll
