@@ -398,17 +398,18 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         tc_fence_after();
         if (live) {
           uint64_t see[2] = {~0ull, ~0ull};
+          bool masked = false;                      // a row of the warp does not see all of the tile
           if (special) {
-            see[0] = valid ? mask.sees(a, w.seq, i, t * kKeys) : 0;
-            see[1] = valid ? mask.sees(a, w.seq, i, t * kKeys + 64) : 0;
-            __syncwarp();
+            see[0] = valid ? mask.sees(a, w.seq, i, t * kKeys) : ~0ull;
+            see[1] = valid ? mask.sees(a, w.seq, i, t * kKeys + 64) : ~0ull;
+            masked = __any_sync(0xffffffffu, (see[0] & see[1]) != ~0ull);
           }
           float mx = -INFINITY;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float x[64];
             tmem_ld64_sync(s_at + 64 * h, x);
-            if (special) {
+            if (masked) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
                 if (!((h ? see[1] : see[0]) >> c & 1)) x[c] = -INFINITY;
@@ -451,7 +452,7 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             float x[32];
             uint32_t pw[32];                        // upper parts, then lower parts
             tmem_ld32_sync(s_at + c0, x);
-            if (special) {
+            if (masked) {
               const uint32_t there = (uint32_t)((c0 < 64 ? see[0] : see[1]) >> (c0 & 32));
 #pragma unroll
               for (int c = 0; c < 32; ++c)
@@ -490,15 +491,27 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           if (!ok) break;
           const int left = min(kKeys, w.seq.len - t * kKeys), end = (left + 15) / 16 * 16;
           uint8_t* v0 = sv + st * C::kTile;
-          for (int y = max(0, ctx - t * kKeys) * (D / 8) + (threadIdx.x & 127); y < end * (D / 8); y += 128) {
-            const int key = y / (D / 8), c = y % (D / 8);
-            uint8_t* at = v0 + (c >> 3) * C::kHalf + key * 128 + (c & 7) * 16;
-            if (key >= left) {
-              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-            } else if (draft::clear_bad<bf16>(at)) {
-              const int k = (t - ctx / kKeys) * kKeys + key;
-              atomicOr(&bad[k >> 5], 1u << (k & 31));
-              bad[kSpecial * 4] = 1;
+          // a thread has chunk c of every kApart-th key, four at a time
+          constexpr int kApart = 128 / (D / 8);
+          const int c = threadIdx.x % (D / 8), first = max(0, ctx - t * kKeys) / kApart * kApart;
+          uint8_t* at0 = v0 + (c >> 3) * C::kHalf + (c & 7) * 16;
+          for (int key0 = first + (threadIdx.x & 127) / (D / 8); key0 < end; key0 += 4 * kApart) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(at0 + min(key0 + k * kApart, kKeys - 1) * 128);
+            bool odd = key0 + 3 * kApart >= left;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) odd |= draft::has_bad<bf16>(v[k]);
+            if (!odd) continue;
+            for (int key = key0; key < min(end, key0 + 4 * kApart); key += kApart) {
+              uint8_t* at = at0 + key * 128;
+              if (key >= left) {
+                *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+              } else if (t * kKeys + key >= ctx && draft::clear_bad<bf16>(at)) {
+                const int k = (t - ctx / kKeys) * kKeys + key;
+                atomicOr(&bad[k >> 5], 1u << (k & 31));
+                bad[kSpecial * 4] = 1;
+              }
             }
           }
           fence_async_shared();
