@@ -440,3 +440,17 @@ def test_sequences_of_one_and_two_row_tiles(nt, seed, d):
     c = make_case(ctx, ns, 16, 4, 1, d, BF, seed=seed)
     check(c, *call_kernel(nt, c, 1))
     check(c, *call(nt, c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_pieces_of_prompts(nt, kernel, d, dtype):
+    """No masks: items of a sequence's first tokens end before its last keys,
+    wherever that is among tiles and shares."""
+    for seed, (ctx, ns) in enumerate([([0], [256]), ([0, 1, 63, 127, 500], [256, 255, 129, 65, 64]),
+                                      ([0] * 40, [200] * 40), ([2000, 3], [130, 256])]):
+        c = make_case(ctx, ns, 16, 4, 1, d, dtype, kind="causal", seed=seed)
+        got = by(nt, c, kernel)
+        if got:
+            check(c, *got)

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__((Cfg<T, D>::kWarps * 32), 2) draft_spread_kern
     const int per = a.Hkv * a.hgroups, group = j / per, head = j - group * per, kvh = head / a.hgroups;
     if (group * a.tokens >= seq.n) continue;                  // the whole cluster
     const DraftItem it = draft_item(a, seq.n, kvh, head - kvh * a.hgroups, group);
-    const int rows = it.ni * it.nh, n = seq.len, ctx = seq.len - seq.n, new16 = ctx & ~15;
+    const int rows = it.ni * it.nh, n = draft_visible(a, seq, it), ctx = seq.len - seq.n, new16 = ctx & ~15;
     const int64_t token = (int64_t)seq.first + it.i0;
     const int hq = kvh * a.G + it.h0;                         // the first query head
 

@@ -216,7 +216,14 @@ __device__ __forceinline__ DraftItem draft_item(const DraftBatch& a, int n, int 
   return draft_item(a, n, kvh, head - kvh * a.hgroups, item - head * groups);
 }
 
-// Walks a CTA's range segment by segment; as PagedWalk.
+// Positions that the item's tokens see at most: without a mask none behind the last of them.
+__device__ __forceinline__ int draft_visible(const DraftBatch& a, const DraftSeq& s, const DraftItem& it) {
+  return a.bits ? s.len : s.len - s.n + it.i0 + it.ni;
+}
+
+// Walks a CTA's range segment by segment; as PagedWalk.  An item's share of the
+// line is as long as its sequence; its last segment ends where its tokens see
+// nothing more.
 struct DraftWalk {
   int64_t left;           // units of the range not yet handed out
   int b, item, items;
@@ -231,7 +238,7 @@ struct DraftWalk {
   DraftItem it;
   int seg_b, seg_item, seg_items;
   int t0, t1;
-  int end;                // where it ends in the item, in units
+  int end, last;          // where it ends in the item, and where the item's last tile does, in units
   bool begins, ends;
 
   __device__ __forceinline__ void load_next(const DraftBatch& a) {
@@ -293,15 +300,17 @@ struct DraftWalk {
       seg_items = items;
       seq = cur;
       it = draft_item(a, cur.n, kvh, hgroup, group);
-      int from = unit, to = end;           // in tiles
+      last = units;
+      if (groups > 1 && !a.bits) last = ((int)paged_tiles(draft_visible(a, cur, it), tile) + extra) * weight;
+      int from = unit, to = min(end, last);           // in tiles
       if (weight > 1) {
-        from = (unit + weight - 1) / weight;
-        to = (end + weight - 1) / weight;
+        from = (from + weight - 1) / weight;
+        to = (to + weight - 1) / weight;
       }
       t0 = max(0, from - extra);
       t1 = to - extra;
       begins = t0 == 0;
-      ends = to * weight >= units;
+      ends = to * weight >= last;
       left -= end - unit;
       unit = 0;
       step_item(a);
@@ -310,7 +319,7 @@ struct DraftWalk {
   }
   // CTAs that take tiles of the current segment's item, where it begins and does not end (so the range ends inside it)
   __device__ __forceinline__ int parts(const DraftPlan& s, int cta) const {
-    return s.cta_of(s.hi + units - weight - end) - cta + 1;
+    return s.cta_of(s.hi + last - weight - end) - cta + 1;
   }
 };
 
