@@ -29,9 +29,9 @@
 // Measured: 152 contexts of 8,000 keys, 16 rows to a key head, 103 us at d = 128
 // (89% of the copy rate) and 69 at d = 64, where a row's 128 exponentials (1,550
 // cycles of a step's 2,900) are what a stream waits for; with 256 rows d = 128 178
-// and d = 64 141.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128: 312
-// us, 768 TFLOP/s of the result's products, three of which are made for two; a
-// product of 128 x 128 x 16 takes some 93 cycles here, 4,460 of a step's 4,950.
+// and d = 64 141.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128: 299
+// us, 869 TFLOP/s of the result's products, three of which are made for two; a
+// product of 128 x 128 x 16 takes some 93 cycles here, 4,460 of a step's 4,750.
 //
 // Two bf16 for P: one would be off by 2^-8 of P, which shows in the output.
 // The upper part is P cut short, the lower P (1 + 2^-20) less that, so that
@@ -39,7 +39,7 @@
 // that P times it is.
 //
 // Tiles behind the context (new tokens, the last key) are the only ones with a
-// mask, and with rows of V that a product may not read as they are: those
+// mask (applied where a warp's rows do not see all of one), and with rows of V that a product may not read as they are: those
 // behind the last key hold anything and become zeros; values that are not
 // finite are taken out, and added in the end to the rows that see them.
 #include "draft_plan.cuh"
