@@ -454,3 +454,24 @@ def test_pieces_of_prompts(nt, kernel, d, dtype):
         got = by(nt, c, kernel)
         if got:
             check(c, *got)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_no_pages(nt, kernel, dtype):
+    """A pool without pages: every page of the table is a bad one, read as zeros."""
+    c = make_case([20, 0], [4, 2], 16, 4, 2, 64, dtype, seed=2)
+    c["kp"], c["vp"] = c["kp"][:0], c["vp"][:0]
+    pages = nt.KVPages(c["kp"].to(DEV), c["vp"].to(DEV))
+    args = (pages, c["q"].to(DEV), _cu(c["ns"]), c["table"].to(DEV), _i32(c["lens"]), 4)
+    try:
+        if kernel == "call":
+            out = nt.nt_paged_tree_attn(*args, bits=c["bits"].to(DEV))[0]
+        else:
+            out = nt.nt_selftest_paged_tree_attn(kernel, *args, bits=c["bits"].to(DEV))[0]
+    except nt.NTError as e:
+        assert kernel in (1, 2) and e.status == 2
+        return
+    with pytest.raises(nt.NTError) as e:
+        nt.nt_device_status()
+    assert e.value.status == 6 and bool((out == 0).all())
