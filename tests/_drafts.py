@@ -90,12 +90,21 @@ def tree_attn(k_pages, v_pages, q, ns, table, lens, bits=None, scale=None):
 def tree_bound(o, mag, cond, n, dtype):
     """Elementwise bound of the attention's output against fp64, from its
     roundings: the output's own; in bf16 a probability's as the sum of two
-    bf16, 2^-15; of a score in fp32 arithmetic at most 16 steps of its sum
-    |q k| scale (eight products of 16 columns, two steps each, or d / 4 packed
-    sums of four), in numerator and denominator; 16 steps for exponentials
-    and scale; of the sums of p and p v over n keys two steps for each 16 keys
-    and each part of a probability (bf16), or one for each key in turn
-    (fp32); 64 for joins."""
-    c = 2 * 16 * cond + 16 + (n / 4 if dtype == torch.bfloat16 else n + 16 * cond) + 64
+    bf16, 2^-15; of a score at most 16 steps of its sum |q k| scale in bf16
+    (eight products of 16 columns, two steps each), in numerator and
+    denominator; 16 steps for exponentials and scale; of the sums of p and p v
+    over n keys two steps for each 16 keys and each part of a probability
+    (bf16), or one for each key in turn (fp32); 64 for joins.
+
+    fp32 by products of tf32 parts: q = qh + ql with |ql| <= 2^-11 |q|, k = kh +
+    kl with |kl| < 2^-10 |k|; ql kl is left out (2^-21 |q k|, 8 steps of 2^-24),
+    kl and ql are rounded to 11 bits (2^-22 and 2^-23: 4 and 2 steps); the
+    matrix instruction cuts its sums (a step of 2^-23 each, two of them to 16
+    columns: 4 steps of sum |q k| in all), and d / 16 + 1 fp32 adds are a step
+    each, 9 at most: 27, taken as 28, against 16 where d / 4 packed sums are added up.
+    p v likewise: 14 steps for what is left out and rounded, and at most ten for
+    each tile of 64 keys' sums, which the n steps and the 64 hold."""
+    score = 16 if dtype == torch.bfloat16 else 28
+    c = 2 * score * cond + 16 + (n / 4 if dtype == torch.bfloat16 else n) + 64
     p = 2.0 ** -15 if dtype == torch.bfloat16 else 0.0
     return HALF_STEP[dtype] * o.abs() * 1.001 + (p + c * U32) * mag + 1e-38

@@ -92,6 +92,19 @@ def test_forked_since(cache):
     assert cache.table.length == {a: 3, f: 6} and len(cache.table.pages[f]) == 2 and len(cache.table.pages[a]) == 1
 
 
+def test_compacted_since(cache):
+    """The step's block table names the old places."""
+    a, b = cache.add(), cache.add()
+    cache.step([a, b], [5, 5])
+    step = cache.step([b], [3])
+    cache.free(a)
+    cache.compact()
+    before = _state(cache.table)
+    with pytest.raises(ValueError, match="moved"):
+        cache.keep(step, [[1]])
+    assert _state(cache.table) == before and cache.moved == []
+
+
 def test_a_move_that_fails_gives_nothing_up(cache):
     a = cache.add()
     step = cache.step([a], [6])

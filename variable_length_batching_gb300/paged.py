@@ -179,10 +179,13 @@ class Step:
     tokens: int                  # new tokens of all of them
     counts: List[int] = field(default_factory=list)      # and of each
     after: List[int] = field(default_factory=list)       # positions of each with the step's, as the host has them
+    compactions: int = 0                                  # of the cache before the step
 
 
 class PagedCache:
     """Keys and values of many sequences in pages on the device."""
+
+    _compactions = 0
 
     def __init__(self, n_pages: int, page_size: int, H_kv: int, d: int, dtype: torch.dtype = torch.bfloat16,
                  device="cuda"):
@@ -222,6 +225,7 @@ class PagedCache:
         before = list(t.refs), list(t.free_pages), {s: list(p) for s, p in t.pages.items()}
         try:
             self._copy(t.compact(), stream)
+            self._compactions += 1
         except BaseException:
             t.refs, t.free_pages, t.pages = before
             raise
@@ -259,7 +263,7 @@ class PagedCache:
         with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
         return Step(seqs, arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
-                    arr[head:].view(B, width), max(counts + [0]), cu[-1], counts, after)
+                    arr[head:].view(B, width), max(counts + [0]), cu[-1], counts, after, self._compactions)
 
     def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """The step's new keys and values, packed (tokens, H_kv, d): all of
@@ -287,12 +291,14 @@ class PagedCache:
         """Of the step's tokens only ``kept``: for each of its sequences the
         accepted ones' numbers in the step, growing.  Their keys and values
         move up, the rest of the step's positions are given up.  The step has
-        to be the last one of its sequences.  Not while a graph is being
-        captured."""
+        to be the last one of its sequences, with no compaction since.  Not
+        while a graph is being captured."""
         on = self._on(stream, "a step's positions are given up")
         t, ps = self.table, self.table.page_size
         if len(kept) != len(step.seqs) or len(step.counts) != len(step.seqs):
             raise ValueError("one list of kept tokens per sequence")
+        if step.compactions != self._compactions:
+            raise ValueError("pages have been moved since the step")
         flat, cu, lengths = [], [0], []
         for s, n, after, ks in zip(step.seqs, step.counts, step.after, kept):
             t._known(s)
