@@ -936,9 +936,11 @@ size_t nt_paged_tree_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d, in
  *   workspace     >= nt_paged_tree_attn_workspace_bytes(H, H_kv, d, max_new)
  *                 bytes, 16-byte aligned.
  * Softmax statistics and sums are fp32; in bf16 a probability multiplies the
- * values as the sum of two bf16, 2^-15 of it at most away from it.  Results do
- * not depend on scheduling; their rounding may depend on the sizes of the call
- * (B, T, max_new, max_pages, H, the page size), by which a kernel is chosen.
+ * values as the sum of two bf16, 2^-15 of it at most away from it; in fp32 a
+ * product may be made of its factors' tf32 parts, 2^-20 of it at most away.
+ * Results do not depend on scheduling; their rounding may depend on the sizes
+ * of the call (B, T, max_new, max_pages, H, the page size), by which a kernel
+ * is chosen.
  * Asynchronous; nothing is read on the host, so a captured call follows
  * lengths, offsets and masks from replay to replay.
  */
