@@ -249,8 +249,9 @@ cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* 
     const bool wide = p.d == 128;
     Rates r = kTcRates[wide][rows > 128];
     // two row tiles: sequences that need but one, at most those whose tokens leave the average below it, take less
+    // (draft_plan.cuh)
     if (rows > 128)
-      r.tile += (kTcRates[wide][0].tile - r.tile) * fmax(0, 1 - (double)p.T / p.B / (128 / min(128, p.H / p.pool.H)));
+      r.tile *= 1 - (1 - (double)kLight / kHeavy) * fmax(0, 1 - (double)p.T / p.B / (128 / min(128, p.H / p.pool.H)));
     consider(kTc, split_us(p, 128, 1 + (rows > 128), 128, sms, r));
   }
   if (draft_slices_supported(dt, p))

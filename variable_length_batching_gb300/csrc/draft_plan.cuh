@@ -9,8 +9,10 @@
 // number of keys however ragged the batch is, and lengths and offsets stay on
 // the device.  Here the items of a sequence are as many as its tokens need; and
 // where an item may have two row tiles over its keys, a tile of a sequence that
-// needs both counts 5 and one of another 3, as they take (152 contexts of 8,000,
-// d = 128: 178 us against 109), and belongs to the CTA that has its first unit.
+// needs both counts 5 and one of another 2, and belongs to the CTA that has its
+// first unit (16 contexts, trees of 20 to 64 tokens, d = 128: 2.3 us against 0.8; 62
+// contexts of 2,000 with one token beside two pieces of 256: 222 us all alike, 150
+// with 5 and 3, 122 so).
 #pragma once
 
 #include "paged_plan.cuh"
@@ -60,7 +62,7 @@ inline int draft_items_most(const DraftBatch& a) {
 __device__ __forceinline__ int draft_items(const DraftBatch& a, int n) {
   return a.Hkv * a.hgroups * (n <= a.tokens ? 1 : (n + a.tokens - 1) / a.tokens);
 }
-constexpr int kHeavy = 5, kLight = 3;
+constexpr int kHeavy = 5, kLight = 2;
 __host__ __device__ __forceinline__ int draft_weight_most(const DraftBatch& a) { return a.light ? kHeavy : 1; }
 // Units of a tile of a sequence of n new tokens.
 __device__ __forceinline__ int draft_weight(const DraftBatch& a, int n) {
