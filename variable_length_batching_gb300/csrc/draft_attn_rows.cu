@@ -25,8 +25,6 @@
 // see, and 0 times it is not 0; such values are taken out of the tile and
 // added to the rows that do see them (only where new tokens are: older keys
 // are seen by all).
-#include <climits>
-
 #include "draft_plan.cuh"
 #include "draft_worker.cuh"
 
@@ -90,20 +88,21 @@ __global__ void __launch_bounds__((Cfg<T, D, kGroups>::kThreads), (Cfg<T, D, kGr
   const int64_t head_bytes = (int64_t)a.page_size * C::kRow;
   W me(smem + 4 * C::kSide);
   // The first 64 threads have a key of each tile: its page is looked up two tiles ahead, its place stored one ahead.
-  constexpr int kNone = INT_MIN;
-  auto page_of = [&](int t) {
+  auto page_of = [&](int t) {                      // (used by place(), so that nothing waits for it here)
     const uint32_t x = (uint32_t)t * kKeys + tid;
     return tid < kKeys && x < (uint32_t)w.seq.len
-               ? max(a.table[(int64_t)w.seg_b * a.max_pages + x / (uint32_t)a.page_size], -1) : kNone;
+               ? a.table[(int64_t)w.seg_b * a.max_pages + x / (uint32_t)a.page_size] : 0;
   };
   auto place = [&](int t, int id) {
     if (tid >= kKeys) return;
     const uint32_t x = (uint32_t)t * kKeys + tid;
     int64_t off = -1;
-    if ((unsigned)id < (unsigned)a.n_pages)
-      off = ((int64_t)id * a.Hkv + w.it.kvh) * head_bytes + (int64_t)(x % (uint32_t)a.page_size) * C::kRow;
-    else if (id != kNone)
-      flag_device(a.status, kDevCheck);
+    if (x < (uint32_t)w.seq.len) {
+      if ((unsigned)id < (unsigned)a.n_pages)
+        off = ((int64_t)id * a.Hkv + w.it.kvh) * head_bytes + (int64_t)(x % (uint32_t)a.page_size) * C::kRow;
+      else
+        flag_device(a.status, kDevCheck);
+    }
     sh.off[t & 1][tid] = off;
   };
   // A thread has the same chunk of some rows, keys and values.
