@@ -528,9 +528,13 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
       const uint32_t steps = (uint32_t)(t_hi - t_lo) * tiles, mine = s - 2;
       const uint32_t other = s0 + steps - 1 == mine ? mine - 1 : mine + 1;
       const bool some = t_first < t_hi, join = tiles == 1 && steps > 1;
-      // its own last P V first: the other stream's then has no phase but its last to wait for
-      // (a stream without a step has nothing to do, so that items of one tile follow each other in turns)
+      // its own last P V first: the other stream's then has no phase but its last to wait for.
+      // A P V of this segment was issued when all eight warps had left the one before (o_free).  A stream without a
+      // step here (an item of one tile) waits for that itself, so that no warp is more than a segment ahead of
+      // another: else it arrives twice in one phase of o_free, and O, the marks in `bad` or the streams' sums change
+      // under the warps that are still behind.
       if (some) ok = wait(&ctl->pv_done[g], (mine >> 1) & 1, abort, a.status);
+      else if (segs > 0) ok = wait(&ctl->o_free, (segs - 1) & 1, abort, a.status);
       if (ok && join) ok = wait(&ctl->pv_done[g ^ 1], (other >> 1) & 1, abort, a.status);
       if (!ok) break;
       tc_fence_after();
@@ -594,7 +598,8 @@ draft_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
           else if (p.lse) p.lse[(int64_t)h * a.T + tt] = draft::row_lse(m, l, any);
         }
       }
-      if (threadIdx.x == 0)                         // of the segment before, which nobody is in any more
+      // of the segment before, which nobody is in any more; none is in the segment after the next, whose they will be
+      if (threadIdx.x == 0)
         for (int k = 0; k <= kSpecial * 4; ++k) ctl->bad[(segs + 2) % 3][k] = 0;
       tc_fence_before();
       __syncwarp();
