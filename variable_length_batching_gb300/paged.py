@@ -45,13 +45,15 @@ class PageTable:
         self.free_pages = list(range(n_pages - 1, -1, -1))      # taken from the end: low pages first
         self.pages: Dict[int, List[int]] = {}                   # of each sequence, in order
         self.length: Dict[int, int] = {}
+        self.changes: Dict[int, int] = {}                       # extensions and cuts of each: a length may come back
+        self.compactions = 0
         self._next = 0
 
     def add(self) -> int:
         """A new, empty sequence's id."""
         seq = self._next
         self._next += 1
-        self.pages[seq], self.length[seq] = [], 0
+        self.pages[seq], self.length[seq], self.changes[seq] = [], 0, 0
         return seq
 
     def _known(self, seq: int):
@@ -100,6 +102,7 @@ class PageTable:
                 self.refs[pages[-1]] -= 1                       # stays in use: another sequence holds it
                 pages[-1] = dst
             self.length[s] += n
+            self.changes[s] += n > 0
             while len(pages) * self.page_size < self.length[s]:
                 page = self.free_pages.pop()
                 self.refs[page] = 1
@@ -113,6 +116,7 @@ class PageTable:
         for s, n in zip(reversed(seqs), reversed(counts)):
             pages = self.pages[s]
             self.length[s] -= n
+            self.changes[s] -= n > 0
             while len(pages) > -(-self.length[s] // self.page_size):
                 self._drop(pages.pop())
             if pages and pages[-1] in copied:
@@ -130,6 +134,7 @@ class PageTable:
             if not 0 <= n <= self.length[s]:
                 raise ValueError(f"sequence {s} has {self.length[s]} positions, not {n}")
         for s, n in zip(seqs, lengths):
+            self.changes[s] += n < self.length[s]
             self.length[s] = n
             while len(self.pages[s]) > -(-n // self.page_size):
                 self._drop(self.pages[s].pop())
@@ -148,7 +153,7 @@ class PageTable:
         self._known(seq)
         for p in self.pages.pop(seq):
             self._drop(p)
-        del self.length[seq]
+        del self.length[seq], self.changes[seq]
 
     def compact(self) -> Copies:
         """Moves the pages in use to [0, pages in use): returns the (source,
@@ -163,6 +168,7 @@ class PageTable:
         for s, pages in self.pages.items():
             self.pages[s] = [to.get(p, p) for p in pages]
         self.free_pages = list(range(self.n_pages - 1, used - 1, -1))
+        self.compactions += 1
         return list(to.items())
 
 
@@ -180,12 +186,11 @@ class Step:
     counts: List[int] = field(default_factory=list)      # and of each
     after: List[int] = field(default_factory=list)       # positions of each with the step's, as the host has them
     compactions: int = 0                                  # of the cache before the step
+    changes: List[int] = field(default_factory=list)     # of each sequence, the step's among them
 
 
 class PagedCache:
     """Keys and values of many sequences in pages on the device."""
-
-    _compactions = 0
 
     def __init__(self, n_pages: int, page_size: int, H_kv: int, d: int, dtype: torch.dtype = torch.bfloat16,
                  device="cuda"):
@@ -222,12 +227,11 @@ class PagedCache:
         table would change now and the pages at a replay."""
         self._on(stream, "compaction moves pages")
         t = self.table
-        before = list(t.refs), list(t.free_pages), {s: list(p) for s, p in t.pages.items()}
+        before = list(t.refs), list(t.free_pages), {s: list(p) for s, p in t.pages.items()}, t.compactions
         try:
             self._copy(t.compact(), stream)
-            self._compactions += 1
         except BaseException:
-            t.refs, t.free_pages, t.pages = before
+            t.refs, t.free_pages, t.pages, t.compactions = before
             raise
 
     def step(self, seqs: Sequence[int], counts: Sequence[int], stream=None) -> Step:
@@ -263,7 +267,8 @@ class PagedCache:
         with torch.cuda.stream(on):
             arr = host.to(dev, non_blocking=True)
         return Step(seqs, arr[:B + 1], arr[B + 1:2 * B + 1], arr[2 * B + 1:3 * B + 1],
-                    arr[head:].view(B, width), max(counts + [0]), cu[-1], counts, after, self._compactions)
+                    arr[head:].view(B, width), max(counts + [0]), cu[-1], counts, after,
+                    self.table.compactions, [self.table.changes[s] for s in seqs])
 
     def write(self, step: Step, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """The step's new keys and values, packed (tokens, H_kv, d): all of
@@ -291,19 +296,19 @@ class PagedCache:
         """Of the step's tokens only ``kept``: for each of its sequences the
         accepted ones' numbers in the step, growing.  Their keys and values
         move up, the rest of the step's positions are given up.  The step has
-        to be the last one of its sequences, with no compaction since.  Not
-        while a graph is being captured."""
+        to be the last one of its sequences, none of them cut or extended
+        since, with no compaction since.  Not while a graph is being captured."""
         on = self._on(stream, "a step's positions are given up")
         t, ps = self.table, self.table.page_size
-        if len(kept) != len(step.seqs) or len(step.counts) != len(step.seqs):
+        if not len(kept) == len(step.counts) == len(step.changes) == len(step.seqs):
             raise ValueError("one list of kept tokens per sequence")
-        if step.compactions != self._compactions:
+        if step.compactions != t.compactions:
             raise ValueError("pages have been moved since the step")
         flat, cu, lengths = [], [0], []
-        for s, n, after, ks in zip(step.seqs, step.counts, step.after, kept):
+        for s, n, after, changes, ks in zip(step.seqs, step.counts, step.after, step.changes, kept):
             t._known(s)
             ks = [int(k) for k in ks]
-            if t.length[s] != after:
+            if t.changes[s] != changes:                   # the block table may name pages that are another's by now
                 raise ValueError(f"sequence {s} has changed since the step")
             if any(k < 0 or k >= n for k in ks) or any(a >= b for a, b in zip(ks, ks[1:])):
                 raise ValueError(f"kept tokens of sequence {s}: growing numbers below {n}")
