@@ -869,7 +869,8 @@ nt_status nt_paged_resize(const int32_t* d_new_lengths, int32_t B, int32_t page_
  *                 on the context.
  *   d_positions   [T] int32 out, or NULL: pos0 and the number of tokens above
  *                 (for nt_qk_norm_rope).
- * Tokens behind the last segment get no bits and position 0.  Asynchronous.
+ * Tokens behind the last segment get no bits and position 0 (where that
+ * segment is not flagged).  Asynchronous.
  */
 nt_status nt_draft_tree(const int32_t* d_parents, const int32_t* d_cu_seqlens, int32_t B, int64_t T, int32_t max_new,
                         const int32_t* d_pos0, int64_t* d_bits, int32_t* d_positions, void* stream);

@@ -270,15 +270,15 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
   pdl_wait();
   pdl_trigger();
   const int lo = cu[b], hi = cu[b + 1], n = hi - lo, start = pos0 ? pos0[b] : 0;
-  if (b == gridDim.x - 1)                          // tokens that only fill up the batch
-    for (int64_t t = max(hi, 0) + i; t < T; t += blockDim.x) {
-      if (positions) positions[t] = 0;
-      for (int w = 0; w < W; ++w) bits[t * W + w] = 0;
-    }
   if (lo < 0 || hi < lo || hi > T || n > max_new) {
     if (i == 0) flag_device(status, kDevCheck);
     return;
   }
+  if (b == gridDim.x - 1)                          // tokens that only fill up the batch (where the end is known)
+    for (int64_t t = (int64_t)hi + i; t < T; t += blockDim.x) {
+      if (positions) positions[t] = 0;
+      for (int w = 0; w < W; ++w) bits[t * W + w] = 0;
+    }
   Words mine;
   int2 up = make_int2(-1, 0);
   if (i < n) {
