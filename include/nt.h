@@ -914,7 +914,7 @@ size_t nt_paged_tree_attn_workspace_bytes(int32_t H, int32_t H_kv, int32_t d, in
  *   H             a multiple of H_kv.   d in {32, 64, 128}.
  *   d_cu_seqlens  [B+1] int32: sequence b's n_b = cu[b+1] - cu[b] new tokens, 0
  *                 to max_new of them.   B at most 2^30.
- *   max_new       in [0, 256].
+ *   max_new       in [1, 256], or 0 with T = 0.
  *   d_block_table [B, max_pages] int32.   max_pages * page_size at most 2^24
  *                 (NT_ERR_UNSUPPORTED), times T * H at most 1e15
  *                 (NT_ERR_OVERFLOW).

@@ -284,6 +284,7 @@ nt_status check_tree_attn(const nt_kv_pages* pages, const void* q, int64_t q_str
     return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld H=%d max_new=%d", B, (long long)T, H, max_new);
   if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
   if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 sequences", B);
+  if (max_new == 0 && T > 0) return fail(NT_ERR_INVALID, "max_new = 0 with T = %lld tokens", (long long)T);
   if (max_new > kDraftMaxNew) return fail(NT_ERR_UNSUPPORTED, "max_new=%d: at most %d", max_new, kDraftMaxNew);
   if (H % pages->H_kv || H > 65536) return fail(NT_ERR_INVALID, "H=%d must be a multiple of H_kv=%d", H, pages->H_kv);
   if (pages->d != 32 && pages->d != 64 && pages->d != 128)
@@ -1312,7 +1313,7 @@ nt_status nt_paged_tree_attn(const nt_kv_pages* pages, const void* q, int64_t q_
   DraftProblem p;
   const nt_status st = check_tree_attn(pages, q, q_stride, T, H, d_cu_seqlens, B, max_new, d_block_table, max_pages,
                                        d_lengths, d_bits, scale, o, lse, workspace, workspace_bytes, &p);
-  if (st != NT_OK || T == 0 || max_new == 0) return st;
+  if (st != NT_OK || T == 0) return st;
   const cudaError_t e = launch_draft_attn(pages->dtype, p, status_word(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return NT_OK;
@@ -1352,7 +1353,7 @@ nt_status nt_selftest_paged_tree_attn(int32_t kernel, int32_t cluster, const nt_
   DraftProblem p;
   const nt_status st = check_tree_attn(pages, q, q_stride, T, H, d_cu_seqlens, B, max_new, d_block_table, max_pages,
                                        d_lengths, d_bits, scale, o, lse, workspace, workspace_bytes, &p);
-  if (st != NT_OK || T == 0 || max_new == 0) return st;
+  if (st != NT_OK || T == 0) return st;
   if ((kernel == 1 && !draft_tc_supported(pages->dtype, p)) || (kernel == 2 && !draft_slices_supported(pages->dtype, p)))
     return fail(NT_ERR_UNSUPPORTED, "kernel %d does not take this call", kernel);
   if (kernel == 3 && cluster == 0) draft_spread_us(pages->dtype, p, &cluster);
