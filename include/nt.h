@@ -861,7 +861,7 @@ nt_status nt_paged_resize(const int32_t* d_new_lengths, int32_t B, int32_t page_
  *                 (NT_ERR_DEVICE_CHECK) and read as -1.
  *   d_cu_seqlens  [B+1] int32; a segment of more than max_new tokens, or
  *                 outside [0, T], is flagged and not written.   B at most 2^30.
- *   max_new       longest segment, in [1, 256].
+ *   max_new       longest segment, in [1, 256], or 0 with T = 0.
  *   d_bits        [T, ceil(max_new / 64)] int64 out: bit j % 64 of word j / 64
  *                 is set where the token sees token j of its segment: itself
  *                 and those it hangs on, all the way up.

@@ -33,3 +33,21 @@ def test_tokens_behind_a_good_last_segment(nt):
         nt.nt_device_status()
     assert bits.flatten().tolist() == [-9] * 3 + [1, 2] + [0] * 3
     assert positions.tolist() == [-9] * 3 + [20] * 2 + [0] * 3
+
+
+@pytest.mark.parametrize("counts", [[0, 0, 0], [0], []])
+def test_step_without_new_tokens(nt, counts):
+    """The documented calls of a drafted step, with no token in any sequence."""
+    from variable_length_batching_gb300.paged import PagedCache
+    cache = PagedCache(8, 4, 2, 64)
+    seqs = [cache.add() for _ in counts]
+    cache.step(seqs, [3] * len(seqs))
+    step = cache.step(seqs, counts)
+    parents, kv = _i32([]), torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    bits, positions = nt.nt_draft_tree(parents, step.cu_seqlens, step.max_new, step.pos0)
+    cache.write(step, kv, kv)
+    o = cache.attend_tree(step, torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV), bits)
+    cache.keep(step, [[] for _ in counts])
+    nt.nt_device_status()
+    assert o.shape == (0, 4, 64) and bits.numel() == 0 and positions.numel() == 0
+    assert all(cache.table.length[s] == 3 for s in seqs)

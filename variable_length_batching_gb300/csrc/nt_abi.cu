@@ -1218,7 +1218,8 @@ nt_status nt_paged_resize(const int32_t* d_new_lengths, int32_t B, int32_t page_
 
 nt_status nt_draft_tree(const int32_t* d_parents, const int32_t* d_cu_seqlens, int32_t B, int64_t T, int32_t max_new,
                         const int32_t* d_pos0, int64_t* d_bits, int32_t* d_positions, void* stream) {
-  if (B < 0 || T < 0 || max_new < 1) return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld max_new=%d", B, (long long)T, max_new);
+  if (B < 0 || T < 0 || max_new < 0 || (max_new == 0 && T > 0))
+    return fail(NT_ERR_INVALID, "bad sizes B=%d T=%lld max_new=%d", B, (long long)T, max_new);
   if (max_new > kDraftMaxNew) return fail(NT_ERR_UNSUPPORTED, "max_new=%d: at most %d", max_new, kDraftMaxNew);
   if (T > 0x7fffffffLL) return fail(NT_ERR_OVERFLOW, "T = %lld: token counts must fit int32", (long long)T);
   if (B > kMaxSegments) return fail(NT_ERR_OVERFLOW, "B = %d: at most 2^30 segments", B);
