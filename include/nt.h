@@ -839,8 +839,9 @@ nt_status nt_paged_write_slots(const nt_kv_pages* pages, const void* k, int64_t 
  *   d_cu_seqlens  [B+1] int32 out: offsets of the tokens that rows gain.
  *   d_pos0        [B] int32 out: the lengths before.
  *   d_slots       [T] int64 out: where token t of them goes, page * page_size +
- *                 offset; -1 behind the last.  T is the room the caller has;
- *                 T = 0 with NULL where nothing grows.
+ *                 offset; -1 behind the last.  In a page below 0 of a row's
+ *                 table it is -2, and flagged (NT_ERR_DEVICE_CHECK).  T is the
+ *                 room the caller has; T = 0 with NULL where nothing grows.
  *   d_lacking     [2] int32 out: free pages that are missing, and tokens that
  *                 do not fit T.  Where one is not 0 nothing is changed:
  *                 d_cu_seqlens is 0, all slots -1, and d_pos0 the lengths.

@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(kResizeThreads) paged_resize_kernel(const Resi
   const uint32_t ps = a.page_size;
   moves(kAdd, add, [&](uint32_t t, int b, int off, const Change& c) {
     const uint32_t x = (uint32_t)c.old + off, pg = x / ps;
-    a.slots[t] = (int64_t)a.table[(int64_t)b * a.max_pages + pg] * ps + (x - pg * ps);
+    const int id = a.table[(int64_t)b * a.max_pages + pg];
+    if (id < 0) flag_device(a.status, kDevCheck);           // and a slot that is not taken for none
+    a.slots[t] = id < 0 ? -2 : (int64_t)id * ps + (x - pg * ps);
   });
   for (uint32_t t = add + me; t < T; t += all) a.slots[t] = -1;
   if (strip > 1) {
