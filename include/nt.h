@@ -845,6 +845,8 @@ nt_status nt_paged_write_slots(const nt_kv_pages* pages, const void* k, int64_t 
  *   d_lacking     [2] int32 out: free pages that are missing, and tokens that
  *                 do not fit T.  Where one is not 0 nothing is changed:
  *                 d_cu_seqlens is 0, all slots -1, and d_pos0 the lengths.
+ *                 What keeps tokens of such a step and grows rows by them has to
+ *                 be left out: they were never written.
  *   page_size in [1, 65536]; B at most 2^30.  No page may belong to two rows
  * (a table that shares pages is the host's to keep).  Two calls on one state
  * must not overlap.  Asynchronous.

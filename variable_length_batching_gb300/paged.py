@@ -20,6 +20,7 @@ host, and a captured one follows the lengths from replay to replay.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -335,11 +336,14 @@ class DevicePagedCache:
         bits, positions = nt.nt_draft_tree(parents, cu, max_new, pos0)
         cache.write(k, v, slots)
         o = cache.attend_tree(q, cu, max_new, bits)
-        cache.keep(kept, cu_kept, pos0)        # the accepted tokens
-        cache.resize(pos0 + n_kept)
+        cache.keep(kept, cu_kept, pos0, lacking=lacking)        # the accepted tokens
+        cache.resize(pos0 + n_kept, lacking=lacking)
 
-    with tensors on the device throughout.  Calls go in order on one stream:
-    each changes what the next one reads."""
+    with tensors on the device throughout.  Where the first call lacks pages or
+    room for tokens, the step has not happened: nothing is written or kept, no
+    length changes (without ``lacking`` the last two calls would keep tokens
+    that were never written), and o holds nothing.  Calls go in order on one
+    stream: each changes what the next one reads."""
 
     def __init__(self, rows: int, max_pages: int, n_pages: int, page_size: int, H_kv: int, d: int,
                  dtype: torch.dtype = torch.bfloat16, device="cuda"):
@@ -352,10 +356,22 @@ class DevicePagedCache:
         self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)   # from the end
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
 
-    def resize(self, new_lengths: torch.Tensor, tokens: int = 0, stream=None):
+    @staticmethod
+    def _unless(lacking: Optional[torch.Tensor], there: torch.Tensor, otherwise: torch.Tensor, stream) -> torch.Tensor:
+        """``there``, or ``otherwise`` where the resize that returned
+        ``lacking`` changed nothing; decided on the device."""
+        if lacking is None:
+            return there
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            return torch.where(lacking.any(), otherwise, there)
+
+    def resize(self, new_lengths: torch.Tensor, tokens: int = 0, stream=None,
+               lacking: Optional[torch.Tensor] = None):
         """Every row brought to new_lengths (rows): (cu_seqlens, pos0, slots,
         lacking) of the tokens that rows gain, as nt_paged_resize; where
-        ``lacking`` is not 0 nothing has changed."""
+        ``lacking`` is not 0 nothing has changed.  Given the ``lacking`` of an
+        earlier resize, rows stay as they are where that one changed nothing."""
+        new_lengths = self._unless(lacking, new_lengths, self.lengths, stream)
         return nt.nt_paged_resize(self.block_table, self.lengths, self.free_pages, self.n_free, self.page_size,
                                   new_lengths, tokens, stream=stream)
 
@@ -374,7 +390,11 @@ class DevicePagedCache:
         return nt.nt_paged_tree_attn(self.pages, q, cu_seqlens, self.block_table, self.lengths, max_new, bits=bits,
                                      scale=scale, stream=stream)[0]
 
-    def keep(self, kept: torch.Tensor, cu_kept: torch.Tensor, pos0: torch.Tensor, stream=None) -> None:
+    def keep(self, kept: torch.Tensor, cu_kept: torch.Tensor, pos0: torch.Tensor, stream=None,
+             lacking: Optional[torch.Tensor] = None) -> None:
         """The accepted tokens' keys and values moved up behind pos0, as
-        nt_paged_keep; resize() then gives up the others'."""
+        nt_paged_keep; resize() then gives up the others'.  Given the
+        ``lacking`` of the step's resize, nothing is moved where that one
+        changed nothing."""
+        cu_kept = self._unless(lacking, cu_kept, cu_kept[:1], stream)       # (empty segments)
         nt.nt_paged_keep(self.pages, kept, cu_kept, self.block_table, pos0, stream=stream)
