@@ -325,7 +325,8 @@ struct Rows<float, D, kGroups> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
   }
-  // A score by plain multiply-adds, where the parts of an infinite key made NaN of it.
+  // A score by plain multiply-adds, where that of the parts is not finite: the parts of an infinite key make NaN of it,
+  // and a NaN whose payload is all in the bits that the upper part has lost is an infinity there.
   static __device__ __noinline__ float score(const float* q_hi, const float* q_lo, const uint8_t* ks_, int row,
                                              int key) {
     float s = 0.f;
@@ -386,14 +387,14 @@ struct Rows<float, D, kGroups> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[n][i] += sl[n][i];
-        odd |= s[n][i] != s[n][i] && (see[i >> 1] >> (8 * n + 2 * tq + (i & 1)) & 1);
+        odd |= !(fabsf(s[n][i]) <= 3.402823466e38f) && (see[i >> 1] >> (8 * n + 2 * tq + (i & 1)) & 1);
       }
     if (odd) {
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (s[n][i] != s[n][i])
+          if (!(fabsf(s[n][i]) <= 3.402823466e38f))
             s[n][i] = score(reinterpret_cast<const float*>(qh + row0 * D / 4),
                             reinterpret_cast<const float*>(ql + row0 * D / 4), ks_, g + 8 * (i >> 1),
                             key0 + 8 * n + 2 * tq + (i & 1));
