@@ -219,11 +219,15 @@ double draft_items_mean(const DraftProblem& p, const DraftBatch& a) {
 // The call takes the kernel with the least estimated time.  Lengths are on the
 // device, so the estimates go by what the host knows: the tables' size (one
 // sequence fills its table, several 0.4 of it), the tokens and the heads.  The
-// rates were fitted to 4,000 random calls of up to 128 sequences, on which this
-// choice costs 1 to 3% over the best kernel of each (geometric mean; without the
-// spread kernel 6 to 16%, the tensor-memory kernel 10 to 12 at d = 64 and 128,
-// the slices 1.5 at d = 32 and 0.6 at 64, the rows kernel 6 to 11 in bf16 and 51
-// to 75 in fp32).
+// rates were fitted to 4,000 random calls of up to 128 sequences whose tables are
+// as wide as their longest sequence; there this choice cost 1 to 3% over the best
+// kernel of each (geometric mean by type and width; without the spread kernel 6 to
+// 16%, the tensor-memory kernel 10 to 12 at d = 64 and 128, the slices 1.5 at d = 32
+// and 0.6 at 64, the rows kernel 6 to 11 in bf16 and 51 to 75 in fp32).  On 900
+// other such calls the final kernels' choice costs 0.5%, at most 83%; on 300 of
+// them with tables for 131,072 positions, as a table on the device may be, 13% and
+// at most 89% (one context of 777 keys, eight tokens, 12 heads of 64: 6.6 us, and
+// 10.5 in the wide table).
 cudaError_t launch_draft_attn(nt_dtype dt, const DraftProblem& p, unsigned int* status, cudaStream_t s) {
   constexpr Rates kRowsBf16[3] = {{7.15, 1.47, 2.75}, {7.55, 2.0, 2.8}, {8.1, 3.1, 3.9}};
   constexpr Rates kRowsF32[3][3] = {{{7.65, 1.72, 3.8}, {7.65, 2.34, 3.8}, {7.65, 4.1, 3.8}},

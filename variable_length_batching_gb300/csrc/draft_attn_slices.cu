@@ -12,10 +12,14 @@
 // no warp waits for another until the end of a segment, where their results are
 // merged.  The tensor-memory kernel (draft_attn_tc.cu) has 128 rows to a tile,
 // and two hand-offs between warps for every 128 keys: it costs more where rows
-// are few (152 contexts of 8,000 keys, d = 64, 16 rows: 69 us there, 56 here; 32
-// rows 69 and 80), but has no d = 32 (44 us here, 105 on the general kernel), and at
-// d = 128 it was the faster one (64 contexts of up to 8,192 keys, up to 16 rows: 95 us
-// against 122).
+// are few (152 contexts of 8,000 keys in a graph, d = 64, 16 rows: 69 us there, 57
+// here; 32 rows 69 and 81), but has no d = 32 (16 rows 44 us here and 90 on the general
+// kernel, 32 rows 65 and 104, 64 rows 107 and 108), and at d = 128 it was the faster
+// one (64 contexts of up to 8,192 keys, up to 16 rows: 95 us against 122).  At d = 32
+// a slice's bytes are half of those at d = 64 and its softmax is the same: some 265
+// warp instructions to a slice, two consumer warps to a scheduler, which issues in 42%
+// of its cycles and waits for one instruction after the other in the rest; HBM is 44%
+// busy.
 //
 // RG row groups of 16 (1, 2 or 4) share the eight warps with 8 / RG slices of
 // the keys.  A row's mask words are fetched with the queries.  Values that are

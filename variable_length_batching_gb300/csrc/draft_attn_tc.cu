@@ -26,12 +26,13 @@
 // factor of 256, which fp32 sums and the bf16 parts of P bear), so O is rescaled
 // on few tiles.
 //
-// Measured: 152 contexts of 8,000 keys, 16 rows to a key head, 103 us at d = 128
-// (89% of the copy rate) and 69 at d = 64, where a row's 128 exponentials (1,550
-// cycles of a step's 2,900) are what a stream waits for; with 256 rows d = 128 178
-// and d = 64 141.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128: 299
-// us, 869 TFLOP/s of the result's products, three of which are made for two; a
-// product of 128 x 128 x 16 takes some 93 cycles here, 4,460 of a step's 4,750.
+// Measured in a graph: 152 contexts of 8,000 keys, 16 rows to a key head, 103 us at
+// d = 128 (89% of the copy rate) and 69 at d = 64, where a row's 128 exponentials
+// (1,550 cycles of a step's 2,900) are what a stream waits for; with 256 rows d = 128
+// 178 and d = 64 139.  8 pieces of 256 tokens behind 2,000 to 16,000 keys, d = 128:
+// 300 us, 866 TFLOP/s of the result's products, three of which are made for two (a
+// call among others on cold inputs 319); a product of 128 x 128 x 16 takes some 93
+// cycles here, 4,460 of a step's 4,750.
 //
 // Two bf16 for P: one would be off by 2^-8 of P, which shows in the output.
 // The upper part is P cut short, the lower P (1 + 2^-20) less that, so that
@@ -66,7 +67,7 @@ struct Cfg {
   static constexpr int kFit = (int)((227 * 1024 - kCtl - kQBufs * kQ) / kTile);
   static constexpr int kK = kFit / 2, kV = kFit - kK;              // stages of keys and of values
   static constexpr uint32_t kSmem = kQBufs * kQ + (kK + kV) * kTile + kCtl;
-  // an item's cost beside its tiles, in tiles (pieces of 256 tokens, d = 128: 332 us with two, 315 with four)
+  // an item's cost beside its tiles, in tiles (pieces of 256 tokens, d = 128, in a graph: 332 us with two, 315 with four)
   static constexpr int kExtra = D == 64 ? (R == 1 ? 4 : 3) : R == 1 ? 3 : 4;
   static_assert(kK >= 2 && kSmem <= 227 * 1024, "shared memory");
 };

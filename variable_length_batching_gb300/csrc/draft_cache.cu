@@ -18,8 +18,8 @@ namespace {
 // once), a thread a strip of them; pages and tokens are then dealt out one by
 // one over all threads, however they lie in the rows, several searches side
 // by side.  512 prompts of 65,000 tokens and back: 25 us by one CTA, 16.5 by eight,
-// 12.0 by 16; 16 sequences and back: 13.2, 8.4 and 8.4, the launches, cluster barriers
-// and the loads between them.
+// 12.4 by 16 (0.2 more for the flag of pages below 0); 16 sequences and back: 13.2,
+// 8.4 and 8.3, the launches, cluster barriers and the loads between them.
 constexpr int kResizeThreads = 512;
 constexpr int kResizeCtas = 16, kResizePortable = 8;
 constexpr int kResizeUnroll = 4;
@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
 // read before any is written, and then the next run, reads nothing that it
 // has written.  CTAs have a sequence, a range of its heads and a side each; HBM
 // bounds a large batch (256 sequences, 35 tokens each of 8 heads of 256 bytes: 84 MB
-// in 17 us, four words in flight to a thread and 64 warps to an SM; eight and 32
-// took 20), the launch and four dependent loads a small one (16 sequences: 3.2).
+// in 17 us in a graph, four words in flight to a thread and 64 warps to an SM; eight
+// and 32 took 20; as a call on cold inputs 19.3), the launch and four dependent loads a
+// small one (16 sequences: 3.4).
 constexpr int kKeepThreads = 256;
 constexpr int kKeepUnroll = 4;
 
