@@ -1,5 +1,7 @@
 """Steps that PagedCache.keep refuses although the sequence's length is what
 they left it at, without a GPU."""
+import random
+
 import pytest
 import torch
 
@@ -99,3 +101,80 @@ def test_steps_made_by_hand(cache):  # noqa: F811
     with pytest.raises(ValueError):
         cache.keep(bare, [[0]])
     assert cache.table.length[a] == 3
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_use(cache, monkeypatch, seed):  # noqa: F811
+    """Steps, forks, ends, compactions and keeps of any step so far, against a
+    model of every sequence's tokens: a keep is refused, or right."""
+    r = random.Random(seed)
+    pool = [[None] * 4 for _ in range(12)]
+    model, steps, token = {}, [], 0
+    kept_some = refused_some = 0
+
+    def move(pages, kept, cu, table, pos0, stream=None):
+        kept, cu, table, pos0 = kept.tolist(), cu.tolist(), table.tolist(), pos0.tolist()
+        for b in range(len(pos0)):
+            for i, k in enumerate(kept[cu[b]:cu[b + 1]]):
+                src, dst = pos0[b] + k, pos0[b] + i
+                pool[table[b][dst // 4]][dst % 4] = pool[table[b][src // 4]][src % 4]
+
+    def copy(pages, src, dst, stream=None):
+        for a, b in zip(src.tolist(), dst.tolist()):
+            pool[b] = list(pool[a])
+
+    monkeypatch.setattr(paged.nt, "nt_paged_keep", move)
+    monkeypatch.setattr(paged.nt, "nt_paged_copy", copy)
+    for _ in range(400):
+        what = r.choice(["add", "step", "step", "step", "keep", "keep", "keep", "fork", "free", "compact"])
+        live = sorted(model)
+        if what == "add" and len(live) < 5:
+            model[cache.add()] = []
+        elif what == "step" and live:
+            seqs = r.sample(live, r.choice([1, 1, 1, min(2, len(live))]))
+            counts = [r.choice([0, 1, 2, 2, 3]) for _ in seqs]
+            try:
+                step = cache.step(seqs, counts)
+            except paged.OutOfPages:
+                s = r.choice(live)
+                cache.free(s)
+                del model[s]
+                continue
+            added = []
+            for b, (s, n) in enumerate(zip(seqs, counts)):
+                added.append(list(range(token, token + n)))
+                for i in range(n):
+                    x = int(step.pos0[b]) + i
+                    pool[int(step.block_table[b, x // 4])][x % 4] = token
+                    model[s] = model[s] + [token]
+                    token += 1
+            steps.append((step, added))
+        elif what == "keep" and steps:
+            step, added = r.choice(steps[-r.choice([1, 1, 12]):])
+            kept = [sorted(r.sample(range(n), r.randint(0, n))) for n in step.counts]
+            before = _state(cache.table)
+            try:
+                cache.keep(step, kept)
+            except (ValueError, KeyError):
+                assert _state(cache.table) == before
+                refused_some += 1
+            else:
+                kept_some += 1
+                for s, n, new, ks in zip(step.seqs, step.counts, added, kept):
+                    first = len(model[s]) - n
+                    assert model[s][first:] == new               # the step was the last one
+                    model[s] = model[s][:first] + [model[s][first + k] for k in ks]
+        elif what == "fork" and live and len(live) < 5:
+            s = r.choice(live)
+            model[cache.fork(s)] = list(model[s])
+        elif what == "free" and live and r.random() < 0.4:
+            s = r.choice(live)
+            cache.free(s)
+            del model[s]
+        elif what == "compact" and r.random() < 0.3:
+            cache.compact()
+        for s, toks in model.items():
+            pages = cache.table.pages[s]
+            assert cache.table.length[s] == len(toks)
+            assert [pool[pages[x // 4]][x % 4] for x in range(len(toks))] == toks
+    assert kept_some > 10 and refused_some > 10
